@@ -331,6 +331,135 @@ long long moe_layer_workspace_bytes(const moe_layer_t* h, int T_max);
 /* Free the workspace and the handle.  NULL is ignored. */
 void moe_layer_destroy(moe_layer_t* h);
 
+/* ------------------------------------------------------------------ routing
+ *
+ * Routing of tokens to experts as an operator of its own, for scores, biases
+ * and groups that the layer's built-in router (softmax, top-k, renormalise)
+ * does not have, with its gradient for training.  Per token, with the logits
+ * l over E experts:
+ *   s   = softmax(l) or sigmoid(l)                       (the scores)
+ *   c   = s + bias; without a bias the order of l itself (what selects)
+ *   groups of E / groups consecutive experts are ranked by their largest c
+ *         (MOE_GROUP_MAX) or the sum of their two largest (MOE_GROUP_TOP2;
+ *         without a bias, of their two largest s); the experts of the best
+ *         groups_kept groups stay in the choice
+ *   idx = the k largest c, the larger first
+ *   w_j = scale * s_j, or scale * s_j / (sum of the kept s) if renormalised
+ * Ties go to the lower expert and the lower group.  The bias (the balance
+ * bias that training moves against the load) selects only: it is not in w.
+ * A logit of -inf (or a bias of -inf) masks its expert out: it is never
+ * chosen and has the score 0.  A slot left without an expert (a row masked
+ * out altogether, say) gets idx -1 and w 0.  A NaN logit ranks above every
+ * number, and shows as NaN in w.  Scores, sums and weights are fp32, so two
+ * choices whose c differ by a few fp32 roundings may be taken either way;
+ * without a bias (and groups ranked by the maximum) the choice is exact.
+ *
+ * Row t of the logits is at logits + t * row_stride elements (row_stride >=
+ * E), fp32 or bf16, aligned to its type; idx [T, k] int32 and w [T, k] fp32
+ * are overwritten; counts (int32 [E], may be NULL) is overwritten with each
+ * expert's number of tokens.  Outputs must not overlap inputs.  Both calls
+ * are asynchronous, allocate nothing and can be captured in a graph; a handle
+ * holds settings alone and may be used by several streams and threads at
+ * once.  T = 0 writes counts only. */
+typedef struct moe_router moe_router_t;
+
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_TOP2 1
+#define MOE_TYPE_F32 0
+#define MOE_TYPE_BF16 1
+
+/* Limits: 1 <= k <= E <= 256, k <= 16; groups divides E, at most 32;
+ * k <= groups_kept * E / groups; scale finite.  NULL on anything else. */
+moe_router_t* moe_router_create(int E, int k, int score, int groups, int groups_kept, int group_score,
+                                int renormalise, float scale);
+
+int moe_router_forward(const moe_router_t* h, int T, const void* logits, int logits_type,
+                       long long row_stride, const float* bias, int32_t* idx, float* w,
+                       int32_t* counts, void* stream);
+
+/* The gradient of the weights with respect to the logits, for the choice idx
+ * that the forward pass made (the choice itself and the bias have none):
+ * grad_w [T, k] fp32 -> grad_logits, every one of its E columns overwritten,
+ * of the logits' type, rows grad_row_stride elements apart.  Slots with idx
+ * outside [0, E) are passed over; an expert that a row names twice gets the
+ * sum.  grad_logits must not overlap the logits. */
+int moe_router_backward(const moe_router_t* h, int T, const void* logits, int logits_type,
+                        long long row_stride, const int32_t* idx, const float* grad_w,
+                        void* grad_logits, long long grad_row_stride, void* stream);
+
+void moe_router_destroy(moe_router_t* h);
+
+/* -------------------------------------------------------------- 4-bit weights
+ *
+ * A matrix [rows, cols] of 4-bit weights is
+ *   codes   [rows, cols / 2] bytes: column 2 i in the low half, 2 i + 1 in the
+ *           high half of byte i
+ *   scales  [rows, cols / group] bf16, a group being 32, 64 or 128 consecutive
+ *           columns of a row
+ *   zeros   [rows, cols / group] bytes 0..15, or NULL: 8 everywhere
+ *   value = (code - zero) * scale
+ */
+
+/* bf16 weights w [rows, cols] -> codes, scales and, if zeros is not NULL,
+ * zero points.  Per group, with division and rounding (half to even) in fp32:
+ *   without zeros: scale = bf16(max |w| / 7), code = 8 + clamp(round(w / scale), -8, 7)
+ *   with zeros:    lo = min(0, min w), hi = max(0, max w), scale = bf16((hi - lo) / 15),
+ *                  zero = clamp(round(-lo / scale), 0, 15),
+ *                  code = clamp(round(w / scale) + zero, 0, 15)
+ * A scale of 0 divides as 1.  A group with an infinity or a NaN gets the scale
+ * NaN and codes at the zero point.  w and codes are 16-byte aligned, cols a multiple of
+ * group.  Asynchronous, allocates nothing; no two tensors overlap. */
+int moe_w4_quantize(long long rows, int cols, int group, const void* w, void* codes, void* scales,
+                    void* zeros, void* stream);
+
+/* The values as bf16 (one rounding): the way back, to moe_layer_forward for
+ * prompts, whose products the tensor cores bound and not the weights' bytes. */
+int moe_w4_dequantize(long long rows, int cols, int group, const void* codes, const void* scales,
+                      const void* zeros, void* w, void* stream);
+
+/* Experts on 4-bit weights, for decode batches (T <= 1024): given the routing
+ * (idx, w) of moe_router_forward or of moe_layer_get_routing,
+ *   h       = bf16( silu(Wg[e] x_t) * (Wu[e] x_t) )
+ *   out[t]  = bf16( sum_j w[t,j] Wd[e_j] h_j  +  shared expert's, weight 1 )
+ * with the weights' 4-bit values and fp32 sums.  Slots with idx outside
+ * [0, E) add nothing (the rows behind a padded batch's last sequence: idx -1);
+ * an expert named twice by a row counts twice.  Shapes: gate and up
+ * [E + S, f, d], down [E + S, d, f] (groups along the last axis), the shared
+ * expert last.  Limits: those of moe_layer_create, and f <= 32768.
+ * The handle owns a workspace and serves one stream at a time. */
+typedef struct moe_w4 moe_w4_t;
+
+typedef struct moe_w4_weight {
+  const void* codes;
+  const void* scales;
+  const void* zeros; /* NULL for all three matrices or for none */
+} moe_w4_weight;
+
+moe_w4_t* moe_w4_create(int d, int f, int E, int k, int shared_experts, int group);
+
+/* Allocate the workspace for up to T_max (1..1024) tokens on the current
+ * device.  The only allocating call; may be called again. */
+int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream);
+
+/* Bytes that moe_w4_reserve(T_max) allocates; -1 for a NULL handle or a T_max
+ * outside 0..1024. */
+long long moe_w4_workspace_bytes(const moe_w4_t* h, int T_max);
+
+/* The matrices every later forward reads (device pointers, 16-byte aligned,
+ * kept by the caller). */
+int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weight* up,
+                       const moe_w4_weight* down);
+
+/* One pass for T tokens, 0 <= T <= T_max (T = 0 does nothing): x and out
+ * [T, d] bf16, idx [T, k] int32, w [T, k] fp32.  Asynchronous, allocates
+ * nothing, can be captured in a graph. */
+int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const float* w, void* out,
+                   void* stream);
+
+void moe_w4_destroy(moe_w4_t* h);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* moe_last_error(void);
 

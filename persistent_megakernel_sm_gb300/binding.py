@@ -4,7 +4,9 @@ Each C entry point is exposed under its own name on ``lib`` (a ``ctypes.CDLL``
 with argument and return types set from the header).  ``MoELayer`` wraps a
 handle for callers holding torch tensors: it passes ``data_ptr()`` values and
 the current CUDA stream, and turns non-zero status codes into ``MoEError``.
-Every step of the layer runs in the library's kernels.
+Every step of the layer runs in the library's kernels.  ``MoERouter``,
+``w4_quantize`` / ``w4_dequantize`` and ``W4Experts`` do the same for the
+routing operator and the 4-bit experts.
 """
 from __future__ import annotations
 
@@ -29,6 +31,8 @@ OPTIONS = {
 STATS = {"mover_ctas": 1, "tasks": 2, "grid": 3, "gemm_tasks": 4, "mover_tasks": 5, "stolen": 6,
          "ahead": 7, "trace_records": 8, "tile_tokens": 9, "split_k": 10, "bands": 11, "y_bytes": 12,
          "combine_tokens": 13, "pair": 14}
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
 TASK_TYPES = {1: "route", 2: "gather", 3: "gateup", 4: "down", 5: "combine", 6: "plan"}
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
@@ -50,6 +54,18 @@ _SIGNATURES = {
     "moe_layer_workspace_bytes": ([_vp, _i32], _i64),
     "moe_layer_get_trace": ([_vp, _vp, _i32, _vp], _i32),
     "moe_layer_destroy": ([_vp], None),
+    "moe_router_create": ([_i32] * 7 + [ctypes.c_float], _vp),
+    "moe_router_forward": ([_vp, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp], _i32),
+    "moe_router_backward": ([_vp, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _i64, _vp], _i32),
+    "moe_router_destroy": ([_vp], None),
+    "moe_w4_quantize": ([_i64, _i32, _i32] + [_vp] * 5, _i32),
+    "moe_w4_dequantize": ([_i64, _i32, _i32] + [_vp] * 5, _i32),
+    "moe_w4_create": ([_i32] * 6, _vp),
+    "moe_w4_reserve": ([_vp, _i32, _vp], _i32),
+    "moe_w4_workspace_bytes": ([_vp, _i32], _i64),
+    "moe_w4_set_weights": ([_vp, _vp, _vp, _vp], _i32),
+    "moe_w4_forward": ([_vp, _i32, _vp, _vp, _vp, _vp, _vp], _i32),
+    "moe_w4_destroy": ([_vp], None),
     "moe_last_error": ([], ctypes.c_char_p),
 }
 
@@ -91,7 +107,7 @@ def header_symbols(header: str = HEADER) -> list[str]:
     """Names of the functions include/moe.h declares."""
     text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(moe_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", text)))
 
 
 def _err(code: int):
@@ -260,6 +276,220 @@ class MoELayer:
     def close(self):
         if self.h:
             lib.moe_layer_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _on_device(name, t, device, dtype, shape):
+    """_check_tensor for the operators: the exact shape, on ``device`` (the
+    current CUDA device's index, on which the call's stream is)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        _check_tensor(name, t, dtype, shape)
+    if t.get_device() != device:
+        raise MoEError(MOE_E_INVAL, f"{name}: on device {t.get_device()}, the current one is {device}")
+
+
+def _current_device():
+    import torch
+    return torch.cuda.current_device()
+
+
+class MoERouter:
+    """Routing of tokens to experts from their logits (moe_router_* of
+    include/moe.h): ``score`` "softmax" or "sigmoid", an optional balance bias
+    that selects only, ``groups`` of consecutive experts of which the best
+    ``groups_kept`` (by "max" or "top2") stay in the choice, top-k, weights
+    renormalised or not and scaled.  The handle holds settings alone."""
+
+    def __init__(self, E: int, k: int, score: str = "softmax", groups: int = 1, groups_kept: int = 1,
+                 group_score: str = "top2", renormalise: bool = True, scale: float = 1.0):
+        self.h = None
+        if score not in SCORES or group_score not in GROUP_SCORES:
+            raise MoEError(MOE_E_INVAL, f"score is one of {list(SCORES)}, group_score of {list(GROUP_SCORES)}")
+        h = lib.moe_router_create(E, k, SCORES[score], groups, groups_kept, GROUP_SCORES[group_score],
+                                  int(bool(renormalise)), scale)
+        if not h:
+            raise MoEError(MOE_E_INVAL, (lib.moe_last_error() or b"").decode())
+        self.h = ctypes.c_void_p(h)
+        self.E, self.k = E, k
+
+    def _check_logits(self, name, t, device):
+        """Rows of E values, fp32 or bf16, that may be columns of a wider
+        buffer; returns the type code and the row stride."""
+        import torch
+        if t.dtype is torch.float32:
+            kind = 0
+        elif t.dtype is torch.bfloat16:
+            kind = 1
+        else:
+            raise MoEError(MOE_E_INVAL, f"{name}: dtype {t.dtype}, expected torch.float32 or torch.bfloat16")
+        if t.dim() != 2 or t.shape[1] != self.E:
+            raise MoEError(MOE_E_INVAL, f"{name}: shape {list(t.shape)}, expected [T, {self.E}]")
+        rows, step = t.stride()
+        if t.shape[0] <= 1:  # a single row's stride is anything
+            rows = max(rows, self.E)
+        if t.shape[0] and ((step != 1 and self.E > 1) or rows < self.E):
+            raise MoEError(MOE_E_INVAL, f"{name}: strides {[rows, step]}, rows of consecutive values are needed")
+        if not t.is_cuda:
+            raise MoEError(MOE_E_INVAL, f"{name}: not a CUDA tensor")
+        if t.get_device() != device:
+            raise MoEError(MOE_E_INVAL, f"{name}: on device {t.get_device()}, the current one is {device}")
+        return kind, rows
+
+    def forward(self, logits, idx, w, bias=None, counts=None, stream=None):
+        """logits [T, E] -> idx [T, k] int32, w [T, k] fp32 and, if given, counts
+        [E] int32 (each expert's tokens).  ``bias`` [E] fp32 selects only."""
+        import torch
+        dev = _current_device()
+        kind, stride = self._check_logits("logits", logits, dev)
+        T = logits.shape[0]
+        _on_device("idx", idx, dev, torch.int32, (T, self.k))
+        _on_device("w", w, dev, torch.float32, (T, self.k))
+        if bias is not None:
+            _on_device("bias", bias, dev, torch.float32, (self.E,))
+        if counts is not None:
+            _on_device("counts", counts, dev, torch.int32, (self.E,))
+        _err(lib.moe_router_forward(self.h, T, logits.data_ptr(), kind, stride,
+                                    None if bias is None else bias.data_ptr(), idx.data_ptr(),
+                                    w.data_ptr(), None if counts is None else counts.data_ptr(),
+                                    _stream_ptr(stream)))
+        return idx, w
+
+    def backward(self, logits, idx, grad_w, grad_logits, stream=None):
+        """grad_w [T, k] fp32 -> grad_logits [T, E], of the logits' dtype."""
+        import torch
+        dev = _current_device()
+        kind, stride = self._check_logits("logits", logits, dev)
+        out_kind, out_stride = self._check_logits("grad_logits", grad_logits, dev)
+        T = logits.shape[0]
+        if out_kind != kind or grad_logits.shape[0] != T:
+            raise MoEError(MOE_E_INVAL, "grad_logits: dtype and rows must be those of logits")
+        _on_device("idx", idx, dev, torch.int32, (T, self.k))
+        _on_device("grad_w", grad_w, dev, torch.float32, (T, self.k))
+        _err(lib.moe_router_backward(self.h, T, logits.data_ptr(), kind, stride, idx.data_ptr(),
+                                     grad_w.data_ptr(), grad_logits.data_ptr(), out_stride,
+                                     _stream_ptr(stream)))
+        return grad_logits
+
+    def close(self):
+        if self.h:
+            lib.moe_router_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _check_w4(w, codes, scales, zeros):
+    """Shapes of a bf16 matrix (any leading dimensions) and its 4-bit form;
+    returns rows, columns and the group."""
+    import torch
+    dev = _current_device()
+    shape = tuple(w.shape)
+    if len(shape) < 2 or scales.dim() != len(shape) or shape[-1] % 2 != 0:
+        raise MoEError(MOE_E_INVAL, f"weights {list(shape)} and scales {list(scales.shape)}: expected "
+                                    "[..., rows, cols] and [..., rows, cols / group]")
+    cols, n = shape[-1], scales.shape[-1]
+    group = cols // n if n else 0
+    if group not in (32, 64, 128) or group * n != cols:
+        raise MoEError(MOE_E_INVAL, f"{cols} columns and {n} scales a row: groups of 32, 64 or 128 are needed")
+    _on_device("weights", w, dev, torch.bfloat16, shape)
+    _on_device("codes", codes, dev, torch.uint8, shape[:-1] + (cols // 2,))
+    _on_device("scales", scales, dev, torch.bfloat16, shape[:-1] + (n,))
+    if zeros is not None:
+        _on_device("zeros", zeros, dev, torch.uint8, shape[:-1] + (n,))
+    return w.numel() // cols, cols, group
+
+
+def w4_quantize(w, codes, scales, zeros=None, stream=None):
+    """moe_w4_quantize: bf16 w [..., rows, cols] -> codes uint8 [..., rows,
+    cols / 2], scales bf16 [..., rows, cols / group] and, if given, zeros uint8
+    of the scales' shape.  The shape of ``scales`` sets the group (32, 64, 128)."""
+    rows, cols, group = _check_w4(w, codes, scales, zeros)
+    _err(lib.moe_w4_quantize(rows, cols, group, w.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                             None if zeros is None else zeros.data_ptr(), _stream_ptr(stream)))
+    return codes, scales, zeros
+
+
+def w4_dequantize(codes, scales, zeros, w, stream=None):
+    """moe_w4_dequantize: the 4-bit weights' values as bf16 into w."""
+    rows, cols, group = _check_w4(w, codes, scales, zeros)
+    _err(lib.moe_w4_dequantize(rows, cols, group, codes.data_ptr(), scales.data_ptr(),
+                               None if zeros is None else zeros.data_ptr(), w.data_ptr(),
+                               _stream_ptr(stream)))
+    return w
+
+
+class _W4Weight(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp), ("zeros", _vp)]
+
+
+class W4Experts:
+    """The experts' SwiGLU product on 4-bit weights for decode batches, given
+    the routing (moe_w4_* of include/moe.h)."""
+
+    def __init__(self, d: int, f: int, E: int, k: int, shared_experts: int = 0, group: int = 128):
+        self.h = None
+        h = lib.moe_w4_create(d, f, E, k, shared_experts, group)
+        if not h:
+            raise MoEError(MOE_E_INVAL, (lib.moe_last_error() or b"").decode())
+        self.h = ctypes.c_void_p(h)
+        self.d, self.f, self.E, self.k, self.S, self.group = d, f, E, k, shared_experts, group
+        self._weights = self._device = None
+
+    def reserve(self, T_max: int, stream=None):
+        _err(lib.moe_w4_reserve(self.h, T_max, _stream_ptr(stream)))
+        self._device = _current_device()
+
+    def workspace_bytes(self, T_max: int) -> int:
+        return lib.moe_w4_workspace_bytes(self.h, T_max)
+
+    def set_weights(self, gate, up, down):
+        """Each of gate, up, down: (codes, scales, zeros or None), codes uint8
+        [E + S, rows, cols / 2], scales bf16 and zeros uint8 [E + S, rows, cols /
+        group]; rows, cols are f, d for gate and up and d, f for down."""
+        import torch
+        dev = _current_device()
+        n, args = self.E + self.S, []
+        for name, m, rows, cols in (("gate", gate, self.f, self.d), ("up", up, self.f, self.d),
+                                    ("down", down, self.d, self.f)):
+            codes, scales, zeros = m
+            _on_device(name + " codes", codes, dev, torch.uint8, (n, rows, cols // 2))
+            _on_device(name + " scales", scales, dev, torch.bfloat16, (n, rows, cols // self.group))
+            if zeros is not None:
+                _on_device(name + " zeros", zeros, dev, torch.uint8, (n, rows, cols // self.group))
+            args.append(_W4Weight(codes.data_ptr(), scales.data_ptr(),
+                                  None if zeros is None else zeros.data_ptr()))
+        _err(lib.moe_w4_set_weights(self.h, *(ctypes.byref(a) for a in args)))
+        self._weights = (tuple(gate), tuple(up), tuple(down))  # alive while the library holds their pointers
+
+    def forward(self, x, idx, w, out, stream=None):
+        """x [T, d] bf16, idx [T, k] int32 and w [T, k] fp32 (MoERouter.forward's)
+        -> out [T, d] bf16; slots with idx outside [0, E) add nothing."""
+        import torch
+        dev = _current_device()
+        if self._device is not None and dev != self._device:
+            raise MoEError(MOE_E_INVAL, f"the workspace is on device {self._device}, the current one is {dev}")
+        T = x.shape[0]
+        _on_device("x", x, dev, torch.bfloat16, (T, self.d))
+        _on_device("idx", idx, dev, torch.int32, (T, self.k))
+        _on_device("w", w, dev, torch.float32, (T, self.k))
+        _on_device("out", out, dev, torch.bfloat16, (T, self.d))
+        _err(lib.moe_w4_forward(self.h, T, x.data_ptr(), idx.data_ptr(), w.data_ptr(),
+                                out.data_ptr(), _stream_ptr(stream)))
+        return out
+
+    def close(self):
+        if self.h:
+            lib.moe_w4_destroy(self.h)
             self.h = None
 
     def __del__(self):

@@ -3,17 +3,18 @@ from __future__ import annotations
 
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 REPO = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "_build", "libmoe.so")
-SOURCES = ["moe.cu"]
-DEPS = ["moe.cu", "tasks.cuh", "layer.cuh", "ptx.cuh"]
+SOURCES = ["moe.cu", "router.cu", "w4.cu"]
+DEPS = SOURCES + ["tasks.cuh", "layer.cuh", "ptx.cuh", "error.h"]
 HEADER = os.path.join(REPO, "include", "moe.h")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-shared", "-Xcompiler", "-fPIC", "-cudart", "shared"]
+              "-Xcompiler", "-fPIC", "-cudart", "shared"]
 
 
 def _stale() -> bool:
@@ -31,11 +32,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, "-I", os.path.join(REPO, "include"), "-o", tmp,
-           *[os.path.join(CSRC, s) for s in SOURCES]]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+    flags = [*NVCC_FLAGS, *(["-Xptxas=-v"] if verbose else []), "-I", os.path.join(REPO, "include")]
+
+    def compile_one(src: str) -> str:
+        obj = f"{tmp}.{src}.o"
+        subprocess.run([nvcc, *flags, "-c", "-o", obj, os.path.join(CSRC, src)], check=True)
+        return obj
+
+    with ThreadPoolExecutor(len(SOURCES)) as ex:  # one compiler process per source
+        objs = list(ex.map(compile_one, SOURCES))
+    subprocess.run([nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *objs], check=True)
+    for obj in objs:
+        os.remove(obj)
     os.replace(tmp, LIB)
     return LIB
 

@@ -21,6 +21,7 @@
 #include <mutex>
 #include <string>
 
+#include "error.h"
 #include "layer.cuh"
 #include "tasks.cuh"
 
@@ -589,6 +590,14 @@ int cuda_fail(cudaError_t e, const char* what) {
   g_err = std::string(what) + ": " + cudaGetErrorString(e);
   return MOE_E_CUDA;
 }
+
+}  // namespace
+
+int moe::set_error(int code, const char* msg) { return fail(code, msg); }
+int moe::set_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+void moe::clear_error() { g_err.clear(); }
+
+namespace {
 
 #define CK(call)                                   \
   do {                                             \
