@@ -102,66 +102,569 @@ __global__ void __launch_bounds__(256)
 }
 
 // --------------------------------------------------------------------- experts
+//
+// Two kernels, gate/up then down, of the same shape.  An item is 64 weight
+// rows of one expert (gate/up: 32 of each) times a chunk of up to 8 NT of the
+// expert's token rows; a block of eight warps works an item off, its warps
+// taking the 128-column blocks of the product in turn, and adds the warps'
+// sums in shared memory.  Blocks stay resident and take items gridDim apart.
+//
+// A warp's unit is 64 rows x 128 columns: 4 KB of codes, copied
+// asynchronously into the warp's own ring of stages with the token rows'
+// 128 columns beside them, several units ahead and across items.  ldmatrix
+// hands each lane the 8 codes of a row's 32 columns that it needs; a code q
+// becomes the bf16 number 128 + q by placing it in the mantissa, 128 + zero
+// is taken off (exact in bf16), and the tensor core (mma.sync, weights as the
+// 16 rows, tokens as the 8 columns) sums a group's products in fp32 before the
+// scale multiplies the sum: no weight is rounded.  A code word's pairs come
+// out as columns (0, 4), (1, 5), (2, 6), (3, 7), so the tokens' columns are
+// paired the same way: x by byte permutes, h by the order gate/up stores it in.
+constexpr int kRows = 64;             // weight rows of an item
+constexpr int kBlockK = 128;          // columns of a unit
+constexpr int kWCodes = kRows * kBlockK / 2;
+constexpr int kItemWarps = 8;
+constexpr int kSms = 152;
+constexpr int kInline = 1024;         // slots up to which every block lists the experts' rows itself
+constexpr int kMaxSplit = 8;          // K splits of the down product
 
 struct Experts {
-  int T, d, f, E, k, S, group;
+  int T, d, f, E, k, S;
+  int splits;               // K splits of the down product
   Weight gate, up, down;
   const __nv_bfloat16* x;   // [T, d]
   const int* idx;           // [T, k]
   const float* w;           // [T, k]
-  __nv_bfloat16* h;         // [T k + T S, f]
+  __nv_bfloat16* h;         // [T k + T S, f], columns of each 8 in the order 0 4 1 5 2 6 3 7
+  float* y;                 // [splits, T k + T S, d]
+  int* arrived;             // [d / 64] items of a column tile done; zero between passes
+  void* list;               // List and Rows of a batch of more than kInline slots
+  uint16_t *list_slot, *list_row;
   __nv_bfloat16* out;       // [T, d]
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// The experts that have rows, in order.
+struct List {
+  int n_active;
+  int start[kMaxE + 2];          // first of each one's entries in slot and row
+  uint16_t expert[kMaxE + 2];
+};
+
+// Per token row of an expert: its slot (t k + j, and T k + t for the shared
+// expert) and the token.
+struct Rows {
+  uint16_t* slot;
+  uint16_t* row;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
 
-// Dot product of row r of expert e with v [cols], by one warp.
-__device__ float w4_dot(const Weight& m, long long r, int cols, int group, const __nv_bfloat16* v) {
-  const uint32_t* codes = reinterpret_cast<const uint32_t*>(m.codes + r * (cols / 2));
-  const long long g0 = r * (cols / group);
-  float sum = 0.f;
-  for (int i = threadIdx.x & 31; i < cols / 8; i += 32) {
-    const uint32_t word = codes[i];
-    const int g = i * 8 / group;
-    const float s = __bfloat162float(m.scales[g0 + g]), z = m.zeros ? (float)m.zeros[g0 + g] : 8.f;
-    float part = 0.f;
-    for (int j = 0; j < 8; ++j)
-      part += ((float)(word >> (4 * j) & 15u) - z) * __bfloat162float(v[i * 8 + j]);
-    sum += s * part;
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The pair (i, i + 4) of a word of 8 codes, less the zero point; base2 holds
+// 128 + zero twice.
+__device__ __forceinline__ uint32_t code_pair(uint32_t word, int i, uint32_t base2) {
+  return sub2(((word >> (4 * i)) & 0x000f000fu) | 0x43004300u, base2);
+}
+
+// Where column c of a row of h is stored.
+__device__ __forceinline__ int h_place(int c) { return (c & ~7) | ((c & 3) << 1) | (c >> 2 & 1); }
+
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// List the experts' rows (every thread of the block; count [kMaxE] and table
+// [32][kMaxE] are scratch).  Slots keep their order inside an expert, so every
+// block makes the same list.
+__device__ void make_list(const Experts& a, List* l, const Rows& rows, int* count, uint16_t* table) {
+  const int tid = threadIdx.x, lane = tid & 31, n = a.T * a.k;
+  for (int e = tid; e < kMaxE; e += blockDim.x) count[e] = 0;
+  __syncthreads();
+  auto expert_at = [&](int p) {  // -1: none
+    const int e = p < n ? __ldg(a.idx + p) : -1;
+    return (unsigned)e < (unsigned)a.E ? e : -1;
+  };
+  for (int p = tid; p < ((n + 31) & ~31); p += blockDim.x) {
+    const int e = expert_at(p);
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && lane == __ffs(same) - 1) atomicAdd(count + e, __popc(same));
   }
-  return warp_sum(sum);
-}
-
-// The expert of row p of h: slot p of idx, or the shared expert behind them.
-__device__ __forceinline__ int expert_of(const Experts& a, int p) {
-  return p < a.T * a.k ? a.idx[p] : a.E;
-}
-
-__global__ void w4_gate_up(Experts a) {
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5), p = blockIdx.y;
-  const int e = expert_of(a, p);
-  if (e < 0 || e > a.E || (e == a.E && p < a.T * a.k)) return;
-  const __nv_bfloat16* x = a.x + (size_t)(p < a.T * a.k ? p / a.k : p - a.T * a.k) * a.d;
-  const long long r = (long long)e * a.f + n;
-  const float z = w4_dot(a.gate, r, a.d, a.group, x), u = w4_dot(a.up, r, a.d, a.group, x);
-  if ((threadIdx.x & 31) == 0) a.h[(size_t)p * a.f + n] = __float2bfloat16(z / (1.f + expf(-z)) * u);
-}
-
-__global__ void w4_down(Experts a) {
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5), t = blockIdx.y;
-  float sum = 0.f;
-  for (int j = 0; j < a.k + a.S; ++j) {
-    const int p = j < a.k ? t * a.k + j : a.T * a.k + t;
-    const int e = j < a.k ? a.idx[p] : a.E;
-    if (e < 0 || (j < a.k && e >= a.E)) continue;
-    const float y = w4_dot(a.down, (long long)e * a.d + n, a.f, a.group, a.h + (size_t)p * a.f);
-    sum += j < a.k ? a.w[p] * y : y;
+  __syncthreads();
+  if (tid < 32) {  // one warp: 8 experts a lane
+    int c[8], sum = 0, act = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = count[lane * 8 + i];
+      sum += c[i];
+      act += c[i] > 0;
+    }
+    int s0 = sum, a0 = act;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int s1 = __shfl_up_sync(0xffffffffu, s0, o), a1 = __shfl_up_sync(0xffffffffu, a0, o);
+      if (lane >= o) s0 += s1, a0 += a1;
+    }
+    if (lane == 31) {
+      int na = a0, end = s0;
+      if (a.S) {  // the shared expert, every token
+        l->expert[na] = (uint16_t)a.E;
+        l->start[na++] = end;
+        end += a.T;
+      }
+      l->start[na] = end;
+      l->n_active = na;
+    }
+    s0 -= sum, a0 -= act;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      count[lane * 8 + i] = s0;  // from here on the expert's next entry
+      if (c[i] > 0) {
+        l->expert[a0] = (uint16_t)(lane * 8 + i);
+        l->start[a0++] = s0;
+        s0 += c[i];
+      }
+    }
   }
-  if ((threadIdx.x & 31) == 0) a.out[(size_t)t * a.d + n] = __float2bfloat16(sum);
+  // 1024 slots a round: what each run of 32 has of each expert, then where
+  // the run's first one goes
+  for (int p0 = 0; p0 < n; p0 += 1024) {
+    const int runs = min(32, (n - p0 + 31) / 32);
+    __syncthreads();
+    for (int i = tid; i < runs * kMaxE / 2; i += blockDim.x) reinterpret_cast<uint32_t*>(table)[i] = 0u;
+    __syncthreads();
+    for (int q = tid; q < runs * 32; q += blockDim.x) {
+      const int e = expert_at(p0 + q);
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      if (e >= 0 && lane == __ffs(same) - 1) table[(q >> 5) * kMaxE + e] = (uint16_t)__popc(same);
+    }
+    __syncthreads();
+    for (int e = tid; e < kMaxE; e += blockDim.x) {
+      int run = count[e];
+      for (int q = 0; q < runs; ++q) {
+        const int v = table[q * kMaxE + e];
+        table[q * kMaxE + e] = (uint16_t)run;
+        run += v;
+      }
+      count[e] = run;
+    }
+    __syncthreads();
+    for (int q = tid; q < runs * 32; q += blockDim.x) {
+      const int e = expert_at(p0 + q);
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      if (e >= 0) {
+        const int to = table[(q >> 5) * kMaxE + e] + __popc(same & ((1u << lane) - 1u));
+        rows.slot[to] = (uint16_t)(p0 + q);
+        rows.row[to] = (uint16_t)((p0 + q) / a.k);
+      }
+    }
+  }
+  __syncthreads();
+  if (a.S) {
+    const int first = l->start[l->n_active - 1];
+    for (int t = tid; t < a.T; t += blockDim.x) {
+      rows.slot[first + t] = (uint16_t)(n + t);
+      rows.row[first + t] = (uint16_t)t;
+    }
+  }
+  __syncthreads();
+}
+
+// The list of a larger batch, once for both products.
+__global__ void __launch_bounds__(1024) w4_list(Experts a) {
+  __shared__ int count[kMaxE];
+  __shared__ uint16_t table[32 * kMaxE];
+  __shared__ List l;
+  let_next_kernel_start();
+  make_list(a, &l, Rows{a.list_slot, a.list_row}, count, table);
+  for (int i = threadIdx.x; i < (int)sizeof(List) / 4; i += blockDim.x)
+    static_cast<int*>(a.list)[i] = reinterpret_cast<const int*>(&l)[i];
+}
+
+// One item: an expert, 64 of its rows, a K range and a chunk of token rows.
+struct Item {
+  int e, tile, split, rows, first, kb0, kb1;
+};
+
+template <int NT, bool DOWN, int G, bool Z>
+struct Shape {
+  static constexpr int kBytes = kWCodes + NT * 8 * kBlockK * 2;  // a stage
+  static constexpr int kStages = NT == 1 ? 4 : 3;
+  static constexpr int kRing = kBytes * kStages * kItemWarps;
+  static constexpr int kSum = kItemWarps * kRows * 8 * 4;        // the warps' sums of 8 columns
+  static constexpr int kLists = 2 * (kInline + kMaxT) * 2;        // slot and row
+  static constexpr int kSmem = kRing + kSum + kLists + (int)sizeof(List) + (kMaxE + 2) * 4;
+  static_assert(32 * kMaxE * 2 <= kRing && kMaxE * 4 <= kSum && kSmem <= 227 * 1024, "shared memory");
+};
+
+// One pass over the items for one of the two products.
+template <int NT, bool DOWN, int G, bool Z>
+__global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a) {
+  using Sh = Shape<NT, DOWN, G, Z>;
+  extern __shared__ __align__(128) char smem[];
+  char* ring_all = smem;
+  float* sums = reinterpret_cast<float*>(smem + Sh::kRing);
+  uint16_t* lists = reinterpret_cast<uint16_t*>(smem + Sh::kRing + Sh::kSum);
+  List* list = reinterpret_cast<List*>(smem + Sh::kRing + Sh::kSum + Sh::kLists);
+  int* item_start = reinterpret_cast<int*>(list + 1);  // [n_active + 1]
+  __shared__ int last_of_tile;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int K = DOWN ? a.f : a.d;
+  const int rows_of = DOWN ? a.d : a.f;                // weight rows of an expert
+  const int row_tiles = DOWN ? a.d / kRows : a.f / 32;
+  const int splits = DOWN ? a.splits : 1;
+  const int blocks_k = K / kBlockK;
+  constexpr int kChunk = NT * 8;
+  Rows rows{lists, lists + kInline + kMaxT};
+  if (a.T * a.k <= kInline) {
+    if (!DOWN) let_next_kernel_start();
+    make_list(a, list, rows, reinterpret_cast<int*>(sums), reinterpret_cast<uint16_t*>(ring_all));
+  } else {
+    // down starts only after every block of gate/up has seen the list complete
+    if (!DOWN) {
+      wait_for_previous_kernel();
+      let_next_kernel_start();
+    }
+    for (int i = tid; i < (int)sizeof(List) / 4; i += blockDim.x)
+      reinterpret_cast<int*>(list)[i] = __ldcg(static_cast<const int*>(a.list) + i);
+    rows = Rows{a.list_slot, a.list_row};
+    __syncthreads();
+  }
+  if (tid < 32) {  // items of the experts before each one
+    int base = 0;
+    for (int i0 = 0; i0 < list->n_active; i0 += 32) {
+      const int i = i0 + lane;
+      const int mine = i < list->n_active
+                           ? (list->start[i + 1] - list->start[i] + kChunk - 1) / kChunk * row_tiles * splits : 0;
+      int sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (i < list->n_active) item_start[i] = base + sum - mine;
+      base += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) item_start[list->n_active] = base;
+  }
+  __syncthreads();
+  const int n_items = item_start[list->n_active];
+
+  const uint32_t ring = smem_u32(ring_all) + warp * Sh::kStages * Sh::kBytes;
+  const long long kb_row = K / 2;                       // bytes of a row of codes
+  const int groups_row = K / G;
+  const Weight w0 = DOWN ? a.down : a.gate, w1 = DOWN ? a.down : a.up;
+
+  auto item_of = [&](int i, int* at, Item* it) {  // `at` only moves forward
+    while (i >= item_start[*at + 1]) ++*at;
+    const int n = list->start[*at + 1] - list->start[*at];
+    const int chunks = (n + kChunk - 1) / kChunk;
+    const int local = i - item_start[*at];
+    const int c = local % chunks, rest = local / chunks;
+    it->e = list->expert[*at];
+    it->split = DOWN ? rest % splits : 0;
+    it->tile = DOWN ? rest / splits : rest;
+    it->rows = min(kChunk, n - c * kChunk);
+    it->first = list->start[*at] + c * kChunk;
+    it->kb0 = DOWN ? blocks_k * it->split / splits : 0;
+    it->kb1 = DOWN ? blocks_k * (it->split + 1) / splits : blocks_k;
+  };
+
+  // ---- loads of one unit into a stage: the codes, the token rows
+  auto load_codes = [&](const Item& it, int kb, uint32_t stage) {
+    const int r = lane >> 2, c = lane & 3;
+    const uint32_t dst = stage + r * 64 + ((c ^ (r >> 1 & 3)) << 4);
+    const long long first = (long long)it.e * rows_of + (DOWN ? it.tile * kRows : it.tile * 32) + r;
+    const uint8_t* s0 = w0.codes + first * kb_row + kb * 64 + c * 16;
+    const uint8_t* s1 = DOWN ? s0 + 32 * kb_row : w1.codes + first * kb_row + kb * 64 + c * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cp_async16(dst + i * 512, s0 + i * 8 * kb_row);
+      cp_async16(dst + (i + 4) * 512, s1 + i * 8 * kb_row);
+    }
+  };
+  auto load_tokens = [&](const Item& it, int kb, uint32_t stage) {
+    // 16 lanes a row, 16 bytes each; odd rows' halves are swapped
+    const int tr = lane >> 4, tc = lane & 15;
+#pragma unroll
+    for (int i = 0; i < NT * 4; ++i) {
+      const int n = i * 2 + tr;
+      if (n < it.rows) {
+        const size_t row = (DOWN ? rows.slot : rows.row)[it.first + n];
+        const __nv_bfloat16* src = (DOWN ? a.h : a.x) + row * K + kb * kBlockK + tc * 8;
+        cp_async16(stage + kWCodes + n * 256 + ((tc ^ ((n & 1) << 2)) << 4), src);
+      }
+    }
+  };
+
+  // ---- scales (and zero points) of a unit: 8 rows a lane, 128 / G groups each
+  constexpr int kG = kBlockK / G;
+  struct Scales {
+    __nv_bfloat16 s[8][kG];
+    uint8_t z[8][Z ? kG : 1];
+  };
+  auto load_scales = [&](const Item& it, int kb, Scales* sc) {
+    const long long first = (long long)it.e * rows_of + (DOWN ? it.tile * kRows : it.tile * 32) + (lane >> 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long long r = first + (DOWN ? i * 8 : (i & 3) * 8);
+      const Weight& w = i < 4 ? w0 : w1;
+      const long long o = r * groups_row + kb * kG;
+      if constexpr (kG == 1) {
+        sc->s[i][0] = __ldg(w.scales + o);
+        if (Z) sc->z[i][0] = __ldg(w.zeros + o);
+      } else if constexpr (kG == 2) {
+        *reinterpret_cast<uint32_t*>(sc->s[i]) = __ldg(reinterpret_cast<const uint32_t*>(w.scales + o));
+        if (Z) *reinterpret_cast<uint16_t*>(sc->z[i]) = __ldg(reinterpret_cast<const uint16_t*>(w.zeros + o));
+      } else {
+        *reinterpret_cast<uint2*>(sc->s[i]) = __ldg(reinterpret_cast<const uint2*>(w.scales + o));
+        if (Z) *reinterpret_cast<uint32_t*>(sc->z[i]) = __ldg(reinterpret_cast<const uint32_t*>(w.zeros + o));
+      }
+    }
+  };
+
+  // ---- the cursor of the loads, kStages units ahead of the products
+  int l_item, l_at, l_kb;
+  Item l_it{};
+  bool l_more;
+  auto l_skip = [&]() {  // to a unit that exists (a warp may have none in an item)
+    while (l_more && l_kb >= l_it.kb1) {
+      l_item += gridDim.x;
+      l_more = l_item < n_items;
+      if (l_more) {
+        item_of(l_item, &l_at, &l_it);
+        l_kb = l_it.kb0 + warp;
+      }
+    }
+  };
+  auto l_first = [&]() {
+    l_item = blockIdx.x;
+    l_at = 0;
+    l_more = l_item < n_items;
+    if (l_more) {
+      item_of(l_item, &l_at, &l_it);
+      l_kb = l_it.kb0 + warp;
+      l_skip();
+    }
+  };
+  auto l_next = [&](int stage, bool codes, bool tokens) {
+    if (l_more) {
+      if (codes) load_codes(l_it, l_kb, ring + stage * Sh::kBytes);
+      if (tokens) load_tokens(l_it, l_kb, ring + stage * Sh::kBytes);
+      l_kb += kItemWarps;
+      l_skip();
+    }
+  };
+
+  // the codes wait for nobody: down's first stages load while gate/up ends
+  l_first();
+#pragma unroll 1
+  for (int s = 0; s < Sh::kStages; ++s) l_next(s, true, false);
+  if (DOWN) wait_for_previous_kernel();
+  l_first();
+#pragma unroll 1
+  for (int s = 0; s < Sh::kStages; ++s) {
+    l_next(s, false, true);
+    cp_async_commit();
+  }
+
+  int at = 0, stage = 0;
+  for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
+    Item it;
+    item_of(i, &at, &it);
+    float acc[4][NT][4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
+
+    Scales sc;
+    if (it.kb0 + warp < it.kb1) load_scales(it, it.kb0 + warp, &sc);
+    for (int kb = it.kb0 + warp; kb < it.kb1; kb += kItemWarps) {
+      Scales next;
+      if (kb + kItemWarps < it.kb1) load_scales(it, kb + kItemWarps, &next);
+      cp_async_wait<Sh::kStages - 1>();
+      __syncwarp();
+      const uint32_t st = ring + stage * Sh::kBytes;
+      // the tokens' pairs: b[n][c] for columns 32 c + 8 t .. + 7
+      uint4 b[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n * 8 >= it.rows) break;
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 v = lds128(st + kWCodes + (n * 8 + g) * 256 + (((4 * c + t) ^ ((g & 1) << 2)) << 4));
+          if (DOWN) b[n][c] = v;
+          else
+            b[n][c] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                 __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+        }
+      }
+      const int lr = lane & 15, lc = lane >> 4;  // ldmatrix: rows 0-15, chunk of the pair
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        uint32_t code[2][4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          ldmatrix4(st + (m * 16 + lr) * 64 + (((2 * q + lc) ^ (lr >> 1 & 3)) << 4), code[q]);
+#pragma unroll
+        for (int grp = 0; grp < kG; ++grp) {
+          float part[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) part[n][q] = 0.f;
+          uint32_t base0 = 0x43084308u, base1 = 0x43084308u;  // 128 + 8
+          if (Z) {
+            base0 = 0x43004300u + sc.z[2 * m][grp] * 0x00010001u;
+            base1 = 0x43004300u + sc.z[2 * m + 1][grp] * 0x00010001u;
+          }
+#pragma unroll
+          for (int c = grp * G / 32; c < (grp + 1) * G / 32; ++c) {
+            const uint32_t u = code[c >> 1][(c & 1) * 2], v = code[c >> 1][(c & 1) * 2 + 1];
+            uint32_t p0[4], p1[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              p0[q] = code_pair(u, q, base0);
+              p1[q] = code_pair(v, q, base1);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (n * 8 >= it.rows) break;
+              mma16816(part[n], p0[0], p1[0], p0[1], p1[1], b[n][c].x, b[n][c].y);
+              mma16816(part[n], p0[2], p1[2], p0[3], p1[3], b[n][c].z, b[n][c].w);
+            }
+          }
+          const float s0 = __bfloat162float(sc.s[2 * m][grp]), s1 = __bfloat162float(sc.s[2 * m + 1][grp]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc[m][n][0] += s0 * part[n][0];
+            acc[m][n][1] += s0 * part[n][1];
+            acc[m][n][2] += s1 * part[n][2];
+            acc[m][n][3] += s1 * part[n][3];
+          }
+        }
+      }
+      __syncwarp();
+      l_next(stage, true, true);
+      cp_async_commit();
+      stage = stage + 1 == Sh::kStages ? 0 : stage + 1;
+      sc = next;
+    }
+
+    // the warps' sums: [warp][row][8 columns], 8 token rows at a time
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (n * 8 >= it.rows) break;
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        float2* d0 = reinterpret_cast<float2*>(sums + (warp * kRows + m * 16 + (lane >> 2)) * 8 + (lane & 3) * 2);
+        d0[0] = make_float2(acc[m][n][0], acc[m][n][1]);
+        d0[8 * 8 / 2] = make_float2(acc[m][n][2], acc[m][n][3]);
+      }
+      __syncthreads();
+      if constexpr (!DOWN) {
+        const int r = tid >> 3, col = n * 8 + (tid & 7);
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int q = 0; q < kItemWarps; ++q) {
+          g += sums[(q * kRows + r) * 8 + (tid & 7)];
+          u += sums[(q * kRows + 32 + r) * 8 + (tid & 7)];
+        }
+        if (col < it.rows)  // the one rounding between the two products
+          a.h[(size_t)rows.slot[it.first + col] * a.f + h_place(it.tile * 32 + r)] = __float2bfloat16(g / (1.f + expf(-g)) * u);
+      } else {
+        const int c = tid >> 5, col = n * 8 + c;
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          const int r = (tid & 31) + o * 32;
+          float y = 0.f;
+#pragma unroll
+          for (int q = 0; q < kItemWarps; ++q) y += sums[(q * kRows + r) * 8 + c];
+          if (col < it.rows)
+            a.y[((size_t)it.split * (a.T * (a.k + a.S)) + rows.slot[it.first + col]) * a.d + it.tile * kRows + r] = y;
+        }
+      }
+      if (DOWN) __threadfence();
+      __syncthreads();
+    }
+
+    if constexpr (DOWN) {
+      // the item that completes a column tile adds its slots, in slot order
+      if (tid == 0) {
+        const int expected = n_items / row_tiles;
+        const int done = atomicAdd(a.arrived + it.tile, 1) + 1;
+        if (done == expected) a.arrived[it.tile] = 0;
+        last_of_tile = done == expected;
+      }
+      __syncthreads();
+      if (last_of_tile) {
+        __threadfence();
+        const size_t slots = (size_t)a.T * (a.k + a.S);
+        const int col = it.tile * kRows + (tid & 31) * 2;
+        for (int t = tid >> 5; t < a.T; t += kItemWarps) {
+          float2 o = make_float2(0.f, 0.f);
+          for (int j = 0; j < a.k + a.S; ++j) {
+            const int p = j < a.k ? t * a.k + j : a.T * a.k + t;
+            if (j < a.k && (unsigned)__ldg(a.idx + p) >= (unsigned)a.E) continue;
+            float2 y = make_float2(0.f, 0.f);
+            for (int q = 0; q < splits; ++q) {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(a.y + ((size_t)q * slots + p) * a.d + col));
+              y.x += v.x;
+              y.y += v.y;
+            }
+            const float wj = j < a.k ? __ldg(a.w + p) : 1.f;
+            o.x += wj * y.x;
+            o.y += wj * y.y;
+          }
+          *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)t * a.d + col) = __floats2bfloat162_rn(o.x, o.y);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (DOWN && n_items == 0) {  // no slot has an expert
+    for (long long i = (long long)blockIdx.x * blockDim.x + tid; i < (long long)a.T * a.d / 2; i += (long long)gridDim.x * blockDim.x)
+      reinterpret_cast<uint32_t*>(a.out)[i] = 0u;
+  }
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -199,7 +702,80 @@ struct moe_w4 {
 
 namespace {
 
-long long workspace(const moe_w4* h, int T) { return (long long)T * (h->k + h->S) * h->f * 2; }
+// K splits of the down product: few tokens read few experts, and d / 64 row
+// tiles of those alone would leave SMs idle.  In units of a warp's 128
+// columns, a pass takes the items of the fullest block times an item's units
+// (and about half a unit to add the warps' sums up); the split with the least.
+int down_splits(const moe_w4* h, int T) {
+  const long long experts = std::min<long long>(h->E, (long long)T * h->k) + h->S;
+  const long long items = experts * (h->d / kRows);
+  const int blocks = h->f / kBlockK;
+  int best = 1;
+  long long least = 0;
+  for (int s = 1; s <= kMaxSplit && s <= blocks; ++s) {
+    const long long waves = (items * s + kSms - 1) / kSms;
+    const long long units = ((blocks + s - 1) / s + kItemWarps - 1) / kItemWarps;
+    const long long cost = waves * (2 * units + 1);
+    if (s == 1 || cost < least) least = cost, best = s;
+  }
+  return best;
+}
+
+struct Layout {
+  size_t y, arrived, list, slot, row, bytes;
+};
+
+Layout layout(const moe_w4* h, int T_max) {
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  const size_t slots = (size_t)T_max * (h->k + h->S);
+  size_t y = 0;  // shorter batches may split more
+  for (int T = 1; T <= T_max; ++T) y = std::max(y, (size_t)T * (h->k + h->S) * h->d * 4 * down_splits(h, T));
+  Layout l;
+  l.y = up(slots * h->f * 2);
+  l.arrived = l.y + up(y);
+  l.list = l.arrived + up((size_t)h->d / kRows * 4);
+  l.slot = l.list + up(sizeof(List));
+  l.row = l.slot + up(slots * 2);
+  l.bytes = l.row + up(slots * 2);
+  return l;
+}
+
+cudaError_t launch_after(void (*kernel)(Experts), int grid, int threads, int smem, bool overlap, cudaStream_t s,
+                         const Experts& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+struct Kernels {
+  void (*gate_up)(Experts);
+  void (*down)(Experts);
+  int smem;
+};
+
+template <int NT, int G, bool Z>
+Kernels kernels_of() {
+  return Kernels{w4_experts<NT, false, G, Z>, w4_experts<NT, true, G, Z>, Shape<NT, false, G, Z>::kSmem};
+}
+
+Kernels kernels(int nt, int group, bool zeros) {
+  if (nt == 1) {
+    if (group == 32) return zeros ? kernels_of<1, 32, true>() : kernels_of<1, 32, false>();
+    if (group == 64) return zeros ? kernels_of<1, 64, true>() : kernels_of<1, 64, false>();
+    return zeros ? kernels_of<1, 128, true>() : kernels_of<1, 128, false>();
+  }
+  if (group == 32) return zeros ? kernels_of<2, 32, true>() : kernels_of<2, 32, false>();
+  if (group == 64) return zeros ? kernels_of<2, 64, true>() : kernels_of<2, 64, false>();
+  return zeros ? kernels_of<2, 128, true>() : kernels_of<2, 128, false>();
+}
 
 }  // namespace
 
@@ -258,7 +834,7 @@ moe_w4_t* moe_w4_create(int d, int f, int E, int k, int shared_experts, int grou
 }
 
 long long moe_w4_workspace_bytes(const moe_w4_t* h, int T_max) {
-  return !h || T_max < 0 || T_max > kMaxT ? -1 : workspace(h, T_max);
+  return !h || T_max < 0 || T_max > kMaxT ? -1 : (long long)layout(h, T_max).bytes;
 }
 
 int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
@@ -278,14 +854,21 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
     h->T_max = 0;
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_reserve");
-  const size_t bytes = (size_t)workspace(h, T_max);
+  const size_t bytes = layout(h, T_max).bytes;
   if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
     h->ws = nullptr;
     cudaGetLastError();
     return moe::set_error(MOE_E_NOMEM, "workspace allocation failed");
   }
   e = cudaMemsetAsync(h->ws, 0, bytes, s);
-  if (e != cudaSuccess) return moe::set_cuda_error(e, "cudaMemsetAsync");
+  for (int nt = 1; nt <= 2 && e == cudaSuccess; ++nt)
+    for (int z = 0; z < 2 && e == cudaSuccess; ++z) {
+      const Kernels kn = kernels(nt, h->group, z);
+      e = cudaFuncSetAttribute((const void*)kn.gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, kn.smem);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute((const void*)kn.down, cudaFuncAttributeMaxDynamicSharedMemorySize, kn.smem);
+    }
+  if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_reserve");
   h->T_max = T_max;
   moe::clear_error();
   return MOE_OK;
@@ -321,12 +904,35 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   if (!x || !idx || !w || !out) return moe::set_error(MOE_E_INVAL, "null tensor pointer");
   if (!aligned(x, 16) || !aligned(out, 16) || !aligned(idx, 4) || !aligned(w, 4))
     return moe::set_error(MOE_E_INVAL, "x and out must be 16-byte aligned, idx and w 4-byte");
-  Experts a{T, h->d, h->f, h->E, h->k, h->S, h->group, h->gate, h->up, h->down,
-            static_cast<const __nv_bfloat16*>(x), idx, w, reinterpret_cast<__nv_bfloat16*>(h->ws),
-            static_cast<__nv_bfloat16*>(out)};
+  const Layout l = layout(h, h->T_max);
+  Experts a;
+  a.T = T;
+  a.d = h->d;
+  a.f = h->f;
+  a.E = h->E;
+  a.k = h->k;
+  a.S = h->S;
+  a.splits = down_splits(h, T);
+  a.gate = h->gate;
+  a.up = h->up;
+  a.down = h->down;
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.idx = idx;
+  a.w = w;
+  a.h = reinterpret_cast<__nv_bfloat16*>(h->ws);
+  a.y = reinterpret_cast<float*>(h->ws + l.y);
+  a.arrived = reinterpret_cast<int*>(h->ws + l.arrived);
+  a.list = h->ws + l.list;
+  a.list_slot = reinterpret_cast<uint16_t*>(h->ws + l.slot);
+  a.list_row = reinterpret_cast<uint16_t*>(h->ws + l.row);
+  a.out = static_cast<__nv_bfloat16*>(out);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch(w4_gate_up, dim3(h->f / 8, T * (h->k + h->S)), 256, s, a);
-  if (e == cudaSuccess) e = launch(w4_down, dim3(h->d / 8, T), 256, s, a);
+  const Kernels kn = kernels(T <= 8 ? 1 : 2, h->group, h->gate.zeros != nullptr);
+  const bool listed = T * h->k > kInline;
+  cudaError_t e = cudaSuccess;
+  if (listed) e = launch_after(w4_list, 1, 1024, 0, false, s, a);
+  if (e == cudaSuccess) e = launch_after(kn.gate_up, kSms, kItemWarps * 32, kn.smem, listed, s, a);
+  if (e == cudaSuccess) e = launch_after(kn.down, kSms, kItemWarps * 32, kn.smem, true, s, a);
   return e == cudaSuccess ? MOE_OK : moe::set_cuda_error(e, "w4_experts");
 }
 
