@@ -104,28 +104,41 @@ __global__ void __launch_bounds__(256)
 // --------------------------------------------------------------------- experts
 //
 // Two kernels, gate/up then down, of the same shape.  An item is 64 weight
-// rows of one expert (gate/up: 32 of each) times a chunk of up to 8 NT of the
-// expert's token rows; a block of eight warps works an item off, its warps
-// taking the 128-column blocks of the product in turn, and adds the warps'
-// sums in shared memory.  Blocks stay resident and take items gridDim apart.
+// rows of one expert (gate/up: 32 of each) times up to 8 of the expert's token
+// rows; a block of eight warps works an item off, its warps taking the
+// 128-column blocks of the product in turn, and adds the warps' sums in shared
+// memory.  Blocks stay resident, two to an SM, and take items gridDim apart.
 //
 // A warp's unit is 64 rows x 128 columns: 4 KB of codes, copied
-// asynchronously into the warp's own ring of stages with the token rows'
-// 128 columns beside them, several units ahead and across items.  ldmatrix
-// hands each lane the 8 codes of a row's 32 columns that it needs; a code q
-// becomes the bf16 number 128 + q by placing it in the mantissa, 128 + zero
-// is taken off (exact in bf16), and the tensor core (mma.sync, weights as the
-// 16 rows, tokens as the 8 columns) sums a group's products in fp32 before the
-// scale multiplies the sum: no weight is rounded.  A code word's pairs come
-// out as columns (0, 4), (1, 5), (2, 6), (3, 7), so the tokens' columns are
-// paired the same way: x by byte permutes, h by the order gate/up stores it in.
+// asynchronously into the warp's own ring of two stages with the token rows'
+// 128 columns beside them, across items.  ldmatrix hands each lane the word of
+// 8 codes (one row, 8 columns) that it needs of a 32-column chunk.
+//
+// Codes to numbers: a bf16 whose bits are the integer n < 256 is n 2^-133
+// (below 128 a subnormal, from there on the first binade, with the same
+// spacing), and mma.sync takes subnormal operands as they are.  So the codes
+// of columns (0, 4) and (2, 6) are an AND with 000f000f of the word and the
+// word shifted by 8, those of (1, 5) and (3, 7) an AND with 00f000f0, 16 times
+// larger: five instructions for 8 codes.  The tokens' columns are paired the
+// same way and scaled by 2^64, the 16-fold ones by 2^60, both exact in bf16;
+// with |x| below 2^64 nothing overflows, and what is below 2^-57 counts as
+// zero.  A group's sum of q x comes out as an fp32 sum of exact products; the
+// sum of x over the group, from one more mma whose weights are ones, takes the
+// zero point off: scale * 2^69 * (sum q x - zero * sum x).  No weight is
+// rounded.
 constexpr int kRows = 64;             // weight rows of an item
+constexpr int kChunk = 8;             // token rows of an item
 constexpr int kBlockK = 128;          // columns of a unit
-constexpr int kWCodes = kRows * kBlockK / 2;
+constexpr int kCodeBytes = kRows * kBlockK / 2;
+constexpr int kStageBytes = kCodeBytes + kChunk * kBlockK * 2;
+constexpr int kStages = 2;
 constexpr int kItemWarps = 8;
+constexpr int kBlocksSm = 2;
 constexpr int kSms = 152;
-constexpr int kInline = 1024;         // slots up to which every block lists the experts' rows itself
+constexpr int kInline = 32;           // slots up to which every block lists the experts' rows itself
 constexpr int kMaxSplit = 8;          // K splits of the down product
+constexpr uint32_t kScaleX = 0x5f805f80u, kScaleX16 = 0x5d805d80u;  // 2^64, 2^60 twice
+constexpr float kUnscale = 5.9029581035870565e20f;                  // 2^69
 
 struct Experts {
   int T, d, f, E, k, S;
@@ -134,7 +147,9 @@ struct Experts {
   const __nv_bfloat16* x;   // [T, d]
   const int* idx;           // [T, k]
   const float* w;           // [T, k]
-  __nv_bfloat16* h;         // [T k + T S, f], columns of each 8 in the order 0 4 1 5 2 6 3 7
+  // [T k + T S, f], columns of each 8 in the order 0 4 1 5 2 6 3 7, scaled as
+  // the product takes them
+  __nv_bfloat16* h;
   float* y;                 // [splits, T k + T S, d]
   int* arrived;             // [d / 64] items of a column tile done; zero between passes
   void* list;               // List and Rows of a batch of more than kInline slots
@@ -142,7 +157,7 @@ struct Experts {
   __nv_bfloat16* out;       // [T, d]
 };
 
-// The experts that have rows, in order.
+// The experts that have rows, in order (up to kInline slots: of appearance).
 struct List {
   int n_active;
   int start[kMaxE + 2];          // first of each one's entries in slot and row
@@ -183,45 +198,93 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+// c = A B + c, or A B alone for the first of a sum.
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                         uint32_t b0, uint32_t b1, bool first) {
+  if (first)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
-// The pair (i, i + 4) of a word of 8 codes, less the zero point; base2 holds
-// 128 + zero twice.
-__device__ __forceinline__ uint32_t code_pair(uint32_t word, int i, uint32_t base2) {
-  return sub2(((word >> (4 * i)) & 0x000f000fu) | 0x43004300u, base2);
-}
-
-// Where column c of a row of h is stored.
+// Where column c of a row of h is stored, and 2^64 or 2^60.
 __device__ __forceinline__ int h_place(int c) { return (c & ~7) | ((c & 3) << 1) | (c >> 2 & 1); }
+__device__ __forceinline__ float h_scale(int c) { return c & 1 ? 1152921504606846976.f : 18446744073709551616.f; }
 
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// List the experts' rows (every thread of the block; count [kMaxE] and table
-// [32][kMaxE] are scratch).  Slots keep their order inside an expert, so every
-// block makes the same list.
-__device__ void make_list(const Experts& a, List* l, const Rows& rows, int* count, uint16_t* table) {
-  const int tid = threadIdx.x, lane = tid & 31, n = a.T * a.k;
-  for (int e = tid; e < kMaxE; e += blockDim.x) count[e] = 0;
+// The expert of slot p, or -1 if it has none.
+__device__ __forceinline__ int expert_at(const Experts& a, int p) {
+  const int e = p < a.T * a.k ? __ldg(a.idx + p) : -1;
+  return (unsigned)e < (unsigned)a.E ? e : -1;
+}
+
+// The list of at most 32 slots, by the first warp alone.
+__device__ void list_few(const Experts& a, List* l, const Rows& rows) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int e = expert_at(a, lane);
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const bool leads = e >= 0 && lane == __ffs(same) - 1;
+    const unsigned leaders = __ballot_sync(0xffffffffu, leads);
+    int sum = leads ? __popc(same) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const int all = __shfl_sync(0xffffffffu, sum, 31);
+    const int start = __shfl_sync(0xffffffffu, leads ? sum - __popc(same) : 0, __ffs(same) - 1);
+    if (leads) {
+      const int at = __popc(leaders & ((1u << lane) - 1u));
+      l->expert[at] = (uint16_t)e;
+      l->start[at] = start;
+    }
+    if (e >= 0) {
+      const int to = start + __popc(same & ((1u << lane) - 1u));
+      rows.slot[to] = (uint16_t)lane;
+      rows.row[to] = (uint16_t)(lane / a.k);
+    }
+    if (lane == 0) {
+      int n = __popc(leaders);
+      l->start[n] = all;
+      if (a.S) {
+        l->expert[n++] = (uint16_t)a.E;
+        l->start[n] = all + a.T;
+      }
+      l->n_active = n;
+    }
+    if (a.S && lane < a.T) {
+      rows.slot[all + lane] = (uint16_t)(a.T * a.k + lane);
+      rows.row[all + lane] = (uint16_t)lane;
+    }
+  }
   __syncthreads();
-  auto expert_at = [&](int p) {  // -1: none
-    const int e = p < n ? __ldg(a.idx + p) : -1;
-    return (unsigned)e < (unsigned)a.E ? e : -1;
-  };
-  for (int p = tid; p < ((n + 31) & ~31); p += blockDim.x) {
-    const int e = expert_at(p);
+}
+
+// The list of a larger batch, once for both products: one block.  Slots keep
+// their order inside an expert.
+__global__ void __launch_bounds__(1024) w4_list(Experts a) {
+  __shared__ int count[kMaxE];
+  __shared__ uint16_t table[32][kMaxE];
+  __shared__ List l;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.T * a.k;
+  let_next_kernel_start();
+  if (tid < kMaxE) count[tid] = 0;
+  __syncthreads();
+  for (int p = tid; p < ((n + 31) & ~31); p += 1024) {
+    const int e = expert_at(a, p);
     const unsigned same = __match_any_sync(0xffffffffu, e);
     if (e >= 0 && lane == __ffs(same) - 1) atomicAdd(count + e, __popc(same));
   }
@@ -241,78 +304,62 @@ __device__ void make_list(const Experts& a, List* l, const Rows& rows, int* coun
       if (lane >= o) s0 += s1, a0 += a1;
     }
     if (lane == 31) {
-      int na = a0, end = s0;
-      if (a.S) {  // the shared expert, every token
-        l->expert[na] = (uint16_t)a.E;
-        l->start[na++] = end;
-        end += a.T;
+      int na = a0;
+      l.start[na] = s0;
+      if (a.S) {
+        l.expert[na++] = (uint16_t)a.E;
+        l.start[na] = s0 + a.T;
       }
-      l->start[na] = end;
-      l->n_active = na;
+      l.n_active = na;
     }
     s0 -= sum, a0 -= act;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       count[lane * 8 + i] = s0;  // from here on the expert's next entry
       if (c[i] > 0) {
-        l->expert[a0] = (uint16_t)(lane * 8 + i);
-        l->start[a0++] = s0;
+        l.expert[a0] = (uint16_t)(lane * 8 + i);
+        l.start[a0++] = s0;
         s0 += c[i];
       }
     }
   }
-  // 1024 slots a round: what each run of 32 has of each expert, then where
-  // the run's first one goes
+  // 1024 slots a round: what each warp's 32 have of each expert, then where
+  // the warp's first one goes
   for (int p0 = 0; p0 < n; p0 += 1024) {
-    const int runs = min(32, (n - p0 + 31) / 32);
     __syncthreads();
-    for (int i = tid; i < runs * kMaxE / 2; i += blockDim.x) reinterpret_cast<uint32_t*>(table)[i] = 0u;
+    for (int i = tid; i < 32 * kMaxE / 2; i += 1024) reinterpret_cast<uint32_t*>(table)[i] = 0u;
     __syncthreads();
-    for (int q = tid; q < runs * 32; q += blockDim.x) {
-      const int e = expert_at(p0 + q);
-      const unsigned same = __match_any_sync(0xffffffffu, e);
-      if (e >= 0 && lane == __ffs(same) - 1) table[(q >> 5) * kMaxE + e] = (uint16_t)__popc(same);
-    }
+    const int p = p0 + tid;
+    const int e = expert_at(a, p);
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && lane == __ffs(same) - 1) table[warp][e] = (uint16_t)__popc(same);
     __syncthreads();
-    for (int e = tid; e < kMaxE; e += blockDim.x) {
-      int run = count[e];
-      for (int q = 0; q < runs; ++q) {
-        const int v = table[q * kMaxE + e];
-        table[q * kMaxE + e] = (uint16_t)run;
+    if (tid < kMaxE) {
+      int run = count[tid];
+#pragma unroll 8
+      for (int q = 0; q < 32; ++q) {
+        const int v = table[q][tid];
+        table[q][tid] = (uint16_t)run;
         run += v;
       }
-      count[e] = run;
+      count[tid] = run;
     }
     __syncthreads();
-    for (int q = tid; q < runs * 32; q += blockDim.x) {
-      const int e = expert_at(p0 + q);
-      const unsigned same = __match_any_sync(0xffffffffu, e);
-      if (e >= 0) {
-        const int to = table[(q >> 5) * kMaxE + e] + __popc(same & ((1u << lane) - 1u));
-        rows.slot[to] = (uint16_t)(p0 + q);
-        rows.row[to] = (uint16_t)((p0 + q) / a.k);
-      }
+    if (e >= 0) {
+      const int to = table[warp][e] + __popc(same & ((1u << lane) - 1u));
+      a.list_slot[to] = (uint16_t)p;
+      a.list_row[to] = (uint16_t)(p / a.k);
     }
   }
   __syncthreads();
   if (a.S) {
-    const int first = l->start[l->n_active - 1];
-    for (int t = tid; t < a.T; t += blockDim.x) {
-      rows.slot[first + t] = (uint16_t)(n + t);
-      rows.row[first + t] = (uint16_t)t;
+    const int first = l.start[l.n_active - 1];
+    for (int t = tid; t < a.T; t += 1024) {
+      a.list_slot[first + t] = (uint16_t)(n + t);
+      a.list_row[first + t] = (uint16_t)t;
     }
   }
-  __syncthreads();
-}
-
-// The list of a larger batch, once for both products.
-__global__ void __launch_bounds__(1024) w4_list(Experts a) {
-  __shared__ int count[kMaxE];
-  __shared__ uint16_t table[32 * kMaxE];
-  __shared__ List l;
-  let_next_kernel_start();
-  make_list(a, &l, Rows{a.list_slot, a.list_row}, count, table);
-  for (int i = threadIdx.x; i < (int)sizeof(List) / 4; i += blockDim.x)
+  for (int i = tid; i < (int)sizeof(List) / 4; i += 1024)
     static_cast<int*>(a.list)[i] = reinterpret_cast<const int*>(&l)[i];
 }
 
@@ -321,27 +368,20 @@ struct Item {
   int e, tile, split, rows, first, kb0, kb1;
 };
 
-template <int NT, bool DOWN, int G, bool Z>
-struct Shape {
-  static constexpr int kBytes = kWCodes + NT * 8 * kBlockK * 2;  // a stage
-  static constexpr int kStages = NT == 1 ? 4 : 3;
-  static constexpr int kRing = kBytes * kStages * kItemWarps;
-  static constexpr int kSum = kItemWarps * kRows * 8 * 4;        // the warps' sums of 8 columns
-  static constexpr int kLists = 2 * (kInline + kMaxT) * 2;        // slot and row
-  static constexpr int kSmem = kRing + kSum + kLists + (int)sizeof(List) + (kMaxE + 2) * 4;
-  static_assert(32 * kMaxE * 2 <= kRing && kMaxE * 4 <= kSum && kSmem <= 227 * 1024, "shared memory");
-};
+constexpr int kRing = kStageBytes * kStages * kItemWarps;
+constexpr int kSum = kItemWarps * kRows / 2 * kChunk * 4;  // the warps' sums of half the rows
+constexpr int kInlineRows = 2 * kInline;                   // slots, and the shared expert's tokens
+constexpr int kSmem = kRing + kSum + (int)sizeof(List) + (kMaxE + 2) * 4 + 2 * kInlineRows * 2;
+static_assert(kSmem <= 113 * 1024, "two blocks to an SM");
 
 // One pass over the items for one of the two products.
-template <int NT, bool DOWN, int G, bool Z>
-__global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a) {
-  using Sh = Shape<NT, DOWN, G, Z>;
+template <bool DOWN, int G, bool Z>
+__global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const Experts a) {
   extern __shared__ __align__(128) char smem[];
-  char* ring_all = smem;
-  float* sums = reinterpret_cast<float*>(smem + Sh::kRing);
-  uint16_t* lists = reinterpret_cast<uint16_t*>(smem + Sh::kRing + Sh::kSum);
-  List* list = reinterpret_cast<List*>(smem + Sh::kRing + Sh::kSum + Sh::kLists);
+  float* sums = reinterpret_cast<float*>(smem + kRing);
+  List* list = reinterpret_cast<List*>(smem + kRing + kSum);
   int* item_start = reinterpret_cast<int*>(list + 1);  // [n_active + 1]
+  uint16_t* few = reinterpret_cast<uint16_t*>(item_start + kMaxE + 2);
   __shared__ int last_of_tile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = DOWN ? a.f : a.d;
@@ -349,11 +389,10 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
   const int row_tiles = DOWN ? a.d / kRows : a.f / 32;
   const int splits = DOWN ? a.splits : 1;
   const int blocks_k = K / kBlockK;
-  constexpr int kChunk = NT * 8;
-  Rows rows{lists, lists + kInline + kMaxT};
+  Rows rows{few, few + kInlineRows};
   if (a.T * a.k <= kInline) {
     if (!DOWN) let_next_kernel_start();
-    make_list(a, list, rows, reinterpret_cast<int*>(sums), reinterpret_cast<uint16_t*>(ring_all));
+    list_few(a, list, rows);
   } else {
     // down starts only after every block of gate/up has seen the list complete
     if (!DOWN) {
@@ -365,27 +404,28 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
     rows = Rows{a.list_slot, a.list_row};
     __syncthreads();
   }
+  const int n_active = list->n_active;
   if (tid < 32) {  // items of the experts before each one
     int base = 0;
-    for (int i0 = 0; i0 < list->n_active; i0 += 32) {
+    for (int i0 = 0; i0 < n_active; i0 += 32) {
       const int i = i0 + lane;
-      const int mine = i < list->n_active
-                           ? (list->start[i + 1] - list->start[i] + kChunk - 1) / kChunk * row_tiles * splits : 0;
+      const int mine =
+          i < n_active ? (list->start[i + 1] - list->start[i] + kChunk - 1) / kChunk * row_tiles * splits : 0;
       int sum = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += v;
       }
-      if (i < list->n_active) item_start[i] = base + sum - mine;
+      if (i < n_active) item_start[i] = base + sum - mine;
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 0) item_start[list->n_active] = base;
+    if (lane == 0) item_start[n_active] = base;
   }
   __syncthreads();
-  const int n_items = item_start[list->n_active];
+  const int n_items = item_start[n_active];
 
-  const uint32_t ring = smem_u32(ring_all) + warp * Sh::kStages * Sh::kBytes;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
   const long long kb_row = K / 2;                       // bytes of a row of codes
   const int groups_row = K / G;
   const Weight w0 = DOWN ? a.down : a.gate, w1 = DOWN ? a.down : a.up;
@@ -393,25 +433,36 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
   auto item_of = [&](int i, int* at, Item* it) {  // `at` only moves forward
     while (i >= item_start[*at + 1]) ++*at;
     const int n = list->start[*at + 1] - list->start[*at];
-    const int chunks = (n + kChunk - 1) / kChunk;
     const int local = i - item_start[*at];
-    const int c = local % chunks, rest = local / chunks;
+    int c = 0, rest = local;
+    if (n > kChunk) {  // chunks of the same weights side by side
+      const int chunks = (n + kChunk - 1) / kChunk;
+      rest = local / chunks;
+      c = local - rest * chunks;
+    }
     it->e = list->expert[*at];
-    it->split = DOWN ? rest % splits : 0;
-    it->tile = DOWN ? rest / splits : rest;
+    it->split = 0;
+    it->tile = rest;
+    it->kb0 = 0;
+    it->kb1 = blocks_k;
+    if (DOWN && splits > 1) {
+      it->tile = rest / splits;
+      it->split = rest - it->tile * splits;
+      it->kb0 = blocks_k * it->split / splits;
+      it->kb1 = blocks_k * (it->split + 1) / splits;
+    }
     it->rows = min(kChunk, n - c * kChunk);
     it->first = list->start[*at] + c * kChunk;
-    it->kb0 = DOWN ? blocks_k * it->split / splits : 0;
-    it->kb1 = DOWN ? blocks_k * (it->split + 1) / splits : blocks_k;
   };
 
   // ---- loads of one unit into a stage: the codes, the token rows
+  const int lr8 = lane >> 2, lc4 = lane & 3;
   auto load_codes = [&](const Item& it, int kb, uint32_t stage) {
-    const int r = lane >> 2, c = lane & 3;
-    const uint32_t dst = stage + r * 64 + ((c ^ (r >> 1 & 3)) << 4);
-    const long long first = (long long)it.e * rows_of + (DOWN ? it.tile * kRows : it.tile * 32) + r;
-    const uint8_t* s0 = w0.codes + first * kb_row + kb * 64 + c * 16;
-    const uint8_t* s1 = DOWN ? s0 + 32 * kb_row : w1.codes + first * kb_row + kb * 64 + c * 16;
+    const uint32_t dst = stage + lr8 * 64 + ((lc4 ^ (lr8 >> 1 & 3)) << 4);
+    const long long first = (long long)it.e * rows_of + (DOWN ? it.tile * kRows : it.tile * 32) + lr8;
+    const long long o = first * kb_row + kb * 64 + lc4 * 16;
+    const uint8_t* s0 = w0.codes + o;
+    const uint8_t* s1 = DOWN ? s0 + 32 * kb_row : w1.codes + o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       cp_async16(dst + i * 512, s0 + i * 8 * kb_row);
@@ -421,15 +472,12 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
   auto load_tokens = [&](const Item& it, int kb, uint32_t stage) {
     // 16 lanes a row, 16 bytes each; odd rows' halves are swapped
     const int tr = lane >> 4, tc = lane & 15;
+    const uint16_t* row = (DOWN ? rows.slot : rows.row) + it.first + tr;
+    const __nv_bfloat16* from = (DOWN ? a.h : a.x) + kb * kBlockK + tc * 8;
+    const uint32_t dst = stage + kCodeBytes + tr * 256 + ((tc ^ (tr << 2)) << 4);
 #pragma unroll
-    for (int i = 0; i < NT * 4; ++i) {
-      const int n = i * 2 + tr;
-      if (n < it.rows) {
-        const size_t row = (DOWN ? rows.slot : rows.row)[it.first + n];
-        const __nv_bfloat16* src = (DOWN ? a.h : a.x) + row * K + kb * kBlockK + tc * 8;
-        cp_async16(stage + kWCodes + n * 256 + ((tc ^ ((n & 1) << 2)) << 4), src);
-      }
-    }
+    for (int i = 0; i < kChunk / 2; ++i)
+      if (i * 2 + tr < it.rows) cp_async16(dst + i * 512, from + (size_t)row[i * 2] * K);
   };
 
   // ---- scales (and zero points) of a unit: 8 rows a lane, 128 / G groups each
@@ -439,12 +487,12 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
     uint8_t z[8][Z ? kG : 1];
   };
   auto load_scales = [&](const Item& it, int kb, Scales* sc) {
-    const long long first = (long long)it.e * rows_of + (DOWN ? it.tile * kRows : it.tile * 32) + (lane >> 2);
+    const long long first = (long long)it.e * rows_of + (DOWN ? it.tile * kRows : it.tile * 32) + lr8;
+    const long long o0 = first * groups_row + kb * kG;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const long long r = first + (DOWN ? i * 8 : (i & 3) * 8);
       const Weight& w = i < 4 ? w0 : w1;
-      const long long o = r * groups_row + kb * kG;
+      const long long o = o0 + (DOWN ? i * 8 : (i & 3) * 8) * groups_row;
       if constexpr (kG == 1) {
         sc->s[i][0] = __ldg(w.scales + o);
         if (Z) sc->z[i][0] = __ldg(w.zeros + o);
@@ -484,8 +532,8 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
   };
   auto l_next = [&](int stage, bool codes, bool tokens) {
     if (l_more) {
-      if (codes) load_codes(l_it, l_kb, ring + stage * Sh::kBytes);
-      if (tokens) load_tokens(l_it, l_kb, ring + stage * Sh::kBytes);
+      if (codes) load_codes(l_it, l_kb, ring + stage * kStageBytes);
+      if (tokens) load_tokens(l_it, l_kb, ring + stage * kStageBytes);
       l_kb += kItemWarps;
       l_skip();
     }
@@ -494,11 +542,11 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
   // the codes wait for nobody: down's first stages load while gate/up ends
   l_first();
 #pragma unroll 1
-  for (int s = 0; s < Sh::kStages; ++s) l_next(s, true, false);
+  for (int s = 0; s < kStages; ++s) l_next(s, true, false);
   if (DOWN) wait_for_previous_kernel();
   l_first();
 #pragma unroll 1
-  for (int s = 0; s < Sh::kStages; ++s) {
+  for (int s = 0; s < kStages; ++s) {
     l_next(s, false, true);
     cp_async_commit();
   }
@@ -507,36 +555,33 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
   for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
     Item it;
     item_of(i, &at, &it);
-    float acc[4][NT][4];
+    float acc[4][4];
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
+      for (int q = 0; q < 4; ++q) acc[m][q] = 0.f;
 
     Scales sc;
     if (it.kb0 + warp < it.kb1) load_scales(it, it.kb0 + warp, &sc);
+#pragma unroll 1
     for (int kb = it.kb0 + warp; kb < it.kb1; kb += kItemWarps) {
       Scales next;
       if (kb + kItemWarps < it.kb1) load_scales(it, kb + kItemWarps, &next);
-      cp_async_wait<Sh::kStages - 1>();
+      cp_async_wait<kStages - 1>();
       __syncwarp();
-      const uint32_t st = ring + stage * Sh::kBytes;
-      // the tokens' pairs: b[n][c] for columns 32 c + 8 t .. + 7
-      uint4 b[NT][4];
+      const uint32_t st = ring + stage * kStageBytes;
+      // the tokens' pairs of columns 32 c + 8 t .. + 7, and each group's sum
+      uint4 b[4];
+      float sx[kG][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n * 8 >= it.rows) break;
-        const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint4 v = lds128(st + kWCodes + (n * 8 + g) * 256 + (((4 * c + t) ^ ((g & 1) << 2)) << 4));
-          if (DOWN) b[n][c] = v;
-          else
-            b[n][c] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                 __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-        }
+      for (int c = 0; c < 4; ++c) {
+        const uint4 v = lds128(st + kCodeBytes + lr8 * 256 + (((4 * c + lc4) ^ ((lr8 & 1) << 2)) << 4));
+        if (DOWN) b[c] = v;
+        else
+          b[c] = make_uint4(mul2(__byte_perm(v.x, v.z, 0x5410), kScaleX), mul2(__byte_perm(v.x, v.z, 0x7632), kScaleX16),
+                            mul2(__byte_perm(v.y, v.w, 0x5410), kScaleX), mul2(__byte_perm(v.y, v.w, 0x7632), kScaleX16));
+        mma16816(sx[c * 32 / G], 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, b[c].x, b[c].y, c * 32 % G == 0);
+        mma16816(sx[c * 32 / G], 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, b[c].z, b[c].w, false);
       }
       const int lr = lane & 15, lc = lane >> 4;  // ldmatrix: rows 0-15, chunk of the pair
 #pragma unroll
@@ -547,83 +592,69 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
           ldmatrix4(st + (m * 16 + lr) * 64 + (((2 * q + lc) ^ (lr >> 1 & 3)) << 4), code[q]);
 #pragma unroll
         for (int grp = 0; grp < kG; ++grp) {
-          float part[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) part[n][q] = 0.f;
-          uint32_t base0 = 0x43084308u, base1 = 0x43084308u;  // 128 + 8
-          if (Z) {
-            base0 = 0x43004300u + sc.z[2 * m][grp] * 0x00010001u;
-            base1 = 0x43004300u + sc.z[2 * m + 1][grp] * 0x00010001u;
-          }
+          float part[4];
 #pragma unroll
           for (int c = grp * G / 32; c < (grp + 1) * G / 32; ++c) {
             const uint32_t u = code[c >> 1][(c & 1) * 2], v = code[c >> 1][(c & 1) * 2 + 1];
-            uint32_t p0[4], p1[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              p0[q] = code_pair(u, q, base0);
-              p1[q] = code_pair(v, q, base1);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (n * 8 >= it.rows) break;
-              mma16816(part[n], p0[0], p1[0], p0[1], p1[1], b[n][c].x, b[n][c].y);
-              mma16816(part[n], p0[2], p1[2], p0[3], p1[3], b[n][c].z, b[n][c].w);
-            }
+            const uint32_t u8 = u >> 8, v8 = v >> 8;
+            mma16816(part, u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, b[c].x, b[c].y,
+                     c == grp * G / 32);
+            mma16816(part, u8 & 0x000f000fu, v8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x00f000f0u, b[c].z, b[c].w,
+                     false);
           }
           const float s0 = __bfloat162float(sc.s[2 * m][grp]), s1 = __bfloat162float(sc.s[2 * m + 1][grp]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc[m][n][0] += s0 * part[n][0];
-            acc[m][n][1] += s0 * part[n][1];
-            acc[m][n][2] += s1 * part[n][2];
-            acc[m][n][3] += s1 * part[n][3];
-          }
+          const float z0 = Z ? (float)sc.z[2 * m][grp] : 8.f, z1 = Z ? (float)sc.z[2 * m + 1][grp] : 8.f;
+          acc[m][0] += s0 * (part[0] - z0 * sx[grp][0]);
+          acc[m][1] += s0 * (part[1] - z0 * sx[grp][1]);
+          acc[m][2] += s1 * (part[2] - z1 * sx[grp][2]);
+          acc[m][3] += s1 * (part[3] - z1 * sx[grp][3]);
         }
       }
       __syncwarp();
       l_next(stage, true, true);
       cp_async_commit();
-      stage = stage + 1 == Sh::kStages ? 0 : stage + 1;
+      stage ^= 1;
       sc = next;
     }
 
-    // the warps' sums: [warp][row][8 columns], 8 token rows at a time
+    // the warps' sums, half the rows at a time: [warp][32 rows][8 columns];
+    // gate/up: 16 rows of each
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      if (n * 8 >= it.rows) break;
+    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        float2* d0 = reinterpret_cast<float2*>(sums + (warp * kRows + m * 16 + (lane >> 2)) * 8 + (lane & 3) * 2);
-        d0[0] = make_float2(acc[m][n][0], acc[m][n][1]);
-        d0[8 * 8 / 2] = make_float2(acc[m][n][2], acc[m][n][3]);
+      for (int q = 0; q < 2; ++q) {
+        const int m = DOWN ? half * 2 + q : half + q * 2;
+        float2* d0 = reinterpret_cast<float2*>(sums + (warp * 32 + q * 16 + lr8) * 8 + lc4 * 2);
+        d0[0] = make_float2(acc[m][0], acc[m][1]);
+        d0[8 * 8 / 2] = make_float2(acc[m][2], acc[m][3]);
       }
       __syncthreads();
       if constexpr (!DOWN) {
-        const int r = tid >> 3, col = n * 8 + (tid & 7);
-        float g = 0.f, u = 0.f;
+        if (tid < 128) {
+          const int r = tid >> 3, col = tid & 7;
+          float g = 0.f, u = 0.f;
 #pragma unroll
-        for (int q = 0; q < kItemWarps; ++q) {
-          g += sums[(q * kRows + r) * 8 + (tid & 7)];
-          u += sums[(q * kRows + 32 + r) * 8 + (tid & 7)];
+          for (int q = 0; q < kItemWarps; ++q) {
+            g += sums[(q * 32 + r) * 8 + col];
+            u += sums[(q * 32 + 16 + r) * 8 + col];
+          }
+          g *= kUnscale;
+          u *= kUnscale;
+          const int c = it.tile * 32 + half * 16 + r;
+          if (col < it.rows)  // the one rounding between the two products
+            a.h[(size_t)rows.slot[it.first + col] * a.f + h_place(c)] =
+                __float2bfloat16(g / (1.f + expf(-g)) * u * h_scale(c));
         }
-        if (col < it.rows)  // the one rounding between the two products
-          a.h[(size_t)rows.slot[it.first + col] * a.f + h_place(it.tile * 32 + r)] = __float2bfloat16(g / (1.f + expf(-g)) * u);
       } else {
-        const int c = tid >> 5, col = n * 8 + c;
+        const int r = tid & 31, col = tid >> 5;
+        float y = 0.f;
 #pragma unroll
-        for (int o = 0; o < 2; ++o) {
-          const int r = (tid & 31) + o * 32;
-          float y = 0.f;
-#pragma unroll
-          for (int q = 0; q < kItemWarps; ++q) y += sums[(q * kRows + r) * 8 + c];
-          if (col < it.rows)
-            a.y[((size_t)it.split * (a.T * (a.k + a.S)) + rows.slot[it.first + col]) * a.d + it.tile * kRows + r] = y;
-        }
+        for (int q = 0; q < kItemWarps; ++q) y += sums[(q * 32 + r) * 8 + col];
+        if (col < it.rows)
+          a.y[((size_t)it.split * (a.T * (a.k + a.S)) + rows.slot[it.first + col]) * a.d + it.tile * kRows +
+              half * 32 + r] = y * kUnscale;
+        if (half == 1) __threadfence();
       }
-      if (DOWN) __threadfence();
       __syncthreads();
     }
 
@@ -639,12 +670,12 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
       if (last_of_tile) {
         __threadfence();
         const size_t slots = (size_t)a.T * (a.k + a.S);
-        const int col = it.tile * kRows + (tid & 31) * 2;
-        for (int t = tid >> 5; t < a.T; t += kItemWarps) {
+        const int col = it.tile * kRows + lane * 2;
+        for (int t = warp; t < a.T; t += kItemWarps) {
           float2 o = make_float2(0.f, 0.f);
           for (int j = 0; j < a.k + a.S; ++j) {
             const int p = j < a.k ? t * a.k + j : a.T * a.k + t;
-            if (j < a.k && (unsigned)__ldg(a.idx + p) >= (unsigned)a.E) continue;
+            if (j < a.k && expert_at(a, p) < 0) continue;
             float2 y = make_float2(0.f, 0.f);
             for (int q = 0; q < splits; ++q) {
               const float2 v = __ldcg(reinterpret_cast<const float2*>(a.y + ((size_t)q * slots + p) * a.d + col));
@@ -662,7 +693,8 @@ __global__ void __launch_bounds__(kItemWarps * 32, 1) w4_experts(const Experts a
     }
   }
   if (DOWN && n_items == 0) {  // no slot has an expert
-    for (long long i = (long long)blockIdx.x * blockDim.x + tid; i < (long long)a.T * a.d / 2; i += (long long)gridDim.x * blockDim.x)
+    for (long long i = (long long)blockIdx.x * blockDim.x + tid; i < (long long)a.T * a.d / 2;
+         i += (long long)gridDim.x * blockDim.x)
       reinterpret_cast<uint32_t*>(a.out)[i] = 0u;
   }
 }
@@ -713,7 +745,7 @@ int down_splits(const moe_w4* h, int T) {
   int best = 1;
   long long least = 0;
   for (int s = 1; s <= kMaxSplit && s <= blocks; ++s) {
-    const long long waves = (items * s + kSms - 1) / kSms;
+    const long long waves = (items * s + kSms * kBlocksSm - 1) / (kSms * kBlocksSm);
     const long long units = ((blocks + s - 1) / s + kItemWarps - 1) / kItemWarps;
     const long long cost = waves * (2 * units + 1);
     if (s == 1 || cost < least) least = cost, best = s;
@@ -758,23 +790,16 @@ cudaError_t launch_after(void (*kernel)(Experts), int grid, int threads, int sme
 struct Kernels {
   void (*gate_up)(Experts);
   void (*down)(Experts);
-  int smem;
 };
 
-template <int NT, int G, bool Z>
-Kernels kernels_of() {
-  return Kernels{w4_experts<NT, false, G, Z>, w4_experts<NT, true, G, Z>, Shape<NT, false, G, Z>::kSmem};
+template <int G>
+Kernels kernels_of(bool zeros) {
+  return zeros ? Kernels{w4_experts<false, G, true>, w4_experts<true, G, true>}
+               : Kernels{w4_experts<false, G, false>, w4_experts<true, G, false>};
 }
 
-Kernels kernels(int nt, int group, bool zeros) {
-  if (nt == 1) {
-    if (group == 32) return zeros ? kernels_of<1, 32, true>() : kernels_of<1, 32, false>();
-    if (group == 64) return zeros ? kernels_of<1, 64, true>() : kernels_of<1, 64, false>();
-    return zeros ? kernels_of<1, 128, true>() : kernels_of<1, 128, false>();
-  }
-  if (group == 32) return zeros ? kernels_of<2, 32, true>() : kernels_of<2, 32, false>();
-  if (group == 64) return zeros ? kernels_of<2, 64, true>() : kernels_of<2, 64, false>();
-  return zeros ? kernels_of<2, 128, true>() : kernels_of<2, 128, false>();
+Kernels kernels(int group, bool zeros) {
+  return group == 32 ? kernels_of<32>(zeros) : group == 64 ? kernels_of<64>(zeros) : kernels_of<128>(zeros);
 }
 
 }  // namespace
@@ -861,13 +886,12 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
     return moe::set_error(MOE_E_NOMEM, "workspace allocation failed");
   }
   e = cudaMemsetAsync(h->ws, 0, bytes, s);
-  for (int nt = 1; nt <= 2 && e == cudaSuccess; ++nt)
-    for (int z = 0; z < 2 && e == cudaSuccess; ++z) {
-      const Kernels kn = kernels(nt, h->group, z);
-      e = cudaFuncSetAttribute((const void*)kn.gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, kn.smem);
-      if (e == cudaSuccess)
-        e = cudaFuncSetAttribute((const void*)kn.down, cudaFuncAttributeMaxDynamicSharedMemorySize, kn.smem);
-    }
+  for (int z = 0; z < 2 && e == cudaSuccess; ++z) {
+    const Kernels kn = kernels(h->group, z);
+    e = cudaFuncSetAttribute((const void*)kn.gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute((const void*)kn.down, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_reserve");
   h->T_max = T_max;
   moe::clear_error();
@@ -927,12 +951,13 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   a.list_row = reinterpret_cast<uint16_t*>(h->ws + l.row);
   a.out = static_cast<__nv_bfloat16*>(out);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Kernels kn = kernels(T <= 8 ? 1 : 2, h->group, h->gate.zeros != nullptr);
+  const Kernels kn = kernels(h->group, h->gate.zeros != nullptr);
   const bool listed = T * h->k > kInline;
+  constexpr int grid = kSms * kBlocksSm;
   cudaError_t e = cudaSuccess;
   if (listed) e = launch_after(w4_list, 1, 1024, 0, false, s, a);
-  if (e == cudaSuccess) e = launch_after(kn.gate_up, kSms, kItemWarps * 32, kn.smem, listed, s, a);
-  if (e == cudaSuccess) e = launch_after(kn.down, kSms, kItemWarps * 32, kn.smem, true, s, a);
+  if (e == cudaSuccess) e = launch_after(kn.gate_up, grid, kItemWarps * 32, kSmem, listed, s, a);
+  if (e == cudaSuccess) e = launch_after(kn.down, grid, kItemWarps * 32, kSmem, true, s, a);
   return e == cudaSuccess ? MOE_OK : moe::set_cuda_error(e, "w4_experts");
 }
 
