@@ -439,18 +439,21 @@ typedef struct moe_w4_weight {
 
 moe_w4_t* moe_w4_create(int d, int f, int E, int k, int shared_experts, int group);
 
-/* Allocate the workspace for up to T_max (1..1024) tokens on the current
- * device.  The only allocating call; may be called again. */
+/* Allocate the workspace for up to T_max (1..1024) tokens, and room for the
+ * scales, on the current device.  The only allocating call; may be called
+ * again to grow or shrink the workspace. */
 int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream);
 
-/* Bytes that moe_w4_reserve(T_max) allocates; -1 for a NULL handle or a T_max
+/* Bytes that moe_w4_reserve(T_max) allocates in all; -1 for a NULL handle or a T_max
  * outside 0..1024. */
 long long moe_w4_workspace_bytes(const moe_w4_t* h, int T_max);
 
-/* The matrices every later forward reads (device pointers, 16-byte aligned,
- * kept by the caller). */
+/* The matrices of every later forward (device pointers, 16-byte aligned).  The
+ * codes are read where they are and stay the caller's; the scales and zero
+ * points are copied, in the order in which the kernels take them, on `stream`
+ * (call it again when they change).  After moe_w4_reserve. */
 int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weight* up,
-                       const moe_w4_weight* down);
+                       const moe_w4_weight* down, void* stream);
 
 /* One pass for T tokens, 0 <= T <= T_max (T = 0 does nothing): x and out
  * [T, d] bf16, idx [T, k] int32, w [T, k] fp32.  Asynchronous, allocates

@@ -63,7 +63,7 @@ _SIGNATURES = {
     "moe_w4_create": ([_i32] * 6, _vp),
     "moe_w4_reserve": ([_vp, _i32, _vp], _i32),
     "moe_w4_workspace_bytes": ([_vp, _i32], _i64),
-    "moe_w4_set_weights": ([_vp, _vp, _vp, _vp], _i32),
+    "moe_w4_set_weights": ([_vp] * 5, _i32),
     "moe_w4_forward": ([_vp, _i32, _vp, _vp, _vp, _vp, _vp], _i32),
     "moe_w4_destroy": ([_vp], None),
     "moe_last_error": ([], ctypes.c_char_p),
@@ -452,10 +452,11 @@ class W4Experts:
     def workspace_bytes(self, T_max: int) -> int:
         return lib.moe_w4_workspace_bytes(self.h, T_max)
 
-    def set_weights(self, gate, up, down):
-        """Each of gate, up, down: (codes, scales, zeros or None), codes uint8
+    def set_weights(self, gate, up, down, stream=None):
+        """After reserve.  Each of gate, up, down: (codes, scales, zeros or None), codes uint8
         [E + S, rows, cols / 2], scales bf16 and zeros uint8 [E + S, rows, cols /
-        group]; rows, cols are f, d for gate and up and d, f for down."""
+        group]; rows, cols are f, d for gate and up and d, f for down.
+        The codes are read where they are, the scales and zeros copied now."""
         import torch
         dev = _current_device()
         n, args = self.E + self.S, []
@@ -468,7 +469,7 @@ class W4Experts:
                 _on_device(name + " zeros", zeros, dev, torch.uint8, (n, rows, cols // self.group))
             args.append(_W4Weight(codes.data_ptr(), scales.data_ptr(),
                                   None if zeros is None else zeros.data_ptr()))
-        _err(lib.moe_w4_set_weights(self.h, *(ctypes.byref(a) for a in args)))
+        _err(lib.moe_w4_set_weights(self.h, *(ctypes.byref(a) for a in args), _stream_ptr(stream)))
         self._weights = (tuple(gate), tuple(up), tuple(down))  # alive while the library holds their pointers
 
     def forward(self, x, idx, w, out, stream=None):

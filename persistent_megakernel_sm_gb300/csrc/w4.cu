@@ -103,11 +103,12 @@ __global__ void __launch_bounds__(256)
 
 // --------------------------------------------------------------------- experts
 //
-// Two kernels, gate/up then down, of the same shape.  An item is 64 weight
-// rows of one expert (gate/up: 32 of each) times up to 8 of the expert's token
-// rows; a block of eight warps works an item off, its warps taking the
-// 128-column blocks of the product in turn, and adds the warps' sums in shared
-// memory.  Blocks stay resident, two to an SM, and take items gridDim apart.
+// Two kernels, gate/up then down, of the same shape, and a third that adds the
+// slots of a token.  An item is 64 weight rows of one expert (gate/up: 32 of
+// each) times up to 8 of the expert's token rows; a team of 1, 2, 4 or 8 warps
+// works an item off, its warps taking the 128-column blocks of the product in
+// turn, and its first warp adds the others' sums.  Blocks of eight warps stay
+// resident, two to an SM, and teams take items by turns.
 //
 // A warp's unit is 64 rows x 128 columns: 4 KB of codes, copied
 // asynchronously into the warp's own ring of two stages with the token rows'
@@ -136,14 +137,19 @@ constexpr int kItemWarps = 8;
 constexpr int kBlocksSm = 2;
 constexpr int kSms = 152;
 constexpr int kInline = 32;           // slots up to which every block lists the experts' rows itself
-constexpr int kMaxSplit = 8;          // K splits of the down product
+constexpr int kMaxSplit = 16;         // K splits of the down product
 constexpr uint32_t kScaleX = 0x5f805f80u, kScaleX16 = 0x5d805d80u;  // 2^64, 2^60 twice
 constexpr float kUnscale = 5.9029581035870565e20f;                  // 2^69
 
 struct Experts {
   int T, d, f, E, k, S;
+  int team[2];              // warps to an item, gate/up and down
   int splits;               // K splits of the down product
-  Weight gate, up, down;
+  const uint8_t *gate, *up, *down;  // codes
+  // gate/up's and down's scales and zero points as the units take them:
+  // [expert][row tile][128-column block][8 lanes][128 / G groups][8 rows]
+  const uint4* scales[2];
+  const uint2* zeros[2];
   const __nv_bfloat16* x;   // [T, d]
   const int* idx;           // [T, k]
   const float* w;           // [T, k]
@@ -151,7 +157,6 @@ struct Experts {
   // the product takes them
   __nv_bfloat16* h;
   float* y;                 // [splits, T k + T S, d]
-  int* arrived;             // [d / 64] items of a column tile done; zero between passes
   void* list;               // List and Rows of a batch of more than kInline slots
   uint16_t *list_slot, *list_row;
   __nv_bfloat16* out;       // [T, d]
@@ -160,7 +165,7 @@ struct Experts {
 // The experts that have rows, in order (up to kInline slots: of appearance).
 struct List {
   int n_active;
-  int start[kMaxE + 2];          // first of each one's entries in slot and row
+  uint16_t start[kMaxE + 2];     // first of each one's entries in slot and row
   uint16_t expert[kMaxE + 2];
 };
 
@@ -249,7 +254,7 @@ __device__ void list_few(const Experts& a, List* l, const Rows& rows) {
     if (leads) {
       const int at = __popc(leaders & ((1u << lane) - 1u));
       l->expert[at] = (uint16_t)e;
-      l->start[at] = start;
+      l->start[at] = (uint16_t)start;
     }
     if (e >= 0) {
       const int to = start + __popc(same & ((1u << lane) - 1u));
@@ -258,10 +263,10 @@ __device__ void list_few(const Experts& a, List* l, const Rows& rows) {
     }
     if (lane == 0) {
       int n = __popc(leaders);
-      l->start[n] = all;
+      l->start[n] = (uint16_t)all;
       if (a.S) {
         l->expert[n++] = (uint16_t)a.E;
-        l->start[n] = all + a.T;
+        l->start[n] = (uint16_t)(all + a.T);
       }
       l->n_active = n;
     }
@@ -305,10 +310,10 @@ __global__ void __launch_bounds__(1024) w4_list(Experts a) {
     }
     if (lane == 31) {
       int na = a0;
-      l.start[na] = s0;
+      l.start[na] = (uint16_t)s0;
       if (a.S) {
         l.expert[na++] = (uint16_t)a.E;
-        l.start[na] = s0 + a.T;
+        l.start[na] = (uint16_t)(s0 + a.T);
       }
       l.n_active = na;
     }
@@ -318,7 +323,7 @@ __global__ void __launch_bounds__(1024) w4_list(Experts a) {
       count[lane * 8 + i] = s0;  // from here on the expert's next entry
       if (c[i] > 0) {
         l.expert[a0] = (uint16_t)(lane * 8 + i);
-        l.start[a0++] = s0;
+        l.start[a0++] = (uint16_t)s0;
         s0 += c[i];
       }
     }
@@ -369,7 +374,7 @@ struct Item {
 };
 
 constexpr int kRing = kStageBytes * kStages * kItemWarps;
-constexpr int kSum = kItemWarps * kRows / 2 * kChunk * 4;  // the warps' sums of half the rows
+constexpr int kSum = (kItemWarps - 1) * kRows * kChunk * 4;  // the sums of all warps but a team's first
 constexpr int kInlineRows = 2 * kInline;                   // slots, and the shared expert's tokens
 constexpr int kSmem = kRing + kSum + (int)sizeof(List) + (kMaxE + 2) * 4 + 2 * kInlineRows * 2;
 static_assert(kSmem <= 113 * 1024, "two blocks to an SM");
@@ -382,8 +387,10 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
   List* list = reinterpret_cast<List*>(smem + kRing + kSum);
   int* item_start = reinterpret_cast<int*>(list + 1);  // [n_active + 1]
   uint16_t* few = reinterpret_cast<uint16_t*>(item_start + kMaxE + 2);
-  __shared__ int last_of_tile;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int team = a.team[DOWN], member = warp & (team - 1);
+  const int team_id = warp / team * gridDim.x + blockIdx.x;  // an SM's teams are far apart
+  const int teams = kItemWarps / team * gridDim.x;
   const int K = DOWN ? a.f : a.d;
   const int rows_of = DOWN ? a.d : a.f;                // weight rows of an expert
   const int row_tiles = DOWN ? a.d / kRows : a.f / 32;
@@ -427,8 +434,7 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
 
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
   const long long kb_row = K / 2;                       // bytes of a row of codes
-  const int groups_row = K / G;
-  const Weight w0 = DOWN ? a.down : a.gate, w1 = DOWN ? a.down : a.up;
+  const uint8_t *w0 = DOWN ? a.down : a.gate, *w1 = DOWN ? a.down : a.up;
 
   auto item_of = [&](int i, int* at, Item* it) {  // `at` only moves forward
     while (i >= item_start[*at + 1]) ++*at;
@@ -461,8 +467,8 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
     const uint32_t dst = stage + lr8 * 64 + ((lc4 ^ (lr8 >> 1 & 3)) << 4);
     const long long first = (long long)it.e * rows_of + (DOWN ? it.tile * kRows : it.tile * 32) + lr8;
     const long long o = first * kb_row + kb * 64 + lc4 * 16;
-    const uint8_t* s0 = w0.codes + o;
-    const uint8_t* s1 = DOWN ? s0 + 32 * kb_row : w1.codes + o;
+    const uint8_t* s0 = w0 + o;
+    const uint8_t* s1 = DOWN ? s0 + 32 * kb_row : w1 + o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       cp_async16(dst + i * 512, s0 + i * 8 * kb_row);
@@ -483,76 +489,73 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
   // ---- scales (and zero points) of a unit: 8 rows a lane, 128 / G groups each
   constexpr int kG = kBlockK / G;
   struct Scales {
-    __nv_bfloat16 s[8][kG];
-    uint8_t z[8][Z ? kG : 1];
+    uint4 s[kG];
+    uint2 z[Z ? kG : 1];
   };
-  auto load_scales = [&](const Item& it, int kb, Scales* sc) {
-    const long long first = (long long)it.e * rows_of + (DOWN ? it.tile * kRows : it.tile * 32) + lr8;
-    const long long o0 = first * groups_row + kb * kG;
+  auto load_scales = [&](long long unit, Scales* sc) {
+    if (unit < 0) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const Weight& w = i < 4 ? w0 : w1;
-      const long long o = o0 + (DOWN ? i * 8 : (i & 3) * 8) * groups_row;
-      if constexpr (kG == 1) {
-        sc->s[i][0] = __ldg(w.scales + o);
-        if (Z) sc->z[i][0] = __ldg(w.zeros + o);
-      } else if constexpr (kG == 2) {
-        *reinterpret_cast<uint32_t*>(sc->s[i]) = __ldg(reinterpret_cast<const uint32_t*>(w.scales + o));
-        if (Z) *reinterpret_cast<uint16_t*>(sc->z[i]) = __ldg(reinterpret_cast<const uint16_t*>(w.zeros + o));
-      } else {
-        *reinterpret_cast<uint2*>(sc->s[i]) = __ldg(reinterpret_cast<const uint2*>(w.scales + o));
-        if (Z) *reinterpret_cast<uint32_t*>(sc->z[i]) = __ldg(reinterpret_cast<const uint32_t*>(w.zeros + o));
-      }
+    for (int q = 0; q < kG; ++q) {
+      sc->s[q] = __ldg(a.scales[DOWN] + (unit * 8 + lr8) * kG + q);
+      if (Z) sc->z[q] = __ldg(a.zeros[DOWN] + (unit * 8 + lr8) * kG + q);
     }
   };
 
   // ---- the cursor of the loads, kStages units ahead of the products
   int l_item, l_at, l_kb;
+  long long in_stage[kStages];  // the unit that each stage holds, -1: none
   Item l_it{};
   bool l_more;
   auto l_skip = [&]() {  // to a unit that exists (a warp may have none in an item)
     while (l_more && l_kb >= l_it.kb1) {
-      l_item += gridDim.x;
+      l_item += teams;
       l_more = l_item < n_items;
       if (l_more) {
         item_of(l_item, &l_at, &l_it);
-        l_kb = l_it.kb0 + warp;
+        l_kb = l_it.kb0 + member;
       }
     }
   };
   auto l_first = [&]() {
-    l_item = blockIdx.x;
+    l_item = team_id;
     l_at = 0;
     l_more = l_item < n_items;
     if (l_more) {
       item_of(l_item, &l_at, &l_it);
-      l_kb = l_it.kb0 + warp;
+      l_kb = l_it.kb0 + member;
       l_skip();
     }
   };
   auto l_next = [&](int stage, bool codes, bool tokens) {
+    in_stage[stage] = -1;
     if (l_more) {
+      in_stage[stage] = ((long long)l_it.e * row_tiles + l_it.tile) * blocks_k + l_kb;
       if (codes) load_codes(l_it, l_kb, ring + stage * kStageBytes);
       if (tokens) load_tokens(l_it, l_kb, ring + stage * kStageBytes);
-      l_kb += kItemWarps;
+      l_kb += team;
       l_skip();
     }
   };
 
   // the codes wait for nobody: down's first stages load while gate/up ends
   l_first();
-#pragma unroll 1
+#pragma unroll
   for (int s = 0; s < kStages; ++s) l_next(s, true, false);
-  if (DOWN) wait_for_previous_kernel();
+  Scales sc;
+  load_scales(in_stage[0], &sc);
+  if (DOWN) {
+    let_next_kernel_start();
+    wait_for_previous_kernel();
+  }
   l_first();
-#pragma unroll 1
+#pragma unroll
   for (int s = 0; s < kStages; ++s) {
     l_next(s, false, true);
     cp_async_commit();
   }
 
   int at = 0, stage = 0;
-  for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
+  for (int i = team_id; i < n_items; i += teams) {
     Item it;
     item_of(i, &at, &it);
     float acc[4][4];
@@ -561,142 +564,183 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[m][q] = 0.f;
 
-    Scales sc;
-    if (it.kb0 + warp < it.kb1) load_scales(it, it.kb0 + warp, &sc);
 #pragma unroll 1
-    for (int kb = it.kb0 + warp; kb < it.kb1; kb += kItemWarps) {
+    for (int kb = it.kb0 + member; kb < it.kb1; kb += team) {
       Scales next;
-      if (kb + kItemWarps < it.kb1) load_scales(it, kb + kItemWarps, &next);
+      load_scales(stage ? in_stage[0] : in_stage[1], &next);
       cp_async_wait<kStages - 1>();
       __syncwarp();
       const uint32_t st = ring + stage * kStageBytes;
-      // the tokens' pairs of columns 32 c + 8 t .. + 7, and each group's sum
-      uint4 b[4];
-      float sx[kG][4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint4 v = lds128(st + kCodeBytes + lr8 * 256 + (((4 * c + lc4) ^ ((lr8 & 1) << 2)) << 4));
-        if (DOWN) b[c] = v;
-        else
-          b[c] = make_uint4(mul2(__byte_perm(v.x, v.z, 0x5410), kScaleX), mul2(__byte_perm(v.x, v.z, 0x7632), kScaleX16),
-                            mul2(__byte_perm(v.y, v.w, 0x5410), kScaleX), mul2(__byte_perm(v.y, v.w, 0x7632), kScaleX16));
-        mma16816(sx[c * 32 / G], 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, b[c].x, b[c].y, c * 32 % G == 0);
-        mma16816(sx[c * 32 / G], 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, b[c].z, b[c].w, false);
-      }
+      float part[4][4], sx[4];
       const int lr = lane & 15, lc = lane >> 4;  // ldmatrix: rows 0-15, chunk of the pair
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        uint32_t code[2][4];
+      for (int q = 0; q < 2; ++q) {  // 64 columns: two chunks of 32
+        uint32_t code[4][4];
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          ldmatrix4(st + (m * 16 + lr) * 64 + (((2 * q + lc) ^ (lr >> 1 & 3)) << 4), code[q]);
+        for (int m = 0; m < 4; ++m)
+          ldmatrix4(st + (m * 16 + lr) * 64 + (((2 * q + lc) ^ (lr >> 1 & 3)) << 4), code[m]);
 #pragma unroll
-        for (int grp = 0; grp < kG; ++grp) {
-          float part[4];
+        for (int half = 0; half < 2; ++half) {
+          const int c = 2 * q + half;
+          const bool first = c * 32 % G == 0;
+          // the tokens' pairs of columns 32 c + 8 t .. + 7
+          const uint4 v = lds128(st + kCodeBytes + lr8 * 256 + (((4 * c + lc4) ^ ((lr8 & 1) << 2)) << 4));
+          uint4 b = v;
+          if (!DOWN)
+            b = make_uint4(mul2(__byte_perm(v.x, v.z, 0x5410), kScaleX), mul2(__byte_perm(v.x, v.z, 0x7632), kScaleX16),
+                           mul2(__byte_perm(v.y, v.w, 0x5410), kScaleX), mul2(__byte_perm(v.y, v.w, 0x7632), kScaleX16));
 #pragma unroll
-          for (int c = grp * G / 32; c < (grp + 1) * G / 32; ++c) {
-            const uint32_t u = code[c >> 1][(c & 1) * 2], v = code[c >> 1][(c & 1) * 2 + 1];
-            const uint32_t u8 = u >> 8, v8 = v >> 8;
-            mma16816(part, u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u, b[c].x, b[c].y,
-                     c == grp * G / 32);
-            mma16816(part, u8 & 0x000f000fu, v8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x00f000f0u, b[c].z, b[c].w,
-                     false);
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t u = code[m][half * 2], w = code[m][half * 2 + 1];
+            mma16816(part[m], u & 0x000f000fu, w & 0x000f000fu, u & 0x00f000f0u, w & 0x00f000f0u, b.x, b.y, first);
           }
-          const float s0 = __bfloat162float(sc.s[2 * m][grp]), s1 = __bfloat162float(sc.s[2 * m + 1][grp]);
-          const float z0 = Z ? (float)sc.z[2 * m][grp] : 8.f, z1 = Z ? (float)sc.z[2 * m + 1][grp] : 8.f;
-          acc[m][0] += s0 * (part[0] - z0 * sx[grp][0]);
-          acc[m][1] += s0 * (part[1] - z0 * sx[grp][1]);
-          acc[m][2] += s1 * (part[2] - z1 * sx[grp][2]);
-          acc[m][3] += s1 * (part[3] - z1 * sx[grp][3]);
+          mma16816(sx, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, b.x, b.y, first);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t u = code[m][half * 2] >> 8, w = code[m][half * 2 + 1] >> 8;
+            mma16816(part[m], u & 0x000f000fu, w & 0x000f000fu, u & 0x00f000f0u, w & 0x00f000f0u, b.z, b.w, false);
+          }
+          mma16816(sx, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, b.z, b.w, false);
+          if ((c + 1) * 32 % G == 0) {  // the group ends
+            const int grp = c * 32 / G;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t s2 = m == 0 ? sc.s[grp].x : m == 1 ? sc.s[grp].y : m == 2 ? sc.s[grp].z : sc.s[grp].w;
+              const float s0 = __uint_as_float(s2 << 16), s1 = __uint_as_float(s2 & 0xffff0000u);
+              const uint32_t z2 = !Z ? 0u : (m < 2 ? sc.z[grp].x : sc.z[grp].y) >> (m & 1) * 16;
+              const float z0 = Z ? (float)(z2 & 15u) : 8.f, z1 = Z ? (float)(z2 >> 8 & 15u) : 8.f;
+              acc[m][0] += s0 * (part[m][0] - z0 * sx[0]);
+              acc[m][1] += s0 * (part[m][1] - z0 * sx[1]);
+              acc[m][2] += s1 * (part[m][2] - z1 * sx[2]);
+              acc[m][3] += s1 * (part[m][3] - z1 * sx[3]);
+            }
+          }
         }
       }
       __syncwarp();
-      l_next(stage, true, true);
+      if (stage) l_next(1, true, true);
+      else l_next(0, true, true);
       cp_async_commit();
       stage ^= 1;
       sc = next;
     }
 
-    // the warps' sums, half the rows at a time: [warp][32 rows][8 columns];
-    // gate/up: 16 rows of each
+    if (team > 1) {  // the first warp adds the others' sums: [member][m][lane]
+      const int bar = 1 + warp / team;
+      float4* buf = reinterpret_cast<float4*>(sums) + (warp - warp / team - 1) * 4 * 32 + lane;
+      if (member > 0) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int m = DOWN ? half * 2 + q : half + q * 2;
-        float2* d0 = reinterpret_cast<float2*>(sums + (warp * 32 + q * 16 + lr8) * 8 + lc4 * 2);
-        d0[0] = make_float2(acc[m][0], acc[m][1]);
-        d0[8 * 8 / 2] = make_float2(acc[m][2], acc[m][3]);
+        for (int m = 0; m < 4; ++m) buf[m * 32] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
       }
-      __syncthreads();
-      if constexpr (!DOWN) {
-        if (tid < 128) {
-          const int r = tid >> 3, col = tid & 7;
-          float g = 0.f, u = 0.f;
+      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(team * 32) : "memory");
+      if (member == 0) {
+        for (int q = 1; q < team; ++q) {
 #pragma unroll
-          for (int q = 0; q < kItemWarps; ++q) {
-            g += sums[(q * 32 + r) * 8 + col];
-            u += sums[(q * 32 + 16 + r) * 8 + col];
+          for (int m = 0; m < 4; ++m) {
+            const float4 v = buf[(q * 4 + m) * 32];
+            acc[m][0] += v.x;
+            acc[m][1] += v.y;
+            acc[m][2] += v.z;
+            acc[m][3] += v.w;
           }
-          g *= kUnscale;
-          u *= kUnscale;
-          const int c = it.tile * 32 + half * 16 + r;
-          if (col < it.rows)  // the one rounding between the two products
-            a.h[(size_t)rows.slot[it.first + col] * a.f + h_place(c)] =
-                __float2bfloat16(g / (1.f + expf(-g)) * u * h_scale(c));
+        }
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(team * 32) : "memory");
+      if (member > 0) continue;
+    }
+    // a lane's values: rows g and g + 8 of each 16, token rows 2 t and 2 t + 1
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int col = lc4 * 2 + j;
+      if (col >= it.rows) break;
+      const size_t slot = rows.slot[it.first + col];
+      if constexpr (!DOWN) {
+        __nv_bfloat16* h = a.h + slot * a.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int m = q >> 1, v = (q & 1) * 2 + j;
+          const int c = it.tile * 32 + m * 16 + (q & 1) * 8 + lr8;
+          const float g = acc[m][v] * kUnscale, u = acc[m + 2][v] * kUnscale;
+          h[h_place(c)] = __float2bfloat16(g / (1.f + expf(-g)) * u * h_scale(c));  // the one rounding between the products
         }
       } else {
-        const int r = tid & 31, col = tid >> 5;
-        float y = 0.f;
+        float* y = a.y + ((size_t)it.split * (a.T * (a.k + a.S)) + slot) * a.d + it.tile * kRows + lr8;
 #pragma unroll
-        for (int q = 0; q < kItemWarps; ++q) y += sums[(q * 32 + r) * 8 + col];
-        if (col < it.rows)
-          a.y[((size_t)it.split * (a.T * (a.k + a.S)) + rows.slot[it.first + col]) * a.d + it.tile * kRows +
-              half * 32 + r] = y * kUnscale;
-        if (half == 1) __threadfence();
-      }
-      __syncthreads();
-    }
-
-    if constexpr (DOWN) {
-      // the item that completes a column tile adds its slots, in slot order
-      if (tid == 0) {
-        const int expected = n_items / row_tiles;
-        const int done = atomicAdd(a.arrived + it.tile, 1) + 1;
-        if (done == expected) a.arrived[it.tile] = 0;
-        last_of_tile = done == expected;
-      }
-      __syncthreads();
-      if (last_of_tile) {
-        __threadfence();
-        const size_t slots = (size_t)a.T * (a.k + a.S);
-        const int col = it.tile * kRows + lane * 2;
-        for (int t = warp; t < a.T; t += kItemWarps) {
-          float2 o = make_float2(0.f, 0.f);
-          for (int j = 0; j < a.k + a.S; ++j) {
-            const int p = j < a.k ? t * a.k + j : a.T * a.k + t;
-            if (j < a.k && expert_at(a, p) < 0) continue;
-            float2 y = make_float2(0.f, 0.f);
-            for (int q = 0; q < splits; ++q) {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(a.y + ((size_t)q * slots + p) * a.d + col));
-              y.x += v.x;
-              y.y += v.y;
-            }
-            const float wj = j < a.k ? __ldg(a.w + p) : 1.f;
-            o.x += wj * y.x;
-            o.y += wj * y.y;
-          }
-          *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)t * a.d + col) = __floats2bfloat162_rn(o.x, o.y);
+        for (int m = 0; m < 4; ++m) {
+          y[m * 16] = acc[m][j] * kUnscale;
+          y[m * 16 + 8] = acc[m][2 + j] * kUnscale;
         }
       }
-      __syncthreads();
     }
   }
-  if (DOWN && n_items == 0) {  // no slot has an expert
-    for (long long i = (long long)blockIdx.x * blockDim.x + tid; i < (long long)a.T * a.d / 2;
-         i += (long long)gridDim.x * blockDim.x)
-      reinterpret_cast<uint32_t*>(a.out)[i] = 0u;
+}
+
+// Arrange scales and zero points once as the units take them: one thread per
+// lane and group of a unit.  first, second: the matrices of a unit's first and last 32
+// rows (gate and up; down twice, second32 = 1).
+__global__ void __launch_bounds__(256)
+    w4_arrange(Weight first, Weight second, int second32, long long units, int tile_rows, int blocks_k, int kg,
+               uint4* scales, uint2* zeros) {
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < units * 8 * kg; i += (long long)gridDim.x * 256) {
+    const int grp = (int)(i % kg), g = (int)(i / kg % 8);
+    const long long unit = i / kg / 8;
+    const int kb = (int)(unit % blocks_k);
+    const long long tile = unit / blocks_k;  // over the experts
+    union {
+      uint4 q;
+      __nv_bfloat16 b[8];
+    } s;
+    union {
+      uint2 q;
+      uint8_t b[8];
+    } z;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const Weight& m = r < 4 ? first : second;
+      const long long row = tile * tile_rows + (second32 ? r * 8 : (r & 3) * 8) + g;
+      const long long o = (row * blocks_k + kb) * kg + grp;
+      s.b[r] = m.scales[o];
+      if (zeros) z.b[r] = m.zeros[o] & 15;
+    }
+    scales[i] = s.q;
+    if (zeros) zeros[i] = z.q;
   }
+}
+
+// out[t] = the weighted sum of the token's slots, in slot order, each the sum
+// of its K splits, in order.
+__global__ void __launch_bounds__(128) w4_combine(const Experts a) {
+  const int t = blockIdx.y, col = (blockIdx.x * 128 + threadIdx.x) * 4;
+  wait_for_previous_kernel();
+  if (col >= a.d) return;
+  const size_t slots = (size_t)a.T * (a.k + a.S);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < a.k + a.S; ++j) {
+    const int p = j < a.k ? t * a.k + j : a.T * a.k + t;
+    if (j < a.k && expert_at(a, p) < 0) continue;
+    const float wj = j < a.k ? __ldg(a.w + p) : 1.f;
+    const float* from = a.y + (size_t)p * a.d + col;
+    float4 y = __ldcg(reinterpret_cast<const float4*>(from));
+#pragma unroll 4
+    for (int q = 1; q < a.splits; ++q) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(from + q * slots * a.d));
+      y.x += v.x;
+      y.y += v.y;
+      y.z += v.z;
+      y.w += v.w;
+    }
+    o.x += wj * y.x;
+    o.y += wj * y.y;
+    o.z += wj * y.z;
+    o.w += wj * y.w;
+  }
+  union {
+    __nv_bfloat162 b[2];
+    uint2 u;
+  } r;
+  r.b[0] = __floats2bfloat162_rn(o.x, o.y);
+  r.b[1] = __floats2bfloat162_rn(o.z, o.w);
+  *reinterpret_cast<uint2*>(a.out + (size_t)t * a.d + col) = r.u;
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -730,52 +774,88 @@ struct moe_w4 {
   int T_max = 0;
   Weight gate{}, up{}, down{};
   char* ws = nullptr;
+  char* arranged = nullptr;  // the scales' and zero points' copies
 };
 
 namespace {
 
-// K splits of the down product: few tokens read few experts, and d / 64 row
-// tiles of those alone would leave SMs idle.  In units of a warp's 128
-// columns, a pass takes the items of the fullest block times an item's units
-// (and about half a unit to add the warps' sums up); the split with the least.
-int down_splits(const moe_w4* h, int T) {
-  const long long experts = std::min<long long>(h->E, (long long)T * h->k) + h->S;
-  const long long items = experts * (h->d / kRows);
-  const int blocks = h->f / kBlockK;
-  int best = 1;
-  long long least = 0;
-  for (int s = 1; s <= kMaxSplit && s <= blocks; ++s) {
-    const long long waves = (items * s + kSms * kBlocksSm - 1) / (kSms * kBlocksSm);
-    const long long units = ((blocks + s - 1) / s + kItemWarps - 1) / kItemWarps;
-    const long long cost = waves * (2 * units + 1);
-    if (s == 1 || cost < least) least = cost, best = s;
-  }
+// Teams of warps and K splits.  A warp on its own is cheapest per item, but
+// few tokens read few experts, and their row tiles alone would leave warps
+// idle.  Estimated time of one product with `team` warps to an item and
+// `splits` K splits, in us: an SM streams a unit in 0.1 at best, a warp with
+// its two stages in 0.6, and each item ends with about 0.3 (0.5 where a team
+// adds up).
+float estimate(long long items, int blocks, int team, int splits) {
+  const long long per_sm = (items * splits + kSms - 1) / kSms;
+  const int units = (blocks + splits - 1) / splits;
+  const int teams = kItemWarps * kBlocksSm / team;
+  const float stream = 0.1f * per_sm * units;
+  const float chain = (float)((per_sm + teams - 1) / teams) * (0.6f * ((units + team - 1) / team) + (team > 1 ? 0.5f : 0.3f));
+  return std::max(stream, chain) + 0.02f * splits;
+}
+
+struct Split {
+  int team, splits;
+};
+
+Split best_split(long long items, int blocks, int most_splits) {
+  Split best{1, 1};
+  float least = INFINITY;
+  for (int splits = 1; splits <= most_splits && splits <= blocks; ++splits)
+    for (int team = 1; team <= kItemWarps; team *= 2) {
+      const float t = estimate(items, blocks, team, splits);
+      if (t < least * 0.999f) least = t, best = Split{team, splits};
+    }
   return best;
 }
 
+// Experts that T tokens can reach, each with its chunks of token rows if they
+// spread evenly.
+long long chunks_of(const moe_w4* h, int T) {
+  const long long experts = std::min<long long>(h->E, (long long)T * h->k);
+  const long long rows = ((long long)T * h->k + experts - 1) / experts;
+  return experts * ((rows + kChunk - 1) / kChunk) + (h->S ? (T + kChunk - 1) / kChunk : 0);
+}
+
+Split gate_up_split(const moe_w4* h, int T) { return best_split(chunks_of(h, T) * (h->f / 32), h->d / kBlockK, 1); }
+
+Split down_split(const moe_w4* h, int T) {
+  return best_split(chunks_of(h, T) * (h->d / kRows), h->f / kBlockK, kMaxSplit);
+}
+
 struct Layout {
-  size_t y, arrived, list, slot, row, bytes;
+  size_t y, list, slot, row, bytes;
 };
 
 Layout layout(const moe_w4* h, int T_max) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   const size_t slots = (size_t)T_max * (h->k + h->S);
   size_t y = 0;  // shorter batches may split more
-  for (int T = 1; T <= T_max; ++T) y = std::max(y, (size_t)T * (h->k + h->S) * h->d * 4 * down_splits(h, T));
+  for (int T = 1; T <= T_max; ++T) y = std::max(y, (size_t)T * (h->k + h->S) * h->d * 4 * down_split(h, T).splits);
   Layout l;
   l.y = up(slots * h->f * 2);
-  l.arrived = l.y + up(y);
-  l.list = l.arrived + up((size_t)h->d / kRows * 4);
+  l.list = l.y + up(y);
   l.slot = l.list + up(sizeof(List));
   l.row = l.slot + up(slots * 2);
   l.bytes = l.row + up(slots * 2);
   return l;
 }
 
-cudaError_t launch_after(void (*kernel)(Experts), int grid, int threads, int smem, bool overlap, cudaStream_t s,
+// The copies that moe_w4_set_weights makes: gate/up's scales, down's, and the
+// zero points of both.
+struct Arranged {
+  size_t down, zeros, zeros_down, bytes;
+};
+
+Arranged arranged(const moe_w4* h) {
+  const size_t n = (size_t)(h->E + h->S) * h->f * h->d / h->group;  // of one matrix
+  return Arranged{2 * n * 2, 3 * n * 2, 3 * n * 2 + 2 * n, 3 * n * 3};
+}
+
+cudaError_t launch_after(void (*kernel)(Experts), dim3 grid, int threads, int smem, bool overlap, cudaStream_t s,
                          const Experts& a) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
@@ -859,7 +939,7 @@ moe_w4_t* moe_w4_create(int d, int f, int E, int k, int shared_experts, int grou
 }
 
 long long moe_w4_workspace_bytes(const moe_w4_t* h, int T_max) {
-  return !h || T_max < 0 || T_max > kMaxT ? -1 : (long long)layout(h, T_max).bytes;
+  return !h || T_max < 0 || T_max > kMaxT ? -1 : (long long)(layout(h, T_max).bytes + arranged(h).bytes);
 }
 
 int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
@@ -880,7 +960,8 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_reserve");
   const size_t bytes = layout(h, T_max).bytes;
-  if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
+  if (!h->arranged && cudaMalloc(&h->arranged, arranged(h).bytes) != cudaSuccess) h->arranged = nullptr;
+  if (!h->arranged || cudaMalloc(&h->ws, bytes) != cudaSuccess) {
     h->ws = nullptr;
     cudaGetLastError();
     return moe::set_error(MOE_E_NOMEM, "workspace allocation failed");
@@ -899,7 +980,7 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
 }
 
 int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weight* up,
-                       const moe_w4_weight* down) {
+                       const moe_w4_weight* down, void* stream) {
   if (!h) return moe::set_error(MOE_E_INVAL, "null handle");
   const moe_w4_weight* m[3] = {gate, up, down};
   for (auto* p : m) {
@@ -912,6 +993,20 @@ int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weig
     return Weight{static_cast<const uint8_t*>(p->codes), static_cast<const __nv_bfloat16*>(p->scales),
                   static_cast<const uint8_t*>(p->zeros)};
   };
+  if (!h->arranged) return moe::set_error(MOE_E_STATE, "moe_w4_reserve was not called");
+  const Arranged at = arranged(h);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int kg = kBlockK / h->group;
+  const bool z = gate->zeros != nullptr;
+  cudaError_t e = cudaSuccess;
+  for (int d = 0; d < 2 && e == cudaSuccess; ++d) {
+    const int tile_rows = d ? kRows : 32, blocks_k = (d ? h->f : h->d) / kBlockK;
+    const long long units = (long long)(h->E + h->S) * ((d ? h->d : h->f) / tile_rows) * blocks_k;
+    e = launch(w4_arrange, convert_grid(units * 8 * kg), 256, s, take(d ? down : gate), take(d ? down : up), d, units,
+               tile_rows, blocks_k, kg, reinterpret_cast<uint4*>(h->arranged + (d ? at.down : 0)),
+               z ? reinterpret_cast<uint2*>(h->arranged + (d ? at.zeros_down : at.zeros)) : nullptr);
+  }
+  if (e != cudaSuccess) return moe::set_cuda_error(e, "w4_arrange");
   h->gate = take(gate);
   h->up = take(up);
   h->down = take(down);
@@ -936,16 +1031,23 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   a.E = h->E;
   a.k = h->k;
   a.S = h->S;
-  a.splits = down_splits(h, T);
-  a.gate = h->gate;
-  a.up = h->up;
-  a.down = h->down;
+  const Split down = down_split(h, T);
+  a.team[0] = gate_up_split(h, T).team;
+  a.team[1] = down.team;
+  a.splits = down.splits;
+  a.gate = h->gate.codes;
+  a.up = h->up.codes;
+  a.down = h->down.codes;
+  const Arranged at = arranged(h);
+  a.scales[0] = reinterpret_cast<const uint4*>(h->arranged);
+  a.scales[1] = reinterpret_cast<const uint4*>(h->arranged + at.down);
+  a.zeros[0] = reinterpret_cast<const uint2*>(h->arranged + at.zeros);
+  a.zeros[1] = reinterpret_cast<const uint2*>(h->arranged + at.zeros_down);
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.idx = idx;
   a.w = w;
   a.h = reinterpret_cast<__nv_bfloat16*>(h->ws);
   a.y = reinterpret_cast<float*>(h->ws + l.y);
-  a.arrived = reinterpret_cast<int*>(h->ws + l.arrived);
   a.list = h->ws + l.list;
   a.list_slot = reinterpret_cast<uint16_t*>(h->ws + l.slot);
   a.list_row = reinterpret_cast<uint16_t*>(h->ws + l.row);
@@ -953,17 +1055,19 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Kernels kn = kernels(h->group, h->gate.zeros != nullptr);
   const bool listed = T * h->k > kInline;
-  constexpr int grid = kSms * kBlocksSm;
+  const dim3 grid(kSms * kBlocksSm);
   cudaError_t e = cudaSuccess;
-  if (listed) e = launch_after(w4_list, 1, 1024, 0, false, s, a);
+  if (listed) e = launch_after(w4_list, dim3(1), 1024, 0, false, s, a);
   if (e == cudaSuccess) e = launch_after(kn.gate_up, grid, kItemWarps * 32, kSmem, listed, s, a);
   if (e == cudaSuccess) e = launch_after(kn.down, grid, kItemWarps * 32, kSmem, true, s, a);
+  if (e == cudaSuccess) e = launch_after(w4_combine, dim3((h->d / 4 + 127) / 128, T), 128, 0, true, s, a);
   return e == cudaSuccess ? MOE_OK : moe::set_cuda_error(e, "w4_experts");
 }
 
 void moe_w4_destroy(moe_w4_t* h) {
   if (!h) return;
   if (h->ws) cudaFree(h->ws);
+  if (h->arranged) cudaFree(h->arranged);
   delete h;
 }
 

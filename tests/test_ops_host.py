@@ -119,11 +119,11 @@ def test_w4_calls_validate(lib):
         assert lib.moe_w4_forward(h, 1, 16, 16, 16, 16, None) == pkg.MOE_E_STATE  # before reserve
         m = lambda *p: binding.ctypes.byref(binding._W4Weight(*p))  # noqa: E731
         good, zero = m(16, 16, None), m(16, 16, 16)
-        assert lib.moe_w4_set_weights(h, good, good, good) == pkg.MOE_OK
-        assert lib.moe_w4_set_weights(h, good, good, zero) == pkg.MOE_E_INVAL  # some with zero points
-        assert lib.moe_w4_set_weights(h, good, good, None) == pkg.MOE_E_INVAL
-        assert lib.moe_w4_set_weights(h, m(None, 16, None), good, good) == pkg.MOE_E_INVAL
-        assert lib.moe_w4_set_weights(h, m(16, 8, None), good, good) == pkg.MOE_E_INVAL
+        assert lib.moe_w4_set_weights(h, good, good, good, None) == pkg.MOE_E_STATE  # before reserve
+        assert lib.moe_w4_set_weights(h, good, good, zero, None) == pkg.MOE_E_INVAL  # some with zero points
+        assert lib.moe_w4_set_weights(h, good, good, None, None) == pkg.MOE_E_INVAL
+        assert lib.moe_w4_set_weights(h, m(None, 16, None), good, good, None) == pkg.MOE_E_INVAL
+        assert lib.moe_w4_set_weights(h, m(16, 8, None), good, good, None) == pkg.MOE_E_INVAL
         assert lib.moe_w4_forward(None, 1, 16, 16, 16, 16, None) == pkg.MOE_E_INVAL
     finally:
         lib.moe_w4_destroy(h)
@@ -212,7 +212,7 @@ def test_w4_binding_passes_and_refuses(rec):
     binding.w4_dequantize(c, s, None, w, stream=0)
     e = binding.W4Experts(256, 384, 3, 2, shared_experts=1, group=32)
     gate, down = mat(4, 384, 256), mat(4, 256, 384)
-    e.set_weights(gate, gate, down)
+    e.set_weights(gate, gate, down, stream=0)
     x, idx, wt = _dev(7, 256, dtype=bf), _dev(7, 2, dtype=torch.int32), _dev(7, 2)
     e.forward(x, idx, wt, _dev(7, 256, dtype=bf), stream=0)
     assert "moe_w4_forward" in rec.calls and rec.calls.count("moe_w4_quantize") == 2
@@ -225,9 +225,9 @@ def test_w4_binding_passes_and_refuses(rec):
         lambda: binding.w4_quantize(w, c, s.float(), stream=0),
         lambda: binding.w4_quantize(w.transpose(1, 2), c, s, stream=0),
         lambda: binding.w4_dequantize(c, s, z.int(), w, stream=0),
-        lambda: e.set_weights(down, gate, down),
-        lambda: e.set_weights(gate, gate, mat(3, 256, 384)),
-        lambda: e.set_weights(mat(4, 384, 256, 64), gate, down),
+        lambda: e.set_weights(down, gate, down, stream=0),
+        lambda: e.set_weights(gate, gate, mat(3, 256, 384), stream=0),
+        lambda: e.set_weights(mat(4, 384, 256, 64), gate, down, stream=0),
         lambda: e.forward(x.float(), idx, wt, x, stream=0),
         lambda: e.forward(x, idx.long(), wt, x, stream=0),
         lambda: e.forward(x, idx, wt[:6], x, stream=0),
