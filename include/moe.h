@@ -461,6 +461,11 @@ int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weig
 int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const float* w, void* out,
                    void* stream);
 
+/* Synchronise `stream`, then return and clear the device status of the passes
+ * since the last call: MOE_OK, MOE_E_TIMEOUT (a wait inside a kernel ran out,
+ * the pass's output is undefined), or MOE_E_CUDA when a CUDA error is pending. */
+int moe_w4_status(moe_w4_t* h, void* stream);
+
 void moe_w4_destroy(moe_w4_t* h);
 
 /* Message of the last failed call on this thread ("" if none). */

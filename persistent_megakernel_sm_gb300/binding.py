@@ -65,6 +65,7 @@ _SIGNATURES = {
     "moe_w4_workspace_bytes": ([_vp, _i32], _i64),
     "moe_w4_set_weights": ([_vp] * 5, _i32),
     "moe_w4_forward": ([_vp, _i32, _vp, _vp, _vp, _vp, _vp], _i32),
+    "moe_w4_status": ([_vp, _vp], _i32),
     "moe_w4_destroy": ([_vp], None),
     "moe_last_error": ([], ctypes.c_char_p),
 }
@@ -487,6 +488,13 @@ class W4Experts:
         _err(lib.moe_w4_forward(self.h, T, x.data_ptr(), idx.data_ptr(), w.data_ptr(),
                                 out.data_ptr(), _stream_ptr(stream)))
         return out
+
+    def status(self, stream=None) -> int:
+        return lib.moe_w4_status(self.h, _stream_ptr(stream))
+
+    def check(self, stream=None):
+        """Synchronise and raise if a wait inside the kernels ran out."""
+        _err(self.status(stream))
 
     def close(self):
         if self.h:

@@ -10,7 +10,7 @@ REPO = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "_build", "libmoe.so")
 SOURCES = ["moe.cu", "router.cu", "w4.cu"]
-DEPS = SOURCES + ["tasks.cuh", "layer.cuh", "ptx.cuh", "error.h"]
+DEPS = SOURCES + ["tasks.cuh", "layer.cuh", "ptx.cuh", "error.h", "tmap.h", "w4_tiles.cuh"]
 HEADER = os.path.join(REPO, "include", "moe.h")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",

@@ -6,6 +6,7 @@
 // or 128 consecutive columns of a row and, optionally, one zero point (0..15,
 // a byte) for each group: value = (code - zero) * scale, zero 8 where there
 // are no zero points.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -16,6 +17,8 @@
 
 #include "error.h"
 #include "moe.h"
+#include "ptx.cuh"
+#include "tmap.h"
 
 namespace {
 
@@ -110,10 +113,10 @@ __global__ void __launch_bounds__(256)
 // turn, and its first warp adds the others' sums.  Blocks of eight warps stay
 // resident, two to an SM, and teams take items by turns.
 //
-// A warp's unit is 64 rows x 128 columns: 4 KB of codes, copied
-// asynchronously into the warp's own ring of two stages with the token rows'
-// 128 columns beside them, across items.  ldmatrix hands each lane the word of
-// 8 codes (one row, 8 columns) that it needs of a 32-column chunk.
+// A warp's unit is 64 rows x 128 columns: 4 KB of codes, loaded by TMA into the
+// warp's own ring of two stages with the token rows' 128 columns and the scales
+// beside them, across items; one barrier a stage.  ldmatrix hands each lane the
+// word of 8 codes (one row, 8 columns) that it needs of a 32-column chunk.
 //
 // Codes to numbers: a bf16 whose bits are the integer n < 256 is n 2^-133
 // (below 128 a subnormal, from there on the first binade, with the same
@@ -131,12 +134,13 @@ constexpr int kRows = 64;             // weight rows of an item
 constexpr int kChunk = 8;             // token rows of an item
 constexpr int kBlockK = 128;          // columns of a unit
 constexpr int kCodeBytes = kRows * kBlockK / 2;
-constexpr int kStageBytes = kCodeBytes + kChunk * kBlockK * 2;
+constexpr int kTokenBytes = kBlockK * 2;  // of one token row of a unit
 constexpr int kStages = 2;
 constexpr int kItemWarps = 8;
 constexpr int kBlocksSm = 2;
 constexpr int kSms = 152;
 constexpr int kInline = 32;           // slots up to which every block lists the experts' rows itself
+constexpr int kTileMinRows = 12;      // mean token rows of an expert from which the tile kernels run
 constexpr int kMaxSplit = 16;         // K splits of the down product
 constexpr uint32_t kScaleX = 0x5f805f80u, kScaleX16 = 0x5d805d80u;  // 2^64, 2^60 twice
 constexpr float kUnscale = 5.9029581035870565e20f;                  // 2^69
@@ -145,7 +149,6 @@ struct Experts {
   int T, d, f, E, k, S;
   int team[2];              // warps to an item, gate/up and down
   int splits;               // K splits of the down product
-  const uint8_t *gate, *up, *down;  // codes
   // gate/up's and down's scales and zero points as the units take them:
   // [expert][row tile][128-column block][8 lanes][128 / G groups][8 rows]
   const uint4* scales[2];
@@ -157,8 +160,10 @@ struct Experts {
   // the product takes them
   __nv_bfloat16* h;
   float* y;                 // [splits, T k + T S, d]
+  int* status;              // MOE_E_TIMEOUT if a wait ran out
   void* list;               // List and Rows of a batch of more than kInline slots
   uint16_t *list_slot, *list_row;
+  __nv_bfloat16* xg;        // [T k + T S, d] x in the order of the list (large batches)
   __nv_bfloat16* out;       // [T, d]
 };
 
@@ -176,20 +181,17 @@ struct Rows {
   uint16_t* row;
 };
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
+using moe::bulk_load;
+using moe::fence_proxy_async_shared;
+using moe::mbar_init;
+using moe::smem_u32;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+// The codes of both products: [rows of all experts, bytes of a row], boxes of
+// 64 bytes x 32 rows (gate, up) or 64 (down), 64-byte swizzle: a row's 16-byte
+// chunk c lies at chunk c ^ (row / 2 % 4), so that ldmatrix meets no conflicts.
+struct Maps {
+  CUtensorMap gate, up, down;
+};
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -220,6 +222,17 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
 }
 
 // Where column c of a row of h is stored, and 2^64 or 2^60.
@@ -368,25 +381,62 @@ __global__ void __launch_bounds__(1024) w4_list(Experts a) {
     static_cast<int*>(a.list)[i] = reinterpret_cast<const int*>(&l)[i];
 }
 
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+// Wait for a stage's loads, two seconds at most: then the error is noted, no
+// later wait lasts, and the pass goes on, its output undefined.
+__device__ __forceinline__ void wait_stage(uint64_t* bar, uint32_t parity, int* status) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (moe::mbar_try_wait(bar, parity)) return;
+  if (moe::ld_relaxed(status) != 0) return;
+  if (!moe::mbar_wait(bar, parity, moe::globaltimer() + 2000000000ull)) *status = MOE_E_TIMEOUT;
+}
+
 // One item: an expert, 64 of its rows, a K range and a chunk of token rows.
 struct Item {
   int e, tile, split, rows, first, kb0, kb1;
 };
 
-constexpr int kRing = kStageBytes * kStages * kItemWarps;
-constexpr int kSum = (kItemWarps - 1) * kRows * kChunk * 4;  // the sums of all warps but a team's first
 constexpr int kInlineRows = 2 * kInline;                   // slots, and the shared expert's tokens
-constexpr int kSmem = kRing + kSum + (int)sizeof(List) + (kMaxE + 2) * 4 + 2 * kInlineRows * 2;
-static_assert(kSmem <= 113 * 1024, "two blocks to an SM");
+
+// Shared memory of a block, every region [warp][stage].
+template <int G, bool Z>
+struct Smem {
+  static constexpr int kG = kBlockK / G;  // groups of a unit's row
+  static constexpr int kScaleBytes = kRows * kG * 2;
+  static constexpr int kZeroBytes = Z ? kRows * kG : 0;
+  static constexpr int kSlots = kItemWarps * kStages;
+  static constexpr int kCodes = 0;
+  static constexpr int kTokens = kCodes + kSlots * kCodeBytes;
+  static constexpr int kScales = kTokens + kSlots * kChunk * kTokenBytes;
+  static constexpr int kZeros = kScales + kSlots * kScaleBytes;
+  static constexpr int kBars = kZeros + kSlots * kZeroBytes;
+  static constexpr int kLast = kBars + kSlots * 8;             // the stage of each warp's sums
+  static constexpr int kItemStart = kLast + kItemWarps * 4;
+  static constexpr int kList = kItemStart + (kMaxE + 2) * 4;
+  static constexpr int kFew = kList + (int)sizeof(List);
+  static constexpr int kBytes = kFew + 2 * kInlineRows * 2 + 512;  // and the alignment of the codes
+  static_assert(kBytes <= 113 * 1024 - 128, "two blocks to an SM");
+};
 
 // One pass over the items for one of the two products.
 template <bool DOWN, int G, bool Z>
-__global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const Experts a) {
-  extern __shared__ __align__(128) char smem[];
-  float* sums = reinterpret_cast<float*>(smem + kRing);
-  List* list = reinterpret_cast<List*>(smem + kRing + kSum);
-  int* item_start = reinterpret_cast<int*>(list + 1);  // [n_active + 1]
-  uint16_t* few = reinterpret_cast<uint16_t*>(item_start + kMaxE + 2);
+__global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
+    w4_experts(const Experts a, const __grid_constant__ Maps maps) {
+  using Sm = Smem<G, Z>;
+  constexpr int kG = Sm::kG;
+  extern __shared__ char smem_raw[];
+  const int lr8 = threadIdx.x >> 2 & 7, lc4 = threadIdx.x & 3;  // an mma fragment's row and column pair
+  char* smem = smem_raw + (-smem_u32(smem_raw) & 511u);
+  int* sums_stage = reinterpret_cast<int*>(smem + Sm::kLast);
+  int* item_start = reinterpret_cast<int*>(smem + Sm::kItemStart);  // [n_active + 1]
+  List* list = reinterpret_cast<List*>(smem + Sm::kList);
+  uint16_t* few = reinterpret_cast<uint16_t*>(smem + Sm::kFew);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int team = a.team[DOWN], member = warp & (team - 1);
   const int team_id = warp / team * gridDim.x + blockIdx.x;  // an SM's teams are far apart
@@ -397,6 +447,10 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
   const int splits = DOWN ? a.splits : 1;
   const int blocks_k = K / kBlockK;
   Rows rows{few, few + kInlineRows};
+  if (tid < Sm::kSlots) {
+    mbar_init(reinterpret_cast<uint64_t*>(smem + Sm::kBars) + tid, 1);
+    moe::fence_mbar_init();
+  }
   if (a.T * a.k <= kInline) {
     if (!DOWN) let_next_kernel_start();
     list_few(a, list, rows);
@@ -432,10 +486,6 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
   __syncthreads();
   const int n_items = item_start[n_active];
 
-  const uint32_t ring = smem_u32(smem) + warp * kStages * kStageBytes;
-  const long long kb_row = K / 2;                       // bytes of a row of codes
-  const uint8_t *w0 = DOWN ? a.down : a.gate, *w1 = DOWN ? a.down : a.up;
-
   auto item_of = [&](int i, int* at, Item* it) {  // `at` only moves forward
     while (i >= item_start[*at + 1]) ++*at;
     const int n = list->start[*at + 1] - list->start[*at];
@@ -461,100 +511,82 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
     it->first = list->start[*at] + c * kChunk;
   };
 
-  // ---- loads of one unit into a stage: the codes, the token rows
-  const int lr8 = lane >> 2, lc4 = lane & 3;
-  auto load_codes = [&](const Item& it, int kb, uint32_t stage) {
-    const uint32_t dst = stage + lr8 * 64 + ((lc4 ^ (lr8 >> 1 & 3)) << 4);
-    const long long first = (long long)it.e * rows_of + (DOWN ? it.tile * kRows : it.tile * 32) + lr8;
-    const long long o = first * kb_row + kb * 64 + lc4 * 16;
-    const uint8_t* s0 = w0 + o;
-    const uint8_t* s1 = DOWN ? s0 + 32 * kb_row : w1 + o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      cp_async16(dst + i * 512, s0 + i * 8 * kb_row);
-      cp_async16(dst + (i + 4) * 512, s1 + i * 8 * kb_row);
-    }
-  };
-  auto load_tokens = [&](const Item& it, int kb, uint32_t stage) {
-    // 16 lanes a row, 16 bytes each; odd rows' halves are swapped
-    const int tr = lane >> 4, tc = lane & 15;
-    const uint16_t* row = (DOWN ? rows.slot : rows.row) + it.first + tr;
-    const __nv_bfloat16* from = (DOWN ? a.h : a.x) + kb * kBlockK + tc * 8;
-    const uint32_t dst = stage + kCodeBytes + tr * 256 + ((tc ^ (tr << 2)) << 4);
-#pragma unroll
-    for (int i = 0; i < kChunk / 2; ++i)
-      if (i * 2 + tr < it.rows) cp_async16(dst + i * 512, from + (size_t)row[i * 2] * K);
-  };
-
-  // ---- scales (and zero points) of a unit: 8 rows a lane, 128 / G groups each
-  constexpr int kG = kBlockK / G;
-  struct Scales {
-    uint4 s[kG];
-    uint2 z[Z ? kG : 1];
-  };
-  auto load_scales = [&](long long unit, Scales* sc) {
-    if (unit < 0) return;
-#pragma unroll
-    for (int q = 0; q < kG; ++q) {
-      sc->s[q] = __ldg(a.scales[DOWN] + (unit * 8 + lr8) * kG + q);
-      if (Z) sc->z[q] = __ldg(a.zeros[DOWN] + (unit * 8 + lr8) * kG + q);
-    }
-  };
+  const uint32_t codes = smem_u32(smem + Sm::kCodes) + warp * kStages * kCodeBytes;
+  char* tokens = smem + Sm::kTokens + warp * kStages * kChunk * kTokenBytes;
+  char* scales = smem + Sm::kScales + warp * kStages * Sm::kScaleBytes;
+  char* zeros = smem + Sm::kZeros + warp * kStages * Sm::kZeroBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBars) + warp * kStages;
 
   // ---- the cursor of the loads, kStages units ahead of the products
-  int l_item, l_at, l_kb;
-  long long in_stage[kStages];  // the unit that each stage holds, -1: none
+  int l_item, l_at = 0, l_kb = 0, l_row = 0;
   Item l_it{};
+  long long l_unit = 0;          // of the item's first column block
+  const char* l_token = nullptr;  // lane n: token row n
   bool l_more;
-  auto l_skip = [&]() {  // to a unit that exists (a warp may have none in an item)
-    while (l_more && l_kb >= l_it.kb1) {
-      l_item += teams;
+  auto l_seek = [&]() {  // the next item from l_item on of which this warp has a unit
+    while (true) {
       l_more = l_item < n_items;
-      if (l_more) {
-        item_of(l_item, &l_at, &l_it);
-        l_kb = l_it.kb0 + member;
-      }
-    }
-  };
-  auto l_first = [&]() {
-    l_item = team_id;
-    l_at = 0;
-    l_more = l_item < n_items;
-    if (l_more) {
+      if (!l_more) return;
       item_of(l_item, &l_at, &l_it);
       l_kb = l_it.kb0 + member;
-      l_skip();
+      if (l_kb < l_it.kb1) break;
+      l_item += teams;
     }
+    l_row = l_it.e * rows_of + l_it.tile * (DOWN ? kRows : 32);
+    l_unit = ((long long)l_it.e * row_tiles + l_it.tile) * blocks_k;
+    if (lane < l_it.rows)
+      l_token = reinterpret_cast<const char*>((DOWN ? a.h : a.x) + (size_t)(DOWN ? rows.slot : rows.row)[l_it.first + lane] * K);
   };
-  auto l_next = [&](int stage, bool codes, bool tokens) {
-    in_stage[stage] = -1;
-    if (l_more) {
-      in_stage[stage] = ((long long)l_it.e * row_tiles + l_it.tile) * blocks_k + l_kb;
-      if (codes) load_codes(l_it, l_kb, ring + stage * kStageBytes);
-      if (tokens) load_tokens(l_it, l_kb, ring + stage * kStageBytes);
-      l_kb += team;
-      l_skip();
+  auto l_next = [&](int stage, bool weights, bool rest) {
+    if (!l_more) return;
+    uint64_t* bar = bars + stage;
+    if (lane == 0) {
+      uint32_t bytes = rest ? l_it.rows * kTokenBytes : 0;
+      if (weights) bytes += kCodeBytes + Sm::kScaleBytes + Sm::kZeroBytes;
+      if (rest) moe::mbar_arrive_expect_tx(bar, bytes);
+      else mbar_expect(bar, bytes);
+      if (weights) {
+        const uint32_t dst = codes + stage * kCodeBytes;
+        if (DOWN) {
+          tma_load(dst, &maps.down, bar, l_kb * 64, l_row);
+        } else {
+          tma_load(dst, &maps.gate, bar, l_kb * 64, l_row);
+          tma_load(dst + kCodeBytes / 2, &maps.up, bar, l_kb * 64, l_row);
+        }
+        bulk_load(scales + stage * Sm::kScaleBytes, a.scales[DOWN] + (l_unit + l_kb) * (Sm::kScaleBytes / 16),
+                  Sm::kScaleBytes, bar);
+        if (Z)
+          bulk_load(zeros + stage * Sm::kZeroBytes, a.zeros[DOWN] + (l_unit + l_kb) * (Sm::kZeroBytes / 8),
+                    Sm::kZeroBytes, bar);
+      }
+    }
+    if (rest && lane < l_it.rows)
+      bulk_load(tokens + (stage * kChunk + lane) * kTokenBytes, l_token + l_kb * kTokenBytes, kTokenBytes, bar);
+    l_kb += team;
+    if (l_kb >= l_it.kb1) {
+      l_item += teams;
+      l_seek();
     }
   };
 
-  // the codes wait for nobody: down's first stages load while gate/up ends
-  l_first();
-#pragma unroll
+  // the weights wait for nobody: down's first stages load while gate/up ends
+  l_item = team_id;
+  l_seek();
+#pragma unroll 1
   for (int s = 0; s < kStages; ++s) l_next(s, true, false);
-  Scales sc;
-  load_scales(in_stage[0], &sc);
   if (DOWN) {
     let_next_kernel_start();
     wait_for_previous_kernel();
+    moe::fence_proxy_async_global();
   }
-  l_first();
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    l_next(s, false, true);
-    cp_async_commit();
-  }
+  l_item = team_id;
+  l_at = 0;
+  l_seek();
+#pragma unroll 1
+  for (int s = 0; s < kStages; ++s) l_next(s, false, true);
 
   int at = 0, stage = 0;
+  uint32_t phase = 0;  // bit s: the parity that stage s waits for
   for (int i = team_id; i < n_items; i += teams) {
     Item it;
     item_of(i, &at, &it);
@@ -566,11 +598,12 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
 
 #pragma unroll 1
     for (int kb = it.kb0 + member; kb < it.kb1; kb += team) {
-      Scales next;
-      load_scales(stage ? in_stage[0] : in_stage[1], &next);
-      cp_async_wait<kStages - 1>();
-      __syncwarp();
-      const uint32_t st = ring + stage * kStageBytes;
+      wait_stage(bars + stage, phase >> stage & 1u, a.status);
+      phase ^= 1u << stage;
+      const uint32_t st = codes + stage * kCodeBytes;
+      const uint32_t tk = smem_u32(tokens) + (stage * kChunk + lr8) * kTokenBytes + lc4 * 16;
+      const uint32_t sc = smem_u32(scales) + stage * Sm::kScaleBytes + lr8 * kG * 16;
+      const uint32_t zr = smem_u32(zeros) + stage * Sm::kZeroBytes + lr8 * kG * 8;
       float part[4][4], sx[4];
       const int lr = lane & 15, lc = lane >> 4;  // ldmatrix: rows 0-15, chunk of the pair
 #pragma unroll
@@ -584,7 +617,7 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
           const int c = 2 * q + half;
           const bool first = c * 32 % G == 0;
           // the tokens' pairs of columns 32 c + 8 t .. + 7
-          const uint4 v = lds128(st + kCodeBytes + lr8 * 256 + (((4 * c + lc4) ^ ((lr8 & 1) << 2)) << 4));
+          const uint4 v = lds128(tk + c * 64);
           uint4 b = v;
           if (!DOWN)
             b = make_uint4(mul2(__byte_perm(v.x, v.z, 0x5410), kScaleX), mul2(__byte_perm(v.x, v.z, 0x7632), kScaleX16),
@@ -603,11 +636,13 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
           mma16816(sx, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, b.z, b.w, false);
           if ((c + 1) * 32 % G == 0) {  // the group ends
             const int grp = c * 32 / G;
+            const uint4 s4 = lds128(sc + grp * 16);
+            const uint2 z4 = Z ? lds64(zr + grp * 8) : make_uint2(0u, 0u);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-              const uint32_t s2 = m == 0 ? sc.s[grp].x : m == 1 ? sc.s[grp].y : m == 2 ? sc.s[grp].z : sc.s[grp].w;
+              const uint32_t s2 = m == 0 ? s4.x : m == 1 ? s4.y : m == 2 ? s4.z : s4.w;
               const float s0 = __uint_as_float(s2 << 16), s1 = __uint_as_float(s2 & 0xffff0000u);
-              const uint32_t z2 = !Z ? 0u : (m < 2 ? sc.z[grp].x : sc.z[grp].y) >> (m & 1) * 16;
+              const uint32_t z2 = (m < 2 ? z4.x : z4.y) >> (m & 1) * 16;
               const float z0 = Z ? (float)(z2 & 15u) : 8.f, z1 = Z ? (float)(z2 >> 8 & 15u) : 8.f;
               acc[m][0] += s0 * (part[m][0] - z0 * sx[0]);
               acc[m][1] += s0 * (part[m][1] - z0 * sx[1]);
@@ -618,26 +653,30 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
         }
       }
       __syncwarp();
-      if (stage) l_next(1, true, true);
-      else l_next(0, true, true);
-      cp_async_commit();
+      // a member's last stage of an item holds its sums until they are added
+      if (team == 1 || kb + team < it.kb1) l_next(stage, true, true);
       stage ^= 1;
-      sc = next;
     }
 
-    if (team > 1) {  // the first warp adds the others' sums: [member][m][lane]
+    if (team > 1) {  // the first warp adds the others' sums
       const int bar = 1 + warp / team;
-      float4* buf = reinterpret_cast<float4*>(sums) + (warp - warp / team - 1) * 4 * 32 + lane;
-      if (member > 0) {
+      const bool had = it.kb0 + member < it.kb1;  // this warp had a unit, whose stage is free
+      const int free_stage = stage ^ 1;
+      if (member > 0 && had) {
+        float4* buf = reinterpret_cast<float4*>(smem + Sm::kCodes + (warp * kStages + free_stage) * kCodeBytes) + lane;
 #pragma unroll
         for (int m = 0; m < 4; ++m) buf[m * 32] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
       }
+      if (lane == 0) sums_stage[warp] = had ? free_stage : -1;
       asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(team * 32) : "memory");
       if (member == 0) {
         for (int q = 1; q < team; ++q) {
+          if (sums_stage[warp + q] < 0) continue;
+          const float4* buf =
+              reinterpret_cast<const float4*>(smem + Sm::kCodes + ((warp + q) * kStages + sums_stage[warp + q]) * kCodeBytes) + lane;
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const float4 v = buf[(q * 4 + m) * 32];
+            const float4 v = buf[m * 32];
             acc[m][0] += v.x;
             acc[m][1] += v.y;
             acc[m][2] += v.z;
@@ -646,6 +685,11 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm) w4_experts(const E
         }
       }
       asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(team * 32) : "memory");
+      if (had) {
+        fence_proxy_async_shared();  // the sums were written by the threads, TMA writes next
+        __syncwarp();
+        l_next(free_stage, true, true);
+      }
       if (member > 0) continue;
     }
     // a lane's values: rows g and g + 8 of each 16, token rows 2 t and 2 t + 1
@@ -743,6 +787,8 @@ __global__ void __launch_bounds__(128) w4_combine(const Experts a) {
   *reinterpret_cast<uint2*>(a.out + (size_t)t * a.d + col) = r.u;
 }
 
+#include "w4_tiles.cuh"
+
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 int check_matrix(long long rows, int cols, int group, const void* codes, const void* scales, const void* w) {
@@ -772,26 +818,34 @@ dim3 convert_grid(long long n8) { return dim3((unsigned)std::min<long long>((n8 
 struct moe_w4 {
   int d, f, E, k, S, group;
   int T_max = 0;
-  Weight gate{}, up{}, down{};
+  bool weights = false, zeros = false;  // set, with zero points
+  Maps maps;
+  TileMaps tile_maps;
   char* ws = nullptr;
   char* arranged = nullptr;  // the scales' and zero points' copies
 };
 
 namespace {
 
-// Teams of warps and K splits.  A warp on its own is cheapest per item, but
-// few tokens read few experts, and their row tiles alone would leave warps
-// idle.  Estimated time of one product with `team` warps to an item and
-// `splits` K splits, in us: an SM streams a unit in 0.1 at best, a warp with
-// its two stages in 0.6, and each item ends with about 0.3 (0.5 where a team
-// adds up).
+// Teams of warps and K splits.  Estimated time, in us, of one product with
+// `team` warps to an item and `splits` K splits: with w of an SM's 16 warps at
+// work each takes 0.28 + 0.125 w for a unit (fitted to 6, 12 and 16 warps);
+// an SM's items come in rounds of 16 / team, and each round ends with the
+// teams' sums and the results (a warp alone 0.5, eight together 1.4).  Long
+// chains of units end at different times (0.15 a unit), and the splits' partial
+// sums cost the combine about 0.4 each.  One token of the
+// 4096 x 14336 eight-expert layer: 53 us with single warps and no split, 42
+// with teams of 4 and 4 splits; 64 tokens of 128 experts: 97 us with teams of
+// 8 in both products, 85 with teams of 2 and single warps.
 float estimate(long long items, int blocks, int team, int splits) {
   const long long per_sm = (items * splits + kSms - 1) / kSms;
-  const int units = (blocks + splits - 1) / splits;
+  const int units = ((blocks + splits - 1) / splits + team - 1) / team;
   const int teams = kItemWarps * kBlocksSm / team;
-  const float stream = 0.1f * per_sm * units;
-  const float chain = (float)((per_sm + teams - 1) / teams) * (0.6f * ((units + team - 1) / team) + (team > 1 ? 0.5f : 0.3f));
-  return std::max(stream, chain) + 0.02f * splits;
+  const long long full = per_sm / teams, rest = per_sm % teams;
+  auto unit_us = [](long long warps) { return 0.28f + 0.125f * (float)warps; };
+  const float round = team == 1 ? 0.5f : team == 8 ? 1.4f : 0.6f;
+  return units * ((float)full * unit_us(teams * team) + (rest ? unit_us(rest * team) : 0.f)) +
+         round * (float)(full + (rest > 0)) + 0.15f * units + 0.4f * (splits - 1);
 }
 
 struct Split {
@@ -817,24 +871,51 @@ long long chunks_of(const moe_w4* h, int T) {
   return experts * ((rows + kChunk - 1) / kChunk) + (h->S ? (T + kChunk - 1) / kChunk : 0);
 }
 
-Split gate_up_split(const moe_w4* h, int T) { return best_split(chunks_of(h, T) * (h->f / 32), h->d / kBlockK, 1); }
+// How a batch of T tokens is run.
+struct Run {
+  bool tiles;   // on the kernels of w4_tiles.cuh
+  Split gate_up, down;
+};
 
-Split down_split(const moe_w4* h, int T) {
-  return best_split(chunks_of(h, T) * (h->d / kRows), h->f / kBlockK, kMaxSplit);
+Run run_of(const moe_w4* h, int T) {
+  const long long experts = std::min<long long>(h->E, (long long)T * h->k);
+  Run r;
+  r.tiles = T * h->k > kInline && (long long)T * h->k >= kTileMinRows * experts;
+  if (!r.tiles) {
+    r.gate_up = best_split(chunks_of(h, T) * (h->f / 32), h->d / kBlockK, 1);
+    r.down = best_split(chunks_of(h, T) * (h->d / kRows), h->f / kBlockK, kMaxSplit);
+    return r;
+  }
+  // a block to an SM: the K split whose fullest block has the fewest columns
+  // to do, with about three column blocks' time at the end of each item
+  const long long rows = ((long long)T * h->k + experts - 1) / experts;
+  const long long items = (experts * ((rows + kTileTokens - 1) / kTileTokens) +
+                           (h->S ? (T + kTileTokens - 1) / kTileTokens : 0)) * ((h->d + 2 * kTileRows - 1) / (2 * kTileRows));
+  const int blocks = h->f / kBlockK;
+  r.gate_up = Split{1, 1};
+  r.down = Split{1, 1};
+  long long least = 0;
+  for (int s = 1; s <= kMaxSplit && s <= blocks; ++s) {
+    const long long cost = (items * s + kSms - 1) / kSms * ((blocks + s - 1) / s + 3) + s;
+    if (s == 1 || cost < least) least = cost, r.down.splits = s;
+  }
+  return r;
 }
 
 struct Layout {
-  size_t y, list, slot, row, bytes;
+  size_t y, xg, status, list, slot, row, bytes;
 };
 
 Layout layout(const moe_w4* h, int T_max) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   const size_t slots = (size_t)T_max * (h->k + h->S);
   size_t y = 0;  // shorter batches may split more
-  for (int T = 1; T <= T_max; ++T) y = std::max(y, (size_t)T * (h->k + h->S) * h->d * 4 * down_split(h, T).splits);
+  for (int T = 1; T <= T_max; ++T) y = std::max(y, (size_t)T * (h->k + h->S) * h->d * 4 * run_of(h, T).down.splits);
   Layout l;
   l.y = up(slots * h->f * 2);
-  l.list = l.y + up(y);
+  l.xg = l.y + up(y);
+  l.status = l.xg + up(slots * h->d * 2);
+  l.list = l.status + 256;
   l.slot = l.list + up(sizeof(List));
   l.row = l.slot + up(slots * 2);
   l.bytes = l.row + up(slots * 2);
@@ -852,8 +933,9 @@ Arranged arranged(const moe_w4* h) {
   return Arranged{2 * n * 2, 3 * n * 2, 3 * n * 2 + 2 * n, 3 * n * 3};
 }
 
-cudaError_t launch_after(void (*kernel)(Experts), dim3 grid, int threads, int smem, bool overlap, cudaStream_t s,
-                         const Experts& a) {
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, int smem, bool overlap, cudaStream_t s,
+                         const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
@@ -864,22 +946,49 @@ cudaError_t launch_after(void (*kernel)(Experts), dim3 grid, int threads, int sm
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = overlap ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Codes [rows, bytes]: boxes of 64 bytes x box_rows, 64-byte swizzle.
+bool encode_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t bytes, uint32_t box_rows) {
+  cuuint64_t dims[2] = {bytes, rows};
+  cuuint64_t strides[1] = {bytes};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return moe::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// bf16 rows [rows, cols]: boxes of 64 columns x 32 rows, 128-byte swizzle.
+bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * 2};
+  cuuint32_t box[2] = {64, 32};
+  cuuint32_t es[2] = {1, 1};
+  return moe::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Kernels {
-  void (*gate_up)(Experts);
-  void (*down)(Experts);
+  void (*gate_up)(Experts, Maps);
+  void (*down)(Experts, Maps);
+  void (*tiles_gate_up)(Experts, TileMaps);
+  void (*tiles_down)(Experts, TileMaps);
+  int smem, tiles_smem;
 };
 
-template <int G>
-Kernels kernels_of(bool zeros) {
-  return zeros ? Kernels{w4_experts<false, G, true>, w4_experts<true, G, true>}
-               : Kernels{w4_experts<false, G, false>, w4_experts<true, G, false>};
+template <int G, bool Z>
+Kernels kernels_of() {
+  return Kernels{w4_experts<false, G, Z>, w4_experts<true, G, Z>, w4_tiles<false, G, Z>, w4_tiles<true, G, Z>,
+                 Smem<G, Z>::kBytes, TileSmem<G, Z>::kBytes};
 }
 
 Kernels kernels(int group, bool zeros) {
-  return group == 32 ? kernels_of<32>(zeros) : group == 64 ? kernels_of<64>(zeros) : kernels_of<128>(zeros);
+  if (group == 32) return zeros ? kernels_of<32, true>() : kernels_of<32, false>();
+  if (group == 64) return zeros ? kernels_of<64, true>() : kernels_of<64, false>();
+  return zeros ? kernels_of<128, true>() : kernels_of<128, false>();
 }
 
 }  // namespace
@@ -951,6 +1060,7 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (e == cudaSuccess && (major != 10 || minor != 3))
     return moe::set_error(MOE_E_INVAL, "this library is built for sm_103a (GB300) only");
+  if (!moe::encode_fn()) return moe::set_error(MOE_E_CUDA, "cuTensorMapEncodeTiled is not available");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (e == cudaSuccess && h->ws) {
     e = cudaStreamSynchronize(s);
@@ -969,11 +1079,21 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
   e = cudaMemsetAsync(h->ws, 0, bytes, s);
   for (int z = 0; z < 2 && e == cudaSuccess; ++z) {
     const Kernels kn = kernels(h->group, z);
-    e = cudaFuncSetAttribute((const void*)kn.gate_up, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute((const void*)kn.down, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const struct {
+      const void* f;
+      int smem;
+    } all[] = {{(const void*)kn.gate_up, kn.smem},
+               {(const void*)kn.down, kn.smem},
+               {(const void*)kn.tiles_gate_up, kn.tiles_smem},
+               {(const void*)kn.tiles_down, kn.tiles_smem}};
+    for (const auto& k : all)
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_reserve");
+  const Layout l = layout(h, T_max);
+  const uint64_t slots = (uint64_t)T_max * (h->k + h->S);
+  if (!encode_rows(&h->tile_maps.x, h->ws + l.xg, slots, h->d) || !encode_rows(&h->tile_maps.h, h->ws, slots, h->f))
+    return moe::set_error(MOE_E_INVAL, "tensor map encoding failed");
   h->T_max = T_max;
   moe::clear_error();
   return MOE_OK;
@@ -1007,9 +1127,16 @@ int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weig
                z ? reinterpret_cast<uint2*>(h->arranged + (d ? at.zeros_down : at.zeros)) : nullptr);
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "w4_arrange");
-  h->gate = take(gate);
-  h->up = take(up);
-  h->down = take(down);
+  const uint64_t n = h->E + h->S;
+  if (!encode_codes(&h->maps.gate, gate->codes, n * h->f, h->d / 2, 32) ||
+      !encode_codes(&h->maps.up, up->codes, n * h->f, h->d / 2, 32) ||
+      !encode_codes(&h->maps.down, down->codes, n * h->d, h->f / 2, kRows) ||
+      !encode_codes(&h->tile_maps.gate, gate->codes, n * h->f, h->d / 2, kTileRows) ||
+      !encode_codes(&h->tile_maps.up, up->codes, n * h->f, h->d / 2, kTileRows) ||
+      !encode_codes(&h->tile_maps.down, down->codes, n * h->d, h->f / 2, kTileRows))
+    return moe::set_error(MOE_E_INVAL, "tensor map encoding failed");
+  h->weights = true;
+  h->zeros = z;
   return MOE_OK;
 }
 
@@ -1017,7 +1144,7 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
                    void* stream) {
   if (!h) return moe::set_error(MOE_E_INVAL, "null handle");
   if (!h->ws) return moe::set_error(MOE_E_STATE, "moe_w4_reserve was not called");
-  if (!h->gate.codes) return moe::set_error(MOE_E_STATE, "moe_w4_set_weights was not called");
+  if (!h->weights) return moe::set_error(MOE_E_STATE, "moe_w4_set_weights was not called");
   if (T < 0 || T > h->T_max) return moe::set_error(MOE_E_INVAL, "T out of range (0..T_max)");
   if (T == 0) return MOE_OK;
   if (!x || !idx || !w || !out) return moe::set_error(MOE_E_INVAL, "null tensor pointer");
@@ -1031,13 +1158,10 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   a.E = h->E;
   a.k = h->k;
   a.S = h->S;
-  const Split down = down_split(h, T);
-  a.team[0] = gate_up_split(h, T).team;
-  a.team[1] = down.team;
-  a.splits = down.splits;
-  a.gate = h->gate.codes;
-  a.up = h->up.codes;
-  a.down = h->down.codes;
+  const Run r = run_of(h, T);
+  a.team[0] = r.gate_up.team;
+  a.team[1] = r.down.team;
+  a.splits = r.down.splits;
   const Arranged at = arranged(h);
   a.scales[0] = reinterpret_cast<const uint4*>(h->arranged);
   a.scales[1] = reinterpret_cast<const uint4*>(h->arranged + at.down);
@@ -1048,20 +1172,41 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   a.w = w;
   a.h = reinterpret_cast<__nv_bfloat16*>(h->ws);
   a.y = reinterpret_cast<float*>(h->ws + l.y);
+  a.xg = reinterpret_cast<__nv_bfloat16*>(h->ws + l.xg);
+  a.status = reinterpret_cast<int*>(h->ws + l.status);
   a.list = h->ws + l.list;
   a.list_slot = reinterpret_cast<uint16_t*>(h->ws + l.slot);
   a.list_row = reinterpret_cast<uint16_t*>(h->ws + l.row);
   a.out = static_cast<__nv_bfloat16*>(out);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Kernels kn = kernels(h->group, h->gate.zeros != nullptr);
+  const Kernels kn = kernels(h->group, h->zeros);
   const bool listed = T * h->k > kInline;
-  const dim3 grid(kSms * kBlocksSm);
   cudaError_t e = cudaSuccess;
   if (listed) e = launch_after(w4_list, dim3(1), 1024, 0, false, s, a);
-  if (e == cudaSuccess) e = launch_after(kn.gate_up, grid, kItemWarps * 32, kSmem, listed, s, a);
-  if (e == cudaSuccess) e = launch_after(kn.down, grid, kItemWarps * 32, kSmem, true, s, a);
+  if (r.tiles) {
+    if (e == cudaSuccess) e = launch_after(w4_gather, dim3(T * (h->k + h->S)), 128, 0, true, s, a);
+    if (e == cudaSuccess) e = launch_after(kn.tiles_gate_up, dim3(kSms), kTileThreads, kn.tiles_smem, true, s, a, h->tile_maps);
+    if (e == cudaSuccess) e = launch_after(kn.tiles_down, dim3(kSms), kTileThreads, kn.tiles_smem, true, s, a, h->tile_maps);
+  } else {
+    const dim3 grid(kSms * kBlocksSm);
+    if (e == cudaSuccess) e = launch_after(kn.gate_up, grid, kItemWarps * 32, kn.smem, listed, s, a, h->maps);
+    if (e == cudaSuccess) e = launch_after(kn.down, grid, kItemWarps * 32, kn.smem, true, s, a, h->maps);
+  }
   if (e == cudaSuccess) e = launch_after(w4_combine, dim3((h->d / 4 + 127) / 128, T), 128, 0, true, s, a);
   return e == cudaSuccess ? MOE_OK : moe::set_cuda_error(e, "w4_experts");
+}
+
+int moe_w4_status(moe_w4_t* h, void* stream) {
+  if (!h) return moe::set_error(MOE_E_INVAL, "null handle");
+  if (!h->ws) return moe::set_error(MOE_E_STATE, "moe_w4_reserve was not called");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* at = reinterpret_cast<int*>(h->ws + layout(h, h->T_max).status);
+  int status = 0;
+  cudaError_t e = cudaMemcpyAsync(&status, at, sizeof(int), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && status) e = cudaMemsetAsync(at, 0, sizeof(int), s);
+  if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_status");
+  return status ? moe::set_error(status, "device wait timed out") : MOE_OK;
 }
 
 void moe_w4_destroy(moe_w4_t* h) {
