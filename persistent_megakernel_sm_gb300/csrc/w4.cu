@@ -149,8 +149,11 @@ struct Experts {
   int T, d, f, E, k, S;
   int team[2];              // warps to an item, gate/up and down
   int splits;               // K splits of the down product
+  int scale_groups[2];      // an expert's fours of row tiles, gate/up and down
+  int tile_tokens;          // token rows of an item of the tile kernels
   // gate/up's and down's scales and zero points as the units take them:
-  // [expert][row tile][128-column block][8 lanes][128 / G groups][8 rows]
+  // [expert][4 row tiles][128-column block][row tile][8 lanes][128 / G groups][8
+  // rows], the last four tiles of an expert filled up
   const uint4* scales[2];
   const uint2* zeros[2];
   const __nv_bfloat16* x;   // [T, d]
@@ -388,10 +391,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 }
 
 // Wait for a stage's loads, two seconds at most: then the error is noted, no
-// later wait lasts, and the pass goes on, its output undefined.
+// later wait lasts, and the pass goes on, its output undefined.  The clock and
+// the noted error are looked at only after many tries: a load from global
+// memory between two tries makes a wait end most of a microsecond late.
 __device__ __forceinline__ void wait_stage(uint64_t* bar, uint32_t parity, int* status) {
 #pragma unroll 1
-  for (int i = 0; i < 64; ++i)
+  for (int i = 0; i < 1 << 14; ++i)
     if (moe::mbar_try_wait(bar, parity)) return;
   if (moe::ld_relaxed(status) != 0) return;
   if (!moe::mbar_wait(bar, parity, moe::globaltimer() + 2000000000ull)) *status = MOE_E_TIMEOUT;
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
   // ---- the cursor of the loads, kStages units ahead of the products
   int l_item, l_at = 0, l_kb = 0, l_row = 0;
   Item l_it{};
-  long long l_unit = 0;          // of the item's first column block
+  long long l_unit = 0;          // of the item's first column block; the next is 4 on
   const char* l_token = nullptr;  // lane n: token row n
   bool l_more;
   auto l_seek = [&]() {  // the next item from l_item on of which this warp has a unit
@@ -533,7 +538,7 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
       l_item += teams;
     }
     l_row = l_it.e * rows_of + l_it.tile * (DOWN ? kRows : 32);
-    l_unit = ((long long)l_it.e * row_tiles + l_it.tile) * blocks_k;
+    l_unit = ((long long)l_it.e * a.scale_groups[DOWN] + (l_it.tile >> 2)) * blocks_k * 4 + (l_it.tile & 3);
     if (lane < l_it.rows)
       l_token = reinterpret_cast<const char*>((DOWN ? a.h : a.x) + (size_t)(DOWN ? rows.slot : rows.row)[l_it.first + lane] * K);
   };
@@ -553,10 +558,10 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
           tma_load(dst, &maps.gate, bar, l_kb * 64, l_row);
           tma_load(dst + kCodeBytes / 2, &maps.up, bar, l_kb * 64, l_row);
         }
-        bulk_load(scales + stage * Sm::kScaleBytes, a.scales[DOWN] + (l_unit + l_kb) * (Sm::kScaleBytes / 16),
+        bulk_load(scales + stage * Sm::kScaleBytes, a.scales[DOWN] + (l_unit + l_kb * 4) * (Sm::kScaleBytes / 16),
                   Sm::kScaleBytes, bar);
         if (Z)
-          bulk_load(zeros + stage * Sm::kZeroBytes, a.zeros[DOWN] + (l_unit + l_kb) * (Sm::kZeroBytes / 8),
+          bulk_load(zeros + stage * Sm::kZeroBytes, a.zeros[DOWN] + (l_unit + l_kb * 4) * (Sm::kZeroBytes / 8),
                     Sm::kZeroBytes, bar);
       }
     }
@@ -720,16 +725,20 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
 }
 
 // Arrange scales and zero points once as the units take them: one thread per
-// lane and group of a unit.  first, second: the matrices of a unit's first and last 32
-// rows (gate and up; down twice, second32 = 1).
+// lane and group of a unit.  first, second: the matrices of a unit's first and
+// last 32 rows (gate and up; down twice, both32 = 0).
 __global__ void __launch_bounds__(256)
-    w4_arrange(Weight first, Weight second, int second32, long long units, int tile_rows, int blocks_k, int kg,
+    w4_arrange(Weight first, Weight second, int both32, int experts, int row_tiles, int blocks_k, int kg,
                uint4* scales, uint2* zeros) {
+  const int fours = (row_tiles + 3) / 4;
+  const long long units = (long long)experts * fours * blocks_k * 4;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < units * 8 * kg; i += (long long)gridDim.x * 256) {
     const int grp = (int)(i % kg), g = (int)(i / kg % 8);
     const long long unit = i / kg / 8;
-    const int kb = (int)(unit % blocks_k);
-    const long long tile = unit / blocks_k;  // over the experts
+    const int kb = (int)(unit / 4 % blocks_k);
+    const long long four = unit / 4 / blocks_k;  // over the experts
+    const int tile = (int)(four % fours) * 4 + (int)(unit & 3);
+    if (tile >= row_tiles) continue;
     union {
       uint4 q;
       __nv_bfloat16 b[8];
@@ -741,7 +750,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const Weight& m = r < 4 ? first : second;
-      const long long row = tile * tile_rows + (second32 ? r * 8 : (r & 3) * 8) + g;
+      const long long row =
+          (four / fours * row_tiles + tile) * (both32 ? 32 : kRows) + (both32 ? (r & 3) * 8 : r * 8) + g;
       const long long o = (row * blocks_k + kb) * kg + grp;
       s.b[r] = m.scales[o];
       if (zeros) z.b[r] = m.zeros[o] & 15;
@@ -820,7 +830,8 @@ struct moe_w4 {
   int T_max = 0;
   bool weights = false, zeros = false;  // set, with zero points
   Maps maps;
-  TileMaps tile_maps;
+  TileMaps tile_maps;                                              // x and h: of the pass
+  CUtensorMap x_maps[kTileTokens / 32], h_maps[kTileTokens / 32];  // by an item's token rows
   char* ws = nullptr;
   char* arranged = nullptr;  // the scales' and zero points' copies
 };
@@ -873,15 +884,15 @@ long long chunks_of(const moe_w4* h, int T) {
 
 // How a batch of T tokens is run.
 struct Run {
-  bool tiles;   // on the kernels of w4_tiles.cuh
+  int tokens;   // > 0: on the kernels of w4_tiles.cuh, so many token rows an item
   Split gate_up, down;
 };
 
 Run run_of(const moe_w4* h, int T) {
   const long long experts = std::min<long long>(h->E, (long long)T * h->k);
   Run r;
-  r.tiles = T * h->k > kInline && (long long)T * h->k >= kTileMinRows * experts;
-  if (!r.tiles) {
+  r.tokens = 0;
+  if (T * h->k <= kInline || (long long)T * h->k < kTileMinRows * experts) {
     r.gate_up = best_split(chunks_of(h, T) * (h->f / 32), h->d / kBlockK, 1);
     r.down = best_split(chunks_of(h, T) * (h->d / kRows), h->f / kBlockK, kMaxSplit);
     return r;
@@ -889,8 +900,11 @@ Run run_of(const moe_w4* h, int T) {
   // a block to an SM: the K split whose fullest block has the fewest columns
   // to do, with about three column blocks' time at the end of each item
   const long long rows = ((long long)T * h->k + experts - 1) / experts;
-  const long long items = (experts * ((rows + kTileTokens - 1) / kTileTokens) +
-                           (h->S ? (T + kTileTokens - 1) / kTileTokens : 0)) * ((h->d + 2 * kTileRows - 1) / (2 * kTileRows));
+  // room for an expert with three deviations more rows than the mean
+  const int room = (int)(rows + 3.f * sqrtf((float)rows));
+  r.tokens = std::min(kTileTokens, (room + 31) / 32 * 32);
+  const long long items = (experts * ((rows + r.tokens - 1) / r.tokens) + (h->S ? (T + r.tokens - 1) / r.tokens : 0)) *
+                          ((h->d + 2 * kTileRows - 1) / (2 * kTileRows));
   const int blocks = h->f / kBlockK;
   r.gate_up = Split{1, 1};
   r.down = Split{1, 1};
@@ -928,9 +942,13 @@ struct Arranged {
   size_t down, zeros, zeros_down, bytes;
 };
 
+// Fours of row tiles of an expert: 128 rows of gate and up, 256 of down.
+int fours(const moe_w4* h, bool down) { return down ? (h->d + 255) / 256 : h->f / 128; }
+
 Arranged arranged(const moe_w4* h) {
-  const size_t n = (size_t)(h->E + h->S) * h->f * h->d / h->group;  // of one matrix
-  return Arranged{2 * n * 2, 3 * n * 2, 3 * n * 2 + 2 * n, 3 * n * 3};
+  const size_t n = (size_t)(h->E + h->S) * 256 / h->group;  // scales of a four and a column
+  const size_t gate_up = n * fours(h, false) * h->d, down = n * fours(h, true) * h->f;
+  return Arranged{2 * gate_up, 2 * (gate_up + down), 2 * (gate_up + down) + gate_up, 3 * (gate_up + down)};
 }
 
 template <typename... A>
@@ -960,11 +978,11 @@ bool encode_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t byte
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 rows [rows, cols]: boxes of 64 columns x 32 rows, 128-byte swizzle.
-bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols) {
+// bf16 rows [rows, cols]: boxes of 64 columns x box_rows, 128-byte swizzle.
+bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {64, 32};
+  cuuint32_t box[2] = {64, box_rows};
   cuuint32_t es[2] = {1, 1};
   return moe::encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -976,13 +994,13 @@ struct Kernels {
   void (*down)(Experts, Maps);
   void (*tiles_gate_up)(Experts, TileMaps);
   void (*tiles_down)(Experts, TileMaps);
-  int smem, tiles_smem;
+  int smem;
 };
 
 template <int G, bool Z>
 Kernels kernels_of() {
   return Kernels{w4_experts<false, G, Z>, w4_experts<true, G, Z>, w4_tiles<false, G, Z>, w4_tiles<true, G, Z>,
-                 Smem<G, Z>::kBytes, TileSmem<G, Z>::kBytes};
+                 Smem<G, Z>::kBytes};
 }
 
 Kernels kernels(int group, bool zeros) {
@@ -1084,16 +1102,18 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
       int smem;
     } all[] = {{(const void*)kn.gate_up, kn.smem},
                {(const void*)kn.down, kn.smem},
-               {(const void*)kn.tiles_gate_up, kn.tiles_smem},
-               {(const void*)kn.tiles_down, kn.tiles_smem}};
+               {(const void*)kn.tiles_gate_up, 227 * 1024},
+               {(const void*)kn.tiles_down, 227 * 1024}};
     for (const auto& k : all)
       if (e == cudaSuccess) e = cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_reserve");
   const Layout l = layout(h, T_max);
   const uint64_t slots = (uint64_t)T_max * (h->k + h->S);
-  if (!encode_rows(&h->tile_maps.x, h->ws + l.xg, slots, h->d) || !encode_rows(&h->tile_maps.h, h->ws, slots, h->f))
-    return moe::set_error(MOE_E_INVAL, "tensor map encoding failed");
+  for (uint32_t n = 0; n < kTileTokens / 32; ++n)
+    if (!encode_rows(&h->x_maps[n], h->ws + l.xg, slots, h->d, 32 * n + 32) ||
+        !encode_rows(&h->h_maps[n], h->ws, slots, h->f, 32 * n + 32))
+      return moe::set_error(MOE_E_INVAL, "tensor map encoding failed");
   h->T_max = T_max;
   moe::clear_error();
   return MOE_OK;
@@ -1120,10 +1140,10 @@ int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weig
   const bool z = gate->zeros != nullptr;
   cudaError_t e = cudaSuccess;
   for (int d = 0; d < 2 && e == cudaSuccess; ++d) {
-    const int tile_rows = d ? kRows : 32, blocks_k = (d ? h->f : h->d) / kBlockK;
-    const long long units = (long long)(h->E + h->S) * ((d ? h->d : h->f) / tile_rows) * blocks_k;
-    e = launch(w4_arrange, convert_grid(units * 8 * kg), 256, s, take(d ? down : gate), take(d ? down : up), d, units,
-               tile_rows, blocks_k, kg, reinterpret_cast<uint4*>(h->arranged + (d ? at.down : 0)),
+    const int row_tiles = d ? h->d / kRows : h->f / 32, blocks_k = (d ? h->f : h->d) / kBlockK;
+    const long long units = (long long)(h->E + h->S) * fours(h, d) * blocks_k * 4;
+    e = launch(w4_arrange, convert_grid(units * 8 * kg), 256, s, take(d ? down : gate), take(d ? down : up), 1 - d,
+               h->E + h->S, row_tiles, blocks_k, kg, reinterpret_cast<uint4*>(h->arranged + (d ? at.down : 0)),
                z ? reinterpret_cast<uint2*>(h->arranged + (d ? at.zeros_down : at.zeros)) : nullptr);
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "w4_arrange");
@@ -1162,6 +1182,9 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   a.team[0] = r.gate_up.team;
   a.team[1] = r.down.team;
   a.splits = r.down.splits;
+  a.tile_tokens = r.tokens;
+  a.scale_groups[0] = fours(h, false);
+  a.scale_groups[1] = fours(h, true);
   const Arranged at = arranged(h);
   a.scales[0] = reinterpret_cast<const uint4*>(h->arranged);
   a.scales[1] = reinterpret_cast<const uint4*>(h->arranged + at.down);
@@ -1183,10 +1206,13 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   const bool listed = T * h->k > kInline;
   cudaError_t e = cudaSuccess;
   if (listed) e = launch_after(w4_list, dim3(1), 1024, 0, false, s, a);
-  if (r.tiles) {
+  if (r.tokens) {
+    const int smem = tile_smem(r.tokens, h->group, h->zeros).bytes;
+    h->tile_maps.x = h->x_maps[r.tokens / 32 - 1];
+    h->tile_maps.h = h->h_maps[r.tokens / 32 - 1];
     if (e == cudaSuccess) e = launch_after(w4_gather, dim3(T * (h->k + h->S)), 128, 0, true, s, a);
-    if (e == cudaSuccess) e = launch_after(kn.tiles_gate_up, dim3(kSms), kTileThreads, kn.tiles_smem, true, s, a, h->tile_maps);
-    if (e == cudaSuccess) e = launch_after(kn.tiles_down, dim3(kSms), kTileThreads, kn.tiles_smem, true, s, a, h->tile_maps);
+    if (e == cudaSuccess) e = launch_after(kn.tiles_gate_up, dim3(kSms), kTileThreads, smem, true, s, a, h->tile_maps);
+    if (e == cudaSuccess) e = launch_after(kn.tiles_down, dim3(kSms), kTileThreads, smem, true, s, a, h->tile_maps);
   } else {
     const dim3 grid(kSms * kBlocksSm);
     if (e == cudaSuccess) e = launch_after(kn.gate_up, grid, kItemWarps * 32, kn.smem, listed, s, a, h->maps);

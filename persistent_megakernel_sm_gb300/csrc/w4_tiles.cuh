@@ -2,12 +2,19 @@
 // the products on the fifth-generation tensor cores (part of w4.cu).
 //
 // An item is 256 weight rows of one expert (gate/up: 128 of each, down: 256)
-// times up to 128 of its token rows.  Codes come in by TMA; eight warps, a
-// warpgroup for each 128 rows, turn a block of 128 columns into bf16 numbers
-// and store them as an MMA operand in tensor memory (lane = weight row), and
-// one thread issues the MMAs: A from tensor memory, the tokens from shared
-// memory, fp32 sums in tensor memory over all of K.  Two operand buffers per
-// warpgroup and four stages keep loads, conversion and MMAs apart.
+// times up to 96 of its token rows.  Codes come in by TMA; sixteen warps, a
+// warpgroup for each 64 columns of a block of 128 and each 128 rows, turn them
+// into bf16 numbers and store them as an MMA operand in tensor memory (lane =
+// weight row), and a warp for each 128 rows issues the MMAs: A from tensor
+// memory, the tokens from shared memory, fp32 sums in tensor memory over all of
+// K.  Two sets of sums, so that a further warpgroup takes an item's sums out
+// while the next item's come in.  As many stages as fit (8 for 32 tokens an
+// item, 5 for 96) cover a stage's way from its loads' start to its MMAs' end.
+//
+// An MMA of 128 x 16 by 16 to 96 tokens takes 30 to 60 cycles to issue from one
+// warp whatever its width, so 16 of them and their commits, on two warps, bound
+// a block of 16 KB of codes at some 600 cycles; its loads take 690 at the whole
+// device's bandwidth.
 //
 // A code q as an operand: the bits n = q (or 16 q, for every other pair) of the
 // word are the bf16 number n 2^-133, and one bf16 fused multiply-add with
@@ -18,41 +25,53 @@
 // scaling the sums instead would cost one fp32 operation per row, token and
 // group, as many as the conversion itself at 64 tokens.
 //
-// Per 128 columns and warp the conversion is 16 words x (5 + 4) instructions;
-// the tokens' rows are read again for every 256 weight rows, which is why both
-// matrices (or twice the rows) share them.
+// A conversion is 5 + 4 instructions for 8 codes.  The tokens' rows are read
+// again for every 256 weight rows, which is why both matrices (or twice the
+// rows) share them.
 #pragma once
 
-constexpr int kTileTokens = 128;
+constexpr int kTileTokens = 96;      // at most
 constexpr int kTileRows = 128;       // of one MMA; two of them share the tokens
-constexpr int kTileStages = 4;
-constexpr int kTileThreads = 320;    // 8 conversion warps, the loads' and the MMAs'
-constexpr uint32_t kAColumn = 256;   // operand buffers: [tile][buffer][64 columns]
+constexpr int kTileStages = 8;       // at most
+constexpr int kConvertWarps = 16;
+constexpr int kFirstConvert = 4;     // warps 0 and 3 load, 1 and 2 issue the MMAs
+constexpr int kFirstOut = kFirstConvert + kConvertWarps;  // four warps take the sums out
+constexpr int kTileThreads = (kFirstOut + 4) * 32;
+// tensor memory: sums [set][tile][96 columns], operands [tile][half][32 columns]
+constexpr uint32_t kAColumn = 4 * kTileTokens;
 constexpr float kTileUnscale = 137438953472.f;  // 2^37
 
 // x gathered by expert, and h: [T k + T S, columns], columns of each 8 in the
 // order 0 4 1 5 2 6 3 7, in the order of the list.
 struct TileMaps {
   CUtensorMap gate, up, down;  // codes, boxes of 64 bytes x 128 rows, 64-byte swizzle
-  CUtensorMap x, h;            // boxes of 64 columns x 32 rows, 128-byte swizzle
+  CUtensorMap x, h;            // boxes of 64 columns x an item's token rows, 128-byte swizzle
 };
 
-template <int G, bool Z>
+// Shared memory: `stages` stages, then the barriers and the list.  In a stage,
+// tokens [2 halves of 64 columns][token][128 bytes], codes [2 tiles][128
+// rows][64 bytes], 4 blocks of 64 rows' scales and zero points.
 struct TileSmem {
-  static constexpr int kG = kBlockK / G;
-  static constexpr int kTokens = 0;                                  // [2 halves of 64 columns][128 rows][128 bytes]
-  static constexpr int kHalf = kTileTokens * 128;
-  static constexpr int kCodes = kTokens + 2 * kHalf;                 // [2 tiles][128 rows][64 bytes]
-  static constexpr int kScales = kCodes + 2 * kTileRows * 64;        // 4 blocks of 64 rows
-  static constexpr int kZeros = kScales + 4 * kRows * kG * 2;
-  static constexpr int kStage = (kZeros + (Z ? 4 * kRows * kG : 0) + 1023) / 1024 * 1024;
-  static constexpr int kWeightBytes = 2 * kTileRows * 64 + 4 * kRows * kG * (Z ? 3 : 2);
-  static constexpr int kBars = kTileStages * kStage;
-  static constexpr int kItemStart = kBars + 128;
-  static constexpr int kList = kItemStart + (kMaxE + 2) * 4;
-  static constexpr int kBytes = kList + (int)sizeof(List) + 1024;
-  static_assert(kBytes <= 227 * 1024, "one block to an SM");
+  int half, codes, scales, zeros, stage, stages, bars, bytes;
 };
+
+constexpr int kTileBars = 3 * 64 + 64;  // full, empty; operands and sums
+constexpr int kTileTail = kTileBars + (kMaxE + 2) * 4 + (int)sizeof(List);
+
+__host__ __device__ constexpr TileSmem tile_smem(int tokens, int group, bool zeros) {
+  TileSmem m{};
+  const int kg = kBlockK / group;
+  m.half = tokens * 128;
+  m.codes = 2 * m.half;
+  m.scales = m.codes + 2 * kTileRows * 64;
+  m.zeros = m.scales + 4 * kRows * kg * 2;
+  m.stage = (m.zeros + (zeros ? 4 * kRows * kg : 0) + 1023) / 1024 * 1024;
+  const int fit = (227 * 1024 - 1024 - kTileTail) / m.stage;
+  m.stages = fit < kTileStages ? fit : kTileStages;
+  m.bars = m.stages * m.stage;
+  m.bytes = m.bars + kTileTail + 1024;
+  return m;
+}
 
 struct TileItem {
   int e, tile, split, rows, first, kb0, kb1;
@@ -82,13 +101,49 @@ __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b_de
       : "memory");
 }
 
+// Whether a barrier's phase is over, without waiting.  A look takes most of
+// 200 cycles even at a barrier that is ready, so the loops look one step ahead.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+// Arrive on the barrier at `bar` when the MMAs issued so far are done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+// Volatile, so that a conversion stays in front of the wait that follows it.
+__device__ __forceinline__ uint32_t fma2v(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  asm volatile("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul2v(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm volatile("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -122,19 +177,20 @@ __global__ void __launch_bounds__(128) w4_gather(Experts a) {
 template <bool DOWN, int G, bool Z>
 __global__ void __launch_bounds__(kTileThreads, 1)
     w4_tiles(const Experts a, const __grid_constant__ TileMaps maps) {
-  using Sm = TileSmem<G, Z>;
-  constexpr int kG = Sm::kG;
+  constexpr int kG = kBlockK / G;
+  const int most = a.tile_tokens;  // token rows of an item
+  const TileSmem sm = tile_smem(most, G, Z);
   extern __shared__ char smem_raw[];
   char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Sm::kBars);  // a stage's loads
-  uint64_t* empty = full + kTileStages;                            // 8 warps and the MMAs are done with it
-  uint64_t* a_full = empty + kTileStages;                          // [buffer] both tiles' operands stored
-  uint64_t* a_free = a_full + 2;                                   // [buffer] read by the MMAs
-  uint64_t* d_full = a_free + 2;                                   // an item's sums
-  uint64_t* d_free = d_full + 1;                                   // read by the 8 warps
-  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(d_free + 1);
-  int* item_start = reinterpret_cast<int*>(smem + Sm::kItemStart);
-  List* list = reinterpret_cast<List*>(smem + Sm::kList);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + sm.bars);  // a stage's loads, the weights' and the tokens'
+  uint64_t* empty = full + kTileStages;                            // 16 warps and the MMAs are done with it
+  uint64_t* a_full = empty + kTileStages;                          // [tile][half] the operand is stored (4 warps)
+  uint64_t* a_free = a_full + 4;                                   // [tile][half] read by the MMAs
+  uint64_t* d_full = a_free + 4;                                   // [set] an item's sums, both tiles'
+  uint64_t* d_free = d_full + 2;                                   // [set] read by 4 warps
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(d_free + 2);
+  int* item_start = reinterpret_cast<int*>(smem + sm.bars + kTileBars);
+  List* list = reinterpret_cast<List*>(item_start + kMaxE + 2);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = DOWN ? a.f : a.d;
   const int rows_of = DOWN ? a.d : a.f;
@@ -144,19 +200,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int blocks_k = K / kBlockK;
 
   if (tid == 0) {
-    for (int s = 0; s < kTileStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, 9);
+    for (int s = 0; s < sm.stages; ++s) {
+      mbar_init(full + s, 2);
+      mbar_init(empty + s, kConvertWarps + 2);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(a_full + b, 8);
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(a_full + b, 4);
       mbar_init(a_free + b, 1);
     }
-    mbar_init(d_full, 1);
-    mbar_init(d_free, 8);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(d_full + b, 2);
+      mbar_init(d_free + b, 4);
+    }
     moe::fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 0) {
     moe::tmem_alloc<1>(tmem_at, 512);
     moe::tmem_relinquish<1>();
   }
@@ -170,7 +228,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int base = 0;
     for (int i0 = 0; i0 < n_active; i0 += 32) {
       const int i = i0 + lane;
-      const int mine = i < n_active ? (list->start[i + 1] - list->start[i] + kTileTokens - 1) / kTileTokens * row_tiles *
+      const int mine = i < n_active ? (list->start[i + 1] - list->start[i] + most - 1) / most * row_tiles *
                                           splits : 0;
       int sum = mine;
 #pragma unroll
@@ -193,7 +251,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto item_of = [&](int i, int* at, TileItem* it) {  // `at` only moves forward
     while (i >= item_start[*at + 1]) ++*at;
     const int n = list->start[*at + 1] - list->start[*at];
-    const int chunks = (n + kTileTokens - 1) / kTileTokens;
+    const int chunks = (n + most - 1) / most;
     const int local = i - item_start[*at], rest = local / chunks, c = local - rest * chunks;
     it->e = list->expert[*at];
     it->tile = rest / splits;
@@ -206,191 +264,208 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     it->first = list->start[*at] + c * per;
   };
 
-  if (warp == 8) {
-    if (lane == 0) {  // ---------------------------------------------- loads
+  if (warp == 0 || warp == 3) {  // ------------------- loads: weights, tokens
+    if (elect_one()) {
+      const bool weights = warp == 0;
       int at = 0, s = 0;
       uint32_t phase = 1;  // a fresh barrier's preceding phase has passed
-      bool waited = false;
+      if (!weights) {      // the tokens (h) are the kernel's before; the weights wait for nobody
+        wait_for_previous_kernel();
+        moe::fence_proxy_async_global();
+      }
       for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
         TileItem it;
         item_of(i, &at, &it);
-        const int row0 = it.e * rows_of + it.tile * tile_rows;
-        // rows past the expert's belong to the next one (or are zero): never stored
-        const int boxes = (it.rows + 31) / 32;
-        // scale blocks of 64 rows (gate/up: 32 of each) that follow one another
-        const int blocks = min(4, (rows_of - it.tile * tile_rows + (DOWN ? 63 : 31)) / (DOWN ? 64 : 32));
-        const long long unit0 =
-            ((long long)it.e * (rows_of / (DOWN ? 64 : 32)) + (long long)it.tile * 4) * blocks_k;
-        const uint32_t weights = 2 * kTileRows * 64 + blocks * kRows * kG * (Z ? 3 : 2);
+        const int row = it.e * rows_of + it.tile * tile_rows;
+        // scale blocks of 64 rows (gate/up: 32 of each), four to a group
+        const long long unit = ((long long)it.e * a.scale_groups[DOWN] + it.tile) * blocks_k;
+        constexpr uint32_t kScaleBytes = 4 * kRows * kG * 2, kZeroBytes = Z ? 4 * kRows * kG : 0;
         for (int kb = it.kb0; kb < it.kb1; ++kb) {
           wait_stage(empty + s, phase, a.status);
-          char* st = smem + s * Sm::kStage;
-          moe::mbar_arrive_expect_tx(full + s, weights + boxes * 2 * 32 * 128);
-          const uint32_t codes = smem_u32(st + Sm::kCodes);
-          tma_load(codes, DOWN ? &maps.down : &maps.gate, full + s, kb * 64, row0);
-          tma_load(codes + kTileRows * 64, DOWN ? &maps.down : &maps.up, full + s, kb * 64, DOWN ? row0 + kTileRows : row0);
-          for (int q = 0; q < blocks; ++q) {
-            const long long unit = unit0 + (long long)q * blocks_k + kb;
-            bulk_load(st + Sm::kScales + q * kRows * kG * 2, a.scales[DOWN] + unit * (kRows * kG * 2 / 16),
-                      kRows * kG * 2, full + s);
+          const uint32_t st = smem_u32(smem) + s * sm.stage;
+          if (weights) {
+            moe::mbar_arrive_expect_tx(full + s, 2 * kTileRows * 64 + kScaleBytes + kZeroBytes);
+            tma_load(st + sm.codes, DOWN ? &maps.down : &maps.gate, full + s, kb * 64, row);
+            tma_load(st + sm.codes + kTileRows * 64, DOWN ? &maps.down : &maps.up, full + s, kb * 64,
+                     DOWN ? row + kTileRows : row);
+            bulk_load(smem + s * sm.stage + sm.scales, a.scales[DOWN] + (unit + kb) * (kScaleBytes / 16), kScaleBytes,
+                      full + s);
             if (Z)
-              bulk_load(st + Sm::kZeros + q * kRows * kG, a.zeros[DOWN] + unit * (kRows * kG / 8), kRows * kG, full + s);
+              bulk_load(smem + s * sm.stage + sm.zeros, a.zeros[DOWN] + (unit + kb) * (kZeroBytes / 8), kZeroBytes,
+                        full + s);
+          } else {
+            // rows past the expert's belong to the next one (or are zero): never stored
+            moe::mbar_arrive_expect_tx(full + s, 2 * sm.half);
+            tma_load(st, DOWN ? &maps.h : &maps.x, full + s, kb * kBlockK, it.first);
+            tma_load(st + sm.half, DOWN ? &maps.h : &maps.x, full + s, kb * kBlockK + 64, it.first);
           }
-          if (!waited) {  // the tokens (h) are the kernel's before; the weights wait for nobody
-            wait_for_previous_kernel();
-            moe::fence_proxy_async_global();
-            waited = true;
-          }
-          for (int half = 0; half < 2; ++half)
-            for (int b = 0; b < boxes; ++b)
-              tma_load(smem_u32(st + Sm::kTokens + half * Sm::kHalf + b * 32 * 128), DOWN ? &maps.h : &maps.x, full + s,
-                       kb * kBlockK + half * 64, it.first + b * 32);
-          if (++s == kTileStages) s = 0, phase ^= 1;
+          if (++s == sm.stages) s = 0, phase ^= 1;
         }
       }
     }
-  } else if (warp == 9) {
-    if (lane == 0) {  // ----------------------------------------------- MMAs
-      int at = 0, s = 0, buf = 0, items = 0;
-      uint32_t phase = 0, a_phase = 0;
-      for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++items) {
-        TileItem it;
-        item_of(i, &at, &it);
-        const int n = max(16, (it.rows + 15) & ~15);
-        const uint32_t idesc = moe::idesc_bf16(kTileRows, n);
-        wait_stage(d_free, (items & 1) ^ 1, a.status);
+  } else if (warp < kFirstConvert) {  // ---------------------------------- MMAs
+    // the whole warp loops, on values the compiler can see are the same in all
+    // lanes (they then stay in uniform registers), and one lane issues
+    const int t = __shfl_sync(0xffffffffu, warp, 0) - 1;
+    const uint32_t smem0 = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t full0 = smem0 + sm.bars, a_free0 = full0 + (2 * kTileStages + 4 + t * 2) * 8;
+    const uint64_t half = sm.half >> 4;
+    const uint32_t from = tm + kAColumn + t * 64;
+    int at = 0, s = 0, items = 0;
+    uint32_t phase = 0, a_phase = 0;
+    bool full_ready = false, a_ready = false;
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++items) {
+      TileItem it;
+      item_of(i, &at, &it);
+      const uint32_t idesc = moe::idesc_bf16(kTileRows, max(16, (__shfl_sync(0xffffffffu, it.rows, 0) + 15) & ~15));
+      const int blocks = __shfl_sync(0xffffffffu, it.kb1 - it.kb0, 0);
+      const int set = items & 1;
+      const uint32_t d = tm + (set * 2 + t) * kTileTokens;
+      wait_stage(d_free + set, (items >> 1 & 1) ^ 1, a.status);
+      moe::tc_fence_after();
+      for (int kb = 0; kb < blocks; ++kb) {
+        const uint64_t b = moe::sw128_desc(smem0 + s * sm.stage);
+        if (!full_ready) wait_stage(full + s, phase, a.status);
+        if (!a_ready) wait_stage(a_full + t * 2, a_phase, a.status);
         moe::tc_fence_after();
-        for (int kb = it.kb0; kb < it.kb1; ++kb) {
-          wait_stage(full + s, phase, a.status);
-          wait_stage(a_full + buf, a_phase, a.status);
-          moe::tc_fence_after();
-          const uint32_t tokens = smem_u32(smem + s * Sm::kStage + Sm::kTokens);
+        a_ready = mbar_test(a_full + t * 2 + 1, a_phase);
+        if (elect_one()) {
+          mma_tmem_a(d, from, b, idesc, kb > 0);
 #pragma unroll
-          for (int j = 0; j < kBlockK / 16; ++j) {
-            const uint64_t b = moe::sw128_desc(tokens + (j >> 2) * Sm::kHalf + (j & 3) * 32);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              mma_tmem_a(tmem + t * kTileTokens, tmem + kAColumn + (t * 2 + buf) * 64 + j * 8, b, idesc,
-                         kb > it.kb0 || j > 0);
-          }
-          moe::mma_commit_all<1>(a_free + buf);
-          moe::mma_commit_all<1>(empty + s);
-          if (++s == kTileStages) s = 0, phase ^= 1;
-          buf ^= 1;
-          if (buf == 0) a_phase ^= 1;
+          for (int j = 1; j < 4; ++j) mma_tmem_a(d, from + j * 8, b + j * 2, idesc, true);
+          commit(a_free0);
         }
-        moe::mma_commit_all<1>(d_full);
+        __syncwarp();
+        if (!a_ready) wait_stage(a_full + t * 2 + 1, a_phase, a.status);
+        moe::tc_fence_after();
+        const uint32_t done = full0 + (kTileStages + s) * 8;
+        if (++s == sm.stages) s = 0, phase ^= 1;
+        a_phase ^= 1;
+        full_ready = mbar_test(full + s, phase);
+        a_ready = mbar_test(a_full + t * 2, a_phase);
+        if (elect_one()) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mma_tmem_a(d, from + 32 + j * 8, b + half + j * 2, idesc, true);
+          commit(a_free0 + 8);
+          commit(done);
+        }
+        __syncwarp();
       }
+      if (elect_one()) commit(full0 + (2 * kTileStages + 8 + set) * 8);  // d_full
+      __syncwarp();
     }
-  } else {  // ------------------------------- conversion, and the sums' way out
-    const int t = warp >> 2, row = (warp & 3) * 32 + lane;  // the tile, its row = the tensor memory's lane
-    const uint32_t lane_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  } else if (warp < kFirstOut) {  // ------------------------------- conversion
+    // the tile, the half of a block's columns, the row = the tensor memory's lane
+    const int group = (warp - kFirstConvert) >> 2, t = group & 1, half = group >> 1;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kAColumn + (t * 2 + half) * 32;
     // where this row's scales are in a stage: block, then [8 lanes][groups][8 rows]
     const int in_tile = DOWN ? t * kTileRows + row : row;  // of the item's rows of one matrix
-    const int block = in_tile / (DOWN ? 64 : 32), in_block = in_tile % (DOWN ? 64 : 32);
-    const int scale_at = block * kRows * kG + (in_block & 7) * kG * 8 + (in_block >> 3) + (DOWN ? 0 : t * 4);
+    const int in_block = in_tile % (DOWN ? 64 : 32);
+    const int scale_at =
+        in_tile / (DOWN ? 64 : 32) * kRows * kG + (in_block & 7) * kG * 8 + (in_block >> 3) + (DOWN ? 0 : t * 4);
     const int swizzle = row >> 1 & 3;
-    int at = 0, s = 0, buf = 0, items = 0;
+    const uint32_t code_at = smem_u32(smem) + sm.codes + (t * kTileRows + row) * 64;
+    const uint32_t code0 = code_at + ((half * 2 ^ swizzle) << 4), code1 = code_at + (((half * 2 + 1) ^ swizzle) << 4);
+    int at = 0, s = 0;
     uint32_t phase = 0, a_phase = 1;
-    for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++items) {
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
       TileItem it;
       item_of(i, &at, &it);
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
         wait_stage(full + s, phase, a.status);
-        char* st = smem + s * Sm::kStage;
-        const uint32_t codes = smem_u32(st + Sm::kCodes) + (t * kTileRows + row) * 64;
-        uint4 w[4];
+        const char* st = smem + s * sm.stage;
+        const uint4 w[2] = {lds128(code0 + s * sm.stage), lds128(code1 + s * sm.stage)};
+        uint32_t sc[2], zr[2];  // of each 32 columns
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = lds128(codes + ((c ^ swizzle) << 4));
-        uint32_t sc[kG], zr[kG];
-#pragma unroll
-        for (int q = 0; q < kG; ++q) {
-          sc[q] = reinterpret_cast<const uint16_t*>(st + Sm::kScales)[scale_at + q * 8];
-          zr[q] = Z ? reinterpret_cast<const uint8_t*>(st + Sm::kZeros)[scale_at + q * 8] : 8u;
+        for (int c = 0; c < 2; ++c) {
+          const int q = (half * 2 + c) * 32 / G;
+          sc[c] = reinterpret_cast<const uint16_t*>(st + sm.scales)[scale_at + q * 8];
+          zr[c] = Z ? reinterpret_cast<const uint8_t*>(st + sm.zeros)[scale_at + q * 8] : 8u;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + s);
-        wait_stage(a_free + buf, a_phase, a.status);
-        moe::tc_fence_after();
+        if (++s == sm.stages) s = 0, phase ^= 1;
+        uint32_t r[32];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t r[32];
+        for (int c = 0; c < 2; ++c) {
+          // scale * 2^96 and 2^92 and -8 scale 2^-37, each twice and exact
+          const float sf = __uint_as_float(sc[c] << 16);
+          const uint32_t s1 = bf16_twice(sf * 79228162514264337593543950336.f);
+          const uint32_t s16 = bf16_twice(sf * 4951760157141521099596496896.f);
+          const uint32_t c8 = bf16_twice(sf * -5.820766091346741e-11f);
+          const uint32_t z1 = zr[c] * 0x00010001u, z16 = zr[c] * 0x00100010u;
+          const uint32_t words[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int chunk = half * 2 + c;  // 32 columns
-            const int q = chunk * 32 / G;
-            // scale * 2^96 and 2^92, -8 scale 2^-37, each twice: the exponent
-            // field of a bf16 is bits 7 to 14; a scale of 0 stays 0
-            const float sf = __uint_as_float(sc[q] << 16);
-            const uint32_t s1 = bf16_twice(sf * 79228162514264337593543950336.f), s16 = bf16_twice(sf * 4951760157141521099596496896.f);
-            const uint32_t c8 = bf16_twice(sf * -5.820766091346741e-11f);
-            const uint32_t z1 = zr[q] * 0x00010001u, z16 = zr[q] * 0x00100010u;
-            const uint4 v = w[chunk];
-            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t u = words[k], u8 = u >> 8;
-              uint32_t* o = r + c * 16 + k * 4;
-              if (Z) {
-                o[0] = mul2(sub2(u & 0x000f000fu, z1), s1);
-                o[1] = mul2(sub2(u & 0x00f000f0u, z16), s16);
-                o[2] = mul2(sub2(u8 & 0x000f000fu, z1), s1);
-                o[3] = mul2(sub2(u8 & 0x00f000f0u, z16), s16);
-              } else {
-                o[0] = fma2(u & 0x000f000fu, s1, c8);
-                o[1] = fma2(u & 0x00f000f0u, s16, c8);
-                o[2] = fma2(u8 & 0x000f000fu, s1, c8);
-                o[3] = fma2(u8 & 0x00f000f0u, s16, c8);
-              }
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t u = words[k], u8 = u >> 8;
+            uint32_t* o = r + c * 16 + k * 4;
+            if (Z) {
+              o[0] = mul2v(sub2(u & 0x000f000fu, z1), s1);
+              o[1] = mul2v(sub2(u & 0x00f000f0u, z16), s16);
+              o[2] = mul2v(sub2(u8 & 0x000f000fu, z1), s1);
+              o[3] = mul2v(sub2(u8 & 0x00f000f0u, z16), s16);
+            } else {
+              o[0] = fma2v(u & 0x000f000fu, s1, c8);
+              o[1] = fma2v(u & 0x00f000f0u, s16, c8);
+              o[2] = fma2v(u8 & 0x000f000fu, s1, c8);
+              o[3] = fma2v(u8 & 0x00f000f0u, s16, c8);
             }
           }
-          tmem_st32(lane_at + kAColumn + (t * 2 + buf) * 64 + half * 32, r);
         }
+        // everything but the stores comes before the wait for the last block's MMAs
+        wait_stage(a_free + t * 2 + half, a_phase, a.status);
+        a_phase ^= 1;
+        moe::tc_fence_after();
+        tmem_st32(to, r);
         tmem_st_wait();
         moe::tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(a_full + buf);
-        if (++s == kTileStages) s = 0, phase ^= 1;
-        buf ^= 1;
-        if (buf == 0) a_phase ^= 1;
+        if (lane == 0) mbar_arrive(a_full + t * 2 + half);
       }
-      wait_stage(d_full, items & 1, a.status);
+    }
+  } else {  // ------------------------------------------------ the sums' way out
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const size_t slots = (size_t)a.T * (a.k + a.S);
+    int at = 0, items = 0;
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++items) {
+      TileItem it;
+      item_of(i, &at, &it);
+      const int set = items & 1;
+      wait_stage(d_full + set, items >> 1 & 1, a.status);
       moe::tc_fence_after();
-      if constexpr (!DOWN) {
-        // the warpgroups share the item's tokens, 16 at a time in turn
-        for (int c0 = t * 16; c0 < it.rows; c0 += 32) {
-          float g[16], u[16];
-          moe::tmem_ld2x16(lane_at + c0, lane_at + kTileTokens + c0, g, u);
-          const int col = it.tile * kTileRows + row;
+      const uint32_t from = lane_at + set * 2 * kTileTokens;
+      const int col = it.tile * tile_rows + row;
+      for (int c0 = 0; c0 < it.rows; c0 += 16) {
+        float g[16], u[16];  // gate and up, or rows and rows + 128
+        moe::tmem_ld2x16(from + c0, from + kTileTokens + c0, g, u);
+        const int n = min(16, it.rows - c0);
+        if constexpr (!DOWN) {
           __nv_bfloat16* h = a.h + (size_t)(it.first + c0) * a.f + h_place(col);
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            if (c0 + c >= it.rows) break;
             const float z = g[c] * kTileUnscale;
-            h[(size_t)c * a.f] = __float2bfloat16(z / (1.f + expf(-z)) * (u[c] * kTileUnscale));
+            if (c < n) h[(size_t)c * a.f] = __float2bfloat16(__fdividef(z, 1.f + __expf(-z)) * (u[c] * kTileUnscale));
           }
-        }
-      } else {
-        const int col = it.tile * tile_rows + in_tile;
-        const size_t slots = (size_t)a.T * (a.k + a.S);
-        for (int c0 = 0; c0 < it.rows; c0 += 16) {
-          float y[16];
-          moe::tmem_ld16(lane_at + t * kTileTokens + c0, y);
+        } else {
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            if (c0 + c >= it.rows) break;
-            const size_t slot = it.split * slots + __ldg(a.list_slot + it.first + c0 + c);
-            if (col < a.d) a.y[slot * a.d + col] = y[c] * kTileUnscale;
+            if (c >= n) break;
+            float* y = a.y + (it.split * slots + __ldg(a.list_slot + it.first + c0 + c)) * a.d + col;
+            y[0] = g[c] * kTileUnscale;
+            if (col + kTileRows < a.d) y[kTileRows] = u[c] * kTileUnscale;
           }
         }
       }
       moe::tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(d_free);
+      if (lane == 0) mbar_arrive(d_free + set);
     }
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 0) {
     moe::tc_fence_after();
     moe::tmem_dealloc<1>(tmem, 512);
   }
