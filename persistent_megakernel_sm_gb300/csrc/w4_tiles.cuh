@@ -2,19 +2,20 @@
 // the products on the fifth-generation tensor cores (part of w4.cu).
 //
 // An item is 256 weight rows of one expert (gate/up: 128 of each, down: 256)
-// times up to 96 of its token rows.  Codes come in by TMA; sixteen warps, a
-// warpgroup for each 64 columns of a block of 128 and each 128 rows, turn them
-// into bf16 numbers and store them as an MMA operand in tensor memory (lane =
-// weight row), and a warp for each 128 rows issues the MMAs: A from tensor
-// memory, the tokens from shared memory, fp32 sums in tensor memory over all of
-// K.  Two sets of sums, so that a further warpgroup takes an item's sums out
-// while the next item's come in.  As many stages as fit (8 for 32 tokens an
-// item, 5 for 96) cover a stage's way from its loads' start to its MMAs' end.
+// times up to 128 of its token rows.  Codes come in by TMA; eight warps, a
+// warpgroup for each 128 rows, turn them into bf16 numbers, 64 columns at a
+// time, and store them as an MMA operand in tensor memory (lane = weight row);
+// a warp for each 128 rows issues the MMAs: A from tensor memory, the tokens
+// from shared memory, fp32 sums in tensor memory over all of K; eight warps
+// take an item's sums out.  Operands have four buffers of 64 columns for each
+// 128 rows; with up to 64 tokens an item there is room for two sets of sums, so
+// that one is taken out while the other comes in.  As many stages as fit (8 for
+// 32 tokens an item, 4 for 128) cover a stage's way from its loads' start to
+// its MMAs' end.
 //
-// An MMA of 128 x 16 by 16 to 96 tokens takes 30 to 60 cycles to issue from one
-// warp whatever its width, so 16 of them and their commits, on two warps, bound
-// a block of 16 KB of codes at some 600 cycles; its loads take 690 at the whole
-// device's bandwidth.
+// What bounds it is the way from warp to warp: a look at a barrier takes 100 to
+// 200 cycles even when it is ready, an MMA of any width 30 to 60 to issue.  So
+// the loops look one step ahead and convert before they wait.
 //
 // A code q as an operand: the bits n = q (or 16 q, for every other pair) of the
 // word are the bf16 number n 2^-133, and one bf16 fused multiply-add with
@@ -30,15 +31,16 @@
 // rows) share them.
 #pragma once
 
-constexpr int kTileTokens = 96;      // at most
+constexpr int kTileTokens = 128;     // at most
 constexpr int kTileRows = 128;       // of one MMA; two of them share the tokens
 constexpr int kTileStages = 8;       // at most
-constexpr int kConvertWarps = 16;
+constexpr int kConvertWarps = 8;
 constexpr int kFirstConvert = 4;     // warps 0 and 3 load, 1 and 2 issue the MMAs
-constexpr int kFirstOut = kFirstConvert + kConvertWarps;  // four warps take the sums out
-constexpr int kTileThreads = (kFirstOut + 4) * 32;
-// tensor memory: sums [set][tile][96 columns], operands [tile][half][32 columns]
-constexpr uint32_t kAColumn = 4 * kTileTokens;
+constexpr int kFirstOut = kFirstConvert + kConvertWarps;  // eight warps take the sums out
+constexpr int kOutWarps = 8;
+constexpr int kTileThreads = (kFirstOut + kOutWarps) * 32;
+// tensor memory: sums [set][tile], operands [tile][buffer][half][32 columns]
+constexpr uint32_t kAColumn = 256;
 constexpr float kTileUnscale = 137438953472.f;  // 2^37
 
 // x gathered by expert, and h: [T k + T S, columns], columns of each 8 in the
@@ -55,7 +57,7 @@ struct TileSmem {
   int half, codes, scales, zeros, stage, stages, bars, bytes;
 };
 
-constexpr int kTileBars = 3 * 64 + 64;  // full, empty; operands and sums
+constexpr int kTileBars = 4 * 64 + 64;  // full, empty, operands stored and read; sums
 constexpr int kTileTail = kTileBars + (kMaxE + 2) * 4 + (int)sizeof(List);
 
 __host__ __device__ constexpr TileSmem tile_smem(int tokens, int group, bool zeros) {
@@ -184,10 +186,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   char* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + sm.bars);  // a stage's loads, the weights' and the tokens'
   uint64_t* empty = full + kTileStages;                            // 16 warps and the MMAs are done with it
-  uint64_t* a_full = empty + kTileStages;                          // [tile][half] the operand is stored (4 warps)
-  uint64_t* a_free = a_full + 4;                                   // [tile][half] read by the MMAs
-  uint64_t* d_full = a_free + 4;                                   // [set] an item's sums, both tiles'
-  uint64_t* d_free = d_full + 2;                                   // [set] read by 4 warps
+  uint64_t* a_full = empty + kTileStages;                          // [tile][buffer][half] the operand is stored (4 warps)
+  uint64_t* a_free = a_full + 8;                                   // [tile][buffer][half] read by the MMAs
+  uint64_t* d_full = a_free + 8;                                   // [set] an item's sums, both tiles'
+  uint64_t* d_free = d_full + 2;                                   // [set] read by 8 warps
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(d_free + 2);
   int* item_start = reinterpret_cast<int*>(smem + sm.bars + kTileBars);
   List* list = reinterpret_cast<List*>(item_start + kMaxE + 2);
@@ -198,19 +200,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int row_tiles = (rows_of + tile_rows - 1) / tile_rows;
   const int splits = DOWN ? a.splits : 1;
   const int blocks_k = K / kBlockK;
+  const int sets = most <= 64 ? 2 : 1, sum_columns = sets == 2 ? 64 : 128;
 
   if (tid == 0) {
     for (int s = 0; s < sm.stages; ++s) {
       mbar_init(full + s, 2);
       mbar_init(empty + s, kConvertWarps + 2);
     }
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < 8; ++b) {
       mbar_init(a_full + b, 4);
       mbar_init(a_free + b, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(d_full + b, 2);
-      mbar_init(d_free + b, 4);
+      mbar_init(d_free + b, kOutWarps);
     }
     moe::fence_mbar_init();
   }
@@ -309,57 +312,58 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int t = __shfl_sync(0xffffffffu, warp, 0) - 1;
     const uint32_t smem0 = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t full0 = smem0 + sm.bars, a_free0 = full0 + (2 * kTileStages + 4 + t * 2) * 8;
+    const uint32_t full0 = smem0 + sm.bars, a_free0 = full0 + (2 * kTileStages + 8 + t * 4) * 8;
     const uint64_t half = sm.half >> 4;
-    const uint32_t from = tm + kAColumn + t * 64;
-    int at = 0, s = 0, items = 0;
-    uint32_t phase = 0, a_phase = 0;
+    int at = 0, s = 0, buf = 0, set = 0;
+    uint32_t phase = 0, a_phase = 0, d_phase = 1;
     bool full_ready = false, a_ready = false;
-    for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++items) {
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
       TileItem it;
       item_of(i, &at, &it);
       const uint32_t idesc = moe::idesc_bf16(kTileRows, max(16, (__shfl_sync(0xffffffffu, it.rows, 0) + 15) & ~15));
       const int blocks = __shfl_sync(0xffffffffu, it.kb1 - it.kb0, 0);
-      const int set = items & 1;
-      const uint32_t d = tm + (set * 2 + t) * kTileTokens;
-      wait_stage(d_free + set, (items >> 1 & 1) ^ 1, a.status);
+      const uint32_t d = tm + (set * 2 + t) * sum_columns;
+      wait_stage(d_free + set, d_phase, a.status);
       moe::tc_fence_after();
       for (int kb = 0; kb < blocks; ++kb) {
         const uint64_t b = moe::sw128_desc(smem0 + s * sm.stage);
+        const uint32_t from = tm + kAColumn + (t * 2 + buf) * 64;
+        const uint32_t done = full0 + (kTileStages + s) * 8, read = a_free0 + buf * 16;
+        uint64_t* const a_bar = a_full + (t * 2 + buf) * 2;
         if (!full_ready) wait_stage(full + s, phase, a.status);
-        if (!a_ready) wait_stage(a_full + t * 2, a_phase, a.status);
+        if (!a_ready) wait_stage(a_bar, a_phase, a.status);
         moe::tc_fence_after();
-        a_ready = mbar_test(a_full + t * 2 + 1, a_phase);
+        a_ready = mbar_test(a_bar + 1, a_phase);
         if (elect_one()) {
           mma_tmem_a(d, from, b, idesc, kb > 0);
 #pragma unroll
           for (int j = 1; j < 4; ++j) mma_tmem_a(d, from + j * 8, b + j * 2, idesc, true);
-          commit(a_free0);
+          commit(read);
         }
         __syncwarp();
-        if (!a_ready) wait_stage(a_full + t * 2 + 1, a_phase, a.status);
+        if (!a_ready) wait_stage(a_bar + 1, a_phase, a.status);
         moe::tc_fence_after();
-        const uint32_t done = full0 + (kTileStages + s) * 8;
         if (++s == sm.stages) s = 0, phase ^= 1;
-        a_phase ^= 1;
+        buf ^= 1;
+        if (buf == 0) a_phase ^= 1;
         full_ready = mbar_test(full + s, phase);
-        a_ready = mbar_test(a_full + t * 2, a_phase);
+        a_ready = mbar_test(a_full + (t * 2 + buf) * 2, a_phase);
         if (elect_one()) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) mma_tmem_a(d, from + 32 + j * 8, b + half + j * 2, idesc, true);
-          commit(a_free0 + 8);
+          commit(read + 8);
           commit(done);
         }
         __syncwarp();
       }
-      if (elect_one()) commit(full0 + (2 * kTileStages + 8 + set) * 8);  // d_full
+      if (elect_one()) commit(full0 + (2 * kTileStages + 16 + set) * 8);  // d_full
       __syncwarp();
+      if (++set == sets) set = 0, d_phase ^= 1;
     }
   } else if (warp < kFirstOut) {  // ------------------------------- conversion
-    // the tile, the half of a block's columns, the row = the tensor memory's lane
-    const int group = (warp - kFirstConvert) >> 2, t = group & 1, half = group >> 1;
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kAColumn + (t * 2 + half) * 32;
+    // the tile, and the row = the tensor memory's lane
+    const int t = (warp - kFirstConvert) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kAColumn + t * 128;
     // where this row's scales are in a stage: block, then [8 lanes][groups][8 rows]
     const int in_tile = DOWN ? t * kTileRows + row : row;  // of the item's rows of one matrix
     const int in_block = in_tile % (DOWN ? 64 : 32);
@@ -367,80 +371,91 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         in_tile / (DOWN ? 64 : 32) * kRows * kG + (in_block & 7) * kG * 8 + (in_block >> 3) + (DOWN ? 0 : t * 4);
     const int swizzle = row >> 1 & 3;
     const uint32_t code_at = smem_u32(smem) + sm.codes + (t * kTileRows + row) * 64;
-    const uint32_t code0 = code_at + ((half * 2 ^ swizzle) << 4), code1 = code_at + (((half * 2 + 1) ^ swizzle) << 4);
-    int at = 0, s = 0;
+    int at = 0, s = 0, buf = 0;
     uint32_t phase = 0, a_phase = 1;
+    bool full_ready = false;
     for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
       TileItem it;
       item_of(i, &at, &it);
       for (int kb = it.kb0; kb < it.kb1; ++kb) {
-        wait_stage(full + s, phase, a.status);
+        if (!full_ready) wait_stage(full + s, phase, a.status);
         const char* st = smem + s * sm.stage;
-        const uint4 w[2] = {lds128(code0 + s * sm.stage), lds128(code1 + s * sm.stage)};
-        uint32_t sc[2], zr[2];  // of each 32 columns
+        uint4 w[4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int q = (half * 2 + c) * 32 / G;
-          sc[c] = reinterpret_cast<const uint16_t*>(st + sm.scales)[scale_at + q * 8];
-          zr[c] = Z ? reinterpret_cast<const uint8_t*>(st + sm.zeros)[scale_at + q * 8] : 8u;
+        for (int c = 0; c < 4; ++c) w[c] = lds128(code_at + s * sm.stage + ((c ^ swizzle) << 4));
+        uint32_t sc[kG], zr[kG];
+#pragma unroll
+        for (int q = 0; q < kG; ++q) {
+          sc[q] = reinterpret_cast<const uint16_t*>(st + sm.scales)[scale_at + q * 8];
+          zr[q] = Z ? reinterpret_cast<const uint8_t*>(st + sm.zeros)[scale_at + q * 8] : 8u;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(empty + s);
         if (++s == sm.stages) s = 0, phase ^= 1;
-        uint32_t r[32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          // scale * 2^96 and 2^92 and -8 scale 2^-37, each twice and exact
-          const float sf = __uint_as_float(sc[c] << 16);
-          const uint32_t s1 = bf16_twice(sf * 79228162514264337593543950336.f);
-          const uint32_t s16 = bf16_twice(sf * 4951760157141521099596496896.f);
-          const uint32_t c8 = bf16_twice(sf * -5.820766091346741e-11f);
-          const uint32_t z1 = zr[c] * 0x00010001u, z16 = zr[c] * 0x00100010u;
-          const uint32_t words[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        for (int half = 0; half < 2; ++half) {
+          const int at_buf = (t * 2 + buf) * 2 + half;
+          const bool a_ready = mbar_test(a_free + at_buf, a_phase);
+          if (half == 1) full_ready = mbar_test(full + s, phase);
+          uint32_t r[32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t u = words[k], u8 = u >> 8;
-            uint32_t* o = r + c * 16 + k * 4;
-            if (Z) {
-              o[0] = mul2v(sub2(u & 0x000f000fu, z1), s1);
-              o[1] = mul2v(sub2(u & 0x00f000f0u, z16), s16);
-              o[2] = mul2v(sub2(u8 & 0x000f000fu, z1), s1);
-              o[3] = mul2v(sub2(u8 & 0x00f000f0u, z16), s16);
-            } else {
-              o[0] = fma2v(u & 0x000f000fu, s1, c8);
-              o[1] = fma2v(u & 0x00f000f0u, s16, c8);
-              o[2] = fma2v(u8 & 0x000f000fu, s1, c8);
-              o[3] = fma2v(u8 & 0x00f000f0u, s16, c8);
+          for (int c = 0; c < 2; ++c) {
+            const int q = (half * 2 + c) * 32 / G;
+            // scale * 2^96 and 2^92 and -8 scale 2^-37, each twice and exact
+            const float sf = __uint_as_float(sc[q] << 16);
+            const uint32_t s1 = bf16_twice(sf * 79228162514264337593543950336.f);
+            const uint32_t s16 = bf16_twice(sf * 4951760157141521099596496896.f);
+            const uint32_t c8 = bf16_twice(sf * -5.820766091346741e-11f);
+            const uint32_t z1 = zr[q] * 0x00010001u, z16 = zr[q] * 0x00100010u;
+            const uint4 v = w[half * 2 + c];
+            const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t u = words[k], u8 = u >> 8;
+              uint32_t* o = r + c * 16 + k * 4;
+              if (Z) {
+                o[0] = mul2v(sub2(u & 0x000f000fu, z1), s1);
+                o[1] = mul2v(sub2(u & 0x00f000f0u, z16), s16);
+                o[2] = mul2v(sub2(u8 & 0x000f000fu, z1), s1);
+                o[3] = mul2v(sub2(u8 & 0x00f000f0u, z16), s16);
+              } else {
+                o[0] = fma2v(u & 0x000f000fu, s1, c8);
+                o[1] = fma2v(u & 0x00f000f0u, s16, c8);
+                o[2] = fma2v(u8 & 0x000f000fu, s1, c8);
+                o[3] = fma2v(u8 & 0x00f000f0u, s16, c8);
+              }
             }
           }
+          // everything but the stores comes before the wait for the MMAs of two
+          // blocks ago
+          if (!a_ready) wait_stage(a_free + at_buf, a_phase, a.status);
+          moe::tc_fence_after();
+          tmem_st32(to + buf * 64 + half * 32, r);
+          tmem_st_wait();
+          moe::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(a_full + at_buf);
         }
-        // everything but the stores comes before the wait for the last block's MMAs
-        wait_stage(a_free + t * 2 + half, a_phase, a.status);
-        a_phase ^= 1;
-        moe::tc_fence_after();
-        tmem_st32(to, r);
-        tmem_st_wait();
-        moe::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(a_full + t * 2 + half);
+        buf ^= 1;
+        if (buf == 0) a_phase ^= 1;
       }
     }
   } else {  // ------------------------------------------------ the sums' way out
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const size_t slots = (size_t)a.T * (a.k + a.S);
-    int at = 0, items = 0;
-    for (int i = blockIdx.x; i < n_items; i += gridDim.x, ++items) {
+    int at = 0, set = 0;
+    uint32_t d_phase = 0;
+    for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
       TileItem it;
       item_of(i, &at, &it);
-      const int set = items & 1;
-      wait_stage(d_full + set, items >> 1 & 1, a.status);
+      wait_stage(d_full + set, d_phase, a.status);
       moe::tc_fence_after();
-      const uint32_t from = lane_at + set * 2 * kTileTokens;
+      const uint32_t from = lane_at + set * 2 * sum_columns;
       const int col = it.tile * tile_rows + row;
-      for (int c0 = 0; c0 < it.rows; c0 += 16) {
+      for (int c0 = (warp - kFirstOut) / 4 * 16; c0 < it.rows; c0 += 32) {  // two warps to a row, in turn
         float g[16], u[16];  // gate and up, or rows and rows + 128
-        moe::tmem_ld2x16(from + c0, from + kTileTokens + c0, g, u);
+        moe::tmem_ld2x16(from + c0, from + sum_columns + c0, g, u);
         const int n = min(16, it.rows - c0);
         if constexpr (!DOWN) {
           __nv_bfloat16* h = a.h + (size_t)(it.first + c0) * a.f + h_place(col);
@@ -462,6 +477,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       moe::tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(d_free + set);
+      if (++set == sets) set = 0, d_phase ^= 1;
     }
   }
   __syncthreads();
