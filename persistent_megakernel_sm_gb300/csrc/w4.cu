@@ -35,49 +35,93 @@ struct Weight {
 
 // ------------------------------------------------------------------ conversion
 
-// One warp lane holds 8 consecutive weights; the G / 8 lanes of a group share
-// its range by shuffles.
+// Both directions are bound by their bytes, 2.5 a weight and way: a lane takes
+// 8 consecutive weights (16 bytes), four such a pass, all loads first.
+constexpr int kConvertUnroll = 4;
+
+__device__ __forceinline__ float bf16_low(uint32_t pair) { return __uint_as_float(pair << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
+
+// The 8 codes of a lane's weights by the definition: divisions.
+__device__ __noinline__ uint32_t codes_by_division(uint4 q, float div, float z) {
+  const uint32_t p[4] = {q.x, q.y, q.z, q.w};
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float v = j & 1 ? bf16_high(p[j >> 1]) : bf16_low(p[j >> 1]);
+    word |= (uint32_t)fminf(fmaxf(rintf(v / div) + z, 0.f), 15.f) << (4 * j);
+  }
+  return word;
+}
+
+// The G / 8 lanes of a group share its range by shuffles.  A code is the
+// quotient v / s rounded half to even, but a division a weight would bound the
+// kernel: instead r = round(v * (1 / s)), by adding 1.5 2^23, whose error can
+// matter only where v / s is within a few fp32 steps of halfway between two
+// integers.  There |v - r s|, which is exact (r s has at most 12 bits), is at
+// least s / 2, and the lane divides.  Scales that are zero, subnormal or not
+// finite take that way too.
 template <int G, bool Z>
 __global__ void __launch_bounds__(256)
     w4_quantize(long long n8, const uint4* __restrict__ w, uint32_t* __restrict__ codes,
                 __nv_bfloat16* __restrict__ scales, uint8_t* __restrict__ zeros) {
   constexpr int kLanes = G / 8;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n8; i += (long long)gridDim.x * 256) {
-    // n8 is a multiple of kLanes, so the lanes of a group are here together
-    const unsigned mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
-    union {
-      uint4 q;
-      __nv_bfloat16 b[8];
-    } u;
-    u.q = w[i];
-    float v[8], lo = 0.f, hi = 0.f;
-    bool finite = true;
+  const unsigned mask = (kLanes == 32 ? 0xffffffffu : (1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
+  const long long i0 = (long long)blockIdx.x * (256 * kConvertUnroll) + threadIdx.x;
+  uint4 q[kConvertUnroll];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = __bfloat162float(u.b[j]);
-      finite &= fabsf(v[j]) < INFINITY;
-      lo = fminf(lo, v[j]);
-      hi = fmaxf(hi, v[j]);
+  for (int n = 0; n < kConvertUnroll; ++n)
+    if (i0 + n * 256 < n8) q[n] = __ldcs(w + i0 + n * 256);
+#pragma unroll
+  for (int n = 0; n < kConvertUnroll; ++n) {
+    const long long i = i0 + n * 256;
+    if (i >= n8) break;  // n8 is a multiple of kLanes: the lanes of a group go together
+    const uint32_t p[4] = {q[n].x, q[n].y, q[n].z, q[n].w};
+    // the largest magnitude as bits, from 7f80 on not finite, and for zero
+    // points the range
+    uint32_t top = 0;
+    float lo = 0.f, hi = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      top = __vmaxu2(top, p[j] & 0x7fff7fffu);
+      if (Z) {
+        lo = fminf(lo, fminf(bf16_low(p[j]), bf16_high(p[j])));
+        hi = fmaxf(hi, fmaxf(bf16_low(p[j]), bf16_high(p[j])));
+      }
     }
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
-      finite &= __shfl_xor_sync(mask, (int)finite, o) != 0;
+      top = __vmaxu2(top, __shfl_xor_sync(mask, top, o));
+      if (Z) {
+        lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
+      }
     }
+    top = max(top >> 16, top & 0xffffu);
+    const bool finite = top < 0x7f80u;
     // (hi - lo) / 15, halved first so that no range overflows
-    const float range = Z ? (hi * 0.5f - lo * 0.5f) / 7.5f : fmaxf(hi, -lo) / 7.f;
+    const float range = Z ? (hi * 0.5f - lo * 0.5f) / 7.5f : __uint_as_float(top << 16) / 7.f;
     const __nv_bfloat16 sb = __float2bfloat16(finite ? range : __uint_as_float(0x7fffffffu));
     const float s = __bfloat162float(sb);
     const float div = s == 0.f || !finite ? 1.f : s;
     const float z = !finite ? 8.f : Z ? fminf(fmaxf(rintf(-lo / div), 0.f), 15.f) : 8.f;
+    const bool plain = finite && s >= 1.17549435e-38f;
+    const float inv = plain ? 1.f / s : 0.f, half = 0.5f * s;
+    const float magic = 12582912.f + z;
+    bool near = false;
     uint32_t word = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float q = fminf(fmaxf(rintf((finite ? v[j] : 0.f) / div) + z, 0.f), 15.f);
-      word |= (uint32_t)q << (4 * j);
+    for (int j = 7; j >= 0; --j) {
+      const float v = j & 1 ? bf16_high(p[j >> 1]) : bf16_low(p[j >> 1]);
+      const float t = fmaf(v, inv, magic);
+      near |= fabsf(fmaf(magic - t, s, v)) >= half;
+      uint32_t c = __float_as_uint(t) & 31u;  // magic's low bits are zero
+      if (Z) c = min(c, 15u);                 // hi / s and -lo / s may both be rounded up
+      word = word << 4 | c;
     }
-    codes[i] = word;
+    if (!finite) word = 0x88888888u;
+    else if (near || !plain) word = codes_by_division(q[n], div, z);
+    __stcs(codes + i, word);
     if (i % kLanes == 0) {
       scales[i / kLanes] = sb;
       if (Z) zeros[i / kLanes] = (uint8_t)z;
@@ -85,22 +129,38 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// A code as bf16: 128 + code sits in the mantissa of a number of that binade;
+// less 128 + zero exactly; times the scale, the one rounding.
 template <int G, bool Z>
 __global__ void __launch_bounds__(256)
     w4_dequantize(long long n8, const uint32_t* __restrict__ codes,
                   const __nv_bfloat16* __restrict__ scales, const uint8_t* __restrict__ zeros,
                   uint4* __restrict__ w) {
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n8; i += (long long)gridDim.x * 256) {
-    const uint32_t word = codes[i];
-    const float s = __bfloat162float(scales[i / (G / 8)]);
-    const float z = Z ? (float)zeros[i / (G / 8)] : 8.f;
-    union {
-      uint4 q;
-      __nv_bfloat16 b[8];
-    } u;
+  const long long i0 = (long long)blockIdx.x * (256 * kConvertUnroll) + threadIdx.x;
+  uint32_t word[kConvertUnroll], s2[kConvertUnroll], z2[kConvertUnroll];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u.b[j] = __float2bfloat16(((float)(word >> (4 * j) & 15u) - z) * s);
-    w[i] = u.q;
+  for (int n = 0; n < kConvertUnroll; ++n) {
+    const long long i = i0 + n * 256;
+    if (i >= n8) break;
+    word[n] = __ldcs(codes + i);
+    s2[n] = __bfloat16_as_ushort(__ldg(scales + i / (G / 8)));
+    z2[n] = Z ? __ldg(zeros + i / (G / 8)) : 8u;
+  }
+#pragma unroll
+  for (int n = 0; n < kConvertUnroll; ++n) {
+    const long long i = i0 + n * 256;
+    if (i >= n8) break;
+    const uint32_t s = s2[n] * 0x00010001u, base = 0x43004300u + z2[n] * 0x00010001u;
+    uint32_t v[4];  // columns (j, j + 4)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = ((word[n] >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+      asm("{\n\t.reg .b32 t;\n\tsub.rn.bf16x2 t, %1, %2;\n\tmul.rn.bf16x2 %0, t, %3;\n\t}"
+          : "=r"(v[j])
+          : "r"(u), "r"(base), "r"(s));
+    }
+    __stcs(w + i, make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                             __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632)));
   }
 }
 
@@ -140,7 +200,11 @@ constexpr int kItemWarps = 8;
 constexpr int kBlocksSm = 2;
 constexpr int kSms = 152;
 constexpr int kInline = 32;           // slots up to which every block lists the experts' rows itself
-constexpr int kTileMinRows = 12;      // mean token rows of an expert from which the tile kernels run
+// Mean token rows of an expert from which the tile kernels run: on 128 experts
+// of 2048 x 768, 94 us (small) against 96 at 6 rows, 110 against 97 at 7; on 8 of
+// 4096 x 14336, 156 against 156 at 5 and 172 against 157 at 6; on 64 of 4096 x
+// 1408, 136 against 137 at 6 and 163 against 138 at 7.5.
+constexpr int kTileMinRows = 6;
 constexpr int kMaxSplit = 16;         // K splits of the down product
 constexpr uint32_t kScaleX = 0x5f805f80u, kScaleX16 = 0x5d805d80u;  // 2^64, 2^60 twice
 constexpr float kUnscale = 5.9029581035870565e20f;                  // 2^69
@@ -806,6 +870,7 @@ int check_matrix(long long rows, int cols, int group, const void* codes, const v
   if (rows < 0 || cols < 0 || cols % group != 0)
     return moe::set_error(MOE_E_INVAL, "cols must be a multiple of the group, rows and cols not negative");
   if (rows == 0 || cols == 0) return MOE_OK;
+  if (rows > (1ll << 40) / cols) return moe::set_error(MOE_E_INVAL, "more than 2^40 weights");
   if (!codes || !scales || !w) return moe::set_error(MOE_E_INVAL, "null tensor pointer");
   if (!aligned(codes, 16) || !aligned(w, 16) || !aligned(scales, 2))
     return moe::set_error(MOE_E_INVAL, "weights and codes must be 16-byte aligned, scales 2-byte");
@@ -821,7 +886,10 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t s,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-dim3 convert_grid(long long n8) { return dim3((unsigned)std::min<long long>((n8 + 255) / 256, 152 * 8)); }
+dim3 convert_grid(long long n8) {
+  constexpr int per = 256 * kConvertUnroll;
+  return dim3((unsigned)((n8 + per - 1) / per));
+}
 
 }  // namespace
 
@@ -1142,7 +1210,7 @@ int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weig
   for (int d = 0; d < 2 && e == cudaSuccess; ++d) {
     const int row_tiles = d ? h->d / kRows : h->f / 32, blocks_k = (d ? h->f : h->d) / kBlockK;
     const long long units = (long long)(h->E + h->S) * fours(h, d) * blocks_k * 4;
-    e = launch(w4_arrange, convert_grid(units * 8 * kg), 256, s, take(d ? down : gate), take(d ? down : up), 1 - d,
+    e = launch(w4_arrange, dim3((unsigned)std::min<long long>((units * 8 * kg + 255) / 256, kSms * 8)), 256, s, take(d ? down : gate), take(d ? down : up), 1 - d,
                h->E + h->S, row_tiles, blocks_k, kg, reinterpret_cast<uint4*>(h->arranged + (d ? at.down : 0)),
                z ? reinterpret_cast<uint2*>(h->arranged + (d ? at.zeros_down : at.zeros)) : nullptr);
   }
