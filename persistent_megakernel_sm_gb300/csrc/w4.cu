@@ -54,19 +54,35 @@ __device__ __noinline__ uint32_t codes_by_division(uint4 q, float div, float z) 
   return word;
 }
 
-// The G / 8 lanes of a group share its range by shuffles.  A code is the
-// quotient v / s rounded half to even, but a division a weight would bound the
-// kernel: instead r = round(v * (1 / s)), by adding 1.5 2^23, whose error can
-// matter only where v / s is within a few fp32 steps of halfway between two
-// integers.  There |v - r s|, which is exact (r s has at most 12 bits), is at
-// least s / 2, and the lane divides.  Scales that are zero, subnormal or not
-// finite take that way too.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // NaN wins
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// v / s + magic, rounded to an integer (half to even), for magic = 1.5 2^23:
+// the sum's last bit is 1.  One correction of the quotient by
+// its remainder (Markstein) makes it exact where v / s is halfway between two
+// integers: the remainder v - q s is exact, and what is left of the
+// reciprocal's error is far below the quotient's last bit.  Where it is not
+// halfway it is at least 2^-9 s from it (v and s have 8 bits each).
+__device__ __forceinline__ float rounded_quotient(float v, float s, float inv, float magic) {
+  const float q = v * inv;
+  return fmaf(fmaf(-q, s, v), inv, q) + magic;
+}
+
+// The G / 8 lanes of a group share its range by shuffles: the largest value and
+// the largest negated one, at least 0 each, packed.  A division a weight would
+// bound the kernel; only scales that are zero, subnormal or not finite take it.
+// The scale itself: max / 7 is never near halfway between two bf16 numbers (7
+// times an odd number is odd), so a product does; (hi - lo) / 15 can be, and
+// divides.
 template <int G, bool Z>
 __global__ void __launch_bounds__(256)
     w4_quantize(long long n8, const uint4* __restrict__ w, uint32_t* __restrict__ codes,
                 __nv_bfloat16* __restrict__ scales, uint8_t* __restrict__ zeros) {
   constexpr int kLanes = G / 8;
-  const unsigned mask = (kLanes == 32 ? 0xffffffffu : (1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
+  const unsigned mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
   const long long i0 = (long long)blockIdx.x * (256 * kConvertUnroll) + threadIdx.x;
   uint4 q[kConvertUnroll];
 #pragma unroll
@@ -77,50 +93,34 @@ __global__ void __launch_bounds__(256)
     const long long i = i0 + n * 256;
     if (i >= n8) break;  // n8 is a multiple of kLanes: the lanes of a group go together
     const uint32_t p[4] = {q[n].x, q[n].y, q[n].z, q[n].w};
-    // the largest magnitude as bits, from 7f80 on not finite, and for zero
-    // points the range
-    uint32_t top = 0;
-    float lo = 0.f, hi = 0.f;
+    const uint32_t above = max2(max2(p[0], p[1]), max2(p[2], p[3]));
+    const uint32_t below = max2(max2(p[0] ^ 0x80008000u, p[1] ^ 0x80008000u), max2(p[2] ^ 0x80008000u, p[3] ^ 0x80008000u));
+    uint32_t range = max2(max2(__byte_perm(above, below, 0x5410), __byte_perm(above, below, 0x7632)), 0u);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      top = __vmaxu2(top, p[j] & 0x7fff7fffu);
-      if (Z) {
-        lo = fminf(lo, fminf(bf16_low(p[j]), bf16_high(p[j])));
-        hi = fmaxf(hi, fmaxf(bf16_low(p[j]), bf16_high(p[j])));
-      }
-    }
-#pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) {
-      top = __vmaxu2(top, __shfl_xor_sync(mask, top, o));
-      if (Z) {
-        lo = fminf(lo, __shfl_xor_sync(mask, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, o));
-      }
-    }
-    top = max(top >> 16, top & 0xffffu);
-    const bool finite = top < 0x7f80u;
-    // (hi - lo) / 15, halved first so that no range overflows
-    const float range = Z ? (hi * 0.5f - lo * 0.5f) / 7.5f : __uint_as_float(top << 16) / 7.f;
-    const __nv_bfloat16 sb = __float2bfloat16(finite ? range : __uint_as_float(0x7fffffffu));
+    for (int o = kLanes / 2; o; o >>= 1) range = max2(range, __shfl_xor_sync(mask, range, o));
+    const float hi = bf16_low(range), lo = bf16_high(range);  // lo: how far below zero
+    // (hi + lo) / 15, halved first so that no range overflows
+    const float step = Z ? (hi * 0.5f + lo * 0.5f) / 7.5f : fmaxf(hi, lo) * (1.f / 7.f);
+    const bool finite = hi + lo < INFINITY || (hi < INFINITY && lo < INFINITY);
+    const __nv_bfloat16 sb = __float2bfloat16(finite ? step : __uint_as_float(0x7fffffffu));
     const float s = __bfloat162float(sb);
-    const float div = s == 0.f || !finite ? 1.f : s;
-    const float z = !finite ? 8.f : Z ? fminf(fmaxf(rintf(-lo / div), 0.f), 15.f) : 8.f;
     const bool plain = finite && s >= 1.17549435e-38f;
-    const float inv = plain ? 1.f / s : 0.f, half = 0.5f * s;
-    const float magic = 12582912.f + z;
-    bool near = false;
+    const float inv = 1.f / s;
+    float z = 8.f;
+    if (Z) {
+      z = fminf(rounded_quotient(lo, s, inv, 12582912.f) - 12582912.f, 15.f);
+      if (!plain) z = !finite ? 8.f : fminf(rintf(lo / (s == 0.f ? 1.f : s)), 15.f);
+    }
+    const int zero = (int)z - 0x4b400000;  // less the bits of 1.5 2^23
     uint32_t word = 0;
 #pragma unroll
     for (int j = 7; j >= 0; --j) {
       const float v = j & 1 ? bf16_high(p[j >> 1]) : bf16_low(p[j >> 1]);
-      const float t = fmaf(v, inv, magic);
-      near |= fabsf(fmaf(magic - t, s, v)) >= half;
-      uint32_t c = __float_as_uint(t) & 31u;  // magic's low bits are zero
-      if (Z) c = min(c, 15u);                 // hi / s and -lo / s may both be rounded up
-      word = word << 4 | c;
+      int c = __float_as_int(rounded_quotient(v, s, inv, 12582912.f)) + zero;
+      if (Z) c = min(c, 15);  // hi / s and lo / s may both be rounded up
+      word = word * 16u + (uint32_t)c;
     }
-    if (!finite) word = 0x88888888u;
-    else if (near || !plain) word = codes_by_division(q[n], div, z);
+    if (!plain) word = finite ? codes_by_division(q[n], s == 0.f ? 1.f : s, z) : 0x88888888u;
     __stcs(codes + i, word);
     if (i % kLanes == 0) {
       scales[i / kLanes] = sb;
