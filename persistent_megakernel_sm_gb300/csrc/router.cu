@@ -42,7 +42,7 @@ constexpr int kMaxK = 16;
 constexpr int kMaxGroups = 32;
 constexpr int kWarps = 8;           // of a block
 constexpr int kVals = 8;            // experts of a lane
-constexpr int kGridCap = 152 * 8;   // blocks that fill the SMs; longer batches loop
+constexpr int kSms = 152;
 constexpr unsigned kAll = 0xffffffffu;
 
 struct Route {
@@ -452,23 +452,39 @@ int pow2_from(int n) {
 
 int lanes_of(int E) { return std::max(4, pow2_from((E + kVals - 1) / kVals)); }
 
-// How many rows a warp takes together, and blocks: with few rows one at a time
-// (or as many as the lanes hold), to spread them; with many, enough to give
-// most lanes a slot, and for the gradient never more than a lane each.
+// How many rows a warp takes together, and blocks.
 struct Shape {
   int rows, kpad, blocks;
 };
 
 Shape shape_of(const Route& r, int T, bool backward) {
-  const int at_once = 32 / lanes_of(r.E);
+  const int lanes = lanes_of(r.E), at_once = 32 / lanes;
   Shape s;
   s.kpad = pow2_from(r.k);
-  const int together = std::min(max_rows(lanes_of(r.E)), std::max(1, 32 / s.kpad));
-  s.rows = at_once;
-  if (T > 152 * kWarps * 2 * at_once) s.rows = std::max(at_once, together);
-  if (backward) s.rows = std::min(s.rows, together);
-  const long long n = ((long long)T + (long long)kWarps * s.rows - 1) / (kWarps * s.rows);
-  s.blocks = (int)std::min<long long>(n, kGridCap);
+  const int together = std::min(max_rows(lanes), std::max(1, 32 / s.kpad));
+  auto tasks_of = [&](int rows) { return ((long long)T + rows - 1) / rows; };
+  int cap;
+  if (backward) {
+    // a slot a lane is most of the work: all the rows a warp has lanes for, once
+    // there are several rows for every warp of the device (32768 rows of 256
+    // experts: 12.9 us at 4 rows a warp, 27.6 at 1)
+    s.rows = T > kSms * kWarps * 2 * at_once ? together : std::min(at_once, together);
+    cap = kSms * 8;
+  } else {
+    // three blocks an SM are resident and take rows by turns: the rows together
+    // that give the fullest warp the least to do, its slots costing about a
+    // sixth of a choice each pass (32768 rows of 64 experts: 14.5 us so, 16.5
+    // with as many blocks as there is work for)
+    cap = kSms * 3;
+    s.rows = at_once;
+    float least = INFINITY;
+    for (int rows = at_once; rows <= std::max(at_once, together); rows *= 2) {
+      const long long passes = (tasks_of(rows) + cap * kWarps - 1) / (cap * kWarps);
+      const float cost = (float)passes * ((float)rows / at_once + 0.17f);
+      if (cost < least) least = cost, s.rows = rows;
+    }
+  }
+  s.blocks = (int)std::min<long long>((tasks_of(s.rows) + kWarps - 1) / kWarps, cap);
   return s;
 }
 
