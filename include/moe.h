@@ -216,6 +216,20 @@ int moe_layer_forward(moe_layer_t* h, int T, const void* x, const void* router_w
                       const void* w_gate, const void* w_up, const void* w_down, void* out,
                       void* stream);
 
+/* The same forward pass on a routing that the caller gives, in place of the
+ * layer's own router: idx [T, k] int32 and w [T, k] fp32 (device pointers,
+ * 4-byte aligned), as moe_router_forward writes them -- sigmoid scores, groups,
+ * a balance bias, weights that are not renormalised.
+ *   out[t] = bf16( sum_j w[t,j] * y_{idx[t,j]}  +  y_shared )
+ * Each token's k experts are in [0, E) and distinct; else the pass ends in
+ * MOE_E_DEVICE (moe_layer_status) and its output is undefined.  The router bias
+ * does not enter.  Everything else (modes, options, routing readback, status)
+ * is that of moe_layer_forward; with the same routing the output has the same
+ * bits. */
+int moe_layer_forward_routed(moe_layer_t* h, int T, const void* x, const int32_t* idx,
+                             const float* w, const void* w_gate, const void* w_up,
+                             const void* w_down, void* out, void* stream);
+
 /* The forward pass with the residual add and the RMSNorm that end the MoE
  * megakernel (xxqk.cn/news/665650 section 1 lists them after the weighted
  * merge) fused into the combine.  Per token t, with layer[t] the value
@@ -335,7 +349,8 @@ void moe_layer_destroy(moe_layer_t* h);
  *
  * Routing of tokens to experts as an operator of its own, for scores, biases
  * and groups that the layer's built-in router (softmax, top-k, renormalise)
- * does not have, with its gradient for training.  Per token, with the logits
+ * does not have, with its gradient for training; moe_layer_forward_routed and
+ * moe_w4_forward take its result.  Per token, with the logits
  * l over E experts:
  *   s   = softmax(l) or sigmoid(l)                       (the scores)
  *   c   = s + bias; without a bias the order of l itself (what selects)

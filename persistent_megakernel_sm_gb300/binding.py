@@ -46,6 +46,7 @@ _SIGNATURES = {
     "moe_layer_forward_noalloc": ([_vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
     "moe_layer_forward_residual_norm": ([_vp, _i32] + [_vp] * 7 + [ctypes.c_float, _vp, _vp, _vp],
                                         _i32),
+    "moe_layer_forward_routed": ([_vp, _i32] + [_vp] * 8, _i32),
     "moe_layer_calibrate": ([_vp, _i32] + [_vp] * 6 + [_i32, _vp, _vp], _i32),
     "moe_layer_get_routing": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
     "moe_layer_status": ([_vp, _vp], _i32),
@@ -191,6 +192,22 @@ class MoELayer:
         _err(lib.moe_layer_forward(self.h, T, x.data_ptr(), router_w.data_ptr(),
                                    w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
                                    out.data_ptr(), _stream_ptr(stream)))
+        return out
+
+    def forward_routed(self, x, idx, w, w_gate, w_up, w_down, out, stream=None):
+        """moe_layer_forward_routed: the forward pass on a given routing, idx [T, k]
+        int32 and w [T, k] fp32 (MoERouter.forward's)."""
+        import torch
+        T, n = x.shape[0], self.E + self.S
+        _check_tensor("w_gate", w_gate, torch.bfloat16, (n, self.f, self.d))
+        _check_tensor("w_up", w_up, torch.bfloat16, (n, self.f, self.d))
+        _check_tensor("w_down", w_down, torch.bfloat16, (n, self.d, self.f))
+        self._check_rows(T, x=x, out=out)
+        _check_tensor("idx", idx, torch.int32, (T, self.k))
+        _check_tensor("w", w, torch.float32, (T, self.k))
+        _err(lib.moe_layer_forward_routed(self.h, T, x.data_ptr(), idx.data_ptr(), w.data_ptr(),
+                                          w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
+                                          out.data_ptr(), _stream_ptr(stream)))
         return out
 
     def forward_residual_norm(self, x, router_w, w_gate, w_up, w_down, residual, gamma, eps,

@@ -155,6 +155,9 @@ struct Params {
   const __nv_bfloat16* gamma;     // [d]
   __nv_bfloat16* norm_out;        // [T, d]
   float eps;
+  // the routing, where the caller gives it (both or none)
+  const int* idx_in;  // [T, k]
+  const float* w_in;  // [T, k]
   // routing workspace
   int* idx;          // [T, k]
   float* wgt;        // [T, k]

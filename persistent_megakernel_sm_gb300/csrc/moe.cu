@@ -1148,8 +1148,15 @@ struct Fuse {
   void* norm_out;
 };
 
+// The caller's routing, in place of the router's (or none).
+struct Given {
+  const int32_t* idx;
+  const float* w;
+};
+
 int forward_impl(moe_layer_t* h, int T, const void* x, const void* router_w, const void* w_gate,
-                 const void* w_up, const void* w_down, void* out, const Fuse* fz, void* stream) {
+                 const void* w_up, const void* w_down, void* out, const Fuse* fz, void* stream,
+                 const Given* given = nullptr) {
   if (!h) return fail(MOE_E_INVAL, "null handle");
   if (!h->ws) return fail(MOE_E_STATE, "moe_layer_reserve was not called");
   if (T < 0 || T > h->T_max) return fail(MOE_E_INVAL, "T out of range (0..T_max)");
@@ -1246,6 +1253,12 @@ int forward_impl(moe_layer_t* h, int T, const void* x, const void* router_w, con
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.wr = static_cast<const __nv_bfloat16*>(router_w);
   p.bias = h->bias;
+  if (given) {
+    p.idx_in = given->idx;
+    p.w_in = given->w;
+    p.route_ks = 1;  // nothing to split
+    p.n_route_tasks = cdiv(p.n_route, P);
+  }
   if (fz) {
     p.residual = static_cast<const __nv_bfloat16*>(fz->residual);
     p.gamma = static_cast<const __nv_bfloat16*>(fz->gamma);
@@ -1380,6 +1393,17 @@ int moe_layer_forward(moe_layer_t* h, int T, const void* x, const void* router_w
                       const void* w_gate, const void* w_up, const void* w_down, void* out,
                       void* stream) {
   return forward_impl(h, T, x, router_w, w_gate, w_up, w_down, out, nullptr, stream);
+}
+
+int moe_layer_forward_routed(moe_layer_t* h, int T, const void* x, const int32_t* idx,
+                             const float* w, const void* w_gate, const void* w_up,
+                             const void* w_down, void* out, void* stream) {
+  if (T > 0 && (!idx || !w)) return fail(MOE_E_INVAL, "null idx or w");
+  if ((reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(w)) & 3)
+    return fail(MOE_E_INVAL, "idx and w must be 4-byte aligned");
+  const Given given{idx, w};
+  // no router product: its weights' tensor map, never loaded from, is of x
+  return forward_impl(h, T, x, x, w_gate, w_up, w_down, out, nullptr, stream, &given);
 }
 
 int moe_layer_forward_residual_norm(moe_layer_t* h, int T, const void* x, const void* router_w,

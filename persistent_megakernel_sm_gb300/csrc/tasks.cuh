@@ -1681,6 +1681,46 @@ __device__ __forceinline__ void route_epilogue_k(const Params& p, Ctrl* c, int t
   else route_epilogue<16>(p, c, tile, nt, lg, ls, xch);
 }
 
+// A router tile whose routing the caller gave (moe_layer_forward_routed): the
+// tile's share of what the epilogue above leaves behind -- slots, token masks,
+// ranks and counts -- from idx_in and w_in.  A slot outside [0, E) sets no bit
+// and an expert named twice sets one, so that the plan's check of the counts
+// ends the pass in MOE_E_DEVICE.
+__device__ __noinline__ void route_given(const Params& p, Ctrl* c, int tile, int nt) {
+  const int E = p.E, k = p.k, rt = p.rt, t0 = tile * rt, m = threadIdx.x;
+  const bool valid = m < nt;
+  const size_t o = (size_t)(t0 + m) * k;
+  if (m < rt) {  // whole warps
+    for (int s = 0; s < k; ++s) {
+      int e = valid ? __ldg(p.idx_in + o + s) : -1;
+      if ((unsigned)e >= (unsigned)E) e = -1;
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      if (e >= 0 && (m & 31) == __ffs(same) - 1) c->mask[e * 4 + (m >> 5)] |= same;
+      __syncwarp();
+      if (valid) {
+        p.idx[o + s] = max(e, 0);
+        p.wgt[o + s] = __ldg(p.w_in + o + s);
+      }
+    }
+  }
+  cta_sync();
+  if (valid) {
+    const uint32_t below = (1u << (m & 31)) - 1u;
+    for (int s = 0; s < k; ++s) {
+      const int e = min((unsigned)__ldg(p.idx_in + o + s), (unsigned)(E - 1));
+      const uint32_t* mk = c->mask + e * 4;
+      int r = __popc(mk[m >> 5] & below);
+      for (int q = 0; q < m >> 5; ++q) r += __popc(mk[q]);
+      p.rank[o + s] = r;
+    }
+  }
+  for (int e = threadIdx.x; e < E; e += kThreads) {
+    const uint32_t* mk = c->mask + e * 4;
+    p.tile_cnt[(size_t)tile * E + e] = __popc(mk[0]) + __popc(mk[1]) + __popc(mk[2]) + __popc(mk[3]);
+    reinterpret_cast<uint4*>(p.rmask)[(size_t)tile * E + e] = make_uint4(mk[0], mk[1], mk[2], mk[3]);
+  }
+}
+
 // One router task: router tile P pt + r for the CTA of rank r, K split
 // `split` of p.route_ks, as one MMA of the worker: each CTA's 128 A rows are
 // its tile's tokens; for a pair the experts (N, padded to 32) are split in
@@ -1705,6 +1745,11 @@ __device__ bool route_task(const Params& p, const Maps& maps, int pt, int split,
   for (int i = threadIdx.x; i < kMaxE * 4; i += kThreads) c->mask[i] = 0u;
   for (int e = threadIdx.x; e < kMaxE; e += kThreads)
     c->bias_s[e] = (p.bias && e < p.E) ? __ldg(p.bias + e) : 0.f;
+  if (p.idx_in) {  // no product, and no GEMM task's end
+    cta_sync();
+    if (mine) route_given(p, c, tile, nt);
+    return mine;
+  }
   GemmJob job;
   job.a0 = &maps.xr;
   job.a1 = nullptr;

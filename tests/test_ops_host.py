@@ -130,6 +130,20 @@ def test_w4_calls_validate(lib):
     lib.moe_w4_destroy(None)
 
 
+def test_routed_forward_validates(lib):
+    h = lib.moe_layer_create(2048, 768, 128, 8, 0)
+    try:
+        f, ptrs = lib.moe_layer_forward_routed, [16] * 4
+        assert f(h, 1, 16, None, 16, *ptrs, None) == pkg.MOE_E_INVAL
+        assert f(h, 1, 16, 16, None, *ptrs, None) == pkg.MOE_E_INVAL
+        assert f(h, 1, 16, 18, 16, *ptrs, None) == pkg.MOE_E_INVAL
+        assert f(h, 1, 16, 16, 17, *ptrs, None) == pkg.MOE_E_INVAL
+        assert f(h, 1, 16, 16, 16, *ptrs, None) == pkg.MOE_E_STATE  # before reserve
+        assert f(None, 1, 16, 16, 16, *ptrs, None) == pkg.MOE_E_INVAL
+    finally:
+        lib.moe_layer_destroy(h)
+
+
 # ---- the binding's checks, with the library replaced by a recorder
 
 class _OnDevice(torch.Tensor):
@@ -199,6 +213,25 @@ def test_router_binding_passes_and_refuses(rec):
         binding.MoERouter(64, 6, score="tanh")
     assert rec.calls == before
     r.close()
+
+
+def test_routed_binding_passes_and_refuses(rec):
+    bf = torch.bfloat16
+    layer = binding.MoELayer(256, 384, 8, 2, 1)
+    gate, down, x = _dev(9, 384, 256, dtype=bf), _dev(9, 256, 384, dtype=bf), _dev(5, 256, dtype=bf)
+    idx, w = _dev(5, 2, dtype=torch.int32), _dev(5, 2)
+    layer.forward_routed(x, idx, w, gate, gate, down, x, stream=0)
+    assert "moe_layer_forward_routed" in rec.calls
+    before = list(rec.calls)
+    for args in ((x, idx.long(), w, gate, gate, down, x), (x, idx[:4], w, gate, gate, down, x),
+                 (x, idx, w.to(bf), gate, gate, down, x), (x, idx, w, down, gate, down, x),
+                 (x, idx, w, gate, gate, gate, x), (x.float(), idx, w, gate, gate, down, x),
+                 (x, idx, w, gate, gate, down, x[:4])):
+        with pytest.raises(binding.MoEError) as err:
+            layer.forward_routed(*args, stream=0)
+        assert err.value.code == binding.MOE_E_INVAL
+    assert rec.calls == before
+    layer.close()
 
 
 def test_w4_binding_passes_and_refuses(rec):
