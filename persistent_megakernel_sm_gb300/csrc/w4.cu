@@ -359,21 +359,44 @@ __device__ void list_few(const Experts& a, List* l, const Rows& rows) {
 }
 
 // The list of a larger batch, once for both products: one block.  Slots keep
-// their order inside an expert.
+// their order inside an expert.  1024 slots a round: what each warp's 32 have of
+// each expert, then a prefix over the warps.  More than one round counts first
+// (`before`: what the rounds before have), since an expert's first entry lies
+// behind every earlier expert's last.
 __global__ void __launch_bounds__(1024) w4_list(Experts a) {
-  __shared__ int count[kMaxE];
+  __shared__ int count[kMaxE], before[kMaxE];
   __shared__ uint16_t table[32][kMaxE];
   __shared__ List l;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.T * a.k;
+  wait_for_previous_kernel();
   let_next_kernel_start();
-  if (tid < kMaxE) count[tid] = 0;
-  __syncthreads();
-  for (int p = tid; p < ((n + 31) & ~31); p += 1024) {
-    const int e = expert_at(a, p);
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) atomicAdd(count + e, __popc(same));
-  }
-  __syncthreads();
+  const int rounds = (n + 1023) / 1024;
+  int e = -1;
+  unsigned same = 0;
+  // a round's table, and its prefix over the warps on top of `from`
+  auto tabulate = [&](int round, int* from) {
+    for (int i = tid; i < 32 * kMaxE / 2; i += 1024) reinterpret_cast<uint32_t*>(table)[i] = 0u;
+    e = expert_at(a, round * 1024 + tid);
+    same = __match_any_sync(0xffffffffu, e);
+    __syncthreads();
+    if (e >= 0 && lane == __ffs(same) - 1) table[warp][e] = (uint16_t)__popc(same);
+    __syncthreads();
+    if (tid < kMaxE) {
+      int run = from[tid];
+      const int warps = min(32, (n - round * 1024 + 31) / 32);
+#pragma unroll 8
+      for (int q = 0; q < warps; ++q) {
+        const int v = table[q][tid];
+        table[q][tid] = (uint16_t)run;
+        run += v;
+      }
+      from[tid] = run;
+    }
+    __syncthreads();
+  };
+  if (tid < kMaxE) count[tid] = before[tid] = 0;
+  for (int r = 0; r < rounds; ++r) tabulate(r, count);
+  __shared__ int start[kMaxE];
   if (tid < 32) {  // one warp: 8 experts a lane
     int c[8], sum = 0, act = 0;
 #pragma unroll
@@ -400,7 +423,7 @@ __global__ void __launch_bounds__(1024) w4_list(Experts a) {
     s0 -= sum, a0 -= act;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      count[lane * 8 + i] = s0;  // from here on the expert's next entry
+      start[lane * 8 + i] = s0;
       if (c[i] > 0) {
         l.expert[a0] = (uint16_t)(lane * 8 + i);
         l.start[a0++] = (uint16_t)s0;
@@ -408,35 +431,16 @@ __global__ void __launch_bounds__(1024) w4_list(Experts a) {
       }
     }
   }
-  // 1024 slots a round: what each warp's 32 have of each expert, then where
-  // the warp's first one goes
-  for (int p0 = 0; p0 < n; p0 += 1024) {
-    __syncthreads();
-    for (int i = tid; i < 32 * kMaxE / 2; i += 1024) reinterpret_cast<uint32_t*>(table)[i] = 0u;
-    __syncthreads();
-    const int p = p0 + tid;
-    const int e = expert_at(a, p);
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs(same) - 1) table[warp][e] = (uint16_t)__popc(same);
-    __syncthreads();
-    if (tid < kMaxE) {
-      int run = count[tid];
-#pragma unroll 8
-      for (int q = 0; q < 32; ++q) {
-        const int v = table[q][tid];
-        table[q][tid] = (uint16_t)run;
-        run += v;
-      }
-      count[tid] = run;
-    }
-    __syncthreads();
-    if (e >= 0) {
-      const int to = table[warp][e] + __popc(same & ((1u << lane) - 1u));
-      a.list_slot[to] = (uint16_t)p;
-      a.list_row[to] = (uint16_t)(p / a.k);
-    }
-  }
   __syncthreads();
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) tabulate(r, before);
+    if (e >= 0) {
+      const int to = start[e] + table[warp][e] + __popc(same & ((1u << lane) - 1u));
+      a.list_slot[to] = (uint16_t)(r * 1024 + tid);
+      a.list_row[to] = (uint16_t)((r * 1024 + tid) / a.k);
+    }
+    __syncthreads();
+  }
   if (a.S) {
     const int first = l.start[l.n_active - 1];
     for (int t = tid; t < a.T; t += 1024) {
@@ -520,15 +524,16 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
     mbar_init(reinterpret_cast<uint64_t*>(smem + Sm::kBars) + tid, 1);
     moe::fence_mbar_init();
   }
+  // gate/up is a pass's first kernel (or follows the list's): it waits for what
+  // came before the pass; down starts only after every block of it has, so that
+  // down may read the routing, or the list, at once
+  if (!DOWN) {
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+  }
   if (a.T * a.k <= kInline) {
-    if (!DOWN) let_next_kernel_start();
     list_few(a, list, rows);
   } else {
-    // down starts only after every block of gate/up has seen the list complete
-    if (!DOWN) {
-      wait_for_previous_kernel();
-      let_next_kernel_start();
-    }
     for (int i = tid; i < (int)sizeof(List) / 4; i += blockDim.x)
       reinterpret_cast<int*>(list)[i] = __ldcg(static_cast<const int*>(a.list) + i);
     rows = Rows{a.list_slot, a.list_row};
@@ -826,31 +831,49 @@ __global__ void __launch_bounds__(256)
 }
 
 // out[t] = the weighted sum of the token's slots, in slot order, each the sum
-// of its K splits, in order.
+// of its K splits, in order.  The loads of four slots and splits go out
+// together, whether the slot has an expert or not: one after the other they
+// took 13 us for one token of 8 slots.
 __global__ void __launch_bounds__(128) w4_combine(const Experts a) {
   const int t = blockIdx.y, col = (blockIdx.x * 128 + threadIdx.x) * 4;
+  const int n = a.k + a.S;
+  const size_t slots = (size_t)a.T * n;
+  let_next_kernel_start();
   wait_for_previous_kernel();
   if (col >= a.d) return;
-  const size_t slots = (size_t)a.T * (a.k + a.S);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < a.k + a.S; ++j) {
-    const int p = j < a.k ? t * a.k + j : a.T * a.k + t;
-    if (j < a.k && expert_at(a, p) < 0) continue;
-    const float wj = j < a.k ? __ldg(a.w + p) : 1.f;
-    const float* from = a.y + (size_t)p * a.d + col;
-    float4 y = __ldcg(reinterpret_cast<const float4*>(from));
+  for (int j0 = 0; j0 < n; j0 += 4) {
+    const float* from[4];
+    float wj[4];
+    bool live[4];
+    float4 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = min(j0 + i, n - 1), p = j < a.k ? t * a.k + j : a.T * a.k + t;
+      live[i] = j0 + i < n && (j >= a.k || expert_at(a, p) >= 0);
+      wj[i] = j < a.k ? __ldg(a.w + p) : 1.f;
+      from[i] = a.y + (size_t)p * a.d + col;
+      y[i] = __ldcg(reinterpret_cast<const float4*>(from[i]));
+    }
 #pragma unroll 4
     for (int q = 1; q < a.splits; ++q) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(from + q * slots * a.d));
-      y.x += v.x;
-      y.y += v.y;
-      y.z += v.z;
-      y.w += v.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(from[i] + q * slots * a.d));
+        y[i].x += v.x;
+        y[i].y += v.y;
+        y[i].z += v.z;
+        y[i].w += v.w;
+      }
     }
-    o.x += wj * y.x;
-    o.y += wj * y.y;
-    o.z += wj * y.z;
-    o.w += wj * y.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!live[i]) continue;
+      o.x += wj[i] * y[i].x;
+      o.y += wj[i] * y[i].y;
+      o.z += wj[i] * y[i].z;
+      o.w += wj[i] * y[i].w;
+    }
   }
   union {
     __nv_bfloat162 b[2];
@@ -1019,8 +1042,11 @@ Arranged arranged(const moe_w4* h) {
   return Arranged{2 * gate_up, 2 * (gate_up + down), 2 * (gate_up + down) + gate_up, 3 * (gate_up + down)};
 }
 
+// Every kernel of a pass may be launched before the one in front of it has
+// ended, and waits for it itself (wait_for_previous_kernel) before it touches
+// anything that is written on the stream; so may the first of the next pass.
 template <typename... A>
-cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, int smem, bool overlap, cudaStream_t s,
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, int smem, cudaStream_t s,
                          const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -1031,7 +1057,7 @@ cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, int smem,
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = overlap ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -1273,20 +1299,20 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   const Kernels kn = kernels(h->group, h->zeros);
   const bool listed = T * h->k > kInline;
   cudaError_t e = cudaSuccess;
-  if (listed) e = launch_after(w4_list, dim3(1), 1024, 0, false, s, a);
+  if (listed) e = launch_after(w4_list, dim3(1), 1024, 0, s, a);
   if (r.tokens) {
     const int smem = tile_smem(r.tokens, h->group, h->zeros).bytes;
     h->tile_maps.x = h->x_maps[r.tokens / 32 - 1];
     h->tile_maps.h = h->h_maps[r.tokens / 32 - 1];
-    if (e == cudaSuccess) e = launch_after(w4_gather, dim3(T * (h->k + h->S)), 128, 0, true, s, a);
-    if (e == cudaSuccess) e = launch_after(kn.tiles_gate_up, dim3(kSms), kTileThreads, smem, true, s, a, h->tile_maps);
-    if (e == cudaSuccess) e = launch_after(kn.tiles_down, dim3(kSms), kTileThreads, smem, true, s, a, h->tile_maps);
+    if (e == cudaSuccess) e = launch_after(w4_gather, dim3(T * (h->k + h->S)), 128, 0, s, a);
+    if (e == cudaSuccess) e = launch_after(kn.tiles_gate_up, dim3(kSms), kTileThreads, smem, s, a, h->tile_maps);
+    if (e == cudaSuccess) e = launch_after(kn.tiles_down, dim3(kSms), kTileThreads, smem, s, a, h->tile_maps);
   } else {
     const dim3 grid(kSms * kBlocksSm);
-    if (e == cudaSuccess) e = launch_after(kn.gate_up, grid, kItemWarps * 32, kn.smem, listed, s, a, h->maps);
-    if (e == cudaSuccess) e = launch_after(kn.down, grid, kItemWarps * 32, kn.smem, true, s, a, h->maps);
+    if (e == cudaSuccess) e = launch_after(kn.gate_up, grid, kItemWarps * 32, kn.smem, s, a, h->maps);
+    if (e == cudaSuccess) e = launch_after(kn.down, grid, kItemWarps * 32, kn.smem, s, a, h->maps);
   }
-  if (e == cudaSuccess) e = launch_after(w4_combine, dim3((h->d / 4 + 127) / 128, T), 128, 0, true, s, a);
+  if (e == cudaSuccess) e = launch_after(w4_combine, dim3((h->d / 4 + 127) / 128, T), 128, 0, s, a);
   return e == cudaSuccess ? MOE_OK : moe::set_cuda_error(e, "w4_experts");
 }
 
