@@ -305,16 +305,44 @@ class MoELayer:
 
 def _on_device(name, t, device, dtype, shape):
     """_check_tensor for the operators: the exact shape, on ``device`` (the
-    current CUDA device's index, on which the call's stream is)."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        _check_tensor(name, t, dtype, shape)
-    if t.get_device() != device:
-        raise MoEError(MOE_E_INVAL, f"{name}: on device {t.get_device()}, the current one is {device}")
+    current CUDA device's index, on which the call's stream is).  A call of a few
+    microseconds makes several of these checks, so what is right costs four
+    comparisons; a host tensor's device is -1."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == device:
+        return
+    _check_tensor(name, t, dtype, shape)
+    raise MoEError(MOE_E_INVAL, f"{name}: on device {t.get_device()}, the current one is {device}")
+
+
+class _Torch:
+    """What the operators' calls need of torch, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.f32, self.bf16, self.i32, self.u8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+        self.current_device = torch.cuda.current_device
+        # the current stream's handle without a Stream object around it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+_torch_names = None
+
+
+def _torch():
+    global _torch_names
+    if _torch_names is None:
+        _torch_names = _Torch()
+    return _torch_names
 
 
 def _current_device():
-    import torch
-    return torch.cuda.current_device()
+    return _torch().current_device()
+
+
+def _stream_on(stream, device):
+    """The handle of ``stream``, or of the current stream of ``device``."""
+    return _torch().raw_stream(device) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 class MoERouter:
@@ -335,14 +363,15 @@ class MoERouter:
             raise MoEError(MOE_E_INVAL, (lib.moe_last_error() or b"").decode())
         self.h = ctypes.c_void_p(h)
         self.E, self.k = E, k
+        self._c_forward, self._c_backward = lib.moe_router_forward, lib.moe_router_backward
 
     def _check_logits(self, name, t, device):
         """Rows of E values, fp32 or bf16, that may be columns of a wider
         buffer; returns the type code and the row stride."""
-        import torch
-        if t.dtype is torch.float32:
+        tt = _torch()
+        if t.dtype is tt.f32:
             kind = 0
-        elif t.dtype is torch.bfloat16:
+        elif t.dtype is tt.bf16:
             kind = 1
         else:
             raise MoEError(MOE_E_INVAL, f"{name}: dtype {t.dtype}, expected torch.float32 or torch.bfloat16")
@@ -362,36 +391,34 @@ class MoERouter:
     def forward(self, logits, idx, w, bias=None, counts=None, stream=None):
         """logits [T, E] -> idx [T, k] int32, w [T, k] fp32 and, if given, counts
         [E] int32 (each expert's tokens).  ``bias`` [E] fp32 selects only."""
-        import torch
-        dev = _current_device()
-        kind, stride = self._check_logits("logits", logits, dev)
+        tt, dev = _torch(), _current_device()
+        kind, row = self._check_logits("logits", logits, dev)
         T = logits.shape[0]
-        _on_device("idx", idx, dev, torch.int32, (T, self.k))
-        _on_device("w", w, dev, torch.float32, (T, self.k))
+        _on_device("idx", idx, dev, tt.i32, (T, self.k))
+        _on_device("w", w, dev, tt.f32, (T, self.k))
         if bias is not None:
-            _on_device("bias", bias, dev, torch.float32, (self.E,))
+            _on_device("bias", bias, dev, tt.f32, (self.E,))
         if counts is not None:
-            _on_device("counts", counts, dev, torch.int32, (self.E,))
-        _err(lib.moe_router_forward(self.h, T, logits.data_ptr(), kind, stride,
-                                    None if bias is None else bias.data_ptr(), idx.data_ptr(),
-                                    w.data_ptr(), None if counts is None else counts.data_ptr(),
-                                    _stream_ptr(stream)))
+            _on_device("counts", counts, dev, tt.i32, (self.E,))
+        _err(self._c_forward(self.h, T, logits.data_ptr(), kind, row,
+                             None if bias is None else bias.data_ptr(), idx.data_ptr(),
+                             w.data_ptr(), None if counts is None else counts.data_ptr(),
+                             _stream_on(stream, dev)))
         return idx, w
 
     def backward(self, logits, idx, grad_w, grad_logits, stream=None):
         """grad_w [T, k] fp32 -> grad_logits [T, E], of the logits' dtype."""
-        import torch
-        dev = _current_device()
-        kind, stride = self._check_logits("logits", logits, dev)
-        out_kind, out_stride = self._check_logits("grad_logits", grad_logits, dev)
+        tt, dev = _torch(), _current_device()
+        kind, row = self._check_logits("logits", logits, dev)
+        out_kind, out_row = self._check_logits("grad_logits", grad_logits, dev)
         T = logits.shape[0]
         if out_kind != kind or grad_logits.shape[0] != T:
             raise MoEError(MOE_E_INVAL, "grad_logits: dtype and rows must be those of logits")
-        _on_device("idx", idx, dev, torch.int32, (T, self.k))
-        _on_device("grad_w", grad_w, dev, torch.float32, (T, self.k))
-        _err(lib.moe_router_backward(self.h, T, logits.data_ptr(), kind, stride, idx.data_ptr(),
-                                     grad_w.data_ptr(), grad_logits.data_ptr(), out_stride,
-                                     _stream_ptr(stream)))
+        _on_device("idx", idx, dev, tt.i32, (T, self.k))
+        _on_device("grad_w", grad_w, dev, tt.f32, (T, self.k))
+        _err(self._c_backward(self.h, T, logits.data_ptr(), kind, row, idx.data_ptr(),
+                              grad_w.data_ptr(), grad_logits.data_ptr(), out_row,
+                              _stream_on(stream, dev)))
         return grad_logits
 
     def close(self):
@@ -408,9 +435,8 @@ class MoERouter:
 
 def _check_w4(w, codes, scales, zeros):
     """Shapes of a bf16 matrix (any leading dimensions) and its 4-bit form;
-    returns rows, columns and the group."""
-    import torch
-    dev = _current_device()
+    returns rows, columns, the group and the device."""
+    tt, dev = _torch(), _current_device()
     shape = tuple(w.shape)
     if len(shape) < 2 or scales.dim() != len(shape) or shape[-1] % 2 != 0:
         raise MoEError(MOE_E_INVAL, f"weights {list(shape)} and scales {list(scales.shape)}: expected "
@@ -419,30 +445,30 @@ def _check_w4(w, codes, scales, zeros):
     group = cols // n if n else 0
     if group not in (32, 64, 128) or group * n != cols:
         raise MoEError(MOE_E_INVAL, f"{cols} columns and {n} scales a row: groups of 32, 64 or 128 are needed")
-    _on_device("weights", w, dev, torch.bfloat16, shape)
-    _on_device("codes", codes, dev, torch.uint8, shape[:-1] + (cols // 2,))
-    _on_device("scales", scales, dev, torch.bfloat16, shape[:-1] + (n,))
+    _on_device("weights", w, dev, tt.bf16, shape)
+    _on_device("codes", codes, dev, tt.u8, shape[:-1] + (cols // 2,))
+    _on_device("scales", scales, dev, tt.bf16, shape[:-1] + (n,))
     if zeros is not None:
-        _on_device("zeros", zeros, dev, torch.uint8, shape[:-1] + (n,))
-    return w.numel() // cols, cols, group
+        _on_device("zeros", zeros, dev, tt.u8, shape[:-1] + (n,))
+    return w.numel() // cols, cols, group, dev
 
 
 def w4_quantize(w, codes, scales, zeros=None, stream=None):
     """moe_w4_quantize: bf16 w [..., rows, cols] -> codes uint8 [..., rows,
     cols / 2], scales bf16 [..., rows, cols / group] and, if given, zeros uint8
     of the scales' shape.  The shape of ``scales`` sets the group (32, 64, 128)."""
-    rows, cols, group = _check_w4(w, codes, scales, zeros)
+    rows, cols, group, dev = _check_w4(w, codes, scales, zeros)
     _err(lib.moe_w4_quantize(rows, cols, group, w.data_ptr(), codes.data_ptr(), scales.data_ptr(),
-                             None if zeros is None else zeros.data_ptr(), _stream_ptr(stream)))
+                             None if zeros is None else zeros.data_ptr(), _stream_on(stream, dev)))
     return codes, scales, zeros
 
 
 def w4_dequantize(codes, scales, zeros, w, stream=None):
     """moe_w4_dequantize: the 4-bit weights' values as bf16 into w."""
-    rows, cols, group = _check_w4(w, codes, scales, zeros)
+    rows, cols, group, dev = _check_w4(w, codes, scales, zeros)
     _err(lib.moe_w4_dequantize(rows, cols, group, codes.data_ptr(), scales.data_ptr(),
                                None if zeros is None else zeros.data_ptr(), w.data_ptr(),
-                               _stream_ptr(stream)))
+                               _stream_on(stream, dev)))
     return w
 
 
@@ -462,6 +488,7 @@ class W4Experts:
         self.h = ctypes.c_void_p(h)
         self.d, self.f, self.E, self.k, self.S, self.group = d, f, E, k, shared_experts, group
         self._weights = self._device = None
+        self._c_forward = lib.moe_w4_forward
 
     def reserve(self, T_max: int, stream=None):
         _err(lib.moe_w4_reserve(self.h, T_max, _stream_ptr(stream)))
@@ -475,35 +502,37 @@ class W4Experts:
         [E + S, rows, cols / 2], scales bf16 and zeros uint8 [E + S, rows, cols /
         group]; rows, cols are f, d for gate and up and d, f for down.
         The codes are read where they are, the scales and zeros copied now."""
-        import torch
-        dev = _current_device()
+        tt, dev = _torch(), _current_device()
+        self._check_device(dev)
         n, args = self.E + self.S, []
         for name, m, rows, cols in (("gate", gate, self.f, self.d), ("up", up, self.f, self.d),
                                     ("down", down, self.d, self.f)):
             codes, scales, zeros = m
-            _on_device(name + " codes", codes, dev, torch.uint8, (n, rows, cols // 2))
-            _on_device(name + " scales", scales, dev, torch.bfloat16, (n, rows, cols // self.group))
+            _on_device(name + " codes", codes, dev, tt.u8, (n, rows, cols // 2))
+            _on_device(name + " scales", scales, dev, tt.bf16, (n, rows, cols // self.group))
             if zeros is not None:
-                _on_device(name + " zeros", zeros, dev, torch.uint8, (n, rows, cols // self.group))
+                _on_device(name + " zeros", zeros, dev, tt.u8, (n, rows, cols // self.group))
             args.append(_W4Weight(codes.data_ptr(), scales.data_ptr(),
                                   None if zeros is None else zeros.data_ptr()))
-        _err(lib.moe_w4_set_weights(self.h, *(ctypes.byref(a) for a in args), _stream_ptr(stream)))
+        _err(lib.moe_w4_set_weights(self.h, *(ctypes.byref(a) for a in args), _stream_on(stream, dev)))
         self._weights = (tuple(gate), tuple(up), tuple(down))  # alive while the library holds their pointers
+
+    def _check_device(self, dev):
+        if dev != self._device and self._device is not None:
+            raise MoEError(MOE_E_INVAL, f"the workspace is on device {self._device}, the current one is {dev}")
 
     def forward(self, x, idx, w, out, stream=None):
         """x [T, d] bf16, idx [T, k] int32 and w [T, k] fp32 (MoERouter.forward's)
         -> out [T, d] bf16; slots with idx outside [0, E) add nothing."""
-        import torch
-        dev = _current_device()
-        if self._device is not None and dev != self._device:
-            raise MoEError(MOE_E_INVAL, f"the workspace is on device {self._device}, the current one is {dev}")
+        tt, dev = _torch(), _current_device()
+        self._check_device(dev)
         T = x.shape[0]
-        _on_device("x", x, dev, torch.bfloat16, (T, self.d))
-        _on_device("idx", idx, dev, torch.int32, (T, self.k))
-        _on_device("w", w, dev, torch.float32, (T, self.k))
-        _on_device("out", out, dev, torch.bfloat16, (T, self.d))
-        _err(lib.moe_w4_forward(self.h, T, x.data_ptr(), idx.data_ptr(), w.data_ptr(),
-                                out.data_ptr(), _stream_ptr(stream)))
+        _on_device("x", x, dev, tt.bf16, (T, self.d))
+        _on_device("idx", idx, dev, tt.i32, (T, self.k))
+        _on_device("w", w, dev, tt.f32, (T, self.k))
+        _on_device("out", out, dev, tt.bf16, (T, self.d))
+        _err(self._c_forward(self.h, T, x.data_ptr(), idx.data_ptr(), w.data_ptr(), out.data_ptr(),
+                             _stream_on(stream, dev)))
         return out
 
     def status(self, stream=None) -> int:

@@ -916,10 +916,32 @@ dim3 convert_grid(long long n8) {
 
 }  // namespace
 
+namespace {
+
+struct Split {
+  int team, splits;
+};
+
+// How a batch of T tokens is run.
+struct Run {
+  int tokens;   // > 0: on the kernels of w4_tiles.cuh, so many token rows an item
+  Split gate_up, down;
+};
+
+// The workspace's regions, offsets from its start; h is first.
+struct Layout {
+  size_t y, xg, status, list, slot, row, bytes;
+};
+
+}  // namespace
+
 struct moe_w4 {
   int d, f, E, k, S, group;
   int T_max = 0;
   bool weights = false, zeros = false;  // set, with zero points
+  Layout l{};
+  Run run{};                            // of batches of run_T tokens
+  int run_T = 0;
   Maps maps;
   TileMaps tile_maps;                                              // x and h: of the pass
   CUtensorMap x_maps[kTileTokens / 32], h_maps[kTileTokens / 32];  // by an item's token rows
@@ -950,10 +972,6 @@ float estimate(long long items, int blocks, int team, int splits) {
          round * (float)(full + (rest > 0)) + 0.15f * units + 0.4f * (splits - 1);
 }
 
-struct Split {
-  int team, splits;
-};
-
 Split best_split(long long items, int blocks, int most_splits) {
   Split best{1, 1};
   float least = INFINITY;
@@ -972,12 +990,6 @@ long long chunks_of(const moe_w4* h, int T) {
   const long long rows = ((long long)T * h->k + experts - 1) / experts;
   return experts * ((rows + kChunk - 1) / kChunk) + (h->S ? (T + kChunk - 1) / kChunk : 0);
 }
-
-// How a batch of T tokens is run.
-struct Run {
-  int tokens;   // > 0: on the kernels of w4_tiles.cuh, so many token rows an item
-  Split gate_up, down;
-};
 
 Run run_of(const moe_w4* h, int T) {
   const long long experts = std::min<long long>(h->E, (long long)T * h->k);
@@ -1006,10 +1018,6 @@ Run run_of(const moe_w4* h, int T) {
   }
   return r;
 }
-
-struct Layout {
-  size_t y, xg, status, list, slot, row, bytes;
-};
 
 Layout layout(const moe_w4* h, int T_max) {
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
@@ -1181,7 +1189,8 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
     h->T_max = 0;
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_reserve");
-  const size_t bytes = layout(h, T_max).bytes;
+  const Layout l = layout(h, T_max);
+  const size_t bytes = l.bytes;
   if (!h->arranged && cudaMalloc(&h->arranged, arranged(h).bytes) != cudaSuccess) h->arranged = nullptr;
   if (!h->arranged || cudaMalloc(&h->ws, bytes) != cudaSuccess) {
     h->ws = nullptr;
@@ -1202,12 +1211,12 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
       if (e == cudaSuccess) e = cudaFuncSetAttribute(k.f, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_reserve");
-  const Layout l = layout(h, T_max);
   const uint64_t slots = (uint64_t)T_max * (h->k + h->S);
   for (uint32_t n = 0; n < kTileTokens / 32; ++n)
     if (!encode_rows(&h->x_maps[n], h->ws + l.xg, slots, h->d, 32 * n + 32) ||
         !encode_rows(&h->h_maps[n], h->ws, slots, h->f, 32 * n + 32))
       return moe::set_error(MOE_E_INVAL, "tensor map encoding failed");
+  h->l = l;
   h->T_max = T_max;
   moe::clear_error();
   return MOE_OK;
@@ -1264,7 +1273,9 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   if (!x || !idx || !w || !out) return moe::set_error(MOE_E_INVAL, "null tensor pointer");
   if (!aligned(x, 16) || !aligned(out, 16) || !aligned(idx, 4) || !aligned(w, 4))
     return moe::set_error(MOE_E_INVAL, "x and out must be 16-byte aligned, idx and w 4-byte");
-  const Layout l = layout(h, h->T_max);
+  const Layout& l = h->l;
+  if (h->run_T != T) h->run = run_of(h, T), h->run_T = T;
+  const Run& r = h->run;
   Experts a;
   a.T = T;
   a.d = h->d;
@@ -1272,7 +1283,6 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   a.E = h->E;
   a.k = h->k;
   a.S = h->S;
-  const Run r = run_of(h, T);
   a.team[0] = r.gate_up.team;
   a.team[1] = r.down.team;
   a.splits = r.down.splits;
@@ -1320,7 +1330,7 @@ int moe_w4_status(moe_w4_t* h, void* stream) {
   if (!h) return moe::set_error(MOE_E_INVAL, "null handle");
   if (!h->ws) return moe::set_error(MOE_E_STATE, "moe_w4_reserve was not called");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int* at = reinterpret_cast<int*>(h->ws + layout(h, h->T_max).status);
+  int* at = reinterpret_cast<int*>(h->ws + h->l.status);
   int status = 0;
   cudaError_t e = cudaMemcpyAsync(&status, at, sizeof(int), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
