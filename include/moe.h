@@ -398,8 +398,8 @@ int moe_router_forward(const moe_router_t* h, int T, const void* logits, int log
  * that the forward pass made (the choice itself and the bias have none):
  * grad_w [T, k] fp32 -> grad_logits, every one of its E columns overwritten,
  * of the logits' type, rows grad_row_stride elements apart.  Slots with idx
- * outside [0, E) are passed over; an expert that a row names twice gets the
- * sum.  grad_logits must not overlap the logits. */
+ * outside [0, E) or naming a masked expert (logit -inf) are passed over; an
+ * expert that a row names twice gets the sum.  grad_logits must not overlap the logits. */
 int moe_router_backward(const moe_router_t* h, int T, const void* logits, int logits_type,
                         long long row_stride, const int32_t* idx, const float* grad_w,
                         void* grad_logits, long long grad_row_stride, void* stream);
@@ -438,7 +438,11 @@ int moe_w4_dequantize(long long rows, int cols, int group, const void* codes, co
  * (idx, w) of moe_router_forward or of moe_layer_get_routing,
  *   h       = bf16( silu(Wg[e] x_t) * (Wu[e] x_t) )
  *   out[t]  = bf16( sum_j w[t,j] Wd[e_j] h_j  +  shared expert's, weight 1 )
- * with the weights' 4-bit values and fp32 sums.  Slots with idx outside
+ * with the weights' 4-bit values and fp32 sums.  (From about 6 rows an expert
+ * on, the tensor-core kernels round each weight to bf16, as moe_w4_dequantize
+ * does; with fewer no weight is rounded.)  Magnitudes of x and h are taken to
+ * lie below 2^64, those below 2^-57 count as zero; scales between 2^-86 and
+ * 2^31, or 0.  Slots with idx outside
  * [0, E) add nothing (the rows behind a padded batch's last sequence: idx -1);
  * an expert named twice by a row counts twice.  Shapes: gate and up
  * [E + S, f, d], down [E + S, d, f] (groups along the last axis), the shared

@@ -380,10 +380,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     const int row_of = lane / kpad, j = lane & (kpad - 1);
     const long long ts = t0 + row_of;
     const bool slot = row_of < rows && ts < T && j < k;
-    int e = slot ? idx[ts * k + j] : -1;
-    const bool live = (unsigned)e < (unsigned)E;
+    const int e = slot ? idx[ts * k + j] : -1;
+    const float lj = (unsigned)e < (unsigned)E ? to_float(logits[ts * stride + e]) : -INFINITY;
+    const bool live = lj != -INFINITY;  // nor a masked expert, whose score is 0
     const float g = live ? grad_w[ts * k + j] : 0.f;
-    const float lj = live ? to_float(logits[ts * stride + e]) : -INFINITY;
     float add = 0.f;  // what this slot adds to its expert's gradient
     if (r.renorm) {
       const float m = share_base(r.score, lj, live, kpad);

@@ -188,8 +188,9 @@ __global__ void __launch_bounds__(256)
 // with |x| below 2^64 nothing overflows, and what is below 2^-57 counts as
 // zero.  A group's sum of q x comes out as an fp32 sum of exact products; the
 // sum of x over the group, from one more mma whose weights are ones, takes the
-// zero point off: scale * 2^69 * (sum q x - zero * sum x).  No weight is
-// rounded.
+// zero point off: scale * (sum q x - zero * sum x), with the scale kept 2^40
+// times too large and the other 2^29 at the end, so that the product of a small
+// scale and a small sum does not vanish.  No weight is rounded.
 constexpr int kRows = 64;             // weight rows of an item
 constexpr int kChunk = 8;             // token rows of an item
 constexpr int kBlockK = 128;          // columns of a unit
@@ -205,9 +206,11 @@ constexpr int kInline = 32;           // slots up to which every block lists the
 // 4096 x 14336, 156 against 156 at 5 and 172 against 157 at 6; on 64 of 4096 x
 // 1408, 136 against 137 at 6 and 163 against 138 at 7.5.
 constexpr int kTileMinRows = 6;
+constexpr int kFewSums = 64;
 constexpr int kMaxSplit = 16;         // K splits of the down product
 constexpr uint32_t kScaleX = 0x5f805f80u, kScaleX16 = 0x5d805d80u;  // 2^64, 2^60 twice
-constexpr float kUnscale = 5.9029581035870565e20f;                  // 2^69
+constexpr float kScaleUp = 1099511627776.f;                         // 2^40, in the arranged scales
+constexpr float kUnscale = 536870912.f;                             // 2^29
 
 struct Experts {
   int T, d, f, E, k, S;
@@ -227,6 +230,7 @@ struct Experts {
   // the product takes them
   __nv_bfloat16* h;
   float* y;                 // [splits, T k + T S, d]
+  int* arrived;             // [d / 64] items of a column tile done, zero between passes; null: w4_combine adds
   int* status;              // MOE_E_TIMEOUT if a wait ran out
   void* list;               // List and Rows of a batch of more than kInline slots
   uint16_t *list_slot, *list_row;
@@ -458,16 +462,17 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return v;
 }
 
-// Wait for a stage's loads, two seconds at most: then the error is noted, no
-// later wait lasts, and the pass goes on, its output undefined.  The clock and
-// the noted error are looked at only after many tries: a load from global
-// memory between two tries makes a wait end most of a microsecond late.
+// Wait for a barrier, two seconds at most: then the error is noted and the pass
+// goes on, its output undefined, every later wait lasting 10 ms at most (so that
+// a block still waits for copies of its own before it ends).  The clock and the
+// noted error are looked at only after many tries: a load from global memory
+// between two tries makes a wait end most of a microsecond late.
 __device__ __forceinline__ void wait_stage(uint64_t* bar, uint32_t parity, int* status) {
 #pragma unroll 1
   for (int i = 0; i < 1 << 14; ++i)
     if (moe::mbar_try_wait(bar, parity)) return;
-  if (moe::ld_relaxed(status) != 0) return;
-  if (!moe::mbar_wait(bar, parity, moe::globaltimer() + 2000000000ull)) *status = MOE_E_TIMEOUT;
+  const uint64_t limit = moe::ld_relaxed(status) != 0 ? 10000000ull : 2000000000ull;
+  if (!moe::mbar_wait(bar, parity, moe::globaltimer() + limit)) *status = MOE_E_TIMEOUT;
 }
 
 // One item: an expert, 64 of its rows, a K range and a chunk of token rows.
@@ -496,6 +501,44 @@ struct Smem {
   static constexpr int kBytes = kFew + 2 * kInlineRows * 2 + 512;  // and the alignment of the codes
   static_assert(kBytes <= 113 * 1024 - 128, "two blocks to an SM");
 };
+
+__device__ __forceinline__ void add_to(float2& a, float2 b) { a.x += b.x, a.y += b.y; }
+__device__ __forceinline__ void add_to(float4& a, float4 b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
+__device__ __forceinline__ float2 times(float w, float2 a) { return make_float2(w * a.x, w * a.y); }
+__device__ __forceinline__ float4 times(float w, float4 a) { return make_float4(w * a.x, w * a.y, w * a.z, w * a.w); }
+
+// A token's output at some columns: the weighted sum of its slots, in slot
+// order, each the sum of its K splits, in order.  The loads of four slots and
+// splits go out together, whether the slot has an expert or not.
+template <typename V>
+__device__ __forceinline__ V combine_token(const Experts& a, int t, int col) {
+  const int n = a.k + a.S;
+  const size_t slots = (size_t)a.T * n;
+  V o{};
+  for (int j0 = 0; j0 < n; j0 += 4) {
+    const float* from[4];
+    float wj[4];
+    bool live[4];
+    V y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = min(j0 + i, n - 1), p = j < a.k ? t * a.k + j : a.T * a.k + t;
+      live[i] = j0 + i < n && (j >= a.k || expert_at(a, p) >= 0);
+      wj[i] = j < a.k ? __ldg(a.w + p) : 1.f;
+      from[i] = a.y + (size_t)p * a.d + col;
+      y[i] = __ldcg(reinterpret_cast<const V*>(from[i]));
+    }
+#pragma unroll 4
+    for (int q = 1; q < a.splits; ++q) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add_to(y[i], __ldcg(reinterpret_cast<const V*>(from[i] + q * slots * a.d)));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (live[i]) add_to(o, times(wj[i], y[i]));
+  }
+  return o;
+}
 
 // One pass over the items for one of the two products.
 template <bool DOWN, int G, bool Z>
@@ -559,6 +602,13 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
   }
   __syncthreads();
   const int n_items = item_start[n_active];
+
+  if (DOWN && a.arrived && n_items == 0) {  // no slot has an expert, and no kernel follows
+    wait_for_previous_kernel();
+    for (int i = blockIdx.x * blockDim.x + tid; i < a.T * a.d / 2; i += gridDim.x * blockDim.x)
+      reinterpret_cast<uint32_t*>(a.out)[i] = 0u;
+    return;
+  }
 
   auto item_of = [&](int i, int* at, Item* it) {  // `at` only moves forward
     while (i >= item_start[*at + 1]) ++*at;
@@ -790,6 +840,23 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
         }
       }
     }
+    if (DOWN && a.arrived) {  // the warp that completes a column tile adds its tokens' slots
+      __threadfence();
+      __syncwarp();
+      int last = 0;
+      if (lane == 0) {
+        last = atomicAdd(a.arrived + it.tile, 1) + 1 == n_items / row_tiles;
+        if (last) a.arrived[it.tile] = 0;
+      }
+      if (__shfl_sync(0xffffffffu, last, 0)) {
+        __threadfence();
+        for (int t = 0; t < a.T; ++t) {
+          const float2 o = combine_token<float2>(a, t, it.tile * kRows + lane * 2);
+          *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)t * a.d + it.tile * kRows + lane * 2) =
+              __floats2bfloat162_rn(o.x, o.y);
+        }
+      }
+    }
   }
 }
 
@@ -822,7 +889,7 @@ __global__ void __launch_bounds__(256)
       const long long row =
           (four / fours * row_tiles + tile) * (both32 ? 32 : kRows) + (both32 ? (r & 3) * 8 : r * 8) + g;
       const long long o = (row * blocks_k + kb) * kg + grp;
-      s.b[r] = m.scales[o];
+      s.b[r] = __float2bfloat16(__bfloat162float(m.scales[o]) * kScaleUp);  // exact
       if (zeros) z.b[r] = m.zeros[o] & 15;
     }
     scales[i] = s.q;
@@ -830,51 +897,12 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// out[t] = the weighted sum of the token's slots, in slot order, each the sum
-// of its K splits, in order.  The loads of four slots and splits go out
-// together, whether the slot has an expert or not: one after the other they
-// took 13 us for one token of 8 slots.
 __global__ void __launch_bounds__(128) w4_combine(const Experts a) {
   const int t = blockIdx.y, col = (blockIdx.x * 128 + threadIdx.x) * 4;
-  const int n = a.k + a.S;
-  const size_t slots = (size_t)a.T * n;
   let_next_kernel_start();
   wait_for_previous_kernel();
   if (col >= a.d) return;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j0 = 0; j0 < n; j0 += 4) {
-    const float* from[4];
-    float wj[4];
-    bool live[4];
-    float4 y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = min(j0 + i, n - 1), p = j < a.k ? t * a.k + j : a.T * a.k + t;
-      live[i] = j0 + i < n && (j >= a.k || expert_at(a, p) >= 0);
-      wj[i] = j < a.k ? __ldg(a.w + p) : 1.f;
-      from[i] = a.y + (size_t)p * a.d + col;
-      y[i] = __ldcg(reinterpret_cast<const float4*>(from[i]));
-    }
-#pragma unroll 4
-    for (int q = 1; q < a.splits; ++q) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(from[i] + q * slots * a.d));
-        y[i].x += v.x;
-        y[i].y += v.y;
-        y[i].z += v.z;
-        y[i].w += v.w;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!live[i]) continue;
-      o.x += wj[i] * y[i].x;
-      o.y += wj[i] * y[i].y;
-      o.z += wj[i] * y[i].z;
-      o.w += wj[i] * y[i].w;
-    }
-  }
+  const float4 o = combine_token<float4>(a, t, col);
   union {
     __nv_bfloat162 b[2];
     uint2 u;
@@ -930,7 +958,7 @@ struct Run {
 
 // The workspace's regions, offsets from its start; h is first.
 struct Layout {
-  size_t y, xg, status, list, slot, row, bytes;
+  size_t y, xg, status, arrived, list, slot, row, bytes;
 };
 
 }  // namespace
@@ -1028,7 +1056,8 @@ Layout layout(const moe_w4* h, int T_max) {
   l.y = up(slots * h->f * 2);
   l.xg = l.y + up(y);
   l.status = l.xg + up(slots * h->d * 2);
-  l.list = l.status + 256;
+  l.arrived = l.status + 256;
+  l.list = l.arrived + up((size_t)h->d / kRows * 4);
   l.slot = l.list + up(sizeof(List));
   l.row = l.slot + up(slots * 2);
   l.bytes = l.row + up(slots * 2);
@@ -1300,6 +1329,10 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   a.h = reinterpret_cast<__nv_bfloat16*>(h->ws);
   a.y = reinterpret_cast<float*>(h->ws + l.y);
   a.xg = reinterpret_cast<__nv_bfloat16*>(h->ws + l.xg);
+  // few partial sums: the last item of a column tile adds them, and no third
+  // kernel follows (one token of the eight-expert layer 44.1 -> 42.9 us)
+  const bool few = !r.tokens && T * (h->k + h->S) * r.down.splits <= kFewSums;
+  a.arrived = few ? reinterpret_cast<int*>(h->ws + l.arrived) : nullptr;
   a.status = reinterpret_cast<int*>(h->ws + l.status);
   a.list = h->ws + l.list;
   a.list_slot = reinterpret_cast<uint16_t*>(h->ws + l.slot);
@@ -1322,7 +1355,7 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
     if (e == cudaSuccess) e = launch_after(kn.gate_up, grid, kItemWarps * 32, kn.smem, s, a, h->maps);
     if (e == cudaSuccess) e = launch_after(kn.down, grid, kItemWarps * 32, kn.smem, s, a, h->maps);
   }
-  if (e == cudaSuccess) e = launch_after(w4_combine, dim3((h->d / 4 + 127) / 128, T), 128, 0, s, a);
+  if (e == cudaSuccess && !a.arrived) e = launch_after(w4_combine, dim3((h->d / 4 + 127) / 128, T), 128, 0, s, a);
   return e == cudaSuccess ? MOE_OK : moe::set_cuda_error(e, "w4_experts");
 }
 

@@ -401,11 +401,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int q = (half * 2 + c) * 32 / G;
-            // scale * 2^96 and 2^92 and -8 scale 2^-37, each twice and exact
+            // scale * 2^96 and 2^92 and -8 scale 2^-37, each twice and exact, from
+            // the arranged scale * 2^40
             const float sf = __uint_as_float(sc[q] << 16);
-            const uint32_t s1 = bf16_twice(sf * 79228162514264337593543950336.f);
-            const uint32_t s16 = bf16_twice(sf * 4951760157141521099596496896.f);
-            const uint32_t c8 = bf16_twice(sf * -5.820766091346741e-11f);
+            const uint32_t s1 = bf16_twice(sf * 72057594037927936.f);
+            const uint32_t s16 = bf16_twice(sf * 4503599627370496.f);
+            const uint32_t c8 = bf16_twice(sf * -5.293955920339377e-23f);
             const uint32_t z1 = zr[q] * 0x00010001u, z16 = zr[q] * 0x00100010u;
             const uint4 v = w[half * 2 + c];
             const uint32_t words[4] = {v.x, v.y, v.z, v.w};

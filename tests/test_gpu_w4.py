@@ -123,6 +123,12 @@ class Case:
             assert np.linalg.norm(got - want) <= ref.EXPERTS_NORM * np.linalg.norm(want)
 
 
+    def checked(self):
+        layer = self.layer()
+        self.check(self.run(layer))
+        layer.check()
+
+
 CASES = {
     # T, d, E, k, f, S, group, zeros
     "one_token": (1, 256, 8, 2, 384, 0, 128, False),
@@ -273,3 +279,96 @@ def test_route_then_experts_and_the_bf16_layer_on_the_same_weights():
     layer.close()
     assert np.array_equal(np.sort(routing["idx"], 1), np.sort(idx.cpu().numpy(), 1))
     assert np.all(np.abs(hz.bf16_to_f64(full) - host(out)) <= 1e-2 + 1e-2 * np.abs(host(out)) + off)
+
+
+# --------------------------------------------- the ways a batch can be run
+
+@pytest.mark.parametrize("group,zeros", [(32, False), (32, True), (64, False), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("T", [1, 5, 40, 90])
+def test_every_kernel_with_every_group_and_zero_point(T, group, zeros):
+    """One token (the fused sums), a few rows (the small kernels), 20 and 45 rows
+    an expert (the tile kernels), with rows of 384 and 640 columns: row tiles
+    that do not fill a four of them."""
+    Case(T, 384, 4, 2, 640, 1, group, zeros, seed=T + group).checked()
+
+
+@pytest.mark.parametrize("rows", [6, 31, 32, 33, 63, 64, 65, 96, 97, 128, 129, 200])
+def test_tiles_with_token_counts_about_their_widths(rows):
+    c = Case(rows, 256, 2, 1, 256, 0, 128, False, seed=rows)
+    c.idx[:] = 1
+    c.idx[rows // 2:rows // 2 + 1] = 0
+    c.checked()
+
+
+def test_uneven_experts_on_the_tile_kernels():
+    """One expert has most of the rows, one a single row, one none."""
+    c = Case(300, 128, 5, 2, 384, 0, 64, True, seed=77)
+    rng = np.random.default_rng(1)
+    c.idx[:, 0], c.idx[:, 1] = 3, np.where(rng.random(300) < 0.1, 1, 2)
+    c.idx[9, 1] = 0
+    c.idx[250:] = -1
+    c.w[250:] = 0
+    c.checked()
+
+
+def test_nothing_to_do_writes_zeros():
+    for T in (1, 3, 64):
+        c = Case(T, 128, 8, 2, 128, 0, 128, False, seed=T)
+        c.idx[:] = -1
+        layer = c.layer()
+        assert np.all(c.run(layer) == 0)
+        c.idx[:] = [0, 1]
+        c.check(c.run(layer))
+
+
+def test_largest_batch():
+    """T = 1024, k = 16: 16384 slots, listed in 16 rounds."""
+    c = Case(1024, 128, 64, 16, 128, 0, 128, False, seed=91)
+    got = c.run()
+    rows = np.r_[0:8, 511:515, 1016:1024]
+    want, off = ref.experts(c.x[rows], c.idx[rows], c.w[rows].astype(np.float64), c.gate, c.up, c.down, 64, 0)
+    assert np.all(np.abs(got[rows] - want) <= off)
+    assert np.all(np.isfinite(got))
+
+
+def test_two_layers_at_once_on_two_streams():
+    import torch
+    a, b = Case(1, 512, 8, 2, 1024, 0, 128, False, seed=95), Case(64, 512, 8, 2, 1024, 0, 64, True, seed=96)
+    la, lb = a.layer(), b.layer()
+    want = [a.run(la), b.run(lb)]
+    ins = [(dev_bf16(c.x), dev(c.idx), dev(c.w), torch.empty(c.shape[0], 512, dtype=torch.bfloat16, device="cuda"))
+           for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for layer, i, s in zip((la, lb), ins, streams):
+            with torch.cuda.stream(s):
+                layer.forward(*i)
+    torch.cuda.synchronize()
+    for i, w in zip(ins, want):
+        assert np.array_equal(host(i[3]), w)
+    la.check(), lb.check()
+
+
+def test_magnitudes_at_the_ends_of_the_range():
+    """x of 2^40 and 2^-40, scales of 2^-60: h and out far from one."""
+    for T in (3, 24):
+        c = Case(T, 128, 2, 1, 128, 0, 128, False, seed=5)
+        c.x = c.x * 2.0 ** np.where(np.arange(T) % 2, -20, 20)[:, None]
+        c.down = (c.down[0], c.down[1] * 2.0 ** -60, None)
+        c.checked()
+
+
+def test_weights_replaced():
+    import torch
+    a, b = Case(9, 128, 4, 2, 256, 0, 64, True, seed=1), Case(9, 128, 4, 2, 256, 0, 64, False, seed=2)
+    layer = a.layer()
+    a.check(a.run(layer))
+    second = [(dev(c), dev_bf16(s), dev(z)) for c, s, z in (b.gate, b.up, b.down)]
+    layer.set_weights(*second)
+    for _, s, _ in second:
+        s.zero_()                       # copied: later changes are not seen
+    b.check(b.run(layer))
+    layer.reserve(50)                   # a larger workspace keeps them
+    b.check(b.run(layer))
+    torch.cuda.synchronize()
