@@ -16,13 +16,13 @@
 //   sigmoid, renormalised: dl_j = scale a_j (1 - s_j) (g_j - sum_i g_i a_i)
 //
 // A row's logits are in the registers of 4, 8, 16 or 32 lanes, 8 consecutive
-// experts each, so a warp chooses for 8 to 1 rows at once; the lowest lane with
-// the maximum is the lowest expert, so a selection round is a maximum over the
-// row's lanes, one ballot and a search among 8 values.  The weights follow for
-// the chosen alone, a lane a slot, for several rows together.  What bounds both
-// kernels is instructions, not the 2 to 4 bytes a logit: at 8192 rows of 256
-// experts in 8 groups, top 8, the selection rounds are half of them.  Scores
-// and sums are fp32.
+// experts each, so a warp chooses for 8 to 1 rows at once, from few candidates
+// (choose below).  The weights follow for the chosen alone, a lane a slot, for
+// several rows together.  What bounds the choice is instructions, not the 2 to 4
+// bytes a logit: 870 of a warp for a row of 256 experts in 8 groups, top 8 (8192
+// rows 14.4 us, their bytes 1.2); the gradient waits for the gathered logits,
+// then writes every expert (32768 rows of 256 fp32 11.6 us, those writes 4.9).
+// Scores and sums are fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -43,11 +43,17 @@ constexpr int kMaxGroups = 32;
 constexpr int kWarps = 8;           // of a block
 constexpr int kVals = 8;            // experts of a lane
 constexpr int kSms = 152;
+// Blocks resident on an SM.  More hide more latency, fewer leave a warp more rows
+// together: 8192 rows of 256 grouped experts 14.4 us at 2 and 3, 16.4 at 4, 32768
+// of 64 experts 14.4, 12.8 and 14.4; the gradient of 32768 rows of 256 12.3 at 3,
+// 11.6 at 4, 13.7 at 5.
+constexpr int kForward = 3, kBackward = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
 struct Route {
   int E, k, score, groups, kept, group_score, renorm;
   float scale;
+  int span;  // log2 of the lanes of a group, if it is 8 experts of each of 1, 2, 4 ... lanes, or -1
 };
 
 // Rows a warp takes together, at most.
@@ -170,8 +176,13 @@ __device__ __forceinline__ void row_softmax(float (&v)[VPL], float* top, float* 
   for (int i = 0; i < VPL; ++i) v[i] *= *inv;
 }
 
-// For the choice alone: within 4e-7.
-__device__ __forceinline__ float fast_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
+// For the choice alone: within 4e-7, by the device's 2^x and reciprocal.
+__device__ __forceinline__ float fast_sigmoid(float l) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
 
 __device__ __forceinline__ float sigmoid(float l) {
   const float e = expf(-fabsf(l));
@@ -192,22 +203,128 @@ __device__ __forceinline__ float share_base(int score, float l, bool live, int n
   return score == MOE_SCORE_SOFTMAX ? m : fminf(m, 0.f);
 }
 
-// `rows`: rows a warp takes together, a multiple of 32 / LANES; kpad: k rounded
-// up to a power of two.
+// The two largest of this lane's and the lane o away's.
+__device__ __forceinline__ void merge_top2(uint32_t& m1, uint32_t& m2, int o) {
+  const uint32_t o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
+  m2 = max(max(m2, o2), min(m1, o1));
+  m1 = max(m1, o1);
+}
+
+// What ranks a group of these two largest keys; at least kDead.
+__device__ __forceinline__ uint32_t level_of(uint32_t m1, uint32_t m2, bool top2) {
+  if (top2 && m1 > kDead && m2 > kDead) m1 = key_of(value_of(m1) + value_of(m2));
+  return max(m1, kDead);
+}
+
+// pick[0..k) = the experts of the k largest keys of the row held by LANES
+// lanes, larger first, the lower expert on ties; -1 where none is left.
+//
+// k rounds on the lanes' largest keys alone give a bound that at least k keys
+// (of as many lanes) reach and few others do (k = 8 of 256: 9 to 11 on
+// average); these candidates are listed in the experts' order and each is
+// ranked against the others, in about 170 instructions where k rounds of a
+// maximum, its expert and its removal over all keys took 500 (8192 rows 20.6 us
+// so, 16.5 with candidates).  Rows with more candidates than kHold a lane (many
+// equal logits) are still chosen by such rounds.
+constexpr int kHold = 2;
+
+template <int LANES>
+__device__ __forceinline__ void choose(uint32_t (&key)[kVals], int k, int e0, int sub, int at_once, uint2* cand,
+                                       int* pick) {
+  constexpr unsigned kRun = LANES == 32 ? kAll : (1u << (LANES & 31)) - 1u;
+  uint32_t best = key[0];
+#pragma unroll
+  for (int i = 1; i < kVals; ++i) best = max(best, key[i]);
+  uint32_t bound = 0u, rest = best;
+  for (int j = 0; j < k; ++j) {
+    bound = run_max<LANES>(rest);
+    rest = rest == bound ? 0u : rest;
+  }
+  bound = max(bound, kDead + 1u);
+  int mine = 0, before = 0;
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) mine += key[i] >= bound;
+  const int shift = LANES == 32 ? 0 : at_once * LANES;
+  int n = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {  // the lanes' counts, 0 to 8, added bit by bit
+    const unsigned with = __ballot_sync(kAll, mine >> b & 1) >> shift & kRun;
+    before += __popc(with & ((1u << sub) - 1u)) << b;
+    n += __popc(with) << b;
+  }
+  if (!__any_sync(kAll, n > kHold * LANES)) {
+#pragma unroll
+    for (int i = 0; i < kVals; ++i)
+      if (key[i] >= bound) cand[before++] = make_uint2(key[i], e0 + i);
+    __syncwarp();
+    uint2 c[kHold];
+    int rank[kHold];
+#pragma unroll
+    for (int h = 0; h < kHold; ++h) {
+      const int q = h * LANES + sub;
+      c[h] = q < n ? cand[q] : make_uint2(0u, 0u);
+      rank[h] = 0;
+    }
+    const int most = LANES == 32 ? n : __reduce_max_sync(kAll, n);
+    if (most <= LANES) {
+      for (int o = 0; o < most; ++o)
+        rank[0] += __shfl_sync(kAll, c[0].x, o, LANES) > (o < sub ? c[0].x - 1u : c[0].x);
+    } else {
+#pragma unroll
+      for (int f = 0; f < kHold; ++f) {
+        for (int o = 0; o < LANES && f * LANES + o < most; ++o) {
+          const uint32_t v = __shfl_sync(kAll, c[f].x, o, LANES);
+#pragma unroll
+          for (int h = 0; h < kHold; ++h) rank[h] += v > (f < h || (f == h && o < sub) ? c[h].x - 1u : c[h].x);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < kHold; ++h)
+      if (h * LANES + sub < n && rank[h] < k) pick[rank[h]] = (int)c[h].y;
+    for (int j = n + sub; j < k; j += LANES) pick[j] = -1;
+    __syncwarp();  // the candidates' place is free again
+    return;
+  }
+  for (int j = 0; j < k; ++j) {
+    const uint32_t m = run_max<LANES>(best);
+    const unsigned with = __ballot_sync(kAll, best == m) >> shift & kRun;
+    const bool here = sub == __ffs(with) - 1;
+    const uint32_t hit = here && m > kDead ? m : 1u;  // no key is 1
+    int e = -1;
+#pragma unroll
+    for (int i = kVals - 1; i >= 0; --i) e = key[i] == hit ? i : e;
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) key[i] = e == i ? 0u : key[i];
+    if (here) {
+      pick[j] = e < 0 ? -1 : e0 + e;
+      best = max(max(max(key[0], key[1]), max(key[2], key[3])), max(max(key[4], key[5]), max(key[6], key[7])));
+    }
+  }
+}
+
+// What a warp takes of the rows, in units of `unit` rows: `base` units, the first
+// `extra` warps one more, at most `units` of them together.  klog: log2 of kpad,
+// k rounded up to a power of two.
+struct Share {
+  int unit, base, extra, units, klog;
+};
+
 template <typename L, int LANES, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32, 3)
-    route_forward(Route r, int T, int rows, int kpad, const L* __restrict__ logits, long long stride,
+__global__ void __launch_bounds__(kWarps * 32, kForward)
+    route_forward(Route r, int T, Share share, const L* __restrict__ logits, long long stride,
                   const float* __restrict__ bias, int* __restrict__ idx, float* __restrict__ w,
                   int* __restrict__ counts) {
   constexpr int kAtOnce = 32 / LANES, kMaxRows = max_rows(LANES);
   __shared__ float s_value[kWarps][32 * kVals];
   __shared__ uint32_t s_level[kWarps][kAtOnce][kMaxGroups];
+  __shared__ uint2 s_cand[kWarps][32 * kHold];
   __shared__ int s_pick[kWarps][kMaxRows][kMaxK];
   __shared__ float2 s_norm[kWarps][kMaxRows];
   __shared__ int s_count[kMaxE];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & (LANES - 1), at_once = lane / LANES;
-  const int E = r.E, k = r.k, e0 = sub * kVals;
+  const int E = r.E, k = r.k, klog = share.klog, kpad = 1 << klog, e0 = sub * kVals;
   const int gs = E / r.groups;
   if (counts) {
     for (int e = threadIdx.x; e < E; e += kWarps * 32) s_count[e] = 0;
@@ -220,16 +337,24 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   const bool by_level = r.groups > 1;
   const bool level_of_scores = by_level && top2;
   const bool need_p = r.score == MOE_SCORE_SOFTMAX && (!r.renorm || bias || level_of_scores);
-  // groups: `per` lanes walk each group (one lane several groups if there are
-  // more groups than lanes); which group this lane's experts are in
+  // groups that are not whole lanes: `per` lanes walk each group (one lane
+  // several groups if there are more groups than lanes); which group this
+  // lane's experts are in
   int per = LANES;
-  while (per > 1 && per * r.groups > LANES) per >>= 1;
   int in_group[kVals];
+  if (by_level && r.span < 0) {
+    while (per > 1 && per * r.groups > LANES) per >>= 1;
 #pragma unroll
-  for (int i = 0; i < kVals; ++i) in_group[i] = by_level && e0 + i < E ? (e0 + i) / gs : 0;
+    for (int i = 0; i < kVals; ++i) in_group[i] = e0 + i < E ? (e0 + i) / gs : 0;
+  }
 
-  for (long long t0 = ((long long)blockIdx.x * kWarps + warp) * rows; t0 < T; t0 += (long long)gridDim.x * kWarps * rows) {
-    for (int r0 = 0; r0 < rows && t0 + r0 < T; r0 += kAtOnce) {
+  const int w_id = blockIdx.x * kWarps + warp;
+  int left = share.base + (w_id < share.extra);
+  long long t0 = ((long long)w_id * share.base + min(w_id, share.extra)) * share.unit;
+  for (int now; left > 0; left -= now, t0 += now * share.unit) {
+    now = min(left, share.units);
+    const int rows = now * share.unit;
+    for (int r0 = 0; r0 < rows; r0 += kAtOnce) {
       const long long t = t0 + r0 + at_once;
       const L* row = logits + (t < T ? t : T - 1) * stride;
       float l[kVals], s[kVals];
@@ -245,15 +370,39 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         for (int i = 0; i < kVals; ++i) s[i] = fast_sigmoid(l[i]);
       }
       uint32_t key[kVals];
+      if (bias) {
 #pragma unroll
-      for (int i = 0; i < kVals; ++i) key[i] = l[i] == -INFINITY ? 0u : key_of(bias ? s[i] + b[i] : l[i]);
-      if (by_level) {
+        for (int i = 0; i < kVals; ++i) key[i] = l[i] == -INFINITY ? 0u : key_of(s[i] + b[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) key[i] = key_of(l[i]);
+      }
+      if (by_level && r.span >= 0) {
+        // a group is some lanes: its two largest by exchanges among them
+        uint32_t m1 = 0u, m2 = 0u;
+#pragma unroll
+        for (int i = 0; i < kVals; ++i) {
+          const uint32_t v = key[i] > kDead && level_of_scores && !bias ? key_of(s[i]) : key[i];
+          m2 = max(m2, min(m1, v));
+          m1 = max(m1, v);
+        }
+        for (int o = (1 << r.span) >> 1; o; o >>= 1) merge_top2(m1, m2, o);
+        const uint32_t level = level_of(m1, m2, top2);
+        const int g = sub >> r.span;
+        int rank = 0;
+        for (int o = 0; o < r.groups; ++o)
+          rank += __shfl_sync(kAll, level, o << r.span, LANES) > (o < g ? level - 1u : level);
+        if (rank >= r.kept) {
+#pragma unroll
+          for (int i = 0; i < kVals; ++i) key[i] = 0u;
+        }
+      } else if (by_level) {
         // the value each expert gives its group: c, s without a bias, or l where
         // the largest alone counts
         uint32_t* value = reinterpret_cast<uint32_t*>(s_value[warp]) + at_once * LANES * kVals;
 #pragma unroll
         for (int i = 0; i < kVals; ++i)
-          value[e0 + i] = key[i] != 0u && level_of_scores && !bias ? key_of(s[i]) : key[i];
+          value[e0 + i] = key[i] > kDead && level_of_scores && !bias ? key_of(s[i]) : key[i];
         __syncwarp();
         for (int g0 = 0; g0 < r.groups; g0 += LANES / per) {
           const int g = g0 + sub / per, step = sub & (per - 1);
@@ -267,23 +416,15 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
               m1 = max(m1, v);
             }
           }
-          for (int o = per >> 1; o; o >>= 1) {
-            const uint32_t o1 = __shfl_xor_sync(kAll, m1, o), o2 = __shfl_xor_sync(kAll, m2, o);
-            m2 = max(max(m2, o2), min(m1, o1));
-            m1 = max(m1, o1);
-          }
-          if (top2 && m1 > kDead && m2 > kDead) m1 = key_of(value_of(m1) + value_of(m2));
-          if (g < r.groups && step == 0) s_level[warp][at_once][g] = max(m1, kDead);
+          for (int o = per >> 1; o; o >>= 1) merge_top2(m1, m2, o);
+          if (g < r.groups && step == 0) s_level[warp][at_once][g] = level_of(m1, m2, top2);
         }
         __syncwarp();
         uint32_t kept = 0u;
         for (int g = sub; g < r.groups; g += LANES) {
           const uint32_t level = s_level[warp][at_once][g];
           int rank = 0;
-          for (int o = 0; o < r.groups; ++o) {
-            const uint32_t v = s_level[warp][at_once][o];
-            rank += v > level || (v == level && o < g);
-          }
+          for (int o = 0; o < r.groups; ++o) rank += s_level[warp][at_once][o] > (o < g ? level - 1u : level);
           if (rank < r.kept) kept |= 1u << g;
         }
         for (int o = LANES / 2; o; o >>= 1) kept |= __shfl_xor_sync(kAll, kept, o);
@@ -291,30 +432,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
         for (int i = 0; i < kVals; ++i)
           if (!(kept >> in_group[i] & 1u)) key[i] = 0u;
       }
-      uint32_t best = key[0];
-#pragma unroll
-      for (int i = 1; i < kVals; ++i) best = max(best, key[i]);
-      int* pick = s_pick[warp][r0 + at_once];
-      for (int j = 0; j < k; ++j) {
-        const uint32_t m = run_max<LANES>(best);
-        unsigned with = __ballot_sync(kAll, best == m);
-        if (LANES < 32) with = with >> (at_once * LANES) & ((1u << (LANES & 31)) - 1u);
-        const bool mine = sub == __ffs(with) - 1;
-        const uint32_t hit = mine && m > kDead ? m : 1u;  // no key is 1
-        int e = -1;
-#pragma unroll
-        for (int i = kVals - 1; i >= 0; --i) e = key[i] == hit ? i : e;
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) key[i] = e == i ? 0u : key[i];
-        if (mine) {
-          pick[j] = e < 0 ? -1 : e0 + e;
-          best = max(max(max(key[0], key[1]), max(key[2], key[3])), max(max(key[4], key[5]), max(key[6], key[7])));
-        }
-      }
+      choose<LANES>(key, k, e0, sub, at_once, s_cand[warp] + at_once * LANES * kHold, s_pick[warp][r0 + at_once]);
     }
     __syncwarp();
     for (int q0 = 0; q0 < rows * kpad; q0 += 32) {
-      const int row_of = (q0 + lane) / kpad, j = lane & (kpad - 1);
+      const int row_of = (q0 + lane) >> klog, j = lane & (kpad - 1);
       const long long t = t0 + row_of;
       const bool slot = row_of < rows && t < T && j < k;
       const int e = slot ? s_pick[warp][row_of][j] : -1;
@@ -351,8 +473,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
 // time by 32 / LANES rows: what the softmax gives every expert, or zero, with
 // the slots' shares added.
 template <typename L, int LANES, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32, 3)
-    route_backward(Route r, int T, int rows, int kpad, const L* __restrict__ logits, long long stride,
+__global__ void __launch_bounds__(kWarps * 32, kBackward)
+    route_backward(Route r, int T, Share share, const L* __restrict__ logits, long long stride,
                    const int* __restrict__ idx, const float* __restrict__ grad_w,
                    L* __restrict__ grad, long long grad_stride) {
   constexpr int kAtOnce = 32 / LANES, kMaxRows = max_rows(LANES);
@@ -361,12 +483,28 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
   __shared__ float s_dot[kWarps][kMaxRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & (LANES - 1), at_once = lane / LANES;
-  const int E = r.E, k = r.k, e0 = sub * kVals;
+  const int E = r.E, k = r.k, klog = share.klog, kpad = 1 << klog, e0 = sub * kVals;
   const bool dense = r.score == MOE_SCORE_SOFTMAX && !r.renorm;
   // rows of zeros to add to; the entries added to are set back below
   for (int i = lane; i < kMaxRows * LANES * kVals; i += 32) (&s_row[warp][0][0])[i] = 0.f;
   __syncwarp();
-  for (long long t0 = ((long long)blockIdx.x * kWarps + warp) * rows; t0 < T; t0 += (long long)gridDim.x * kWarps * rows) {
+  const int w_id = blockIdx.x * kWarps + warp;
+  int left = share.base + (w_id < share.extra);
+  long long t0 = ((long long)w_id * share.base + min(w_id, share.extra)) * share.unit;
+  const int row_of = lane >> klog, j = lane & (kpad - 1);
+  int rows = min(left, share.units) * share.unit;
+  bool slot = row_of < rows && t0 + row_of < T && j < k;
+  int e = slot ? idx[(t0 + row_of) * k + j] : -1;
+  float g = slot ? grad_w[(t0 + row_of) * k + j] : 0.f;
+  float lj = (unsigned)e < (unsigned)E ? to_float(logits[(t0 + row_of) * stride + e]) : -INFINITY;
+  while (left > 0) {
+    // the next slots are on their way while these are worked on
+    left -= share.units;
+    const long long t1 = t0 + rows;
+    const int rows1 = max(min(left, share.units) * share.unit, 0);
+    slot = row_of < rows1 && t1 + row_of < T && j < k;
+    const int e1 = slot ? idx[(t1 + row_of) * k + j] : -1;
+    const float g1 = slot ? grad_w[(t1 + row_of) * k + j] : 0.f;
     if (dense) {
       for (int r0 = 0; r0 < rows && t0 + r0 < T; r0 += kAtOnce) {
         const long long t = t0 + r0 + at_once;
@@ -377,13 +515,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
       }
       __syncwarp();
     }
-    const int row_of = lane / kpad, j = lane & (kpad - 1);
-    const long long ts = t0 + row_of;
-    const bool slot = row_of < rows && ts < T && j < k;
-    const int e = slot ? idx[ts * k + j] : -1;
-    const float lj = (unsigned)e < (unsigned)E ? to_float(logits[ts * stride + e]) : -INFINITY;
-    const bool live = lj != -INFINITY;  // nor a masked expert, whose score is 0
-    const float g = live ? grad_w[ts * k + j] : 0.f;
+    const bool live = lj != -INFINITY;  // not a masked expert, whose score is 0
+    if (!live) g = 0.f;
     float add = 0.f;  // what this slot adds to its expert's gradient
     if (r.renorm) {
       const float m = share_base(r.score, lj, live, kpad);
@@ -415,6 +548,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     const bool leads = live && lane == __ffs(same) - 1;
     if (leads) s_row[warp][row_of][e] = add;
     __syncwarp();
+    lj = (unsigned)e1 < (unsigned)E ? to_float(logits[(t1 + row_of) * stride + e1]) : -INFINITY;
     for (int r0 = 0; r0 < rows && t0 + r0 < T; r0 += kAtOnce) {
       const long long t = t0 + r0 + at_once;
       const bool mine = r0 + at_once < rows && t < T;  // rows of fewer than the lanes hold
@@ -436,6 +570,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3)
     __syncwarp();
     if (leads) s_row[warp][row_of][e] = 0.f;
     __syncwarp();
+    e = e1, g = g1, t0 = t1, rows = rows1;
   }
 }
 
@@ -444,47 +579,36 @@ bool rows_aligned(const void* p, long long stride, size_t size) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (size_t)stride * size % 16 == 0;
 }
 
-int pow2_from(int n) {
-  int p = 1;
-  while (p < n) p <<= 1;
-  return p;
+int log2_from(int n) {  // rounded up
+  int l = 0;
+  while (1 << l < n) ++l;
+  return l;
 }
 
-int lanes_of(int E) { return std::max(4, pow2_from((E + kVals - 1) / kVals)); }
+int lanes_of(int E) { return std::max(4, 1 << log2_from((E + kVals - 1) / kVals)); }
 
-// How many rows a warp takes together, and blocks.
-struct Shape {
-  int rows, kpad, blocks;
-};
+// Route::span
+int span_of(int E, int groups) {
+  const int lanes = E / groups / kVals;
+  return E / groups % kVals == 0 && (lanes & (lanes - 1)) == 0 ? log2_from(lanes) : -1;
+}
 
-Shape shape_of(const Route& r, int T, bool backward) {
-  const int lanes = lanes_of(r.E), at_once = 32 / lanes;
-  Shape s;
-  s.kpad = pow2_from(r.k);
-  const int together = std::min(max_rows(lanes), std::max(1, 32 / s.kpad));
-  auto tasks_of = [&](int rows) { return ((long long)T + rows - 1) / rows; };
-  int cap;
-  if (backward) {
-    // a slot a lane is most of the work: all the rows a warp has lanes for, once
-    // there are several rows for every warp of the device (32768 rows of 256
-    // experts: 12.9 us at 4 rows a warp, 27.6 at 1)
-    s.rows = T > kSms * kWarps * 2 * at_once ? together : std::min(at_once, together);
-    cap = kSms * 8;
-  } else {
-    // three blocks an SM are resident and take rows by turns: the rows together
-    // that give the fullest warp the least to do, its slots costing about a
-    // sixth of a choice each pass (32768 rows of 64 experts: 14.5 us so, 16.5
-    // with as many blocks as there is work for)
-    cap = kSms * 3;
-    s.rows = at_once;
-    float least = INFINITY;
-    for (int rows = at_once; rows <= std::max(at_once, together); rows *= 2) {
-      const long long passes = (tasks_of(rows) + cap * kWarps - 1) / (cap * kWarps);
-      const float cost = (float)passes * ((float)rows / at_once + 0.17f);
-      if (cost < least) least = cost, s.rows = rows;
-    }
-  }
-  s.blocks = (int)std::min<long long>((tasks_of(s.rows) + kWarps - 1) / kWarps, cap);
+// The resident warps share the rows, to within one unit of each other, so that
+// each weighs the slots of its few rows together and all end at about the same
+// time: 8192 rows of 256 grouped experts 14.4 us, 16.5 with a grid's stride of
+// single rows; 32768 of 64 experts 12.8 and 14.4.
+Share split_of(const Route& r, int T, bool backward, int* blocks) {
+  const int lanes = lanes_of(r.E);
+  Share s;
+  s.klog = log2_from(r.k);
+  // as many rows together as have a lane for each slot; the choice takes all the
+  // rows that a warp holds even so
+  const int together = std::min(max_rows(lanes), 32 >> s.klog);
+  s.unit = backward ? std::min(32 / lanes, together) : 32 / lanes;
+  s.units = std::max(1, together / s.unit);
+  const int units = (int)(((long long)T + s.unit - 1) / s.unit);
+  *blocks = std::min((units + kWarps - 1) / kWarps, kSms * (backward ? kBackward : kForward));
+  s.base = units / (*blocks * kWarps), s.extra = units % (*blocks * kWarps);
   return s;
 }
 
@@ -557,7 +681,8 @@ moe_router_t* moe_router_create(int E, int k, int score, int groups, int groups_
     moe::set_error(MOE_E_NOMEM, "out of host memory");
     return nullptr;
   }
-  h->r = Route{E, k, score, groups, groups_kept, group_score, renormalise, scale};
+  h->r = Route{E, k, score, groups, groups_kept, group_score, renormalise, scale,
+               span_of(E, groups)};
   moe::clear_error();
   return h;
 }
@@ -572,8 +697,9 @@ int moe_router_forward(const moe_router_t* h, int T, const void* logits, int log
   if (!aligned4(bias) || !aligned4(idx) || !aligned4(w) || !aligned4(counts))
     return moe::set_error(MOE_E_INVAL, "bias, idx, w and counts must be 4-byte aligned");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Shape shape = shape_of(h->r, T, false);
-  if (counts && shape.blocks != 1) {  // a single block writes its counts, more add theirs
+  int blocks = 0;
+  const Share share = T ? split_of(h->r, T, false, &blocks) : Share{};
+  if (counts && blocks != 1) {  // a single block writes its counts, more add theirs
     cudaError_t e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * h->r.E, s);
     if (e != cudaSuccess) return moe::set_cuda_error(e, "cudaMemsetAsync");
   }
@@ -583,8 +709,7 @@ int moe_router_forward(const moe_router_t* h, int T, const void* logits, int log
     constexpr int LANES = decltype(n)::value;
     const L* p = static_cast<const L*>(logits);
     const bool vec = h->r.E % kVals == 0 && rows_aligned(p, row_stride, sizeof(L));
-    return launch(vec ? route_forward<L, LANES, true> : route_forward<L, LANES, false>, shape.blocks, s, h->r, T,
-                  shape.rows, shape.kpad, p, row_stride, bias, static_cast<int*>(idx), w, static_cast<int*>(counts));
+    return launch(vec ? route_forward<L, LANES, true> : route_forward<L, LANES, false>, blocks, s, h->r, T, share, p, row_stride, bias, static_cast<int*>(idx), w, static_cast<int*>(counts));
   };
   cudaError_t e = logits_type == MOE_TYPE_F32 ? by_lanes<float>(h->r.E, go) : by_lanes<__nv_bfloat16>(h->r.E, go);
   return e == cudaSuccess ? MOE_OK : moe::set_cuda_error(e, "route_forward");
@@ -602,7 +727,8 @@ int moe_router_backward(const moe_router_t* h, int T, const void* logits, int lo
   if (grad_row_stride < h->r.E)
     return moe::set_error(MOE_E_INVAL, "rows of grad_logits overlap: the row stride is below E");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const Shape shape = shape_of(h->r, T, true);
+  int blocks;
+  const Share share = split_of(h->r, T, true, &blocks);
   auto go = [&](auto l, auto n) {
     using L = decltype(l);
     constexpr int LANES = decltype(n)::value;
@@ -610,8 +736,7 @@ int moe_router_backward(const moe_router_t* h, int T, const void* logits, int lo
     L* g = static_cast<L*>(grad_logits);
     const bool vec = h->r.E % kVals == 0 && rows_aligned(p, row_stride, sizeof(L)) &&
                      rows_aligned(g, grad_row_stride, sizeof(L));
-    return launch(vec ? route_backward<L, LANES, true> : route_backward<L, LANES, false>, shape.blocks, s, h->r, T,
-                  shape.rows, shape.kpad, p, row_stride, static_cast<const int*>(idx), grad_w, g, grad_row_stride);
+    return launch(vec ? route_backward<L, LANES, true> : route_backward<L, LANES, false>, blocks, s, h->r, T, share, p, row_stride, static_cast<const int*>(idx), grad_w, g, grad_row_stride);
   };
   cudaError_t e = logits_type == MOE_TYPE_F32 ? by_lanes<float>(h->r.E, go) : by_lanes<__nv_bfloat16>(h->r.E, go);
   return e == cudaSuccess ? MOE_OK : moe::set_cuda_error(e, "route_backward");

@@ -131,6 +131,39 @@ def test_ties_go_to_the_lower_expert_and_extremes_stay_finite(score, renorm):
     check(r, l)
 
 
+@pytest.mark.parametrize("E,k", [(256, 8), (256, 16), (130, 5), (100, 16), (64, 6), (60, 16), (32, 3), (20, 16), (7, 7)])
+def test_rows_of_many_equal_logits(E, k):
+    """From no candidate beyond k to all experts alike, rows of both beside each
+    other in a warp."""
+    rng = np.random.default_rng(E + k)
+    l = rng.integers(0, 4, (61, E)).astype(np.float64)
+    l[::7] = rng.permuted(np.tile(np.arange(float(E)), (len(l[::7]), 1)), axis=1)   # none alike
+    l[1::7] = 0.5                                                                  # all alike
+    l[2::7, : E // 2] = -np.inf
+    l[3::7, k // 2 :] = -np.inf                                                    # fewer than k
+    l[4::7] = np.sort(l[4::7], axis=1)                                             # the best in a few lanes
+    l[5::7] = np.arange(float(E))
+    check(settings(E, k), l)
+
+
+@pytest.mark.parametrize("E,groups", [(256, 32), (256, 16), (256, 8), (256, 2), (64, 4), (128, 16), (24, 3), (96, 4),
+                                      (192, 8), (200, 5), (32, 2)])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_groups_of_whole_lanes_and_others(E, groups, group_score):
+    rng = np.random.default_rng(E + groups)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32).astype(np.float64)
+    kept = max(1, groups // 2)
+    k = min(6, E // groups * kept)
+    for biased in (False, True):
+        for score in ("softmax", "sigmoid"):
+            r = settings(E, k, score, groups, kept, group_score)
+            b = bias if biased else None
+            check(r, ref.clear_logits(rng, 19, r, b, masked=0.3), b)
+    # equal groups: the lower ones are kept
+    r = settings(E, k, "sigmoid", groups, kept, group_score)
+    check(r, np.zeros((3, E)))
+
+
 def test_nan_and_infinite_logits_show():
     l = np.zeros((3, 40))
     l[0, 9] = np.nan
