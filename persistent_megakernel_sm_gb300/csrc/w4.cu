@@ -8,6 +8,7 @@
 // are no zero points.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -202,10 +203,11 @@ constexpr int kBlocksSm = 2;
 constexpr int kSms = 152;
 constexpr int kInline = 32;           // slots up to which every block lists the experts' rows itself
 // Mean token rows of an expert from which the tile kernels run: on 128 experts
-// of 2048 x 768, 94 us (small) against 96 at 6 rows, 110 against 97 at 7; on 8 of
-// 4096 x 14336, 156 against 156 at 5 and 172 against 157 at 6; on 64 of 4096 x
-// 1408, 136 against 137 at 6 and 163 against 138 at 7.5.
-constexpr int kTileMinRows = 6;
+// of 2048 x 768, 92 us (small) against 102 at 6 rows, 113 against 102 at 8; on 8
+// of 4096 x 14336, 167 against 172 at 6 and 186 against 172 at 8.
+constexpr int kTileMinRows = 7;
+// Partial sums of a pass (slots times K splits) up to which the last item of a
+// column tile adds them: more are added sooner by a kernel of their own.
 constexpr int kFewSums = 64;
 constexpr int kMaxSplit = 16;         // K splits of the down product
 constexpr uint32_t kScaleX = 0x5f805f80u, kScaleX16 = 0x5d805d80u;  // 2^64, 2^60 twice
@@ -223,6 +225,8 @@ struct Experts {
   // rows], the last four tiles of an expert filled up
   const uint4* scales[2];
   const uint2* zeros[2];
+  const uint4* tile_scales; // gate/up's in fp16, each row's divided by the power of two in exps (large batches)
+  const short2* exps;       // [(E + S) f] of gate and up
   const __nv_bfloat16* x;   // [T, d]
   const int* idx;           // [T, k]
   const float* w;           // [T, k]
@@ -234,7 +238,8 @@ struct Experts {
   int* status;              // MOE_E_TIMEOUT if a wait ran out
   void* list;               // List and Rows of a batch of more than kInline slots
   uint16_t *list_slot, *list_row;
-  __nv_bfloat16* xg;        // [T k + T S, d] x in the order of the list (large batches)
+  __half* xg;               // [T k + T S, d] x in the order of the list, in fp16 (large batches)
+  int* x_exp;               // [T k + T S] the power of two that each of its rows was divided by
   __nv_bfloat16* out;       // [T, d]
 };
 
@@ -860,12 +865,14 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
   }
 }
 
+#include "w4_tiles.cuh"
+
 // Arrange scales and zero points once as the units take them: one thread per
 // lane and group of a unit.  first, second: the matrices of a unit's first and
 // last 32 rows (gate and up; down twice, both32 = 0).
 __global__ void __launch_bounds__(256)
     w4_arrange(Weight first, Weight second, int both32, int experts, int row_tiles, int blocks_k, int kg,
-               uint4* scales, uint2* zeros) {
+               uint4* scales, uint2* zeros, uint4* tile_scales, const short2* exps) {
   const int fours = (row_tiles + 3) / 4;
   const long long units = (long long)experts * fours * blocks_k * 4;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < units * 8 * kg; i += (long long)gridDim.x * 256) {
@@ -883,16 +890,23 @@ __global__ void __launch_bounds__(256)
       uint2 q;
       uint8_t b[8];
     } z;
+    union {
+      uint4 q;
+      __half h[8];
+    } t;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const Weight& m = r < 4 ? first : second;
       const long long row =
           (four / fours * row_tiles + tile) * (both32 ? 32 : kRows) + (both32 ? (r & 3) * 8 : r * 8) + g;
       const long long o = (row * blocks_k + kb) * kg + grp;
-      s.b[r] = __float2bfloat16(__bfloat162float(m.scales[o]) * kScaleUp);  // exact
+      const float v = __bfloat162float(m.scales[o]);
+      s.b[r] = __float2bfloat16(v * kScaleUp);  // exact
+      if (tile_scales) t.h[r] = __float2half_rn(times_two_to(v, kScaleTop - (r < 4 ? exps[row].x : exps[row].y)));
       if (zeros) z.b[r] = m.zeros[o] & 15;
     }
     scales[i] = s.q;
+    if (tile_scales) tile_scales[i] = t.q;
     if (zeros) zeros[i] = z.q;
   }
 }
@@ -911,8 +925,6 @@ __global__ void __launch_bounds__(128) w4_combine(const Experts a) {
   r.b[1] = __floats2bfloat162_rn(o.z, o.w);
   *reinterpret_cast<uint2*>(a.out + (size_t)t * a.d + col) = r.u;
 }
-
-#include "w4_tiles.cuh"
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -958,7 +970,7 @@ struct Run {
 
 // The workspace's regions, offsets from its start; h is first.
 struct Layout {
-  size_t y, xg, status, arrived, list, slot, row, bytes;
+  size_t y, xg, x_exp, status, arrived, list, slot, row, bytes;
 };
 
 }  // namespace
@@ -1055,7 +1067,8 @@ Layout layout(const moe_w4* h, int T_max) {
   Layout l;
   l.y = up(slots * h->f * 2);
   l.xg = l.y + up(y);
-  l.status = l.xg + up(slots * h->d * 2);
+  l.x_exp = l.xg + up(slots * h->d * 2);
+  l.status = l.x_exp + up(slots * 4);
   l.arrived = l.status + 256;
   l.list = l.arrived + up((size_t)h->d / kRows * 4);
   l.slot = l.list + up(sizeof(List));
@@ -1064,10 +1077,10 @@ Layout layout(const moe_w4* h, int T_max) {
   return l;
 }
 
-// The copies that moe_w4_set_weights makes: gate/up's scales, down's, and the
-// zero points of both.
+// The copies that moe_w4_set_weights makes: gate/up's scales, down's, gate/up's
+// for the tile kernels and its rows' exponents, and the zero points of both.
 struct Arranged {
-  size_t down, zeros, zeros_down, bytes;
+  size_t down, tile, exps, zeros, zeros_down, bytes;
 };
 
 // Fours of row tiles of an expert: 128 rows of gate and up, 256 of down.
@@ -1076,7 +1089,14 @@ int fours(const moe_w4* h, bool down) { return down ? (h->d + 255) / 256 : h->f 
 Arranged arranged(const moe_w4* h) {
   const size_t n = (size_t)(h->E + h->S) * 256 / h->group;  // scales of a four and a column
   const size_t gate_up = n * fours(h, false) * h->d, down = n * fours(h, true) * h->f;
-  return Arranged{2 * gate_up, 2 * (gate_up + down), 2 * (gate_up + down) + gate_up, 3 * (gate_up + down)};
+  Arranged at;  // every size is a multiple of 256 bytes
+  at.down = 2 * gate_up;
+  at.tile = at.down + 2 * down;
+  at.exps = at.tile + 2 * gate_up;
+  at.zeros = at.exps + (size_t)(h->E + h->S) * h->f * sizeof(short2);
+  at.zeros_down = at.zeros + gate_up;
+  at.bytes = at.zeros_down + down;
+  return at;
 }
 
 // Every kernel of a pass may be launched before the one in front of it has
@@ -1270,13 +1290,17 @@ int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weig
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int kg = kBlockK / h->group;
   const bool z = gate->zeros != nullptr;
-  cudaError_t e = cudaSuccess;
+  short2* exps = reinterpret_cast<short2*>(h->arranged + at.exps);
+  const long long rows = (long long)(h->E + h->S) * h->f;
+  cudaError_t e = launch(w4_row_exponents, dim3((unsigned)((rows + 7) / 8)), 256, s, take(gate).scales, take(up).scales, rows,
+                         h->d / h->group, exps);
   for (int d = 0; d < 2 && e == cudaSuccess; ++d) {
     const int row_tiles = d ? h->d / kRows : h->f / 32, blocks_k = (d ? h->f : h->d) / kBlockK;
     const long long units = (long long)(h->E + h->S) * fours(h, d) * blocks_k * 4;
     e = launch(w4_arrange, dim3((unsigned)std::min<long long>((units * 8 * kg + 255) / 256, kSms * 8)), 256, s, take(d ? down : gate), take(d ? down : up), 1 - d,
                h->E + h->S, row_tiles, blocks_k, kg, reinterpret_cast<uint4*>(h->arranged + (d ? at.down : 0)),
-               z ? reinterpret_cast<uint2*>(h->arranged + (d ? at.zeros_down : at.zeros)) : nullptr);
+               z ? reinterpret_cast<uint2*>(h->arranged + (d ? at.zeros_down : at.zeros)) : nullptr,
+               d ? nullptr : reinterpret_cast<uint4*>(h->arranged + at.tile), static_cast<const short2*>(exps));
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "w4_arrange");
   const uint64_t n = h->E + h->S;
@@ -1323,12 +1347,15 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   a.scales[1] = reinterpret_cast<const uint4*>(h->arranged + at.down);
   a.zeros[0] = reinterpret_cast<const uint2*>(h->arranged + at.zeros);
   a.zeros[1] = reinterpret_cast<const uint2*>(h->arranged + at.zeros_down);
+  a.tile_scales = reinterpret_cast<const uint4*>(h->arranged + at.tile);
+  a.exps = reinterpret_cast<const short2*>(h->arranged + at.exps);
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.idx = idx;
   a.w = w;
   a.h = reinterpret_cast<__nv_bfloat16*>(h->ws);
   a.y = reinterpret_cast<float*>(h->ws + l.y);
-  a.xg = reinterpret_cast<__nv_bfloat16*>(h->ws + l.xg);
+  a.xg = reinterpret_cast<__half*>(h->ws + l.xg);
+  a.x_exp = reinterpret_cast<int*>(h->ws + l.x_exp);
   // few partial sums: the last item of a column tile adds them, and no third
   // kernel follows (one token of the eight-expert layer 44.1 -> 42.9 us)
   const bool few = !r.tokens && T * (h->k + h->S) * r.down.splits <= kFewSums;

@@ -359,6 +359,42 @@ def test_magnitudes_at_the_ends_of_the_range():
         c.checked()
 
 
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_magnitudes_within_rows(T, zeros):
+    """Scales 2^20 apart within a weight row and 2^6 between rows, values 2^16
+    apart within a token row and 2^8 between rows, a row of zeros and one of
+    subnormal numbers.  |gate|, |up| are under 2^(14 + 12 + 3), so h is in the
+    range that the operator takes (2^64)."""
+    c = Case(T, 256, 2, 1, 384, 0, 32, zeros, seed=T)
+    rng = np.random.default_rng(T)
+    for name in ("gate", "up", "down"):
+        codes, scales, z = getattr(c, name)
+        scales = scales * 2.0 ** rng.integers(-10, 11, scales.shape)
+        scales = scales * 2.0 ** rng.integers(-3, 4, scales.shape[:-1])[..., None]
+        setattr(c, name, (codes, ref.bf16(scales), z))
+    c.x = c.x * 2.0 ** rng.integers(-8, 9, c.x.shape) * 2.0 ** rng.integers(-4, 5, (T, 1))
+    if T > 2:
+        c.x[3] = 0.0
+        c.x[4] = 2.0 ** -133 * rng.integers(-100, 101, 256)
+    c.x = ref.bf16(c.x)
+    got = c.run()
+    want, off = ref.experts(c.x, c.idx, c.w.astype(np.float64), c.gate, c.up, c.down, 2, 0)
+    assert np.all(np.abs(got - want) <= off + 2.0 ** -60)
+
+
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+@pytest.mark.parametrize("T", [3, 40])
+def test_a_row_that_is_not_finite_stays_its_own(T, bad):
+    c = Case(T, 256, 2, 1, 128, 1, 64, False, seed=T)
+    c.x[1, 77] = bad
+    got = c.run()
+    assert np.all(~np.isfinite(got[1]))
+    keep = np.arange(T) != 1
+    want, off = ref.experts(c.x[keep], c.idx[keep], c.w[keep].astype(np.float64), c.gate, c.up, c.down, 2, 1)
+    assert np.all(np.abs(got[keep] - want) <= off)
+
+
 def test_weights_replaced():
     import torch
     a, b = Case(9, 128, 4, 2, 256, 0, 64, True, seed=1), Case(9, 128, 4, 2, 256, 0, 64, False, seed=2)
