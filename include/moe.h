@@ -438,12 +438,12 @@ int moe_w4_dequantize(long long rows, int cols, int group, const void* codes, co
  * (idx, w) of moe_router_forward or of moe_layer_get_routing,
  *   h       = bf16( silu(Wg[e] x_t) * (Wu[e] x_t) )
  *   out[t]  = bf16( sum_j w[t,j] Wd[e_j] h_j  +  shared expert's, weight 1 )
- * with the weights' 4-bit values and fp32 sums.  (From a mean of 7 rows an
- * expert on, the kernels for larger batches round gate's and up's weights to 11
- * bits and down's to bf16, as moe_w4_dequantize does; with fewer no weight is
- * rounded.)  Magnitudes of x and h are taken to lie below 2^64, those below
- * 2^-57 count as zero; scales between 2^-86 and 2^31, or 0.  In larger batches
- * scales under 2^-24 of their row's largest lose bits.  Slots with idx outside
+ * with the weights' 4-bit values and fp32 sums.  (From a mean of 9 rows an
+ * expert on, the kernels for larger batches round each weight to 11 bits; with
+ * fewer no weight is rounded.)  Magnitudes of x and h are taken to lie below
+ * 2^64, those below 2^-57 count as zero; scales between 2^-86 and 2^31, or 0.
+ * In larger batches a scale under 2^-24 of its weight row's largest, and a value
+ * of x or h under 2^-29 of its token row's, lose bits.  Slots with idx outside
  * [0, E) add nothing (the rows behind a padded batch's last sequence: idx -1);
  * an expert named twice by a row counts twice.  Shapes: gate and up
  * [E + S, f, d], down [E + S, d, f] (groups along the last axis), the shared

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(256)
 // --------------------------------------------------------------------- experts
 //
 // Two kernels, gate/up then down, of the same shape, and a third that adds the
-// slots of a token.  An item is 64 weight rows of one expert (gate/up: 32 of
+// slots of a token (with few of them the last item of a column tile does).  An item is 64 weight rows of one expert (gate/up: 32 of
 // each) times up to 8 of the expert's token rows; a team of 1, 2, 4 or 8 warps
 // works an item off, its warps taking the 128-column blocks of the product in
 // turn, and its first warp adds the others' sums.  Blocks of eight warps stay
@@ -202,10 +202,11 @@ constexpr int kItemWarps = 8;
 constexpr int kBlocksSm = 2;
 constexpr int kSms = 152;
 constexpr int kInline = 32;           // slots up to which every block lists the experts' rows itself
-// Mean token rows of an expert from which the tile kernels run: on 128 experts
-// of 2048 x 768, 92 us (small) against 102 at 6 rows, 113 against 102 at 8; on 8
-// of 4096 x 14336, 167 against 172 at 6 and 186 against 172 at 8.
-constexpr int kTileMinRows = 7;
+// Mean token rows of an expert from which the tile kernels run.  The small
+// kernels take 8 rows at once; on 128 experts of 2048 x 768, 113 us (small)
+// against 115 at 8 rows, 121 against 120 at 9; on 8 of 4096 x 14336, 186 against
+// 189 at 8 and 228 against 190 at 9.
+constexpr int kTileMinRows = 9;
 // Partial sums of a pass (slots times K splits) up to which the last item of a
 // column tile adds them: more are added sooner by a kernel of their own.
 constexpr int kFewSums = 64;
@@ -225,21 +226,25 @@ struct Experts {
   // rows], the last four tiles of an expert filled up
   const uint4* scales[2];
   const uint2* zeros[2];
-  const uint4* tile_scales; // gate/up's in fp16, each row's divided by the power of two in exps (large batches)
-  const short2* exps;       // [(E + S) f] of gate and up
+  // large batches: the scales in fp16, each row's divided by the power of two in
+  // exps, of gate, up and down
+  const uint4* tile_scales[2];
+  const short* exps[3];
   const __nv_bfloat16* x;   // [T, d]
   const int* idx;           // [T, k]
   const float* w;           // [T, k]
-  // [T k + T S, f], columns of each 8 in the order 0 4 1 5 2 6 3 7, scaled as
-  // the product takes them
+  // [T k + T S, f], columns of each 8 in the order 0 4 1 5 2 6 3 7 and scaled as
+  // the product takes them; as they are in large batches
   __nv_bfloat16* h;
   float* y;                 // [splits, T k + T S, d]
   int* arrived;             // [d / 64] items of a column tile done, zero between passes; null: w4_combine adds
   int* status;              // MOE_E_TIMEOUT if a wait ran out
   void* list;               // List and Rows of a batch of more than kInline slots
   uint16_t *list_slot, *list_row;
-  __half* xg;               // [T k + T S, d] x in the order of the list, in fp16 (large batches)
-  int* x_exp;               // [T k + T S] the power of two that each of its rows was divided by
+  // large batches: x [T k + T S, d] in the order of the list and h, in fp16, and
+  // the powers of two that their rows were divided by
+  __half *x16, *h16;
+  int *x_exp, *h_exp;
   __nv_bfloat16* out;       // [T, d]
 };
 
@@ -872,7 +877,8 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
 // last 32 rows (gate and up; down twice, both32 = 0).
 __global__ void __launch_bounds__(256)
     w4_arrange(Weight first, Weight second, int both32, int experts, int row_tiles, int blocks_k, int kg,
-               uint4* scales, uint2* zeros, uint4* tile_scales, const short2* exps) {
+               uint4* scales, uint2* zeros, uint4* tile_scales, const short* exps_first,
+               const short* exps_second) {
   const int fours = (row_tiles + 3) / 4;
   const long long units = (long long)experts * fours * blocks_k * 4;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < units * 8 * kg; i += (long long)gridDim.x * 256) {
@@ -902,11 +908,11 @@ __global__ void __launch_bounds__(256)
       const long long o = (row * blocks_k + kb) * kg + grp;
       const float v = __bfloat162float(m.scales[o]);
       s.b[r] = __float2bfloat16(v * kScaleUp);  // exact
-      if (tile_scales) t.h[r] = __float2half_rn(times_two_to(v, kScaleTop - (r < 4 ? exps[row].x : exps[row].y)));
+      t.h[r] = __float2half_rn(times_two_to(v, kScaleTop - (r < 4 ? exps_first : exps_second)[row]));
       if (zeros) z.b[r] = m.zeros[o] & 15;
     }
     scales[i] = s.q;
-    if (tile_scales) tile_scales[i] = t.q;
+    tile_scales[i] = t.q;
     if (zeros) zeros[i] = z.q;
   }
 }
@@ -970,7 +976,7 @@ struct Run {
 
 // The workspace's regions, offsets from its start; h is first.
 struct Layout {
-  size_t y, xg, x_exp, status, arrived, list, slot, row, bytes;
+  size_t y, x16, h16, x_exp, h_exp, status, arrived, list, slot, row, bytes;
 };
 
 }  // namespace
@@ -1066,9 +1072,11 @@ Layout layout(const moe_w4* h, int T_max) {
   for (int T = 1; T <= T_max; ++T) y = std::max(y, (size_t)T * (h->k + h->S) * h->d * 4 * run_of(h, T).down.splits);
   Layout l;
   l.y = up(slots * h->f * 2);
-  l.xg = l.y + up(y);
-  l.x_exp = l.xg + up(slots * h->d * 2);
-  l.status = l.x_exp + up(slots * 4);
+  l.x16 = l.y + up(y);
+  l.h16 = l.x16 + up(slots * h->d * 2);
+  l.x_exp = l.h16 + up(slots * h->f * 2);
+  l.h_exp = l.x_exp + up(slots * 4);
+  l.status = l.h_exp + up(slots * 4);
   l.arrived = l.status + 256;
   l.list = l.arrived + up((size_t)h->d / kRows * 4);
   l.slot = l.list + up(sizeof(List));
@@ -1077,10 +1085,10 @@ Layout layout(const moe_w4* h, int T_max) {
   return l;
 }
 
-// The copies that moe_w4_set_weights makes: gate/up's scales, down's, gate/up's
-// for the tile kernels and its rows' exponents, and the zero points of both.
+// The copies that moe_w4_set_weights makes: gate/up's scales and down's, the same
+// for the tile kernels with the rows' exponents, and the zero points of both.
 struct Arranged {
-  size_t down, tile, exps, zeros, zeros_down, bytes;
+  size_t down, tile, tile_down, exps[3], zeros, zeros_down, bytes;
 };
 
 // Fours of row tiles of an expert: 128 rows of gate and up, 256 of down.
@@ -1092,8 +1100,11 @@ Arranged arranged(const moe_w4* h) {
   Arranged at;  // every size is a multiple of 256 bytes
   at.down = 2 * gate_up;
   at.tile = at.down + 2 * down;
-  at.exps = at.tile + 2 * gate_up;
-  at.zeros = at.exps + (size_t)(h->E + h->S) * h->f * sizeof(short2);
+  at.tile_down = at.tile + 2 * gate_up;
+  at.exps[0] = at.tile_down + 2 * down;
+  at.exps[1] = at.exps[0] + (size_t)(h->E + h->S) * h->f * sizeof(short);
+  at.exps[2] = at.exps[1] + (size_t)(h->E + h->S) * h->f * sizeof(short);
+  at.zeros = at.exps[2] + (size_t)(h->E + h->S) * h->d * sizeof(short);
   at.zeros_down = at.zeros + gate_up;
   at.bytes = at.zeros_down + down;
   return at;
@@ -1129,7 +1140,7 @@ bool encode_codes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t byte
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 rows [rows, cols]: boxes of 64 columns x box_rows, 128-byte swizzle.
+// 16-bit rows [rows, cols]: boxes of 64 columns x box_rows, 128-byte swizzle.
 bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * 2};
@@ -1262,8 +1273,8 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
   if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_reserve");
   const uint64_t slots = (uint64_t)T_max * (h->k + h->S);
   for (uint32_t n = 0; n < kTileTokens / 32; ++n)
-    if (!encode_rows(&h->x_maps[n], h->ws + l.xg, slots, h->d, 32 * n + 32) ||
-        !encode_rows(&h->h_maps[n], h->ws, slots, h->f, 32 * n + 32))
+    if (!encode_rows(&h->x_maps[n], h->ws + l.x16, slots, h->d, 32 * n + 32) ||
+        !encode_rows(&h->h_maps[n], h->ws + l.h16, slots, h->f, 32 * n + 32))
       return moe::set_error(MOE_E_INVAL, "tensor map encoding failed");
   h->l = l;
   h->T_max = T_max;
@@ -1290,17 +1301,23 @@ int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weig
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int kg = kBlockK / h->group;
   const bool z = gate->zeros != nullptr;
-  short2* exps = reinterpret_cast<short2*>(h->arranged + at.exps);
-  const long long rows = (long long)(h->E + h->S) * h->f;
-  cudaError_t e = launch(w4_row_exponents, dim3((unsigned)((rows + 7) / 8)), 256, s, take(gate).scales, take(up).scales, rows,
-                         h->d / h->group, exps);
+  cudaError_t e = cudaSuccess;
+  short* exps[3];
+  for (int i = 0; i < 3; ++i) {
+    exps[i] = reinterpret_cast<short*>(h->arranged + at.exps[i]);
+    const long long rows = (long long)(h->E + h->S) * (i < 2 ? h->f : h->d);
+    if (e == cudaSuccess)
+      e = launch(w4_row_exponents, dim3((unsigned)((rows + 7) / 8)), 256, s, take(m[i]).scales, rows,
+                 (i < 2 ? h->d : h->f) / h->group, exps[i]);
+  }
   for (int d = 0; d < 2 && e == cudaSuccess; ++d) {
     const int row_tiles = d ? h->d / kRows : h->f / 32, blocks_k = (d ? h->f : h->d) / kBlockK;
     const long long units = (long long)(h->E + h->S) * fours(h, d) * blocks_k * 4;
     e = launch(w4_arrange, dim3((unsigned)std::min<long long>((units * 8 * kg + 255) / 256, kSms * 8)), 256, s, take(d ? down : gate), take(d ? down : up), 1 - d,
                h->E + h->S, row_tiles, blocks_k, kg, reinterpret_cast<uint4*>(h->arranged + (d ? at.down : 0)),
                z ? reinterpret_cast<uint2*>(h->arranged + (d ? at.zeros_down : at.zeros)) : nullptr,
-               d ? nullptr : reinterpret_cast<uint4*>(h->arranged + at.tile), static_cast<const short2*>(exps));
+               reinterpret_cast<uint4*>(h->arranged + (d ? at.tile_down : at.tile)),
+               static_cast<const short*>(exps[d ? 2 : 0]), static_cast<const short*>(exps[d ? 2 : 1]));
   }
   if (e != cudaSuccess) return moe::set_cuda_error(e, "w4_arrange");
   const uint64_t n = h->E + h->S;
@@ -1347,15 +1364,18 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
   a.scales[1] = reinterpret_cast<const uint4*>(h->arranged + at.down);
   a.zeros[0] = reinterpret_cast<const uint2*>(h->arranged + at.zeros);
   a.zeros[1] = reinterpret_cast<const uint2*>(h->arranged + at.zeros_down);
-  a.tile_scales = reinterpret_cast<const uint4*>(h->arranged + at.tile);
-  a.exps = reinterpret_cast<const short2*>(h->arranged + at.exps);
+  a.tile_scales[0] = reinterpret_cast<const uint4*>(h->arranged + at.tile);
+  a.tile_scales[1] = reinterpret_cast<const uint4*>(h->arranged + at.tile_down);
+  for (int i = 0; i < 3; ++i) a.exps[i] = reinterpret_cast<const short*>(h->arranged + at.exps[i]);
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.idx = idx;
   a.w = w;
   a.h = reinterpret_cast<__nv_bfloat16*>(h->ws);
   a.y = reinterpret_cast<float*>(h->ws + l.y);
-  a.xg = reinterpret_cast<__half*>(h->ws + l.xg);
+  a.x16 = reinterpret_cast<__half*>(h->ws + l.x16);
+  a.h16 = reinterpret_cast<__half*>(h->ws + l.h16);
   a.x_exp = reinterpret_cast<int*>(h->ws + l.x_exp);
+  a.h_exp = reinterpret_cast<int*>(h->ws + l.h_exp);
   // few partial sums: the last item of a column tile adds them, and no third
   // kernel follows (one token of the eight-expert layer 44.1 -> 42.9 us)
   const bool few = !r.tokens && T * (h->k + h->S) * r.down.splits <= kFewSums;
@@ -1374,8 +1394,9 @@ int moe_w4_forward(moe_w4_t* h, int T, const void* x, const int32_t* idx, const 
     const int smem = tile_smem(r.tokens, h->group, h->zeros).bytes;
     h->tile_maps.x = h->x_maps[r.tokens / 32 - 1];
     h->tile_maps.h = h->h_maps[r.tokens / 32 - 1];
-    if (e == cudaSuccess) e = launch_after(w4_gather, dim3(T * (h->k + h->S)), 128, 0, s, a);
+    if (e == cudaSuccess) e = launch_after(w4_rows<false>, dim3(T * (h->k + h->S)), 256, 0, s, a);
     if (e == cudaSuccess) e = launch_after(kn.tiles_gate_up, dim3(kSms), kTileThreads, smem, s, a, h->tile_maps);
+    if (e == cudaSuccess) e = launch_after(w4_rows<true>, dim3(T * (h->k + h->S)), 256, 0, s, a);
     if (e == cudaSuccess) e = launch_after(kn.tiles_down, dim3(kSms), kTileThreads, smem, s, a, h->tile_maps);
   } else {
     const dim3 grid(kSms * kBlocksSm);

@@ -17,29 +17,22 @@
 // 200 cycles even when it is ready, an MMA of any width 30 to 60 to issue.  So
 // the loops look one step ahead and convert before they wait.
 //
-// A code q as an operand, gate and up: the bits 0x6400 + q (0x5400 + 16 q, for
-// every other pair) are the fp16 number 1024 + q (64 + q), so a subtraction
-// gives q - zero, exact, and a multiply (q - zero) scale, rounded to 11 bits.
-// For fp16's range, each weight row's scales are divided by a power of two (the
-// largest one's), each token row's values too, and the sums multiplied back:
-// what is lost lies under 2^-35 of a row's largest scale and 2^-39 of a token's
-// largest value.
+// A code q as an operand: the bits 0x6400 + q (0x5400 + 16 q, for every other
+// pair) are the fp16 number 1024 + q (64 + q), so a subtraction gives q - zero,
+// exact, and a multiply (q - zero) scale, rounded to 11 bits.  (Scaling the sums
+// instead, which rounds nothing, would cost one fp32 operation per row, token and
+// group, as many as the conversion itself at 64 tokens; in bf16 a conversion is
+// 5 + 4 instructions and 256 tokens of the eight-expert layer took 189 us in place
+// of 224, but the output was off by 3.4e-3 of its norm in place of 2.4e-3, of
+// which 1.7e-3 are its own rounding to bf16 and as much h's.)  For fp16's range, each weight row's
+// scales are divided by a power of two, the largest one's, and each row of x and
+// of h too, by kernels of their own (w4_row_exponents once, w4_rows in every
+// pass); the sums are multiplied back.  Scales under 2^-24 of their row's
+// largest, and values under 2^-29 of theirs, lose bits.
 //
-// Down: h has no such factor before all of its row is known, so its product is
-// in bf16.  The bits n = q (or 16 q) are the bf16 number n 2^-133, and one bf16
-// fused multiply-add with scale * 2^96 (2^92) and -8 scale 2^-37 gives
-// (q - 8) scale 2^-37, rounded once (8 scale is exact); with zero points the
-// subtraction comes first, exact, and the multiply rounds.  So a weight of down
-// is its 4-bit value rounded to bf16 -- what moe_w4_dequantize gives -- where the
-// small-batch kernels round none: scaling the sums instead would cost one fp32
-// operation per row, token and group, as many as the conversion itself at 64
-// tokens.  Against the formula the output is off by 2.8e-3 of its norm, 2.3e-3
-// with the small-batch kernels, 3.4e-3 with both products' weights in bf16, of
-// which 1.7e-3 are its own rounding to bf16.
-//
-// A conversion is 5 + 8 instructions for 8 codes, 5 + 4 in down without zero
-// points.  The tokens' rows are read again for every 256 weight rows, which is
-// why both matrices (or twice the rows) share them.
+// A conversion is 5 + 8 instructions for 8 codes.  The tokens' rows are read
+// again for every 256 weight rows, which is why both matrices (or twice the
+// rows) share them.
 #pragma once
 
 constexpr int kTileTokens = 128;     // at most
@@ -52,7 +45,6 @@ constexpr int kOutWarps = 8;
 constexpr int kTileThreads = (kFirstOut + kOutWarps) * 32;
 // tensor memory: sums [set][tile], operands [tile][buffer][half][32 columns]
 constexpr uint32_t kAColumn = 256;
-constexpr float kTileUnscale = 137438953472.f;  // 2^37
 
 // x gathered by expert, and h: [T k + T S, columns], columns of each 8 in the
 // order 0 4 1 5 2 6 3 7, in the order of the list.
@@ -103,7 +95,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) 
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D (+)= A B^T, A [128 x 16] bf16 in tensor memory (lane = row, 8 columns), B
+// D (+)= A B^T, A [128 x 16] fp16 in tensor memory (lane = row, 8 columns), B
 // in shared memory, K-major.
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, bool add) {
   asm volatile(
@@ -147,25 +139,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Volatile, so that a conversion stays in front of the wait that follows it.
-__device__ __forceinline__ uint32_t fma2v(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm volatile("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t mul2v(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm volatile("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t sub2h(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -179,15 +152,11 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   return r;
 }
 
+// Volatile, so that a conversion stays in front of the wait that follows it.
 __device__ __forceinline__ uint32_t mul2hv(uint32_t a, uint32_t b) {
   uint32_t r;
   asm volatile("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-
-__device__ __forceinline__ uint32_t bf16_twice(float v) {
-  const uint32_t b = __bfloat16_as_ushort(__float2bfloat16(v));
-  return b | b << 16;
 }
 
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 to 127
@@ -206,63 +175,71 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) { return max((int)(bit
 
 constexpr int kScaleTop = 10, kTokenTop = 14;  // a row's largest scale is 2^10 to 2^11, 15 times that in fp16's range
 
-// Per weight row of gate and up the power of two of its largest scale: a warp a row.
+// Per weight row the power of two of its largest scale: a warp a row.
 __global__ void __launch_bounds__(256)
-    w4_row_exponents(const __nv_bfloat16* gate, const __nv_bfloat16* up, long long rows, int groups, short2* exps) {
+    w4_row_exponents(const __nv_bfloat16* scales, long long rows, int groups, short* exps) {
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
-  uint32_t m[2] = {0u, 0u};
-  for (int g = threadIdx.x & 31; g < groups; g += 32) {
-    m[0] = max(m[0], finite_bits(__bfloat16_as_ushort(gate[row * groups + g])));
-    m[1] = max(m[1], finite_bits(__bfloat16_as_ushort(up[row * groups + g])));
-  }
-  m[0] = __reduce_max_sync(0xffffffffu, m[0]);
-  m[1] = __reduce_max_sync(0xffffffffu, m[1]);
-  if ((threadIdx.x & 31) == 0) exps[row] = make_short2((short)exponent_of(m[0]), (short)exponent_of(m[1]));
+  uint32_t m = 0u;
+  for (int g = threadIdx.x & 31; g < groups; g += 32)
+    m = max(m, finite_bits(__bfloat16_as_ushort(scales[row * groups + g])));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) exps[row] = (short)exponent_of(m);
 }
 
-// Token rows in the order of the list, in fp16 with their largest value at 2^14
-// to 2^15: one block a row.
-__global__ void __launch_bounds__(128) w4_gather(Experts a) {
-  constexpr int kKeep = 4;  // loads a thread keeps until the factor is known; more are read again
-  __shared__ uint32_t most[4];
+// The rows of x in the order of the list, or of h (H), as the tiles take them: in
+// fp16 with their largest value at 2^14 to 2^15 (below that if it is under
+// 2^-113).  One block a row; bound by its chain of loads (512 rows of 14336
+// columns 9 us alone).
+template <bool H>
+__global__ void __launch_bounds__(256) w4_rows(Experts a) {
+  constexpr int kKeep = H ? 8 : 4;  // loads a thread keeps until the factor is known; more are read again
+  __shared__ uint32_t most[8];
+  if (H) let_next_kernel_start();  // it has the list already
   wait_for_previous_kernel();
-  let_next_kernel_start();
-  const int pos = blockIdx.x, tid = threadIdx.x;
+  if (!H) let_next_kernel_start();
+  const int pos = blockIdx.x, tid = threadIdx.x, cols = H ? a.f : a.d;
   const List* list = static_cast<const List*>(a.list);
+  const int row = H ? pos : __ldcg(a.list_row + pos);  // whatever it is behind the list's end
   if (pos >= __ldcg(&list->start[__ldcg(&list->n_active)])) return;
-  const uint4* from = reinterpret_cast<const uint4*>(a.x + (size_t)__ldcg(a.list_row + pos) * a.d);
-  uint4* to = reinterpret_cast<uint4*>(a.xg + (size_t)pos * a.d);
-  const int n = a.d / 8;
+  const uint4* from = reinterpret_cast<const uint4*>((H ? a.h : a.x) + (size_t)row * cols);
+  uint4* to = reinterpret_cast<uint4*>((H ? a.h16 : a.x16) + (size_t)pos * cols);
+  const int n = cols / 8;
+  auto words = [](const uint4& v, auto&& f) { f(v.x), f(v.y), f(v.z), f(v.w); };
   uint4 keep[kKeep];
-  uint32_t m = 0u;
-  auto look = [&](const uint4& v) {
-    for (uint32_t w : {v.x, v.y, v.z, v.w}) m = max(m, max(finite_bits(w), finite_bits(w >> 16)));
-  };
 #pragma unroll
-  for (int q = 0; q < kKeep; ++q) keep[q] = tid + q * 128 < n ? __ldg(from + tid + q * 128) : make_uint4(0u, 0u, 0u, 0u);
+  for (int q = 0; q < kKeep; ++q) keep[q] = tid + q * 256 < n ? __ldcg(from + tid + q * 256) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t two = 0u;  // the largest magnitudes of even and of odd columns
+  auto look = [&](uint32_t w) { two = __vmaxu2(two, w & 0x7fff7fffu); };
 #pragma unroll
-  for (int q = 0; q < kKeep; ++q) look(keep[q]);
-  for (int i = tid + kKeep * 128; i < n; i += 128) look(__ldg(from + i));
-  m = __reduce_max_sync(0xffffffffu, m);
+  for (int q = 0; q < kKeep; ++q) words(keep[q], look);
+  for (int i = tid + kKeep * 256; i < n; i += 256) words(__ldcg(from + i), look);
+  uint32_t m = __reduce_max_sync(0xffffffffu, max(two & 0xffffu, two >> 16));
+  if (m >= 0x7f80u) {  // of the finite ones alone
+    m = 0u;
+    auto finite = [&](uint32_t w) { m = max(m, max(finite_bits(w), finite_bits(w >> 16))); };
+    for (int i = tid; i < n; i += 256) words(__ldcg(from + i), finite);
+    m = __reduce_max_sync(0xffffffffu, m);
+  }
   if ((tid & 31) == 0) most[tid >> 5] = m;
   __syncthreads();
-  const int e = exponent_of(max(max(most[0], most[1]), max(most[2], most[3])));
-  if (tid == 0) a.x_exp[pos] = e;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) m = max(m, most[q]);
+  const int e = max(exponent_of(m), kTokenTop - 127);
+  if (tid == 0) (H ? a.h_exp : a.x_exp)[pos] = e;
+  const float factor = two_to(kTokenTop - e);
   auto put = [&](int i, const uint4& v) {
-    // as fp16 in the order of w's two halves, then the columns' order
-    auto two = [&](uint32_t lo, uint32_t hi) {  // bf16 bits in the upper halves
-      const __half2 h = __floats2half2_rn(times_two_to(__uint_as_float(lo), kTokenTop - e),
-                                          times_two_to(__uint_as_float(hi), kTokenTop - e));
+    auto pair = [&](uint32_t lo, uint32_t hi) {  // two numbers' bits in the upper halves
+      const __half2 h = __floats2half2_rn(__uint_as_float(lo) * factor, __uint_as_float(hi) * factor);
       return *reinterpret_cast<const uint32_t*>(&h);
     };
-    to[i] = make_uint4(two(v.x << 16, v.z << 16), two(v.x & 0xffff0000u, v.z & 0xffff0000u), two(v.y << 16, v.w << 16),
-                       two(v.y & 0xffff0000u, v.w & 0xffff0000u));
+    to[i] = make_uint4(pair(v.x << 16, v.z << 16), pair(v.x & 0xffff0000u, v.z & 0xffff0000u), pair(v.y << 16, v.w << 16),
+                       pair(v.y & 0xffff0000u, v.w & 0xffff0000u));
   };
 #pragma unroll
   for (int q = 0; q < kKeep; ++q)
-    if (tid + q * 128 < n) put(tid + q * 128, keep[q]);
-  for (int i = tid + kKeep * 128; i < n; i += 128) put(i, __ldg(from + i));
+    if (tid + q * 256 < n) put(tid + q * 256, keep[q]);
+  for (int i = tid + kKeep * 256; i < n; i += 256) put(i, __ldcg(from + i));
 }
 
 template <bool DOWN, int G, bool Z>
@@ -380,7 +357,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             tma_load(st + sm.codes, DOWN ? &maps.down : &maps.gate, full + s, kb * 64, row);
             tma_load(st + sm.codes + kTileRows * 64, DOWN ? &maps.down : &maps.up, full + s, kb * 64,
                      DOWN ? row + kTileRows : row);
-            bulk_load(smem + s * sm.stage + sm.scales, (DOWN ? a.scales[1] : a.tile_scales) + (unit + kb) * (kScaleBytes / 16), kScaleBytes,
+            bulk_load(smem + s * sm.stage + sm.scales, a.tile_scales[DOWN] + (unit + kb) * (kScaleBytes / 16), kScaleBytes,
                       full + s);
             if (Z)
               bulk_load(smem + s * sm.stage + sm.zeros, a.zeros[DOWN] + (unit + kb) * (kZeroBytes / 8), kZeroBytes,
@@ -410,7 +387,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       TileItem it;
       item_of(i, &at, &it);
       const uint32_t idesc = moe::idesc_bf16(kTileRows, max(16, (__shfl_sync(0xffffffffu, it.rows, 0) + 15) & ~15)) &
-                             (DOWN ? ~0u : ~(1u << 7 | 1u << 10));  // both operands bf16, or both fp16
+                             ~(1u << 7 | 1u << 10);  // both operands fp16
       const int blocks = __shfl_sync(0xffffffffu, it.kb1 - it.kb0, 0);
       const uint32_t d = tm + (set * 2 + t) * sum_columns;
       wait_stage(d_free + set, d_phase, a.status);
@@ -493,12 +470,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int q = (half * 2 + c) * 32 / G;
-            // scale * 2^96 and 2^92 and -8 scale 2^-37, each twice and exact, from
-            // the arranged scale * 2^40
-            const float sf = __uint_as_float(sc[q] << 16);
-            const uint32_t s1 = DOWN ? bf16_twice(sf * 72057594037927936.f) : sc[q] * 0x00010001u;
-            const uint32_t s16 = bf16_twice(sf * 4503599627370496.f);
-            const uint32_t c8 = bf16_twice(sf * -5.293955920339377e-23f);
+            const uint32_t s1 = sc[q] * 0x00010001u;
             const uint32_t z1 = zr[q] * 0x00010001u, z16 = zr[q] * 0x00100010u;
             const uint4 v = w[half * 2 + c];
             const uint32_t words[4] = {v.x, v.y, v.z, v.w};
@@ -506,22 +478,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int k = 0; k < 4; ++k) {
               const uint32_t u = words[k], u8 = u >> 8;
               uint32_t* o = r + c * 16 + k * 4;
-              if (!DOWN) {
-                o[0] = mul2hv(sub2h(and_or(u, m1, 0x64006400u), z1 + 0x64006400u), s1);
-                o[1] = mul2hv(sub2h(and_or(u, m16, 0x54005400u), z16 + 0x54005400u), s1);
-                o[2] = mul2hv(sub2h(and_or(u8, m1, 0x64006400u), z1 + 0x64006400u), s1);
-                o[3] = mul2hv(sub2h(and_or(u8, m16, 0x54005400u), z16 + 0x54005400u), s1);
-              } else if (Z) {
-                o[0] = mul2v(sub2(u & 0x000f000fu, z1), s1);
-                o[1] = mul2v(sub2(u & 0x00f000f0u, z16), s16);
-                o[2] = mul2v(sub2(u8 & 0x000f000fu, z1), s1);
-                o[3] = mul2v(sub2(u8 & 0x00f000f0u, z16), s16);
-              } else {
-                o[0] = fma2v(u & 0x000f000fu, s1, c8);
-                o[1] = fma2v(u & 0x00f000f0u, s16, c8);
-                o[2] = fma2v(u8 & 0x000f000fu, s1, c8);
-                o[3] = fma2v(u8 & 0x00f000f0u, s16, c8);
-              }
+              o[0] = mul2hv(sub2h(and_or(u, m1, 0x64006400u), z1 + 0x64006400u), s1);
+              o[1] = mul2hv(sub2h(and_or(u, m16, 0x54005400u), z16 + 0x54005400u), s1);
+              o[2] = mul2hv(sub2h(and_or(u8, m1, 0x64006400u), z1 + 0x64006400u), s1);
+              o[3] = mul2hv(sub2h(and_or(u8, m16, 0x54005400u), z16 + 0x54005400u), s1);
             }
           }
           // everything but the stores comes before the wait for the MMAs of two
@@ -544,41 +504,37 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const size_t slots = (size_t)a.T * (a.k + a.S);
     int at = 0, set = 0;
     uint32_t d_phase = 0;
-    if (!DOWN) wait_for_previous_kernel();  // the tokens' exponents
+    wait_for_previous_kernel();  // the tokens' exponents
     for (int i = blockIdx.x; i < n_items; i += gridDim.x) {
       TileItem it;
       item_of(i, &at, &it);
+      const int col = it.tile * tile_rows + row;
       // the powers of two in halves, so that no partial product leaves the range
-      const short2 exps = DOWN ? short2{} : __ldg(a.exps + (size_t)it.e * rows_of + it.tile * tile_rows + row);
-      const float g1 = two_to(exps.x >> 1), g2 = two_to(exps.x - (exps.x >> 1));
-      const float u1 = two_to(exps.y >> 1), u2 = two_to(exps.y - (exps.y >> 1));
+      const size_t at_row = (size_t)it.e * rows_of + col;
+      const int e0 = __ldg(a.exps[DOWN ? 2 : 0] + at_row);
+      const int e1 = !DOWN ? __ldg(a.exps[1] + at_row) : col + kTileRows < a.d ? __ldg(a.exps[2] + at_row + kTileRows) : 0;
+      const float g1 = two_to(e0 >> 1), g2 = two_to(e0 - (e0 >> 1)), u1 = two_to(e1 >> 1), u2 = two_to(e1 - (e1 >> 1));
       wait_stage(d_full + set, d_phase, a.status);
       moe::tc_fence_after();
       const uint32_t from = lane_at + set * 2 * sum_columns;
-      const int col = it.tile * tile_rows + row;
       for (int c0 = (warp - kFirstOut) / 4 * 16; c0 < it.rows; c0 += 32) {  // two warps to a row, in turn
         float g[16], u[16];  // gate and up, or rows and rows + 128
-        const int exp_of = (!DOWN && c0 + (lane & 15) < it.rows ? __ldcg(a.x_exp + it.first + c0 + (lane & 15)) : 0) -
-                           kScaleTop - kTokenTop;
-        const float x_half = two_to(lane < 16 ? exp_of >> 1 : exp_of - (exp_of >> 1));
+        const int* exps = (DOWN ? a.h_exp : a.x_exp) + it.first + c0;
+        const int x_e = (c0 + (lane & 15) < it.rows ? __ldcg(exps + (lane & 15)) : 0) - kScaleTop - kTokenTop;
+        const float x_half = two_to(lane < 16 ? x_e >> 1 : x_e - (x_e >> 1));
         moe::tmem_ld2x16(from + c0, from + sum_columns + c0, g, u);
         const int n = min(16, it.rows - c0);
-        if constexpr (!DOWN) {
-          __nv_bfloat16* h = a.h + (size_t)(it.first + c0) * a.f + h_place(col);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (c >= n) break;
-            const float x1 = __shfl_sync(0xffffffffu, x_half, c), x2 = __shfl_sync(0xffffffffu, x_half, 16 + c);
-            const float z = g[c] * g1 * x1 * g2 * x2;
-            h[(size_t)c * a.f] = __float2bfloat16(__fdividef(z, 1.f + __expf(-z)) * (u[c] * u1 * x1 * u2 * x2));
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (c >= n) break;
+        for (int c = 0; c < 16; ++c) {
+          if (c >= n) break;
+          const float x1 = __shfl_sync(0xffffffffu, x_half, c), x2 = __shfl_sync(0xffffffffu, x_half, 16 + c);
+          const float z = g[c] * g1 * x1 * g2 * x2, v = u[c] * u1 * x1 * u2 * x2;
+          if constexpr (!DOWN) {
+            a.h[(size_t)(it.first + c0 + c) * a.f + col] = __float2bfloat16(__fdividef(z, 1.f + __expf(-z)) * v);
+          } else {
             float* y = a.y + (it.split * slots + __ldg(a.list_slot + it.first + c0 + c)) * a.d + col;
-            y[0] = g[c] * kTileUnscale;
-            if (col + kTileRows < a.d) y[kTileRows] = u[c] * kTileUnscale;
+            if (col < a.d) y[0] = z;
+            if (col + kTileRows < a.d) y[kTileRows] = v;
           }
         }
       }
