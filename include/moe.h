@@ -461,7 +461,7 @@ moe_w4_t* moe_w4_create(int d, int f, int E, int k, int shared_experts, int grou
 
 /* Allocate the workspace for up to T_max (1..1024) tokens, and room for the
  * scales, on the current device.  The only allocating call; may be called
- * again to grow or shrink the workspace. */
+ * again, on the same device, to grow or shrink the workspace. */
 int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream);
 
 /* Bytes that moe_w4_reserve(T_max) allocates in all; -1 for a NULL handle or a T_max

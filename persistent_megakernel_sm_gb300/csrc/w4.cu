@@ -993,6 +993,7 @@ struct moe_w4 {
   CUtensorMap x_maps[kTileTokens / 32], h_maps[kTileTokens / 32];  // by an item's token rows
   char* ws = nullptr;
   char* arranged = nullptr;  // the scales' and zero points' copies
+  int device = -1;           // where they are
 };
 
 namespace {
@@ -1241,6 +1242,8 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
   if (e == cudaSuccess && (major != 10 || minor != 3))
     return moe::set_error(MOE_E_INVAL, "this library is built for sm_103a (GB300) only");
   if (!moe::encode_fn()) return moe::set_error(MOE_E_CUDA, "cuTensorMapEncodeTiled is not available");
+  if (e == cudaSuccess && h->arranged && h->device != dev)
+    return moe::set_error(MOE_E_STATE, "the handle was reserved on another device");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (e == cudaSuccess && h->ws) {
     e = cudaStreamSynchronize(s);
@@ -1252,6 +1255,7 @@ int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream) {
   const Layout l = layout(h, T_max);
   const size_t bytes = l.bytes;
   if (!h->arranged && cudaMalloc(&h->arranged, arranged(h).bytes) != cudaSuccess) h->arranged = nullptr;
+  h->device = dev;
   if (!h->arranged || cudaMalloc(&h->ws, bytes) != cudaSuccess) {
     h->ws = nullptr;
     cudaGetLastError();
@@ -1415,7 +1419,8 @@ int moe_w4_status(moe_w4_t* h, void* stream) {
   int status = 0;
   cudaError_t e = cudaMemcpyAsync(&status, at, sizeof(int), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && status) e = cudaMemsetAsync(at, 0, sizeof(int), s);
+  // with the arrivals that the pass may have left
+  if (e == cudaSuccess && status) e = cudaMemsetAsync(at, 0, h->l.list - h->l.status, s);
   if (e != cudaSuccess) return moe::set_cuda_error(e, "moe_w4_status");
   return status ? moe::set_error(status, "device wait timed out") : MOE_OK;
 }
