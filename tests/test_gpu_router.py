@@ -193,6 +193,28 @@ def test_rows_of_a_wider_buffer_and_unaligned_rows():
         assert counts.sum() == 250
 
 
+def test_rows_over_four_gigabytes_apart():
+    """Offsets that pass 32 bits, forward and back."""
+    import torch
+    r = settings(64, 6)
+    wide = torch.empty(3, (1 << 31) + 64, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(31)
+    l = ref.clear_logits(rng, 3, r, None, to=ref.bf16)
+    view = wide[:, :64]
+    view.copy_(dev(l, torch.bfloat16))
+    idx, w, counts = forward(r, view)
+    want_idx, want_w = ref.route(l, r, None)
+    assert np.array_equal(idx, want_idx)
+    assert np.all(np.abs(w - want_w) <= weight_tolerance(l) * np.abs(want_w))
+    grad = torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda")
+    far = wide[:, 64:128]
+    args = torch.from_numpy(idx).cuda(), dev(rng.standard_normal((3, 6)))
+    make(r).backward(view, *args, grad)
+    make(r).backward(view, *args, far)
+    torch.cuda.synchronize()
+    assert torch.equal(grad, far) and grad.abs().max() > 0
+
+
 def test_no_rows_and_no_counts():
     import torch
     r = settings(64, 4)

@@ -281,6 +281,30 @@ def test_route_then_experts_and_the_bf16_layer_on_the_same_weights():
     assert np.all(np.abs(hz.bf16_to_f64(full) - host(out)) <= 1e-2 + 1e-2 * np.abs(host(out)) + off)
 
 
+def test_conversion_of_more_than_2_to_the_31_weights():
+    import torch
+    from persistent_megakernel_sm_gb300 import w4_dequantize, w4_quantize
+    n, k = (1 << 17) + 8, 1 << 14
+    w = torch.zeros(n, k, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(3)
+    rows = ref.bf16(rng.standard_normal((4, k)))
+    at = [0, (1 << 17) - 1, 1 << 17, n - 1]
+    for r, v in zip(at, rows):
+        w[r] = dev_bf16(v)
+    codes = torch.zeros(n, k // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(n, k // 32, dtype=torch.bfloat16, device="cuda")
+    zeros = torch.zeros(n, k // 32, dtype=torch.uint8, device="cuda")
+    w4_quantize(w, codes, scales, zeros)
+    want = ref.quantize(rows, 32, True)
+    for got, v in zip((codes, scales, zeros), want):
+        got = got[at]
+        assert np.array_equal(host(got) if got.dtype == torch.bfloat16 else got.cpu().numpy(), v)
+    w.fill_(7.0)
+    w4_dequantize(codes, scales, zeros, w)
+    assert np.array_equal(host(w[at]), ref.bf16(ref.values(*want)))
+    assert torch.count_nonzero(w[5:105]) == 0
+
+
 # --------------------------------------------- the ways a batch can be run
 
 @pytest.mark.parametrize("group,zeros", [(32, False), (32, True), (64, False), (64, True), (128, False), (128, True)])
