@@ -305,6 +305,39 @@ def test_conversion_of_more_than_2_to_the_31_weights():
     assert torch.count_nonzero(w[5:105]) == 0
 
 
+def test_experts_behind_2_to_the_31_bytes_of_codes():
+    """The last of 80 experts of 4096 x 14336, by the small kernels and by the tile
+    kernels, against its product in 64 bits."""
+    import torch
+    from persistent_megakernel_sm_gb300 import W4Experts
+    E, d, f, group = 80, 4096, 14336, 128
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def matrix(rows, cols):
+        codes = torch.randint(0, 256, (E, rows, cols // 2), dtype=torch.uint8, device="cuda", generator=g)
+        scales = (0.5 + torch.rand(E, rows, cols // group, device="cuda", generator=g)) / (4.6 * cols ** 0.5)
+        return codes, scales.bfloat16(), None
+
+    def last(m):
+        q = torch.stack((m[0][-1] & 15, m[0][-1] >> 4), -1).flatten(1).double() - 8
+        return q * m[1][-1].double().repeat_interleave(group, 1)
+
+    gate, up, down = matrix(f, d), matrix(f, d), matrix(d, f)
+    experts = W4Experts(d, f, E, 1, group=group)
+    experts.reserve(720)
+    experts.set_weights(gate, up, down)
+    for T in (2, 720):
+        x = torch.randn(T, d, device="cuda", generator=g).bfloat16()
+        idx = torch.full((T, 1), E - 1, dtype=torch.int32, device="cuda")
+        w = torch.ones(T, 1, device="cuda")
+        out = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+        experts.forward(x, idx, w, out)
+        xd = x.double()
+        want = (torch.nn.functional.silu(xd @ last(gate).T) * (xd @ last(up).T)) @ last(down).T
+        assert float((out.double() - want).norm() / want.norm()) <= ref.EXPERTS_NORM
+    experts.check()
+
+
 # --------------------------------------------- the ways a batch can be run
 
 @pytest.mark.parametrize("group,zeros", [(32, False), (32, True), (64, False), (64, True), (128, False), (128, True)])
