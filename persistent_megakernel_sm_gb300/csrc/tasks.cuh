@@ -1742,6 +1742,9 @@ __device__ bool route_task(const Params& p, const Maps& maps, int pt, int split,
   const int nkb = p.d / kBK;
   const int epad = ((p.E + 15) / 16) * 16;   // logit columns read back
   const int nmma = ((p.E + 16 * P - 1) / (16 * P)) * (16 * P);  // MMA N over the worker
+  // a tile ends with reads of the masks, which a CTA that runs tiles one after
+  // another (moe_static_kernel) has not all behind it here
+  cta_sync();
   for (int i = threadIdx.x; i < kMaxE * 4; i += kThreads) c->mask[i] = 0u;
   for (int e = threadIdx.x; e < kMaxE; e += kThreads)
     c->bias_s[e] = (p.bias && e < p.E) ? __ldg(p.bias + e) : 0.f;
