@@ -364,8 +364,8 @@ void moe_layer_destroy(moe_layer_t* h);
  * bias that training moves against the load) selects only: it is not in w.
  * A logit of -inf (or a bias of -inf) masks its expert out: it is never
  * chosen and has the score 0.  A slot left without an expert (a row masked
- * out altogether, say) gets idx -1 and w 0.  A NaN logit ranks above every
- * number, and shows as NaN in w.  Scores, sums and weights are fp32, so two
+ * out altogether, say) gets idx -1 and w 0.  A NaN logit of an expert that is
+ * not masked ranks above every number, and shows as NaN in w.  Scores, sums and weights are fp32, so two
  * choices whose c differ by a few fp32 roundings may be taken either way;
  * without a bias (and groups ranked by the maximum) the choice is exact.
  *

@@ -370,9 +370,9 @@ __global__ void __launch_bounds__(kWarps * 32, kForward)
         for (int i = 0; i < kVals; ++i) s[i] = fast_sigmoid(l[i]);
       }
       uint32_t key[kVals];
-      if (bias) {
+      if (bias) {  // masked by either, even if the other is NaN (which fminf passes over)
 #pragma unroll
-        for (int i = 0; i < kVals; ++i) key[i] = l[i] == -INFINITY ? 0u : key_of(s[i] + b[i]);
+        for (int i = 0; i < kVals; ++i) key[i] = fminf(l[i], b[i]) == -INFINITY ? 0u : key_of(s[i] + b[i]);
       } else {
 #pragma unroll
         for (int i = 0; i < kVals; ++i) key[i] = key_of(l[i]);
