@@ -413,7 +413,8 @@ void moe_router_destroy(moe_router_t* h);
  *           high half of byte i
  *   scales  [rows, cols / group] bf16, a group being 32, 64 or 128 consecutive
  *           columns of a row
- *   zeros   [rows, cols / group] bytes 0..15, or NULL: 8 everywhere
+ *   zeros   [rows, cols / group] bytes, of which the low four bits count, or
+ *           NULL: 8 everywhere
  *   value = (code - zero) * scale
  */
 

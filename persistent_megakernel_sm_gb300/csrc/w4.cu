@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(256)
   for (int n = 0; n < kConvertUnroll; ++n) {
     const long long i = i0 + n * 256;
     if (i >= n8) break;
-    const uint32_t s = s2[n] * 0x00010001u, base = 0x43004300u + z2[n] * 0x00010001u;
+    const uint32_t s = s2[n] * 0x00010001u, base = 0x43004300u + (z2[n] & 15u) * 0x00010001u;
     uint32_t v[4];  // columns (j, j + 4)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
