@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -31,20 +32,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
     nvcc = os.environ.get("NVCC", "nvcc")
-    tmp = LIB + f".tmp{os.getpid()}"
     flags = [*NVCC_FLAGS, *(["-Xptxas=-v"] if verbose else []), "-I", os.path.join(REPO, "include")]
+    # beside the library, so that it can be moved into place; gone whatever fails
+    with tempfile.TemporaryDirectory(prefix="tmp", dir=os.path.dirname(LIB)) as tmp:
+        def compile_one(src: str) -> str:
+            obj = os.path.join(tmp, f"{src}.o")
+            subprocess.run([nvcc, *flags, "-c", "-o", obj, os.path.join(CSRC, src)], check=True)
+            return obj
 
-    def compile_one(src: str) -> str:
-        obj = f"{tmp}.{src}.o"
-        subprocess.run([nvcc, *flags, "-c", "-o", obj, os.path.join(CSRC, src)], check=True)
-        return obj
-
-    with ThreadPoolExecutor(len(SOURCES)) as ex:  # one compiler process per source
-        objs = list(ex.map(compile_one, SOURCES))
-    subprocess.run([nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *objs], check=True)
-    for obj in objs:
-        os.remove(obj)
-    os.replace(tmp, LIB)
+        with ThreadPoolExecutor(len(SOURCES)) as ex:  # one compiler process per source
+            objs = list(ex.map(compile_one, SOURCES))
+        lib = os.path.join(tmp, "libmoe.so")
+        subprocess.run([nvcc, *NVCC_FLAGS, "-shared", "-o", lib, *objs], check=True)
+        os.replace(lib, LIB)
     return LIB
 
 
