@@ -218,14 +218,17 @@ int moe_layer_forward(moe_layer_t* h, int T, const void* x, const void* router_w
 
 /* The same forward pass on a routing that the caller gives, in place of the
  * layer's own router: idx [T, k] int32 and w [T, k] fp32 (device pointers,
- * 4-byte aligned), as moe_router_forward writes them -- sigmoid scores, groups,
- * a balance bias, weights that are not renormalised.
+ * 4-byte aligned), such as moe_router_forward writes them -- sigmoid scores,
+ * groups, a balance bias, weights that are not renormalised.
  *   out[t] = bf16( sum_j w[t,j] * y_{idx[t,j]}  +  y_shared )
  * Each token's k experts are in [0, E) and distinct; else the pass ends in
- * MOE_E_DEVICE (moe_layer_status) and its output is undefined.  The router bias
- * does not enter.  Everything else (modes, options, routing readback, status)
- * is that of moe_layer_forward; with the same routing the output has the same
- * bits. */
+ * MOE_E_DEVICE (moe_layer_status) and its output is undefined.  So the slots
+ * that moe_router_forward left without an expert (idx -1: rows of padding, or
+ * with fewer than k experts not masked) have to name some other expert of the
+ * row first; their w is 0, and adds nothing as long as that expert's y is
+ * finite.  The router bias does not enter.  Everything else (modes, options,
+ * routing readback, status) is that of moe_layer_forward; with the same routing
+ * the output has the same bits. */
 int moe_layer_forward_routed(moe_layer_t* h, int T, const void* x, const int32_t* idx,
                              const float* w, const void* w_gate, const void* w_up,
                              const void* w_down, void* out, void* stream);

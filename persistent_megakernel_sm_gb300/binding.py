@@ -196,7 +196,8 @@ class MoELayer:
 
     def forward_routed(self, x, idx, w, w_gate, w_up, w_down, out, stream=None):
         """moe_layer_forward_routed: the forward pass on a given routing, idx [T, k]
-        int32 and w [T, k] fp32 (MoERouter.forward's)."""
+        int32 and w [T, k] fp32 (MoERouter.forward's, without slots of -1: a token's
+        k experts are in [0, E) and distinct, or the pass ends in MOE_E_DEVICE)."""
         import torch
         T, n = x.shape[0], self.E + self.S
         _check_tensor("w_gate", w_gate, torch.bfloat16, (n, self.f, self.d))
