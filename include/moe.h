@@ -199,7 +199,8 @@ moe_layer_t* moe_layer_create(int d, int f, int E, int k, int shared_experts);
  * (routing arrays, permuted activations, expert intermediates, scheduler
  * state) and cache the device properties.  The only allocating call besides
  * moe_layer_forward_host's first use; call it before any stream capture.
- * May be called again to grow or shrink. */
+ * May be called again to grow or shrink; a graph captured before that holds the
+ * freed workspace and must not be replayed. */
 int moe_layer_reserve(moe_layer_t* h, int T_max, void* stream);
 
 /* Set the per-expert router bias (fp32 [E] device pointer, added to the
@@ -465,7 +466,8 @@ moe_w4_t* moe_w4_create(int d, int f, int E, int k, int shared_experts, int grou
 
 /* Allocate the workspace for up to T_max (1..1024) tokens, and room for the
  * scales, on the current device.  The only allocating call; may be called
- * again, on the same device, to grow or shrink the workspace. */
+ * again, on the same device, to grow or shrink the workspace: a graph captured
+ * before that holds the freed one and must not be replayed. */
 int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream);
 
 /* Bytes that moe_w4_reserve(T_max) allocates in all; -1 for a NULL handle or a T_max
@@ -475,7 +477,10 @@ long long moe_w4_workspace_bytes(const moe_w4_t* h, int T_max);
 /* The matrices of every later forward (device pointers, 16-byte aligned).  The
  * codes are read where they are and stay the caller's; the scales and zero
  * points are copied, in the order in which the kernels take them, on `stream`
- * (call it again when they change).  After moe_w4_reserve. */
+ * (call it again when they change).  After moe_w4_reserve.  A captured pass
+ * reads the copies as they are when it is replayed, but the codes where they
+ * were when it was captured: new weights in the old tensors reach it by this
+ * call, others need another capture. */
 int moe_w4_set_weights(moe_w4_t* h, const moe_w4_weight* gate, const moe_w4_weight* up,
                        const moe_w4_weight* down, void* stream);
 
