@@ -366,12 +366,14 @@ void moe_layer_destroy(moe_layer_t* h);
  *   w_j = scale * s_j, or scale * s_j / (sum of the kept s) if renormalised
  * Ties go to the lower expert and the lower group.  The bias (the balance
  * bias that training moves against the load) selects only: it is not in w.
- * A logit of -inf (or a bias of -inf) masks its expert out: it is never
- * chosen and has the score 0.  A slot left without an expert (a row masked
- * out altogether, say) gets idx -1 and w 0.  A NaN logit of an expert that is
- * not masked ranks above every number, and shows as NaN in w.  Scores, sums and weights are fp32, so two
- * choices whose c differ by a few fp32 roundings may be taken either way;
- * without a bias (and groups ranked by the maximum) the choice is exact.
+ * A logit of -inf masks its expert out: it is never chosen and has the score 0.
+ * A bias of -inf keeps its expert from being chosen, whatever its logit.  A
+ * slot left without an expert (a row masked out altogether, say) gets idx -1
+ * and w 0.  A NaN logit of an expert that is not masked ranks above every
+ * number, and shows as NaN in w.  Scores, sums and weights are fp32, and the
+ * sigmoid scores that select (not those in w) are within 4e-7: two choices
+ * whose c are nearer than that and a few fp32 roundings may be taken either
+ * way.  Without a bias (and groups ranked by the maximum) the choice is exact.
  *
  * Row t of the logits is at logits + t * row_stride elements (row_stride >=
  * E), fp32 or bf16, aligned to its type; idx [T, k] int32 and w [T, k] fp32
@@ -444,8 +446,9 @@ int moe_w4_dequantize(long long rows, int cols, int group, const void* codes, co
  *   h       = bf16( silu(Wg[e] x_t) * (Wu[e] x_t) )
  *   out[t]  = bf16( sum_j w[t,j] Wd[e_j] h_j  +  shared expert's, weight 1 )
  * with the weights' 4-bit values and fp32 sums.  (From a mean of 9 rows an
- * expert on, the kernels for larger batches round each weight to 11 bits; with
- * fewer no weight is rounded.)  Magnitudes of x and h are taken to lie below
+ * expert and 33 slots on, the kernels for larger batches round each weight to 11
+ * bits; with fewer no weight is rounded.  So a token's bits may differ from one
+ * batch size to another.)  Magnitudes of x and h are taken to lie below
  * 2^64, those below 2^-57 count as zero; scales between 2^-86 and 2^31, or 0.
  * In larger batches a scale under 2^-24 of its weight row's largest, and a value
  * of x or h under 2^-29 of its token row's, lose bits.  Slots with idx outside
@@ -465,9 +468,11 @@ typedef struct moe_w4_weight {
 moe_w4_t* moe_w4_create(int d, int f, int E, int k, int shared_experts, int group);
 
 /* Allocate the workspace for up to T_max (1..1024) tokens, and room for the
- * scales, on the current device.  The only allocating call; may be called
- * again, on the same device, to grow or shrink the workspace: a graph captured
- * before that holds the freed one and must not be replayed. */
+ * scales (they are kept twice over, for small and for larger batches: 4 bytes
+ * a group, and one for its zero point), on the current device.  The only
+ * allocating call; may be called again, on the same device, to grow or shrink
+ * the workspace: a graph captured before that holds the freed one and must not
+ * be replayed. */
 int moe_w4_reserve(moe_w4_t* h, int T_max, void* stream);
 
 /* Bytes that moe_w4_reserve(T_max) allocates in all; -1 for a NULL handle or a T_max

@@ -19,7 +19,7 @@
 // experts each, so a warp chooses for 8 to 1 rows at once, from few candidates
 // (choose below).  The weights follow for the chosen alone, a lane a slot, for
 // several rows together.  What bounds the choice is instructions, not the 2 to 4
-// bytes a logit: 870 of a warp for a row of 256 experts in 8 groups, top 8 (8192
+// bytes a logit: 920 of a warp for a row of 256 experts in 8 groups, top 8 (8192
 // rows 14.4 us, their bytes 1.2); the gradient waits for the gathered logits,
 // then writes every expert (32768 rows of 256 fp32 10.5 us, those writes 4.9).
 // Scores and sums are fp32.
@@ -176,7 +176,8 @@ __device__ __forceinline__ void row_softmax(float (&v)[VPL], float* top, float* 
   for (int i = 0; i < VPL; ++i) v[i] *= *inv;
 }
 
-// For the choice alone: within 4e-7, by the device's 2^x and reciprocal.
+// For the choice alone: within 4e-7 of the score (which is at most 1), by the
+// device's 2^x and reciprocal; a far negative logit's score keeps fewer bits.
 __device__ __forceinline__ float fast_sigmoid(float l) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.44269504f));

@@ -185,10 +185,11 @@ __global__ void __launch_bounds__(256)
 // --------------------------------------------------------------------- experts
 //
 // Two kernels, gate/up then down, of the same shape, and a third that adds the
-// slots of a token (with few of them the last item of a column tile does).  An item is 64 weight rows of one expert (gate/up: 32 of
-// each) times up to 8 of the expert's token rows; a team of 1, 2, 4 or 8 warps
-// works an item off, its warps taking the 128-column blocks of the product in
-// turn, and its first warp adds the others' sums.  Blocks of eight warps stay
+// slots of a token (with few of them the last item of a column tile does).  An
+// item is 64 weight rows of one expert (gate/up: 32 of each) times up to 8 of the
+// expert's token rows; a team of 1, 2, 4 or 8 warps works an item off, its warps
+// taking the 128-column blocks of the product in turn, and its first warp adds the
+// others' sums.  Blocks of eight warps stay
 // resident, two to an SM, and teams take items by turns.
 //
 // A warp's unit is 64 rows x 128 columns: 4 KB of codes, loaded by TMA into the
@@ -222,7 +223,12 @@ constexpr int kInline = 32;           // slots up to which every block lists the
 // Mean token rows of an expert from which the tile kernels run.  The small
 // kernels take 8 rows at once; on 128 experts of 2048 x 768, 113 us (small)
 // against 115 at 8 rows, 121 against 120 at 9; on 8 of 4096 x 14336, 186 against
-// 189 at 8 and 228 against 190 at 9.
+// 189 at 8 and 228 against 190 at 9; both in groups of 128 without zero points,
+// the other kinds take the same number.  The mean is that of the routed experts:
+// a few experts with many rows among idle ones, or a shared expert's T rows, stay
+// on the small kernels where the mean is below (1024 tokens on 8 of 256 experts of
+// 2048 x 768, 256 rows each, 147 us; 256 tokens of 256 + 1 experts of 7168 x 2048,
+// eight each, 1600 us, their bytes 862).
 constexpr int kTileMinRows = 9;
 // Partial sums of a pass (slots times K splits) up to which the last item of a
 // column tile adds them: more are added sooner by a kernel of their own.
@@ -856,7 +862,9 @@ __global__ void __launch_bounds__(kItemWarps * 32, kBlocksSm)
           const int m = q >> 1, v = (q & 1) * 2 + j;
           const int c = it.tile * 32 + m * 16 + (q & 1) * 8 + lr8;
           const float g = acc[m][v] * kUnscale, u = acc[m + 2][v] * kUnscale;
-          h[h_place(c)] = __float2bfloat16(g / (1.f + expf(-g)) * u * h_scale(c));  // the one rounding between the products
+          // the one rounding between the products, to what the next one multiplies:
+          // the output is off by 2.4e-3 of its norm, its own rounding alone 1.7e-3
+          h[h_place(c)] = __float2bfloat16(g / (1.f + expf(-g)) * u * h_scale(c));
         }
       } else {
         float* y = a.y + ((size_t)it.split * (a.T * (a.k + a.S)) + slot) * a.d + it.tile * kRows + lr8;
@@ -1021,10 +1029,11 @@ namespace {
 // an SM's items come in rounds of 16 / team, and each round ends with the
 // teams' sums and the results (a warp alone 0.5, eight together 1.4).  Long
 // chains of units end at different times (0.15 a unit), and the splits' partial
-// sums cost the combine about 0.4 each.  One token of the
-// 4096 x 14336 eight-expert layer: 53 us with single warps and no split, 42
-// with teams of 4 and 4 splits; 64 tokens of 128 experts: 97 us with teams of
-// 8 in both products, 85 with teams of 2 and single warps.
+// sums cost the combine about 0.4 each.  The numbers are fitted to two layers and
+// not measured apart from them.  One token of the 4096 x 14336 eight-expert
+// layer: 53 us with single warps and no split, 42 with teams of 4 and 4 splits;
+// 64 tokens of 128 experts of 2048 x 768: 97 us with teams of 8 in both products,
+// 85 with teams of 2 and single warps.
 float estimate(long long items, int blocks, int team, int splits) {
   const long long per_sm = (items * splits + kSms - 1) / kSms;
   const int units = ((blocks + splits - 1) / splits + team - 1) / team;

@@ -24,11 +24,11 @@
 // group, as many as the conversion itself at 64 tokens; in bf16 a conversion is
 // 5 + 4 instructions and 256 tokens of the eight-expert layer took 189 us in place
 // of 224, but the output was off by 3.4e-3 of its norm in place of 2.4e-3, of
-// which 1.7e-3 are its own rounding to bf16 and as much h's.)  For fp16's range, each weight row's
-// scales are divided by a power of two, the largest one's, and each row of x and
-// of h too, by kernels of their own (w4_row_exponents once, w4_rows in every
-// pass); the sums are multiplied back.  Scales under 2^-24 of their row's
-// largest, and values under 2^-29 of theirs, lose bits.
+// which 1.7e-3 are its own rounding to bf16 and as much h's.)  For fp16's range,
+// each weight row's scales are divided by a power of two, the largest one's, and
+// each row of x and of h too, by kernels of their own (w4_row_exponents once,
+// w4_rows in every pass); the sums are multiplied back.  Scales under 2^-24 of
+// their row's largest, and values under 2^-29 of theirs, lose bits.
 //
 // A conversion is 5 + 8 instructions for 8 codes.  The tokens' rows are read
 // again for every 256 weight rows, which is why both matrices (or twice the
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (c >= n) break;
           const float x1 = __shfl_sync(0xffffffffu, x_half, c), x2 = __shfl_sync(0xffffffffu, x_half, 16 + c);
           const float z = g[c] * g1 * x1 * g2 * x2, v = u[c] * u1 * x1 * u2 * x2;
-          if constexpr (!DOWN) {
+          if constexpr (!DOWN) {  // bf16, the h that the header defines, though fp16 operands could hold more
             a.h[(size_t)(it.first + c0 + c) * a.f + col] = __float2bfloat16(__fdividef(z, 1.f + __expf(-z)) * v);
           } else {
             float* y = a.y + (it.split * slots + __ldg(a.list_slot + it.first + c0 + c)) * a.d + col;
