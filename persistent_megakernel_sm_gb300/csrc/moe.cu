@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   ok = ok && grid_barrier(p, c, gen, st);
   const int n_groups = ok ? ld_relaxed(&p.sched->n_groups) : 0;
   const int n_routed = n_groups - p.n_shared_groups;
+  ok = ok && n_groups > 0;  // else the plan refused the routing, and pos holds no rows of this pass
   for (int i = w; ok && i < n_routed * 8; i += W) {  // (routed group, chunk)
     const int g = p.n_shared_groups + (i >> 3), ch = i & 7;
     if (ch * gather_rows(p) < load_group(p, g).nrows) gather_task(p, g, ch, st.rank, P, smem, c, st);
@@ -559,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 __global__ void __launch_bounds__(kThreads, 1)
     k_combine(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+  if (p.sched->n_groups == 0) return;  // the plan refused the routing, and pos holds no rows of this pass
   char* smem;
   Ctrl* c;
   CtaState st;
