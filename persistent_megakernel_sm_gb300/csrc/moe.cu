@@ -1001,6 +1001,7 @@ int moe_layer_reserve(moe_layer_t* h, int T_max, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (h->ws) {
     CK(cudaStreamSynchronize(s));
+    if (h->view.ws == h->ws) h->view.ws = nullptr;  // the last pass's results go with it
     CK(cudaFree(h->ws));
     h->ws = nullptr;
   }
