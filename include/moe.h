@@ -502,6 +502,136 @@ int moe_w4_status(moe_w4_t* h, void* stream);
 
 void moe_w4_destroy(moe_w4_t* h);
 
+/* --------------------------------------------------------------- 8-bit rows
+ *
+ * Activations kept for the backward pass in half their bytes.  Rows [rows, cols]
+ * of bf16 or fp32 values are held as
+ *   codes   [rows, cols] int8
+ *   scales  [rows, ceil(cols / group)] bf16, a group being 32, 64 or 128
+ *           consecutive columns of a row, its last one maybe shorter
+ *   value = code * scale,  scale = bf16(max |v| / 127) over the group,
+ *   code = clamp(round(v / scale), -127, 127)
+ * with division and rounding (half to even) in fp32.  A scale of 0 divides as 1.
+ * A group with an infinity or a NaN gets the scale NaN and codes 0.
+ * moe_norm_forward writes such rows, and moe_norm_backward reads them. */
+typedef struct moe_rows8 {
+  void* codes;
+  void* scales;
+} moe_rows8;
+
+/* v [rows, cols] of `type` (MOE_TYPE_F32, MOE_TYPE_BF16), contiguous -> codes and
+ * scales; and the way back, rounded once to `type`.  Any cols; tensors are aligned
+ * to their types (16 bytes, 8 for the codes, and cols a multiple of the group are
+ * faster).  At most 2^38 values.  Asynchronous, allocate nothing; no two tensors
+ * overlap. */
+int moe_rows8_quantize(long long rows, int cols, int type, int group, const void* v, void* codes, void* scales,
+                       void* stream);
+int moe_rows8_dequantize(long long rows, int cols, int type, int group, const void* codes, const void* scales, void* v,
+                         void* stream);
+
+/* ------------------------------------------------------ norms about a block
+ *
+ * What stands between two blocks of a network whose blocks read a normalised
+ * residual stream: the norm behind a block (post), its gate and factor, the
+ * residual add, and the norm in front of the next block (pre).  Per token, with
+ * the residual r, the block's output y and a gate g:
+ *   p    = N_post(y), or y
+ *   out  = r + scale * g * p                   rounded to r's type
+ *   norm = bf16(N_pre(out))                    of the rounded sum, or not at all
+ *   N(x) = (x - m) * rstd * gain + shift,  rstd = 1 / sqrt(mean((x - m)^2) + eps),
+ *          m = 0 (MOE_NORM_RMS, no shift) or mean(x) (MOE_NORM_LAYER)
+ * with fp32 sums.  A gain of NULL is 1, a shift of NULL 0; with unit_offset a gain
+ * is 1 + what is stored.  The gate: MOE_GATE_NONE 1; MOE_GATE_CHANNEL [d] of
+ * the gains' type; MOE_GATE_TOKEN [T] fp32; MOE_GATE_ELEMENT [T, d] bf16, rows
+ * gate_stride elements apart.
+ *
+ * y and norm are bf16, the residual and out of residual_type.  Row t of a tensor
+ * is at its pointer + t * its stride elements (stride >= d); every tensor is
+ * aligned to its type, and rows of a multiple of 8 columns that are aligned to 16
+ * bytes (codes to 8) are faster.  Any d from 1 to 32768.  A row with an infinity or
+ * a NaN makes itself NaN, no other. */
+#define MOE_NORM_NONE 0
+#define MOE_NORM_RMS 1
+#define MOE_NORM_LAYER 2
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1
+#define MOE_GATE_TOKEN 2
+#define MOE_GATE_ELEMENT 3
+
+typedef struct moe_norm moe_norm_t;
+
+typedef struct moe_norm_params {
+  const void *pre_gain, *pre_shift, *post_gain, *post_shift; /* [d] each, or NULL */
+  const void* gate;                                          /* NULL with MOE_GATE_NONE */
+  long long gate_stride;                                     /* MOE_GATE_ELEMENT */
+  int type; /* MOE_TYPE_* of gains, shifts and a channel gate */
+} moe_norm_params;
+
+/* group: of the 8-bit rows.  eps finite and >= 0, scale finite.  NULL on anything
+ * else. */
+moe_norm_t* moe_norm_create(int d, int pre, int post, int gate, float eps, float scale, int unit_offset, int group);
+
+/* out is written where y is given (it may be the residual itself, in place);
+ * without y, post norm and gate, norm is that of the residual (the first block's).
+ * stats [T, 4] fp32, 16-byte aligned, may be NULL: post norm's mean and rstd, pre
+ * norm's mean and rstd, as the backward pass takes them (0 and 1 where there is no
+ * norm).  out8 and y8, each may be NULL: out and y as 8-bit rows, codes [T, d]
+ * contiguous, scales 4-byte aligned.  No other tensors overlap.  Asynchronous,
+ * allocates nothing, can be captured in a graph; needs no workspace, so a handle
+ * may be used by several streams and threads at once.  T = 0 does nothing. */
+int moe_norm_forward(const moe_norm_t* h, int T, int residual_type, const void* residual, long long residual_stride,
+                     const void* y, long long y_stride, const moe_norm_params* params, void* out, long long out_stride,
+                     void* norm, long long norm_stride, float* stats, const moe_rows8* out8, const moe_rows8* y8,
+                     void* stream);
+
+/* What the forward pass left: out and y as they were or as 8-bit rows (out: only if
+ * grad_norm is given; y: only for the gradients that need it: any but grad_residual,
+ * and grad_y with neither post norm nor gate). */
+typedef struct moe_norm_kept {
+  const void* out;
+  long long out_stride;
+  const moe_rows8* out8;
+  const void* y;
+  long long y_stride;
+  const moe_rows8* y8;
+  const float* stats; /* may be NULL where no norm is passed through */
+} moe_norm_kept;
+
+/* Gradients that are wanted, overwritten; NULL: not wanted.  fp32 [d], but those of
+ * a token gate fp32 [T] and of an element gate bf16 [T, d]. */
+typedef struct moe_norm_grads {
+  float *pre_gain, *pre_shift, *post_gain, *post_shift;
+  void* gate;
+  long long gate_stride;
+} moe_norm_grads;
+
+/* Allocate the workspace (moe_norm_workspace_bytes: 10 MB, less for narrow rows)
+ * for gradients [d], on the current device.  Once is enough; the only allocating
+ * call. */
+int moe_norm_reserve(moe_norm_t* h, void* stream);
+long long moe_norm_workspace_bytes(const moe_norm_t* h);
+
+/* With u = (x - m) * rstd from what was kept and stats as they were saved:
+ *   through a norm, for the gradient q of its output and t = q * gain,
+ *     rstd * (t - u * mean(t u) - [layer] mean(t))
+ *   G = grad_out + (grad_norm through the pre norm);   grad_residual = G
+ *   P = scale * g * G;   grad_y = P through the post norm
+ *   grad gain = sum over rows of q u, grad shift = sum of q  (q: grad_norm, or P)
+ *   grad gate = scale * G * p, summed over the rows (channel) or columns (token)
+ * grad_out (of residual_type) or grad_norm (bf16) may be NULL: zero.
+ * grad_residual (of residual_type; may be grad_out itself, in place) and grad_y (bf16)
+ * may be NULL: not wanted.  No other tensors overlap.  Sums over rows are fp32, in
+ * an order that T and d alone decide.  Asynchronous, allocates nothing, can be
+ * captured in a graph; one stream at a time where gradients [d] are wanted (they
+ * use the workspace; graphs replayed at once need handles of their own).  T = 0
+ * writes zeros to the gradients [d]. */
+int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void* grad_out, long long grad_out_stride,
+                      const void* grad_norm, long long grad_norm_stride, const moe_norm_params* params,
+                      const moe_norm_kept* kept, void* grad_residual, long long grad_residual_stride, void* grad_y,
+                      long long grad_y_stride, const moe_norm_grads* grads, void* stream);
+
+void moe_norm_destroy(moe_norm_t* h);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* moe_last_error(void);
 

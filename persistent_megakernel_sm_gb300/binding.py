@@ -6,7 +6,8 @@ handle for callers holding torch tensors: it passes ``data_ptr()`` values and
 the current CUDA stream, and turns non-zero status codes into ``MoEError``.
 Every step of the layer runs in the library's kernels.  ``MoERouter``,
 ``w4_quantize`` / ``w4_dequantize`` and ``W4Experts`` do the same for the
-routing operator and the 4-bit experts.
+routing operator and the 4-bit experts, ``rows8_quantize`` / ``rows8_dequantize``
+and ``MoEBlockNorm`` for 8-bit rows and the norms about a block.
 """
 from __future__ import annotations
 
@@ -33,6 +34,8 @@ STATS = {"mover_ctas": 1, "tasks": 2, "grid": 3, "gemm_tasks": 4, "mover_tasks":
          "combine_tokens": 13, "pair": 14}
 SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORES = {"max": 0, "top2": 1}
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
 TASK_TYPES = {1: "route", 2: "gather", 3: "gateup", 4: "down", 5: "combine", 6: "plan"}
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
@@ -68,6 +71,14 @@ _SIGNATURES = {
     "moe_w4_forward": ([_vp, _i32, _vp, _vp, _vp, _vp, _vp], _i32),
     "moe_w4_status": ([_vp, _vp], _i32),
     "moe_w4_destroy": ([_vp], None),
+    "moe_rows8_quantize": ([_i64] + [_i32] * 3 + [_vp] * 4, _i32),
+    "moe_rows8_dequantize": ([_i64] + [_i32] * 3 + [_vp] * 4, _i32),
+    "moe_norm_create": ([_i32] * 4 + [ctypes.c_float] * 2 + [_i32] * 2, _vp),
+    "moe_norm_reserve": ([_vp, _vp], _i32),
+    "moe_norm_workspace_bytes": ([_vp], _i64),
+    "moe_norm_forward": ([_vp, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64] + [_vp] * 4, _i32),
+    "moe_norm_backward": ([_vp, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp], _i32),
+    "moe_norm_destroy": ([_vp], None),
     "moe_last_error": ([], ctypes.c_char_p),
 }
 
@@ -321,6 +332,7 @@ class _Torch:
     def __init__(self):
         import torch
         self.f32, self.bf16, self.i32, self.u8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+        self.i8 = torch.int8
         self.current_device = torch.cuda.current_device
         # the current stream's handle without a Stream object around it
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -546,6 +558,243 @@ class W4Experts:
     def close(self):
         if self.h:
             lib.moe_w4_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class _Rows8(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp)]
+
+
+def _type_code(name, t):
+    tt = _torch()
+    if t.dtype is tt.f32:
+        return 0
+    if t.dtype is tt.bf16:
+        return 1
+    raise MoEError(MOE_E_INVAL, f"{name}: dtype {t.dtype}, expected torch.float32 or torch.bfloat16")
+
+
+def _check_rows8(v, codes, scales, group):
+    """Values [..., cols] and their 8-bit form; returns rows, columns, the type and the device."""
+    tt, dev = _torch(), _current_device()
+    if group not in (32, 64, 128):
+        raise MoEError(MOE_E_INVAL, f"group {group}: 32, 64 or 128")
+    shape = tuple(v.shape)
+    if not shape:
+        raise MoEError(MOE_E_INVAL, "values: expected [..., cols]")
+    kind, cols = _type_code("values", v), shape[-1]
+    _on_device("values", v, dev, v.dtype, shape)
+    _on_device("codes", codes, dev, tt.i8, shape)
+    _on_device("scales", scales, dev, tt.bf16, shape[:-1] + (-(-cols // group),))
+    return (v.numel() // cols if cols else 0), cols, kind, dev
+
+
+def rows8_quantize(v, codes, scales, group: int = 128, stream=None):
+    """moe_rows8_quantize: v [..., cols] bf16 or fp32 -> codes int8 of its shape and
+    scales bf16 [..., ceil(cols / group)]."""
+    rows, cols, kind, dev = _check_rows8(v, codes, scales, group)
+    _err(lib.moe_rows8_quantize(rows, cols, kind, group, v.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                _stream_on(stream, dev)))
+    return codes, scales
+
+
+def rows8_dequantize(codes, scales, v, group: int = 128, stream=None):
+    """moe_rows8_dequantize: the 8-bit rows' values into v, bf16 or fp32."""
+    rows, cols, kind, dev = _check_rows8(v, codes, scales, group)
+    _err(lib.moe_rows8_dequantize(rows, cols, kind, group, codes.data_ptr(), scales.data_ptr(), v.data_ptr(),
+                                  _stream_on(stream, dev)))
+    return v
+
+
+class _NormParams(ctypes.Structure):
+    _fields_ = [("pre_gain", _vp), ("pre_shift", _vp), ("post_gain", _vp), ("post_shift", _vp), ("gate", _vp),
+                ("gate_stride", _i64), ("type", _i32)]
+
+
+class _NormKept(ctypes.Structure):
+    _fields_ = [("out", _vp), ("out_stride", _i64), ("out8", _vp), ("y", _vp), ("y_stride", _i64), ("y8", _vp),
+                ("stats", _vp)]
+
+
+class _NormGrads(ctypes.Structure):
+    _fields_ = [("pre_gain", _vp), ("pre_shift", _vp), ("post_gain", _vp), ("post_shift", _vp), ("gate", _vp),
+                ("gate_stride", _i64)]
+
+
+class MoEBlockNorm:
+    """The norms about a block with its gate and the residual add, and their
+    gradient (moe_norm_* of include/moe.h): out = residual + scale * gate *
+    N_post(y), norm = N_pre(out).  ``pre`` (in front of the next block) and
+    ``post`` (behind this one) are "none", "rms" or "layer"; ``gate`` "none",
+    "channel" [d], "token" [T] fp32 or "element" [T, d] bf16; with
+    ``unit_offset`` gains are 1 + what is stored; ``group``: of rows kept in 8 bits."""
+
+    def __init__(self, d: int, pre: str = "rms", post: str = "none", gate: str = "none", eps: float = 1e-6,
+                 scale: float = 1.0, unit_offset: bool = False, group: int = 128):
+        self.h = None
+        if pre not in NORMS or post not in NORMS or gate not in GATES:
+            raise MoEError(MOE_E_INVAL, f"norms are of {list(NORMS)}, the gate of {list(GATES)}")
+        h = lib.moe_norm_create(d, NORMS[pre], NORMS[post], GATES[gate], eps, scale, int(bool(unit_offset)), group)
+        if not h:
+            raise MoEError(MOE_E_INVAL, (lib.moe_last_error() or b"").decode())
+        self.h = ctypes.c_void_p(h)
+        self.d, self.pre, self.post, self.gate, self.group = d, pre, post, gate, group
+        self._device = None
+        self._c_forward, self._c_backward = lib.moe_norm_forward, lib.moe_norm_backward
+
+    def reserve(self, stream=None):
+        """The workspace of backward passes that return gradients [d], on the current device."""
+        _err(lib.moe_norm_reserve(self.h, _stream_ptr(stream)))
+        self._device = _current_device()
+
+    def workspace_bytes(self) -> int:
+        return lib.moe_norm_workspace_bytes(self.h)
+
+    def _rows(self, name, t, T, dtype, dev):
+        """Rows of d values that may be columns of a wider buffer: (pointer, row stride)."""
+        if t is None:
+            return None, 0
+        if t.dtype is not dtype:
+            raise MoEError(MOE_E_INVAL, f"{name}: dtype {t.dtype}, expected {dtype}")
+        if t.dim() != 2 or t.shape[0] != T or t.shape[1] != self.d:
+            raise MoEError(MOE_E_INVAL, f"{name}: shape {list(t.shape)}, expected [{T}, {self.d}]")
+        rows, step = t.stride()
+        if T <= 1:  # a single row's stride is anything
+            rows = self.d
+        if T and ((step != 1 and self.d > 1) or rows < self.d):
+            raise MoEError(MOE_E_INVAL, f"{name}: strides {[rows, step]}, rows of consecutive values are needed")
+        self._where(name, t, dev)
+        return t.data_ptr(), rows
+
+    @staticmethod
+    def _where(name, t, dev):
+        if not t.is_cuda:
+            raise MoEError(MOE_E_INVAL, f"{name}: not a CUDA tensor")
+        if t.get_device() != dev:
+            raise MoEError(MOE_E_INVAL, f"{name}: on device {t.get_device()}, the current one is {dev}")
+
+    def _params(self, T, dev, gate, **vectors):
+        """The gains, shifts and gate as the C call takes them."""
+        tt = _torch()
+        kind, of, p = 1, None, _NormParams()
+        if self.gate == "channel" and gate is not None:
+            vectors["gate"] = gate
+        for name, t in vectors.items():
+            if t is None:
+                continue
+            code = _type_code(name, t)
+            if of is not None and t.dtype is not of:
+                raise MoEError(MOE_E_INVAL, f"{name}: dtype {t.dtype}, the other gains and shifts have {of}")
+            kind, of = code, t.dtype
+            _on_device(name, t, dev, of, (self.d,))
+            setattr(p, name, t.data_ptr())
+        if gate is not None:
+            if self.gate == "token":
+                _on_device("gate", gate, dev, tt.f32, (T,))
+                p.gate = gate.data_ptr()
+            elif self.gate == "element":
+                p.gate, p.gate_stride = self._rows("gate", gate, T, tt.bf16, dev)
+            elif self.gate == "none":
+                raise MoEError(MOE_E_INVAL, "gate: the handle has none")
+        p.type = kind
+        return p
+
+    def _rows8(self, name, held, T, dev):
+        if held is None:
+            return None
+        codes, scales = held
+        tt = _torch()
+        _on_device(name + " codes", codes, dev, tt.i8, (T, self.d))
+        _on_device(name + " scales", scales, dev, tt.bf16, (T, -(-self.d // self.group)))
+        return ctypes.byref(_Rows8(codes.data_ptr(), scales.data_ptr()))
+
+    def forward(self, residual, y, out, norm, pre_gain=None, pre_shift=None, post_gain=None, post_shift=None, gate=None,
+                stats=None, out8=None, y8=None, stream=None):
+        """residual, out [T, d] bf16 or fp32, y, norm [T, d] bf16 (rows may be columns
+        of a wider buffer).  ``out`` may be ``residual``; ``y`` and ``out`` None: the
+        norm of the residual alone; ``norm`` None where ``pre`` is "none".  ``stats`` [T, 4]
+        fp32 is for backward; ``out8`` and ``y8``, (codes int8 [T, d], scales bf16
+        [T, ceil(d / group)]), keep out and y as 8-bit rows."""
+        tt, dev = _torch(), _current_device()
+        T = residual.shape[0]
+        kind = _type_code("residual", residual)
+        r, r_row = self._rows("residual", residual, T, residual.dtype, dev)
+        yp, y_row = self._rows("y", y, T, tt.bf16, dev)
+        o, o_row = self._rows("out", out, T, residual.dtype, dev)
+        n, n_row = self._rows("norm", norm, T, tt.bf16, dev)
+        if stats is not None:
+            _on_device("stats", stats, dev, tt.f32, (T, 4))
+        p = self._params(T, dev, gate, pre_gain=pre_gain, pre_shift=pre_shift, post_gain=post_gain, post_shift=post_shift)
+        _err(self._c_forward(self.h, T, kind, r, r_row, yp, y_row, ctypes.byref(p), o, o_row, n, n_row,
+                             None if stats is None else stats.data_ptr(), self._rows8("out8", out8, T, dev),
+                             self._rows8("y8", y8, T, dev), _stream_on(stream, dev)))
+        return out, norm
+
+    def _kept(self, name, t, T, dtype, dev):
+        """What was kept of a tensor: as it was, or (codes, scales)."""
+        if isinstance(t, (tuple, list)):
+            return None, 0, self._rows8(name, t, T, dev)
+        return (*self._rows(name, t, T, dtype, dev), None)
+
+    def backward(self, grad_out, grad_norm, grad_residual, grad_y, stats=None, out=None, y=None, pre_gain=None,
+                 pre_shift=None, post_gain=None, post_shift=None, gate=None, grad_gate=None, grad_pre_gain=None,
+                 grad_pre_shift=None, grad_post_gain=None, grad_post_shift=None, stream=None):
+        """grad_out [T, d] (of the residual's type) and grad_norm [T, d] bf16, one of
+        them may be None, and what the forward pass left: ``stats``, ``out`` and ``y``,
+        each as it was or as (codes, scales).  Writes the gradients that are given:
+        grad_residual (of the residual's type; may be grad_out), grad_y bf16, those of
+        gains, shifts and a channel gate fp32 [d], of a token gate fp32 [T], of an
+        element gate bf16 [T, d].  After ``reserve`` where a gradient [d] is wanted."""
+        tt, dev = _torch(), _current_device()
+        if self._device is not None and dev != self._device:
+            raise MoEError(MOE_E_INVAL, f"the workspace is on device {self._device}, the current one is {dev}")
+        some = grad_norm if grad_norm is not None else grad_out
+        if some is None:
+            raise MoEError(MOE_E_INVAL, "grad_out and grad_norm: one of them at least")
+        T = some.shape[0]
+        of = next((t for t in (grad_out, grad_residual, out) if t is not None and not isinstance(t, (tuple, list))), None)
+        dtype = tt.bf16 if of is None else of.dtype
+        kind = 1 if of is None else _type_code("grad_out, grad_residual or out", of)
+        go, go_row = self._rows("grad_out", grad_out, T, dtype, dev)
+        gn, gn_row = self._rows("grad_norm", grad_norm, T, tt.bf16, dev)
+        gr, gr_row = self._rows("grad_residual", grad_residual, T, dtype, dev)
+        gy, gy_row = self._rows("grad_y", grad_y, T, tt.bf16, dev)
+        p = self._params(T, dev, gate, pre_gain=pre_gain, pre_shift=pre_shift, post_gain=post_gain, post_shift=post_shift)
+        kept = _NormKept()
+        kept.out, kept.out_stride, out8 = self._kept("out", out, T, dtype, dev)
+        kept.y, kept.y_stride, y8 = self._kept("y", y, T, tt.bf16, dev)
+        if out8 is not None:
+            kept.out8 = ctypes.cast(out8, _vp)
+        if y8 is not None:
+            kept.y8 = ctypes.cast(y8, _vp)
+        if stats is not None:
+            _on_device("stats", stats, dev, tt.f32, (T, 4))
+            kept.stats = stats.data_ptr()
+        grads = _NormGrads()
+        for name, t in (("pre_gain", grad_pre_gain), ("pre_shift", grad_pre_shift), ("post_gain", grad_post_gain),
+                        ("post_shift", grad_post_shift)):
+            if t is not None:
+                _on_device("grad_" + name, t, dev, tt.f32, (self.d,))
+                setattr(grads, name, t.data_ptr())
+        if grad_gate is not None:
+            if self.gate == "element":
+                grads.gate, grads.gate_stride = self._rows("grad_gate", grad_gate, T, tt.bf16, dev)
+            else:
+                _on_device("grad_gate", grad_gate, dev, tt.f32, (T,) if self.gate == "token" else (self.d,))
+                grads.gate = grad_gate.data_ptr()
+        _err(self._c_backward(self.h, T, kind, go, go_row, gn, gn_row, ctypes.byref(p), ctypes.byref(kept), gr, gr_row,
+                              gy, gy_row, ctypes.byref(grads), _stream_on(stream, dev)))
+        return grad_residual, grad_y
+
+    def close(self):
+        if self.h:
+            lib.moe_norm_destroy(self.h)
             self.h = None
 
     def __del__(self):
