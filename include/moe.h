@@ -632,6 +632,54 @@ int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void*
 
 void moe_norm_destroy(moe_norm_t* h);
 
+/* ------------------------------------------------- the layer for a few tokens
+ *
+ * moe_layer_forward's and moe_layer_forward_routed's operation for 1 to 16 tokens
+ * (decode, speculative decode), in one cooperative kernel that streams the chosen
+ * experts' weights: the same tensors, layouts and limits.  What differs:
+ *   - h is not rounded to bf16 but kept to 16 bits, with its weight w in it;
+ *   - a logit of -inf (a bias of -inf) masks its expert out, as moe_router_forward
+ *     has it; a slot without an expert gets idx -1 and w 0, and adds nothing;
+ *   - a given routing may have empty slots (idx outside [0, E): the rows behind a
+ *     padded batch's last sequence) and may name an expert twice in a row, which
+ *     then counts twice; a row of empty slots gets the shared expert's output, or
+ *     zeros;
+ *   - weights of experts that a token did not choose do not reach it, an infinity
+ *     or a NaN among them neither.
+ * The handle owns a workspace and serves one stream at a time; graphs that may run
+ * at once need handles of their own. */
+typedef struct moe_decode moe_decode_t;
+
+/* Limits: those of moe_layer_create, and f <= 32768.  NULL on anything else. */
+moe_decode_t* moe_decode_create(int d, int f, int E, int k, int shared_experts);
+
+/* Allocate the workspace for up to T_max (1..16) tokens, on the current device.  The
+ * only allocating call; may be called again, on the same device, to grow or shrink
+ * it: a graph captured before that holds the freed one and must not be replayed. */
+int moe_decode_reserve(moe_decode_t* h, int T_max, void* stream);
+
+/* Bytes that moe_decode_reserve(T_max) allocates; -1 for a NULL handle or a T_max
+ * outside 0..16. */
+long long moe_decode_workspace_bytes(const moe_decode_t* h, int T_max);
+
+/* One pass for T tokens, 0 <= T <= T_max (T = 0 does nothing), with the layer's
+ * router.  bias (fp32 [E]) may be NULL; idx [T, k] int32 and w [T, k] fp32, each may
+ * be NULL, get the choice, the larger logit first.  Asynchronous, allocates nothing,
+ * can be captured in a graph.  Outputs must not overlap inputs. */
+int moe_decode_forward(moe_decode_t* h, int T, const void* x, const void* router_w, const float* bias, const void* w_gate,
+                       const void* w_up, const void* w_down, void* out, int32_t* idx, float* w, void* stream);
+
+/* The same on a given routing. */
+int moe_decode_forward_routed(moe_decode_t* h, int T, const void* x, const int32_t* idx, const float* w, const void* w_gate,
+                              const void* w_up, const void* w_down, void* out, void* stream);
+
+/* Synchronise `stream`, then return and clear the device status of the passes
+ * since the last call: MOE_OK, MOE_E_TIMEOUT (a grid-wide wait ran out, the pass's
+ * output is undefined), or MOE_E_CUDA when a CUDA error is pending. */
+int moe_decode_status(moe_decode_t* h, void* stream);
+
+void moe_decode_destroy(moe_decode_t* h);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* moe_last_error(void);
 

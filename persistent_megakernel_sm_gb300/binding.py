@@ -7,7 +7,8 @@ the current CUDA stream, and turns non-zero status codes into ``MoEError``.
 Every step of the layer runs in the library's kernels.  ``MoERouter``,
 ``w4_quantize`` / ``w4_dequantize`` and ``W4Experts`` do the same for the
 routing operator and the 4-bit experts, ``rows8_quantize`` / ``rows8_dequantize``
-and ``MoEBlockNorm`` for 8-bit rows and the norms about a block.
+and ``MoEBlockNorm`` for 8-bit rows and the norms about a block, ``MoEDecode`` for
+the layer at a few tokens.
 """
 from __future__ import annotations
 
@@ -79,6 +80,13 @@ _SIGNATURES = {
     "moe_norm_forward": ([_vp, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64] + [_vp] * 4, _i32),
     "moe_norm_backward": ([_vp, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp], _i32),
     "moe_norm_destroy": ([_vp], None),
+    "moe_decode_create": ([_i32] * 5, _vp),
+    "moe_decode_reserve": ([_vp, _i32, _vp], _i32),
+    "moe_decode_workspace_bytes": ([_vp, _i32], _i64),
+    "moe_decode_forward": ([_vp, _i32] + [_vp] * 10, _i32),
+    "moe_decode_forward_routed": ([_vp, _i32] + [_vp] * 8, _i32),
+    "moe_decode_status": ([_vp, _vp], _i32),
+    "moe_decode_destroy": ([_vp], None),
     "moe_last_error": ([], ctypes.c_char_p),
 }
 
@@ -795,6 +803,85 @@ class MoEBlockNorm:
     def close(self):
         if self.h:
             lib.moe_norm_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class MoEDecode:
+    """The whole layer for 1 to 16 tokens in one kernel (moe_decode_* of include/moe.h)."""
+
+    def __init__(self, d: int, f: int, E: int, k: int, shared_experts: int = 0):
+        self.h = None
+        h = lib.moe_decode_create(d, f, E, k, shared_experts)
+        if not h:
+            raise MoEError(MOE_E_INVAL, (lib.moe_last_error() or b"").decode())
+        self.h = ctypes.c_void_p(h)
+        self.d, self.f, self.E, self.k, self.S = d, f, E, k, shared_experts
+        self._device = None
+        self._c_forward, self._c_routed = lib.moe_decode_forward, lib.moe_decode_forward_routed
+
+    def reserve(self, T_max: int, stream=None):
+        _err(lib.moe_decode_reserve(self.h, T_max, _stream_ptr(stream)))
+        self._device = _current_device()
+
+    def workspace_bytes(self, T_max: int) -> int:
+        return lib.moe_decode_workspace_bytes(self.h, T_max)
+
+    def _check(self, x, w_gate, w_up, w_down, out, dev):
+        if dev != self._device and self._device is not None:
+            raise MoEError(MOE_E_INVAL, f"the workspace is on device {self._device}, the current one is {dev}")
+        bf, n, T = _torch().bf16, self.E + self.S, x.shape[0]
+        _on_device("x", x, dev, bf, (T, self.d))
+        _on_device("w_gate", w_gate, dev, bf, (n, self.f, self.d))
+        _on_device("w_up", w_up, dev, bf, (n, self.f, self.d))
+        _on_device("w_down", w_down, dev, bf, (n, self.d, self.f))
+        _on_device("out", out, dev, bf, (T, self.d))
+        return T
+
+    def forward(self, x, router_w, w_gate, w_up, w_down, out, bias=None, idx=None, w=None, stream=None):
+        """x [T, d] -> out [T, d] with the layer's router; idx [T, k] int32 and w [T, k]
+        fp32, if given, get the choice."""
+        tt, dev = _torch(), _current_device()
+        T = self._check(x, w_gate, w_up, w_down, out, dev)
+        _on_device("router_w", router_w, dev, tt.bf16, (self.E, self.d))
+        if bias is not None:
+            _on_device("bias", bias, dev, tt.f32, (self.E,))
+        if idx is not None:
+            _on_device("idx", idx, dev, tt.i32, (T, self.k))
+        if w is not None:
+            _on_device("w", w, dev, tt.f32, (T, self.k))
+        _err(self._c_forward(self.h, T, x.data_ptr(), router_w.data_ptr(), None if bias is None else bias.data_ptr(),
+                             w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), out.data_ptr(),
+                             None if idx is None else idx.data_ptr(), None if w is None else w.data_ptr(),
+                             _stream_on(stream, dev)))
+        return out
+
+    def forward_routed(self, x, idx, w, w_gate, w_up, w_down, out, stream=None):
+        """The same on a given routing, idx [T, k] int32 and w [T, k] fp32; slots with
+        idx outside [0, E) add nothing."""
+        tt, dev = _torch(), _current_device()
+        T = self._check(x, w_gate, w_up, w_down, out, dev)
+        _on_device("idx", idx, dev, tt.i32, (T, self.k))
+        _on_device("w", w, dev, tt.f32, (T, self.k))
+        _err(self._c_routed(self.h, T, x.data_ptr(), idx.data_ptr(), w.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+                            w_down.data_ptr(), out.data_ptr(), _stream_on(stream, dev)))
+        return out
+
+    def status(self, stream=None) -> int:
+        return lib.moe_decode_status(self.h, _stream_ptr(stream))
+
+    def check(self, stream=None):
+        """Synchronise and raise if a wait inside the kernel ran out."""
+        _err(self.status(stream))
+
+    def close(self):
+        if self.h:
+            lib.moe_decode_destroy(self.h)
             self.h = None
 
     def __del__(self):

@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 REPO = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "_build", "libmoe.so")
-SOURCES = ["moe.cu", "router.cu", "rows8.cu", "norm.cu", "w4.cu"]
+SOURCES = ["moe.cu", "router.cu", "rows8.cu", "norm.cu", "decode.cu", "w4.cu"]
 DEPS = SOURCES + ["tasks.cuh", "layer.cuh", "ptx.cuh", "error.h", "tmap.h", "w4_tiles.cuh", "rows8.cuh"]
 HEADER = os.path.join(REPO, "include", "moe.h")
 

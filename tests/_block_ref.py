@@ -110,3 +110,36 @@ def backward(c, p, gate, stats, grad_out, grad_norm, out, y):
             Ps = ry * (ts + vs * (ts * vs).mean(1, keepdims=True) + (ts.mean(1, keepdims=True) if layer else 0))
     got["y"] = P, Ps
     return got
+
+
+# ------------------------------------------------------- the layer for a few tokens
+
+def choice(x, router_w, bias, k):
+    """idx and w of the layer's router: the larger logit first, the lower expert on ties, -1 for what is masked."""
+    logits = x @ router_w.T + (0 if bias is None else bias)
+    idx = np.argsort(-logits, axis=1, kind="stable")[:, :k].astype(np.int32)
+    top = np.take_along_axis(logits, idx.astype(np.int64), 1)
+    with np.errstate(invalid="ignore"):
+        w = np.where(np.isneginf(top), 0.0, np.exp(top - np.where(np.isneginf(top[:, :1]), 0, top[:, :1])))
+    idx[np.isneginf(top)] = -1
+    total = w.sum(1, keepdims=True)
+    return idx, w / np.where(total > 0, total, 1)
+
+
+def experts(x, idx, w, gate, up, down, shared):
+    """out and a bound on what fp32 sums and a 16-bit h lose of it: 128 roundings of the terms' sum for a product (no
+    chain of sums has as many), and 2^-16 of h."""
+    E = len(gate) - shared
+    out, err = np.zeros_like(x), np.zeros_like(x)
+    rel = 128 * U32
+    slots = [(t, int(e), w[t, j]) for t in range(len(x)) for j, e in enumerate(idx[t]) if 0 <= e < E]
+    slots += [(t, E, 1.0) for t in range(len(x)) if shared]
+    for t, e, wt in slots:
+        z, u = gate[e] @ x[t], up[e] @ x[t]
+        ez, eu = rel * (np.abs(gate[e]) @ np.abs(x[t])), rel * (np.abs(up[e]) @ np.abs(x[t]))
+        s = z / (1 + np.exp(-z))
+        h = s * u
+        eh = 1.1 * ez * (np.abs(u) + eu) + np.abs(s) * eu + (2.0 ** -16 + 16 * U32) * np.abs(h)
+        out[t] += wt * (down[e] @ h)
+        err[t] += np.abs(wt) * (np.abs(down[e]) @ (eh + rel * np.abs(h)))
+    return out, err
