@@ -10,13 +10,16 @@
 //      h' = w silu(Wg x) (Wu x) for its share of the experts' f rows   grid-wide wait
 //   3  out = sum over the listed experts of Wd h' for its share of the d rows: no
 //      block needs another's sums, so there is no combine
-// A product's tile is 16 weight rows times 8 or 16 token columns (gate and up: 8 rows
-// of each, so that a lane has both for its values) on mma.sync m16n8k16.  The tensor
-// cores are nearly idle here; they are used because a multiply-add for every weight
-// and token would not keep up with HBM.  Weights go from HBM straight to the
-// registers that the mma takes: a lane loads 16 bytes of a row, which the mma sees
-// as another order of the same columns, the same for tokens.  A block's 16 warps
-// split the columns; each loads a step ahead, and their sums meet in shared memory.
+// A product's tile is 32 weight rows (16 of gate and 16 of up) times 8 or 16 token
+// columns on mma.sync m16n8k16.  The tensor cores are nearly idle here; they are used
+// because a multiply-add for every weight and token would not keep up with HBM.  A
+// stage is 512 columns of a tile and of the tokens that its expert has.  Four warps of
+// a block bring its weights by bulk copies, four more the tokens' columns, into a ring of
+// single rows (160 to 180 KB an SM on their way, whatever a stage has of them); the
+// weights do not wait for the grid, so the ring is full of down's first ones when h' is
+// complete.  Eight warps, in teams that take stages by turns, multiply, and their sums
+// meet in shared memory once a tile.  A lane reads 16 bytes of a row at once, which the
+// mma sees as another order of the same columns, the same for the tokens'.
 //
 // Columns are the tokens themselves.  A token that did not choose an expert has a
 // zero column there and takes nothing from its sums, which are kept apart expert by
@@ -31,8 +34,8 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <atomic>
 #include <new>
+#include <type_traits>
 
 #include "error.h"
 #include "moe.h"
@@ -43,9 +46,17 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kMaxT = 16, kMaxK = 16, kMaxE = 256, kMaxD = 32768;
-constexpr int kWarps = 16, kThreads = kWarps * 32;
-constexpr int kBlock = 32;     // columns of a step's block: two mma
-constexpr int kColumn = 20;    // floats of a token's column of a tile: 16, and 4 so that its lanes miss each other's banks
+constexpr int kWarps = 8, kConsumers = kWarps * 32;
+constexpr int kTeams = 2, kTeam = kWarps / kTeams;
+constexpr int kBringers = 4;     // warps that bring weights, and as many that bring tokens
+constexpr int kThreads = kConsumers + 2 * kBringers * 32;
+constexpr int kBlock = 32;       // columns of two mma
+constexpr int kRows = 32;        // of a tile: gate and up 16 each
+constexpr int kChunk = 512;      // columns of a stage
+constexpr int kBlocks = kChunk / kBlock / kTeam;  // of a warp
+constexpr int kPitch = kChunk * 2 + 64;  // bytes of a row: two rows next to each other use all banks
+constexpr int kColumn = 36;      // floats of a token's column of sums: 32, and 4 so that its lanes miss each other's banks
+constexpr int kStages = 16;      // on their way, at most
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
@@ -73,6 +84,7 @@ struct List {
   int expert[kMaxE + 1];
   int start[kMaxE + 1];           // of its slots
   uint32_t tokens[kMaxE + 1];     // that chose it
+  uint8_t order[kMaxE + 1][kMaxT];  // the same, one after another
   float w[kMaxE + 1][kMaxT];      // their weights
   int place[kMaxE];               // of an expert in the list, -1
   int idx[kMaxT][kMaxK];
@@ -98,9 +110,15 @@ __device__ __forceinline__ void mma_block(float (&c)[4], const uint4 (&a)[2], ui
   mma(c, a[0].z, a[1].z, a[0].w, a[1].w, b.z, b.w);
 }
 
-// Every block arrives; false if the wait ran out somewhere.
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(moe::smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
+
+// Every block's consumers arrive; false if the wait ran out somewhere.
 __device__ bool grid_wait(Sched* s, int gen, uint64_t deadline, int* ok) {
-  __syncthreads();
+  sync_consumers();
   if (threadIdx.x == 0) {
     *ok = 1;
     __threadfence();
@@ -119,7 +137,7 @@ __device__ bool grid_wait(Sched* s, int gen, uint64_t deadline, int* ok) {
     }
     __threadfence();
   }
-  __syncthreads();
+  sync_consumers();
   return *ok != 0;
 }
 
@@ -183,13 +201,13 @@ __device__ void choose(const Decode& p, List* list, int t) {
 // The experts that the tokens chose, in order, with their tokens and weights.
 __device__ void make_list(const Decode& p, List* list) {
   const int tid = threadIdx.x, lane = tid & 31;
-  for (int e = tid; e < p.E; e += kThreads) list->place[e] = -1;
-  __syncthreads();
-  for (int i = tid; i < p.T * p.k; i += kThreads) {
+  for (int e = tid; e < p.E; e += kConsumers) list->place[e] = -1;
+  sync_consumers();
+  for (int i = tid; i < p.T * p.k; i += kConsumers) {
     const int e = list->idx[i / p.k][i % p.k];
     if ((unsigned)e < (unsigned)p.E) list->place[e] = 0;
   }
-  __syncthreads();
+  sync_consumers();
   if (tid < 32) {
     int n = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -204,11 +222,11 @@ __device__ void make_list(const Decode& p, List* list) {
       list->n = n + p.S;
     }
   }
-  __syncthreads();
+  sync_consumers();
   const int n = list->n;
-  for (int i = tid; i < n * kMaxT; i += kThreads) list->w[i / kMaxT][i % kMaxT] = 0.f;
-  for (int i = tid; i < n; i += kThreads) list->tokens[i] = p.S && i == n - 1 ? (1u << p.T) - 1u : 0u;
-  __syncthreads();
+  for (int i = tid; i < n * kMaxT; i += kConsumers) list->w[i / kMaxT][i % kMaxT] = 0.f;
+  for (int i = tid; i < n; i += kConsumers) list->tokens[i] = p.S && i == n - 1 ? (1u << p.T) - 1u : 0u;
+  sync_consumers();
   if (tid < p.T) {  // a token's slots in order: an expert named twice has both weights
     for (int j = 0; j < p.k; ++j) {
       const int e = list->idx[tid][j];
@@ -219,11 +237,13 @@ __device__ void make_list(const Decode& p, List* list) {
     }
     if (p.S) list->w[n - 1][tid] = 1.f;
   }
-  __syncthreads();
+  sync_consumers();
   if (tid < 32) {
     int base = 0;
     for (int i0 = 0; i0 < n; i0 += 32) {
       const int mine = i0 + lane < n ? __popc(list->tokens[i0 + lane]) : 0;
+      for (int j = 0, left = mine ? (int)list->tokens[i0 + lane] : 0; left; ++j, left &= left - 1)
+        list->order[i0 + lane][j] = (uint8_t)(__ffs(left) - 1);
       int sum = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -234,278 +254,430 @@ __device__ void make_list(const Decode& p, List* list) {
       base += __shfl_sync(kAll, sum, 31);
     }
   }
-  __syncthreads();
+  sync_consumers();
 }
 
-// A tile's place: its two row blocks' first rows and how many of them there are.
-struct Tile {
-  const bf16 *lo, *hi;   // row 0 of rows 0..7 and of rows 8..15
-  int n_lo, n_hi;        // rows that are there
-  int at, first;         // list entry (phase 2), first row of the matrix
-};
-
-// Warps' sums of the tiles of a batch; two batches, so that one wait a batch is enough.
+// Warps' sums of a tile; two tiles' worth, so that one wait a tile is enough.
 template <int NT>
 struct Sums {
-  static constexpr int kTiles = 4 / NT, kTile = NT * 8 * kColumn;
-  float v[2][kTiles][kWarps][kTile];
+  static constexpr int kTile = NT * 8 * kColumn;
+  float v[2][kWarps][kTile];
 };
 
 template <int NT>
-__device__ __forceinline__ void put_sums(float* to, const float (&acc)[NT][4]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float* c = to + (n * 8 + 2 * t) * kColumn + g;
-    c[0] = acc[n][0], c[kColumn] = acc[n][1], c[8] = acc[n][2], c[kColumn + 8] = acc[n][3];
-  }
-}
-
-// The tiles [0, n) of a block's share.  Each warp goes over its column blocks
-// [b0, b1) of every tile, U at a time, the next step's loads under way while this
-// one's mma run.  tile(i) gives a tile, load_b(tile, block, b) the token columns of a
-// block, row(block) its offset from a row block's first row, change(block) whether a
-// block begins another expert's columns, whose sums `keep` adds up, and end(i, row,
-// token, sum) takes a finished sum, all threads of the block together.
-template <int NT, int NB, int U, typename TileOf, typename RowPtr, typename LoadB, typename Close, typename End>
-__device__ __forceinline__ void run_tiles(int n, int b0, int b1, int stride, Sums<NT>* sums, TileOf&& tile_of, RowPtr&& at,
-                                          LoadB&& load_b, Close&& close, End&& end) {
-  using S = Sums<NT>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c8 = (lane & 3) * 8;
-  uint4 a[2][U][2], b[2][U][NB];
-  Tile now, next;
-  auto load = [&](int buf, const Tile& tile, int block) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool there = block + u < b1;
-      const long long o = there ? at(block + u) + (long long)g * stride + c8 : 0;
-      a[buf][u][0] = there && g < tile.n_lo ? load_weights(tile.lo + o) : make_uint4(0, 0, 0, 0);
-      a[buf][u][1] = there && g < tile.n_hi ? load_weights(tile.hi + o) : make_uint4(0, 0, 0, 0);
-      if (there) {
-        load_b(tile, block + u, b[buf][u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NB; ++i) b[buf][u][i] = make_uint4(0, 0, 0, 0);
-      }
-    }
-  };
-  if (n == 0) return;
-  float total[NT][4] = {};
-  int i = 0, block = b0;
-  now = tile_of(0);
-  load(0, now, block);
-  auto step = [&](auto which) {
-    constexpr int buf = decltype(which)::value;
-    const bool last = block + U >= b1;
-    int i2 = i, block2 = block + U;
-    if (last) {
-      i2 = i + 1, block2 = b0;
-      if (i2 < n) next = tile_of(i2);
-    } else {
-      next = now;
-    }
-    if (i2 < n) load(buf ^ 1, next, block2);
-    float part[NT][4] = {};
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int q = 0; q < NB; ++q) mma_block(part[q % NT], a[buf][u], b[buf][u][q]);
-      // the sums so far are one expert's, or the step's end
-      if (u == U - 1 || close(block + u)) {
-        const uint32_t tokens = close.tokens(now, block + u);
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          const int t0 = q * 8 + (lane & 3) * 2;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (tokens >> (t0 + (j & 1)) & 1u) total[q][j] += part[q][j];
-            part[q][j] = 0.f;
-          }
-        }
-      }
-    }
-    if (last) {
-      const int in = i % S::kTiles, batch = i / S::kTiles & 1;
-      put_sums<NT>(sums->v[batch][in][warp], total);
-#pragma unroll
-      for (int q = 0; q < NT; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) total[q][j] = 0.f;
-      if (in == S::kTiles - 1 || i == n - 1) {
-        __syncthreads();
-        const int tid = threadIdx.x, first = i - in;  // 16 rows x 8 NT tokens x kTiles: a thread each
-        const int mine = tid / (NT * 128), token = tid / 16 % (NT * 8), row = tid & 15;
-        float s = 0.f;
-        if (mine <= in) {
-          const float* c = &sums->v[batch][mine][0][token * kColumn + row];
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) s += c[w * S::kTile];
-        }
-        end(first + mine, mine <= in, row, token, s);
-      }
-    }
-    i = i2, block = block2, now = next;
-  };
-  while (true) {
-    step(std::integral_constant<int, 0>{});
-    if (i >= n) break;
-    step(std::integral_constant<int, 1>{});
-    if (i >= n) break;
-  }
-  __syncthreads();  // the sums' memory is free again
-}
-
-// run_tiles' `close` where all columns are one product's.
-struct OneProduct {
-  uint32_t all;
-  __device__ __forceinline__ bool operator()(int) const { return false; }
-  __device__ __forceinline__ uint32_t tokens(const Tile&, int) const { return all; }
+struct Smem {
+  static constexpr int kRing = NT == 1 ? 168 : 152;  // rows; a stage has 64 at most
+  char ring[kRing][kPitch];
+  Sums<NT> sums;
+  List list;
+  uint64_t full[kStages], empty[kStages], h_ready;
+  int abort;  // a wait ran out: nothing more is brought
 };
 
-// Columns run through the listed experts' f, one after another.
-struct ByExpert {
-  const List* list;
-  int blocks;  // of an expert
-  __device__ __forceinline__ bool operator()(int block) const { return (block + 1) % blocks == 0; }
-  __device__ __forceinline__ uint32_t tokens(const Tile&, int block) const {
-    const int at = block / blocks;
-    return at < list->n ? list->tokens[at] : 0u;
+// Where one side of the ring stands: the stage's barriers and its first row.
+template <int RING>
+struct At {
+  int stage = 0, row = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int rows) {
+    if (++stage == kStages) stage = 0, parity ^= 1;
+    row += rows;
+    if (row >= RING) row -= RING;
+  }
+  __device__ __forceinline__ int at(int i) const { return row + i >= RING ? row + i - RING : row + i; }
+};
+
+// A bringing warp's view of what is free: a stage's rows are the consumers' until its
+// `empty` completes.
+template <int NT>
+struct Room {
+  Smem<NT>* sm;
+  uint64_t deadline;
+  At<Smem<NT>::kRing> at;        // of the next stage
+  int oldest = 0, out = 0, used = 0;
+  uint32_t oldest_parity = 0;
+  int rows_of = 0;               // lane i: rows of the stage on barriers i
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+    bool done = false;
+    while (!done && !*static_cast<volatile int*>(&sm->abort)) {
+      for (int i = 0; i < 32 && !done; ++i) done = moe::mbar_try_wait(bar, parity);
+      if (!done && moe::globaltimer() > deadline) break;
+    }
+    return __all_sync(kAll, done);
+  }
+  // room for a stage of `rows`; false if the wait ran out
+  __device__ __forceinline__ bool make(int rows) {
+    while (used + rows > Smem<NT>::kRing || out == kStages) {
+      if (!wait(&sm->empty[oldest], oldest_parity)) return false;
+      used -= __shfl_sync(kAll, rows_of, oldest);
+      --out;
+      if (++oldest == kStages) oldest = 0, oldest_parity ^= 1;
+    }
+    return true;
+  }
+  __device__ __forceinline__ void take(int rows) {
+    if ((threadIdx.x & 31) == at.stage) rows_of = rows;
+    used += rows, ++out;
+    at.next(rows);
+  }
+};
+
+// A block's share of the experts' f rows, in tiles of 16 (of gate and of up) that end
+// where an expert's end.
+struct GateUpTiles {
+  int f, r0, r1, a0, lead, lead_tiles, per, n;
+
+  __device__ __forceinline__ GateUpTiles(int f_, int r0_, int r1_) : f(f_), r0(r0_), r1(r1_) {
+    a0 = r0 / f;
+    lead = min(r1, (a0 + 1) * f) - r0;  // rows of the first expert
+    lead_tiles = (lead + 15) / 16, per = f / 16;
+    const int rest = r1 - r0 - lead;
+    n = r1 > r0 ? lead_tiles + rest / f * per + (rest % f + 15) / 16 : 0;
+  }
+  // list entry, its first row there, rows
+  __device__ __forceinline__ void get(int i, int* at, int* first, int* rows) const {
+    int row, end;
+    if (i < lead_tiles) {
+      row = r0 + 16 * i, end = r0 + lead;
+    } else {
+      const int q = (i - lead_tiles) / per;
+      row = (a0 + 1 + q) * f + (i - lead_tiles) % per * 16;
+      end = min(r1, (a0 + 2 + q) * f);
+    }
+    *at = row / f, *first = row % f, *rows = min(16, end - row);
   }
 };
 
 __device__ __forceinline__ int share(long long total, int part, int parts) { return (int)(total * part / parts); }
 
+// What a stage is: weight rows (and how many of them are there), the tokens that it is
+// for, and how many rows each of them has (h': two).
+struct Stage {
+  int rows, tokens, parts, columns;
+  __device__ __forceinline__ int all() const { return rows + parts * __popc(tokens); }
+};
+
+// The consumers' side of `tiles` tiles of `chunks` stages each.  stage(tile, c) says
+// what a stage is, high(tile) where its rows 16 to 31 begin; end(tile, row, token,
+// sum) takes each finished sum, all threads together.  A wait that runs out leaves its
+// mark in `abort`; no barrier of the block is left out.
+template <int NT, int PARTS, typename StageOf, typename High, typename End>
+__device__ __forceinline__ void consume(Smem<NT>* sm, At<Smem<NT>::kRing>& at, int& turn, int tiles, int chunks, uint64_t deadline,
+                                        int* status, StageOf&& stage_of, High&& high, End&& end) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int team = warp / kTeam, member = warp % kTeam;
+  bool fine = true;
+  for (int i = 0; i < tiles; ++i) {
+    float total[2][NT][4] = {};
+    const int hi = high(i);
+    for (int c = 0; c < chunks; ++c) {
+      const Stage st = stage_of(i, c);
+      if (turn == team) {
+        fine = fine && moe::mbar_wait(&sm->full[at.stage], at.parity, deadline);
+        const char* a_rows[2][2];
+        const char* b_rows[PARTS * NT];
+        const int in_row = t * 16 + member * (kBlocks * kBlock * 2);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          a_rows[m][0] = sm->ring[at.at(8 * m + g)] + in_row;
+          a_rows[m][1] = sm->ring[at.at(hi + 8 * m + g)] + in_row;
+        }
+        const int n = __popc(st.tokens);
+#pragma unroll
+        for (int q = 0; q < PARTS * NT; ++q) {
+          const int token = q % NT * 8 + g;
+          b_rows[q] = st.tokens >> token & 1
+                          ? sm->ring[at.at(st.rows + q / NT * n + __popc(st.tokens & ((1 << token) - 1)))] + in_row : nullptr;
+        }
+        float part[2][NT][4] = {};
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u) {
+          if ((member * kBlocks + u) * kBlock >= st.columns) break;
+          uint4 b[PARTS * NT];
+#pragma unroll
+          for (int q = 0; q < PARTS * NT; ++q)
+            b[q] = b_rows[q] ? *reinterpret_cast<const uint4*>(b_rows[q] + u * kBlock * 2) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint4 a[2] = {*reinterpret_cast<const uint4*>(a_rows[m][0] + u * kBlock * 2),
+                                *reinterpret_cast<const uint4*>(a_rows[m][1] + u * kBlock * 2)};
+#pragma unroll
+            for (int q = 0; q < PARTS * NT; ++q) mma_block(part[m][q % NT], a, b[q]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->empty[at.stage]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int q = 0; q < NT; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (st.tokens >> (q * 8 + t * 2 + (j & 1)) & 1) total[m][q][j] += part[m][q][j];
+      }
+      at.next(st.all());
+      if (++turn == kTeams) turn = 0;
+    }
+    float* mine = sm->sums.v[i & 1][warp];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        float* to = mine + (q * 8 + 2 * t) * kColumn + 8 * m + g;
+        to[0] = total[m][q][0], to[kColumn] = total[m][q][1], to[16] = total[m][q][2], to[kColumn + 16] = total[m][q][3];
+      }
+    sync_consumers();
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {  // 32 rows of 8 tokens: a thread each
+      const int row = lane, token = q * 8 + warp;
+      const float* from = sm->sums.v[i & 1][0] + token * kColumn + row;
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += from[w * Sums<NT>::kTile];
+      end(i, row, token, s);
+    }
+  }
+  if (!fine) {
+    *status = MOE_E_TIMEOUT;
+    *static_cast<volatile int*>(&sm->abort) = 1;
+  }
+}
+
+// The router's logits: a block's share of its rows, each lane 8 columns at a time.
+template <int NT>
+__device__ __forceinline__ void logits(const Decode& p, Smem<NT>* sm, int e0, int e1) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int nkb = p.d / kBlock, b0 = share(nkb, warp, kWarps), b1 = share(nkb, warp + 1, kWarps);
+  for (int e = e0; e < e1; e += 8) {  // rows 8 to 15 of the mma are not used
+    float total[NT][4] = {};
+    constexpr int U = 4;
+    for (int kb = b0; kb < b1; kb += U) {
+      uint4 a[U][2], b[U][NT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int col = (kb + u) * kBlock + t * 8;
+        const bool there = kb + u < b1;
+        a[u][1] = make_uint4(0, 0, 0, 0);
+        a[u][0] = there && e + g < e1 ? load_weights(p.router_w + (size_t)(e + g) * p.d + col) : a[u][1];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          b[u][n] = there && n * 8 + g < p.T ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(n * 8 + g) * p.d + col)) : a[u][1];
+      }
+      float part[NT][4] = {};
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_block(part[n], a[u], b[u][n]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) total[n][j] += part[n][j];
+    }
+    float* mine = sm->sums.v[0][warp];
+    sync_consumers();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) mine[(n * 8 + 2 * t + j) * kColumn + g] = total[n][j];
+    sync_consumers();
+    const int row = tid & 7, token = tid >> 3;
+    if (token < p.T && e + row < e1) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += sm->sums.v[0][w][token * kColumn + row];
+      p.logits[token * p.E + e + row] = s + (p.bias ? p.bias[e + row] : 0.f);
+    }
+  }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constant__ Decode p) {
-  extern __shared__ __align__(16) char smem[];
-  Sums<NT>* sums = reinterpret_cast<Sums<NT>*>(smem);
-  List* list = reinterpret_cast<List*>(smem + sizeof(Sums<NT>));
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c8 = (lane & 3) * 8;
+  extern __shared__ __align__(128) char smem_raw[];
+  Smem<NT>* sm = reinterpret_cast<Smem<NT>*>(smem_raw);
+  List* list = &sm->list;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int block = blockIdx.x, blocks = gridDim.x;
   const uint64_t deadline = moe::globaltimer() + kLimitNs;
-  int gen = tid == 0 ? moe::ld_acquire(&p.sched->gen) : 0;
-  const int nkb = p.d / kBlock;
-
-  auto load_x = [&](uint32_t tokens, int kb, uint4 (&b)[NT]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int t = n * 8 + g;
-      b[n] = tokens >> t & 1u ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)t * p.d + kb * kBlock + c8))
-                              : make_uint4(0, 0, 0, 0);
+  const bool producer = warp >= kWarps;
+  if (tid < kStages) {
+    moe::mbar_init(&sm->full[tid], kBringers + kBringers * 32);
+    moe::mbar_init(&sm->empty[tid], kTeam);
+    if (tid == 0) moe::mbar_init(&sm->h_ready, 1);
+    moe::fence_mbar_init();
+  }
+  if (tid == 0) sm->abort = 0;
+  bool fine = true;
+  int gen = 0;
+  if (!producer) {
+    gen = tid == 0 ? moe::ld_acquire(&p.sched->gen) : 0;
+    if (p.router_w) {  // 1: logits, and the choice
+      logits<NT>(p, sm, share(p.E, block, blocks), share(p.E, block + 1, blocks));
+      fine = grid_wait(p.sched, gen++, deadline, &list->ok);
+      if (fine)
+        for (int t = warp; t < p.T; t += kWarps) choose(p, list, t);
+    } else {
+      for (int i = tid; i < p.T * p.k; i += kConsumers) {
+        list->idx[i / p.k][i % p.k] = p.idx_in[i];
+        list->idx_w[i / p.k][i % p.k] = p.w_in[i];
+      }
     }
-  };
-  const uint32_t all = (1u << p.T) - 1u;
-
-  // 1: logits
-  if (p.router_w) {
-    const int e0 = share(p.E, block, blocks), e1 = share(p.E, block + 1, blocks);
-    auto tile_of = [&](int i) {
-      const int e = e0 + 16 * i;
-      const bf16* row = p.router_w + (size_t)e * p.d;
-      return Tile{row, row + 8 * p.d, min(8, e1 - e), min(8, max(0, e1 - e - 8)), 0, e};
-    };
-    run_tiles<NT, NT, 2>((e1 - e0 + 15) / 16, share(nkb, warp, kWarps), share(nkb, warp + 1, kWarps), p.d, sums, tile_of,
-                         [](int kb) { return kb * kBlock; },
-                         [&](const Tile&, int kb, uint4 (&b)[NT]) { load_x(all, kb, b); }, OneProduct{all},
-                         [&](int i, bool there, int row, int token, float s) {
-                           const int e = e0 + 16 * i + row;
-                           if (there && e < e1 && token < p.T) p.logits[token * p.E + e] = s + (p.bias ? p.bias[e] : 0.f);
-                         });
-    if (!grid_wait(p.sched, gen++, deadline, &list->ok)) return;
-    if (warp < p.T) choose(p, list, warp);
-  } else {
-    for (int i = tid; i < p.T * p.k; i += kThreads) {
-      list->idx[i / p.k][i % p.k] = p.idx_in[i];
-      list->idx_w[i / p.k][i % p.k] = p.w_in[i];
+    sync_consumers();
+    if (fine) {
+      if (block == 0 && p.router_w)
+        for (int i = tid; i < p.T * p.k; i += kConsumers) {
+          if (p.idx_out) p.idx_out[i] = list->idx[i / p.k][i % p.k];
+          if (p.w_out) p.w_out[i] = list->idx_w[i / p.k][i % p.k];
+        }
+      make_list(p, list);
     }
+    if (tid == 0 && !fine) sm->abort = 1;
   }
   __syncthreads();
-  if (block == 0 && p.router_w)
-    for (int i = tid; i < p.T * p.k; i += kThreads) {
-      if (p.idx_out) p.idx_out[i] = list->idx[i / p.k][i % p.k];
-      if (p.w_out) p.w_out[i] = list->idx_w[i / p.k][i % p.k];
-    }
-  make_list(p, list);
+  if (sm->abort) return;  // nothing is on its way yet
 
-  // 2: gate and up
-  {
-    const long long rows = (long long)list->n * p.f;
-    const int r0 = share(rows, block, blocks), r1 = share(rows, block + 1, blocks);
-    // tiles of 8 rows from r0 on, none over an expert's end
-    const int a0 = r0 / p.f, lead = min(r1, (a0 + 1) * p.f) - r0;  // rows of the first expert
-    const int lead_tiles = (lead + 7) / 8, per = p.f / 8;
-    const int rest = r1 - r0 - lead;
-    auto tile_of = [&](int i) {
-      int row, end;
-      if (i < lead_tiles) {
-        row = r0 + 8 * i, end = r0 + lead;
-      } else {
-        const int q = (i - lead_tiles) / per;
-        row = (a0 + 1 + q) * p.f + (i - lead_tiles) % per * 8;
-        end = min(r1, (a0 + 2 + q) * p.f);
+  const long long rows = (long long)list->n * p.f;
+  const GateUpTiles gate_up(p.f, share(rows, block, blocks), share(rows, block + 1, blocks));
+  const int d0 = share(p.d, block, blocks), d1 = share(p.d, block + 1, blocks);
+  const int down_tiles = (d1 - d0 + kRows - 1) / kRows;
+  const int x_chunks = (p.d + kChunk - 1) / kChunk, f_chunks = (p.f + kChunk - 1) / kChunk;
+  volatile int* abort = &sm->abort;
+  const int n_list = list->n;
+
+  if (producer) {
+    Room<NT> room{sm, deadline};
+    const int bringer = warp - kWarps;
+    bool go = true;
+    if (bringer < kBringers) {
+      const int mine = lane * kBringers + bringer;  // the lane's row of a tile
+      int issued = 0;
+      // a stage: `row` is the lane's weight row at the chunk
+      auto bring = [&](const Stage& st, const bf16* row) {
+        const int rows = st.all();
+        if (!room.make(rows)) return false;
+        const bool there = mine < st.rows;
+        const unsigned all = __ballot_sync(kAll, there);
+        uint64_t* full = &sm->full[room.at.stage];
+        moe::fence_proxy_async_shared();  // tokens' copies may have been in these rows before
+        if (lane == 0) moe::mbar_arrive_expect_tx(full, (uint32_t)__popc(all) * st.columns * 2);
+        __syncwarp();
+        if (there) moe::bulk_load(sm->ring[room.at.at(mine)], row, (uint32_t)st.columns * 2, full);
+        room.take(rows);
+        ++issued;
+        return true;
+      };
+      for (int i = 0; go && i < gate_up.n; ++i) {
+        int a, first, n;
+        gate_up.get(i, &a, &first, &n);
+        const bf16* base = (mine < n ? p.gate : p.up) + ((size_t)list->expert[a] * p.f + first + (mine < n ? mine : mine - n)) * p.d;
+        const int tokens = (int)list->tokens[a];
+        for (int c = 0; go && c < x_chunks; ++c)
+          go = bring(Stage{2 * n, tokens, 1, min(kChunk, p.d - c * kChunk)}, base + c * kChunk);
       }
-      const int at = row / p.f, n = min(8, end - row);
-      const size_t o = ((size_t)list->expert[at] * p.f + row % p.f) * p.d;
-      return Tile{p.gate + o, p.up + o, n, n, at, row % p.f};
+      for (int i = 0; go && i < down_tiles; ++i) {
+        const int first = d0 + i * kRows, n = min(kRows, d1 - first);
+        for (int a = 0; go && a < n_list; ++a) {
+          const bf16* base = p.down + ((size_t)list->expert[a] * p.d + first + mine) * p.f;
+          const int tokens = (int)list->tokens[a];
+          for (int c = 0; go && c < f_chunks; ++c)
+            go = bring(Stage{n, tokens, 2, min(kChunk, p.f - c * kChunk)}, base + c * kChunk);
+        }
+      }
+      // what is on its way arrives before the block ends, whatever became of the others
+      const uint64_t last = moe::globaltimer() + kLimitNs;
+      for (int i = max(0, issued - kStages); i < issued; ++i)
+        moe::mbar_wait(&sm->full[i % kStages], (uint32_t)(i / kStages) & 1u, last);
+      return;
+    }
+    // the tokens' columns: a warp brings a quarter of them, 16 bytes a lane, two rows at once
+    constexpr int kPart = kChunk / kBringers, kLanes = kPart / 8;
+    const int part = (bringer - kBringers) * kPart, sub = lane / kLanes, in_part = lane % kLanes * 8;
+    // x's rows are the entry's tokens, h's its slots
+    auto bring = [&](const Stage& st, const bf16* base, const bf16* base2, size_t stride, const uint8_t* order) {
+      const int rows = st.all();
+      if (!room.make(rows)) return false;
+      const int n = __popc(st.tokens), all = rows - st.rows;
+      if (part + in_part < st.columns) {
+#pragma unroll 4
+        for (int j = sub; j < all; j += 32 / kLanes) {
+          const int slot = j < n ? j : j - n;
+          const bf16* row = (j < n ? base : base2) + (size_t)(order ? order[slot] : slot) * stride;
+          moe::cp_async16(sm->ring[room.at.at(st.rows + j)] + (part + in_part) * 2, row + part + in_part);
+        }
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(moe::smem_u32(&sm->full[room.at.stage])) : "memory");
+      room.take(rows);
+      return true;
     };
-    const int tiles = r1 > r0 ? lead_tiles + rest / p.f * per + (rest % p.f + 7) / 8 : 0;
-    struct ByTile {
-      const List* list;
-      __device__ __forceinline__ bool operator()(int) const { return false; }
-      __device__ __forceinline__ uint32_t tokens(const Tile& t, int) const { return list->tokens[t.at]; }
-    };
-    run_tiles<NT, NT, NT == 1 ? 4 : 2>(
-        tiles, share(nkb, warp, kWarps), share(nkb, warp + 1, kWarps), p.d, sums, tile_of,
-        [](int kb) { return kb * kBlock; },
-        [&](const Tile& t, int kb, uint4 (&b)[NT]) { load_x(list->tokens[t.at], kb, b); }, ByTile{list},
-        [&](int i, bool there, int row, int token, float s) {
-          const float up = __shfl_xor_sync(kAll, s, 8);  // rows 8 to 15 are up's
-          if (!there || row >= 8) return;
-          const Tile t = tile_of(i);
-          const uint32_t tokens = list->tokens[t.at];
-          if (row >= t.n_lo || !(tokens >> token & 1u)) return;
-          const float h = s / (1.f + expf(-s)) * up * list->w[t.at][token];
-          const size_t slot = list->start[t.at] + __popc(tokens & ((1u << token) - 1u));
-          const bf16 hi = __float2bfloat16_rn(h);
-          p.h_hi[slot * p.f + t.first + row] = hi;
-          // an infinity or a NaN is all in the first part
-          const float rest = h - __bfloat162float(hi);
-          p.h_lo[slot * p.f + t.first + row] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-        });
+    for (int i = 0; go && i < gate_up.n; ++i) {
+      int a, first, n;
+      gate_up.get(i, &a, &first, &n);
+      const int tokens = (int)list->tokens[a];
+      for (int c = 0; go && c < x_chunks; ++c)
+        go = bring(Stage{2 * n, tokens, 1, min(kChunk, p.d - c * kChunk)}, p.x + c * kChunk, nullptr, p.d, list->order[a]);
+    }
+    go = go && room.wait(&sm->h_ready, 0);
+    for (int i = 0; go && i < down_tiles; ++i) {
+      const int n = min(kRows, d1 - d0 - i * kRows);
+      for (int a = 0; go && a < n_list; ++a) {
+        const int tokens = (int)list->tokens[a];
+        const size_t at = (size_t)list->start[a] * p.f;
+        for (int c = 0; go && c < f_chunks; ++c)
+          go = bring(Stage{n, tokens, 2, min(kChunk, p.f - c * kChunk)}, p.h_hi + at + c * kChunk, p.h_lo + at + c * kChunk,
+                     p.f, nullptr);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
   }
-  if (!grid_wait(p.sched, gen++, deadline, &list->ok)) return;
+
+  At<Smem<NT>::kRing> at;
+  int turn = 0;
+  // 2: gate and up
+  consume<NT, 1>(
+      sm, at, turn, gate_up.n, x_chunks, deadline, &p.sched->status,
+      [&](int i, int c) {
+        int a, first, n;
+        gate_up.get(i, &a, &first, &n);
+        return Stage{2 * n, (int)list->tokens[a], 1, min(kChunk, p.d - c * kChunk)};
+      },
+      [&](int i) {
+        int a, first, n;
+        gate_up.get(i, &a, &first, &n);
+        return n;
+      },
+      [&](int i, int row, int token, float s) {
+        const float up = __shfl_xor_sync(kAll, s, 16);  // rows 16 to 31 are up's
+        int a, first, n;
+        gate_up.get(i, &a, &first, &n);
+        const uint32_t tokens = list->tokens[a];
+        if (row >= n || !(tokens >> token & 1u)) return;
+        const float h = s / (1.f + expf(-s)) * up * list->w[a][token];
+        const size_t slot = list->start[a] + __popc(tokens & ((1u << token) - 1u));
+        const bf16 hi = __float2bfloat16_rn(h);
+        p.h_hi[slot * p.f + first + row] = hi;
+        // an infinity or a NaN is all in the first part
+        const float rest = h - __bfloat162float(hi);
+        p.h_lo[slot * p.f + first + row] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+      });
+  if (!grid_wait(p.sched, gen++, deadline, &list->ok) || *abort) {
+    if (tid == 0) *abort = 1;
+    return;
+  }
+  if (tid == 0) mbar_arrive(&sm->h_ready);
 
   // 3: down
-  {
-    const int r0 = share(p.d, block, blocks), r1 = share(p.d, block + 1, blocks);
-    const int per = p.f / kBlock;
-    const long long nb = (long long)list->n * per;
-    auto tile_of = [&](int i) {
-      const int row = r0 + 16 * i;
-      const bf16* at = p.down + (size_t)row * p.f;
-      return Tile{at, at + 8 * (size_t)p.f, min(8, r1 - row), min(8, max(0, r1 - row - 8)), 0, row};
-    };
-    run_tiles<NT, 2 * NT, 2>(
-        (r1 - r0 + 15) / 16, share(nb, warp, kWarps), share(nb, warp + 1, kWarps), p.f, sums, tile_of,
-        [&](int b) { return (long long)list->expert[b / per] * p.d * p.f + b % per * kBlock; },
-        [&](const Tile&, int b, uint4 (&v)[2 * NT]) {
-          const int at = b / per;
-          const uint32_t tokens = list->tokens[at];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int t = n * 8 + g;
-            const bool on = tokens >> t & 1u;
-            const size_t o = (size_t)(list->start[at] + __popc(tokens & ((1u << t) - 1u))) * p.f + b % per * kBlock + c8;
-            v[n] = on ? __ldcg(reinterpret_cast<const uint4*>(p.h_hi + o)) : make_uint4(0, 0, 0, 0);
-            v[NT + n] = on ? __ldcg(reinterpret_cast<const uint4*>(p.h_lo + o)) : make_uint4(0, 0, 0, 0);
-          }
-        },
-        ByExpert{list, per},
-        [&](int i, bool there, int row, int token, float s) {
-          const int r = r0 + 16 * i + row;
-          if (there && r < r1 && token < p.T) p.out[(size_t)token * p.d + r] = __float2bfloat16_rn(s);
-        });
-  }
+  consume<NT, 2>(
+      sm, at, turn, down_tiles, n_list * f_chunks, deadline, &p.sched->status,
+      [&](int i, int c) {
+        const int a = c / f_chunks;
+        return Stage{min(kRows, d1 - d0 - i * kRows), (int)list->tokens[a], 2, min(kChunk, p.f - (c - a * f_chunks) * kChunk)};
+      },
+      [](int) { return 16; },
+      [&](int i, int row, int token, float s) {
+        const int r = d0 + i * kRows + row;
+        if (r < d1 && token < p.T) p.out[(size_t)token * p.d + r] = __float2bfloat16_rn(s);
+      });
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -538,7 +710,7 @@ Layout layout(const moe_decode* h, int T_max) {
 
 template <int NT>
 constexpr int smem_bytes() {
-  return (int)(sizeof(Sums<NT>) + sizeof(List));
+  return (int)sizeof(Smem<NT>);
 }
 
 int check_call(moe_decode* h, int T, const void* x, const void* gate, const void* up, const void* down, const void* out) {
