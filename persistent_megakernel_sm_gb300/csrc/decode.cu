@@ -323,29 +323,18 @@ struct Room {
   }
 };
 
-// A block's share of the experts' f rows, in tiles of 16 (of gate and of up) that end
-// where an expert's end.
+// A block's share of the experts' f rows, tile by tile: at most 16 (of gate and of
+// up), none over an expert's end.  Stepped along: a division a tile in every warp, a
+// stage even, is what the kernel then waits for.
 struct GateUpTiles {
-  int f, r0, r1, a0, lead, lead_tiles, per, n;
-
-  __device__ __forceinline__ GateUpTiles(int f_, int r0_, int r1_) : f(f_), r0(r0_), r1(r1_) {
-    a0 = r0 / f;
-    lead = min(r1, (a0 + 1) * f) - r0;  // rows of the first expert
-    lead_tiles = (lead + 15) / 16, per = f / 16;
-    const int rest = r1 - r0 - lead;
-    n = r1 > r0 ? lead_tiles + rest / f * per + (rest % f + 15) / 16 : 0;
-  }
-  // list entry, its first row there, rows
-  __device__ __forceinline__ void get(int i, int* at, int* first, int* rows) const {
-    int row, end;
-    if (i < lead_tiles) {
-      row = r0 + 16 * i, end = r0 + lead;
-    } else {
-      const int q = (i - lead_tiles) / per;
-      row = (a0 + 1 + q) * f + (i - lead_tiles) % per * 16;
-      end = min(r1, (a0 + 2 + q) * f);
-    }
-    *at = row / f, *first = row % f, *rows = min(16, end - row);
+  int f, left;      // rows still to come, with this tile's
+  int entry, first; // of the list, first row there
+  __device__ __forceinline__ GateUpTiles(int f_, int r0, int r1) : f(f_), left(r1 - r0), entry(r0 / f_), first(r0 % f_) {}
+  __device__ __forceinline__ int rows() const { return min(min(16, left), f - first); }
+  __device__ __forceinline__ void next() {
+    const int n = rows();
+    left -= n, first += n;
+    if (first == f) ++entry, first = 0;
   }
 };
 
@@ -358,91 +347,109 @@ struct Stage {
   __device__ __forceinline__ int all() const { return rows + parts * __popc(tokens); }
 };
 
-// The consumers' side of `tiles` tiles of `chunks` stages each.  stage(tile, c) says
-// what a stage is, high(tile) where its rows 16 to 31 begin; end(tile, row, token,
-// sum) takes each finished sum, all threads together.  A wait that runs out leaves its
-// mark in `abort`; no barrier of the block is left out.
-template <int NT, int PARTS, typename StageOf, typename High, typename End>
-__device__ __forceinline__ void consume(Smem<NT>* sm, At<Smem<NT>::kRing>& at, int& turn, int tiles, int chunks, uint64_t deadline,
-                                        int* status, StageOf&& stage_of, High&& high, End&& end) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int team = warp / kTeam, member = warp % kTeam;
+// A consumer warp's way through the stages.  A wait that runs out leaves its mark in
+// `abort`; no barrier of the block is left out.
+template <int NT>
+struct Consumer {
+  Smem<NT>* sm;
+  uint64_t deadline;
+  int* status;
+  At<Smem<NT>::kRing> at;
+  int turn = 0, tile = 0;   // the team whose stage is next; tiles so far
   bool fine = true;
-  for (int i = 0; i < tiles; ++i) {
-    float total[2][NT][4] = {};
-    const int hi = high(i);
-    for (int c = 0; c < chunks; ++c) {
-      const Stage st = stage_of(i, c);
-      if (turn == team) {
-        fine = fine && moe::mbar_wait(&sm->full[at.stage], at.parity, deadline);
-        const char* a_rows[2][2];
-        const char* b_rows[PARTS * NT];
-        const int in_row = t * 16 + member * (kBlocks * kBlock * 2);
+  float total[2][NT][4];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) total[m][q][j] = 0.f;
+  }
+
+  // One stage; the mma's rows 8 to 15 are those from `hi` on.
+  template <int PARTS>
+  __device__ __forceinline__ void stage(const Stage& st, int hi) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int team = warp / kTeam, member = warp % kTeam;
+    const int n = __popc(st.tokens);
+    if (turn == team) {
+      const char* a_rows[2][2];
+      const char* b_rows[PARTS * NT];
+      const int in_row = t * 16 + member * (kBlocks * kBlock * 2);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        a_rows[m][0] = sm->ring[at.at(8 * m + g)] + in_row;
+        a_rows[m][1] = sm->ring[at.at(hi + 8 * m + g)] + in_row;
+      }
+#pragma unroll
+      for (int q = 0; q < PARTS * NT; ++q) {
+        const int token = q % NT * 8 + g;
+        b_rows[q] = st.tokens >> token & 1
+                        ? sm->ring[at.at(st.rows + q / NT * n + __popc(st.tokens & ((1 << token) - 1)))] + in_row : nullptr;
+      }
+      fine = fine && moe::mbar_wait(&sm->full[at.stage], at.parity, deadline);
+      float part[2][NT][4] = {};
+#pragma unroll
+      for (int u = 0; u < kBlocks; ++u) {
+        if ((member * kBlocks + u) * kBlock >= st.columns) break;
+        uint4 b[PARTS * NT];
+#pragma unroll
+        for (int q = 0; q < PARTS * NT; ++q)
+          b[q] = b_rows[q] ? *reinterpret_cast<const uint4*>(b_rows[q] + u * kBlock * 2) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          a_rows[m][0] = sm->ring[at.at(8 * m + g)] + in_row;
-          a_rows[m][1] = sm->ring[at.at(hi + 8 * m + g)] + in_row;
+          const uint4 a[2] = {*reinterpret_cast<const uint4*>(a_rows[m][0] + u * kBlock * 2),
+                              *reinterpret_cast<const uint4*>(a_rows[m][1] + u * kBlock * 2)};
+#pragma unroll
+          for (int q = 0; q < PARTS * NT; ++q) mma_block(part[m][q % NT], a, b[q]);
         }
-        const int n = __popc(st.tokens);
-#pragma unroll
-        for (int q = 0; q < PARTS * NT; ++q) {
-          const int token = q % NT * 8 + g;
-          b_rows[q] = st.tokens >> token & 1
-                          ? sm->ring[at.at(st.rows + q / NT * n + __popc(st.tokens & ((1 << token) - 1)))] + in_row : nullptr;
-        }
-        float part[2][NT][4] = {};
-#pragma unroll
-        for (int u = 0; u < kBlocks; ++u) {
-          if ((member * kBlocks + u) * kBlock >= st.columns) break;
-          uint4 b[PARTS * NT];
-#pragma unroll
-          for (int q = 0; q < PARTS * NT; ++q)
-            b[q] = b_rows[q] ? *reinterpret_cast<const uint4*>(b_rows[q] + u * kBlock * 2) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const uint4 a[2] = {*reinterpret_cast<const uint4*>(a_rows[m][0] + u * kBlock * 2),
-                                *reinterpret_cast<const uint4*>(a_rows[m][1] + u * kBlock * 2)};
-#pragma unroll
-            for (int q = 0; q < PARTS * NT; ++q) mma_block(part[m][q % NT], a, b[q]);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->empty[at.stage]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int q = 0; q < NT; ++q)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (st.tokens >> (q * 8 + t * 2 + (j & 1)) & 1) total[m][q][j] += part[m][q][j];
       }
-      at.next(st.all());
-      if (++turn == kTeams) turn = 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->empty[at.stage]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (st.tokens >> (q * 8 + t * 2 + (j & 1)) & 1) total[m][q][j] += part[m][q][j];
     }
-    float* mine = sm->sums.v[i & 1][warp];
+    at.next(st.rows + PARTS * n);
+    if (++turn == kTeams) turn = 0;
+  }
+
+  // The warps' sums together: end(row, token, sum), all threads at once.
+  template <typename End>
+  __device__ __forceinline__ void finish(End&& end) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    float(*sums)[Sums<NT>::kTile] = sm->sums.v[tile++ & 1];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
-        float* to = mine + (q * 8 + 2 * t) * kColumn + 8 * m + g;
+        float* to = sums[warp] + (q * 8 + 2 * t) * kColumn + 8 * m + g;
         to[0] = total[m][q][0], to[kColumn] = total[m][q][1], to[16] = total[m][q][2], to[kColumn + 16] = total[m][q][3];
       }
     sync_consumers();
 #pragma unroll
     for (int q = 0; q < NT; ++q) {  // 32 rows of 8 tokens: a thread each
       const int row = lane, token = q * 8 + warp;
-      const float* from = sm->sums.v[i & 1][0] + token * kColumn + row;
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += from[w * Sums<NT>::kTile];
-      end(i, row, token, s);
+      for (int w = 0; w < kWarps; ++w) s += sums[w][token * kColumn + row];
+      end(row, token, s);
     }
+    clear();
   }
-  if (!fine) {
+
+  __device__ __forceinline__ void tell() {
+    if (fine) return;
     *status = MOE_E_TIMEOUT;
     *static_cast<volatile int*>(&sm->abort) = 1;
   }
-}
+};
 
 // The router's logits: a block's share of its rows, each lane 8 columns at a time.
 template <int NT>
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   if (sm->abort) return;  // nothing is on its way yet
 
   const long long rows = (long long)list->n * p.f;
-  const GateUpTiles gate_up(p.f, share(rows, block, blocks), share(rows, block + 1, blocks));
+  GateUpTiles gate_up(p.f, share(rows, block, blocks), share(rows, block + 1, blocks));
   const int d0 = share(p.d, block, blocks), d1 = share(p.d, block + 1, blocks);
   const int down_tiles = (d1 - d0 + kRows - 1) / kRows;
   const int x_chunks = (p.d + kChunk - 1) / kChunk, f_chunks = (p.f + kChunk - 1) / kChunk;
@@ -566,9 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
         ++issued;
         return true;
       };
-      for (int i = 0; go && i < gate_up.n; ++i) {
-        int a, first, n;
-        gate_up.get(i, &a, &first, &n);
+      for (; go && gate_up.left > 0; gate_up.next()) {
+        const int a = gate_up.entry, first = gate_up.first, n = gate_up.rows();
         const bf16* base = (mine < n ? p.gate : p.up) + ((size_t)list->expert[a] * p.f + first + (mine < n ? mine : mine - n)) * p.d;
         const int tokens = (int)list->tokens[a];
         for (int c = 0; go && c < x_chunks; ++c)
@@ -609,9 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
       room.take(rows);
       return true;
     };
-    for (int i = 0; go && i < gate_up.n; ++i) {
-      int a, first, n;
-      gate_up.get(i, &a, &first, &n);
+    for (; go && gate_up.left > 0; gate_up.next()) {
+      const int a = gate_up.entry, n = gate_up.rows();
       const int tokens = (int)list->tokens[a];
       for (int c = 0; go && c < x_chunks; ++c)
         go = bring(Stage{2 * n, tokens, 1, min(kChunk, p.d - c * kChunk)}, p.x + c * kChunk, nullptr, p.d, list->order[a]);
@@ -631,35 +636,26 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
     return;
   }
 
-  At<Smem<NT>::kRing> at;
-  int turn = 0;
+  Consumer<NT> me{sm, deadline, &p.sched->status};
+  me.clear();
   // 2: gate and up
-  consume<NT, 1>(
-      sm, at, turn, gate_up.n, x_chunks, deadline, &p.sched->status,
-      [&](int i, int c) {
-        int a, first, n;
-        gate_up.get(i, &a, &first, &n);
-        return Stage{2 * n, (int)list->tokens[a], 1, min(kChunk, p.d - c * kChunk)};
-      },
-      [&](int i) {
-        int a, first, n;
-        gate_up.get(i, &a, &first, &n);
-        return n;
-      },
-      [&](int i, int row, int token, float s) {
-        const float up = __shfl_xor_sync(kAll, s, 16);  // rows 16 to 31 are up's
-        int a, first, n;
-        gate_up.get(i, &a, &first, &n);
-        const uint32_t tokens = list->tokens[a];
-        if (row >= n || !(tokens >> token & 1u)) return;
-        const float h = s / (1.f + expf(-s)) * up * list->w[a][token];
-        const size_t slot = list->start[a] + __popc(tokens & ((1u << token) - 1u));
-        const bf16 hi = __float2bfloat16_rn(h);
-        p.h_hi[slot * p.f + first + row] = hi;
-        // an infinity or a NaN is all in the first part
-        const float rest = h - __bfloat162float(hi);
-        p.h_lo[slot * p.f + first + row] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-      });
+  for (; gate_up.left > 0; gate_up.next()) {
+    const int a = gate_up.entry, first = gate_up.first, n = gate_up.rows();
+    const uint32_t tokens = list->tokens[a];
+    for (int c = 0; c < x_chunks; ++c) me.template stage<1>(Stage{2 * n, (int)tokens, 1, min(kChunk, p.d - c * kChunk)}, n);
+    me.finish([&](int row, int token, float s) {
+      const float up = __shfl_xor_sync(kAll, s, 16);  // rows 16 to 31 are up's
+      if (row >= n || !(tokens >> token & 1u)) return;
+      const float h = s / (1.f + expf(-s)) * up * list->w[a][token];
+      const size_t slot = list->start[a] + __popc(tokens & ((1u << token) - 1u));
+      const bf16 hi = __float2bfloat16_rn(h);
+      p.h_hi[slot * p.f + first + row] = hi;
+      // an infinity or a NaN is all in the first part
+      const float rest = h - __bfloat162float(hi);
+      p.h_lo[slot * p.f + first + row] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
+    });
+  }
+  me.tell();
   if (!grid_wait(p.sched, gen++, deadline, &list->ok) || *abort) {
     if (tid == 0) *abort = 1;
     return;
@@ -667,17 +663,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   if (tid == 0) mbar_arrive(&sm->h_ready);
 
   // 3: down
-  consume<NT, 2>(
-      sm, at, turn, down_tiles, n_list * f_chunks, deadline, &p.sched->status,
-      [&](int i, int c) {
-        const int a = c / f_chunks;
-        return Stage{min(kRows, d1 - d0 - i * kRows), (int)list->tokens[a], 2, min(kChunk, p.f - (c - a * f_chunks) * kChunk)};
-      },
-      [](int) { return 16; },
-      [&](int i, int row, int token, float s) {
-        const int r = d0 + i * kRows + row;
-        if (r < d1 && token < p.T) p.out[(size_t)token * p.d + r] = __float2bfloat16_rn(s);
-      });
+  for (int r0 = d0; r0 < d1; r0 += kRows) {
+    const int n = min(kRows, d1 - r0);
+    for (int a = 0; a < n_list; ++a) {
+      const int tokens = (int)list->tokens[a];
+      for (int c = 0; c < f_chunks; ++c) me.template stage<2>(Stage{n, tokens, 2, min(kChunk, p.f - c * kChunk)}, 16);
+    }
+    me.finish([&](int row, int token, float s) {
+      if (r0 + row < d1 && token < p.T) p.out[(size_t)token * p.d + r0 + row] = __float2bfloat16_rn(s);
+    });
+  }
+  me.tell();
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
