@@ -13,7 +13,7 @@
 // A product's tile is 32 weight rows (16 of gate and 16 of up) times 8 or 16 token
 // columns on mma.sync m16n8k16.  The tensor cores are nearly idle here; they are used
 // because a multiply-add for every weight and token would not keep up with HBM.  A
-// stage is 512 columns of a tile and of the tokens that its expert has.  Four warps of
+// stage is 512 or 1024 columns of a tile and of the tokens that its expert has.  Four warps of
 // a block bring its weights by bulk copies, four more the tokens' columns, into a ring of
 // single rows (160 to 180 KB an SM on their way, whatever a stage has of them); the
 // weights do not wait for the grid, so the ring is full of down's first ones when h' is
@@ -52,9 +52,6 @@ constexpr int kBringers = 4;     // warps that bring weights, and as many that b
 constexpr int kThreads = kConsumers + 2 * kBringers * 32;
 constexpr int kBlock = 32;       // columns of two mma
 constexpr int kRows = 32;        // of a tile: gate and up 16 each
-constexpr int kChunk = 512;      // columns of a stage
-constexpr int kBlocks = kChunk / kBlock / kTeam;  // of a warp
-constexpr int kPitch = kChunk * 2 + 64;  // bytes of a row: two rows next to each other use all banks
 constexpr int kColumn = 36;      // floats of a token's column of sums: 32, and 4 so that its lanes miss each other's banks
 constexpr int kStages = 16;      // on their way, at most
 constexpr unsigned kAll = 0xffffffffu;
@@ -82,14 +79,13 @@ struct Decode {
 struct List {
   int n;
   int expert[kMaxE + 1];
-  int start[kMaxE + 1];           // of its slots
-  uint32_t tokens[kMaxE + 1];     // that chose it
+  int start[kMaxE + 1];             // of its slots
+  uint32_t tokens[kMaxE + 1];       // that chose it
   uint8_t order[kMaxE + 1][kMaxT];  // the same, one after another
-  float w[kMaxE + 1][kMaxT];      // their weights
-  int place[kMaxE];               // of an expert in the list, -1
-  int idx[kMaxT][kMaxK];
-  float idx_w[kMaxT][kMaxK];
-  int ok;                         // of the last grid-wide wait
+  uint32_t by_expert[kMaxE];        // tokens, of every routed expert
+  float w[kMaxE + 1][kMaxT];        // their weights, of every expert
+  int warp_experts[kWarps], warp_slots[kWarps];
+  int ok;                           // of the last grid-wide wait
 };
 
 __device__ __forceinline__ uint4 load_weights(const bf16* p) {
@@ -102,12 +98,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Rows g and g + 8 of a tile, 32 columns, times a column block.
-__device__ __forceinline__ void mma_block(float (&c)[4], const uint4 (&a)[2], uint4 b) {
-  mma(c, a[0].x, a[1].x, a[0].y, a[1].y, b.x, b.y);
-  mma(c, a[0].z, a[1].z, a[0].w, a[1].w, b.z, b.w);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -150,123 +140,119 @@ __device__ __forceinline__ uint32_t key_of(float v) {
 }
 
 // A warp chooses for token t from its logits: the k largest, the lower expert on
-// ties, their weights exp(l - max) over the kept ones' sum.
-__device__ void choose(const Decode& p, List* list, int t) {
+// ties, their weights exp(l - max) over the kept ones' sum.  Lane j gets slot j.
+__device__ __forceinline__ void choose(const Decode& p, int t, int* expert, float* weight) {
+  constexpr int kPer = kMaxE / 32;
   const int lane = threadIdx.x & 31;
-  uint32_t key[kMaxE / 32];
-  float l[kMaxE / 32];
+  uint32_t key[kPer];
+  float l[kPer];
 #pragma unroll
-  for (int i = 0; i < kMaxE / 32; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = e < p.E ? __ldcg(p.logits + t * p.E + e) : -INFINITY;
-    key[i] = key_of(l[i]);
-  }
+  for (int i = 0; i < kPer; ++i) l[i] = lane * kPer + i < p.E ? __ldcg(p.logits + t * p.E + lane * kPer + i) : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) key[i] = key_of(l[i]);
   float mine = -INFINITY;  // the logit of slot `lane`
   int my_e = -1;
   for (int j = 0; j < p.k; ++j) {
-    uint32_t best = 0;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < kMaxE / 32; ++i) best = max(best, key[i]);
-    best = __reduce_max_sync(kAll, best);
-    if (best <= kDead) break;
-    int at = kMaxE;
-#pragma unroll
-    for (int i = kMaxE / 32 - 1; i >= 0; --i)
-      if (key[i] == best) at = lane + 32 * i;
-    at = __reduce_min_sync(kAll, at);
+    for (int i = 1; i < kPer; ++i) best = max(best, key[i]);
+    const uint32_t most = __reduce_max_sync(kAll, best);
+    if (most <= kDead) break;
+    const int leader = __ffs(__ballot_sync(kAll, best == most)) - 1;
+    int at = 0;
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMaxE / 32; ++i)
-      if (lane + 32 * i == at) v = l[i], key[i] = 0;
-    v = __shfl_sync(kAll, v, at & 31);
+    for (int i = kPer - 1; i >= 0; --i)
+      if (key[i] == most) at = i, v = l[i];
+    if (lane == leader) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i == at) key[i] = 0;
+    }
+    at = __shfl_sync(kAll, lane * kPer + at, leader);
+    v = __shfl_sync(kAll, v, leader);
     if (lane == j) mine = v, my_e = at;
   }
-  float top = mine, sum;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float v = __shfl_xor_sync(kAll, top, o);
-    top = (v > top || v != v) ? v : top;  // NaN stays
-  }
-  // equal logits weigh the same, infinities too
+  // the first is the largest (a NaN, if there is one); equal logits weigh the same, infinities too
+  const float top = __shfl_sync(kAll, mine, 0);
   const float e = my_e < 0 ? 0.f : mine == top ? 1.f : expf(mine - top);
-  sum = e;
+  float sum = e;
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-  if (lane < p.k) {
-    list->idx[t][lane] = my_e;
-    list->idx_w[t][lane] = my_e < 0 ? 0.f : e / sum;
+  *expert = my_e;
+  *weight = my_e < 0 ? 0.f : e / sum;
+}
+
+// Lane j's slot of token t into the lists by expert.
+__device__ __forceinline__ void enter(const Decode& p, List* list, int t, int e, float w) {
+  const bool live = (threadIdx.x & 31) < p.k && (unsigned)e < (unsigned)p.E;
+  if (!p.router_w) {  // an expert that the caller named twice has both weights, in slot order
+    const int mine = live ? e : -1 - (int)(threadIdx.x & 31);
+    float sum = 0.f;
+    for (int j = 0; j < p.k; ++j) {
+      const float v = __shfl_sync(kAll, w, j);
+      if (__shfl_sync(kAll, mine, j) == mine) sum += v;
+    }
+    w = sum;
+  }
+  if (live) {
+    atomicOr(&list->by_expert[e], 1u << t);
+    list->w[e][t] = w;
   }
 }
 
-// The experts that the tokens chose, in order, with their tokens and weights.
-__device__ void make_list(const Decode& p, List* list) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  for (int e = tid; e < p.E; e += kConsumers) list->place[e] = -1;
-  sync_consumers();
-  for (int i = tid; i < p.T * p.k; i += kConsumers) {
-    const int e = list->idx[i / p.k][i % p.k];
-    if ((unsigned)e < (unsigned)p.E) list->place[e] = 0;
-  }
-  sync_consumers();
-  if (tid < 32) {
-    int n = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const bool live = e0 + lane < p.E && list->place[e0 + lane] == 0;
-      const unsigned m = __ballot_sync(kAll, live);
-      const int at = n + __popc(m & ((1u << lane) - 1u));
-      if (live) list->place[e0 + lane] = at, list->expert[at] = e0 + lane;
-      n += __popc(m);
-    }
-    if (lane == 0) {
-      if (p.S) list->expert[n] = p.E;
-      list->n = n + p.S;
-    }
-  }
-  sync_consumers();
-  const int n = list->n;
-  for (int i = tid; i < n * kMaxT; i += kConsumers) list->w[i / kMaxT][i % kMaxT] = 0.f;
-  for (int i = tid; i < n; i += kConsumers) list->tokens[i] = p.S && i == n - 1 ? (1u << p.T) - 1u : 0u;
-  sync_consumers();
-  if (tid < p.T) {  // a token's slots in order: an expert named twice has both weights
-    for (int j = 0; j < p.k; ++j) {
-      const int e = list->idx[tid][j];
-      if ((unsigned)e >= (unsigned)p.E) continue;
-      const int at = list->place[e];
-      list->w[at][tid] += list->idx_w[tid][j];
-      atomicOr(&list->tokens[at], 1u << tid);
-    }
-    if (p.S) list->w[n - 1][tid] = 1.f;
-  }
-  sync_consumers();
-  if (tid < 32) {
-    int base = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int mine = i0 + lane < n ? __popc(list->tokens[i0 + lane]) : 0;
-      for (int j = 0, left = mine ? (int)list->tokens[i0 + lane] : 0; left; ++j, left &= left - 1)
-        list->order[i0 + lane][j] = (uint8_t)(__ffs(left) - 1);
-      int sum = mine;
+// The experts that the tokens chose, in order, from the lists by expert: a thread each.
+__device__ __forceinline__ void make_list(const Decode& p, List* list) {
+  static_assert(kMaxE <= kConsumers, "a thread an expert");
+  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+  const uint32_t tokens = e < p.E ? list->by_expert[e] : 0u;
+  const unsigned live = __ballot_sync(kAll, tokens != 0);
+  const int mine = __popc(tokens);
+  int sum = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, sum, o);
-        if (lane >= o) sum += v;
-      }
-      if (i0 + lane < n) list->start[i0 + lane] = base + sum - mine;
-      base += __shfl_sync(kAll, sum, 31);
-    }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, sum, o);
+    if (lane >= o) sum += v;
   }
+  if (lane == 31) list->warp_experts[warp] = __popc(live), list->warp_slots[warp] = sum;
   sync_consumers();
+  int n = 0, slots = 0, n_all = 0, slots_all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int a = list->warp_experts[w], b = list->warp_slots[w];
+    if (w < warp) n += a, slots += b;
+    n_all += a, slots_all += b;
+  }
+  auto put = [&](int at, int expert, int start, uint32_t of) {
+    list->expert[at] = expert, list->start[at] = start, list->tokens[at] = of;
+    int j = 0;
+    for (uint32_t left = of; left; left &= left - 1) list->order[at][j++] = (uint8_t)(__ffs(left) - 1);
+  };
+  if (tokens) put(n + __popc(live & ((1u << lane) - 1u)), e, slots + sum - mine, tokens);
+  if (e == 0) {
+    list->n = n_all + p.S;
+    if (p.S) put(n_all, p.E, slots_all, (1u << p.T) - 1u);
+  }
 }
 
 // Warps' sums of a tile; two tiles' worth, so that one wait a tile is enough.
 template <int NT>
 struct Sums {
   static constexpr int kTile = NT * 8 * kColumn;
-  float v[2][kWarps][kTile];
+  float v[2][kWarps][kTile];  // of the logits, at first: of all 16 warps
 };
+static_assert(kThreads / 32 <= 2 * kWarps, "the logits' sums");
 
 template <int NT>
 struct Smem {
-  static constexpr int kRing = NT == 1 ? 168 : 152;  // rows; a stage has 64 at most
+  // Columns of a stage.  A stage costs the warps that bring and use it several hundred
+  // cycles whatever it holds, so longer is better (4 tokens of 128 experts of 2048 x
+  // 768: 76 us with 512, 65 with 1024), as long as the ring holds a few stages with
+  // all the tokens' rows (13 tokens of 32 + 1 experts of 7168 x 2048: 524 and 689).
+  static constexpr int kChunk = NT == 1 ? 1024 : 512;
+  static constexpr int kBlocks = kChunk / kBlock / kTeam;  // of a warp
+  static constexpr int kPitch = kChunk * 2 + 64;  // bytes of a row: two rows next to each other use all banks
+  static constexpr int kRing = NT == 1 ? 86 : 152;  // rows; a stage has 64 at most (48 with 8 tokens)
   char ring[kRing][kPitch];
   Sums<NT> sums;
   List list;
@@ -351,70 +337,86 @@ struct Stage {
 // `abort`; no barrier of the block is left out.
 template <int NT>
 struct Consumer {
+  static constexpr int kBlocks = Smem<NT>::kBlocks;
   Smem<NT>* sm;
   uint64_t deadline;
   int* status;
   At<Smem<NT>::kRing> at;
   int turn = 0, tile = 0;   // the team whose stage is next; tiles so far
   bool fine = true;
-  float total[2][NT][4];
+  float total[NT][2][4];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int q = 0; q < NT; ++q)
 #pragma unroll
-      for (int q = 0; q < NT; ++q)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) total[m][q][j] = 0.f;
+        for (int j = 0; j < 4; ++j) total[q][m][j] = 0.f;
   }
 
-  // One stage; the mma's rows 8 to 15 are those from `hi` on.
-  template <int PARTS>
+  // 8 tokens' columns of a stage times M times 16 of its rows: 0 to 7 and 8 to 15 more
+  // of the mma are rows 8 m and hi + 8 m on.  Sums of their own for both mma of a block
+  // and both parts: one after another they would wait for each other.
+  template <int PARTS, int M>
+  __device__ __forceinline__ void multiply(const Stage& st, int hi, int tokens_before, uint32_t tokens, int n, float (&sum)[2][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int in_row = t * 16 + threadIdx.x / 32 % kTeam * (kBlocks * kBlock * 2);
+    const char* b_rows[PARTS];
+    const bool on = tokens >> g & 1;
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q)
+      b_rows[q] = sm->ring[at.at(st.rows + q * n + tokens_before + (on ? __popc(tokens & ((1u << g) - 1u)) : 0))] + in_row;
+    float part[M][PARTS][2][4] = {};
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      // columns come in multiples of 128
+      if (u % 4 == 0 && u > 0 && (threadIdx.x / 32 % kTeam * kBlocks + u) * kBlock >= st.columns) break;
+      uint4 b[PARTS];
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) {
+        b[q] = *reinterpret_cast<const uint4*>(b_rows[q] + u * kBlock * 2);
+        if (!on) b[q] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const uint4 a0 = *reinterpret_cast<const uint4*>(sm->ring[at.at(8 * m + g)] + in_row + u * kBlock * 2);
+        const uint4 a1 = *reinterpret_cast<const uint4*>(sm->ring[at.at(hi + 8 * m + g)] + in_row + u * kBlock * 2);
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) {
+          mma(part[m][q][0], a0.x, a1.x, a0.y, a1.y, b[q].x, b[q].y);
+          mma(part[m][q][1], a0.z, a1.z, a0.w, a1.w, b[q].z, b[q].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float s = part[m][0][0][j] + part[m][0][1][j];
+        if (PARTS == 2) s += part[m][PARTS - 1][0][j] + part[m][PARTS - 1][1][j];
+        if (tokens >> (t * 2 + (j & 1)) & 1) sum[m][j] += s;
+      }
+  }
+
+  // One stage, M as in multiply.
+  template <int PARTS, int M>
   __device__ __forceinline__ void stage(const Stage& st, int hi) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int team = warp / kTeam, member = warp % kTeam;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = __popc(st.tokens);
-    if (turn == team) {
-      const char* a_rows[2][2];
-      const char* b_rows[PARTS * NT];
-      const int in_row = t * 16 + member * (kBlocks * kBlock * 2);
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        a_rows[m][0] = sm->ring[at.at(8 * m + g)] + in_row;
-        a_rows[m][1] = sm->ring[at.at(hi + 8 * m + g)] + in_row;
-      }
-#pragma unroll
-      for (int q = 0; q < PARTS * NT; ++q) {
-        const int token = q % NT * 8 + g;
-        b_rows[q] = st.tokens >> token & 1
-                        ? sm->ring[at.at(st.rows + q / NT * n + __popc(st.tokens & ((1 << token) - 1)))] + in_row : nullptr;
-      }
+    if (turn == warp / kTeam) {
       fine = fine && moe::mbar_wait(&sm->full[at.stage], at.parity, deadline);
-      float part[2][NT][4] = {};
+      if (warp % kTeam * (kBlocks * kBlock) < st.columns) {
+        int before = 0;
 #pragma unroll
-      for (int u = 0; u < kBlocks; ++u) {
-        if ((member * kBlocks + u) * kBlock >= st.columns) break;
-        uint4 b[PARTS * NT];
-#pragma unroll
-        for (int q = 0; q < PARTS * NT; ++q)
-          b[q] = b_rows[q] ? *reinterpret_cast<const uint4*>(b_rows[q] + u * kBlock * 2) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint4 a[2] = {*reinterpret_cast<const uint4*>(a_rows[m][0] + u * kBlock * 2),
-                              *reinterpret_cast<const uint4*>(a_rows[m][1] + u * kBlock * 2)};
-#pragma unroll
-          for (int q = 0; q < PARTS * NT; ++q) mma_block(part[m][q % NT], a, b[q]);
+        for (int q = 0; q < NT; ++q) {
+          const uint32_t tokens = (uint32_t)st.tokens >> (8 * q) & 0xffu;
+          if (NT == 1 || tokens) multiply<PARTS, M>(st, hi, before, tokens, n, total[q]);
+          before += __popc(tokens);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->empty[at.stage]);
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int q = 0; q < NT; ++q)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (st.tokens >> (q * 8 + t * 2 + (j & 1)) & 1) total[m][q][j] += part[m][q][j];
     }
     at.next(st.rows + PARTS * n);
     if (++turn == kTeams) turn = 0;
@@ -430,7 +432,7 @@ struct Consumer {
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
         float* to = sums[warp] + (q * 8 + 2 * t) * kColumn + 8 * m + g;
-        to[0] = total[m][q][0], to[kColumn] = total[m][q][1], to[16] = total[m][q][2], to[kColumn + 16] = total[m][q][3];
+        to[0] = total[q][m][0], to[kColumn] = total[q][m][1], to[16] = total[q][m][2], to[kColumn + 16] = total[q][m][3];
       }
     sync_consumers();
 #pragma unroll
@@ -455,44 +457,46 @@ struct Consumer {
 template <int NT>
 __device__ __forceinline__ void logits(const Decode& p, Smem<NT>* sm, int e0, int e1) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int nkb = p.d / kBlock, b0 = share(nkb, warp, kWarps), b1 = share(nkb, warp + 1, kWarps);
+  const int nkb = p.d / kBlock, b0 = share(nkb, warp, kThreads / 32), b1 = share(nkb, warp + 1, kThreads / 32);
   for (int e = e0; e < e1; e += 8) {  // rows 8 to 15 of the mma are not used
     float total[NT][4] = {};
-    constexpr int U = 4;
+    constexpr int U = NT == 1 ? 8 : 4;
     for (int kb = b0; kb < b1; kb += U) {
-      uint4 a[U][2], b[U][NT];
+      uint4 a[U], b[U][NT];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int col = (kb + u) * kBlock + t * 8;
         const bool there = kb + u < b1;
-        a[u][1] = make_uint4(0, 0, 0, 0);
-        a[u][0] = there && e + g < e1 ? load_weights(p.router_w + (size_t)(e + g) * p.d + col) : a[u][1];
+        a[u] = there && e + g < e1 ? load_weights(p.router_w + (size_t)(e + g) * p.d + col) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          b[u][n] = there && n * 8 + g < p.T ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(n * 8 + g) * p.d + col)) : a[u][1];
+          b[u][n] = there && n * 8 + g < p.T ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)(n * 8 + g) * p.d + col)) : make_uint4(0, 0, 0, 0);
       }
-      float part[NT][4] = {};
+      float part[NT][2][4] = {};
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_block(part[n], a[u], b[u][n]);
+        for (int n = 0; n < NT; ++n) {
+          mma(part[n][0], a[u].x, 0, a[u].y, 0, b[u][n].x, b[u][n].y);
+          mma(part[n][1], a[u].z, 0, a[u].w, 0, b[u][n].z, b[u][n].w);
+        }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) total[n][j] += part[n][j];
+        for (int j = 0; j < 2; ++j) total[n][j] += part[n][0][j] + part[n][1][j];
     }
-    float* mine = sm->sums.v[0][warp];
-    sync_consumers();
+    float* mine = sm->sums.v[0][0] + warp * Sums<NT>::kTile;
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) mine[(n * 8 + 2 * t + j) * kColumn + g] = total[n][j];
-    sync_consumers();
+    __syncthreads();
     const int row = tid & 7, token = tid >> 3;
     if (token < p.T && e + row < e1) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += sm->sums.v[0][w][token * kColumn + row];
+      for (int w = 0; w < kThreads / 32; ++w) s += sm->sums.v[0][0][w * Sums<NT>::kTile + token * kColumn + row];
       p.logits[token * p.E + e + row] = s + (p.bias ? p.bias[e + row] : 0.f);
     }
   }
@@ -503,6 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   extern __shared__ __align__(128) char smem_raw[];
   Smem<NT>* sm = reinterpret_cast<Smem<NT>*>(smem_raw);
   List* list = &sm->list;
+  constexpr int kChunk = Smem<NT>::kChunk;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int block = blockIdx.x, blocks = gridDim.x;
   const uint64_t deadline = moe::globaltimer() + kLimitNs;
@@ -514,28 +519,28 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
     moe::fence_mbar_init();
   }
   if (tid == 0) sm->abort = 0;
+  if (tid < p.E) list->by_expert[tid] = 0;
+  if (tid < p.T) list->w[p.E][tid] = 1.f;  // the shared expert's
   bool fine = true;
-  int gen = 0;
+  int gen = tid == 0 ? moe::ld_acquire(&p.sched->gen) : 0;
+  // 1: logits, and the choice
+  if (p.router_w) logits<NT>(p, sm, share(p.E, block, blocks), share(p.E, block + 1, blocks));
   if (!producer) {
-    gen = tid == 0 ? moe::ld_acquire(&p.sched->gen) : 0;
-    if (p.router_w) {  // 1: logits, and the choice
-      logits<NT>(p, sm, share(p.E, block, blocks), share(p.E, block + 1, blocks));
-      fine = grid_wait(p.sched, gen++, deadline, &list->ok);
-      if (fine)
-        for (int t = warp; t < p.T; t += kWarps) choose(p, list, t);
-    } else {
-      for (int i = tid; i < p.T * p.k; i += kConsumers) {
-        list->idx[i / p.k][i % p.k] = p.idx_in[i];
-        list->idx_w[i / p.k][i % p.k] = p.w_in[i];
-      }
-    }
-    sync_consumers();
+    if (p.router_w) fine = grid_wait(p.sched, gen++, deadline, &list->ok);
+    else sync_consumers();
     if (fine) {
-      if (block == 0 && p.router_w)
-        for (int i = tid; i < p.T * p.k; i += kConsumers) {
-          if (p.idx_out) p.idx_out[i] = list->idx[i / p.k][i % p.k];
-          if (p.w_out) p.w_out[i] = list->idx_w[i / p.k][i % p.k];
+      for (int t = warp; t < p.T; t += kWarps) {
+        int e = -1;
+        float w = 0.f;
+        if (p.router_w) choose(p, t, &e, &w);
+        else if (lane < p.k) e = p.idx_in[t * p.k + lane], w = p.w_in[t * p.k + lane];
+        enter(p, list, t, e, w);
+        if (block == 0 && lane < p.k && p.router_w) {
+          if (p.idx_out) p.idx_out[t * p.k + lane] = e;
+          if (p.w_out) p.w_out[t * p.k + lane] = w;
         }
+      }
+      sync_consumers();
       make_list(p, list);
     }
     if (tid == 0 && !fine) sm->abort = 1;
@@ -640,13 +645,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   me.clear();
   // 2: gate and up
   for (; gate_up.left > 0; gate_up.next()) {
-    const int a = gate_up.entry, first = gate_up.first, n = gate_up.rows();
+    const int a = gate_up.entry, first = gate_up.first, n = gate_up.rows(), expert = list->expert[a];
     const uint32_t tokens = list->tokens[a];
-    for (int c = 0; c < x_chunks; ++c) me.template stage<1>(Stage{2 * n, (int)tokens, 1, min(kChunk, p.d - c * kChunk)}, n);
+    for (int c = 0; c < x_chunks; ++c) {
+      const Stage st{2 * n, (int)tokens, 1, min(kChunk, p.d - c * kChunk)};
+      if (n > 8) me.template stage<1, 2>(st, n);
+      else me.template stage<1, 1>(st, n);
+    }
     me.finish([&](int row, int token, float s) {
       const float up = __shfl_xor_sync(kAll, s, 16);  // rows 16 to 31 are up's
       if (row >= n || !(tokens >> token & 1u)) return;
-      const float h = s / (1.f + expf(-s)) * up * list->w[a][token];
+      const float h = s / (1.f + expf(-s)) * up * list->w[expert][token];
       const size_t slot = list->start[a] + __popc(tokens & ((1u << token) - 1u));
       const bf16 hi = __float2bfloat16_rn(h);
       p.h_hi[slot * p.f + first + row] = hi;
@@ -667,10 +676,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
     const int n = min(kRows, d1 - r0);
     for (int a = 0; a < n_list; ++a) {
       const int tokens = (int)list->tokens[a];
-      for (int c = 0; c < f_chunks; ++c) me.template stage<2>(Stage{n, tokens, 2, min(kChunk, p.f - c * kChunk)}, 16);
+      for (int c = 0; c < f_chunks; ++c) {
+        const Stage st{n, tokens, 2, min(kChunk, p.f - c * kChunk)};
+        if (n > 16) me.template stage<2, 2>(st, 16);
+        else me.template stage<2, 1>(st, 8);
+      }
     }
     me.finish([&](int row, int token, float s) {
-      if (r0 + row < d1 && token < p.T) p.out[(size_t)token * p.d + r0 + row] = __float2bfloat16_rn(s);
+      if (n <= 16) {  // the sums' rows 0 to 7 and 16 to 23 are the tile's first 16
+        if (row & 8) return;
+        row = (row & 7) + (row >> 4) * 8;
+      }
+      if (row < n && token < p.T) p.out[(size_t)token * p.d + r0 + row] = __float2bfloat16_rn(s);
     });
   }
   me.tell();
