@@ -58,7 +58,8 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr uint64_t kLimitNs = 2000000000ull;
 
 struct Sched {
-  int count, gen, status;
+  unsigned long long arrived;  // blocks, at all waits since it was cleared
+  int status;
 };
 
 struct Decode {
@@ -85,6 +86,8 @@ struct List {
   uint32_t by_expert[kMaxE];        // tokens, of every routed expert
   float w[kMaxE + 1][kMaxT];        // their weights, of every expert
   int warp_experts[kWarps], warp_slots[kWarps];
+  int chosen[kWarps][kMaxK];
+  float logit[kWarps][kMaxK];
   int ok;                           // of the last grid-wide wait
 };
 
@@ -106,26 +109,24 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 __device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
-// Every block's consumers arrive; false if the wait ran out somewhere.
-__device__ bool grid_wait(Sched* s, int gen, uint64_t deadline, int* ok) {
+// Every block's consumers arrive; false if the wait ran out somewhere.  `target` (of
+// thread 0): the arrivals that make it complete.
+__device__ bool grid_wait(Sched* s, unsigned long long target, uint64_t deadline, int* ok) {
   sync_consumers();
   if (threadIdx.x == 0) {
-    *ok = 1;
-    __threadfence();
-    if (moe::atom_add_acq_rel(&s->count, 1) == (int)gridDim.x - 1) {
-      s->count = 0;
-      moe::st_release(&s->gen, gen + 1);
-    } else {
-      while (moe::ld_acquire(&s->gen) == gen) {
-        if (moe::ld_relaxed(&s->status) != 0 || moe::globaltimer() > deadline) {
-          if (moe::ld_acquire(&s->gen) != gen) break;
-          s->status = MOE_E_TIMEOUT;
-          *ok = 0;
-          break;
-        }
+    int fine = 1;
+    asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(&s->arrived) : "memory");
+    unsigned long long now;
+    for (int i = 0;; ++i) {
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(now) : "l"(&s->arrived) : "memory");
+      if (now >= target) break;
+      if (i % 16 == 15 && (moe::ld_relaxed(&s->status) != 0 || moe::globaltimer() > deadline)) {
+        s->status = MOE_E_TIMEOUT;
+        fine = 0;
+        break;
       }
     }
-    __threadfence();
+    *ok = fine;
   }
   sync_consumers();
   return *ok != 0;
@@ -138,41 +139,54 @@ __device__ __forceinline__ uint32_t key_of(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
   return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
+
+// The larger first.
+__device__ __forceinline__ void order_two(uint64_t& a, uint64_t& b) {
+  const bool swap = a < b;
+  const uint64_t hi = swap ? b : a;
+  b = swap ? a : b;
+  a = hi;
+}
 
 // A warp chooses for token t from its logits: the k largest, the lower expert on
-// ties, their weights exp(l - max) over the kept ones' sum.  Lane j gets slot j.
-__device__ __forceinline__ void choose(const Decode& p, int t, int* expert, float* weight) {
-  constexpr int kPer = kMaxE / 32;
+// ties, their weights exp(l - max) over the kept ones' sum.  Lane j gets slot j.  A
+// lane puts its PER experts in order once, so that each choice waits for no more than
+// the lanes' first ones' largest and who has it.
+template <int PER>
+__device__ __forceinline__ void choose(const Decode& p, List* list, int t, int* expert, float* weight) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[kPer];
-  float l[kPer];
+  int* chosen = list->chosen[threadIdx.x >> 5];
+  float* logit = list->logit[threadIdx.x >> 5];
+  uint64_t key[PER + 1];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) l[i] = lane * kPer + i < p.E ? __ldcg(p.logits + t * p.E + lane * kPer + i) : -INFINITY;
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t k = lane * PER + i < p.E ? key_of(__ldcg(p.logits + t * p.E + lane * PER + i)) : 0u;
+    key[i] = (uint64_t)k << 32 | (uint32_t)(PER - 1 - i);
+  }
+  key[PER] = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) key[i] = key_of(l[i]);
-  float mine = -INFINITY;  // the logit of slot `lane`
-  int my_e = -1;
+  for (int round = 0; round < PER; ++round)  // neighbours, PER rounds
+#pragma unroll
+    for (int i = round & 1; i + 1 < PER; i += 2) order_two(key[i], key[i + 1]);
+  if (lane < p.k) chosen[lane] = -1;
+  __syncwarp();
   for (int j = 0; j < p.k; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < kPer; ++i) best = max(best, key[i]);
+    const uint32_t best = (uint32_t)(key[0] >> 32);
     const uint32_t most = __reduce_max_sync(kAll, best);
     if (most <= kDead) break;
-    const int leader = __ffs(__ballot_sync(kAll, best == most)) - 1;
-    int at = 0;
-    float v = 0.f;
+    if (lane == __ffs(__ballot_sync(kAll, best == most)) - 1) {
+      chosen[j] = lane * PER + PER - 1 - (int)(uint32_t)key[0];
+      logit[j] = value_of(most);
 #pragma unroll
-    for (int i = kPer - 1; i >= 0; --i)
-      if (key[i] == most) at = i, v = l[i];
-    if (lane == leader) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i == at) key[i] = 0;
+      for (int i = 0; i < PER; ++i) key[i] = key[i + 1];
     }
-    at = __shfl_sync(kAll, lane * kPer + at, leader);
-    v = __shfl_sync(kAll, v, leader);
-    if (lane == j) mine = v, my_e = at;
   }
+  __syncwarp();
+  const int my_e = lane < p.k ? chosen[lane] : -1;
+  const float mine = my_e < 0 ? -INFINITY : logit[lane];
   // the first is the largest (a NaN, if there is one); equal logits weigh the same, infinities too
   const float top = __shfl_sync(kAll, mine, 0);
   const float e = my_e < 0 ? 0.f : mine == top ? 1.f : expf(mine - top);
@@ -181,6 +195,7 @@ __device__ __forceinline__ void choose(const Decode& p, int t, int* expert, floa
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
   *expert = my_e;
   *weight = my_e < 0 ? 0.f : e / sum;
+  __syncwarp();
 }
 
 // Lane j's slot of token t into the lists by expert.
@@ -522,18 +537,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   if (tid < p.E) list->by_expert[tid] = 0;
   if (tid < p.T) list->w[p.E][tid] = 1.f;  // the shared expert's
   bool fine = true;
-  int gen = tid == 0 ? moe::ld_acquire(&p.sched->gen) : 0;
+  // arrivals before this pass: a whole number of grids, and maybe others' first ones of this pass
+  unsigned long long target = 0;
+  if (tid == 0) target = *static_cast<volatile unsigned long long*>(&p.sched->arrived) / blocks * blocks;
   // 1: logits, and the choice
   if (p.router_w) logits<NT>(p, sm, share(p.E, block, blocks), share(p.E, block + 1, blocks));
   if (!producer) {
-    if (p.router_w) fine = grid_wait(p.sched, gen++, deadline, &list->ok);
+    if (p.router_w) fine = grid_wait(p.sched, target += blocks, deadline, &list->ok);
     else sync_consumers();
     if (fine) {
       for (int t = warp; t < p.T; t += kWarps) {
         int e = -1;
         float w = 0.f;
-        if (p.router_w) choose(p, t, &e, &w);
-        else if (lane < p.k) e = p.idx_in[t * p.k + lane], w = p.w_in[t * p.k + lane];
+        if (p.router_w) {
+          if (p.E <= 128) choose<4>(p, list, t, &e, &w);
+          else choose<8>(p, list, t, &e, &w);
+        } else if (lane < p.k) e = p.idx_in[t * p.k + lane], w = p.w_in[t * p.k + lane];
         enter(p, list, t, e, w);
         if (block == 0 && lane < p.k && p.router_w) {
           if (p.idx_out) p.idx_out[t * p.k + lane] = e;
@@ -665,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
     });
   }
   me.tell();
-  if (!grid_wait(p.sched, gen++, deadline, &list->ok) || *abort) {
+  if (!grid_wait(p.sched, target += blocks, deadline, &list->ok) || *abort) {
     if (tid == 0) *abort = 1;
     return;
   }
