@@ -47,7 +47,7 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kMaxT = 16, kMaxK = 16, kMaxE = 256, kMaxD = 32768;
 constexpr int kWarps = 8, kConsumers = kWarps * 32;
-constexpr int kTeams = 2, kTeam = kWarps / kTeams;
+constexpr int kTeams = 1, kTeam = kWarps / kTeams;
 constexpr int kBringers = 4;     // warps that bring weights, and as many that bring tokens
 constexpr int kThreads = kConsumers + 2 * kBringers * 32;
 constexpr int kBlock = 32;       // columns of two mma
@@ -250,13 +250,13 @@ __device__ __forceinline__ void make_list(const Decode& p, List* list) {
   }
 }
 
-// Warps' sums of a tile; two tiles' worth, so that one wait a tile is enough.
+// Warps' sums of a tile; with 8 tokens two tiles' worth, so that one wait a tile is
+// enough.
 template <int NT>
 struct Sums {
-  static constexpr int kTile = NT * 8 * kColumn;
-  float v[2][kWarps][kTile];  // of the logits, at first: of all 16 warps
+  static constexpr int kTile = NT * 8 * kColumn, kTiles = NT == 1 ? 2 : 1;
+  float v[kTiles][kWarps][kTile];
 };
-static_assert(kThreads / 32 <= 2 * kWarps, "the logits' sums");
 
 template <int NT>
 struct Smem {
@@ -264,10 +264,10 @@ struct Smem {
   // cycles whatever it holds, so longer is better (4 tokens of 128 experts of 2048 x
   // 768: 76 us with 512, 65 with 1024), as long as the ring holds a few stages with
   // all the tokens' rows (13 tokens of 32 + 1 experts of 7168 x 2048: 524 and 689).
-  static constexpr int kChunk = NT == 1 ? 1024 : 512;
+  static constexpr int kChunk = 1024;
   static constexpr int kBlocks = kChunk / kBlock / kTeam;  // of a warp
   static constexpr int kPitch = kChunk * 2 + 64;  // bytes of a row: two rows next to each other use all banks
-  static constexpr int kRing = NT == 1 ? 86 : 152;  // rows; a stage has 64 at most (48 with 8 tokens)
+  static constexpr int kRing = 86;  // rows; a stage has 64 at most
   char ring[kRing][kPitch];
   Sums<NT> sums;
   List list;
@@ -324,22 +324,40 @@ struct Room {
   }
 };
 
+__device__ __forceinline__ int share(long long total, int part, int parts) { return (int)(total * part / parts); }
+
 // A block's share of the experts' f rows, tile by tile: at most 16 (of gate and of
-// up), none over an expert's end.  Stepped along: a division a tile in every warp, a
-// stage even, is what the kernel then waits for.
+// up), none over an expert's end.  Every block has its part of the shared expert's
+// rows, first, and of the others' together: the shared expert's stages hold all
+// tokens, and blocks that had nothing else would keep the grid waiting.  Stepped along:
+// a division a tile in every warp, a stage even, is what the kernel then waits for.
 struct GateUpTiles {
-  int f, left;      // rows still to come, with this tile's
-  int entry, first; // of the list, first row there
-  __device__ __forceinline__ GateUpTiles(int f_, int r0, int r1) : f(f_), left(r1 - r0), entry(r0 / f_), first(r0 % f_) {}
-  __device__ __forceinline__ int rows() const { return min(min(16, left), f - first); }
+  const List* list;
+  int f, left, later;  // rows still to come, with this tile's; of the other experts behind the shared one's
+  int entry, first;    // of the list, first row there
+  int later_entry, later_first;
+  __device__ __forceinline__ GateUpTiles(const List* l, int f_, int shared, int block, int blocks) : list(l), f(f_) {
+    const int routed = l->n - shared;
+    const int r0 = share((long long)routed * f, block, blocks), r1 = share((long long)routed * f, block + 1, blocks);
+    left = r1 - r0, entry = r0 / f, first = r0 % f;
+    later = 0;
+    if (shared) {
+      later = left, later_entry = entry, later_first = first;
+      first = share(f, block, blocks), left = share(f, block + 1, blocks) - first, entry = routed;
+      if (left == 0) other();
+    }
+  }
+  __device__ __forceinline__ void other() { left = later, entry = later_entry, first = later_first, later = 0; }
+  // with more tokens fewer rows, so that two stages still fit into the ring
+  __device__ __forceinline__ int rows() const { return min(min(__popc(list->tokens[entry]) > 11 ? 12 : 16, left), f - first); }
   __device__ __forceinline__ void next() {
     const int n = rows();
     left -= n, first += n;
-    if (first == f) ++entry, first = 0;
+    if (left == 0 && later > 0) other();
+    else if (first == f) ++entry, first = 0;
   }
 };
 
-__device__ __forceinline__ int share(long long total, int part, int parts) { return (int)(total * part / parts); }
 
 // What a stage is: weight rows (and how many of them are there), the tokens that it is
 // for, and how many rows each of them has (h': two).
@@ -414,7 +432,8 @@ struct Consumer {
       }
   }
 
-  // One stage, M as in multiply.
+  // One stage, M as in multiply.  Columns are the tokens, or (a product of one part, whose
+  // tile has one expert) those of them that are there, one after another.
   template <int PARTS, int M>
   __device__ __forceinline__ void stage(const Stage& st, int hi) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -425,7 +444,7 @@ struct Consumer {
         int before = 0;
 #pragma unroll
         for (int q = 0; q < NT; ++q) {
-          const uint32_t tokens = (uint32_t)st.tokens >> (8 * q) & 0xffu;
+          const uint32_t tokens = (PARTS == 1 ? (1u << n) - 1u : (uint32_t)st.tokens) >> (8 * q) & 0xffu;
           if (NT == 1 || tokens) multiply<PARTS, M>(st, hi, before, tokens, n, total[q]);
           before += __popc(tokens);
         }
@@ -437,11 +456,12 @@ struct Consumer {
     if (++turn == kTeams) turn = 0;
   }
 
-  // The warps' sums together: end(row, token, sum), all threads at once.
+  // The warps' sums together: end(row, column, sum), all threads at once.
   template <typename End>
   __device__ __forceinline__ void finish(End&& end) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    float(*sums)[Sums<NT>::kTile] = sm->sums.v[tile++ & 1];
+    float(*sums)[Sums<NT>::kTile] = sm->sums.v[tile++ % Sums<NT>::kTiles];
+    if (Sums<NT>::kTiles == 1) sync_consumers();  // the last tile's have been read
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -452,11 +472,11 @@ struct Consumer {
     sync_consumers();
 #pragma unroll
     for (int q = 0; q < NT; ++q) {  // 32 rows of 8 tokens: a thread each
-      const int row = lane, token = q * 8 + warp;
+      const int row = lane, column = q * 8 + warp;
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += sums[w][token * kColumn + row];
-      end(row, token, s);
+      for (int w = 0; w < kWarps; ++w) s += sums[w][column * kColumn + row];
+      end(row, column, s);
     }
     clear();
   }
@@ -500,7 +520,8 @@ __device__ __forceinline__ void logits(const Decode& p, Smem<NT>* sm, int e0, in
 #pragma unroll
         for (int j = 0; j < 2; ++j) total[n][j] += part[n][0][j] + part[n][1][j];
     }
-    float* mine = sm->sums.v[0][0] + warp * Sums<NT>::kTile;
+    float* all = reinterpret_cast<float*>(sm->ring);  // nothing is on its way yet
+    float* mine = all + warp * Sums<NT>::kTile;
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -511,7 +532,7 @@ __device__ __forceinline__ void logits(const Decode& p, Smem<NT>* sm, int e0, in
     if (token < p.T && e + row < e1) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kThreads / 32; ++w) s += sm->sums.v[0][0][w * Sums<NT>::kTile + token * kColumn + row];
+      for (int w = 0; w < kThreads / 32; ++w) s += all[w * Sums<NT>::kTile + token * kColumn + row];
       p.logits[token * p.E + e + row] = s + (p.bias ? p.bias[e + row] : 0.f);
     }
   }
@@ -567,10 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   __syncthreads();
   if (sm->abort) return;  // nothing is on its way yet
 
-  const long long rows = (long long)list->n * p.f;
-  GateUpTiles gate_up(p.f, share(rows, block, blocks), share(rows, block + 1, blocks));
+  GateUpTiles gate_up(list, p.f, p.S, block, blocks);
   const int d0 = share(p.d, block, blocks), d1 = share(p.d, block + 1, blocks);
-  const int down_tiles = (d1 - d0 + kRows - 1) / kRows;
+  const int down_tiles = (d1 - d0 + kRows - 1) / kRows, down_rows = (d1 - d0 + down_tiles - 1) / max(1, down_tiles);
   const int x_chunks = (p.d + kChunk - 1) / kChunk, f_chunks = (p.f + kChunk - 1) / kChunk;
   volatile int* abort = &sm->abort;
   const int n_list = list->n;
@@ -605,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
           go = bring(Stage{2 * n, tokens, 1, min(kChunk, p.d - c * kChunk)}, base + c * kChunk);
       }
       for (int i = 0; go && i < down_tiles; ++i) {
-        const int first = d0 + i * kRows, n = min(kRows, d1 - first);
+        const int first = d0 + i * down_rows, n = min(down_rows, d1 - first);
         for (int a = 0; go && a < n_list; ++a) {
           const bf16* base = p.down + ((size_t)list->expert[a] * p.d + first + mine) * p.f;
           const int tokens = (int)list->tokens[a];
@@ -647,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
     }
     go = go && room.wait(&sm->h_ready, 0);
     for (int i = 0; go && i < down_tiles; ++i) {
-      const int n = min(kRows, d1 - d0 - i * kRows);
+      const int n = min(down_rows, d1 - d0 - i * down_rows);
       for (int a = 0; go && a < n_list; ++a) {
         const int tokens = (int)list->tokens[a];
         const size_t at = (size_t)list->start[a] * p.f;
@@ -671,11 +691,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
       if (n > 8) me.template stage<1, 2>(st, n);
       else me.template stage<1, 1>(st, n);
     }
-    me.finish([&](int row, int token, float s) {
+    me.finish([&](int row, int column, float s) {
       const float up = __shfl_xor_sync(kAll, s, 16);  // rows 16 to 31 are up's
-      if (row >= n || !(tokens >> token & 1u)) return;
-      const float h = s / (1.f + expf(-s)) * up * list->w[expert][token];
-      const size_t slot = list->start[a] + __popc(tokens & ((1u << token) - 1u));
+      if (row >= n || column >= __popc(tokens)) return;
+      const float h = s / (1.f + expf(-s)) * up * list->w[expert][list->order[a][column]];
+      const size_t slot = list->start[a] + column;
       const bf16 hi = __float2bfloat16_rn(h);
       p.h_hi[slot * p.f + first + row] = hi;
       // an infinity or a NaN is all in the first part
@@ -691,8 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   if (tid == 0) mbar_arrive(&sm->h_ready);
 
   // 3: down
-  for (int r0 = d0; r0 < d1; r0 += kRows) {
-    const int n = min(kRows, d1 - r0);
+  for (int r0 = d0; r0 < d1; r0 += down_rows) {
+    const int n = min(down_rows, d1 - r0);
     for (int a = 0; a < n_list; ++a) {
       const int tokens = (int)list->tokens[a];
       for (int c = 0; c < f_chunks; ++c) {
