@@ -605,7 +605,8 @@ typedef struct moe_norm_grads {
   long long gate_stride;
 } moe_norm_grads;
 
-/* Allocate the workspace (moe_norm_workspace_bytes: 10 MB, less for narrow rows)
+/* Allocate the workspace (moe_norm_workspace_bytes: 20 MB, less for narrow rows,
+ * 80 MB for the widest)
  * for gradients [d], on the current device.  Once is enough; the only allocating
  * call. */
 int moe_norm_reserve(moe_norm_t* h, void* stream);

@@ -10,8 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 REPO = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "_build", "libmoe.so")
-SOURCES = ["moe.cu", "router.cu", "rows8.cu", "norm.cu", "decode.cu", "w4.cu"]
-DEPS = SOURCES + ["tasks.cuh", "layer.cuh", "ptx.cuh", "error.h", "tmap.h", "w4_tiles.cuh", "rows8.cuh"]
+SOURCES = ["moe.cu", "router.cu", "rows8.cu", "norm.cu", "norm_grad.cu", "decode.cu", "w4.cu"]
+DEPS = SOURCES + ["tasks.cuh", "layer.cuh", "ptx.cuh", "error.h", "tmap.h", "w4_tiles.cuh", "rows8.cuh", "norm.cuh"]
 HEADER = os.path.join(REPO, "include", "moe.h")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",

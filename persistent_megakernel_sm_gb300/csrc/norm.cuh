@@ -1,0 +1,699 @@
+// The norms about a block, with its gate and the residual stream, and their
+// gradient.  Per token (row), with the residual r, the block's output y, a gate g
+// and a factor s:
+//   p   = N_post(y)                  or y itself
+//   out = r + s g p                  rounded to r's type
+//   n   = N_pre(out)                 of the rounded sum: what the next block reads
+//   N(x) = (x - m) / sqrt(mean (x - m)^2 + eps) * gain + shift, m the mean (layer)
+//   or 0 (rms)
+// Backward, with u = (x - m) rstd of a norm, t = (gradient) * gain:
+//   through the norm  rstd (t - u mean(t u) - [layer] mean(t))
+//   G = grad_out + (that of n),  grad_r = G,  grad of p = s g G, again through the
+//   post norm; grad gain = sum over rows of (gradient) u, grad shift of (gradient),
+//   grad g = s G p over the rows, the columns or neither.
+// The second norm's means are linear in G, which is grad_out + rstd t less multiples
+// of 1 and u, so all of a row's sums are taken in one go, before either norm's
+// means are known: one exchange a row.
+//
+// What bounds both is HBM, so the rest is kept out of its way.  A block holds a row (a
+// cluster of 2 to 8 blocks one that is too wide), a lane up to 4 times 8 consecutive
+// columns of it, and goes over its rows as a pipeline: while one row is finished, the
+// next one's sums are taken and the rows behind are on their way, so a row costs one
+// exchange of the block's warps.  Rows come by asynchronous 16-byte copies into slots
+// of shared memory that belong to the thread that reads them: no barrier guards them.
+// Rows that are not aligned come as the 16-byte pieces that they lie in, shifted when
+// they are read (a piece between two lanes comes twice, the second time from L1), and
+// leave a warp's 256 columns at a time, each store along the row.  Gains and shifts stay
+// in shared memory; products and sums run in pairs.  Sums over rows are kept in
+// registers, written once a block and added by a second kernel in a fixed order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+#include <new>
+#include <type_traits>
+
+#include "error.h"
+#include "moe.h"
+#include "ptx.cuh"
+#include "rows8.cuh"
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kMaxD = 32768;
+constexpr int kThreads = 512;            // of a block, at most
+constexpr int kMaxStages = 4;            // rows under way
+constexpr int kSms = 152;
+constexpr int kRing = 200 * 1024;        // shared memory of an SM for all of it
+constexpr int kMaxSmem = 227 * 1024;     // of a block
+constexpr int kMaxCluster = 16;          // 8 are portable; 16 for the widest rows that are not aligned
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kNone = MOE_NORM_NONE, kRms = MOE_NORM_RMS, kLayer = MOE_NORM_LAYER;
+
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ------------------------------------------------------------------------ pairs
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+
+// 8 columns.
+struct Eight {
+  float2 v[4];
+  __device__ __forceinline__ float get(int i) const { return i & 1 ? v[i >> 1].y : v[i >> 1].x; }
+  __device__ __forceinline__ void set(int i, float x) { (i & 1 ? v[i >> 1].y : v[i >> 1].x) = x; }
+  __device__ __forceinline__ void cut(int n) {  // zeros from column n on
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= n) set(i, 0.f);
+  }
+};
+
+__device__ __forceinline__ Eight unpack(const uint32_t (&w)[4]) {
+  Eight e;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  return e;
+}
+__device__ __forceinline__ uint4 pack(const Eight& e) {
+  union {
+    __nv_bfloat162 b[4];
+    uint4 q;
+  } u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u.b[i] = __floats2bfloat162_rn(e.v[i].x, e.v[i].y);
+  return u.q;
+}
+
+// ------------------------------------------------------------------------ slots
+
+// cp.async of 16 or 8 bytes, of which n are read and the rest zero, and of 4.
+__device__ __forceinline__ void copy16(void* to, const void* from, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(moe::smem_u32(to)), "l"(from), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy8(void* to, const void* from, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(moe::smem_u32(to)), "l"(from), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy4(void* to, const void* from, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(moe::smem_u32(to)), "l"(from), "r"(n) : "memory");
+}
+
+// Rows of a tensor: where row 0 begins and how far the next is, in elements.
+template <typename T>
+struct Rows {
+  T* p;
+  long long stride;
+  __device__ __forceinline__ T* at(long long t) const { return p + t * stride; }
+};
+
+struct Rows8 {
+  int8_t* codes;  // null: none
+  bf16* scales;
+};
+
+struct Shape {
+  int T, d, stages;
+  int field[5];    // offsets of a stage's fields, in bytes
+  int stage;       // bytes of a stage
+  int vec;         // where the gains and shifts begin
+  int out;         // where the warps' rows for unaligned stores begin
+  int parts;       // where the warps' parts of the sums begin, for this row and the one before
+  int groups, group_lanes;  // of 8-bit rows
+  float scale, eps, one;    // one: 1 where gains are stored less 1
+};
+
+// Pieces of 16 bytes (codes: of 8) that hold 8 columns: those of aligned rows, one
+// more of others.
+template <typename T, bool VEC>
+__host__ __device__ constexpr int pieces() {
+  return (int)sizeof(T) / 2 + (VEC ? 0 : 1);
+}
+template <bool VEC>
+__host__ __device__ constexpr int pieces8() {
+  return VEC ? 1 : 2;
+}
+
+// `units`: threads times a thread's eights; unit: chunk * threads + thread.  A field is
+// one plane of 16 bytes a unit for each piece, or of 8 and one of 4 for a scale.
+template <typename T, bool VEC>
+__device__ __forceinline__ void fetch(char* field, int units, int unit, const T* row, int col, int d) {
+  if (col >= d) return;
+  uint4* slot = reinterpret_cast<uint4*>(field) + unit;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < pieces<T, true>(); ++i) moe::cp_async16(slot + i * units, row + col + i * (16 / sizeof(T)));
+  } else {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + col);
+    const int end = (int)(at & 15) + min(8, d - col) * (int)sizeof(T);  // from the first piece's begin
+    const char* from = reinterpret_cast<const char*>(at & ~(uintptr_t)15);
+#pragma unroll
+    for (int i = 0; i < pieces<T, false>(); ++i)
+      if (16 * i < end) copy16(slot + i * units, from + 16 * i, min(16, end - 16 * i));
+  }
+}
+
+// N words from byte `shift` of the words before on; `shift` is a row's.
+template <int N, int M>
+__device__ __forceinline__ void shifted(const uint32_t (&w)[M], int shift, uint32_t (&out)[N]) {
+  uint32_t a[M + 1], b[M + 1];
+#pragma unroll
+  for (int i = 0; i < M; ++i) a[i] = w[i];
+  a[M] = 0;
+  if (M - N >= 3) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) b[i] = shift & 8 ? (i + 2 < M ? a[i + 2] : 0u) : a[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < M; ++i) b[i] = a[i];
+  }
+#pragma unroll
+  for (int i = 0; i < M; ++i) a[i] = shift & 4 ? (i + 1 < M ? b[i + 1] : 0u) : b[i];
+#pragma unroll
+  for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(a[i], a[i + 1], (shift & 3) * 8);
+}
+
+__device__ __forceinline__ void put_words(uint4 q, uint32_t* w) { w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w; }
+
+// What was fetched.  n: the columns that are there.
+template <typename T, bool VEC>
+__device__ __forceinline__ Eight read(const char* field, int units, int unit, const T* row, int n) {
+  constexpr int kPieces = pieces<T, VEC>(), kWords = (int)sizeof(T) * 2;
+  const uint4* slot = reinterpret_cast<const uint4*>(field) + unit;
+  uint32_t in[4 * kPieces], w[kWords];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) put_words(slot[i * units], in + 4 * i);
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = in[i];
+  } else {
+    shifted(in, (int)(reinterpret_cast<uintptr_t>(row) & 15), w);
+  }
+  Eight e;
+  if constexpr (sizeof(T) == 2) {
+    e = unpack(w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e.v[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+  if (!VEC && n < 8) e.cut(n);
+  return e;
+}
+
+template <bool VEC>
+__device__ __forceinline__ void fetch8(char* field, int units, int unit, const Rows8& r, long long t, const Shape& a, int col) {
+  if (col >= a.d) return;
+  uint2* slot = reinterpret_cast<uint2*>(field) + unit;
+  const int8_t* row = r.codes + t * a.d + col;
+  if constexpr (VEC) {
+    copy8(slot, row, 8);
+  } else {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row);
+    const int end = (int)(at & 7) + min(8, a.d - col);
+    const char* from = reinterpret_cast<const char*>(at & ~(uintptr_t)7);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (8 * i < end) copy8(slot + i * units, from + 8 * i, min(8, end - 8 * i));
+  }
+  // the word that the scale is in; the tensor may end in its middle
+  const long long scale = t * a.groups + col / (8 * a.group_lanes);
+  const bool last = scale == (long long)a.T * a.groups - 1 && !(scale & 1);
+  copy4(field + (size_t)units * 8 * pieces8<VEC>() + 4 * unit, r.scales + (scale & ~1ll), last ? 2 : 4);
+}
+
+template <bool VEC>
+__device__ __forceinline__ Eight read8(const char* field, int units, int unit, const Rows8& r, long long t, const Shape& a, int col,
+                                       int n) {
+  const uint2* slot = reinterpret_cast<const uint2*>(field) + unit;
+  uint32_t w[2];
+  const uint2 q = slot[0];
+  if constexpr (VEC) {
+    w[0] = q.x, w[1] = q.y;
+  } else {
+    const uint2 q2 = slot[units];
+    const uint32_t in[4] = {q.x, q.y, q2.x, q2.y};
+    shifted(in, (int)(reinterpret_cast<uintptr_t>(r.codes + t * a.d) & 7), w);
+  }
+  const uint32_t word = *reinterpret_cast<const uint32_t*>(field + (size_t)units * 8 * pieces8<VEC>() + 4 * unit);
+  const bool odd = (t * a.groups + col / (8 * a.group_lanes)) & 1;
+  const float s = __uint_as_float(odd ? word & 0xffff0000u : word << 16);
+  float x[8];
+  moe::rows8_floats(w[0], x);
+  moe::rows8_floats(w[1], x + 4);
+  Eight e;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e.v[i] = mul2(make_float2(x[2 * i], x[2 * i + 1]), two(s));
+  if (!VEC && n < 8) e.cut(n);
+  return e;
+}
+
+// ----------------------------------------------------------------------- stores
+
+// A thread's 8 columns to a row.  VEC: at once; else by way of the warp's own 1 KB,
+// each store along the row (lane_col: the warp's first column and the lane).
+template <bool VEC>
+__device__ __forceinline__ void store_row(bf16* row, uint4 q, int col, int d, float* warp_row) {
+  if constexpr (VEC) {
+    if (col < d) __stcs(reinterpret_cast<uint4*>(row + col), q);
+  } else {
+    const int lane = threadIdx.x & 31, lane_col = col - 7 * lane;
+    __syncwarp();
+    reinterpret_cast<uint4*>(warp_row)[lane] = q;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane_col + 32 * i < d) row[lane_col + 32 * i] = reinterpret_cast<bf16*>(warp_row)[lane + 32 * i];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_row(float* row, const Eight& e, int col, int d, float* warp_row) {
+  const float4 a = make_float4(e.v[0].x, e.v[0].y, e.v[1].x, e.v[1].y), b = make_float4(e.v[2].x, e.v[2].y, e.v[3].x, e.v[3].y);
+  if constexpr (VEC) {
+    if (col >= d) return;
+    __stcs(reinterpret_cast<float4*>(row + col), a);
+    __stcs(reinterpret_cast<float4*>(row + col) + 1, b);
+  } else {
+    const int lane = threadIdx.x & 31, lane_col = col - 7 * lane;
+    __syncwarp();
+    reinterpret_cast<float4*>(warp_row)[lane * 2] = a;
+    reinterpret_cast<float4*>(warp_row)[lane * 2 + 1] = b;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane_col + 32 * i < d) row[lane_col + 32 * i] = warp_row[lane + 32 * i];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_row(bf16* row, const Eight& e, int col, int d, float* warp_row) {
+  store_row<VEC>(row, pack(e), col, d, warp_row);
+}
+
+// The thread's 8 columns of a row of T, held in 8 bits; zeros behind the row's end.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_rows8(const Rows8& r, long long t, const Shape& a, const Eight& e, int col, float* warp_row) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) most = max(most, moe::abs_bits(e.get(i)));
+  for (int o = a.group_lanes >> 1; o; o >>= 1) most = max(most, __shfl_xor_sync(kAll, most, o));
+  const bf16 s = moe::rows8_scale<T>(most);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = e.get(i);
+  uint32_t word[2];
+  moe::rows8_codes<T>(v, s, word);
+  const int lane = threadIdx.x & 31;
+  if constexpr (VEC) {
+    if (col < a.d) __stcs(reinterpret_cast<uint2*>(r.codes + t * a.d + col), make_uint2(word[0], word[1]));
+  } else {
+    const int lane_col = col - 7 * lane;
+    __syncwarp();
+    reinterpret_cast<uint2*>(warp_row)[lane] = make_uint2(word[0], word[1]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane_col + 32 * i < a.d) r.codes[t * a.d + lane_col + 32 * i] = reinterpret_cast<int8_t*>(warp_row)[lane + 32 * i];
+  }
+  if (col < a.d && (lane & (a.group_lanes - 1)) == 0) r.scales[t * a.groups + col / (8 * a.group_lanes)] = s;
+}
+
+// ------------------------------------------------------------------------- sums
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// Mean and summed squares about it of n values, put together with another n's
+// (Chan, Golub and LeVeque): no large sums are taken from one another.
+struct Moments {
+  float n, mean, m2;
+};
+
+__device__ __forceinline__ Moments both(const Moments& a, const Moments& b) {
+  if (a.n == 0.f) return b;  // an empty side's square could overflow
+  if (b.n == 0.f) return a;
+  const float n = a.n + b.n;
+  const float part = __fdividef(b.n, n), off = b.mean - a.mean;
+  return Moments{n, fmaf(off, part, a.mean), a.m2 + fmaf(off * off, a.n * part, b.m2)};
+}
+
+__device__ __forceinline__ Moments warp_moments(Moments m) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+    m = both(m, Moments{__shfl_xor_sync(kAll, m.n, o), __shfl_xor_sync(kAll, m.mean, o), __shfl_xor_sync(kAll, m.m2, o)});
+  // the two sides of an exchange round differently: one lane's for all
+  return Moments{m.n, __shfl_sync(kAll, m.mean, 0), __shfl_sync(kAll, m.m2, 0)};
+}
+
+// What a norm is made of, of a thread's columns: the moments, or the sum of squares.
+template <bool LAYER>
+struct Part {
+  Moments m{0.f, 0.f, 0.f};
+  __device__ __forceinline__ void add(const Eight& e, int n) {
+    float2 s = add2(add2(e.v[0], e.v[1]), add2(e.v[2], e.v[3]));  // zeros behind the row's end
+    const float mean = n == 8 ? (s.x + s.y) * 0.125f : n ? __fdividef(s.x + s.y, (float)n) : 0.f;
+    s = make_float2(0.f, 0.f);
+    Eight off = e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) off.v[i] = add2(off.v[i], two(-mean));
+    if (n < 8) off.cut(n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fma2(off.v[i], off.v[i], s);
+    m = both(m, Moments{(float)n, mean, s.x + s.y});
+  }
+  __device__ __forceinline__ float2 warp() const {
+    const Moments w = warp_moments(m);
+    return make_float2(w.mean, w.m2);
+  }
+};
+template <>
+struct Part<false> {
+  float2 squares = make_float2(0.f, 0.f);
+  __device__ __forceinline__ void add(const Eight& e, int) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) squares = fma2(e.v[i], e.v[i], squares);
+  }
+  __device__ __forceinline__ float2 warp() const { return make_float2(warp_sum(squares.x + squares.y), 0.f); }
+};
+
+// (mean, rstd) from every warp's part; count(w): the columns of warp w.
+template <bool LAYER, typename Count>
+__device__ __forceinline__ float2 whole(const float2* parts, int stride, int warps, float inv_d, float eps, Count&& count) {
+  const int lane = threadIdx.x & 31;
+  float mean = 0.f, m2;
+  if constexpr (LAYER) {
+    Moments m{0.f, 0.f, 0.f};
+    for (int w = lane; w < warps; w += 32) {
+      const float2 p = parts[w * stride];
+      m = both(m, Moments{(float)count(w), p.x, p.y});
+    }
+    m = warp_moments(m);
+    mean = m.mean, m2 = m.m2;
+  } else {
+    float s = 0.f;
+    for (int w = lane; w < warps; w += 32) s += parts[w * stride].x;
+    m2 = warp_sum(s);
+  }
+  return make_float2(mean, __frsqrt_rn(fmaf(m2, inv_d, eps)));
+}
+
+__device__ __forceinline__ Eight load_params(const void* p, int f32, int col, int n, float none, float plus) {
+  Eight e;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    e.set(i, !p ? none : i >= n ? 0.f
+                                : plus + (f32 ? static_cast<const float*>(p)[col + i]
+                                              : __bfloat162float(static_cast<const bf16*>(p)[col + i])));
+  return e;
+}
+
+// Eight numbers a unit in shared memory, in two planes.
+struct Kept {
+  float4* base;
+  int units;
+  __device__ __forceinline__ void write(int i, int unit, const Eight& e) const {
+    base[(2 * i) * units + unit] = make_float4(e.v[0].x, e.v[0].y, e.v[1].x, e.v[1].y);
+    base[(2 * i + 1) * units + unit] = make_float4(e.v[2].x, e.v[2].y, e.v[3].x, e.v[3].y);
+  }
+  __device__ __forceinline__ Eight read(int i, int unit) const {
+    const float4 a = base[(2 * i) * units + unit], b = base[(2 * i + 1) * units + unit];
+    Eight e;
+    e.v[0] = make_float2(a.x, a.y), e.v[1] = make_float2(a.z, a.w), e.v[2] = make_float2(b.x, b.y), e.v[3] = make_float2(b.z, b.w);
+    return e;
+  }
+};
+
+// The blocks of a cluster exchange their warps' parts; a single block's warps too.
+struct Team {
+  int blocks, rank, warps;  // warps: of the whole team
+
+  __device__ __forceinline__ Team() {
+    uint32_t n, r;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    blocks = (int)n, rank = (int)r, warps = (int)(n * blockDim.x / 32);
+  }
+  // one lane writes to every block
+  __device__ __forceinline__ void write(float4* at, float4 v) const {
+    if (blocks == 1) {
+      *at = v;
+    } else {
+      for (int b = 0; b < blocks; ++b) {
+        const uint32_t to = moe::mapa_shared(moe::smem_u32(at), (uint32_t)b);
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                     : "memory");
+      }
+    }
+  }
+  __device__ __forceinline__ void exchange() const {
+    if (blocks > 1) asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    else __syncthreads();
+  }
+};
+
+// Before anything is under way: slots of columns behind the row's end, which no copy
+// reaches, are read as zeros; and a cluster's blocks all have to run before one writes
+// to another.
+__device__ __forceinline__ void begin(const Shape& a, const Team& team, char* smem, int columns) {
+  if (columns > a.d) {
+    for (int o = threadIdx.x; o < a.stages * a.stage / 16; o += blockDim.x) reinterpret_cast<uint4*>(smem)[o] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
+  if (team.blocks > 1) moe::cluster_sync();
+}
+
+// Rows in a ring of stages: the stage of the row that enters, and of those behind it.
+struct Ring {
+  char* base;
+  int stage, stages, at = 0;
+  __device__ __forceinline__ char* slot(int back) const {  // of the row that entered `back` rows ago
+    const int i = at - back;
+    return base + (i < 0 ? i + stages : i) * stage;
+  }
+  __device__ __forceinline__ void next() {
+    if (++at == stages) at = 0;
+  }
+};
+
+// Until the row that enters has come, if LEFT more may still be on their way behind it.
+__device__ __forceinline__ void wait_copies(int left) {
+  if (left == 0) moe::cp_async_wait<0>();
+  else if (left == 1) moe::cp_async_wait<1>();
+  else moe::cp_async_wait<2>();
+}
+
+// ------------------------------------------------------------------------- host
+
+template <typename T>
+bool rows_aligned(const Rows<T>& r) {  // for 16-byte vectors
+  return reinterpret_cast<uintptr_t>(r.p) % 16 == 0 && (size_t)r.stride * sizeof(T) % 16 == 0;
+}
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+size_t type_size(int type) { return type == MOE_TYPE_F32 ? 4 : 2; }
+
+// How a kernel is laid over rows: eights of a lane, blocks of a row, their threads, and
+// how many of them an SM is given.
+struct Plan {
+  int chunks, blocks, threads, per_sm, smem;
+};
+
+// A block's threads and shared memory for `chunks` eights a lane: as many blocks to a
+// row as it takes for `least` stages to fit, as many blocks to an SM as it then has
+// room for, up to sm_threads threads, and as many stages, up to kMaxStages.
+Plan lay_out(Shape* a, int chunks, int sm_threads, const int (&field_bytes)[5], int kept, int quads, int least, bool vec) {
+  Plan p;
+  p.chunks = chunks;
+  const int lanes = (a->d + 7) / 8;
+  int rest = 0, parts = 0, units = 0;
+  auto with = [&](int blocks) {
+    p.blocks = blocks;
+    p.threads = ((lanes + blocks * chunks - 1) / (blocks * chunks) + 31) / 32 * 32;
+    units = p.threads * chunks;
+    a->stage = 0;
+    for (int i = 0; i < 5; ++i) a->field[i] = a->stage, a->stage += (field_bytes[i] + 15) / 16 * 16 * units;
+    parts = 2 * quads * p.blocks * p.threads / 32 * 16;
+    rest = kept * 32 * units + (vec ? 0 : p.threads * 32) + parts;
+    return p.threads <= kThreads && least * a->stage + rest <= kRing;
+  };
+  int blocks = 1;
+  while (!with(blocks) && blocks < kMaxCluster) blocks *= 2;
+  p.per_sm = std::max(1, std::min({16, sm_threads / p.threads, kRing / (least * a->stage + rest)}));
+  a->stages = std::max(least, std::min(kMaxStages, (kRing / p.per_sm - rest) / std::max(1, a->stage)));
+  a->vec = a->stages * a->stage;
+  a->out = a->vec + kept * 32 * units;
+  a->parts = a->vec + rest - parts;
+  p.smem = a->vec + rest;
+  return p;
+}
+
+template <typename, bool, bool, int, int>
+struct ForwardKernel;
+template <typename, bool, bool, int, int>
+struct BackwardKernel;
+
+// Shared memory beyond 48 KB and clusters beyond 8 are asked for once a kernel and device.
+template <typename Kernel, typename F>
+cudaError_t allow_smem(F* kernel) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <typename... A>
+cudaError_t launch(void (*kernel)(A...), unsigned grid, int cluster, int threads, int smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // kernels wait themselves
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+struct moe_norm {
+  int d, pre, post, gate, group;
+  float eps, scale, one;
+  float* sums = nullptr;  // of the teams of a backward pass
+  int device = -1;
+};
+
+namespace {
+
+// Rows that a backward pass takes at once, at most: its teams.
+int most_teams(const moe_norm* h) {
+  int most = 1;
+  for (int chunks = 1; chunks <= 2; ++chunks) {
+    const int threads = ((h->d + 8 * chunks - 1) / (8 * chunks) + 31) / 32 * 32;
+    most = std::max(most, kSms * std::max(1, std::min(16, kThreads / threads)));
+  }
+  return most;
+}
+
+Shape shape_of(const moe_norm* h, int T) {
+  Shape a = {};
+  a.T = T;
+  a.d = h->d;
+  a.scale = h->scale;
+  a.eps = h->eps;
+  a.one = h->one;
+  a.groups = (h->d + h->group - 1) / h->group;
+  a.group_lanes = h->group / 8;
+  return a;
+}
+
+// Eights of a lane.  What a row costs a thread beside its columns (the exchanges, the
+// root) is shared by more of them; with few rows more threads are sooner done.
+int chunks_of(int d, int T, int most) {
+  if (T <= 2 * kSms) return 1;
+  const int lanes = (d + 7) / 8;
+  int c = 1;
+  while (c < most && c * 32 < lanes) c *= 2;
+  return c;
+}
+
+// f(aligned, pre norm a layer norm, post norm, eights of a lane), as types; with a
+// layer norm a lane has one.
+template <typename F>
+cudaError_t by_kind(const moe_norm* h, bool vec, int chunks, F&& f) {
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  constexpr std::integral_constant<int, kNone> none{};
+  constexpr std::integral_constant<int, kRms> rms{};
+  constexpr std::integral_constant<int, kLayer> layer{};
+  auto by_norms = [&](auto v) {
+    if (h->pre == kLayer)
+      return h->post == kNone ? f(v, std::true_type{}, none, one) : h->post == kRms ? f(v, std::true_type{}, rms, one) : f(v, std::true_type{}, layer, one);
+    if (h->post == kLayer) return f(v, std::false_type{}, layer, one);
+    if (h->post == kNone) return chunks == 1 ? f(v, std::false_type{}, none, one) : f(v, std::false_type{}, none, two);
+    return chunks == 1 ? f(v, std::false_type{}, rms, one) : f(v, std::false_type{}, rms, two);
+  };
+  return vec ? by_norms(std::true_type{}) : by_norms(std::false_type{});
+}
+
+const char* check_params(const moe_norm* h, const moe_norm_params* p) {
+  if (!p) return "null params";
+  if (p->type != MOE_TYPE_F32 && p->type != MOE_TYPE_BF16) return "gains and shifts are MOE_TYPE_F32 or MOE_TYPE_BF16";
+  const void* all[] = {p->pre_gain, p->pre_shift, p->post_gain, p->post_shift};
+  for (const void* q : all)
+    if (!aligned(q, type_size(p->type))) return "gains and shifts must be aligned to their type";
+  if (h->pre == kNone && p->pre_gain) return "a gain for a norm that the handle does not have";
+  if (h->post == kNone && p->post_gain) return "a gain for a norm that the handle does not have";
+  if ((h->pre != kLayer && p->pre_shift) || (h->post != kLayer && p->post_shift)) return "only layer norms have a shift";
+  if ((h->gate != MOE_GATE_NONE) != (p->gate != nullptr)) return "the gate must be given as the handle has it";
+  const size_t gate_size = h->gate == MOE_GATE_CHANNEL ? type_size(p->type) : h->gate == MOE_GATE_TOKEN ? 4 : 2;
+  if (!aligned(p->gate, gate_size)) return "the gate must be aligned to its type";
+  if (h->gate == MOE_GATE_ELEMENT && p->gate_stride < h->d) return "rows of the gate overlap: the row stride is below d";
+  return nullptr;
+}
+
+const char* check_rows8(const moe_rows8* r) {
+  if (!r) return nullptr;
+  if (!r->codes || !r->scales) return "null codes or scales of 8-bit rows";
+  if (!aligned(r->scales, 4)) return "scales of 8-bit rows must be 4-byte aligned";
+  return nullptr;
+}
+
+const char* check_rows(const moe_norm* h, const void* p, int type, long long stride) {
+  if (!p) return nullptr;
+  if (!aligned(p, type_size(type))) return "tensors must be aligned to their type";
+  if (stride < h->d) return "rows overlap: a row stride is below d";
+  return nullptr;
+}
+
+Rows8 rows8_of(const moe_rows8* r) {
+  return r ? Rows8{static_cast<int8_t*>(r->codes), static_cast<bf16*>(r->scales)} : Rows8{nullptr, nullptr};
+}
+
+template <typename T>
+Rows<T> rows_of(const void* p, long long stride) {
+  return Rows<T>{static_cast<T*>(const_cast<void*>(p)), stride};
+}
+
+}  // namespace
+

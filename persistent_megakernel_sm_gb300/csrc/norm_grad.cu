@@ -1,0 +1,497 @@
+// The norms about a block: the gradient (the formulas: norm.cuh).
+#include "norm.cuh"
+
+namespace {
+
+// --------------------------------------------------------------------- backward
+
+template <typename R>
+struct Backward {
+  Shape a;
+  Rows<const R> grad_out, kept_out;  // null: none; kept_out, y: null where they are kept in 8 bits
+  Rows<const bf16> grad_norm, y, gate_rows;
+  Rows8 out8, y8;
+  const float4* stats;
+  const float* gate_tokens;
+  const void *pre_gain, *post_gain, *post_shift, *gate_columns;
+  int params_f32;
+  Rows<R> grad_residual;  // null: not wanted
+  Rows<bf16> grad_y, grad_gate_rows;
+  float* grad_gate_tokens;
+  float* sums;            // [teams, 4, d]: gradient times u and gradient, of the pre norm and of the post norm
+};
+
+// The sums of a row, in the order in which they are reduced, of G' = grad_out + rstd t,
+// x = u of the pre norm, v = u gain g of the post norm, w = gain g, b its shift.
+enum { kTU, kUV, kXV, kT, kV, kUW, kXW, kW, kUB, kXB, kB, kSums };
+
+// Fours of them that a row has: kTU, kUV and kXV, with layer norms up to all.
+__host__ __device__ constexpr int quads_of(bool pre_layer, int post) { return pre_layer || post == kLayer ? 3 : 1; }
+
+template <typename R, bool VEC, bool PRE_LAYER, int POST, int CH>
+__global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant__ Backward<R> f) {
+  extern __shared__ __align__(16) char smem[];
+  constexpr int quads = quads_of(PRE_LAYER, POST);
+  constexpr bool POST_LAYER = POST == kLayer;
+  const Shape& a = f.a;
+  const Team team;
+  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x, units = CH * threads;
+  const int warp = team.rank * (threads / 32) + (tid >> 5);
+  const int first = blockIdx.x / team.blocks, step = gridDim.x / team.blocks;
+  const int rows = first < a.T ? (a.T - first - 1) / step + 1 : 0;
+  float* warp_row = reinterpret_cast<float*>(smem + a.out) + (tid >> 5) * 256;
+  const Kept kept{reinterpret_cast<float4*>(smem + a.vec), units};
+  Ring ring{smem, a.stage, a.stages};
+  auto row_at = [&](int i) { return (long long)first + (long long)i * step; };
+  auto unit_of = [&](int c) { return c * threads + tid; };
+  auto col_of = [&](int c) { return (team.rank * units + c * threads + tid) * 8; };
+  auto there = [&](int c) { return max(0, min(8, a.d - col_of(c))); };
+  const bool has_y = f.y.p || f.y8.codes, has_norm = f.grad_norm.p != nullptr;
+  const bool token_shift = POST_LAYER && f.grad_gate_tokens && f.post_shift;
+
+  wait_for_previous_kernel();
+  let_next_kernel_start();
+  begin(a, team, smem, team.blocks * units * 8);
+  auto start = [&](int i, char* slot) {
+    if (i < rows) {
+      const long long t = row_at(i);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int unit = unit_of(c), col = col_of(c);
+        if (f.grad_out.p) fetch<R, VEC>(slot + a.field[0], units, unit, f.grad_out.at(t), col, a.d);
+        if (has_norm) {
+          fetch<bf16, VEC>(slot + a.field[1], units, unit, f.grad_norm.at(t), col, a.d);
+          if (f.out8.codes) fetch8<VEC>(slot + a.field[2], units, unit, f.out8, t, a, col);
+          else fetch<R, VEC>(slot + a.field[2], units, unit, f.kept_out.at(t), col, a.d);
+        }
+        if (f.y8.codes) fetch8<VEC>(slot + a.field[3], units, unit, f.y8, t, a, col);
+        else if (f.y.p) fetch<bf16, VEC>(slot + a.field[3], units, unit, f.y.at(t), col, a.d);
+        if (f.gate_rows.p) fetch<bf16, VEC>(slot + a.field[4], units, unit, f.gate_rows.at(t), col, a.d);
+      }
+    }
+    moe::cp_async_commit();
+  };
+  const int ahead = a.stages - 1;  // row i - 1 leaves its stage to row i + ahead
+  for (int i = 0; i < ahead; ++i) start(i, smem + i * a.stage);
+
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {  // 0: the pre norm's gain; 1, 2: the post norm's with the gate's columns, and its shift
+    const int col = col_of(c), n = there(c);
+    kept.write(0, unit_of(c), load_params(f.pre_gain, f.params_f32, col, n, 1.f, a.one));
+    Eight w = load_params(f.post_gain, f.params_f32, col, n, 1.f, a.one);
+    const Eight gate = load_params(f.gate_columns, f.params_f32, col, n, 1.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], gate.v[j]);
+    kept.write(1, unit_of(c), w);
+    if (POST_LAYER && f.post_shift) kept.write(2, unit_of(c), load_params(f.post_shift, f.params_f32, col, n, 0.f, 0.f));
+  }
+
+  // u of the pre norm, and of the post norm (y itself where there is none)
+  auto read_x = [&](const char* slot, long long t, int c, float4 st) {
+    Eight x = f.out8.codes ? read8<VEC>(slot + a.field[2], units, unit_of(c), f.out8, t, a, col_of(c), there(c))
+                           : read<R, VEC>(slot + a.field[2], units, unit_of(c), f.kept_out.at(t), there(c));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (PRE_LAYER) x.v[j] = add2(x.v[j], two(-st.z));
+      x.v[j] = mul2(x.v[j], two(st.w));
+    }
+    if (PRE_LAYER && there(c) < 8) x.cut(there(c));  // 0 - mean behind the row's end
+    return x;
+  };
+  auto read_y = [&](const char* slot, long long t, int c, float4 st) {
+    Eight y = f.y8.codes ? read8<VEC>(slot + a.field[3], units, unit_of(c), f.y8, t, a, col_of(c), there(c))
+                         : read<bf16, VEC>(slot + a.field[3], units, unit_of(c), f.y.at(t), there(c));
+    if (POST != kNone) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (POST_LAYER) y.v[j] = add2(y.v[j], two(-st.x));
+        y.v[j] = mul2(y.v[j], two(st.y));
+      }
+      if (POST_LAYER && there(c) < 8) y.cut(there(c));
+    }
+    return y;
+  };
+  auto read_grad = [&](const char* slot, long long t, int c) {
+    if (f.grad_out.p) return read<R, VEC>(slot + a.field[0], units, unit_of(c), f.grad_out.at(t), there(c));
+    Eight z;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z.v[j] = make_float2(0.f, 0.f);
+    return z;
+  };
+
+  float2 acc_tu[CH][4], acc_t[PRE_LAYER ? CH : 1][4], acc_v[CH][4], acc_g[POST_LAYER ? CH : 1][4];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      acc_tu[c][j] = acc_v[c][j] = make_float2(0.f, 0.f);
+      if (PRE_LAYER) acc_t[PRE_LAYER ? c : 0][j] = make_float2(0.f, 0.f);
+      if (POST_LAYER) acc_g[POST_LAYER ? c : 0][j] = make_float2(0.f, 0.f);
+    }
+  float4 st = make_float4(0.f, 1.f, 0.f, 1.f), st_next = st, st_ahead = st;
+  float gate_t = 1.f, gate_next = 1.f, gate_ahead = 1.f;
+  auto look_ahead = [&](int i) {  // a row's numbers, an iteration before its sums
+    if (i >= rows) return;
+    if (f.stats) st_ahead = __ldg(f.stats + row_at(i));
+    if (f.gate_tokens) gate_ahead = __ldg(f.gate_tokens + row_at(i));
+  };
+  look_ahead(0);
+  float total[4 * quads] = {};
+  const bool sums_post = POST != kNone || f.grad_gate_tokens;
+  const float inv_d = 1.f / (float)a.d;
+#pragma unroll 1
+  for (int i = 0; i < rows + 1; ++i) {
+    st = st_next, gate_t = gate_next;
+    st_next = st_ahead, gate_next = gate_ahead;
+    look_ahead(i + 1);
+    float2 sum[4 * quads];
+#pragma unroll
+    for (int q = 0; q < 4 * quads; ++q) sum[q] = make_float2(0.f, 0.f);
+    auto more = [&](int q, float2 p, float2 v) {
+      if (q < 4 * quads) sum[q < 4 * quads ? q : 0] = fma2(p, v, sum[q < 4 * quads ? q : 0]);
+    };
+    if (i < rows) {  // row i's sums
+      wait_copies(ahead - 1);
+      const char* slot = ring.slot(0);
+      const long long t = row_at(i);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        Eight go = read_grad(slot, t, c), x;
+        if (has_norm) {
+          x = read_x(slot, t, c, st_next);
+          const Eight gn = read<bf16, VEC>(slot + a.field[1], units, unit_of(c), f.grad_norm.at(t), there(c));
+          const Eight k = kept.read(0, unit_of(c));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 tj = mul2(gn.v[j], k.v[j]);
+            more(kTU, tj, x.v[j]);
+            if (PRE_LAYER) more(kT, tj, two(1.f));
+            go.v[j] = fma2(tj, two(st_next.w), go.v[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x.v[j] = make_float2(0.f, 0.f);
+        }
+        if (sums_post) {
+          Eight w = kept.read(1, unit_of(c));
+          const Eight y = read_y(slot, t, c, st_next);
+          if (f.gate_rows.p) {
+            const Eight g = read<bf16, VEC>(slot + a.field[4], units, unit_of(c), f.gate_rows.at(t), there(c));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], g.v[j]);
+          }
+          if (PRE_LAYER && there(c) < 8) w.cut(there(c));  // a gain of 1 behind the row's end
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = mul2(y.v[j], w.v[j]);
+            more(kUV, go.v[j], v);
+            more(kXV, x.v[j], v);
+            if (PRE_LAYER) more(kV, v, two(1.f));
+            if (POST_LAYER) {
+              more(kUW, go.v[j], w.v[j]);
+              more(kXW, x.v[j], w.v[j]);
+              if (PRE_LAYER) more(kW, w.v[j], two(1.f));
+            }
+          }
+          if (token_shift) {
+            const Eight b = kept.read(2, unit_of(c));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              more(kUB, go.v[j], b.v[j]);
+              more(kXB, x.v[j], b.v[j]);
+              if (PRE_LAYER) more(kB, b.v[j], two(1.f));
+            }
+          }
+        }
+      }
+    }
+    if (i >= 1) {  // row i - 1's gradients
+      const long long t = row_at(i - 1);
+      const char* slot = ring.slot(1);
+      const float c1 = total[kTU] * inv_d, c2 = PRE_LAYER ? total[kT] * inv_d : 0.f;
+      auto of = [&](int uv, int xv, int ones) {
+        auto at = [&](int q) { return total[q < 4 * quads ? q : 0]; };
+        return at(uv) - (has_norm ? st.w * (c1 * at(xv) + (PRE_LAYER ? c2 * at(ones) : 0.f)) : 0.f);
+      };
+      // sum of G v = sum of G' v - rstd (c2 sum of v + c1 sum of x v), and so on
+      const float e1 = sums_post ? a.scale * of(kUV, kXV, kV) : 0.f;
+      const float m1 = e1 * gate_t * inv_d, m2 = POST_LAYER ? a.scale * gate_t * of(kUW, kXW, kW) * inv_d : 0.f;
+      if (f.grad_gate_tokens && warp == 0 && lane == 0)
+        f.grad_gate_tokens[t] = e1 + (token_shift ? a.scale * of(kUB, kXB, kB) : 0.f);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        Eight g = read_grad(slot, t, c);
+        if (has_norm) {
+          const Eight x = read_x(slot, t, c, st);
+          const Eight gn = read<bf16, VEC>(slot + a.field[1], units, unit_of(c), f.grad_norm.at(t), there(c));
+          const Eight k = kept.read(0, unit_of(c));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc_tu[c][j] = fma2(gn.v[j], x.v[j], acc_tu[c][j]);
+            if (PRE_LAYER) acc_t[PRE_LAYER ? c : 0][j] = add2(gn.v[j], acc_t[PRE_LAYER ? c : 0][j]);
+            float2 v = fma2(x.v[j], two(-c1), mul2(gn.v[j], k.v[j]));
+            if (PRE_LAYER) v = add2(v, two(-c2));
+            g.v[j] = fma2(v, two(st.w), g.v[j]);
+          }
+        }
+        if (f.grad_residual.p) store_row<VEC>(f.grad_residual.at(t), g, col_of(c), a.d, warp_row);
+        if (!has_y && !f.grad_y.p) continue;
+        Eight y, w = kept.read(1, unit_of(c));
+        if (has_y) y = read_y(slot, t, c, st);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], two(a.scale * gate_t));  // from here on s g G, but for the gates below
+        if (f.gate_rows.p) {
+          if (f.grad_gate_rows.p) {  // s G p
+            Eight p;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p.v[j] = mul2(y.v[j], w.v[j]);
+            if (POST_LAYER && f.post_shift) {
+              const Eight b = kept.read(2, unit_of(c));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) p.v[j] = add2(p.v[j], b.v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p.v[j] = mul2(p.v[j], g.v[j]);
+            store_row<VEC>(f.grad_gate_rows.at(t), p, col_of(c), a.d, warp_row);
+          }
+          const Eight gate = read<bf16, VEC>(slot + a.field[4], units, unit_of(c), f.gate_rows.at(t), there(c));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], gate.v[j]);
+        }
+        // a gate of columns is put on the sums over rows, and its gradient taken from
+        // them, at the end: here without it
+        if (has_y) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc_v[c][j] = fma2(g.v[j], y.v[j], acc_v[c][j]);
+            if (POST_LAYER) acc_g[POST_LAYER ? c : 0][j] = add2(g.v[j], acc_g[POST_LAYER ? c : 0][j]);
+          }
+        }
+        if (f.grad_y.p) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            g.v[j] = mul2(g.v[j], w.v[j]);
+            if (POST != kNone) {
+              g.v[j] = fma2(y.v[j], two(-m1), g.v[j]);
+              if (POST_LAYER) g.v[j] = add2(g.v[j], two(-m2));
+              g.v[j] = mul2(g.v[j], two(st.y));
+            }
+          }
+          store_row<VEC>(f.grad_y.at(t), g, col_of(c), a.d, warp_row);
+        }
+      }
+    }
+    start(i + ahead, ring.slot(1));
+    ring.next();
+    float4* at = reinterpret_cast<float4*>(smem + a.parts) + (i & 1) * quads * team.warps;
+#pragma unroll
+    for (int q = 0; q < quads; ++q) {
+      auto reduced = [&](int n) { return quads == 1 && n == kT ? 0.f : n < kSums ? warp_sum(sum[n].x + sum[n].y) : 0.f; };
+      const float4 v = make_float4(reduced(4 * q), reduced(4 * q + 1), reduced(4 * q + 2), reduced(4 * q + 3));
+      if (lane == 0) team.write(&at[q * team.warps + warp], v);
+    }
+    team.exchange();
+#pragma unroll
+    for (int q = 0; q < quads; ++q) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = lane; w < team.warps; w += 32) {
+        const float4 p = at[q * team.warps + w];
+        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+      }
+      total[4 * q] = warp_sum(v.x), total[4 * q + 1] = warp_sum(v.y), total[4 * q + 2] = warp_sum(v.z);
+      if (quads > 1 && 4 * q + 3 < kSums) total[4 * q + 3] = warp_sum(v.w);
+    }
+  }
+
+  if (!f.sums) return;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    float* to = f.sums + (long long)first * 4 * a.d + col_of(c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= there(c)) break;
+      auto get = [&](const float2(&v)[4]) { return j & 1 ? v[j >> 1].y : v[j >> 1].x; };
+      to[j] = get(acc_tu[c]);
+      if (PRE_LAYER) to[a.d + j] = get(acc_t[PRE_LAYER ? c : 0]);
+      to[2 * a.d + j] = get(acc_v[c]);
+      if (POST_LAYER) to[3 * a.d + j] = get(acc_g[POST_LAYER ? c : 0]);
+    }
+  }
+}
+
+struct Columns {
+  int d, teams, post_layer, pre_layer, params_f32;
+  const float* sums;
+  const void *post_gain, *post_shift, *gate_columns;
+  float one;
+  float *pre_gain_grad, *pre_shift_grad, *post_gain_grad, *post_shift_grad, *gate_grad;  // null: not wanted
+};
+
+// The teams' sums of 32 columns, added in order by 32 warps' shares.
+__global__ void __launch_bounds__(1024) norm_columns(const Columns c) {
+  __shared__ float part[4][32][33];
+  wait_for_previous_kernel();
+  let_next_kernel_start();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  float v[4] = {};
+  if (col < c.d) {
+    const bool wanted[4] = {c.pre_gain_grad != nullptr, c.pre_layer && c.pre_shift_grad,
+                            c.post_gain_grad || c.gate_grad, c.post_layer && (c.post_shift_grad || c.gate_grad)};
+    for (int t = warp; t < c.teams; t += 32) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (wanted[q]) v[q] += __ldcg(c.sums + ((long long)t * 4 + q) * c.d + col);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) part[q][warp][lane] = v[q];
+  __syncthreads();
+  if (warp >= 4) return;
+  float s = 0.f;
+  for (int w = 0; w < 32; ++w) s += part[warp][w][lane];
+  __syncwarp();
+  part[warp][0][lane] = s;
+  __threadfence_block();
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  if (warp != 0 || col >= c.d) return;
+  const float pre_gain = part[0][0][lane], pre_shift = part[1][0][lane];
+  const float with_u = part[2][0][lane], alone = part[3][0][lane];
+  auto param = [&](const void* p, float none) {
+    return !p ? none : c.params_f32 ? static_cast<const float*>(p)[col] : __bfloat162float(static_cast<const bf16*>(p)[col]);
+  };
+  if (c.pre_gain_grad) c.pre_gain_grad[col] = pre_gain;
+  if (c.pre_shift_grad) c.pre_shift_grad[col] = pre_shift;
+  const float gate = param(c.gate_columns, 1.f);
+  if (c.post_gain_grad) c.post_gain_grad[col] = gate * with_u;
+  if (c.post_shift_grad) c.post_shift_grad[col] = gate * alone;
+  if (c.gate_grad) {
+    const float gain = c.post_gain ? param(c.post_gain, 1.f) + c.one : 1.f;
+    c.gate_grad[col] = gain * with_u + (c.post_shift ? param(c.post_shift, 0.f) * alone : 0.f);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void* grad_out, long long grad_out_stride,
+                      const void* grad_norm, long long grad_norm_stride, const moe_norm_params* params,
+                      const moe_norm_kept* kept, void* grad_residual, long long grad_residual_stride, void* grad_y,
+                      long long grad_y_stride, const moe_norm_grads* grads, void* stream) {
+  if (!h) return moe::set_error(MOE_E_INVAL, "null handle");
+  if (T < 0) return moe::set_error(MOE_E_INVAL, "T must not be negative");
+  if (residual_type != MOE_TYPE_F32 && residual_type != MOE_TYPE_BF16)
+    return moe::set_error(MOE_E_INVAL, "the residual is MOE_TYPE_F32 or MOE_TYPE_BF16");
+  if (!kept || !grads) return moe::set_error(MOE_E_INVAL, "null kept or grads");
+  const char* bad = check_params(h, params);
+  if (!bad) bad = check_rows8(kept->out8);
+  if (!bad) bad = check_rows8(kept->y8);
+  if (bad) return moe::set_error(MOE_E_INVAL, bad);
+  const moe_norm_grads& g = *grads;
+  // a gradient is of something that is there
+  if ((g.pre_gain && !params->pre_gain) || (g.pre_shift && !params->pre_shift) || (g.post_gain && !params->post_gain) ||
+      (g.post_shift && !params->post_shift) || (g.gate && !params->gate))
+    return moe::set_error(MOE_E_INVAL, "a gradient of something that was not given");
+  float* const columns[] = {g.pre_gain, g.pre_shift, g.post_gain, g.post_shift,
+                            h->gate == MOE_GATE_CHANNEL ? static_cast<float*>(g.gate) : nullptr};
+  bool any = false;
+  for (const float* c : columns) {
+    if (!aligned(c, 4)) return moe::set_error(MOE_E_INVAL, "gradients must be aligned to their type");
+    any = any || c;
+  }
+  if (any && !h->sums) return moe::set_error(MOE_E_STATE, "moe_norm_reserve was not called");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    for (float* c : columns)
+      if (c)
+        if (cudaError_t e = cudaMemsetAsync(c, 0, sizeof(float) * h->d, s)) return moe::set_cuda_error(e, "cudaMemsetAsync");
+    return MOE_OK;
+  }
+  const bool has_norm = grad_norm != nullptr;
+  const bool has_y = kept->y || kept->y8;
+  if (!grad_out && !grad_norm) bad = "no gradient to start from";
+  else if (has_norm && h->pre == kNone) bad = "the gradient of a norm that the handle does not have";
+  else if (!has_norm && (g.pre_gain || g.pre_shift)) bad = "gradients of the pre norm need that of its output";
+  else if (kept->out && kept->out8) bad = "out is kept in one form";
+  else if (kept->y && kept->y8) bad = "y is kept in one form";
+  else if (has_norm && !kept->out && !kept->out8) bad = "the gradient of the norm needs what was kept of out";
+  else if (!has_y && ((h->post != kNone && grad_y) || g.post_gain || g.post_shift || g.gate)) bad = "these gradients need what was kept of y";
+  else if ((has_norm || h->post != kNone) && !kept->stats) bad = "the gradients of norms need stats";
+  else if (!grad_residual && !grad_y && !any && !g.gate) bad = "no gradient is wanted";
+  else if (!aligned(kept->stats, 16)) bad = "stats must be 16-byte aligned";
+  else if (h->gate == MOE_GATE_TOKEN && !aligned(g.gate, 4)) bad = "gradients must be aligned to their type";
+  if (!bad) bad = check_rows(h, grad_out, residual_type, grad_out_stride);
+  if (!bad) bad = check_rows(h, grad_norm, MOE_TYPE_BF16, grad_norm_stride);
+  if (!bad) bad = check_rows(h, kept->out, residual_type, kept->out_stride);
+  if (!bad) bad = check_rows(h, kept->y, MOE_TYPE_BF16, kept->y_stride);
+  if (!bad) bad = check_rows(h, grad_residual, residual_type, grad_residual_stride);
+  if (!bad) bad = check_rows(h, grad_y, MOE_TYPE_BF16, grad_y_stride);
+  if (!bad && h->gate == MOE_GATE_ELEMENT) bad = check_rows(h, g.gate, MOE_TYPE_BF16, g.gate_stride);
+  if (!bad && grad_out && grad_out == grad_residual && grad_out_stride != grad_residual_stride)
+    bad = "grad_residual in grad_out's place needs its row stride";
+  if (bad) return moe::set_error(MOE_E_INVAL, bad);
+  int teams = 0;
+  auto go = [&](auto r) {
+    using R = decltype(r);
+    Backward<R> f = {};
+    f.a = shape_of(h, T);
+    f.grad_out = rows_of<const R>(grad_out, grad_out_stride);
+    f.grad_norm = rows_of<const bf16>(grad_norm, grad_norm_stride);
+    if (has_norm) {
+      f.kept_out = rows_of<const R>(kept->out, kept->out_stride);
+      f.out8 = rows8_of(kept->out8);
+    }
+    f.y = rows_of<const bf16>(kept->y, kept->y_stride);
+    f.y8 = rows8_of(kept->y8);
+    f.stats = reinterpret_cast<const float4*>(kept->stats);
+    f.pre_gain = params->pre_gain, f.post_gain = params->post_gain, f.post_shift = params->post_shift;
+    f.params_f32 = params->type == MOE_TYPE_F32;
+    if (h->gate == MOE_GATE_CHANNEL) f.gate_columns = params->gate;
+    if (h->gate == MOE_GATE_TOKEN) {
+      f.gate_tokens = static_cast<const float*>(params->gate);
+      f.grad_gate_tokens = static_cast<float*>(g.gate);
+    }
+    if (h->gate == MOE_GATE_ELEMENT) {
+      f.gate_rows = rows_of<const bf16>(params->gate, params->gate_stride);
+      f.grad_gate_rows = rows_of<bf16>(g.gate, g.gate_stride);
+    }
+    f.grad_residual = rows_of<R>(grad_residual, grad_residual_stride);
+    f.grad_y = rows_of<bf16>(grad_y, grad_y_stride);
+    f.sums = any ? h->sums : nullptr;
+    const bool vec = h->d % 8 == 0 && rows_aligned(f.grad_out) && rows_aligned(f.grad_norm) && rows_aligned(f.kept_out) &&
+                     rows_aligned(f.y) && rows_aligned(f.gate_rows) && rows_aligned(f.grad_residual) &&
+                     rows_aligned(f.grad_y) && rows_aligned(f.grad_gate_rows) && aligned(f.out8.codes, 8) &&
+                     aligned(f.y8.codes, 8);
+    const int piece = vec ? 16 : 32, size = (int)sizeof(R) * 8 + (vec ? 0 : 16), codes = vec ? 16 : 32;
+    const int bytes[5] = {grad_out ? size : 0, has_norm ? piece : 0, !has_norm ? 0 : f.out8.codes ? codes : size,
+                          f.y8.codes ? codes : f.y.p ? piece : 0, f.gate_rows.p ? piece : 0};
+    const bool layers = h->pre == kLayer || h->post == kLayer;
+    const Plan p = lay_out(&f.a, chunks_of(h->d, T, layers ? 1 : 2), kThreads, bytes, f.post_shift ? 3 : 2,
+                           quads_of(h->pre == kLayer, h->post), 2, vec);
+    teams = std::min({T, kSms * p.per_sm / p.blocks, most_teams(h)});
+    return by_kind(h, vec, p.chunks, [&](auto v, auto layer, auto post, auto c) {
+      constexpr bool VEC = decltype(v)::value, LAYER = decltype(layer)::value;
+      constexpr int POST = decltype(post)::value, CH = decltype(c)::value;
+      auto* kernel = norm_backward<R, VEC, LAYER, POST, CH>;
+      cudaError_t e = allow_smem<BackwardKernel<R, VEC, LAYER, POST, CH>>(kernel);
+      return e == cudaSuccess ? launch(kernel, (unsigned)(teams * p.blocks), p.blocks, p.threads, p.smem, s, f) : e;
+    });
+  };
+  cudaError_t e = residual_type == MOE_TYPE_F32 ? go(0.f) : go(bf16());
+  if (e == cudaSuccess && any) {
+    Columns c = {};
+    c.d = h->d, c.teams = teams;
+    c.post_layer = h->post == kLayer, c.pre_layer = h->pre == kLayer;
+    c.params_f32 = params->type == MOE_TYPE_F32;
+    c.sums = h->sums;
+    c.post_gain = params->post_gain, c.post_shift = params->post_shift;
+    if (h->gate == MOE_GATE_CHANNEL) c.gate_columns = params->gate;
+    c.one = h->one;
+    c.pre_gain_grad = columns[0], c.pre_shift_grad = columns[1], c.post_gain_grad = columns[2];
+    c.post_shift_grad = columns[3], c.gate_grad = columns[4];
+    e = launch(norm_columns, (unsigned)((h->d + 31) / 32), 1, 1024, 0, s, c);
+  }
+  return e == cudaSuccess ? MOE_OK : moe::set_cuda_error(e, "norm_backward");
+}
+
+}  // extern "C"

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256)
     for (int j = 0; j < 8; ++j) most = max(most, moe::abs_bits(x[n][j]));
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) most = max(most, __shfl_xor_sync(mask, most, o));
-    const __nv_bfloat16 s = moe::rows8_scale(most);
+    const __nv_bfloat16 s = moe::rows8_scale<T>(most);
     uint32_t word[2];
     moe::rows8_codes<T>(x[n], s, word);
     __stcs(codes + i, make_uint2(word[0], word[1]));
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(256)
     uint32_t most = 0;
 #pragma unroll
     for (int i = i0; i < i0 + kSteps; ++i) most = max(most, moe::abs_bits(x[i]));
-    const __nv_bfloat16 s = moe::rows8_scale(__reduce_max_sync(kAll, most));
+    const __nv_bfloat16 s = moe::rows8_scale<T>(__reduce_max_sync(kAll, most));
     float in[4] = {};
     uint32_t word[1];
 #pragma unroll
