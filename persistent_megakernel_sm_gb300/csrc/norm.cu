@@ -19,169 +19,127 @@ struct Forward {
   Rows8 out8, y8;
 };
 
-// Of the rows team, team + teams, ...: iteration i takes the post norm's sums of row i,
-// writes row i - 2's norm, and row i - 1's sum (into the residual's slot too) with the
-// sums of its norm.
-template <typename R, bool VEC, bool PRE_LAYER, int POST, int CH>
+// Rows team, team + teams, ... of the tensors.
+// SAVE: 8-bit rows may be wanted; a kernel that cannot write them runs with fewer registers.
+template <typename R, bool VEC, bool PRE_LAYER, int POST, int CH, bool SAVE>
 __global__ void __launch_bounds__(kThreads, VEC ? 2 : 1) norm_forward(const __grid_constant__ Forward<R> f) {
   extern __shared__ __align__(16) char smem[];
   const Shape& a = f.a;
-  const Team team;
-  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x, units = CH * threads;
-  const int warp = team.rank * (threads / 32) + (tid >> 5);
-  const int first = blockIdx.x / team.blocks, step = gridDim.x / team.blocks;
-  const int rows = first < a.T ? (a.T - first - 1) / step + 1 : 0;
+  Team team(smem + a.parts);
+  const int tid = threadIdx.x, threads = blockDim.x, units = CH * threads;
+  const int step = gridDim.x / team.blocks;
   float* warp_row = reinterpret_cast<float*>(smem + a.out) + (tid >> 5) * 256;
   const Kept kept{reinterpret_cast<float4*>(smem + a.vec), units};
-  Ring ring{smem, a.stage, a.stages};
   const float inv_d = 1.f / (float)a.d;
-  const bool has_norm = f.norm.p != nullptr;
-  auto row_at = [&](int i) { return (long long)first + (long long)i * step; };
-  auto unit_of = [&](int c) { return c * threads + tid; };
-  auto col_of = [&](int c) { return (team.rank * units + c * threads + tid) * 8; };
-  auto there = [&](int c) { return max(0, min(8, a.d - col_of(c))); };
-  // columns of warp w of the team: those of its lanes in each of its eights
-  auto count = [&](int w) {
-    int n = 0;
-    const int at = w / (threads / 32) * units + w % (threads / 32) * 32;
+  int col[CH], n[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) n += max(0, min(256, a.d - (at + c * threads) * 8));
-    return n;
-  };
+  for (int c = 0; c < CH; ++c) col[c] = (team.rank * units + c * threads + tid) * 8, n[c] = max(0, min(8, a.d - col[c]));
 
   wait_for_previous_kernel();
   let_next_kernel_start();
   begin(a, team, smem, team.blocks * units * 8);
-  auto start = [&](int i, char* slot) {
-    if (i < rows) {
-      const long long t = row_at(i);
+  auto start = [&](long long t, char* slot) {
+    if (t < a.T) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        fetch<R, VEC>(slot + a.field[0], units, unit_of(c), f.residual.at(t), col_of(c), a.d);
-        if (f.y.p) fetch<bf16, VEC>(slot + a.field[1], units, unit_of(c), f.y.at(t), col_of(c), a.d);
-        if (f.gate_rows.p) fetch<bf16, VEC>(slot + a.field[2], units, unit_of(c), f.gate_rows.at(t), col_of(c), a.d);
+        const int unit = c * threads + tid;
+        fetch<R, VEC>(slot + a.field[0], units, unit, f.residual.at(t), col[c], a.d);
+        if (f.y.p) fetch<bf16, VEC>(slot + a.field[1], units, unit, f.y.at(t), col[c], a.d);
+        if (f.gate_rows.p) fetch<bf16, VEC>(slot + a.field[2], units, unit, f.gate_rows.at(t), col[c], a.d);
       }
     }
     moe::cp_async_commit();
   };
-  const int ahead = a.stages - 2;  // rows fetched before they enter: row i - 2 leaves its stage to row i + ahead
-  for (int i = 0; i < ahead; ++i) start(i, smem + i * a.stage);
+  long long t = blockIdx.x / team.blocks;
+  for (int i = 0; i < a.stages; ++i) start(t + (long long)i * step, smem + i * a.stage);
 
+  // 0: s g gain of the post norm, 1: the pre norm's gain, 2 and 3: their shifts
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {  // 0, 2: s g gain and s g shift of the post norm; 1, 3: gain and shift of the pre norm
-    const int col = col_of(c), n = there(c);
-    const Eight gate = load_params(f.gate_columns, f.params_f32, col, n, 1.f, 0.f);
+  for (int c = 0; c < CH; ++c) {
+    const int unit = c * threads + tid;
+    const Eight gate = load_params(f.gate_columns, f.params_f32, col[c], n[c], 1.f, 0.f);
     auto with_gate = [&](Eight e) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e.v[i] = mul2(e.v[i], mul2(gate.v[i], two(a.scale)));
+      for (int j = 0; j < 4; ++j) e.v[j] = mul2(e.v[j], mul2(gate.v[j], two(a.scale)));
       return e;
     };
-    kept.write(0, unit_of(c), with_gate(load_params(f.post_gain, f.params_f32, col, n, 1.f, a.one)));
-    kept.write(1, unit_of(c), load_params(f.pre_gain, f.params_f32, col, n, 1.f, a.one));
-    if (POST == kLayer && f.post_shift) kept.write(2, unit_of(c), with_gate(load_params(f.post_shift, f.params_f32, col, n, 0.f, 0.f)));
-    if (PRE_LAYER && f.pre_shift) kept.write(3, unit_of(c), load_params(f.pre_shift, f.params_f32, col, n, 0.f, 0.f));
+    kept.write(0, unit, with_gate(load_params(f.post_gain, f.params_f32, col[c], n[c], 1.f, a.one)));
+    kept.write(1, unit, load_params(f.pre_gain, f.params_f32, col[c], n[c], 1.f, a.one));
+    if (POST == kLayer && f.post_shift) kept.write(2, unit, with_gate(load_params(f.post_shift, f.params_f32, col[c], n[c], 0.f, 0.f)));
+    if (PRE_LAYER && f.pre_shift) kept.write(3, unit, load_params(f.pre_shift, f.params_f32, col[c], n[c], 0.f, 0.f));
   }
+  auto param = [&](int which, int c) { return kept.read(which, c * threads + tid); };
 
-  float2 post = make_float2(0.f, 1.f), pre = make_float2(0.f, 1.f), post_before = post;
-  float gate_t = 1.f, gate_next = 1.f;
+  char* slot = smem;
 #pragma unroll 1
-  for (int i = 0; i < rows + 2; ++i) {
-    Part<POST == kLayer> post_part;
-    Part<PRE_LAYER> pre_part;
-    if (i < rows) {
-      wait_copies(ahead - 1);
-      const char* slot = ring.slot(0);
-      if (f.gate_tokens) gate_next = __ldg(f.gate_tokens + row_at(i));
-      if (f.y.p && (POST != kNone || f.y8.codes)) {
+  for (; t < a.T; t += step) {
+    const float gate_t = f.gate_tokens ? __ldg(f.gate_tokens + t) : 1.f;
+    wait_copies(a.stages);
+    Eight sum[CH];
+    float2 post = make_float2(0.f, 1.f), pre = post;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const Eight y = read<bf16, VEC>(slot + a.field[1], units, unit_of(c), f.y.at(row_at(i)), there(c));
-          if (POST != kNone) post_part.add(y, there(c));
-          if (f.y8.codes) store_rows8<bf16, VEC>(f.y8, row_at(i), a, y, col_of(c), warp_row);
-        }
-      }
-    }
-    if (i >= 2) {
-      const long long t = row_at(i - 2);
-      const char* slot = ring.slot(2);
-      if (has_norm) {
+    for (int c = 0; c < CH; ++c) sum[c] = read<R, VEC>(slot + a.field[0], units, c * threads + tid, f.residual.at(t), n[c]);
+    if (f.y.p) {
+      Eight y[CH];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          // without y the slot holds the residual as it came
-          Eight v = f.y.p ? read<R, true>(slot + a.field[0], units, unit_of(c), nullptr, 8)
-                          : read<R, VEC>(slot + a.field[0], units, unit_of(c), f.residual.at(t), there(c));
-          const Eight gain = kept.read(1, unit_of(c));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (PRE_LAYER) v.v[j] = add2(v.v[j], two(-pre.x));
-            v.v[j] = mul2(mul2(v.v[j], two(pre.y)), gain.v[j]);
-          }
-          if (PRE_LAYER && f.pre_shift) {
-            const Eight shift = kept.read(3, unit_of(c));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v.v[j] = add2(v.v[j], shift.v[j]);
-          }
-          store_row<VEC>(f.norm.at(t), v, col_of(c), a.d, warp_row);
-        }
-      }
-      if (f.stats && warp == 0 && lane == 0) f.stats[t] = make_float4(post_before.x, post_before.y, pre.x, pre.y);
-    }
-    if (i >= 1 && i <= rows) {
-      const long long t = row_at(i - 1);
-      char* slot = ring.slot(1);
+      for (int c = 0; c < CH; ++c) y[c] = read<bf16, VEC>(slot + a.field[1], units, c * threads + tid, f.y.at(t), n[c]);
+      if (POST != kNone) post = moments<POST == kLayer, CH>(team, y, n, inv_d, a.eps);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        Eight sum = read<R, VEC>(slot + a.field[0], units, unit_of(c), f.residual.at(t), there(c));
-        if (f.y.p) {
-          Eight y = read<bf16, VEC>(slot + a.field[1], units, unit_of(c), f.y.at(t), there(c));
-          const Eight k = kept.read(0, unit_of(c));
+        if (SAVE && f.y8.codes) store_rows8<bf16, VEC>(f.y8, t, a, y[c], col[c], warp_row);
+        const Eight k = param(0, c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (POST == kLayer) y.v[j] = add2(y.v[j], two(-post.x));
-            y.v[j] = mul2(POST == kNone ? y.v[j] : mul2(y.v[j], two(post.y)), k.v[j]);
-          }
-          if (POST == kLayer && f.post_shift) {
-            const Eight b = kept.read(2, unit_of(c));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y.v[j] = add2(y.v[j], b.v[j]);
-          }
-          if (f.gate_rows.p) {
-            const Eight g = read<bf16, VEC>(slot + a.field[2], units, unit_of(c), f.gate_rows.at(t), there(c));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y.v[j] = mul2(y.v[j], g.v[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sum.v[j] = fma2(y.v[j], two(gate_t), sum.v[j]);
-          if (POST == kLayer && there(c) < 8) sum.cut(there(c));  // 0 - mean behind the row's end
-          uint4* held = reinterpret_cast<uint4*>(slot + a.field[0]) + unit_of(c);
-          if constexpr (sizeof(R) == 2) {
-            const uint4 q = pack(sum);
-            store_row<VEC>(f.out.at(t), q, col_of(c), a.d, warp_row);
-            held[0] = q;
-            uint32_t w[4];
-            put_words(q, w);
-            sum = unpack(w);
-          } else {
-            store_row<VEC>(f.out.at(t), sum, col_of(c), a.d, warp_row);
-            reinterpret_cast<float4*>(held)[0] = make_float4(sum.v[0].x, sum.v[0].y, sum.v[1].x, sum.v[1].y);
-            reinterpret_cast<float4*>(held)[units] = make_float4(sum.v[2].x, sum.v[2].y, sum.v[3].x, sum.v[3].y);
-          }
+        for (int j = 0; j < 4; ++j) {
+          if (POST == kLayer) y[c].v[j] = add2(y[c].v[j], two(-post.x));
+          if (POST != kNone) y[c].v[j] = mul2(y[c].v[j], two(post.y));
+          y[c].v[j] = mul2(y[c].v[j], k.v[j]);
         }
-        if (f.out8.codes) store_rows8<R, VEC>(f.out8, t, a, sum, col_of(c), warp_row);
-        pre_part.add(sum, there(c));
+        if (POST == kLayer && f.post_shift) {
+          const Eight b = param(2, c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[c].v[j] = add2(y[c].v[j], b.v[j]);
+        }
+        if (f.gate_rows.p) {
+          const Eight g = read<bf16, VEC>(slot + a.field[2], units, c * threads + tid, f.gate_rows.at(t), n[c]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[c].v[j] = mul2(y[c].v[j], g.v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[c].v[j] = fma2(y[c].v[j], two(gate_t), sum[c].v[j]);
+        if (POST == kLayer && n[c] < 8) sum[c].cut(n[c]);  // 0 - mean behind the row's end
+        if constexpr (sizeof(R) == 2) {
+          const uint4 q = pack(sum[c]);
+          store_row<VEC>(f.out.at(t), q, col[c], a.d, warp_row);
+          uint32_t w[4];
+          put_words(q, w);
+          sum[c] = unpack(w);
+        } else {
+          store_row<VEC>(f.out.at(t), sum[c], col[c], a.d, warp_row);
+        }
       }
     }
-    start(i + ahead, ring.slot(2));
-    ring.next();
-    const float2 post_sum = POST != kNone ? post_part.warp() : make_float2(0.f, 0.f);
-    const float2 pre_sum = pre_part.warp();
-    float4* at = reinterpret_cast<float4*>(smem + a.parts) + (i & 1) * team.warps;
-    if (lane == 0) team.write(&at[warp], make_float4(post_sum.x, post_sum.y, pre_sum.x, pre_sum.y));
-    team.exchange();
-    post_before = post;
-    gate_t = gate_next;
-    if (POST != kNone) post = whole<POST == kLayer>(reinterpret_cast<const float2*>(at), 2, team.warps, inv_d, a.eps, count);
-    if (has_norm) pre = whole<PRE_LAYER>(reinterpret_cast<const float2*>(at) + 1, 2, team.warps, inv_d, a.eps, count);
+    if (f.norm.p) pre = moments<PRE_LAYER, CH>(team, sum, n, inv_d, a.eps);
+    start(t + (long long)a.stages * step, slot);  // all of the row has been read
+    slot += a.stage;
+    if (slot == smem + a.vec) slot = smem;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (SAVE && f.out8.codes) store_rows8<R, VEC>(f.out8, t, a, sum[c], col[c], warp_row);
+      if (!f.norm.p) continue;
+      const Eight gain = param(1, c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (PRE_LAYER) sum[c].v[j] = add2(sum[c].v[j], two(-pre.x));
+        sum[c].v[j] = mul2(mul2(sum[c].v[j], two(pre.y)), gain.v[j]);
+      }
+      if (PRE_LAYER && f.pre_shift) {
+        const Eight shift = param(3, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[c].v[j] = add2(sum[c].v[j], shift.v[j]);
+      }
+      store_row<VEC>(f.norm.at(t), sum[c], col[c], a.d, warp_row);
+    }
+    if (f.stats && team.rank == 0 && tid == 0) f.stats[t] = make_float4(post.x, post.y, pre.x, pre.y);
   }
 }
 
@@ -294,15 +252,19 @@ int moe_norm_forward(const moe_norm_t* h, int T, int residual_type, const void* 
     const int bytes[5] = {size, y ? piece : 0, f.gate_rows.p ? piece : 0, 0, 0};
     const bool layers = h->pre == kLayer || h->post == kLayer;
     const Plan p = lay_out(&f.a, chunks_of(h->d, T, layers ? 1 : 2), vec ? 2 * kThreads : kThreads, bytes,
-                           f.pre_shift ? 4 : f.post_shift ? 3 : 2, 1, 3, vec);
+                           f.pre_shift ? 4 : f.post_shift ? 3 : 2, 1, vec);
     const int teams = std::min(T, kSms * p.per_sm / p.blocks);
     return by_kind(h, vec, p.chunks, [&](auto v, auto layer, auto post, auto c) {
       constexpr bool VEC = decltype(v)::value, LAYER = decltype(layer)::value;
       constexpr int POST = decltype(post)::value, CH = decltype(c)::value;
-      auto* kernel = norm_forward<R, VEC, LAYER, POST, CH>;
-      cudaError_t e = allow_smem<ForwardKernel<R, VEC, LAYER, POST, CH>>(kernel);
-      return e == cudaSuccess ? launch(kernel, (unsigned)(teams * p.blocks), p.blocks, p.threads, p.smem,
-                                       static_cast<cudaStream_t>(stream), f) : e;
+      auto with = [&](auto s) {
+        constexpr bool SAVE = decltype(s)::value;
+        auto* kernel = norm_forward<R, VEC, LAYER, POST, CH, SAVE>;
+        cudaError_t e = allow_smem<ForwardKernel<R, VEC, LAYER, POST, CH, SAVE>>(kernel);
+        return e == cudaSuccess ? launch(kernel, (unsigned)(teams * p.blocks), p.blocks, p.threads, p.smem,
+                                         static_cast<cudaStream_t>(stream), f) : e;
+      };
+      return out8 || y8 ? with(std::true_type{}) : with(std::false_type{});
     });
   };
   const cudaError_t e = residual_type == MOE_TYPE_F32 ? go(0.f) : go(bf16());

@@ -16,15 +16,15 @@
 // means are known: one exchange a row.
 //
 // What bounds both is HBM, so the rest is kept out of its way.  A block holds a row (a
-// cluster of 2 to 8 blocks one that is too wide), a lane up to 4 times 8 consecutive
-// columns of it, and goes over its rows as a pipeline: while one row is finished, the
-// next one's sums are taken and the rows behind are on their way, so a row costs one
-// exchange of the block's warps.  Rows come by asynchronous 16-byte copies into slots
-// of shared memory that belong to the thread that reads them: no barrier guards them.
-// Rows that are not aligned come as the 16-byte pieces that they lie in, shifted when
-// they are read (a piece between two lanes comes twice, the second time from L1), and
-// leave a warp's 256 columns at a time, each store along the row.  Gains and shifts stay
-// in shared memory; products and sums run in pairs.  Sums over rows are kept in
+// cluster of up to 16 blocks one that is too wide), a lane one or two times 8
+// consecutive columns of it, in registers; while it works on a row, the next ones are on
+// their way: by asynchronous 16-byte copies into slots of shared memory that belong to
+// the thread that reads them, so that no barrier guards them.  Rows that are not aligned
+// come as the 16-byte pieces that they lie in, shifted when they are read (a piece
+// between two lanes comes twice, the second time from L1), and leave a warp's 256
+// columns at a time, each store along the row.  The forward pass exchanges sums between
+// the block's warps twice a row, a layer norm once more for each norm (the mean first,
+// then the squares about it); the gradient once.  Sums over rows are kept in
 // registers, written once a block and added by a second kernel in a fixed order.
 #pragma once
 
@@ -62,28 +62,9 @@ __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepc
 
 // ------------------------------------------------------------------------ pairs
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 
 // 8 columns.
@@ -344,87 +325,7 @@ __device__ __forceinline__ void store_rows8(const Rows8& r, long long t, const S
   if (col < a.d && (lane & (a.group_lanes - 1)) == 0) r.scales[t * a.groups + col / (8 * a.group_lanes)] = s;
 }
 
-// ------------------------------------------------------------------------- sums
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
-
-// Mean and summed squares about it of n values, put together with another n's
-// (Chan, Golub and LeVeque): no large sums are taken from one another.
-struct Moments {
-  float n, mean, m2;
-};
-
-__device__ __forceinline__ Moments both(const Moments& a, const Moments& b) {
-  if (a.n == 0.f) return b;  // an empty side's square could overflow
-  if (b.n == 0.f) return a;
-  const float n = a.n + b.n;
-  const float part = __fdividef(b.n, n), off = b.mean - a.mean;
-  return Moments{n, fmaf(off, part, a.mean), a.m2 + fmaf(off * off, a.n * part, b.m2)};
-}
-
-__device__ __forceinline__ Moments warp_moments(Moments m) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1)
-    m = both(m, Moments{__shfl_xor_sync(kAll, m.n, o), __shfl_xor_sync(kAll, m.mean, o), __shfl_xor_sync(kAll, m.m2, o)});
-  // the two sides of an exchange round differently: one lane's for all
-  return Moments{m.n, __shfl_sync(kAll, m.mean, 0), __shfl_sync(kAll, m.m2, 0)};
-}
-
-// What a norm is made of, of a thread's columns: the moments, or the sum of squares.
-template <bool LAYER>
-struct Part {
-  Moments m{0.f, 0.f, 0.f};
-  __device__ __forceinline__ void add(const Eight& e, int n) {
-    float2 s = add2(add2(e.v[0], e.v[1]), add2(e.v[2], e.v[3]));  // zeros behind the row's end
-    const float mean = n == 8 ? (s.x + s.y) * 0.125f : n ? __fdividef(s.x + s.y, (float)n) : 0.f;
-    s = make_float2(0.f, 0.f);
-    Eight off = e;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) off.v[i] = add2(off.v[i], two(-mean));
-    if (n < 8) off.cut(n);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s = fma2(off.v[i], off.v[i], s);
-    m = both(m, Moments{(float)n, mean, s.x + s.y});
-  }
-  __device__ __forceinline__ float2 warp() const {
-    const Moments w = warp_moments(m);
-    return make_float2(w.mean, w.m2);
-  }
-};
-template <>
-struct Part<false> {
-  float2 squares = make_float2(0.f, 0.f);
-  __device__ __forceinline__ void add(const Eight& e, int) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) squares = fma2(e.v[i], e.v[i], squares);
-  }
-  __device__ __forceinline__ float2 warp() const { return make_float2(warp_sum(squares.x + squares.y), 0.f); }
-};
-
-// (mean, rstd) from every warp's part; count(w): the columns of warp w.
-template <bool LAYER, typename Count>
-__device__ __forceinline__ float2 whole(const float2* parts, int stride, int warps, float inv_d, float eps, Count&& count) {
-  const int lane = threadIdx.x & 31;
-  float mean = 0.f, m2;
-  if constexpr (LAYER) {
-    Moments m{0.f, 0.f, 0.f};
-    for (int w = lane; w < warps; w += 32) {
-      const float2 p = parts[w * stride];
-      m = both(m, Moments{(float)count(w), p.x, p.y});
-    }
-    m = warp_moments(m);
-    mean = m.mean, m2 = m.m2;
-  } else {
-    float s = 0.f;
-    for (int w = lane; w < warps; w += 32) s += parts[w * stride].x;
-    m2 = warp_sum(s);
-  }
-  return make_float2(mean, __frsqrt_rn(fmaf(m2, inv_d, eps)));
-}
+// ------------------------------------------------------------------- parameters
 
 __device__ __forceinline__ Eight load_params(const void* p, int f32, int col, int n, float none, float plus) {
   Eight e;
@@ -452,33 +353,132 @@ struct Kept {
   }
 };
 
-// The blocks of a cluster exchange their warps' parts; a single block's warps too.
-struct Team {
-  int blocks, rank, warps;  // warps: of the whole team
+// ------------------------------------------------------------------------- sums
 
-  __device__ __forceinline__ Team() {
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// Four sums over a warp at once: two exchanges hand the lanes one of the four each,
+// three more add it up; lanes 0, 8, 16 and 24 have v.x, v.y, v.z, v.w.
+__device__ __forceinline__ float warp_sum4(float4 v) {
+  const int lane = threadIdx.x & 31;
+  const bool up = lane & 16, right = lane & 8;
+  float a = (up ? v.z : v.x) + __shfl_xor_sync(kAll, up ? v.x : v.z, 16);
+  const float b = (up ? v.w : v.y) + __shfl_xor_sync(kAll, up ? v.y : v.w, 16);
+  a = (right ? b : a) + __shfl_xor_sync(kAll, right ? a : b, 8);
+#pragma unroll
+  for (int o = 4; o; o >>= 1) a += __shfl_xor_sync(kAll, a, o);
+  return a;
+}
+
+// The blocks of a cluster exchange their warps' sums; a single block's warps too.
+struct Team {
+  float4* parts;                 // of all warps, twice: for this exchange and the last one
+  int blocks, rank, warps, warp; // warps: of the whole team; warp: of all
+  int turn = 0;
+
+  __device__ __forceinline__ Team(char* at) : parts(reinterpret_cast<float4*>(at)) {
     uint32_t n, r;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     blocks = (int)n, rank = (int)r, warps = (int)(n * blockDim.x / 32);
+    warp = (int)(r * (blockDim.x / 32) + threadIdx.x / 32);
   }
-  // one lane writes to every block
-  __device__ __forceinline__ void write(float4* at, float4 v) const {
+  // What a warp's lane (of every eighth, or the first alone) has of its sums to every
+  // block, and the wait for all of them.
+  __device__ __forceinline__ void put(float* to, float v, bool mine) const {
     if (blocks == 1) {
-      *at = v;
-    } else {
-      for (int b = 0; b < blocks; ++b) {
-        const uint32_t to = moe::mapa_shared(moe::smem_u32(at), (uint32_t)b);
-        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                     : "memory");
-      }
+      if (mine) *to = v;
+    } else if (mine) {
+      for (int b = 0; b < blocks; ++b)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(moe::mapa_shared(moe::smem_u32(to), (uint32_t)b)), "f"(v) : "memory");
     }
   }
   __device__ __forceinline__ void exchange() const {
     if (blocks > 1) asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
     else __syncthreads();
   }
+  // N fours of sums over all threads of the team
+  template <int N>
+  __device__ __forceinline__ void sum(float4 (&v)[N]) {
+    const int lane = threadIdx.x & 31;
+    float mine[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) mine[q] = warp_sum4(v[q]);
+    if (warps > 1) {
+      float4* at = parts + turn * N * warps;
+      turn ^= 1;
+#pragma unroll
+      for (int q = 0; q < N; ++q) put(reinterpret_cast<float*>(at + q * warps + warp) + (lane >> 3), mine[q], (lane & 7) == 0);
+      exchange();
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        float4 t = lane < warps ? at[q * warps + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (blocks > 1)
+          for (int w = lane + 32; w < warps; w += 32) {
+            const float4 p = at[q * warps + w];
+            t.x += p.x, t.y += p.y, t.z += p.z, t.w += p.w;
+          }
+        mine[q] = warp_sum4(t);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      v[q] = make_float4(__shfl_sync(kAll, mine[q], 0), __shfl_sync(kAll, mine[q], 8), __shfl_sync(kAll, mine[q], 16),
+                         __shfl_sync(kAll, mine[q], 24));
+  }
+  // one sum
+  __device__ __forceinline__ float sum(float v) {
+    const int lane = threadIdx.x & 31;
+    v = warp_sum(v);
+    if (warps == 1) return v;
+    float* at = reinterpret_cast<float*>(parts) + turn * warps;
+    turn ^= 1;
+    put(at + warp, v, lane == 0);
+    exchange();
+    if (blocks == 1) {  // at most 16 warps
+      float s = (lane & 15) < warps ? at[lane & 15] : 0.f;
+#pragma unroll
+      for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+      return s;
+    }
+    float s = 0.f;
+    for (int w = lane; w < warps; w += 32) s += at[w];
+    return warp_sum(s);
+  }
 };
+static_assert(kThreads / 32 <= 16, "a block's warps");
+
+// A norm's mean and rstd of the team's row, CH eights of it in each thread, zeros behind
+// its end; n: how many of them are columns.
+template <bool LAYER, int CH>
+__device__ __forceinline__ float2 moments(Team& team, const Eight (&e)[CH], const int (&n)[CH], float inv_d, float eps) {
+  float mean = 0.f;
+  if (LAYER) {
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s = add2(s, e[c].v[j]);
+    mean = team.sum(s.x + s.y) * inv_d;
+  }
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    Eight off = e[c];
+    if (LAYER) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) off.v[j] = add2(off.v[j], two(-mean));
+      if (n[c] < 8) off.cut(n[c]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s = fma2(off.v[j], off.v[j], s);
+  }
+  return make_float2(mean, rsqrtf(fmaf(team.sum(s.x + s.y), inv_d, eps)));
+}
 
 // Before anything is under way: slots of columns behind the row's end, which no copy
 // reaches, are read as zeros; and a cluster's blocks all have to run before one writes
@@ -491,24 +491,11 @@ __device__ __forceinline__ void begin(const Shape& a, const Team& team, char* sm
   if (team.blocks > 1) moe::cluster_sync();
 }
 
-// Rows in a ring of stages: the stage of the row that enters, and of those behind it.
-struct Ring {
-  char* base;
-  int stage, stages, at = 0;
-  __device__ __forceinline__ char* slot(int back) const {  // of the row that entered `back` rows ago
-    const int i = at - back;
-    return base + (i < 0 ? i + stages : i) * stage;
-  }
-  __device__ __forceinline__ void next() {
-    if (++at == stages) at = 0;
-  }
-};
-
-// Until the row that enters has come, if LEFT more may still be on their way behind it.
-__device__ __forceinline__ void wait_copies(int left) {
-  if (left == 0) moe::cp_async_wait<0>();
-  else if (left == 1) moe::cp_async_wait<1>();
-  else moe::cp_async_wait<2>();
+// Until the oldest of a.stages rows under way has come.
+__device__ __forceinline__ void wait_copies(int stages) {
+  if (stages == 2) moe::cp_async_wait<1>();
+  else if (stages == 3) moe::cp_async_wait<2>();
+  else moe::cp_async_wait<3>();
 }
 
 // ------------------------------------------------------------------------- host
@@ -528,9 +515,10 @@ struct Plan {
 };
 
 // A block's threads and shared memory for `chunks` eights a lane: as many blocks to a
-// row as it takes for `least` stages to fit, as many blocks to an SM as it then has
+// row as it takes for two stages to fit, as many blocks to an SM as it then has
 // room for, up to sm_threads threads, and as many stages, up to kMaxStages.
-Plan lay_out(Shape* a, int chunks, int sm_threads, const int (&field_bytes)[5], int kept, int quads, int least, bool vec) {
+Plan lay_out(Shape* a, int chunks, int sm_threads, const int (&field_bytes)[5], int kept, int quads, bool vec) {
+  constexpr int least = 2;
   Plan p;
   p.chunks = chunks;
   const int lanes = (a->d + 7) / 8;
@@ -556,7 +544,7 @@ Plan lay_out(Shape* a, int chunks, int sm_threads, const int (&field_bytes)[5], 
   return p;
 }
 
-template <typename, bool, bool, int, int>
+template <typename, bool, bool, int, int, bool>
 struct ForwardKernel;
 template <typename, bool, bool, int, int>
 struct BackwardKernel;

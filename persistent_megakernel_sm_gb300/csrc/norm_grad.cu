@@ -34,90 +34,54 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
   constexpr int quads = quads_of(PRE_LAYER, POST);
   constexpr bool POST_LAYER = POST == kLayer;
   const Shape& a = f.a;
-  const Team team;
-  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x, units = CH * threads;
-  const int warp = team.rank * (threads / 32) + (tid >> 5);
+  Team team(smem + a.parts);
+  const int tid = threadIdx.x, threads = blockDim.x, units = CH * threads;
   const int first = blockIdx.x / team.blocks, step = gridDim.x / team.blocks;
-  const int rows = first < a.T ? (a.T - first - 1) / step + 1 : 0;
   float* warp_row = reinterpret_cast<float*>(smem + a.out) + (tid >> 5) * 256;
   const Kept kept{reinterpret_cast<float4*>(smem + a.vec), units};
-  Ring ring{smem, a.stage, a.stages};
-  auto row_at = [&](int i) { return (long long)first + (long long)i * step; };
-  auto unit_of = [&](int c) { return c * threads + tid; };
-  auto col_of = [&](int c) { return (team.rank * units + c * threads + tid) * 8; };
-  auto there = [&](int c) { return max(0, min(8, a.d - col_of(c))); };
+  const float inv_d = 1.f / (float)a.d;
+  int col[CH], n[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) col[c] = (team.rank * units + c * threads + tid) * 8, n[c] = max(0, min(8, a.d - col[c]));
   const bool has_y = f.y.p || f.y8.codes, has_norm = f.grad_norm.p != nullptr;
   const bool token_shift = POST_LAYER && f.grad_gate_tokens && f.post_shift;
 
   wait_for_previous_kernel();
   let_next_kernel_start();
   begin(a, team, smem, team.blocks * units * 8);
-  auto start = [&](int i, char* slot) {
-    if (i < rows) {
-      const long long t = row_at(i);
+  auto start = [&](long long t, char* slot) {
+    if (t < a.T) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int unit = unit_of(c), col = col_of(c);
-        if (f.grad_out.p) fetch<R, VEC>(slot + a.field[0], units, unit, f.grad_out.at(t), col, a.d);
+        const int unit = c * threads + tid;
+        if (f.grad_out.p) fetch<R, VEC>(slot + a.field[0], units, unit, f.grad_out.at(t), col[c], a.d);
         if (has_norm) {
-          fetch<bf16, VEC>(slot + a.field[1], units, unit, f.grad_norm.at(t), col, a.d);
-          if (f.out8.codes) fetch8<VEC>(slot + a.field[2], units, unit, f.out8, t, a, col);
-          else fetch<R, VEC>(slot + a.field[2], units, unit, f.kept_out.at(t), col, a.d);
+          fetch<bf16, VEC>(slot + a.field[1], units, unit, f.grad_norm.at(t), col[c], a.d);
+          if (f.out8.codes) fetch8<VEC>(slot + a.field[2], units, unit, f.out8, t, a, col[c]);
+          else fetch<R, VEC>(slot + a.field[2], units, unit, f.kept_out.at(t), col[c], a.d);
         }
-        if (f.y8.codes) fetch8<VEC>(slot + a.field[3], units, unit, f.y8, t, a, col);
-        else if (f.y.p) fetch<bf16, VEC>(slot + a.field[3], units, unit, f.y.at(t), col, a.d);
-        if (f.gate_rows.p) fetch<bf16, VEC>(slot + a.field[4], units, unit, f.gate_rows.at(t), col, a.d);
+        if (f.y8.codes) fetch8<VEC>(slot + a.field[3], units, unit, f.y8, t, a, col[c]);
+        else if (f.y.p) fetch<bf16, VEC>(slot + a.field[3], units, unit, f.y.at(t), col[c], a.d);
+        if (f.gate_rows.p) fetch<bf16, VEC>(slot + a.field[4], units, unit, f.gate_rows.at(t), col[c], a.d);
       }
     }
     moe::cp_async_commit();
   };
-  const int ahead = a.stages - 1;  // row i - 1 leaves its stage to row i + ahead
-  for (int i = 0; i < ahead; ++i) start(i, smem + i * a.stage);
+  for (int i = 0; i < a.stages; ++i) start(first + (long long)i * step, smem + i * a.stage);
 
+  // 0: the pre norm's gain, 1: the post norm's with the gate's columns, 2: its shift
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {  // 0: the pre norm's gain; 1, 2: the post norm's with the gate's columns, and its shift
-    const int col = col_of(c), n = there(c);
-    kept.write(0, unit_of(c), load_params(f.pre_gain, f.params_f32, col, n, 1.f, a.one));
-    Eight w = load_params(f.post_gain, f.params_f32, col, n, 1.f, a.one);
-    const Eight gate = load_params(f.gate_columns, f.params_f32, col, n, 1.f, 0.f);
+  for (int c = 0; c < CH; ++c) {
+    const int unit = c * threads + tid;
+    kept.write(0, unit, load_params(f.pre_gain, f.params_f32, col[c], n[c], 1.f, a.one));
+    Eight w = load_params(f.post_gain, f.params_f32, col[c], n[c], 1.f, a.one);
+    const Eight gate = load_params(f.gate_columns, f.params_f32, col[c], n[c], 1.f, 0.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], gate.v[j]);
-    kept.write(1, unit_of(c), w);
-    if (POST_LAYER && f.post_shift) kept.write(2, unit_of(c), load_params(f.post_shift, f.params_f32, col, n, 0.f, 0.f));
+    kept.write(1, unit, w);
+    if (POST_LAYER && f.post_shift) kept.write(2, unit, load_params(f.post_shift, f.params_f32, col[c], n[c], 0.f, 0.f));
   }
-
-  // u of the pre norm, and of the post norm (y itself where there is none)
-  auto read_x = [&](const char* slot, long long t, int c, float4 st) {
-    Eight x = f.out8.codes ? read8<VEC>(slot + a.field[2], units, unit_of(c), f.out8, t, a, col_of(c), there(c))
-                           : read<R, VEC>(slot + a.field[2], units, unit_of(c), f.kept_out.at(t), there(c));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (PRE_LAYER) x.v[j] = add2(x.v[j], two(-st.z));
-      x.v[j] = mul2(x.v[j], two(st.w));
-    }
-    if (PRE_LAYER && there(c) < 8) x.cut(there(c));  // 0 - mean behind the row's end
-    return x;
-  };
-  auto read_y = [&](const char* slot, long long t, int c, float4 st) {
-    Eight y = f.y8.codes ? read8<VEC>(slot + a.field[3], units, unit_of(c), f.y8, t, a, col_of(c), there(c))
-                         : read<bf16, VEC>(slot + a.field[3], units, unit_of(c), f.y.at(t), there(c));
-    if (POST != kNone) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (POST_LAYER) y.v[j] = add2(y.v[j], two(-st.x));
-        y.v[j] = mul2(y.v[j], two(st.y));
-      }
-      if (POST_LAYER && there(c) < 8) y.cut(there(c));
-    }
-    return y;
-  };
-  auto read_grad = [&](const char* slot, long long t, int c) {
-    if (f.grad_out.p) return read<R, VEC>(slot + a.field[0], units, unit_of(c), f.grad_out.at(t), there(c));
-    Eight z;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) z.v[j] = make_float2(0.f, 0.f);
-    return z;
-  };
+  auto param = [&](int which, int c) { return kept.read(which, c * threads + tid); };
 
   float2 acc_tu[CH][4], acc_t[PRE_LAYER ? CH : 1][4], acc_v[CH][4], acc_g[POST_LAYER ? CH : 1][4];
 #pragma unroll
@@ -128,188 +92,186 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
       if (PRE_LAYER) acc_t[PRE_LAYER ? c : 0][j] = make_float2(0.f, 0.f);
       if (POST_LAYER) acc_g[POST_LAYER ? c : 0][j] = make_float2(0.f, 0.f);
     }
-  float4 st = make_float4(0.f, 1.f, 0.f, 1.f), st_next = st, st_ahead = st;
-  float gate_t = 1.f, gate_next = 1.f, gate_ahead = 1.f;
-  auto look_ahead = [&](int i) {  // a row's numbers, an iteration before its sums
-    if (i >= rows) return;
-    if (f.stats) st_ahead = __ldg(f.stats + row_at(i));
-    if (f.gate_tokens) gate_ahead = __ldg(f.gate_tokens + row_at(i));
-  };
-  look_ahead(0);
-  float total[4 * quads] = {};
   const bool sums_post = POST != kNone || f.grad_gate_tokens;
-  const float inv_d = 1.f / (float)a.d;
+  char* slot = smem;
+  const float4 no_norms = make_float4(0.f, 1.f, 0.f, 1.f);
+  // a row's numbers, a row ahead
+  float4 st_next = f.stats && first < a.T ? __ldg(f.stats + first) : no_norms;
+  float gate_next = f.gate_tokens && first < a.T ? __ldg(f.gate_tokens + first) : 1.f;
 #pragma unroll 1
-  for (int i = 0; i < rows + 1; ++i) {
-    st = st_next, gate_t = gate_next;
-    st_next = st_ahead, gate_next = gate_ahead;
-    look_ahead(i + 1);
+  for (long long t = first; t < a.T; t += step) {
+    const float4 st = st_next;
+    const float gate_t = gate_next;
+    if (t + step < a.T) {
+      if (f.stats) st_next = __ldg(f.stats + t + step);
+      if (f.gate_tokens) gate_next = __ldg(f.gate_tokens + t + step);
+    }
+    wait_copies(a.stages);
+    // x: u of the pre norm; y: u of the post norm, or y itself where there is none;
+    // go: grad_out + rstd t
+    Eight x[CH], y[CH], gn[CH], go[CH], gate[CH];
     float2 sum[4 * quads];
 #pragma unroll
     for (int q = 0; q < 4 * quads; ++q) sum[q] = make_float2(0.f, 0.f);
     auto more = [&](int q, float2 p, float2 v) {
       if (q < 4 * quads) sum[q < 4 * quads ? q : 0] = fma2(p, v, sum[q < 4 * quads ? q : 0]);
     };
-    if (i < rows) {  // row i's sums
-      wait_copies(ahead - 1);
-      const char* slot = ring.slot(0);
-      const long long t = row_at(i);
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        Eight go = read_grad(slot, t, c), x;
-        if (has_norm) {
-          x = read_x(slot, t, c, st_next);
-          const Eight gn = read<bf16, VEC>(slot + a.field[1], units, unit_of(c), f.grad_norm.at(t), there(c));
-          const Eight k = kept.read(0, unit_of(c));
+    for (int c = 0; c < CH; ++c) {
+      const int unit = c * threads + tid;
+      go[c] = x[c] = y[c] = Eight{};
+      if (f.grad_out.p) go[c] = read<R, VEC>(slot + a.field[0], units, unit, f.grad_out.at(t), n[c]);
+      if (has_norm) {
+        gn[c] = read<bf16, VEC>(slot + a.field[1], units, unit, f.grad_norm.at(t), n[c]);
+        x[c] = f.out8.codes ? read8<VEC>(slot + a.field[2], units, unit, f.out8, t, a, col[c], n[c])
+                            : read<R, VEC>(slot + a.field[2], units, unit, f.kept_out.at(t), n[c]);
+        const Eight k = param(0, c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 tj = mul2(gn.v[j], k.v[j]);
-            more(kTU, tj, x.v[j]);
-            if (PRE_LAYER) more(kT, tj, two(1.f));
-            go.v[j] = fma2(tj, two(st_next.w), go.v[j]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x.v[j] = make_float2(0.f, 0.f);
+        for (int j = 0; j < 4; ++j) {
+          if (PRE_LAYER) x[c].v[j] = add2(x[c].v[j], two(-st.z));
+          x[c].v[j] = mul2(x[c].v[j], two(st.w));
         }
-        if (sums_post) {
-          Eight w = kept.read(1, unit_of(c));
-          const Eight y = read_y(slot, t, c, st_next);
-          if (f.gate_rows.p) {
-            const Eight g = read<bf16, VEC>(slot + a.field[4], units, unit_of(c), f.gate_rows.at(t), there(c));
+        if (PRE_LAYER && n[c] < 8) x[c].cut(n[c]);  // 0 - mean behind the row's end
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], g.v[j]);
-          }
-          if (PRE_LAYER && there(c) < 8) w.cut(there(c));  // a gain of 1 behind the row's end
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 v = mul2(y.v[j], w.v[j]);
-            more(kUV, go.v[j], v);
-            more(kXV, x.v[j], v);
-            if (PRE_LAYER) more(kV, v, two(1.f));
-            if (POST_LAYER) {
-              more(kUW, go.v[j], w.v[j]);
-              more(kXW, x.v[j], w.v[j]);
-              if (PRE_LAYER) more(kW, w.v[j], two(1.f));
-            }
-          }
-          if (token_shift) {
-            const Eight b = kept.read(2, unit_of(c));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              more(kUB, go.v[j], b.v[j]);
-              more(kXB, x.v[j], b.v[j]);
-              if (PRE_LAYER) more(kB, b.v[j], two(1.f));
-            }
-          }
+        for (int j = 0; j < 4; ++j) {
+          const float2 tj = mul2(gn[c].v[j], k.v[j]);
+          more(kTU, tj, x[c].v[j]);
+          if (PRE_LAYER) more(kT, tj, two(1.f));
+          go[c].v[j] = fma2(tj, two(st.w), go[c].v[j]);
         }
       }
-    }
-    if (i >= 1) {  // row i - 1's gradients
-      const long long t = row_at(i - 1);
-      const char* slot = ring.slot(1);
-      const float c1 = total[kTU] * inv_d, c2 = PRE_LAYER ? total[kT] * inv_d : 0.f;
-      auto of = [&](int uv, int xv, int ones) {
-        auto at = [&](int q) { return total[q < 4 * quads ? q : 0]; };
-        return at(uv) - (has_norm ? st.w * (c1 * at(xv) + (PRE_LAYER ? c2 * at(ones) : 0.f)) : 0.f);
-      };
-      // sum of G v = sum of G' v - rstd (c2 sum of v + c1 sum of x v), and so on
-      const float e1 = sums_post ? a.scale * of(kUV, kXV, kV) : 0.f;
-      const float m1 = e1 * gate_t * inv_d, m2 = POST_LAYER ? a.scale * gate_t * of(kUW, kXW, kW) * inv_d : 0.f;
-      if (f.grad_gate_tokens && warp == 0 && lane == 0)
-        f.grad_gate_tokens[t] = e1 + (token_shift ? a.scale * of(kUB, kXB, kB) : 0.f);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        Eight g = read_grad(slot, t, c);
-        if (has_norm) {
-          const Eight x = read_x(slot, t, c, st);
-          const Eight gn = read<bf16, VEC>(slot + a.field[1], units, unit_of(c), f.grad_norm.at(t), there(c));
-          const Eight k = kept.read(0, unit_of(c));
+      if (has_y) {
+        y[c] = f.y8.codes ? read8<VEC>(slot + a.field[3], units, unit, f.y8, t, a, col[c], n[c])
+                          : read<bf16, VEC>(slot + a.field[3], units, unit, f.y.at(t), n[c]);
+        if (POST != kNone) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            acc_tu[c][j] = fma2(gn.v[j], x.v[j], acc_tu[c][j]);
-            if (PRE_LAYER) acc_t[PRE_LAYER ? c : 0][j] = add2(gn.v[j], acc_t[PRE_LAYER ? c : 0][j]);
-            float2 v = fma2(x.v[j], two(-c1), mul2(gn.v[j], k.v[j]));
-            if (PRE_LAYER) v = add2(v, two(-c2));
-            g.v[j] = fma2(v, two(st.w), g.v[j]);
+            if (POST_LAYER) y[c].v[j] = add2(y[c].v[j], two(-st.x));
+            y[c].v[j] = mul2(y[c].v[j], two(st.y));
           }
+          if (POST_LAYER && n[c] < 8) y[c].cut(n[c]);
         }
-        if (f.grad_residual.p) store_row<VEC>(f.grad_residual.at(t), g, col_of(c), a.d, warp_row);
-        if (!has_y && !f.grad_y.p) continue;
-        Eight y, w = kept.read(1, unit_of(c));
-        if (has_y) y = read_y(slot, t, c, st);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], two(a.scale * gate_t));  // from here on s g G, but for the gates below
+      }
+      if (f.gate_rows.p) gate[c] = read<bf16, VEC>(slot + a.field[4], units, unit, f.gate_rows.at(t), n[c]);
+      if (sums_post) {
+        Eight w = param(1, c);
         if (f.gate_rows.p) {
-          if (f.grad_gate_rows.p) {  // s G p
-            Eight p;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p.v[j] = mul2(y.v[j], w.v[j]);
-            if (POST_LAYER && f.post_shift) {
-              const Eight b = kept.read(2, unit_of(c));
-#pragma unroll
-              for (int j = 0; j < 4; ++j) p.v[j] = add2(p.v[j], b.v[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p.v[j] = mul2(p.v[j], g.v[j]);
-            store_row<VEC>(f.grad_gate_rows.at(t), p, col_of(c), a.d, warp_row);
-          }
-          const Eight gate = read<bf16, VEC>(slot + a.field[4], units, unit_of(c), f.gate_rows.at(t), there(c));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], gate.v[j]);
+          for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], gate[c].v[j]);
         }
-        // a gate of columns is put on the sums over rows, and its gradient taken from
-        // them, at the end: here without it
-        if (has_y) {
+        if (PRE_LAYER && n[c] < 8) w.cut(n[c]);  // a gain of 1 behind the row's end
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc_v[c][j] = fma2(g.v[j], y.v[j], acc_v[c][j]);
-            if (POST_LAYER) acc_g[POST_LAYER ? c : 0][j] = add2(g.v[j], acc_g[POST_LAYER ? c : 0][j]);
+        for (int j = 0; j < 4; ++j) {
+          const float2 v = mul2(y[c].v[j], w.v[j]);
+          more(kUV, go[c].v[j], v);
+          more(kXV, x[c].v[j], v);
+          if (PRE_LAYER) more(kV, v, two(1.f));
+          if (POST_LAYER) {
+            more(kUW, go[c].v[j], w.v[j]);
+            more(kXW, x[c].v[j], w.v[j]);
+            if (PRE_LAYER) more(kW, w.v[j], two(1.f));
           }
         }
-        if (f.grad_y.p) {
+        if (token_shift) {
+          const Eight b = param(2, c);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            g.v[j] = mul2(g.v[j], w.v[j]);
-            if (POST != kNone) {
-              g.v[j] = fma2(y.v[j], two(-m1), g.v[j]);
-              if (POST_LAYER) g.v[j] = add2(g.v[j], two(-m2));
-              g.v[j] = mul2(g.v[j], two(st.y));
-            }
+            more(kUB, go[c].v[j], b.v[j]);
+            more(kXB, x[c].v[j], b.v[j]);
+            if (PRE_LAYER) more(kB, b.v[j], two(1.f));
           }
-          store_row<VEC>(f.grad_y.at(t), g, col_of(c), a.d, warp_row);
         }
       }
     }
-    start(i + ahead, ring.slot(1));
-    ring.next();
-    float4* at = reinterpret_cast<float4*>(smem + a.parts) + (i & 1) * quads * team.warps;
+    float total[4 * quads];
+    {
+      float4 v[quads];
 #pragma unroll
-    for (int q = 0; q < quads; ++q) {
-      auto reduced = [&](int n) { return quads == 1 && n == kT ? 0.f : n < kSums ? warp_sum(sum[n].x + sum[n].y) : 0.f; };
-      const float4 v = make_float4(reduced(4 * q), reduced(4 * q + 1), reduced(4 * q + 2), reduced(4 * q + 3));
-      if (lane == 0) team.write(&at[q * team.warps + warp], v);
+      for (int q = 0; q < quads; ++q)
+        v[q] = make_float4(sum[4 * q].x + sum[4 * q].y, sum[4 * q + 1].x + sum[4 * q + 1].y, sum[4 * q + 2].x + sum[4 * q + 2].y,
+                           sum[4 * q + 3].x + sum[4 * q + 3].y);
+      team.sum(v);
+#pragma unroll
+      for (int q = 0; q < quads; ++q) total[4 * q] = v[q].x, total[4 * q + 1] = v[q].y, total[4 * q + 2] = v[q].z, total[4 * q + 3] = v[q].w;
     }
-    team.exchange();
+    start(t + (long long)a.stages * step, slot);  // all of the row has been read
+    slot += a.stage;
+    if (slot == smem + a.vec) slot = smem;
+    const float c1 = total[kTU] * inv_d, c2 = PRE_LAYER ? total[kT] * inv_d : 0.f;
+    auto of = [&](int uv, int xv, int ones) {
+      auto at = [&](int q) { return total[q < 4 * quads ? q : 0]; };
+      return at(uv) - (has_norm ? st.w * (c1 * at(xv) + (PRE_LAYER ? c2 * at(ones) : 0.f)) : 0.f);
+    };
+    // sum of G v = sum of G' v - rstd (c2 sum of v + c1 sum of x v), and so on
+    const float e1 = sums_post ? a.scale * of(kUV, kXV, kV) : 0.f;
+    const float m1 = e1 * gate_t * inv_d, m2 = POST_LAYER ? a.scale * gate_t * of(kUW, kXW, kW) * inv_d : 0.f;
+    if (f.grad_gate_tokens && team.rank == 0 && tid == 0)
+      f.grad_gate_tokens[t] = e1 + (token_shift ? a.scale * of(kUB, kXB, kB) : 0.f);
 #pragma unroll
-    for (int q = 0; q < quads; ++q) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = lane; w < team.warps; w += 32) {
-        const float4 p = at[q * team.warps + w];
-        v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+    for (int c = 0; c < CH; ++c) {
+      Eight g = go[c];
+      if (has_norm) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc_tu[c][j] = fma2(gn[c].v[j], x[c].v[j], acc_tu[c][j]);
+          if (PRE_LAYER) acc_t[PRE_LAYER ? c : 0][j] = add2(gn[c].v[j], acc_t[PRE_LAYER ? c : 0][j]);
+          g.v[j] = fma2(x[c].v[j], two(-c1 * st.w), g.v[j]);
+          if (PRE_LAYER) g.v[j] = add2(g.v[j], two(-c2 * st.w));
+        }
       }
-      total[4 * q] = warp_sum(v.x), total[4 * q + 1] = warp_sum(v.y), total[4 * q + 2] = warp_sum(v.z);
-      if (quads > 1 && 4 * q + 3 < kSums) total[4 * q + 3] = warp_sum(v.w);
+      if (f.grad_residual.p) store_row<VEC>(f.grad_residual.at(t), g, col[c], a.d, warp_row);
+      if (!has_y && !f.grad_y.p) continue;
+      const Eight w = param(1, c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], two(a.scale * gate_t));  // from here on s g G, but for the gates below
+      if (f.gate_rows.p) {
+        if (f.grad_gate_rows.p) {  // s G p
+          Eight p;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p.v[j] = mul2(y[c].v[j], w.v[j]);
+          if (POST_LAYER && f.post_shift) {
+            const Eight b = param(2, c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p.v[j] = add2(p.v[j], b.v[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p.v[j] = mul2(p.v[j], g.v[j]);
+          store_row<VEC>(f.grad_gate_rows.at(t), p, col[c], a.d, warp_row);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], gate[c].v[j]);
+      }
+      // a gate of columns is put on the sums over rows, and its gradient taken from
+      // them, at the end: here without it
+      if (has_y) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc_v[c][j] = fma2(g.v[j], y[c].v[j], acc_v[c][j]);
+          if (POST_LAYER) acc_g[POST_LAYER ? c : 0][j] = add2(g.v[j], acc_g[POST_LAYER ? c : 0][j]);
+        }
+      }
+      if (f.grad_y.p) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          g.v[j] = mul2(g.v[j], w.v[j]);
+          if (POST != kNone) {
+            g.v[j] = fma2(y[c].v[j], two(-m1), g.v[j]);
+            if (POST_LAYER) g.v[j] = add2(g.v[j], two(-m2));
+            g.v[j] = mul2(g.v[j], two(st.y));
+          }
+        }
+        store_row<VEC>(f.grad_y.at(t), g, col[c], a.d, warp_row);
+      }
     }
   }
 
   if (!f.sums) return;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    float* to = f.sums + (long long)first * 4 * a.d + col_of(c);
+    float* to = f.sums + (long long)first * 4 * a.d + col[c];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (j >= there(c)) break;
+      if (j >= n[c]) break;
       auto get = [&](const float2(&v)[4]) { return j & 1 ? v[j >> 1].y : v[j >> 1].x; };
       to[j] = get(acc_tu[c]);
       if (PRE_LAYER) to[a.d + j] = get(acc_t[PRE_LAYER ? c : 0]);
@@ -467,7 +429,7 @@ int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void*
                           f.y8.codes ? codes : f.y.p ? piece : 0, f.gate_rows.p ? piece : 0};
     const bool layers = h->pre == kLayer || h->post == kLayer;
     const Plan p = lay_out(&f.a, chunks_of(h->d, T, layers ? 1 : 2), kThreads, bytes, f.post_shift ? 3 : 2,
-                           quads_of(h->pre == kLayer, h->post), 2, vec);
+                           quads_of(h->pre == kLayer, h->post), vec);
     teams = std::min({T, kSms * p.per_sm / p.blocks, most_teams(h)});
     return by_kind(h, vec, p.chunks, [&](auto v, auto layer, auto post, auto c) {
       constexpr bool VEC = decltype(v)::value, LAYER = decltype(layer)::value;
