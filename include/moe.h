@@ -546,9 +546,10 @@ int moe_rows8_dequantize(long long rows, int cols, int type, int group, const vo
  * gate_stride elements apart.
  *
  * y and norm are bf16, the residual and out of residual_type.  Row t of a tensor
- * is at its pointer + t * its stride elements (stride >= d); every tensor is
+ * is at its pointer + t * its stride elements (d <= stride, below 4 GB); every tensor is
  * aligned to its type, and rows of a multiple of 8 columns that are aligned to 16
- * bytes (codes to 8) are faster.  Any d from 1 to 32768.  A row with an infinity or
+ * bytes (codes to 8) are faster.  Any d from 1 to 32768, up to
+ * 2^30 rows.  A row with an infinity or
  * a NaN makes itself NaN, no other. */
 #define MOE_NORM_NONE 0
 #define MOE_NORM_RMS 1

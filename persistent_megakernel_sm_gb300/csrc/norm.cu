@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? 2 : 1) norm_forward(const __gr
   wait_for_previous_kernel();
   let_next_kernel_start();
   begin(a, team, smem, team.blocks * units * 8);
-  auto start = [&](long long t, char* slot) {
+  auto start = [&](int t, char* slot) {
     if (t < a.T) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -50,8 +50,8 @@ __global__ void __launch_bounds__(kThreads, VEC ? 2 : 1) norm_forward(const __gr
     }
     moe::cp_async_commit();
   };
-  long long t = blockIdx.x / team.blocks;
-  for (int i = 0; i < a.stages; ++i) start(t + (long long)i * step, smem + i * a.stage);
+  int t = blockIdx.x / team.blocks;
+  for (int i = 0; i < a.stages; ++i) start(t + i * step, smem + i * a.stage);
 
   // 0: s g gain of the post norm, 1: the pre norm's gain, 2 and 3: their shifts
 #pragma unroll
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? 2 : 1) norm_forward(const __gr
       }
     }
     if (f.norm.p) pre = moments<PRE_LAYER, CH>(team, sum, n, inv_d, a.eps);
-    start(t + (long long)a.stages * step, slot);  // all of the row has been read
+    start(t + a.stages * step, slot);  // all of the row has been read
     slot += a.stage;
     if (slot == smem + a.vec) slot = smem;
 #pragma unroll
@@ -210,7 +210,7 @@ int moe_norm_forward(const moe_norm_t* h, int T, int residual_type, const void* 
                      void* norm, long long norm_stride, float* stats, const moe_rows8* out8, const moe_rows8* y8,
                      void* stream) {
   if (!h) return moe::set_error(MOE_E_INVAL, "null handle");
-  if (T < 0) return moe::set_error(MOE_E_INVAL, "T must not be negative");
+  if (T < 0 || T > kMaxT) return moe::set_error(MOE_E_INVAL, "T must be in 0..2^30");
   if (residual_type != MOE_TYPE_F32 && residual_type != MOE_TYPE_BF16)
     return moe::set_error(MOE_E_INVAL, "the residual is MOE_TYPE_F32 or MOE_TYPE_BF16");
   const char* bad = check_params(h, params);
@@ -250,8 +250,7 @@ int moe_norm_forward(const moe_norm_t* h, int T, int residual_type, const void* 
                      rows_aligned(f.norm) && rows_aligned(f.gate_rows) && aligned(f.out8.codes, 8) && aligned(f.y8.codes, 8);
     const int piece = vec ? 16 : 32, size = (int)sizeof(R) * 8 + (vec ? 0 : 16);
     const int bytes[5] = {size, y ? piece : 0, f.gate_rows.p ? piece : 0, 0, 0};
-    const bool layers = h->pre == kLayer || h->post == kLayer;
-    const Plan p = lay_out(&f.a, chunks_of(h->d, T, layers ? 1 : 2), vec ? 2 * kThreads : kThreads, bytes,
+    const Plan p = lay_out(&f.a, vec ? chunks_of(h->d, T, 2) : 1, kThreads, vec ? 2 * kThreads : kThreads, bytes,
                            f.pre_shift ? 4 : f.post_shift ? 3 : 2, 1, vec);
     const int teams = std::min(T, kSms * p.per_sm / p.blocks);
     return by_kind(h, vec, p.chunks, [&](auto v, auto layer, auto post, auto c) {

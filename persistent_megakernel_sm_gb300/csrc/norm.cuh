@@ -48,7 +48,9 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kMaxD = 32768;
-constexpr int kThreads = 512;            // of a block, at most
+constexpr int kMaxT = 1 << 30;            // a row index and a few strides of the grid stay in 32 bits
+constexpr int kThreads = 512;            // of a block of the forward pass, at most
+constexpr int kGradThreads = 1024;       // of the gradient's
 constexpr int kMaxStages = 4;            // rows under way
 constexpr int kSms = 152;
 constexpr int kRing = 200 * 1024;        // shared memory of an SM for all of it
@@ -108,12 +110,14 @@ __device__ __forceinline__ void copy4(void* to, const void* from, int n) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(moe::smem_u32(to)), "l"(from), "r"(n) : "memory");
 }
 
-// Rows of a tensor: where row 0 begins and how far the next is, in elements.
+// Rows of a tensor: where row 0 begins and how far the next is, in bytes.
 template <typename T>
 struct Rows {
   T* p;
-  long long stride;
-  __device__ __forceinline__ T* at(long long t) const { return p + t * stride; }
+  uint32_t stride;
+  __device__ __forceinline__ T* at(int t) const {  // one multiply-add
+    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + (uint64_t)(uint32_t)t * stride);
+  }
 };
 
 struct Rows8 {
@@ -128,7 +132,7 @@ struct Shape {
   int vec;         // where the gains and shifts begin
   int out;         // where the warps' rows for unaligned stores begin
   int parts;       // where the warps' parts of the sums begin, for this row and the one before
-  int groups, group_lanes;  // of 8-bit rows
+  int groups, group_lanes, group_log;  // of 8-bit rows: of a row; a group's eights, and the logarithm of its columns
   float scale, eps, one;    // one: 1 where gains are stored less 1
 };
 
@@ -210,10 +214,10 @@ __device__ __forceinline__ Eight read(const char* field, int units, int unit, co
 }
 
 template <bool VEC>
-__device__ __forceinline__ void fetch8(char* field, int units, int unit, const Rows8& r, long long t, const Shape& a, int col) {
+__device__ __forceinline__ void fetch8(char* field, int units, int unit, const Rows8& r, int t, const Shape& a, int col) {
   if (col >= a.d) return;
   uint2* slot = reinterpret_cast<uint2*>(field) + unit;
-  const int8_t* row = r.codes + t * a.d + col;
+  const int8_t* row = r.codes + (long long)t * a.d + col;
   if constexpr (VEC) {
     copy8(slot, row, 8);
   } else {
@@ -225,13 +229,13 @@ __device__ __forceinline__ void fetch8(char* field, int units, int unit, const R
       if (8 * i < end) copy8(slot + i * units, from + 8 * i, min(8, end - 8 * i));
   }
   // the word that the scale is in; the tensor may end in its middle
-  const long long scale = t * a.groups + col / (8 * a.group_lanes);
+  const long long scale = (long long)t * a.groups + (col >> a.group_log);
   const bool last = scale == (long long)a.T * a.groups - 1 && !(scale & 1);
   copy4(field + (size_t)units * 8 * pieces8<VEC>() + 4 * unit, r.scales + (scale & ~1ll), last ? 2 : 4);
 }
 
 template <bool VEC>
-__device__ __forceinline__ Eight read8(const char* field, int units, int unit, const Rows8& r, long long t, const Shape& a, int col,
+__device__ __forceinline__ Eight read8(const char* field, int units, int unit, const Rows8& r, int t, const Shape& a, int col,
                                        int n) {
   const uint2* slot = reinterpret_cast<const uint2*>(field) + unit;
   uint32_t w[2];
@@ -241,10 +245,10 @@ __device__ __forceinline__ Eight read8(const char* field, int units, int unit, c
   } else {
     const uint2 q2 = slot[units];
     const uint32_t in[4] = {q.x, q.y, q2.x, q2.y};
-    shifted(in, (int)(reinterpret_cast<uintptr_t>(r.codes + t * a.d) & 7), w);
+    shifted(in, (int)(reinterpret_cast<uintptr_t>(r.codes + (long long)t * a.d) & 7), w);
   }
   const uint32_t word = *reinterpret_cast<const uint32_t*>(field + (size_t)units * 8 * pieces8<VEC>() + 4 * unit);
-  const bool odd = (t * a.groups + col / (8 * a.group_lanes)) & 1;
+  const bool odd = (t * a.groups + (col >> (a.group_log))) & 1;
   const float s = __uint_as_float(odd ? word & 0xffff0000u : word << 16);
   float x[8];
   moe::rows8_floats(w[0], x);
@@ -299,7 +303,7 @@ __device__ __forceinline__ void store_row(bf16* row, const Eight& e, int col, in
 
 // The thread's 8 columns of a row of T, held in 8 bits; zeros behind the row's end.
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_rows8(const Rows8& r, long long t, const Shape& a, const Eight& e, int col, float* warp_row) {
+__device__ __forceinline__ void store_rows8(const Rows8& r, int t, const Shape& a, const Eight& e, int col, float* warp_row) {
   uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) most = max(most, moe::abs_bits(e.get(i)));
@@ -312,7 +316,7 @@ __device__ __forceinline__ void store_rows8(const Rows8& r, long long t, const S
   moe::rows8_codes<T>(v, s, word);
   const int lane = threadIdx.x & 31;
   if constexpr (VEC) {
-    if (col < a.d) __stcs(reinterpret_cast<uint2*>(r.codes + t * a.d + col), make_uint2(word[0], word[1]));
+    if (col < a.d) __stcs(reinterpret_cast<uint2*>(r.codes + (long long)t * a.d + col), make_uint2(word[0], word[1]));
   } else {
     const int lane_col = col - 7 * lane;
     __syncwarp();
@@ -320,9 +324,9 @@ __device__ __forceinline__ void store_rows8(const Rows8& r, long long t, const S
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (lane_col + 32 * i < a.d) r.codes[t * a.d + lane_col + 32 * i] = reinterpret_cast<int8_t*>(warp_row)[lane + 32 * i];
+      if (lane_col + 32 * i < a.d) r.codes[(long long)t * a.d + lane_col + 32 * i] = reinterpret_cast<int8_t*>(warp_row)[lane + 32 * i];
   }
-  if (col < a.d && (lane & (a.group_lanes - 1)) == 0) r.scales[t * a.groups + col / (8 * a.group_lanes)] = s;
+  if (col < a.d && (lane & (a.group_lanes - 1)) == 0) r.scales[(long long)t * a.groups + (col >> a.group_log)] = s;
 }
 
 // ------------------------------------------------------------------- parameters
@@ -439,7 +443,7 @@ struct Team {
     turn ^= 1;
     put(at + warp, v, lane == 0);
     exchange();
-    if (blocks == 1) {  // at most 16 warps
+    if (blocks == 1 && warps <= 16) {
       float s = (lane & 15) < warps ? at[lane & 15] : 0.f;
 #pragma unroll
       for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
@@ -450,7 +454,6 @@ struct Team {
     return warp_sum(s);
   }
 };
-static_assert(kThreads / 32 <= 16, "a block's warps");
 
 // A norm's mean and rstd of the team's row, CH eights of it in each thread, zeros behind
 // its end; n: how many of them are columns.
@@ -502,7 +505,7 @@ __device__ __forceinline__ void wait_copies(int stages) {
 
 template <typename T>
 bool rows_aligned(const Rows<T>& r) {  // for 16-byte vectors
-  return reinterpret_cast<uintptr_t>(r.p) % 16 == 0 && (size_t)r.stride * sizeof(T) % 16 == 0;
+  return reinterpret_cast<uintptr_t>(r.p) % 16 == 0 && r.stride % 16 == 0;
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -517,7 +520,7 @@ struct Plan {
 // A block's threads and shared memory for `chunks` eights a lane: as many blocks to a
 // row as it takes for two stages to fit, as many blocks to an SM as it then has
 // room for, up to sm_threads threads, and as many stages, up to kMaxStages.
-Plan lay_out(Shape* a, int chunks, int sm_threads, const int (&field_bytes)[5], int kept, int quads, bool vec) {
+Plan lay_out(Shape* a, int chunks, int block_threads, int sm_threads, const int (&field_bytes)[5], int kept, int quads, bool vec) {
   constexpr int least = 2;
   Plan p;
   p.chunks = chunks;
@@ -531,11 +534,11 @@ Plan lay_out(Shape* a, int chunks, int sm_threads, const int (&field_bytes)[5], 
     for (int i = 0; i < 5; ++i) a->field[i] = a->stage, a->stage += (field_bytes[i] + 15) / 16 * 16 * units;
     parts = 2 * quads * p.blocks * p.threads / 32 * 16;
     rest = kept * 32 * units + (vec ? 0 : p.threads * 32) + parts;
-    return p.threads <= kThreads && least * a->stage + rest <= kRing;
+    return p.threads <= block_threads && least * a->stage + rest <= kRing;
   };
   int blocks = 1;
   while (!with(blocks) && blocks < kMaxCluster) blocks *= 2;
-  p.per_sm = std::max(1, std::min({16, sm_threads / p.threads, kRing / (least * a->stage + rest)}));
+  p.per_sm = std::max(1, std::min({32, sm_threads / p.threads, kRing / (least * a->stage + rest)}));
   a->stages = std::max(least, std::min(kMaxStages, (kRing / p.per_sm - rest) / std::max(1, a->stage)));
   a->vec = a->stages * a->stage;
   a->out = a->vec + kept * 32 * units;
@@ -546,7 +549,7 @@ Plan lay_out(Shape* a, int chunks, int sm_threads, const int (&field_bytes)[5], 
 
 template <typename, bool, bool, int, int, bool>
 struct ForwardKernel;
-template <typename, bool, bool, int, int>
+template <typename, bool, bool, int>
 struct BackwardKernel;
 
 // Shared memory beyond 48 KB and clusters beyond 8 are asked for once a kernel and device.
@@ -593,14 +596,9 @@ struct moe_norm {
 
 namespace {
 
-// Rows that a backward pass takes at once, at most: its teams.
+// Rows that a gradient takes at once, at most: its teams.
 int most_teams(const moe_norm* h) {
-  int most = 1;
-  for (int chunks = 1; chunks <= 2; ++chunks) {
-    const int threads = ((h->d + 8 * chunks - 1) / (8 * chunks) + 31) / 32 * 32;
-    most = std::max(most, kSms * std::max(1, std::min(16, kThreads / threads)));
-  }
-  return most;
+  return kSms * std::max(1, std::min(32, kGradThreads / (((h->d + 7) / 8 + 31) / 32 * 32)));
 }
 
 Shape shape_of(const moe_norm* h, int T) {
@@ -612,6 +610,7 @@ Shape shape_of(const moe_norm* h, int T) {
   a.one = h->one;
   a.groups = (h->d + h->group - 1) / h->group;
   a.group_lanes = h->group / 8;
+  a.group_log = h->group == 32 ? 5 : h->group == 64 ? 6 : 7;
   return a;
 }
 
@@ -625,23 +624,28 @@ int chunks_of(int d, int T, int most) {
   return c;
 }
 
-// f(aligned, pre norm a layer norm, post norm, eights of a lane), as types; with a
-// layer norm a lane has one.
+// f(aligned, pre norm a layer norm, post norm, eights of a lane), as types.
 template <typename F>
 cudaError_t by_kind(const moe_norm* h, bool vec, int chunks, F&& f) {
-  constexpr std::integral_constant<int, 1> one{};
-  constexpr std::integral_constant<int, 2> two{};
   constexpr std::integral_constant<int, kNone> none{};
   constexpr std::integral_constant<int, kRms> rms{};
   constexpr std::integral_constant<int, kLayer> layer{};
-  auto by_norms = [&](auto v) {
-    if (h->pre == kLayer)
-      return h->post == kNone ? f(v, std::true_type{}, none, one) : h->post == kRms ? f(v, std::true_type{}, rms, one) : f(v, std::true_type{}, layer, one);
-    if (h->post == kLayer) return f(v, std::false_type{}, layer, one);
-    if (h->post == kNone) return chunks == 1 ? f(v, std::false_type{}, none, one) : f(v, std::false_type{}, none, two);
-    return chunks == 1 ? f(v, std::false_type{}, rms, one) : f(v, std::false_type{}, rms, two);
+  auto by_post = [&](auto v, auto pre, auto c) {
+    return h->post == kNone ? f(v, pre, none, c) : h->post == kRms ? f(v, pre, rms, c) : f(v, pre, layer, c);
   };
-  return vec ? by_norms(std::true_type{}) : by_norms(std::false_type{});
+  auto by_chunks = [&](auto v, auto pre) {
+    return chunks == 1 ? by_post(v, pre, std::integral_constant<int, 1>{}) : by_post(v, pre, std::integral_constant<int, 2>{});
+  };
+  auto by_pre = [&](auto v) { return h->pre == kLayer ? by_chunks(v, std::true_type{}) : by_chunks(v, std::false_type{}); };
+  return vec ? by_pre(std::true_type{}) : by_pre(std::false_type{});
+}
+
+const char* check_rows(const moe_norm* h, const void* p, int type, long long stride) {
+  if (!p) return nullptr;
+  if (!aligned(p, type_size(type))) return "tensors must be aligned to their type";
+  if (stride < h->d) return "rows overlap: a row stride is below d";
+  if (stride >= (1ll << 32) / (long long)type_size(type)) return "a row stride must be below 4 GB";
+  return nullptr;
 }
 
 const char* check_params(const moe_norm* h, const moe_norm_params* p) {
@@ -656,7 +660,7 @@ const char* check_params(const moe_norm* h, const moe_norm_params* p) {
   if ((h->gate != MOE_GATE_NONE) != (p->gate != nullptr)) return "the gate must be given as the handle has it";
   const size_t gate_size = h->gate == MOE_GATE_CHANNEL ? type_size(p->type) : h->gate == MOE_GATE_TOKEN ? 4 : 2;
   if (!aligned(p->gate, gate_size)) return "the gate must be aligned to its type";
-  if (h->gate == MOE_GATE_ELEMENT && p->gate_stride < h->d) return "rows of the gate overlap: the row stride is below d";
+  if (h->gate == MOE_GATE_ELEMENT) return check_rows(h, p->gate, MOE_TYPE_BF16, p->gate_stride);
   return nullptr;
 }
 
@@ -667,20 +671,13 @@ const char* check_rows8(const moe_rows8* r) {
   return nullptr;
 }
 
-const char* check_rows(const moe_norm* h, const void* p, int type, long long stride) {
-  if (!p) return nullptr;
-  if (!aligned(p, type_size(type))) return "tensors must be aligned to their type";
-  if (stride < h->d) return "rows overlap: a row stride is below d";
-  return nullptr;
-}
-
 Rows8 rows8_of(const moe_rows8* r) {
   return r ? Rows8{static_cast<int8_t*>(r->codes), static_cast<bf16*>(r->scales)} : Rows8{nullptr, nullptr};
 }
 
 template <typename T>
 Rows<T> rows_of(const void* p, long long stride) {
-  return Rows<T>{static_cast<T*>(const_cast<void*>(p)), stride};
+  return Rows<T>{static_cast<T*>(const_cast<void*>(p)), (uint32_t)(stride * (long long)sizeof(T))};
 }
 
 }  // namespace

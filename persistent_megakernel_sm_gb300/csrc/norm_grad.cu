@@ -28,70 +28,82 @@ enum { kTU, kUV, kXV, kT, kV, kUW, kXW, kW, kUB, kXB, kB, kSums };
 // Fours of them that a row has: kTU, kUV and kXV, with layer norms up to all.
 __host__ __device__ constexpr int quads_of(bool pre_layer, int post) { return pre_layer || post == kLayer ? 3 : 1; }
 
-template <typename R, bool VEC, bool PRE_LAYER, int POST, int CH>
-__global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant__ Backward<R> f) {
+// A lane has one eight, so that a block's warps are many and what they keep from row to
+// row, the sums over rows, leaves them room: a row is read from its slots again once
+// its sums are known.
+template <typename R, bool VEC, bool PRE_LAYER, int POST>
+__global__ void __launch_bounds__(kGradThreads) norm_backward(const __grid_constant__ Backward<R> f) {
   extern __shared__ __align__(16) char smem[];
   constexpr int quads = quads_of(PRE_LAYER, POST);
   constexpr bool POST_LAYER = POST == kLayer;
   const Shape& a = f.a;
   Team team(smem + a.parts);
-  const int tid = threadIdx.x, threads = blockDim.x, units = CH * threads;
+  const int tid = threadIdx.x, units = blockDim.x;
   const int first = blockIdx.x / team.blocks, step = gridDim.x / team.blocks;
   float* warp_row = reinterpret_cast<float*>(smem + a.out) + (tid >> 5) * 256;
   const Kept kept{reinterpret_cast<float4*>(smem + a.vec), units};
   const float inv_d = 1.f / (float)a.d;
-  int col[CH], n[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) col[c] = (team.rank * units + c * threads + tid) * 8, n[c] = max(0, min(8, a.d - col[c]));
+  const int col = (team.rank * units + tid) * 8, n = max(0, min(8, a.d - col));
   const bool has_y = f.y.p || f.y8.codes, has_norm = f.grad_norm.p != nullptr;
   const bool token_shift = POST_LAYER && f.grad_gate_tokens && f.post_shift;
 
   wait_for_previous_kernel();
   let_next_kernel_start();
   begin(a, team, smem, team.blocks * units * 8);
-  auto start = [&](long long t, char* slot) {
+  auto start = [&](int t, char* slot) {
     if (t < a.T) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int unit = c * threads + tid;
-        if (f.grad_out.p) fetch<R, VEC>(slot + a.field[0], units, unit, f.grad_out.at(t), col[c], a.d);
-        if (has_norm) {
-          fetch<bf16, VEC>(slot + a.field[1], units, unit, f.grad_norm.at(t), col[c], a.d);
-          if (f.out8.codes) fetch8<VEC>(slot + a.field[2], units, unit, f.out8, t, a, col[c]);
-          else fetch<R, VEC>(slot + a.field[2], units, unit, f.kept_out.at(t), col[c], a.d);
-        }
-        if (f.y8.codes) fetch8<VEC>(slot + a.field[3], units, unit, f.y8, t, a, col[c]);
-        else if (f.y.p) fetch<bf16, VEC>(slot + a.field[3], units, unit, f.y.at(t), col[c], a.d);
-        if (f.gate_rows.p) fetch<bf16, VEC>(slot + a.field[4], units, unit, f.gate_rows.at(t), col[c], a.d);
+      if (f.grad_out.p) fetch<R, VEC>(slot + a.field[0], units, tid, f.grad_out.at(t), col, a.d);
+      if (has_norm) {
+        fetch<bf16, VEC>(slot + a.field[1], units, tid, f.grad_norm.at(t), col, a.d);
+        if (f.out8.codes) fetch8<VEC>(slot + a.field[2], units, tid, f.out8, t, a, col);
+        else fetch<R, VEC>(slot + a.field[2], units, tid, f.kept_out.at(t), col, a.d);
       }
+      if (f.y8.codes) fetch8<VEC>(slot + a.field[3], units, tid, f.y8, t, a, col);
+      else if (f.y.p) fetch<bf16, VEC>(slot + a.field[3], units, tid, f.y.at(t), col, a.d);
+      if (f.gate_rows.p) fetch<bf16, VEC>(slot + a.field[4], units, tid, f.gate_rows.at(t), col, a.d);
     }
     moe::cp_async_commit();
   };
-  for (int i = 0; i < a.stages; ++i) start(first + (long long)i * step, smem + i * a.stage);
+  for (int i = 0; i < a.stages; ++i) start(first + i * step, smem + i * a.stage);
 
-  // 0: the pre norm's gain, 1: the post norm's with the gate's columns, 2: its shift
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int unit = c * threads + tid;
-    kept.write(0, unit, load_params(f.pre_gain, f.params_f32, col[c], n[c], 1.f, a.one));
-    Eight w = load_params(f.post_gain, f.params_f32, col[c], n[c], 1.f, a.one);
-    const Eight gate = load_params(f.gate_columns, f.params_f32, col[c], n[c], 1.f, 0.f);
+  {  // 0: the pre norm's gain, 1: the post norm's with the gate's columns, 2: its shift
+    kept.write(0, tid, load_params(f.pre_gain, f.params_f32, col, n, 1.f, a.one));
+    Eight w = load_params(f.post_gain, f.params_f32, col, n, 1.f, a.one);
+    const Eight gate = load_params(f.gate_columns, f.params_f32, col, n, 1.f, 0.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], gate.v[j]);
-    kept.write(1, unit, w);
-    if (POST_LAYER && f.post_shift) kept.write(2, unit, load_params(f.post_shift, f.params_f32, col[c], n[c], 0.f, 0.f));
+    kept.write(1, tid, w);
+    if (POST_LAYER && f.post_shift) kept.write(2, tid, load_params(f.post_shift, f.params_f32, col, n, 0.f, 0.f));
   }
-  auto param = [&](int which, int c) { return kept.read(which, c * threads + tid); };
 
-  float2 acc_tu[CH][4], acc_t[PRE_LAYER ? CH : 1][4], acc_v[CH][4], acc_g[POST_LAYER ? CH : 1][4];
-#pragma unroll
-  for (int c = 0; c < CH; ++c)
+  // u of the pre norm, and of the post norm (y itself where there is none)
+  auto read_x = [&](const char* slot, int t, const float4& st) {
+    Eight x = f.out8.codes ? read8<VEC>(slot + a.field[2], units, tid, f.out8, t, a, col, n)
+                           : read<R, VEC>(slot + a.field[2], units, tid, f.kept_out.at(t), n);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      acc_tu[c][j] = acc_v[c][j] = make_float2(0.f, 0.f);
-      if (PRE_LAYER) acc_t[PRE_LAYER ? c : 0][j] = make_float2(0.f, 0.f);
-      if (POST_LAYER) acc_g[POST_LAYER ? c : 0][j] = make_float2(0.f, 0.f);
+      if (PRE_LAYER) x.v[j] = add2(x.v[j], two(-st.z));
+      x.v[j] = mul2(x.v[j], two(st.w));
     }
+    if (PRE_LAYER && n < 8) x.cut(n);  // 0 - mean behind the row's end
+    return x;
+  };
+  auto read_y = [&](const char* slot, int t, const float4& st) {
+    Eight y = f.y8.codes ? read8<VEC>(slot + a.field[3], units, tid, f.y8, t, a, col, n)
+                         : read<bf16, VEC>(slot + a.field[3], units, tid, f.y.at(t), n);
+    if (POST != kNone) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (POST_LAYER) y.v[j] = add2(y.v[j], two(-st.x));
+        y.v[j] = mul2(y.v[j], two(st.y));
+      }
+      if (POST_LAYER && n < 8) y.cut(n);
+    }
+    return y;
+  };
+  const Eight nothing{};
+
+  Eight acc_tu = nothing, acc_t = nothing, acc_v = nothing, acc_g = nothing;
   const bool sums_post = POST != kNone || f.grad_gate_tokens;
   char* slot = smem;
   const float4 no_norms = make_float4(0.f, 1.f, 0.f, 1.f);
@@ -99,7 +111,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
   float4 st_next = f.stats && first < a.T ? __ldg(f.stats + first) : no_norms;
   float gate_next = f.gate_tokens && first < a.T ? __ldg(f.gate_tokens + first) : 1.f;
 #pragma unroll 1
-  for (long long t = first; t < a.T; t += step) {
+  for (int t = first; t < a.T; t += step) {
     const float4 st = st_next;
     const float gate_t = gate_next;
     if (t + step < a.T) {
@@ -107,84 +119,57 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
       if (f.gate_tokens) gate_next = __ldg(f.gate_tokens + t + step);
     }
     wait_copies(a.stages);
-    // x: u of the pre norm; y: u of the post norm, or y itself where there is none;
-    // go: grad_out + rstd t
-    Eight x[CH], y[CH], gn[CH], go[CH], gate[CH];
-    float2 sum[4 * quads];
+    float total[4 * quads];
+    {
+      float2 sum[4 * quads];
 #pragma unroll
-    for (int q = 0; q < 4 * quads; ++q) sum[q] = make_float2(0.f, 0.f);
-    auto more = [&](int q, float2 p, float2 v) {
-      if (q < 4 * quads) sum[q < 4 * quads ? q : 0] = fma2(p, v, sum[q < 4 * quads ? q : 0]);
-    };
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int unit = c * threads + tid;
-      go[c] = x[c] = y[c] = Eight{};
-      if (f.grad_out.p) go[c] = read<R, VEC>(slot + a.field[0], units, unit, f.grad_out.at(t), n[c]);
-      if (has_norm) {
-        gn[c] = read<bf16, VEC>(slot + a.field[1], units, unit, f.grad_norm.at(t), n[c]);
-        x[c] = f.out8.codes ? read8<VEC>(slot + a.field[2], units, unit, f.out8, t, a, col[c], n[c])
-                            : read<R, VEC>(slot + a.field[2], units, unit, f.kept_out.at(t), n[c]);
-        const Eight k = param(0, c);
+      for (int q = 0; q < 4 * quads; ++q) sum[q] = make_float2(0.f, 0.f);
+      auto more = [&](int q, float2 p, float2 v) {
+        if (q < 4 * quads) sum[q < 4 * quads ? q : 0] = fma2(p, v, sum[q < 4 * quads ? q : 0]);
+      };
+      Eight go = f.grad_out.p ? read<R, VEC>(slot + a.field[0], units, tid, f.grad_out.at(t), n) : nothing, x = nothing;
+      if (has_norm) {  // go: grad_out + rstd t
+        x = read_x(slot, t, st);
+        const Eight gn = read<bf16, VEC>(slot + a.field[1], units, tid, f.grad_norm.at(t), n), k = kept.read(0, tid);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (PRE_LAYER) x[c].v[j] = add2(x[c].v[j], two(-st.z));
-          x[c].v[j] = mul2(x[c].v[j], two(st.w));
-        }
-        if (PRE_LAYER && n[c] < 8) x[c].cut(n[c]);  // 0 - mean behind the row's end
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 tj = mul2(gn[c].v[j], k.v[j]);
-          more(kTU, tj, x[c].v[j]);
+          const float2 tj = mul2(gn.v[j], k.v[j]);
+          more(kTU, tj, x.v[j]);
           if (PRE_LAYER) more(kT, tj, two(1.f));
-          go[c].v[j] = fma2(tj, two(st.w), go[c].v[j]);
+          go.v[j] = fma2(tj, two(st.w), go.v[j]);
         }
       }
-      if (has_y) {
-        y[c] = f.y8.codes ? read8<VEC>(slot + a.field[3], units, unit, f.y8, t, a, col[c], n[c])
-                          : read<bf16, VEC>(slot + a.field[3], units, unit, f.y.at(t), n[c]);
-        if (POST != kNone) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (POST_LAYER) y[c].v[j] = add2(y[c].v[j], two(-st.x));
-            y[c].v[j] = mul2(y[c].v[j], two(st.y));
-          }
-          if (POST_LAYER && n[c] < 8) y[c].cut(n[c]);
-        }
-      }
-      if (f.gate_rows.p) gate[c] = read<bf16, VEC>(slot + a.field[4], units, unit, f.gate_rows.at(t), n[c]);
       if (sums_post) {
-        Eight w = param(1, c);
+        Eight w = kept.read(1, tid);
+        const Eight y = read_y(slot, t, st);
         if (f.gate_rows.p) {
+          const Eight g = read<bf16, VEC>(slot + a.field[4], units, tid, f.gate_rows.at(t), n);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], gate[c].v[j]);
+          for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], g.v[j]);
         }
-        if (PRE_LAYER && n[c] < 8) w.cut(n[c]);  // a gain of 1 behind the row's end
+        if (PRE_LAYER && n < 8) w.cut(n);  // a gain of 1 behind the row's end
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 v = mul2(y[c].v[j], w.v[j]);
-          more(kUV, go[c].v[j], v);
-          more(kXV, x[c].v[j], v);
+          const float2 v = mul2(y.v[j], w.v[j]);
+          more(kUV, go.v[j], v);
+          more(kXV, x.v[j], v);
           if (PRE_LAYER) more(kV, v, two(1.f));
           if (POST_LAYER) {
-            more(kUW, go[c].v[j], w.v[j]);
-            more(kXW, x[c].v[j], w.v[j]);
+            more(kUW, go.v[j], w.v[j]);
+            more(kXW, x.v[j], w.v[j]);
             if (PRE_LAYER) more(kW, w.v[j], two(1.f));
           }
         }
         if (token_shift) {
-          const Eight b = param(2, c);
+          const Eight b = kept.read(2, tid);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            more(kUB, go[c].v[j], b.v[j]);
-            more(kXB, x[c].v[j], b.v[j]);
+            more(kUB, go.v[j], b.v[j]);
+            more(kXB, x.v[j], b.v[j]);
             if (PRE_LAYER) more(kB, b.v[j], two(1.f));
           }
         }
       }
-    }
-    float total[4 * quads];
-    {
       float4 v[quads];
 #pragma unroll
       for (int q = 0; q < quads; ++q)
@@ -194,9 +179,6 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
 #pragma unroll
       for (int q = 0; q < quads; ++q) total[4 * q] = v[q].x, total[4 * q + 1] = v[q].y, total[4 * q + 2] = v[q].z, total[4 * q + 3] = v[q].w;
     }
-    start(t + (long long)a.stages * step, slot);  // all of the row has been read
-    slot += a.stage;
-    if (slot == smem + a.vec) slot = smem;
     const float c1 = total[kTU] * inv_d, c2 = PRE_LAYER ? total[kT] * inv_d : 0.f;
     auto of = [&](int uv, int xv, int ones) {
       auto at = [&](int q) { return total[q < 4 * quads ? q : 0]; };
@@ -207,47 +189,49 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
     const float m1 = e1 * gate_t * inv_d, m2 = POST_LAYER ? a.scale * gate_t * of(kUW, kXW, kW) * inv_d : 0.f;
     if (f.grad_gate_tokens && team.rank == 0 && tid == 0)
       f.grad_gate_tokens[t] = e1 + (token_shift ? a.scale * of(kUB, kXB, kB) : 0.f);
+    Eight g = f.grad_out.p ? read<R, VEC>(slot + a.field[0], units, tid, f.grad_out.at(t), n) : nothing;
+    if (has_norm) {
+      const Eight x = read_x(slot, t, st);
+      const Eight gn = read<bf16, VEC>(slot + a.field[1], units, tid, f.grad_norm.at(t), n), k = kept.read(0, tid);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      Eight g = go[c];
-      if (has_norm) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc_tu[c][j] = fma2(gn[c].v[j], x[c].v[j], acc_tu[c][j]);
-          if (PRE_LAYER) acc_t[PRE_LAYER ? c : 0][j] = add2(gn[c].v[j], acc_t[PRE_LAYER ? c : 0][j]);
-          g.v[j] = fma2(x[c].v[j], two(-c1 * st.w), g.v[j]);
-          if (PRE_LAYER) g.v[j] = add2(g.v[j], two(-c2 * st.w));
-        }
+      for (int j = 0; j < 4; ++j) {
+        acc_tu.v[j] = fma2(gn.v[j], x.v[j], acc_tu.v[j]);
+        if (PRE_LAYER) acc_t.v[j] = add2(gn.v[j], acc_t.v[j]);
+        float2 v = fma2(x.v[j], two(-c1), mul2(gn.v[j], k.v[j]));
+        if (PRE_LAYER) v = add2(v, two(-c2));
+        g.v[j] = fma2(v, two(st.w), g.v[j]);
       }
-      if (f.grad_residual.p) store_row<VEC>(f.grad_residual.at(t), g, col[c], a.d, warp_row);
-      if (!has_y && !f.grad_y.p) continue;
-      const Eight w = param(1, c);
+    }
+    if (f.grad_residual.p) store_row<VEC>(f.grad_residual.at(t), g, col, a.d, warp_row);
+    if (has_y || f.grad_y.p) {
+      const Eight w = kept.read(1, tid), y = has_y ? read_y(slot, t, st) : nothing;
 #pragma unroll
       for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], two(a.scale * gate_t));  // from here on s g G, but for the gates below
       if (f.gate_rows.p) {
         if (f.grad_gate_rows.p) {  // s G p
           Eight p;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) p.v[j] = mul2(y[c].v[j], w.v[j]);
+          for (int j = 0; j < 4; ++j) p.v[j] = mul2(y.v[j], w.v[j]);
           if (POST_LAYER && f.post_shift) {
-            const Eight b = param(2, c);
+            const Eight b = kept.read(2, tid);
 #pragma unroll
             for (int j = 0; j < 4; ++j) p.v[j] = add2(p.v[j], b.v[j]);
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) p.v[j] = mul2(p.v[j], g.v[j]);
-          store_row<VEC>(f.grad_gate_rows.at(t), p, col[c], a.d, warp_row);
+          store_row<VEC>(f.grad_gate_rows.at(t), p, col, a.d, warp_row);
         }
+        const Eight gate = read<bf16, VEC>(slot + a.field[4], units, tid, f.gate_rows.at(t), n);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], gate[c].v[j]);
+        for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], gate.v[j]);
       }
       // a gate of columns is put on the sums over rows, and its gradient taken from
       // them, at the end: here without it
       if (has_y) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          acc_v[c][j] = fma2(g.v[j], y[c].v[j], acc_v[c][j]);
-          if (POST_LAYER) acc_g[POST_LAYER ? c : 0][j] = add2(g.v[j], acc_g[POST_LAYER ? c : 0][j]);
+          acc_v.v[j] = fma2(g.v[j], y.v[j], acc_v.v[j]);
+          if (POST_LAYER) acc_g.v[j] = add2(g.v[j], acc_g.v[j]);
         }
       }
       if (f.grad_y.p) {
@@ -255,29 +239,28 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
         for (int j = 0; j < 4; ++j) {
           g.v[j] = mul2(g.v[j], w.v[j]);
           if (POST != kNone) {
-            g.v[j] = fma2(y[c].v[j], two(-m1), g.v[j]);
+            g.v[j] = fma2(y.v[j], two(-m1), g.v[j]);
             if (POST_LAYER) g.v[j] = add2(g.v[j], two(-m2));
             g.v[j] = mul2(g.v[j], two(st.y));
           }
         }
-        store_row<VEC>(f.grad_y.at(t), g, col[c], a.d, warp_row);
+        store_row<VEC>(f.grad_y.at(t), g, col, a.d, warp_row);
       }
     }
+    start(t + a.stages * step, slot);
+    slot += a.stage;
+    if (slot == smem + a.vec) slot = smem;
   }
 
   if (!f.sums) return;
+  float* to = f.sums + (long long)first * 4 * a.d + col;
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    float* to = f.sums + (long long)first * 4 * a.d + col[c];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j >= n[c]) break;
-      auto get = [&](const float2(&v)[4]) { return j & 1 ? v[j >> 1].y : v[j >> 1].x; };
-      to[j] = get(acc_tu[c]);
-      if (PRE_LAYER) to[a.d + j] = get(acc_t[PRE_LAYER ? c : 0]);
-      to[2 * a.d + j] = get(acc_v[c]);
-      if (POST_LAYER) to[3 * a.d + j] = get(acc_g[POST_LAYER ? c : 0]);
-    }
+  for (int j = 0; j < 8; ++j) {
+    if (j >= n) break;
+    to[j] = acc_tu.get(j);
+    if (PRE_LAYER) to[a.d + j] = acc_t.get(j);
+    to[2 * a.d + j] = acc_v.get(j);
+    if (POST_LAYER) to[3 * a.d + j] = acc_g.get(j);
   }
 }
 
@@ -295,14 +278,20 @@ __global__ void __launch_bounds__(1024) norm_columns(const Columns c) {
   wait_for_previous_kernel();
   let_next_kernel_start();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-  float v[4] = {};
-  if (col < c.d) {
-    const bool wanted[4] = {c.pre_gain_grad != nullptr, c.pre_layer && c.pre_shift_grad,
-                            c.post_gain_grad || c.gate_grad, c.post_layer && (c.post_shift_grad || c.gate_grad)};
-    for (int t = warp; t < c.teams; t += 32) {
+  const bool wanted[4] = {c.pre_gain_grad != nullptr, c.pre_layer && c.pre_shift_grad, c.post_gain_grad || c.gate_grad,
+                          c.post_layer && (c.post_shift_grad || c.gate_grad)};
+  float v[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (wanted[q]) v[q] += __ldcg(c.sums + ((long long)t * 4 + q) * c.d + col);
+  for (int q = 0; q < 4; ++q) {
+    v[q] = 0.f;
+    if (!wanted[q] || col >= c.d) continue;
+    const float* from = c.sums + (long long)q * c.d + col;
+    for (int t0 = warp; t0 < c.teams; t0 += 32 * 8) {  // eight at once
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = t0 + 32 * i < c.teams ? __ldcg(from + (long long)(t0 + 32 * i) * 4 * c.d) : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[q] += x[i];
     }
   }
 #pragma unroll
@@ -341,7 +330,7 @@ int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void*
                       const moe_norm_kept* kept, void* grad_residual, long long grad_residual_stride, void* grad_y,
                       long long grad_y_stride, const moe_norm_grads* grads, void* stream) {
   if (!h) return moe::set_error(MOE_E_INVAL, "null handle");
-  if (T < 0) return moe::set_error(MOE_E_INVAL, "T must not be negative");
+  if (T < 0 || T > kMaxT) return moe::set_error(MOE_E_INVAL, "T must be in 0..2^30");
   if (residual_type != MOE_TYPE_F32 && residual_type != MOE_TYPE_BF16)
     return moe::set_error(MOE_E_INVAL, "the residual is MOE_TYPE_F32 or MOE_TYPE_BF16");
   if (!kept || !grads) return moe::set_error(MOE_E_INVAL, "null kept or grads");
@@ -427,15 +416,16 @@ int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void*
     const int piece = vec ? 16 : 32, size = (int)sizeof(R) * 8 + (vec ? 0 : 16), codes = vec ? 16 : 32;
     const int bytes[5] = {grad_out ? size : 0, has_norm ? piece : 0, !has_norm ? 0 : f.out8.codes ? codes : size,
                           f.y8.codes ? codes : f.y.p ? piece : 0, f.gate_rows.p ? piece : 0};
-    const bool layers = h->pre == kLayer || h->post == kLayer;
-    const Plan p = lay_out(&f.a, chunks_of(h->d, T, layers ? 1 : 2), kThreads, bytes, f.post_shift ? 3 : 2,
+    const Plan p = lay_out(&f.a, 1, kGradThreads, kGradThreads, bytes, f.post_shift ? 3 : 2,
                            quads_of(h->pre == kLayer, h->post), vec);
-    teams = std::min({T, kSms * p.per_sm / p.blocks, most_teams(h)});
-    return by_kind(h, vec, p.chunks, [&](auto v, auto layer, auto post, auto c) {
+    // what a team keeps of its rows is written and read once more: 8 rows at least,
+    // unless that leaves SMs idle
+    teams = std::min({T, kSms * p.per_sm / p.blocks, most_teams(h), std::max(kSms / p.blocks, T / 8)});
+    return by_kind(h, vec, 1, [&](auto v, auto layer, auto post, auto) {
       constexpr bool VEC = decltype(v)::value, LAYER = decltype(layer)::value;
-      constexpr int POST = decltype(post)::value, CH = decltype(c)::value;
-      auto* kernel = norm_backward<R, VEC, LAYER, POST, CH>;
-      cudaError_t e = allow_smem<BackwardKernel<R, VEC, LAYER, POST, CH>>(kernel);
+      constexpr int POST = decltype(post)::value;
+      auto* kernel = norm_backward<R, VEC, LAYER, POST>;
+      cudaError_t e = allow_smem<BackwardKernel<R, VEC, LAYER, POST>>(kernel);
       return e == cudaSuccess ? launch(kernel, (unsigned)(teams * p.blocks), p.blocks, p.threads, p.smem, s, f) : e;
     });
   };
