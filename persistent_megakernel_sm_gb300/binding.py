@@ -620,6 +620,10 @@ def rows8_dequantize(codes, scales, v, group: int = 128, stream=None):
     return v
 
 
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
 class _NormParams(ctypes.Structure):
     _fields_ = [("pre_gain", _vp), ("pre_shift", _vp), ("post_gain", _vp), ("post_shift", _vp), ("gate", _vp),
                 ("gate_stride", _i64), ("type", _i32)]
@@ -653,6 +657,7 @@ class MoEBlockNorm:
             raise MoEError(MOE_E_INVAL, (lib.moe_last_error() or b"").decode())
         self.h = ctypes.c_void_p(h)
         self.d, self.pre, self.post, self.gate, self.group = d, pre, post, gate, group
+        self._columns, self._groups = (d,), -(-d // group)
         self._device = None
         self._c_forward, self._c_backward = lib.moe_norm_forward, lib.moe_norm_backward
 
@@ -668,6 +673,10 @@ class MoEBlockNorm:
         """Rows of d values that may be columns of a wider buffer: (pointer, row stride)."""
         if t is None:
             return None, 0
+        # a call of a few microseconds makes several of these checks: what is right and
+        # contiguous costs four comparisons
+        if t.dtype is dtype and t.shape == (T, self.d) and t.is_contiguous() and t.get_device() == dev:
+            return t.data_ptr(), self.d
         if t.dtype is not dtype:
             raise MoEError(MOE_E_INVAL, f"{name}: dtype {t.dtype}, expected {dtype}")
         if t.dim() != 2 or t.shape[0] != T or t.shape[1] != self.d:
@@ -687,31 +696,33 @@ class MoEBlockNorm:
         if t.get_device() != dev:
             raise MoEError(MOE_E_INVAL, f"{name}: on device {t.get_device()}, the current one is {dev}")
 
-    def _params(self, T, dev, gate, **vectors):
+    def _params(self, T, dev, gate, pre_gain, pre_shift, post_gain, post_shift):
         """The gains, shifts and gate as the C call takes them."""
-        tt = _torch()
-        kind, of, p = 1, None, _NormParams()
-        if self.gate == "channel" and gate is not None:
-            vectors["gate"] = gate
-        for name, t in vectors.items():
+        tt, of = _torch(), None
+        columns = gate if self.gate == "channel" else None
+        pointers = []
+        for name, t in (("pre_gain", pre_gain), ("pre_shift", pre_shift), ("post_gain", post_gain),
+                        ("post_shift", post_shift), ("gate", columns)):
             if t is None:
+                pointers.append(None)
                 continue
-            code = _type_code(name, t)
-            if of is not None and t.dtype is not of:
+            if of is None:
+                of = t.dtype
+                _type_code(name, t)
+            elif t.dtype is not of:
                 raise MoEError(MOE_E_INVAL, f"{name}: dtype {t.dtype}, the other gains and shifts have {of}")
-            kind, of = code, t.dtype
-            _on_device(name, t, dev, of, (self.d,))
-            setattr(p, name, t.data_ptr())
-        if gate is not None:
+            _on_device(name, t, dev, of, self._columns)
+            pointers.append(t.data_ptr())
+        stride = 0
+        if gate is not None and columns is None:
             if self.gate == "token":
                 _on_device("gate", gate, dev, tt.f32, (T,))
-                p.gate = gate.data_ptr()
+                pointers[4] = gate.data_ptr()
             elif self.gate == "element":
-                p.gate, p.gate_stride = self._rows("gate", gate, T, tt.bf16, dev)
-            elif self.gate == "none":
+                pointers[4], stride = self._rows("gate", gate, T, tt.bf16, dev)
+            else:
                 raise MoEError(MOE_E_INVAL, "gate: the handle has none")
-        p.type = kind
-        return p
+        return _NormParams(*pointers, stride, 0 if of is tt.f32 else 1)
 
     def _rows8(self, name, held, T, dev):
         if held is None:
@@ -719,8 +730,8 @@ class MoEBlockNorm:
         codes, scales = held
         tt = _torch()
         _on_device(name + " codes", codes, dev, tt.i8, (T, self.d))
-        _on_device(name + " scales", scales, dev, tt.bf16, (T, -(-self.d // self.group)))
-        return ctypes.byref(_Rows8(codes.data_ptr(), scales.data_ptr()))
+        _on_device(name + " scales", scales, dev, tt.bf16, (T, self._groups))
+        return _Rows8(codes.data_ptr(), scales.data_ptr())
 
     def forward(self, residual, y, out, norm, pre_gain=None, pre_shift=None, post_gain=None, post_shift=None, gate=None,
                 stats=None, out8=None, y8=None, stream=None):
@@ -738,10 +749,10 @@ class MoEBlockNorm:
         n, n_row = self._rows("norm", norm, T, tt.bf16, dev)
         if stats is not None:
             _on_device("stats", stats, dev, tt.f32, (T, 4))
-        p = self._params(T, dev, gate, pre_gain=pre_gain, pre_shift=pre_shift, post_gain=post_gain, post_shift=post_shift)
-        _err(self._c_forward(self.h, T, kind, r, r_row, yp, y_row, ctypes.byref(p), o, o_row, n, n_row,
-                             None if stats is None else stats.data_ptr(), self._rows8("out8", out8, T, dev),
-                             self._rows8("y8", y8, T, dev), _stream_on(stream, dev)))
+        p = self._params(T, dev, gate, pre_gain, pre_shift, post_gain, post_shift)
+        _err(self._c_forward(self.h, T, kind, r, r_row, yp, y_row, _ref(p), o, o_row, n, n_row,
+                             None if stats is None else stats.data_ptr(), _ref(self._rows8("out8", out8, T, dev)),
+                             _ref(self._rows8("y8", y8, T, dev)), _stream_on(stream, dev)))
         return out, norm
 
     def _kept(self, name, t, T, dtype, dev):
@@ -773,31 +784,28 @@ class MoEBlockNorm:
         gn, gn_row = self._rows("grad_norm", grad_norm, T, tt.bf16, dev)
         gr, gr_row = self._rows("grad_residual", grad_residual, T, dtype, dev)
         gy, gy_row = self._rows("grad_y", grad_y, T, tt.bf16, dev)
-        p = self._params(T, dev, gate, pre_gain=pre_gain, pre_shift=pre_shift, post_gain=post_gain, post_shift=post_shift)
-        kept = _NormKept()
-        kept.out, kept.out_stride, out8 = self._kept("out", out, T, dtype, dev)
-        kept.y, kept.y_stride, y8 = self._kept("y", y, T, tt.bf16, dev)
-        if out8 is not None:
-            kept.out8 = ctypes.cast(out8, _vp)
-        if y8 is not None:
-            kept.y8 = ctypes.cast(y8, _vp)
+        p = self._params(T, dev, gate, pre_gain, pre_shift, post_gain, post_shift)
+        kept_out, out_row, out8 = self._kept("out", out, T, dtype, dev)
+        kept_y, y_row, y8 = self._kept("y", y, T, tt.bf16, dev)
         if stats is not None:
             _on_device("stats", stats, dev, tt.f32, (T, 4))
-            kept.stats = stats.data_ptr()
-        grads = _NormGrads()
-        for name, t in (("pre_gain", grad_pre_gain), ("pre_shift", grad_pre_shift), ("post_gain", grad_post_gain),
-                        ("post_shift", grad_post_shift)):
+        kept = _NormKept(kept_out, out_row, None if out8 is None else ctypes.addressof(out8), kept_y, y_row,
+                         None if y8 is None else ctypes.addressof(y8), None if stats is None else stats.data_ptr())
+        pointers = []
+        for name, t in (("grad_pre_gain", grad_pre_gain), ("grad_pre_shift", grad_pre_shift),
+                        ("grad_post_gain", grad_post_gain), ("grad_post_shift", grad_post_shift)):
             if t is not None:
-                _on_device("grad_" + name, t, dev, tt.f32, (self.d,))
-                setattr(grads, name, t.data_ptr())
+                _on_device(name, t, dev, tt.f32, self._columns)
+            pointers.append(None if t is None else t.data_ptr())
+        grads = _NormGrads(*pointers)
         if grad_gate is not None:
             if self.gate == "element":
                 grads.gate, grads.gate_stride = self._rows("grad_gate", grad_gate, T, tt.bf16, dev)
             else:
-                _on_device("grad_gate", grad_gate, dev, tt.f32, (T,) if self.gate == "token" else (self.d,))
+                _on_device("grad_gate", grad_gate, dev, tt.f32, (T,) if self.gate == "token" else self._columns)
                 grads.gate = grad_gate.data_ptr()
-        _err(self._c_backward(self.h, T, kind, go, go_row, gn, gn_row, ctypes.byref(p), ctypes.byref(kept), gr, gr_row,
-                              gy, gy_row, ctypes.byref(grads), _stream_on(stream, dev)))
+        _err(self._c_backward(self.h, T, kind, go, go_row, gn, gn_row, _ref(p), _ref(kept), gr, gr_row, gy, gy_row,
+                              _ref(grads), _stream_on(stream, dev)))
         return grad_residual, grad_y
 
     def close(self):

@@ -332,12 +332,31 @@ __device__ __forceinline__ void store_rows8(const Rows8& r, int t, const Shape& 
 // ------------------------------------------------------------------- parameters
 
 __device__ __forceinline__ Eight load_params(const void* p, int f32, int col, int n, float none, float plus) {
-  Eight e;
+  Eight e{};
+  if (!p) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    e.set(i, !p ? none : i >= n ? 0.f
-                                : plus + (f32 ? static_cast<const float*>(p)[col + i]
-                                              : __bfloat162float(static_cast<const bf16*>(p)[col + i])));
+    for (int i = 0; i < 4; ++i) e.v[i] = two(none);
+  } else if (n == 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    uint32_t w[4];
+    if (f32) {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + col);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        put_words(q[h], w);
+        e.v[2 * h] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        e.v[2 * h + 1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+      }
+    } else {
+      put_words(*reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + col), w);
+      e = unpack(w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e.v[i] = add2(e.v[i], two(plus));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) e.set(i, plus + (f32 ? static_cast<const float*>(p)[col + i] : __bfloat162float(static_cast<const bf16*>(p)[col + i])));
+  }
   return e;
 }
 

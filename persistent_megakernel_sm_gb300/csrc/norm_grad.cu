@@ -280,18 +280,19 @@ __global__ void __launch_bounds__(1024) norm_columns(const Columns c) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   const bool wanted[4] = {c.pre_gain_grad != nullptr, c.pre_layer && c.pre_shift_grad, c.post_gain_grad || c.gate_grad,
                           c.post_layer && (c.post_shift_grad || c.gate_grad)};
-  float v[4];
+  float v[4] = {};
+  if (col < c.d) {
+    for (int t0 = warp; t0 < c.teams; t0 += 32 * 5) {  // five teams' at once: 160 are all that SMs of one block have
+      float x[4][5];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    v[q] = 0.f;
-    if (!wanted[q] || col >= c.d) continue;
-    const float* from = c.sums + (long long)q * c.d + col;
-    for (int t0 = warp; t0 < c.teams; t0 += 32 * 8) {  // eight at once
-      float x[8];
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = t0 + 32 * i < c.teams ? __ldcg(from + (long long)(t0 + 32 * i) * 4 * c.d) : 0.f;
+        for (int i = 0; i < 5; ++i)
+          x[q][i] = wanted[q] && t0 + 32 * i < c.teams ? __ldcg(c.sums + ((long long)(t0 + 32 * i) * 4 + q) * c.d + col) : 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[q] += x[i];
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 5; ++i) v[q] += x[q][i];
     }
   }
 #pragma unroll
