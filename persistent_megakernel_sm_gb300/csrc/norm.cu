@@ -22,7 +22,7 @@ struct Forward {
 // Rows team, team + teams, ... of the tensors.
 // SAVE: 8-bit rows may be wanted; a kernel that cannot write them runs with fewer registers.
 template <typename R, bool VEC, bool PRE_LAYER, int POST, int CH, bool SAVE>
-__global__ void __launch_bounds__(kThreads, VEC ? 2 : 1) norm_forward(const __grid_constant__ Forward<R> f) {
+__global__ void __launch_bounds__(kThreads, VEC && !SAVE ? 2 : 1) norm_forward(const __grid_constant__ Forward<R> f) {
   extern __shared__ __align__(16) char smem[];
   const Shape& a = f.a;
   Team team(smem + a.parts);
@@ -250,7 +250,7 @@ int moe_norm_forward(const moe_norm_t* h, int T, int residual_type, const void* 
                      rows_aligned(f.norm) && rows_aligned(f.gate_rows) && aligned(f.out8.codes, 8) && aligned(f.y8.codes, 8);
     const int piece = vec ? 16 : 32, size = (int)sizeof(R) * 8 + (vec ? 0 : 16);
     const int bytes[5] = {size, y ? piece : 0, f.gate_rows.p ? piece : 0, 0, 0};
-    const Plan p = lay_out(&f.a, vec ? chunks_of(h->d, T, 2) : 1, kThreads, vec ? 2 * kThreads : kThreads, bytes,
+    const Plan p = lay_out(&f.a, vec ? chunks_of(h->d, T, 2) : 1, kThreads, vec && !out8 && !y8 ? 2 * kThreads : kThreads, bytes,
                            f.pre_shift ? 4 : f.post_shift ? 3 : 2, 1, vec);
     const int teams = std::min(T, kSms * p.per_sm / p.blocks);
     return by_kind(h, vec, p.chunks, [&](auto v, auto layer, auto post, auto c) {

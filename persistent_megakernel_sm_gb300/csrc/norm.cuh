@@ -309,18 +309,14 @@ __device__ __forceinline__ void store_rows8(const Rows8& r, int t, const Shape& 
   for (int i = 0; i < 8; ++i) most = max(most, moe::abs_bits(e.get(i)));
   for (int o = a.group_lanes >> 1; o; o >>= 1) most = max(most, __shfl_xor_sync(kAll, most, o));
   const bf16 s = moe::rows8_scale<T>(most);
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = e.get(i);
-  uint32_t word[2];
-  moe::rows8_codes<T>(v, s, word);
+  const uint2 word = moe::rows8_codes<T>(e.v, s);
   const int lane = threadIdx.x & 31;
   if constexpr (VEC) {
-    if (col < a.d) __stcs(reinterpret_cast<uint2*>(r.codes + (long long)t * a.d + col), make_uint2(word[0], word[1]));
+    if (col < a.d) __stcs(reinterpret_cast<uint2*>(r.codes + (long long)t * a.d + col), word);
   } else {
     const int lane_col = col - 7 * lane;
     __syncwarp();
-    reinterpret_cast<uint2*>(warp_row)[lane] = make_uint2(word[0], word[1]);
+    reinterpret_cast<uint2*>(warp_row)[lane] = word;
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 8; ++i)

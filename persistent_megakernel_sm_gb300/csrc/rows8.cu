@@ -78,9 +78,9 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) most = max(most, __shfl_xor_sync(mask, most, o));
     const __nv_bfloat16 s = moe::rows8_scale<T>(most);
-    uint32_t word[2];
-    moe::rows8_codes<T>(x[n], s, word);
-    __stcs(codes + i, make_uint2(word[0], word[1]));
+    const float2 two[4] = {make_float2(x[n][0], x[n][1]), make_float2(x[n][2], x[n][3]), make_float2(x[n][4], x[n][5]),
+                           make_float2(x[n][6], x[n][7])};
+    __stcs(codes + i, moe::rows8_codes<T>(two, s));
     if (i % kLanes == 0) scales[i / kLanes] = s;
   }
 }
@@ -128,22 +128,27 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = c0 + i * 32 + lane < cols ? to_float(from[c0 + i * 32 + lane]) : 0.f;
   constexpr int kSteps = G / 32;
+  uint32_t most[8 / kSteps];
 #pragma unroll
-  for (int i0 = 0; i0 < 8; i0 += kSteps) {
-    const int c = c0 + i0 * 32;
+  for (int i = 0; i < 8; ++i) {
+    uint32_t& m = most[i / kSteps];
+    m = i % kSteps ? max(m, moe::abs_bits(x[i])) : moe::abs_bits(x[i]);
+  }
+#pragma unroll
+  for (int g = 0; g < 8 / kSteps; ++g) most[g] = __reduce_max_sync(kAll, most[g]);
+#pragma unroll
+  for (int g = 0; g < 8 / kSteps; ++g) {
+    const int c = c0 + g * G;
     if (c >= cols) break;
-    uint32_t most = 0;
+    const __nv_bfloat16 s = moe::rows8_scale<T>(most[g]);
+    float in[8] = {};
 #pragma unroll
-    for (int i = i0; i < i0 + kSteps; ++i) most = max(most, moe::abs_bits(x[i]));
-    const __nv_bfloat16 s = moe::rows8_scale<T>(__reduce_max_sync(kAll, most));
-    float in[4] = {};
-    uint32_t word[1];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) in[i] = x[i0 + i];
-    moe::rows8_codes<T>(in, s, word);
+    for (int i = 0; i < kSteps; ++i) in[i] = x[g * kSteps + i];
+    const float2 two[4] = {make_float2(in[0], in[1]), make_float2(in[2], in[3]), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    const uint32_t word = moe::rows8_codes<T>(two, s).x;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-      if (c + i * 32 + lane < cols) codes[row * cols + c + i * 32 + lane] = (int8_t)(word[0] >> (8 * i));
+      if (c + i * 32 + lane < cols) codes[row * cols + c + i * 32 + lane] = (int8_t)(word >> (8 * i));
     if (lane == 0) scales[row * groups + c / G] = s;
   }
 }

@@ -108,3 +108,20 @@ def test_offsets_beyond_32_bits():
         back = torch.cat((v[:2], v[-2:])).float().cpu().numpy()
         assert np.array_equal(back, br.bf16(br.rows8_values(want_codes, want_scales, 128)))
         del v, codes, scales
+
+
+@pytest.mark.parametrize("kind", ["bfloat16", "float32"])
+@pytest.mark.parametrize("d", [128, 127])
+def test_quotients_next_to_halves(kind, d):
+    """Values a rounding from halfway between two codes, over scales of every mantissa and of many sizes."""
+    rng = np.random.default_rng(8)
+    rows = []
+    for i in range(400):
+        s = np.float32((128 + i % 128) / 128 * 2.0 ** rng.integers(-110, 100))
+        half = (rng.integers(-127, 127, d) + 0.5).astype(np.float32) * s
+        v = half.copy()
+        for _ in range(2):
+            v = np.where(rng.random(d) < 0.4, np.nextafter(v, rng.choice([-np.inf, np.inf], d).astype(np.float32)), v)
+        v[0] = 127 * s
+        rows.append(v)
+    check(np.array(rows), 128, kind)
