@@ -49,8 +49,7 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kMaxD = 32768;
 constexpr int kMaxT = 1 << 30;            // a row index and a few strides of the grid stay in 32 bits
-constexpr int kThreads = 512;            // of a block of the forward pass, at most
-constexpr int kGradThreads = 1024;       // of the gradient's
+constexpr int kThreads = 512;            // of a block, at most
 constexpr int kMaxStages = 4;            // rows under way
 constexpr int kSms = 152;
 constexpr int kRing = 200 * 1024;        // shared memory of an SM for all of it
@@ -564,7 +563,7 @@ Plan lay_out(Shape* a, int chunks, int block_threads, int sm_threads, const int 
 
 template <typename, bool, bool, int, int, bool>
 struct ForwardKernel;
-template <typename, bool, bool, int>
+template <typename, bool, bool, int, int>
 struct BackwardKernel;
 
 // Shared memory beyond 48 KB and clusters beyond 8 are asked for once a kernel and device.
@@ -613,7 +612,10 @@ namespace {
 
 // Rows that a gradient takes at once, at most: its teams.
 int most_teams(const moe_norm* h) {
-  return kSms * std::max(1, std::min(32, kGradThreads / (((h->d + 7) / 8 + 31) / 32 * 32)));
+  int most = kSms;
+  for (int chunks = 1; chunks <= 2; ++chunks)
+    most = std::max(most, kSms * std::min(32, kThreads / (((h->d + 8 * chunks - 1) / (8 * chunks) + 31) / 32 * 32)));
+  return most;
 }
 
 Shape shape_of(const moe_norm* h, int T) {
@@ -630,10 +632,12 @@ Shape shape_of(const moe_norm* h, int T) {
 }
 
 // Eights of a lane.  What a row costs a thread beside its columns (the exchanges, the
-// root) is shared by more of them; with few rows more threads are sooner done.
+// root, finding its tensors) is shared by two of them (8192 x 4096, gradient: 108 us
+// with one, 95 with two); with few rows more threads are sooner done (512 x 4096: 16.1
+// and 17.7), unless a second block would have to join them (1024 x 16384: 150 and 73).
 int chunks_of(int d, int T, int most) {
-  if (T <= 2 * kSms) return 1;
   const int lanes = (d + 7) / 8;
+  if (T <= 2 * kSms || (T <= 8 * kSms && lanes <= kThreads)) return 1;
   int c = 1;
   while (c < most && c * 32 < lanes) c *= 2;
   return c;

@@ -28,22 +28,23 @@ enum { kTU, kUV, kXV, kT, kV, kUW, kXW, kW, kUB, kXB, kB, kSums };
 // Fours of them that a row has: kTU, kUV and kXV, with layer norms up to all.
 __host__ __device__ constexpr int quads_of(bool pre_layer, int post) { return pre_layer || post == kLayer ? 3 : 1; }
 
-// A lane has one eight, so that a block's warps are many and what they keep from row to
-// row, the sums over rows, leaves them room: a row is read from its slots again once
-// its sums are known.
-template <typename R, bool VEC, bool PRE_LAYER, int POST>
-__global__ void __launch_bounds__(kGradThreads) norm_backward(const __grid_constant__ Backward<R> f) {
+// What a thread keeps from row to row, the sums over rows, takes most of its registers:
+// a row is read from its slots again once its sums are known.
+template <typename R, bool VEC, bool PRE_LAYER, int POST, int CH>
+__global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant__ Backward<R> f) {
   extern __shared__ __align__(16) char smem[];
   constexpr int quads = quads_of(PRE_LAYER, POST);
   constexpr bool POST_LAYER = POST == kLayer;
   const Shape& a = f.a;
   Team team(smem + a.parts);
-  const int tid = threadIdx.x, units = blockDim.x;
+  const int tid = threadIdx.x, threads = blockDim.x, units = CH * threads;
   const int first = blockIdx.x / team.blocks, step = gridDim.x / team.blocks;
   float* warp_row = reinterpret_cast<float*>(smem + a.out) + (tid >> 5) * 256;
   const Kept kept{reinterpret_cast<float4*>(smem + a.vec), units};
   const float inv_d = 1.f / (float)a.d;
-  const int col = (team.rank * units + tid) * 8, n = max(0, min(8, a.d - col));
+  int cols[CH], ns[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) cols[c] = (team.rank * units + c * threads + tid) * 8, ns[c] = max(0, min(8, a.d - cols[c]));
   const bool has_y = f.y.p || f.y8.codes, has_norm = f.grad_norm.p != nullptr;
   const bool token_shift = POST_LAYER && f.grad_gate_tokens && f.post_shift;
 
@@ -52,34 +53,41 @@ __global__ void __launch_bounds__(kGradThreads) norm_backward(const __grid_const
   begin(a, team, smem, team.blocks * units * 8);
   auto start = [&](int t, char* slot) {
     if (t < a.T) {
-      if (f.grad_out.p) fetch<R, VEC>(slot + a.field[0], units, tid, f.grad_out.at(t), col, a.d);
-      if (has_norm) {
-        fetch<bf16, VEC>(slot + a.field[1], units, tid, f.grad_norm.at(t), col, a.d);
-        if (f.out8.codes) fetch8<VEC>(slot + a.field[2], units, tid, f.out8, t, a, col);
-        else fetch<R, VEC>(slot + a.field[2], units, tid, f.kept_out.at(t), col, a.d);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int unit = c * threads + tid, col = cols[c];
+        if (f.grad_out.p) fetch<R, VEC>(slot + a.field[0], units, unit, f.grad_out.at(t), col, a.d);
+        if (has_norm) {
+          fetch<bf16, VEC>(slot + a.field[1], units, unit, f.grad_norm.at(t), col, a.d);
+          if (f.out8.codes) fetch8<VEC>(slot + a.field[2], units, unit, f.out8, t, a, col);
+          else fetch<R, VEC>(slot + a.field[2], units, unit, f.kept_out.at(t), col, a.d);
+        }
+        if (f.y8.codes) fetch8<VEC>(slot + a.field[3], units, unit, f.y8, t, a, col);
+        else if (f.y.p) fetch<bf16, VEC>(slot + a.field[3], units, unit, f.y.at(t), col, a.d);
+        if (f.gate_rows.p) fetch<bf16, VEC>(slot + a.field[4], units, unit, f.gate_rows.at(t), col, a.d);
       }
-      if (f.y8.codes) fetch8<VEC>(slot + a.field[3], units, tid, f.y8, t, a, col);
-      else if (f.y.p) fetch<bf16, VEC>(slot + a.field[3], units, tid, f.y.at(t), col, a.d);
-      if (f.gate_rows.p) fetch<bf16, VEC>(slot + a.field[4], units, tid, f.gate_rows.at(t), col, a.d);
     }
     moe::cp_async_commit();
   };
   for (int i = 0; i < a.stages; ++i) start(first + i * step, smem + i * a.stage);
 
-  {  // 0: the pre norm's gain, 1: the post norm's with the gate's columns, 2: its shift
-    kept.write(0, tid, load_params(f.pre_gain, f.params_f32, col, n, 1.f, a.one));
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {  // 0: the pre norm's gain, 1: the post norm's with the gate's columns, 2: its shift
+    const int unit = c * threads + tid, col = cols[c], n = ns[c];
+    kept.write(0, unit, load_params(f.pre_gain, f.params_f32, col, n, 1.f, a.one));
     Eight w = load_params(f.post_gain, f.params_f32, col, n, 1.f, a.one);
     const Eight gate = load_params(f.gate_columns, f.params_f32, col, n, 1.f, 0.f);
 #pragma unroll
     for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], gate.v[j]);
-    kept.write(1, tid, w);
-    if (POST_LAYER && f.post_shift) kept.write(2, tid, load_params(f.post_shift, f.params_f32, col, n, 0.f, 0.f));
+    kept.write(1, unit, w);
+    if (POST_LAYER && f.post_shift) kept.write(2, unit, load_params(f.post_shift, f.params_f32, col, n, 0.f, 0.f));
   }
 
   // u of the pre norm, and of the post norm (y itself where there is none)
-  auto read_x = [&](const char* slot, int t, const float4& st) {
-    Eight x = f.out8.codes ? read8<VEC>(slot + a.field[2], units, tid, f.out8, t, a, col, n)
-                           : read<R, VEC>(slot + a.field[2], units, tid, f.kept_out.at(t), n);
+  auto read_x = [&](const char* slot, int t, const float4& st, int c) {
+    const int unit = c * threads + tid, col = cols[c], n = ns[c];
+    Eight x = f.out8.codes ? read8<VEC>(slot + a.field[2], units, unit, f.out8, t, a, col, n)
+                           : read<R, VEC>(slot + a.field[2], units, unit, f.kept_out.at(t), n);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (PRE_LAYER) x.v[j] = add2(x.v[j], two(-st.z));
@@ -88,9 +96,10 @@ __global__ void __launch_bounds__(kGradThreads) norm_backward(const __grid_const
     if (PRE_LAYER && n < 8) x.cut(n);  // 0 - mean behind the row's end
     return x;
   };
-  auto read_y = [&](const char* slot, int t, const float4& st) {
-    Eight y = f.y8.codes ? read8<VEC>(slot + a.field[3], units, tid, f.y8, t, a, col, n)
-                         : read<bf16, VEC>(slot + a.field[3], units, tid, f.y.at(t), n);
+  auto read_y = [&](const char* slot, int t, const float4& st, int c) {
+    const int unit = c * threads + tid, col = cols[c], n = ns[c];
+    Eight y = f.y8.codes ? read8<VEC>(slot + a.field[3], units, unit, f.y8, t, a, col, n)
+                         : read<bf16, VEC>(slot + a.field[3], units, unit, f.y.at(t), n);
     if (POST != kNone) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -103,7 +112,7 @@ __global__ void __launch_bounds__(kGradThreads) norm_backward(const __grid_const
   };
   const Eight nothing{};
 
-  Eight acc_tu = nothing, acc_t = nothing, acc_v = nothing, acc_g = nothing;
+  Eight acc_tu[CH]{}, acc_t[PRE_LAYER ? CH : 1]{}, acc_v[CH]{}, acc_g[POST_LAYER ? CH : 1]{};
   const bool sums_post = POST != kNone || f.grad_gate_tokens;
   char* slot = smem;
   const float4 no_norms = make_float4(0.f, 1.f, 0.f, 1.f);
@@ -127,46 +136,50 @@ __global__ void __launch_bounds__(kGradThreads) norm_backward(const __grid_const
       auto more = [&](int q, float2 p, float2 v) {
         if (q < 4 * quads) sum[q < 4 * quads ? q : 0] = fma2(p, v, sum[q < 4 * quads ? q : 0]);
       };
-      Eight go = f.grad_out.p ? read<R, VEC>(slot + a.field[0], units, tid, f.grad_out.at(t), n) : nothing, x = nothing;
-      if (has_norm) {  // go: grad_out + rstd t
-        x = read_x(slot, t, st);
-        const Eight gn = read<bf16, VEC>(slot + a.field[1], units, tid, f.grad_norm.at(t), n), k = kept.read(0, tid);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 tj = mul2(gn.v[j], k.v[j]);
-          more(kTU, tj, x.v[j]);
-          if (PRE_LAYER) more(kT, tj, two(1.f));
-          go.v[j] = fma2(tj, two(st.w), go.v[j]);
-        }
-      }
-      if (sums_post) {
-        Eight w = kept.read(1, tid);
-        const Eight y = read_y(slot, t, st);
-        if (f.gate_rows.p) {
-          const Eight g = read<bf16, VEC>(slot + a.field[4], units, tid, f.gate_rows.at(t), n);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], g.v[j]);
-        }
-        if (PRE_LAYER && n < 8) w.cut(n);  // a gain of 1 behind the row's end
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 v = mul2(y.v[j], w.v[j]);
-          more(kUV, go.v[j], v);
-          more(kXV, x.v[j], v);
-          if (PRE_LAYER) more(kV, v, two(1.f));
-          if (POST_LAYER) {
-            more(kUW, go.v[j], w.v[j]);
-            more(kXW, x.v[j], w.v[j]);
-            if (PRE_LAYER) more(kW, w.v[j], two(1.f));
-          }
-        }
-        if (token_shift) {
-          const Eight b = kept.read(2, tid);
+      for (int c = 0; c < CH; ++c) {
+        const int unit = c * threads + tid, n = ns[c];
+        Eight go = f.grad_out.p ? read<R, VEC>(slot + a.field[0], units, unit, f.grad_out.at(t), n) : nothing, x = nothing;
+        if (has_norm) {  // go: grad_out + rstd t
+          x = read_x(slot, t, st, c);
+          const Eight gn = read<bf16, VEC>(slot + a.field[1], units, unit, f.grad_norm.at(t), n), k = kept.read(0, unit);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            more(kUB, go.v[j], b.v[j]);
-            more(kXB, x.v[j], b.v[j]);
-            if (PRE_LAYER) more(kB, b.v[j], two(1.f));
+            const float2 tj = mul2(gn.v[j], k.v[j]);
+            more(kTU, tj, x.v[j]);
+            if (PRE_LAYER) more(kT, tj, two(1.f));
+            go.v[j] = fma2(tj, two(st.w), go.v[j]);
+          }
+        }
+        if (sums_post) {
+          Eight w = kept.read(1, unit);
+          const Eight y = read_y(slot, t, st, c);
+          if (f.gate_rows.p) {
+            const Eight g = read<bf16, VEC>(slot + a.field[4], units, unit, f.gate_rows.at(t), n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w.v[j] = mul2(w.v[j], g.v[j]);
+          }
+          if (PRE_LAYER && n < 8) w.cut(n);  // a gain of 1 behind the row's end
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = mul2(y.v[j], w.v[j]);
+            more(kUV, go.v[j], v);
+            more(kXV, x.v[j], v);
+            if (PRE_LAYER) more(kV, v, two(1.f));
+            if (POST_LAYER) {
+              more(kUW, go.v[j], w.v[j]);
+              more(kXW, x.v[j], w.v[j]);
+              if (PRE_LAYER) more(kW, w.v[j], two(1.f));
+            }
+          }
+          if (token_shift) {
+            const Eight b = kept.read(2, unit);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              more(kUB, go.v[j], b.v[j]);
+              more(kXB, x.v[j], b.v[j]);
+              if (PRE_LAYER) more(kB, b.v[j], two(1.f));
+            }
           }
         }
       }
@@ -189,62 +202,66 @@ __global__ void __launch_bounds__(kGradThreads) norm_backward(const __grid_const
     const float m1 = e1 * gate_t * inv_d, m2 = POST_LAYER ? a.scale * gate_t * of(kUW, kXW, kW) * inv_d : 0.f;
     if (f.grad_gate_tokens && team.rank == 0 && tid == 0)
       f.grad_gate_tokens[t] = e1 + (token_shift ? a.scale * of(kUB, kXB, kB) : 0.f);
-    Eight g = f.grad_out.p ? read<R, VEC>(slot + a.field[0], units, tid, f.grad_out.at(t), n) : nothing;
-    if (has_norm) {
-      const Eight x = read_x(slot, t, st);
-      const Eight gn = read<bf16, VEC>(slot + a.field[1], units, tid, f.grad_norm.at(t), n), k = kept.read(0, tid);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc_tu.v[j] = fma2(gn.v[j], x.v[j], acc_tu.v[j]);
-        if (PRE_LAYER) acc_t.v[j] = add2(gn.v[j], acc_t.v[j]);
-        float2 v = fma2(x.v[j], two(-c1), mul2(gn.v[j], k.v[j]));
-        if (PRE_LAYER) v = add2(v, two(-c2));
-        g.v[j] = fma2(v, two(st.w), g.v[j]);
-      }
-    }
-    if (f.grad_residual.p) store_row<VEC>(f.grad_residual.at(t), g, col, a.d, warp_row);
-    if (has_y || f.grad_y.p) {
-      const Eight w = kept.read(1, tid), y = has_y ? read_y(slot, t, st) : nothing;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], two(a.scale * gate_t));  // from here on s g G, but for the gates below
-      if (f.gate_rows.p) {
-        if (f.grad_gate_rows.p) {  // s G p
-          Eight p;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) p.v[j] = mul2(y.v[j], w.v[j]);
-          if (POST_LAYER && f.post_shift) {
-            const Eight b = kept.read(2, tid);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p.v[j] = add2(p.v[j], b.v[j]);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) p.v[j] = mul2(p.v[j], g.v[j]);
-          store_row<VEC>(f.grad_gate_rows.at(t), p, col, a.d, warp_row);
-        }
-        const Eight gate = read<bf16, VEC>(slot + a.field[4], units, tid, f.gate_rows.at(t), n);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], gate.v[j]);
-      }
-      // a gate of columns is put on the sums over rows, and its gradient taken from
-      // them, at the end: here without it
-      if (has_y) {
+    for (int c = 0; c < CH; ++c) {
+      const int unit = c * threads + tid, col = cols[c], n = ns[c];
+      Eight g = f.grad_out.p ? read<R, VEC>(slot + a.field[0], units, unit, f.grad_out.at(t), n) : nothing;
+      if (has_norm) {
+        const Eight x = read_x(slot, t, st, c);
+        const Eight gn = read<bf16, VEC>(slot + a.field[1], units, unit, f.grad_norm.at(t), n), k = kept.read(0, unit);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          acc_v.v[j] = fma2(g.v[j], y.v[j], acc_v.v[j]);
-          if (POST_LAYER) acc_g.v[j] = add2(g.v[j], acc_g.v[j]);
+          acc_tu[c].v[j] = fma2(gn.v[j], x.v[j], acc_tu[c].v[j]);
+          if (PRE_LAYER) acc_t[PRE_LAYER ? c : 0].v[j] = add2(gn.v[j], acc_t[PRE_LAYER ? c : 0].v[j]);
+          float2 v = fma2(x.v[j], two(-c1), mul2(gn.v[j], k.v[j]));
+          if (PRE_LAYER) v = add2(v, two(-c2));
+          g.v[j] = fma2(v, two(st.w), g.v[j]);
         }
       }
-      if (f.grad_y.p) {
+      if (f.grad_residual.p) store_row<VEC>(f.grad_residual.at(t), g, col, a.d, warp_row);
+      if (has_y || f.grad_y.p) {
+        const Eight w = kept.read(1, unit), y = has_y ? read_y(slot, t, st, c) : nothing;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          g.v[j] = mul2(g.v[j], w.v[j]);
-          if (POST != kNone) {
-            g.v[j] = fma2(y.v[j], two(-m1), g.v[j]);
-            if (POST_LAYER) g.v[j] = add2(g.v[j], two(-m2));
-            g.v[j] = mul2(g.v[j], two(st.y));
+        for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], two(a.scale * gate_t));  // from here on s g G, but for the gates below
+        if (f.gate_rows.p) {
+          if (f.grad_gate_rows.p) {  // s G p
+            Eight p;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p.v[j] = mul2(y.v[j], w.v[j]);
+            if (POST_LAYER && f.post_shift) {
+              const Eight b = kept.read(2, unit);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) p.v[j] = add2(p.v[j], b.v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p.v[j] = mul2(p.v[j], g.v[j]);
+            store_row<VEC>(f.grad_gate_rows.at(t), p, col, a.d, warp_row);
+          }
+          const Eight gate = read<bf16, VEC>(slot + a.field[4], units, unit, f.gate_rows.at(t), n);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) g.v[j] = mul2(g.v[j], gate.v[j]);
+        }
+        // a gate of columns is put on the sums over rows, and its gradient taken from
+        // them, at the end: here without it
+        if (has_y) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc_v[c].v[j] = fma2(g.v[j], y.v[j], acc_v[c].v[j]);
+            if (POST_LAYER) acc_g[POST_LAYER ? c : 0].v[j] = add2(g.v[j], acc_g[POST_LAYER ? c : 0].v[j]);
           }
         }
-        store_row<VEC>(f.grad_y.at(t), g, col, a.d, warp_row);
+        if (f.grad_y.p) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            g.v[j] = mul2(g.v[j], w.v[j]);
+            if (POST != kNone) {
+              g.v[j] = fma2(y.v[j], two(-m1), g.v[j]);
+              if (POST_LAYER) g.v[j] = add2(g.v[j], two(-m2));
+              g.v[j] = mul2(g.v[j], two(st.y));
+            }
+          }
+          store_row<VEC>(f.grad_y.at(t), g, col, a.d, warp_row);
+        }
       }
     }
     start(t + a.stages * step, slot);
@@ -253,14 +270,17 @@ __global__ void __launch_bounds__(kGradThreads) norm_backward(const __grid_const
   }
 
   if (!f.sums) return;
-  float* to = f.sums + (long long)first * 4 * a.d + col;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (j >= n) break;
-    to[j] = acc_tu.get(j);
-    if (PRE_LAYER) to[a.d + j] = acc_t.get(j);
-    to[2 * a.d + j] = acc_v.get(j);
-    if (POST_LAYER) to[3 * a.d + j] = acc_g.get(j);
+  for (int c = 0; c < CH; ++c) {
+    float* to = f.sums + (long long)first * 4 * a.d + cols[c];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= ns[c]) break;
+      to[j] = acc_tu[c].get(j);
+      if (PRE_LAYER) to[a.d + j] = acc_t[PRE_LAYER ? c : 0].get(j);
+      to[2 * a.d + j] = acc_v[c].get(j);
+      if (POST_LAYER) to[3 * a.d + j] = acc_g[POST_LAYER ? c : 0].get(j);
+    }
   }
 }
 
@@ -417,16 +437,16 @@ int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void*
     const int piece = vec ? 16 : 32, size = (int)sizeof(R) * 8 + (vec ? 0 : 16), codes = vec ? 16 : 32;
     const int bytes[5] = {grad_out ? size : 0, has_norm ? piece : 0, !has_norm ? 0 : f.out8.codes ? codes : size,
                           f.y8.codes ? codes : f.y.p ? piece : 0, f.gate_rows.p ? piece : 0};
-    const Plan p = lay_out(&f.a, 1, kGradThreads, kGradThreads, bytes, f.post_shift ? 3 : 2,
+    const Plan p = lay_out(&f.a, vec ? chunks_of(h->d, T, 2) : 1, kThreads, kThreads, bytes, f.post_shift ? 3 : 2,
                            quads_of(h->pre == kLayer, h->post), vec);
     // what a team keeps of its rows is written and read once more: 8 rows at least,
     // unless that leaves SMs idle
     teams = std::min({T, kSms * p.per_sm / p.blocks, most_teams(h), std::max(kSms / p.blocks, T / 8)});
-    return by_kind(h, vec, 1, [&](auto v, auto layer, auto post, auto) {
+    return by_kind(h, vec, p.chunks, [&](auto v, auto layer, auto post, auto c) {
       constexpr bool VEC = decltype(v)::value, LAYER = decltype(layer)::value;
-      constexpr int POST = decltype(post)::value;
-      auto* kernel = norm_backward<R, VEC, LAYER, POST>;
-      cudaError_t e = allow_smem<BackwardKernel<R, VEC, LAYER, POST>>(kernel);
+      constexpr int POST = decltype(post)::value, CH = decltype(c)::value;
+      auto* kernel = norm_backward<R, VEC, LAYER, POST, CH>;
+      cudaError_t e = allow_smem<BackwardKernel<R, VEC, LAYER, POST, CH>>(kernel);
       return e == cudaSuccess ? launch(kernel, (unsigned)(teams * p.blocks), p.blocks, p.threads, p.smem, s, f) : e;
     });
   };
