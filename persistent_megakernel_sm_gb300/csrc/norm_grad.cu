@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
   const Eight nothing{};
 
   Eight acc_tu[CH]{}, acc_t[PRE_LAYER ? CH : 1]{}, acc_v[CH]{}, acc_g[POST_LAYER ? CH : 1]{};
-  const bool sums_post = POST != kNone || f.grad_gate_tokens;
+  const bool sums_post = has_y && (POST != kNone || f.grad_gate_tokens);
   char* slot = smem;
   const float4 no_norms = make_float4(0.f, 1.f, 0.f, 1.f);
   // a row's numbers, a row ahead

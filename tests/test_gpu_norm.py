@@ -402,3 +402,61 @@ def test_offsets_beyond_32_bits():
     wide[:, :d], wide[:, d:2 * d] = r, y
     n.forward(wide[:, :d], wide[:, d:2 * d], wide[:, 2 * d:3 * d], wide[:, 3 * d:4 * d], pre_gain=g)
     assert torch.equal(wide[:, 2 * d:3 * d], want[0]) and torch.equal(wide[:, 3 * d:4 * d], want[1])
+
+
+@pytest.mark.parametrize("d,pad", [(264, 0), (77, 3), (4104, 0)])
+@pytest.mark.parametrize("post,gate", [("rms", "none"), ("layer", "token"), ("none", "element")])
+def test_the_residuals_gradient_needs_nothing_of_the_block(d, pad, post, gate):
+    """Without y: the gradients that go on through the residual stream, and the pre norm's."""
+    got = Case(6, d, "layer", post, gate, pad=pad).check_backward(drop=("y", "gate"))
+    assert set(got) == {"residual", "pre_gain", "pre_shift"}
+
+
+def test_a_first_call_may_be_captured():
+    """Kernels that no call has used before, in a graph at once."""
+    import torch
+    c = Case(5, 72, "layer", "rms", "element", res="float32", offset=True)
+    want = c.forward()
+    fresh = Case(5, 70, "layer", "layer", "token", res="float32", offset=True, pad=2, seed=3)
+    n = fresh.make()
+    n.reserve()
+    p = fresh.params()
+    r, y = Wide(5, 70, "float32", 2).fill(fresh.residual, "float32"), Wide(5, 70, "bfloat16", 2).fill(fresh.y, "bfloat16")
+    out, norm, stats = Wide(5, 70, "float32", 2), Wide(5, 70, "bfloat16", 2), torch.empty(5, 4, device="cuda")
+    gr, gain = Wide(5, 70, "float32", 2), torch.empty(70, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        n.forward(r.rows, y.rows, out.rows, norm.rows, **p, stats=stats)
+        n.backward(out.rows, norm.rows, gr.rows, None, stats=stats, out=out.rows, y=y.rows, **p, grad_pre_gain=gain)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [host(t) for t in (out.rows, norm.rows, gr.rows, gain)]
+    for t in (out.rows, norm.rows, gr.rows, gain):
+        t.zero_()
+    n.forward(r.rows, y.rows, out.rows, norm.rows, **p, stats=stats)
+    n.backward(out.rows, norm.rows, gr.rows, None, stats=stats, out=out.rows, y=y.rows, **p, grad_pre_gain=gain)
+    assert all(np.array_equal(a, host(b)) for a, b in zip(got, (out.rows, norm.rows, gr.rows, gain)))
+    assert np.all(np.isfinite(want["norm"]))
+
+
+@pytest.mark.parametrize("d", [64, 1000, 4104])
+def test_two_streams_share_a_handle_forward(d):
+    """The handle holds settings alone in the forward pass: calls at once on two streams have their own rows' results."""
+    import torch
+    cases = [Case(300, d, "layer", "rms", "channel", seed=i) for i in range(2)]
+    n = cases[0].make()
+    p = cases[0].params()
+    ins = [[dev(c.residual, "bfloat16"), dev(c.y, "bfloat16")] for c in cases]
+    want = []
+    for r, y in ins:
+        want.append([torch.empty_like(r) for _ in range(2)])
+        n.forward(r, y, *want[-1], **p)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[torch.empty_like(t) for t in w] for w in want]
+    for _ in range(20):
+        for s, (r, y), g in zip(streams, ins, got):
+            n.forward(r, y, *g, **p, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
