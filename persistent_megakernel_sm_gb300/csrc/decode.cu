@@ -10,21 +10,26 @@
 //      h' = w silu(Wg x) (Wu x) for its share of the experts' f rows   grid-wide wait
 //   3  out = sum over the listed experts of Wd h' for its share of the d rows: no
 //      block needs another's sums, so there is no combine
-// A product's tile is 32 weight rows (16 of gate and 16 of up) times 8 or 16 token
-// columns on mma.sync m16n8k16.  The tensor cores are nearly idle here; they are used
-// because a multiply-add for every weight and token would not keep up with HBM.  A
-// stage is 512 or 1024 columns of a tile and of the tokens that its expert has.  Four warps of
-// a block bring its weights by bulk copies, four more the tokens' columns, into a ring of
-// single rows (160 to 180 KB an SM on their way, whatever a stage has of them); the
-// weights do not wait for the grid, so the ring is full of down's first ones when h' is
-// complete.  Eight warps, in teams that take stages by turns, multiply, and their sums
-// meet in shared memory once a tile.  A lane reads 16 bytes of a row at once, which the
-// mma sees as another order of the same columns, the same for the tokens'.
+// A product's tile is up to 32 weight rows (16 of gate and 16 of up) times 8 or 16
+// token columns on mma.sync m16n8k16.  The tensor cores are nearly idle here; they are
+// used because a multiply-add for every weight and token would not keep up with HBM.  A
+// stage is 1024 columns of a tile and of the tokens that its expert has.  Four warps of
+// a block bring its weights by bulk copies, four more the tokens' columns, into a ring
+// of single rows (182 KB an SM, two stages at least on their way); the weights do not
+// wait for the grid, so the ring is full of down's first ones when h' is complete.
+// Eight warps multiply, each an eighth of a stage's columns, and their sums meet in
+// shared memory once a tile.  A lane reads 16 bytes of a row at once, which the mma sees
+// as another order of the same columns, the same for the tokens'.
 //
-// Columns are the tokens themselves.  A token that did not choose an expert has a
-// zero column there and takes nothing from its sums, which are kept apart expert by
+// HBM bounds it: 4 tokens of 32 + 1 experts of 7168 x 2048 take 299 us (6.77 TB/s, the
+// copy rate), 4 of eight experts of 4096 x 14336 6.7 TB/s, 13 to 16 tokens 6.0 to 6.3.
+// One token of 128 experts of 2048 x 768 (76 MB, 11 us) takes 25: the two waits of the
+// grid 1.1 each, logits and choice 5, and streams that end before they are at speed.
+//
+// Down's columns are the tokens themselves.  A token that did not choose an expert has
+// a zero column there and takes nothing from its sums, which are kept apart expert by
 // expert, so an infinity or a NaN in weights that a token did not choose does not
-// reach it.  Sums are fp32, over at most 128 columns in the tensor cores and from
+// reach it.  Gate and up's, whose tile has one expert, are that expert's tokens.  Sums are fp32, over at most 128 columns in the tensor cores and from
 // there on rounded to nearest.  h' is held as the sum of two bf16 numbers, 16 bits
 // in all: its rounding does not show in the output's, and costs one more mma on
 // weights that are there anyway.
@@ -47,12 +52,18 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kMaxT = 16, kMaxK = 16, kMaxE = 256, kMaxD = 32768;
 constexpr int kWarps = 8, kConsumers = kWarps * 32;
-constexpr int kTeams = 1, kTeam = kWarps / kTeams;
 constexpr int kBringers = 4;     // warps that bring weights, and as many that bring tokens
 constexpr int kThreads = kConsumers + 2 * kBringers * 32;
 constexpr int kBlock = 32;       // columns of two mma
 constexpr int kRows = 32;        // of a tile: gate and up 16 each
 constexpr int kColumn = 36;      // floats of a token's column of sums: 32, and 4 so that its lanes miss each other's banks
+// Columns of a stage.  A stage costs the warps that bring and use it several hundred
+// cycles whatever it holds, so longer is better: 4 tokens of 128 experts of 2048 x 768
+// 76 us with 512, 65 with 1024, 16 tokens 196 and 159.
+constexpr int kChunk = 1024;
+constexpr int kBlocks = kChunk / kBlock / kWarps;  // of a warp
+constexpr int kPitch = kChunk * 2 + 64;  // bytes of a row: two rows next to each other use all banks
+constexpr int kRing = 86;        // rows of the ring: 182 KB
 constexpr int kStages = 16;      // on their way, at most
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint64_t kLimitNs = 2000000000ull;
@@ -260,14 +271,6 @@ struct Sums {
 
 template <int NT>
 struct Smem {
-  // Columns of a stage.  A stage costs the warps that bring and use it several hundred
-  // cycles whatever it holds, so longer is better (4 tokens of 128 experts of 2048 x
-  // 768: 76 us with 512, 65 with 1024), as long as the ring holds a few stages with
-  // all the tokens' rows (13 tokens of 32 + 1 experts of 7168 x 2048: 524 and 689).
-  static constexpr int kChunk = 1024;
-  static constexpr int kBlocks = kChunk / kBlock / kTeam;  // of a warp
-  static constexpr int kPitch = kChunk * 2 + 64;  // bytes of a row: two rows next to each other use all banks
-  static constexpr int kRing = 86;  // rows; a stage has 64 at most
   char ring[kRing][kPitch];
   Sums<NT> sums;
   List list;
@@ -276,16 +279,15 @@ struct Smem {
 };
 
 // Where one side of the ring stands: the stage's barriers and its first row.
-template <int RING>
 struct At {
   int stage = 0, row = 0;
   uint32_t parity = 0;
   __device__ __forceinline__ void next(int rows) {
     if (++stage == kStages) stage = 0, parity ^= 1;
     row += rows;
-    if (row >= RING) row -= RING;
+    if (row >= kRing) row -= kRing;
   }
-  __device__ __forceinline__ int at(int i) const { return row + i >= RING ? row + i - RING : row + i; }
+  __device__ __forceinline__ int at(int i) const { return row + i >= kRing ? row + i - kRing : row + i; }
 };
 
 // A bringing warp's view of what is free: a stage's rows are the consumers' until its
@@ -294,7 +296,7 @@ template <int NT>
 struct Room {
   Smem<NT>* sm;
   uint64_t deadline;
-  At<Smem<NT>::kRing> at;        // of the next stage
+  At at;        // of the next stage
   int oldest = 0, out = 0, used = 0;
   uint32_t oldest_parity = 0;
   int rows_of = 0;               // lane i: rows of the stage on barriers i
@@ -309,7 +311,7 @@ struct Room {
   }
   // room for a stage of `rows`; false if the wait ran out
   __device__ __forceinline__ bool make(int rows) {
-    while (used + rows > Smem<NT>::kRing || out == kStages) {
+    while (used + rows > kRing || out == kStages) {
       if (!wait(&sm->empty[oldest], oldest_parity)) return false;
       used -= __shfl_sync(kAll, rows_of, oldest);
       --out;
@@ -370,12 +372,11 @@ struct Stage {
 // `abort`; no barrier of the block is left out.
 template <int NT>
 struct Consumer {
-  static constexpr int kBlocks = Smem<NT>::kBlocks;
   Smem<NT>* sm;
   uint64_t deadline;
   int* status;
-  At<Smem<NT>::kRing> at;
-  int turn = 0, tile = 0;   // the team whose stage is next; tiles so far
+  At at;
+  int tile = 0;  // tiles so far
   bool fine = true;
   float total[NT][2][4];
 
@@ -394,7 +395,7 @@ struct Consumer {
   template <int PARTS, int M>
   __device__ __forceinline__ void multiply(const Stage& st, int hi, int tokens_before, uint32_t tokens, int n, float (&sum)[2][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int in_row = t * 16 + threadIdx.x / 32 % kTeam * (kBlocks * kBlock * 2);
+    const int in_row = t * 16 + threadIdx.x / 32 * (kBlocks * kBlock * 2);
     const char* b_rows[PARTS];
     const bool on = tokens >> g & 1;
 #pragma unroll
@@ -403,8 +404,6 @@ struct Consumer {
     float part[M][PARTS][2][4] = {};
 #pragma unroll
     for (int u = 0; u < kBlocks; ++u) {
-      // columns come in multiples of 128
-      if (u % 4 == 0 && u > 0 && (threadIdx.x / 32 % kTeam * kBlocks + u) * kBlock >= st.columns) break;
       uint4 b[PARTS];
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
@@ -438,22 +437,19 @@ struct Consumer {
   __device__ __forceinline__ void stage(const Stage& st, int hi) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = __popc(st.tokens);
-    if (turn == warp / kTeam) {
-      fine = fine && moe::mbar_wait(&sm->full[at.stage], at.parity, deadline);
-      if (warp % kTeam * (kBlocks * kBlock) < st.columns) {
-        int before = 0;
+    fine = fine && moe::mbar_wait(&sm->full[at.stage], at.parity, deadline);
+    if (warp * (kBlocks * kBlock) < st.columns) {  // a warp's 128 columns are all there or none
+      int before = 0;
 #pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          const uint32_t tokens = (PARTS == 1 ? (1u << n) - 1u : (uint32_t)st.tokens) >> (8 * q) & 0xffu;
-          if (NT == 1 || tokens) multiply<PARTS, M>(st, hi, before, tokens, n, total[q]);
-          before += __popc(tokens);
-        }
+      for (int q = 0; q < NT; ++q) {
+        const uint32_t tokens = (PARTS == 1 ? (1u << n) - 1u : (uint32_t)st.tokens) >> (8 * q) & 0xffu;
+        if (NT == 1 || tokens) multiply<PARTS, M>(st, hi, before, tokens, n, total[q]);
+        before += __popc(tokens);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->empty[at.stage]);
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm->empty[at.stage]);
     at.next(st.rows + PARTS * n);
-    if (++turn == kTeams) turn = 0;
   }
 
   // The warps' sums together: end(row, column, sum), all threads at once.
@@ -543,14 +539,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   extern __shared__ __align__(128) char smem_raw[];
   Smem<NT>* sm = reinterpret_cast<Smem<NT>*>(smem_raw);
   List* list = &sm->list;
-  constexpr int kChunk = Smem<NT>::kChunk;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int block = blockIdx.x, blocks = gridDim.x;
   const uint64_t deadline = moe::globaltimer() + kLimitNs;
   const bool producer = warp >= kWarps;
   if (tid < kStages) {
     moe::mbar_init(&sm->full[tid], kBringers + kBringers * 32);
-    moe::mbar_init(&sm->empty[tid], kTeam);
+    moe::mbar_init(&sm->empty[tid], kWarps);
     if (tid == 0) moe::mbar_init(&sm->h_ready, 1);
     moe::fence_mbar_init();
   }

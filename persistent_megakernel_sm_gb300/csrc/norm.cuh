@@ -26,6 +26,15 @@
 // the block's warps twice a row, a layer norm once more for each norm (the mean first,
 // then the squares about it); the gradient once.  Sums over rows are kept in
 // registers, written once a block and added by a second kernel in a fixed order.
+//
+// 8192 x 7168 in bf16, root mean squares on both sides, fp32 gains, a gate of columns:
+// forward 88 us, 5.3 TB/s (with one norm alone 72, 6.5); with both kept in 8 bits 160; the
+// gradient 167 us, 4.2 TB/s, from 8-bit rows 219; layer norms 145 and 289.  What is left
+// to HBM's time (69 and 104) is instructions: 2.3 an SM and cycle where 4 could be, for
+// 200 to 400 of a warp for 256 columns, most of them conversions of bf16 and what a
+// row costs beside its columns.  4099 x 2047 in rows that are not aligned, layer norms,
+// a gate of rows, fp32: forward 46 us, gradient 105 (HBM's time 17 and 27): three 16-byte
+// pieces for 32 bytes, their shifts, and stores of single values.
 #pragma once
 
 #include <cuda_bf16.h>
