@@ -593,13 +593,13 @@ def _check_rows8(v, codes, scales, group):
     tt, dev = _torch(), _current_device()
     if group not in (32, 64, 128):
         raise MoEError(MOE_E_INVAL, f"group {group}: 32, 64 or 128")
-    shape = tuple(v.shape)
+    shape = v.shape
     if not shape:
         raise MoEError(MOE_E_INVAL, "values: expected [..., cols]")
     kind, cols = _type_code("values", v), shape[-1]
     _on_device("values", v, dev, v.dtype, shape)
     _on_device("codes", codes, dev, tt.i8, shape)
-    _on_device("scales", scales, dev, tt.bf16, shape[:-1] + (-(-cols // group),))
+    _on_device("scales", scales, dev, tt.bf16, (*shape[:-1], -(-cols // group)))
     return (v.numel() // cols if cols else 0), cols, kind, dev
 
 
@@ -696,33 +696,38 @@ class MoEBlockNorm:
         if t.get_device() != dev:
             raise MoEError(MOE_E_INVAL, f"{name}: on device {t.get_device()}, the current one is {dev}")
 
+    def _vector(self, name, t, of, dev):
+        """The pointer of a vector of d values of the type that the others have (None: the first)."""
+        if of is not None and t.dtype is not of:
+            raise MoEError(MOE_E_INVAL, f"{name}: dtype {t.dtype}, the other gains and shifts have {of}")
+        if of is None:
+            _type_code(name, t)
+        _on_device(name, t, dev, t.dtype, self._columns)
+        return t.data_ptr()
+
     def _params(self, T, dev, gate, pre_gain, pre_shift, post_gain, post_shift):
         """The gains, shifts and gate as the C call takes them."""
-        tt, of = _torch(), None
-        columns = gate if self.gate == "channel" else None
-        pointers = []
-        for name, t in (("pre_gain", pre_gain), ("pre_shift", pre_shift), ("post_gain", post_gain),
-                        ("post_shift", post_shift), ("gate", columns)):
-            if t is None:
-                pointers.append(None)
-                continue
-            if of is None:
-                of = t.dtype
-                _type_code(name, t)
-            elif t.dtype is not of:
-                raise MoEError(MOE_E_INVAL, f"{name}: dtype {t.dtype}, the other gains and shifts have {of}")
-            _on_device(name, t, dev, of, self._columns)
-            pointers.append(t.data_ptr())
-        stride = 0
-        if gate is not None and columns is None:
-            if self.gate == "token":
+        tt, of, stride = _torch(), None, 0
+        a = b = c = d = g = None
+        if pre_gain is not None:
+            a, of = self._vector("pre_gain", pre_gain, of, dev), pre_gain.dtype
+        if pre_shift is not None:
+            b, of = self._vector("pre_shift", pre_shift, of, dev), pre_shift.dtype
+        if post_gain is not None:
+            c, of = self._vector("post_gain", post_gain, of, dev), post_gain.dtype
+        if post_shift is not None:
+            d, of = self._vector("post_shift", post_shift, of, dev), post_shift.dtype
+        if gate is not None:
+            if self.gate == "channel":
+                g, of = self._vector("gate", gate, of, dev), gate.dtype
+            elif self.gate == "token":
                 _on_device("gate", gate, dev, tt.f32, (T,))
-                pointers[4] = gate.data_ptr()
+                g = gate.data_ptr()
             elif self.gate == "element":
-                pointers[4], stride = self._rows("gate", gate, T, tt.bf16, dev)
+                g, stride = self._rows("gate", gate, T, tt.bf16, dev)
             else:
                 raise MoEError(MOE_E_INVAL, "gate: the handle has none")
-        return _NormParams(*pointers, stride, 0 if of is tt.f32 else 1)
+        return _NormParams(a, b, c, d, g, stride, 0 if of is tt.f32 else 1)
 
     def _rows8(self, name, held, T, dev):
         if held is None:
@@ -741,18 +746,19 @@ class MoEBlockNorm:
         fp32 is for backward; ``out8`` and ``y8``, (codes int8 [T, d], scales bf16
         [T, ceil(d / group)]), keep out and y as 8-bit rows."""
         tt, dev = _torch(), _current_device()
-        T = residual.shape[0]
+        T, dtype = residual.shape[0], residual.dtype
         kind = _type_code("residual", residual)
-        r, r_row = self._rows("residual", residual, T, residual.dtype, dev)
+        r, r_row = self._rows("residual", residual, T, dtype, dev)
         yp, y_row = self._rows("y", y, T, tt.bf16, dev)
-        o, o_row = self._rows("out", out, T, residual.dtype, dev)
+        o, o_row = (r, r_row) if out is residual else self._rows("out", out, T, dtype, dev)
         n, n_row = self._rows("norm", norm, T, tt.bf16, dev)
         if stats is not None:
             _on_device("stats", stats, dev, tt.f32, (T, 4))
         p = self._params(T, dev, gate, pre_gain, pre_shift, post_gain, post_shift)
-        _err(self._c_forward(self.h, T, kind, r, r_row, yp, y_row, _ref(p), o, o_row, n, n_row,
-                             None if stats is None else stats.data_ptr(), _ref(self._rows8("out8", out8, T, dev)),
-                             _ref(self._rows8("y8", y8, T, dev)), _stream_on(stream, dev)))
+        _err(self._c_forward(self.h, T, kind, r, r_row, yp, y_row, ctypes.byref(p), o, o_row, n, n_row,
+                             None if stats is None else stats.data_ptr(),
+                             None if out8 is None else _ref(self._rows8("out8", out8, T, dev)),
+                             None if y8 is None else _ref(self._rows8("y8", y8, T, dev)), _stream_on(stream, dev)))
         return out, norm
 
     def _kept(self, name, t, T, dtype, dev):

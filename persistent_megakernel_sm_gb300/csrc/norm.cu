@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, VEC && !SAVE ? 2 : 1) norm_forward(c
 #pragma unroll 1
   for (; t < a.T; t += step) {
     const float gate_t = f.gate_tokens ? __ldg(f.gate_tokens + t) : 1.f;
-    wait_copies(a.stages);
+    wait_copies<VEC>(a.stages);
     Eight sum[CH];
     float2 post = make_float2(0.f, 1.f), pre = post;
 #pragma unroll
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, VEC && !SAVE ? 2 : 1) norm_forward(c
       }
     }
     if (f.norm.p) pre = moments<PRE_LAYER, CH>(team, sum, n, inv_d, a.eps);
+    if (!VEC) __syncwarp();
     start(t + a.stages * step, slot);  // all of the row has been read
     slot += a.stage;
     if (slot == smem + a.vec) slot = smem;
@@ -248,8 +249,7 @@ int moe_norm_forward(const moe_norm_t* h, int T, int residual_type, const void* 
     f.out8 = rows8_of(out8), f.y8 = rows8_of(y8);
     const bool vec = h->d % 8 == 0 && rows_aligned(f.residual) && rows_aligned(f.y) && rows_aligned(f.out) &&
                      rows_aligned(f.norm) && rows_aligned(f.gate_rows) && aligned(f.out8.codes, 8) && aligned(f.y8.codes, 8);
-    const int piece = vec ? 16 : 32, size = (int)sizeof(R) * 8 + (vec ? 0 : 16);
-    const int bytes[5] = {size, y ? piece : 0, f.gate_rows.p ? piece : 0, 0, 0};
+    const int bytes[5] = {(int)sizeof(R) * 8, y ? 16 : 0, f.gate_rows.p ? 16 : 0, 0, 0};
     const Plan p = lay_out(&f.a, vec ? chunks_of(h->d, T, 2) : 1, kThreads, vec && !out8 && !y8 ? 2 * kThreads : kThreads, bytes,
                            f.pre_shift ? 4 : f.post_shift ? 3 : 2, 1, vec);
     const int teams = std::min(T, kSms * p.per_sm / p.blocks);

@@ -20,9 +20,9 @@
 // consecutive columns of it, in registers; while it works on a row, the next ones are on
 // their way: by asynchronous 16-byte copies into slots of shared memory that belong to
 // the thread that reads them, so that no barrier guards them.  Rows that are not aligned
-// come as the 16-byte pieces that they lie in, shifted when they are read (a piece
-// between two lanes comes twice, the second time from L1), and leave a warp's 256
-// columns at a time, each store along the row.  The forward pass exchanges sums between
+// come as the 16-byte pieces that they lie in, shifted when they are read (the piece that
+// two lanes share is read by both), and leave a warp's 256 columns at a time, each store
+// along the row.  The forward pass exchanges sums between
 // the block's warps twice a row, a layer norm once more for each norm (the mean first,
 // then the squares about it); the gradient once.  Sums over rows are kept in
 // registers, written once a block and added by a second kernel in a fixed order.
@@ -33,8 +33,8 @@
 // to HBM's time (69 and 104) is instructions: 2.3 an SM and cycle where 4 could be, for
 // 200 to 400 of a warp for 256 columns, most of them conversions of bf16 and what a
 // row costs beside its columns.  4099 x 2047 in rows that are not aligned, layer norms,
-// a gate of rows, fp32: forward 46 us, gradient 105 (HBM's time 17 and 27): three 16-byte
-// pieces for 32 bytes, their shifts, and stores of single values.
+// a gate of rows, fp32: forward 45 us, gradient 83 (HBM's time 17 and 27), for the shifts
+// and the stores of single values.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -144,33 +144,34 @@ struct Shape {
   float scale, eps, one;    // one: 1 where gains are stored less 1
 };
 
-// Pieces of 16 bytes (codes: of 8) that hold 8 columns: those of aligned rows, one
-// more of others.
-template <typename T, bool VEC>
+// `units`: threads times a thread's eights; unit: chunk * threads + thread.  A field is
+// one plane of 16 bytes a unit for 8 bf16, two for 8 fp32 (codes: of 8 bytes, and one of
+// 4 for a scale).  Rows that are not aligned come as the pieces of 16 bytes that they lie
+// in, each unit's from the one that its first column is in; the piece behind them that
+// it may need is the next lane's first, for a warp's last lane one more behind the
+// planes.  So a warp's lanes read what others copied: __syncwarp stands behind
+// the wait for the copies, and before the slots are given to another row.
+template <typename T>
 __host__ __device__ constexpr int pieces() {
-  return (int)sizeof(T) / 2 + (VEC ? 0 : 1);
-}
-template <bool VEC>
-__host__ __device__ constexpr int pieces8() {
-  return VEC ? 1 : 2;
+  return (int)sizeof(T) / 2;
 }
 
-// `units`: threads times a thread's eights; unit: chunk * threads + thread.  A field is
-// one plane of 16 bytes a unit for each piece, or of 8 and one of 4 for a scale.
 template <typename T, bool VEC>
 __device__ __forceinline__ void fetch(char* field, int units, int unit, const T* row, int col, int d) {
-  if (col >= d) return;
   uint4* slot = reinterpret_cast<uint4*>(field) + unit;
+  constexpr int k = pieces<T>();
   if constexpr (VEC) {
+    if (col >= d) return;
 #pragma unroll
-    for (int i = 0; i < pieces<T, true>(); ++i) moe::cp_async16(slot + i * units, row + col + i * (16 / sizeof(T)));
+    for (int i = 0; i < k; ++i) moe::cp_async16(slot + i * units, row + col + i * (16 / sizeof(T)));
   } else {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + col);
-    const int end = (int)(at & 15) + min(8, d - col) * (int)sizeof(T);  // from the first piece's begin
-    const char* from = reinterpret_cast<const char*>(at & ~(uintptr_t)15);
+    const uintptr_t from = reinterpret_cast<uintptr_t>(row + col) & ~(uintptr_t)15;
+    const int left = (int)(reinterpret_cast<uintptr_t>(row + d) - from);  // to the row's end; none: nothing of it is here
 #pragma unroll
-    for (int i = 0; i < pieces<T, false>(); ++i)
-      if (16 * i < end) copy16(slot + i * units, from + 16 * i, min(16, end - 16 * i));
+    for (int i = 0; i < k; ++i)
+      if (left > 16 * i) copy16(slot + i * units, reinterpret_cast<const char*>(from) + 16 * i, min(16, left - 16 * i));
+    if ((unit & 31) == 31 && left > 16 * k)
+      copy16(reinterpret_cast<uint4*>(field) + k * units + unit / 32, reinterpret_cast<const char*>(from) + 16 * k, min(16, left - 16 * k));
   }
 }
 
@@ -199,15 +200,17 @@ __device__ __forceinline__ void put_words(uint4 q, uint32_t* w) { w[0] = q.x, w[
 // What was fetched.  n: the columns that are there.
 template <typename T, bool VEC>
 __device__ __forceinline__ Eight read(const char* field, int units, int unit, const T* row, int n) {
-  constexpr int kPieces = pieces<T, VEC>(), kWords = (int)sizeof(T) * 2;
+  constexpr int k = pieces<T>(), kWords = (int)sizeof(T) * 2;
   const uint4* slot = reinterpret_cast<const uint4*>(field) + unit;
-  uint32_t in[4 * kPieces], w[kWords];
+  uint32_t in[4 * (k + 1)], w[kWords];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) put_words(slot[i * units], in + 4 * i);
+  for (int i = 0; i < k; ++i) put_words(slot[i * units], in + 4 * i);
   if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = in[i];
   } else {
+    const uint4* next = (unit & 31) == 31 ? reinterpret_cast<const uint4*>(field) + k * units + unit / 32 : slot + 1;
+    put_words(*next, in + 4 * k);
     shifted(in, (int)(reinterpret_cast<uintptr_t>(row) & 15), w);
   }
   Eight e;
@@ -221,25 +224,30 @@ __device__ __forceinline__ Eight read(const char* field, int units, int unit, co
   return e;
 }
 
+// Where the scales of a field of codes begin: behind a plane of 8 bytes a unit, and one a warp.
+template <bool VEC>
+__device__ __forceinline__ int scales_at(int units) {
+  return 8 * units + (VEC ? 0 : units / 4);
+}
+
 template <bool VEC>
 __device__ __forceinline__ void fetch8(char* field, int units, int unit, const Rows8& r, int t, const Shape& a, int col) {
-  if (col >= a.d) return;
   uint2* slot = reinterpret_cast<uint2*>(field) + unit;
-  const int8_t* row = r.codes + (long long)t * a.d + col;
+  const int8_t* row = r.codes + (long long)t * a.d;
   if constexpr (VEC) {
-    copy8(slot, row, 8);
+    if (col < a.d) copy8(slot, row + col, 8);
   } else {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row);
-    const int end = (int)(at & 7) + min(8, a.d - col);
-    const char* from = reinterpret_cast<const char*>(at & ~(uintptr_t)7);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (8 * i < end) copy8(slot + i * units, from + 8 * i, min(8, end - 8 * i));
+    const uintptr_t from = reinterpret_cast<uintptr_t>(row + col) & ~(uintptr_t)7;
+    const int left = (int)(reinterpret_cast<uintptr_t>(row + a.d) - from);
+    if (left > 0) copy8(slot, reinterpret_cast<const char*>(from), min(8, left));
+    if ((unit & 31) == 31 && left > 8)
+      copy8(reinterpret_cast<uint2*>(field) + units + unit / 32, reinterpret_cast<const char*>(from) + 8, min(8, left - 8));
   }
+  if (col >= a.d) return;
   // the word that the scale is in; the tensor may end in its middle
   const long long scale = (long long)t * a.groups + (col >> a.group_log);
   const bool last = scale == (long long)a.T * a.groups - 1 && !(scale & 1);
-  copy4(field + (size_t)units * 8 * pieces8<VEC>() + 4 * unit, r.scales + (scale & ~1ll), last ? 2 : 4);
+  copy4(field + scales_at<VEC>(units) + 4 * unit, r.scales + (scale & ~1ll), last ? 2 : 4);
 }
 
 template <bool VEC>
@@ -251,19 +259,20 @@ __device__ __forceinline__ Eight read8(const char* field, int units, int unit, c
   if constexpr (VEC) {
     w[0] = q.x, w[1] = q.y;
   } else {
-    const uint2 q2 = slot[units];
+    const uint2 q2 = (unit & 31) == 31 ? reinterpret_cast<const uint2*>(field)[units + unit / 32] : slot[1];
     const uint32_t in[4] = {q.x, q.y, q2.x, q2.y};
     shifted(in, (int)(reinterpret_cast<uintptr_t>(r.codes + (long long)t * a.d) & 7), w);
   }
-  const uint32_t word = *reinterpret_cast<const uint32_t*>(field + (size_t)units * 8 * pieces8<VEC>() + 4 * unit);
+  const uint32_t word = *reinterpret_cast<const uint32_t*>(field + scales_at<VEC>(units) + 4 * unit);
   const bool odd = (t * a.groups + (col >> (a.group_log))) & 1;
   const float s = __uint_as_float(odd ? word & 0xffff0000u : word << 16);
-  float x[8];
-  moe::rows8_floats(w[0], x);
-  moe::rows8_floats(w[1], x + 4);
   Eight e;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) e.v[i] = mul2(make_float2(x[2 * i], x[2 * i + 1]), two(s));
+  for (int h = 0; h < 2; ++h) {
+    float2 x[2];
+    moe::rows8_floats(w[h], x);
+    e.v[2 * h] = mul2(x[0], two(s)), e.v[2 * h + 1] = mul2(x[1], two(s));
+  }
   if (!VEC && n < 8) e.cut(n);
   return e;
 }
@@ -518,10 +527,12 @@ __device__ __forceinline__ void begin(const Shape& a, const Team& team, char* sm
 }
 
 // Until the oldest of a.stages rows under way has come.
+template <bool VEC>
 __device__ __forceinline__ void wait_copies(int stages) {
   if (stages == 2) moe::cp_async_wait<1>();
   else if (stages == 3) moe::cp_async_wait<2>();
   else moe::cp_async_wait<3>();
+  if (!VEC) __syncwarp();
 }
 
 // ------------------------------------------------------------------------- host
@@ -554,7 +565,8 @@ Plan lay_out(Shape* a, int chunks, int block_threads, int sm_threads, const int 
     p.threads = ((lanes + blocks * chunks - 1) / (blocks * chunks) + 31) / 32 * 32;
     units = p.threads * chunks;
     a->stage = 0;
-    for (int i = 0; i < 5; ++i) a->field[i] = a->stage, a->stage += (field_bytes[i] + 15) / 16 * 16 * units;
+    // a unit's bytes, and behind them a warp's piece (16 bytes, 8 of codes) of rows that are not aligned
+    for (int i = 0; i < 5; ++i) a->field[i] = a->stage, a->stage += field_bytes[i] * units + (vec || !field_bytes[i] ? 0 : units / 2);
     parts = 2 * quads * p.blocks * p.threads / 32 * 16;
     rest = kept * 32 * units + (vec ? 0 : p.threads * 32) + parts;
     return p.threads <= block_threads && least * a->stage + rest <= kRing;
@@ -662,7 +674,9 @@ cudaError_t by_kind(const moe_norm* h, bool vec, int chunks, F&& f) {
     return h->post == kNone ? f(v, pre, none, c) : h->post == kRms ? f(v, pre, rms, c) : f(v, pre, layer, c);
   };
   auto by_chunks = [&](auto v, auto pre) {
-    return chunks == 1 ? by_post(v, pre, std::integral_constant<int, 1>{}) : by_post(v, pre, std::integral_constant<int, 2>{});
+    constexpr std::integral_constant<int, 1> one{};
+    if constexpr (decltype(v)::value) return chunks == 1 ? by_post(v, pre, one) : by_post(v, pre, std::integral_constant<int, 2>{});
+    else return by_post(v, pre, one);  // rows that are not aligned keep more registers busy
   };
   auto by_pre = [&](auto v) { return h->pre == kLayer ? by_chunks(v, std::true_type{}) : by_chunks(v, std::false_type{}); };
   return vec ? by_pre(std::true_type{}) : by_pre(std::false_type{});

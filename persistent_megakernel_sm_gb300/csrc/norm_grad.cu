@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
       if (f.stats) st_next = __ldg(f.stats + t + step);
       if (f.gate_tokens) gate_next = __ldg(f.gate_tokens + t + step);
     }
-    wait_copies(a.stages);
+    wait_copies<VEC>(a.stages);
     float total[4 * quads];
     {
       float2 sum[4 * quads];
@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward(const __grid_constant_
         }
       }
     }
+    if (!VEC) __syncwarp();
     start(t + a.stages * step, slot);
     slot += a.stage;
     if (slot == smem + a.vec) slot = smem;
@@ -434,9 +435,9 @@ int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void*
                      rows_aligned(f.y) && rows_aligned(f.gate_rows) && rows_aligned(f.grad_residual) &&
                      rows_aligned(f.grad_y) && rows_aligned(f.grad_gate_rows) && aligned(f.out8.codes, 8) &&
                      aligned(f.y8.codes, 8);
-    const int piece = vec ? 16 : 32, size = (int)sizeof(R) * 8 + (vec ? 0 : 16), codes = vec ? 16 : 32;
-    const int bytes[5] = {grad_out ? size : 0, has_norm ? piece : 0, !has_norm ? 0 : f.out8.codes ? codes : size,
-                          f.y8.codes ? codes : f.y.p ? piece : 0, f.gate_rows.p ? piece : 0};
+    const int size = (int)sizeof(R) * 8;
+    const int bytes[5] = {grad_out ? size : 0, has_norm ? 16 : 0, !has_norm ? 0 : f.out8.codes ? 12 : size,
+                          f.y8.codes ? 12 : f.y.p ? 16 : 0, f.gate_rows.p ? 16 : 0};
     const Plan p = lay_out(&f.a, vec ? chunks_of(h->d, T, 2) : 1, kThreads, kThreads, bytes, f.post_shift ? 3 : 2,
                            quads_of(h->pre == kLayer, h->post), vec);
     // what a team keeps of its rows is written and read once more: 8 rows at least,

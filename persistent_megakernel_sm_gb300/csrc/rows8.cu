@@ -104,11 +104,11 @@ __global__ void __launch_bounds__(256)
   for (int n = 0; n < kUnroll; ++n) {
     const long long i = i0 + n * 256;
     if (i >= n8) break;
-    float x[8];
-    moe::rows8_floats(word[n].x, x);
-    moe::rows8_floats(word[n].y, x + 4);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= s[n];
+    float2 lo[2], hi[2];
+    moe::rows8_floats(word[n].x, lo);
+    moe::rows8_floats(word[n].y, hi);
+    const float x[8] = {lo[0].x * s[n], lo[0].y * s[n], lo[1].x * s[n], lo[1].y * s[n],
+                        hi[0].x * s[n], hi[0].y * s[n], hi[1].x * s[n], hi[1].y * s[n]};
     store8(v + i * 8, x);
   }
 }

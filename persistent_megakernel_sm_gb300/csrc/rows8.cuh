@@ -80,11 +80,12 @@ __device__ __forceinline__ uint2 rows8_codes(const float2 (&v)[4], __nv_bfloat16
 }
 
 // The four codes of a word as fp32, exactly: 2^23 + 128 + code, less 2^23 + 128.
-__device__ __forceinline__ void rows8_floats(uint32_t word, float* v) {
+__device__ __forceinline__ void rows8_floats(uint32_t word, float2 (&v)[2]) {
   const uint32_t u = word ^ 0x80808080u;  // code + 128
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 | i)) - 8388736.f;
+  auto at = [&](int i) { return __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 | i)); };
+  const float2 base = make_float2(-8388736.f, -8388736.f);
+  v[0] = __fadd2_rn(make_float2(at(0), at(1)), base);
+  v[1] = __fadd2_rn(make_float2(at(2), at(3)), base);
 }
 
 }  // namespace moe
