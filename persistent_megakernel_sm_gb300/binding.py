@@ -597,6 +597,8 @@ def _check_rows8(v, codes, scales, group):
     if not shape:
         raise MoEError(MOE_E_INVAL, "values: expected [..., cols]")
     kind, cols = _type_code("values", v), shape[-1]
+    if cols > 1 << 30:  # more would not reach the C call's int as they are
+        raise MoEError(MOE_E_INVAL, f"values: {cols} columns, 2^30 at most")
     _on_device("values", v, dev, v.dtype, shape)
     _on_device("codes", codes, dev, tt.i8, shape)
     _on_device("scales", scales, dev, tt.bf16, (*shape[:-1], -(-cols // group)))
@@ -668,6 +670,13 @@ class MoEBlockNorm:
 
     def workspace_bytes(self) -> int:
         return lib.moe_norm_workspace_bytes(self.h)
+
+    @staticmethod
+    def _count(t):
+        T = t.shape[0]
+        if T > 1 << 30:  # more would not reach the C call's int as they are
+            raise MoEError(MOE_E_INVAL, f"{T} rows, 2^30 at most")
+        return T
 
     def _rows(self, name, t, T, dtype, dev):
         """Rows of d values that may be columns of a wider buffer: (pointer, row stride)."""
@@ -746,7 +755,7 @@ class MoEBlockNorm:
         fp32 is for backward; ``out8`` and ``y8``, (codes int8 [T, d], scales bf16
         [T, ceil(d / group)]), keep out and y as 8-bit rows."""
         tt, dev = _torch(), _current_device()
-        T, dtype = residual.shape[0], residual.dtype
+        T, dtype = self._count(residual), residual.dtype
         kind = _type_code("residual", residual)
         r, r_row = self._rows("residual", residual, T, dtype, dev)
         yp, y_row = self._rows("y", y, T, tt.bf16, dev)
@@ -782,7 +791,7 @@ class MoEBlockNorm:
         some = grad_norm if grad_norm is not None else grad_out
         if some is None:
             raise MoEError(MOE_E_INVAL, "grad_out and grad_norm: one of them at least")
-        T = some.shape[0]
+        T = self._count(some)
         of = next((t for t in (grad_out, grad_residual, out) if t is not None and not isinstance(t, (tuple, list))), None)
         dtype = tt.bf16 if of is None else of.dtype
         kind = 1 if of is None else _type_code("grad_out, grad_residual or out", of)

@@ -16,7 +16,7 @@
 // means are known: one exchange a row.
 //
 // What bounds both is HBM, so the rest is kept out of its way.  A block holds a row (a
-// cluster of up to 16 blocks one that is too wide), a lane one or two times 8
+// cluster of 2, 4 or 8 blocks one that is too wide), a lane one or two times 8
 // consecutive columns of it, in registers; while it works on a row, the next ones are on
 // their way: by asynchronous 16-byte copies into slots of shared memory that belong to
 // the thread that reads them, so that no barrier guards them.  Rows that are not aligned
@@ -63,7 +63,7 @@ constexpr int kMaxStages = 4;            // rows under way
 constexpr int kSms = 152;
 constexpr int kRing = 200 * 1024;        // shared memory of an SM for all of it
 constexpr int kMaxSmem = 227 * 1024;     // of a block
-constexpr int kMaxCluster = 16;          // 8 are portable; 16 for the widest rows that are not aligned
+constexpr int kMaxCluster = 8;           // blocks of a row
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kNone = MOE_NORM_NONE, kRms = MOE_NORM_RMS, kLayer = MOE_NORM_LAYER;
 
@@ -587,7 +587,7 @@ struct ForwardKernel;
 template <typename, bool, bool, int, int>
 struct BackwardKernel;
 
-// Shared memory beyond 48 KB and clusters beyond 8 are asked for once a kernel and device.
+// Shared memory beyond 48 KB is asked for once a kernel and device.
 template <typename Kernel, typename F>
 cudaError_t allow_smem(F* kernel) {
   static std::atomic<uint64_t> done{0};
@@ -597,7 +597,6 @@ cudaError_t allow_smem(F* kernel) {
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
   e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;
 }

@@ -22,6 +22,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kUnroll = 4;
+constexpr int kMaxCols = 1 << 30;  // a column and a warp's step stay in 32 bits
 
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -192,7 +193,7 @@ int check_rows(long long rows, int cols, int type, int group, const void* v, con
   if (group != 32 && group != 64 && group != 128) return moe::set_error(MOE_E_INVAL, "group must be 32, 64 or 128");
   if (type != MOE_TYPE_F32 && type != MOE_TYPE_BF16)
     return moe::set_error(MOE_E_INVAL, "values are MOE_TYPE_F32 or MOE_TYPE_BF16");
-  if (rows < 0 || cols < 0) return moe::set_error(MOE_E_INVAL, "rows and cols must not be negative");
+  if (rows < 0 || cols < 0 || cols > kMaxCols) return moe::set_error(MOE_E_INVAL, "rows must not be negative, cols in 0..2^30");
   if (rows == 0 || cols == 0) return MOE_OK;
   if (rows > (1ll << 38) / cols) return moe::set_error(MOE_E_INVAL, "more than 2^38 values");
   if (!v || !codes || !scales) return moe::set_error(MOE_E_INVAL, "null tensor pointer");

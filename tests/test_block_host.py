@@ -36,11 +36,27 @@ def test_rows8_calls_validate(lib):
         assert f(4, 100, 1, 32, 16, 16, None, None) == BAD
         assert f((1 << 38) + 1, 1, 1, 32, 16, 16, 16, None) == BAD
         assert f(1 << 37, 1, 1, 32, 16, 16, 16, None) == BAD     # more blocks than a grid has
+        assert f(1, (1 << 30) + 1, 1, 32, 16, 16, 16, None) == BAD
         assert f(0, 100, 1, 32, None, None, None, None) == pkg.MOE_OK
         assert f(4, 0, 1, 32, None, None, None, None) == pkg.MOE_OK
     assert lib.moe_rows8_quantize(4, 100, 0, 32, 18, 16, 16, None) == BAD    # alignment
     assert lib.moe_rows8_quantize(4, 100, 1, 32, 17, 16, 16, None) == BAD
     assert lib.moe_rows8_quantize(4, 100, 1, 32, 16, 16, 17, None) == BAD
+
+
+def test_counts_beyond_the_c_calls_ints_are_refused(rec):  # noqa: F811
+    """A C int would take 2^32 + 4 for 4."""
+    many = (1 << 32) + 4
+    wide = torch.zeros(1, dtype=bf).expand(1, many).as_subclass(type(_dev(1)))
+    tall = torch.zeros(1, 64, dtype=bf).expand(many, 64).as_subclass(type(_dev(1)))
+    n = binding.MoEBlockNorm(64)
+    for call in (lambda: binding.rows8_quantize(wide, wide, wide, stream=0), lambda: n.forward(tall, None, None, tall, stream=0),
+                 lambda: n.backward(tall, None, tall, None, stream=0)):
+        with pytest.raises(binding.MoEError) as err:
+            call()
+        assert err.value.code == BAD
+    assert not [c for c in rec.calls if "quantize" in c or "ward" in c]
+    n.close()
 
 
 def test_rows8_binding_passes_and_refuses(rec):  # noqa: F811
@@ -114,7 +130,7 @@ def test_norm_forward_validates(lib):
     none = lib.moe_norm_create(64, 0, 0, 0, 1e-6, 1.0, 0, 128)
     held = lambda c, s: ctypes.byref(binding._Rows8(c, s))  # noqa: E731
     try:
-        bad = [dict(T=-1), dict(kind=2), dict(r=None), dict(rs=63), dict(ys=63), dict(os=63), dict(ns=63), dict(r=17),
+        bad = [dict(T=-1), dict(T=(1 << 30) + 1), dict(rs=1 << 31), dict(kind=2), dict(r=None), dict(rs=63), dict(ys=63), dict(os=63), dict(ns=63), dict(r=17),
                dict(r=18, kind=0), dict(y=17), dict(n=17), dict(y=None), dict(out=None), dict(n=None), dict(st=8),
                dict(out8=held(None, 16)), dict(out8=held(16, None)), dict(y8=held(16, 18)), dict(out=64, os=72),
                dict(y=None, out=None, y8=held(16, 16)), dict(p=_params(pre_gain=17)), dict(p=_params(pre_shift=16)),
@@ -153,7 +169,7 @@ def test_norm_backward_validates(lib):
     full = dict(out=64, out_stride=64, y=64, y_stride=64, stats=64)
     lp = _params(pre_gain=16, gate=16, gate_stride=64)
     try:
-        bad = [dict(T=-1), dict(kind=2), dict(go=None, gn=None), dict(gos=63), dict(gns=63), dict(grs=63), dict(gys=63),
+        bad = [dict(T=-1), dict(T=(1 << 30) + 1), dict(gos=1 << 31), dict(kind=2), dict(go=None, gn=None), dict(gos=63), dict(gns=63), dict(grs=63), dict(gys=63),
                dict(go=17), dict(gn=17), dict(gr=17), dict(gy=17), dict(go=128, gos=72), dict(gr=None, gy=None),
                dict(kept=dict(full, out=None)), dict(kept=dict(full, stats=None)), dict(kept=dict(full, stats=8)),
                dict(kept=dict(full, out_stride=63)), dict(kept=dict(full, out8=ctypes.addressof(half))),

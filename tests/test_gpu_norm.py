@@ -460,3 +460,12 @@ def test_two_streams_share_a_handle_forward(d):
             n.forward(r, y, *g, **p, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
+
+
+@pytest.mark.parametrize("d,pad", [(4104, 0), (8200, 0), (16392, 0), (32768, 0), (9001, 3)])
+@pytest.mark.parametrize("pre,post,gate,res", [("rms", "rms", "channel", "bfloat16"), ("layer", "layer", "element", "float32")])
+def test_wide_rows_of_long_batches(d, pad, pre, post, gate, res):
+    """Rows enough for a lane to hold two eights, and so wide that a cluster shares each."""
+    c = Case(310, d, pre, post, gate, res=res, pad=pad, scale=0.5, group=64)
+    c.check_forward(save=d == 8200)
+    c.check_backward(save=d == 8200)
