@@ -640,8 +640,10 @@ void moe_norm_destroy(moe_norm_t* h);
  * (decode, speculative decode), in one cooperative kernel that streams the chosen
  * experts' weights: the same tensors, layouts and limits.  What differs:
  *   - h is not rounded to bf16 but kept to 16 bits, with its weight w in it;
- *   - a logit of -inf (a bias of -inf) masks its expert out, as moe_router_forward
- *     has it; a slot without an expert gets idx -1 and w 0, and adds nothing;
+ *   - a logit of -inf masks its expert out, and so does a bias of -inf whatever the
+ *     logit, as moe_router_forward has it; a NaN logit of an expert that is not
+ *     masked ranks above every number, and shows as NaN in w; a slot without an
+ *     expert gets idx -1 and w 0, and adds nothing;
  *   - a given routing may have empty slots (idx outside [0, E): the rows behind a
  *     padded batch's last sequence) and may name an expert twice in a row, which
  *     then counts twice; a row of empty slots gets the shared expert's output, or

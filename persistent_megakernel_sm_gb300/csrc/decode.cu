@@ -529,7 +529,8 @@ __device__ __forceinline__ void logits(const Decode& p, Smem<NT>* sm, int e0, in
       float s = 0.f;
 #pragma unroll
       for (int w = 0; w < kThreads / 32; ++w) s += all[w * Sums<NT>::kTile + token * kColumn + row];
-      p.logits[token * p.E + e + row] = s + (p.bias ? p.bias[e + row] : 0.f);
+      const float b = p.bias ? p.bias[e + row] : 0.f;
+      p.logits[token * p.E + e + row] = b == -INFINITY ? b : s + b;  // masked beside a NaN or an infinity too
     }
   }
 }
