@@ -579,7 +579,8 @@ moe_norm_t* moe_norm_create(int d, int pre, int post, int gate, float eps, float
  * norm).  out8 and y8, each may be NULL: out and y as 8-bit rows, codes [T, d]
  * contiguous, scales 4-byte aligned.  No other tensors overlap.  Asynchronous,
  * allocates nothing, can be captured in a graph; needs no workspace, so a handle
- * may be used by several streams and threads at once.  T = 0 does nothing. */
+ * may be used by several streams and threads at once.  T = 0 does nothing; what has a row
+ * a token (a gate, 8-bit rows) may then be null. */
 int moe_norm_forward(const moe_norm_t* h, int T, int residual_type, const void* residual, long long residual_stride,
                      const void* y, long long y_stride, const moe_norm_params* params, void* out, long long out_stride,
                      void* norm, long long norm_stride, float* stats, const moe_rows8* out8, const moe_rows8* y8,

@@ -214,9 +214,9 @@ int moe_norm_forward(const moe_norm_t* h, int T, int residual_type, const void* 
   if (T < 0 || T > kMaxT) return moe::set_error(MOE_E_INVAL, "T must be in 0..2^30");
   if (residual_type != MOE_TYPE_F32 && residual_type != MOE_TYPE_BF16)
     return moe::set_error(MOE_E_INVAL, "the residual is MOE_TYPE_F32 or MOE_TYPE_BF16");
-  const char* bad = check_params(h, params);
-  if (!bad) bad = check_rows8(out8);
-  if (!bad) bad = check_rows8(y8);
+  const char* bad = check_params(h, params, T);
+  if (!bad) bad = check_rows8(out8, T);
+  if (!bad) bad = check_rows8(y8, T);
   if (bad) return moe::set_error(MOE_E_INVAL, bad);
   if (T == 0) return MOE_OK;
   if (!residual) bad = "null residual";

@@ -689,7 +689,8 @@ const char* check_rows(const moe_norm* h, const void* p, int type, long long str
   return nullptr;
 }
 
-const char* check_params(const moe_norm* h, const moe_norm_params* p) {
+// Without rows (T = 0) what has one a token is an empty tensor, whose pointer may be null.
+const char* check_params(const moe_norm* h, const moe_norm_params* p, int T) {
   if (!p) return "null params";
   if (p->type != MOE_TYPE_F32 && p->type != MOE_TYPE_BF16) return "gains and shifts are MOE_TYPE_F32 or MOE_TYPE_BF16";
   const void* all[] = {p->pre_gain, p->pre_shift, p->post_gain, p->post_shift};
@@ -698,15 +699,16 @@ const char* check_params(const moe_norm* h, const moe_norm_params* p) {
   if (h->pre == kNone && p->pre_gain) return "a gain for a norm that the handle does not have";
   if (h->post == kNone && p->post_gain) return "a gain for a norm that the handle does not have";
   if ((h->pre != kLayer && p->pre_shift) || (h->post != kLayer && p->post_shift)) return "only layer norms have a shift";
-  if ((h->gate != MOE_GATE_NONE) != (p->gate != nullptr)) return "the gate must be given as the handle has it";
+  const bool empty_gate = T == 0 && !p->gate && (h->gate == MOE_GATE_TOKEN || h->gate == MOE_GATE_ELEMENT);
+  if ((h->gate != MOE_GATE_NONE) != (p->gate != nullptr) && !empty_gate) return "the gate must be given as the handle has it";
   const size_t gate_size = h->gate == MOE_GATE_CHANNEL ? type_size(p->type) : h->gate == MOE_GATE_TOKEN ? 4 : 2;
   if (!aligned(p->gate, gate_size)) return "the gate must be aligned to its type";
   if (h->gate == MOE_GATE_ELEMENT) return check_rows(h, p->gate, MOE_TYPE_BF16, p->gate_stride);
   return nullptr;
 }
 
-const char* check_rows8(const moe_rows8* r) {
-  if (!r) return nullptr;
+const char* check_rows8(const moe_rows8* r, int T) {
+  if (!r || T == 0) return nullptr;
   if (!r->codes || !r->scales) return "null codes or scales of 8-bit rows";
   if (!aligned(r->scales, 4)) return "scales of 8-bit rows must be 4-byte aligned";
   return nullptr;

@@ -356,9 +356,9 @@ int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void*
   if (residual_type != MOE_TYPE_F32 && residual_type != MOE_TYPE_BF16)
     return moe::set_error(MOE_E_INVAL, "the residual is MOE_TYPE_F32 or MOE_TYPE_BF16");
   if (!kept || !grads) return moe::set_error(MOE_E_INVAL, "null kept or grads");
-  const char* bad = check_params(h, params);
-  if (!bad) bad = check_rows8(kept->out8);
-  if (!bad) bad = check_rows8(kept->y8);
+  const char* bad = check_params(h, params, T);
+  if (!bad) bad = check_rows8(kept->out8, T);
+  if (!bad) bad = check_rows8(kept->y8, T);
   if (bad) return moe::set_error(MOE_E_INVAL, bad);
   const moe_norm_grads& g = *grads;
   // a gradient is of something that is there
