@@ -382,6 +382,8 @@ int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void*
   }
   const bool has_norm = grad_norm != nullptr;
   const bool has_y = kept->y || kept->y8;
+  // with a post norm these go through it
+  const bool through_post = h->post != kNone && (grad_y || g.post_gain || g.post_shift || g.gate);
   if (!grad_out && !grad_norm) bad = "no gradient to start from";
   else if (has_norm && h->pre == kNone) bad = "the gradient of a norm that the handle does not have";
   else if (!has_norm && (g.pre_gain || g.pre_shift)) bad = "gradients of the pre norm need that of its output";
@@ -389,7 +391,7 @@ int moe_norm_backward(const moe_norm_t* h, int T, int residual_type, const void*
   else if (kept->y && kept->y8) bad = "y is kept in one form";
   else if (has_norm && !kept->out && !kept->out8) bad = "the gradient of the norm needs what was kept of out";
   else if (!has_y && ((h->post != kNone && grad_y) || g.post_gain || g.post_shift || g.gate)) bad = "these gradients need what was kept of y";
-  else if ((has_norm || h->post != kNone) && !kept->stats) bad = "the gradients of norms need stats";
+  else if ((has_norm || through_post) && !kept->stats) bad = "the gradients of norms need stats";
   else if (!grad_residual && !grad_y && !any && !g.gate) bad = "no gradient is wanted";
   else if (!aligned(kept->stats, 16)) bad = "stats must be 16-byte aligned";
   else if (h->gate == MOE_GATE_TOKEN && !aligned(g.gate, 4)) bad = "gradients must be aligned to their type";
