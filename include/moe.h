@@ -652,7 +652,8 @@ void moe_norm_destroy(moe_norm_t* h);
  *   - weights of experts that a token did not choose do not reach it, an infinity
  *     or a NaN among them neither.
  * The handle owns a workspace and serves one stream at a time; graphs that may run
- * at once need handles of their own. */
+ * at once need handles of their own.  Where a wait inside the kernel ran out, the later
+ * passes do nothing until moe_decode_status has been called. */
 typedef struct moe_decode moe_decode_t;
 
 /* Limits: those of moe_layer_create, and f <= 32768.  NULL on anything else. */
@@ -678,9 +679,16 @@ int moe_decode_forward(moe_decode_t* h, int T, const void* x, const void* router
 int moe_decode_forward_routed(moe_decode_t* h, int T, const void* x, const int32_t* idx, const float* w, const void* w_gate,
                               const void* w_up, const void* w_down, void* out, void* stream);
 
+/* Set an option: MOE_OPT_TIMEOUT_NS (from 1000; the default is 2e9), the limit of a pass's
+ * waits; MOE_OPT_FAULT_DROP_TASK, test only: -1 off; 0 or 1 = one block does not
+ * arrive at the grid's wait for the logits, or at that for h, which must end in
+ * MOE_E_TIMEOUT.  Takes effect at the next forward. */
+int moe_decode_set_option(moe_decode_t* h, int key, long long value);
+
 /* Synchronise `stream`, then return and clear the device status of the passes
- * since the last call: MOE_OK, MOE_E_TIMEOUT (a grid-wide wait ran out, the pass's
- * output is undefined), or MOE_E_CUDA when a CUDA error is pending. */
+ * since the last call: MOE_OK, MOE_E_TIMEOUT (a wait of the kernel ran out, that pass's
+ * output is undefined, and the passes after it did nothing), or MOE_E_CUDA when a CUDA
+ * error is pending. */
 int moe_decode_status(moe_decode_t* h, void* stream);
 
 void moe_decode_destroy(moe_decode_t* h);

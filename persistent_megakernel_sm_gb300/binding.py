@@ -85,6 +85,7 @@ _SIGNATURES = {
     "moe_decode_workspace_bytes": ([_vp, _i32], _i64),
     "moe_decode_forward": ([_vp, _i32] + [_vp] * 10, _i32),
     "moe_decode_forward_routed": ([_vp, _i32] + [_vp] * 8, _i32),
+    "moe_decode_set_option": ([_vp, _i32, _i64], _i32),
     "moe_decode_status": ([_vp, _vp], _i32),
     "moe_decode_destroy": ([_vp], None),
     "moe_last_error": ([], ctypes.c_char_p),
@@ -894,6 +895,10 @@ class MoEDecode:
         _err(self._c_routed(self.h, T, x.data_ptr(), idx.data_ptr(), w.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
                             w_down.data_ptr(), out.data_ptr(), _stream_on(stream, dev)))
         return out
+
+    def set_option(self, key, value: int):
+        """moe_decode_set_option: "timeout_ns", the limit of a pass's waits."""
+        _err(lib.moe_decode_set_option(self.h, OPTIONS.get(key, key), int(value)))
 
     def status(self, stream=None) -> int:
         return lib.moe_decode_status(self.h, _stream_ptr(stream))

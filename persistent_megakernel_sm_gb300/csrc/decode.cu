@@ -66,8 +66,12 @@ constexpr int kPitch = kChunk * 2 + 64;  // bytes of a row: two rows next to eac
 constexpr int kRing = 86;        // rows of the ring: 182 KB
 constexpr int kStages = 16;      // on their way, at most
 constexpr unsigned kAll = 0xffffffffu;
-constexpr uint64_t kLimitNs = 2000000000ull;
+constexpr uint64_t kLimitNs = 2000000000ull;  // of a pass's waits, where no option says otherwise
+constexpr uint64_t kDrainNs = 2000000000ull;  // for copies on their way to arrive
 
+// A wait that runs out leaves `arrived` off a whole number of grids, and the next wait
+// would be let through early: so a pass that finds a status does nothing, until
+// moe_decode_status clears both.
 struct Sched {
   unsigned long long arrived;  // blocks, at all waits since it was cleared
   int status;
@@ -75,6 +79,8 @@ struct Sched {
 
 struct Decode {
   int T, d, f, E, k, S;
+  int drop;            // test only: the wait (0: for the logits, 1: for h) at which block 0 does not arrive; -1: none
+  uint64_t limit_ns;   // of the waits
   const bf16 *x, *router_w, *gate, *up, *down;
   const float* bias;
   const int* idx_in;   // routed: the caller's choice, else null
@@ -120,15 +126,16 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 
 __device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
-// Every block's consumers arrive; false if the wait ran out somewhere.  `target` (of
-// thread 0): the arrivals that make it complete.
-__device__ bool grid_wait(Sched* s, unsigned long long target, uint64_t deadline, int* ok) {
+// Every block's consumers arrive; false if the wait ran out somewhere, or if an earlier
+// pass left a `status`.  `target` (of thread 0, as the status): the arrivals that make it
+// complete.
+__device__ bool grid_wait(Sched* s, unsigned long long target, uint64_t deadline, bool arrive, int status, int* ok) {
   sync_consumers();
   if (threadIdx.x == 0) {
-    int fine = 1;
-    asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(&s->arrived) : "memory");
+    int fine = status == 0;
+    if (fine && arrive) asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(&s->arrived) : "memory");
     unsigned long long now;
-    for (int i = 0;; ++i) {
+    for (int i = 0; fine; ++i) {
       asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(now) : "l"(&s->arrived) : "memory");
       if (now >= target) break;
       if (i % 16 == 15 && (moe::ld_relaxed(&s->status) != 0 || moe::globaltimer() > deadline)) {
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   List* list = &sm->list;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int block = blockIdx.x, blocks = gridDim.x;
-  const uint64_t deadline = moe::globaltimer() + kLimitNs;
+  const uint64_t deadline = moe::globaltimer() + p.limit_ns;
   const bool producer = warp >= kWarps;
   if (tid < kStages) {
     moe::mbar_init(&sm->full[tid], kBringers + kBringers * 32);
@@ -553,15 +560,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
   if (tid == 0) sm->abort = 0;
   if (tid < p.E) list->by_expert[tid] = 0;
   if (tid < p.T) list->w[p.E][tid] = 1.f;  // the shared expert's
-  bool fine = true;
   // arrivals before this pass: a whole number of grids, and maybe others' first ones of this pass
   unsigned long long target = 0;
-  if (tid == 0) target = *static_cast<volatile unsigned long long*>(&p.sched->arrived) / blocks * blocks;
+  int status = 0;  // that an earlier pass left
+  if (tid == 0) {
+    target = *static_cast<volatile unsigned long long*>(&p.sched->arrived);
+    status = *static_cast<volatile int*>(&p.sched->status);
+    target = target / blocks * blocks;
+  }
   // 1: logits, and the choice
   if (p.router_w) logits<NT>(p, sm, share(p.E, block, blocks), share(p.E, block + 1, blocks));
   if (!producer) {
-    if (p.router_w) fine = grid_wait(p.sched, target += blocks, deadline, &list->ok);
-    else sync_consumers();
+    bool fine;
+    if (p.router_w) {
+      fine = grid_wait(p.sched, target += blocks, deadline, block != 0 || p.drop != 0, status, &list->ok);
+    } else {
+      if (tid == 0) list->ok = status == 0;
+      sync_consumers();
+      fine = list->ok != 0;
+    }
     if (fine) {
       for (int t = warp; t < p.T; t += kWarps) {
         int e = -1;
@@ -630,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
         }
       }
       // what is on its way arrives before the block ends, whatever became of the others
-      const uint64_t last = moe::globaltimer() + kLimitNs;
+      const uint64_t last = moe::globaltimer() + kDrainNs;
       for (int i = max(0, issued - kStages); i < issued; ++i)
         moe::mbar_wait(&sm->full[i % kStages], (uint32_t)(i / kStages) & 1u, last);
       return;
@@ -700,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_layer(const __grid_constan
     });
   }
   me.tell();
-  if (!grid_wait(p.sched, target += blocks, deadline, &list->ok) || *abort) {
+  if (!grid_wait(p.sched, target += blocks, deadline, block != 0 || p.drop != 1, 0, &list->ok) || *abort) {
     if (tid == 0) *abort = 1;
     return;
   }
@@ -738,7 +755,8 @@ struct Layout {
 
 struct moe_decode {
   int d, f, E, k, S;
-  int T_max = 0, blocks = 0, device = -1;
+  int T_max = 0, blocks = 0, device = -1, drop = -1;
+  uint64_t limit_ns = kLimitNs;
   char* ws = nullptr;
   Layout l{};
 };
@@ -774,6 +792,7 @@ int check_call(moe_decode* h, int T, const void* x, const void* gate, const void
 
 int run(moe_decode* h, Decode& p, cudaStream_t s) {
   p.d = h->d, p.f = h->f, p.E = h->E, p.k = h->k, p.S = h->S;
+  p.drop = h->drop, p.limit_ns = h->limit_ns;
   p.sched = reinterpret_cast<Sched*>(h->ws);
   p.logits = reinterpret_cast<float*>(h->ws + h->l.logits);
   p.h_hi = reinterpret_cast<bf16*>(h->ws + h->l.h_hi);
@@ -857,6 +876,23 @@ int moe_decode_reserve(moe_decode_t* h, int T_max, void* stream) {
   h->l = l;
   h->T_max = T_max;
   moe::clear_error();
+  return MOE_OK;
+}
+
+int moe_decode_set_option(moe_decode_t* h, int key, long long v) {
+  if (!h) return moe::set_error(MOE_E_INVAL, "null handle");
+  switch (key) {
+    case MOE_OPT_TIMEOUT_NS:
+      if (v < 1000) return moe::set_error(MOE_E_INVAL, "timeout below 1 us");
+      h->limit_ns = (uint64_t)v;
+      break;
+    case MOE_OPT_FAULT_DROP_TASK:
+      if (v < -1 || v > 1) return moe::set_error(MOE_E_INVAL, "the waits are 0 and 1; -1: off");
+      h->drop = (int)v;
+      break;
+    default:
+      return moe::set_error(MOE_E_INVAL, "not an option of the layer for a few tokens");
+  }
   return MOE_OK;
 }
 
