@@ -623,8 +623,13 @@ long long moe_norm_workspace_bytes(const moe_norm_t* h);
  *   grad gate = scale * G * p, summed over the rows (channel) or columns (token)
  * grad_out (of residual_type) or grad_norm (bf16) may be NULL: zero.
  * grad_residual (of residual_type; may be grad_out itself, in place) and grad_y (bf16)
- * may be NULL: not wanted.  No other tensors overlap.  Sums over rows are fp32, in
- * an order that T and d alone decide.  Asynchronous, allocates nothing, can be
+ * may be NULL: not wanted.  No other tensors overlap.  Sums over rows are fp32, without
+ * atomics, in an order that the form of the call decides: T, the handle's settings,
+ * residual_type, which tensors are given and whether out and y are kept in 8 bits,
+ * and whether all rows are aligned (to 16 bytes, codes to 8, d a multiple of 8).
+ * Calls of one form have the same bits wherever their tensors are; the same rows in
+ * another form (unaligned, as part of a larger batch) may differ in the last ones, and so
+ * may those of moe_norm_forward.  Asynchronous, allocates nothing, can be
  * captured in a graph; one stream at a time where gradients [d] are wanted (they
  * use the workspace; graphs replayed at once need handles of their own).  T = 0
  * writes zeros to the gradients [d]. */
