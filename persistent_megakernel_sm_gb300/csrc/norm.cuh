@@ -264,7 +264,7 @@ __device__ __forceinline__ Eight read8(const char* field, int units, int unit, c
     shifted(in, (int)(reinterpret_cast<uintptr_t>(r.codes + (long long)t * a.d) & 7), w);
   }
   const uint32_t word = *reinterpret_cast<const uint32_t*>(field + scales_at<VEC>(units) + 4 * unit);
-  const bool odd = (t * a.groups + (col >> (a.group_log))) & 1;
+  const bool odd = ((uint32_t)t * (uint32_t)a.groups + (uint32_t)(col >> a.group_log)) & 1;  // the low bit alone: any width will do
   const float s = __uint_as_float(odd ? word & 0xffff0000u : word << 16);
   Eight e;
 #pragma unroll
