@@ -522,8 +522,9 @@ typedef struct moe_rows8 {
 /* v [rows, cols] of `type` (MOE_TYPE_F32, MOE_TYPE_BF16), contiguous -> codes and
  * scales; and the way back, rounded once to `type`.  Any cols; tensors are aligned
  * to their types (16 bytes, 8 for the codes, and cols a multiple of the group are
- * faster).  At most 2^30 cols and 2^38 values.  Asynchronous, allocate nothing; no two tensors
- * overlap. */
+ * faster).  At most 2^30 cols and 2^38 values; where rows are not whole groups or not
+ * aligned so, at most 2^34 - 8 pieces, rows * ceil(cols / 256).  Asynchronous, allocate
+ * nothing; no two tensors overlap. */
 int moe_rows8_quantize(long long rows, int cols, int type, int group, const void* v, void* codes, void* scales,
                        void* stream);
 int moe_rows8_dequantize(long long rows, int cols, int type, int group, const void* codes, const void* scales, void* v,
