@@ -42,7 +42,9 @@
  *   - every int-returning call returns MOE_OK (0) or one of MOE_E_*; the
  *     message of the last failure on the calling thread is moe_last_error();
  *   - a handle serves one stream at a time; calls on one handle are not
- *     thread-safe.
+ *     thread-safe;
+ *   - a handle's workspace is on the device that was current at its reserve call, and
+ *     that device is current at the later calls that use it.
  * Limits: d % 128 == 0, d <= 32768, f % 128 == 0, 1 <= k <= E <= 256,
  * k <= 16, S <= 1, 0 <= T <= T_max given to moe_layer_reserve, T_max <= 32768.
  */
@@ -656,7 +658,8 @@ void moe_norm_destroy(moe_norm_t* h);
  *     then counts twice; a row of empty slots gets the shared expert's output, or
  *     zeros;
  *   - weights of experts that a token did not choose do not reach it, an infinity
- *     or a NaN among them neither.
+ *     or a NaN among them neither; in a chosen expert's w_down an infinity makes a
+ *     NaN, or an infinity of its sign (h is the sum of two numbers, each times it).
  * The handle owns a workspace and serves one stream at a time; graphs that may run
  * at once need handles of their own.  Where a wait inside the kernel ran out, the later
  * passes do nothing until moe_decode_status has been called. */
