@@ -15,14 +15,16 @@
 // used because a multiply-add for every weight and token would not keep up with HBM.  A
 // stage is 1024 columns of a tile and of the tokens that its expert has.  Four warps of
 // a block bring its weights by bulk copies, four more the tokens' columns, into a ring
-// of single rows (182 KB an SM, two stages at least on their way); the weights do not
-// wait for the grid, so the ring is full of down's first ones when h' is complete.
+// of 86 single rows (182 KB an SM): two of gate and up's stages at least, of down's, with
+// two rows for each token, one where many tokens meet a wide layer (16 tokens of width 7168:
+// 24 + 32 rows).  The weights do not wait for the grid, so the ring is full of down's first
+// ones when h' is complete.
 // Eight warps multiply, each an eighth of a stage's columns, and their sums meet in
 // shared memory once a tile.  A lane reads 16 bytes of a row at once, which the mma sees
 // as another order of the same columns, the same for the tokens'.
 //
-// HBM bounds it: 4 tokens of 32 + 1 experts of 7168 x 2048 take 299 us (6.77 TB/s, the
-// copy rate), 4 of eight experts of 4096 x 14336 6.7 TB/s, 13 to 16 tokens 6.0 to 6.3.
+// HBM bounds it: 4 tokens of 32 + 1 experts of 7168 x 2048 take 306 us (6.7 TB/s; a
+// copy has 6.8), 4 of eight experts of 4096 x 14336 6.7 TB/s, 13 to 16 tokens 6.0 to 6.3.
 // One token of 128 experts of 2048 x 768 (76 MB, 11 us) takes 25: the two waits of the
 // grid 1.1 each, logits and choice 5, and streams that end before they are at speed.
 //

@@ -29,11 +29,12 @@
 //
 // 8192 x 7168 in bf16, root mean squares on both sides, fp32 gains, a gate of columns:
 // forward 88 us, 5.3 TB/s (with one norm alone 72, 6.5); with both kept in 8 bits 160; the
-// gradient 167 us, 4.2 TB/s, from 8-bit rows 219; layer norms 145 and 289.  What is left
-// to HBM's time (69 and 104) is instructions: 2.3 an SM and cycle where 4 could be, for
-// 200 to 400 of a warp for 256 columns, most of them conversions of bf16 and what a
-// row costs beside its columns.  4099 x 2047 in rows that are not aligned, layer norms,
-// a gate of rows, fp32: forward 45 us, gradient 83 (HBM's time 17 and 27), for the shifts
+// gradient 173 us, 4.1 TB/s, from 8-bit rows 222; layer norms 144 and 299; in fp32 154
+// and 358.  What is left to HBM's time (69 and 104, in fp32 104 and 156) is instructions,
+// 200 to 660 of a warp for 256 columns, and the wait for a row's exchange: 14 warps an SM
+// issue 1.7 of them a cycle forward and 1.9 in the gradient, where 4 could be, and the 7 that
+// a wide gradient in fp32 has 0.9.  4099 x 2047 in rows that are not aligned, layer norms,
+// a gate of rows, fp32: forward 46 us, gradient 84 (HBM's time 17 and 27), for the shifts
 // and the stores of single values.
 #pragma once
 
